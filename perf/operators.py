@@ -3,9 +3,12 @@ scales, the routing of tokens to experts, and the routed experts' products.
 
 `run` computes a case either in its plain form (elementary torch operations)
 or, with `own` set, through this package's entry points.  4-bit weights are
-codes q in 0..15, two to a byte along k (the even k in the low half), with an
-FP16 scale and optionally an integer zero point (8 without one) per group:
+codes q in 0..15 with an FP16 scale and optionally an integer zero point (8
+without one) per group:
 W[n][k] = scale[n][k // group] * (q[n][k] - zero[n][k // group]).
+Eight consecutive codes of a row fill a little-endian 32-bit word, the one at
+offset o in bits 16 * (o % 2) + 4 * (o // 2) and up, as the 2-bit trits' words
+are filled: its bytes hold the offsets (0, 2), (4, 6), (1, 3), (5, 7).
 """
 import math
 
@@ -104,7 +107,7 @@ def _weights(gen, lead, n, k, group, zero):
         mid = z.to(torch.float16).repeat_interleave(group, dim=-1)
     q = torch.empty((*lead, n, k), dtype=torch.float16, device="cuda").normal_(0.0, 2.7, generator=gen)
     q = (q + mid).round_().clamp_(0, 15).to(torch.uint8)
-    codes = q[..., 0::2] | (q[..., 1::2] << 4)
+    codes = torch.stack([q[..., o::8] | (q[..., o + 2::8] << 4) for o in (0, 4, 1, 5)], dim=-1).flatten(-2)
     scale = torch.empty((*lead, n, k // group), dtype=torch.float32, device="cuda").uniform_(0.002, 0.012, generator=gen)
     return codes.contiguous(), scale.to(torch.float16), z
 
@@ -188,8 +191,9 @@ def _call(s):
 
 def _dense(codes, scale, zero):
     """The weights in FP32."""
-    q = torch.stack((codes & 15, codes >> 4), dim=-1).float()
-    q = q.reshape(*scale.shape, -1)
+    q = torch.stack((codes & 15, codes >> 4), dim=-1)  # in a word: offsets 0 2 4 6, then 1 3 5 7
+    q = q.reshape(*codes.shape[:-1], -1, 2, 4).transpose(-1, -2)
+    q = q.reshape(*scale.shape, -1).float()
     q = q - (8.0 if zero is None else zero.float().unsqueeze(-1))
     return (q * scale.float().unsqueeze(-1)).flatten(-2)
 
@@ -316,7 +320,11 @@ def _exact_rows(x, codes, scale, zero):
         c = codes[:, j * half:(j + 1) * half]
         xj = x[:, 2 * j * half:2 * (j + 1) * half]
         z = 8.0 if zero is None else zero[:, j].double()
-        dot = xj[:, 0::2] @ (c % 16).double().t() + xj[:, 1::2] @ (c // 16).double().t()
+        dot = torch.zeros_like(y)
+        for o in range(8):
+            byte = 2 * (o % 2) + o // 4
+            nibble = c[:, byte::4] // 16 if o % 4 >= 2 else c[:, byte::4] % 16
+            dot += xj[:, o::8] @ nibble.double().t()
         y += scale[:, j].double() * (dot - xj.sum(dim=1, keepdim=True) * z)
     return y
 
