@@ -373,6 +373,105 @@ tern_status tern_rotate(const uint16_t *R, int32_t block, const uint16_t *x, int
 tern_status tern_rotate_batched(int32_t count, const uint16_t *const *R, int32_t block, const uint16_t *const *x,
                                 const int32_t *k, int32_t m, uint16_t *const *out, void *stream);
 
+/* ---- 4-bit weights, routing, experts: what stands beside the ternary
+ * layers in a model (a vocabulary head or a sensitive projection kept at 4
+ * bits, a layer of experts).
+ *
+ * A 4-bit matrix holds W[n][k] = scale[n][g] * (q[n][k] - zero[n][g]), g =
+ * k / group, with codes q in 0..15.  Layout:
+ *   codes: eight consecutive codes of a row fill a little-endian uint32, the
+ *     one at offset o in bits 16*(o%2) + 4*(o/2) .. +3 (the order of the
+ *     2-bit plane's words); rows of k/2 bytes follow each other.
+ *   scale: FP16 [n][k/group].  zero: uint8 [n][k/group], any value; NULL: 8
+ *     everywhere.
+ * `count` matrices of one shape may be stacked ([count][n][...] in every
+ * array): a layer's experts.  group 32, 64 or 128 and k a multiple of it
+ * (TERN_E_UNSUPPORTED otherwise); any n.  codes 16-byte aligned, scale
+ * 2-byte.  The conventions above hold: x is FP16 [m][k], 16-byte aligned;
+ * FP32 sums; y FP16 (nearest even) or FP32; n == 0 or m == 0 is a no-op,
+ * k == 0 writes zeros; status codes, asynchronous, nothing kept between
+ * calls, every call but tern_q4_pack may be captured into a HIP graph (as
+ * long as its workspace stays its own).  A row of x that holds a NaN or an
+ * infinity reaches its own row of y alone. */
+typedef struct tern_q4 {
+  int32_t n, k, group, count;
+  const uint8_t *codes;   /* [count][n][k/2] */
+  const uint16_t *scale;  /* fp16 [count][n][k/group] */
+  const uint8_t *zero;    /* [count][n][k/group], or NULL */
+} tern_q4;
+
+/* Host-only check of a descriptor.  Makes no HIP call. */
+tern_status tern_q4_check(const tern_q4 *w);
+
+/* Packs codes q (device uint8 [count][n][k], 8-byte aligned) into
+ * dst->codes, which is written.  ws: 4 bytes of device memory or more.
+ * Synchronises stream; TERN_E_INVAL if a code is above 15. */
+tern_status tern_q4_pack(const uint8_t *q, const tern_q4 *dst, void *ws, size_t ws_bytes, void *stream);
+/* The inverse: device uint8 [count][n][k].  Every word is valid. */
+tern_status tern_q4_unpack(const tern_q4 *src, uint8_t *q, void *stream);
+
+/* y = x W^T for one 4-bit matrix (count == 1) and any m >= 0: from a single
+ * row, bound by the reading of the codes, to prefill batches on tiles.  The
+ * integers q - zero meet x on the matrix cores, a group's FP32 sum is then
+ * scaled in FP32: the weights are not rounded, and scales of any size lose
+ * neither range nor precision.  Results are bitwise reproducible.  ws:
+ * tern_q4_workspace_bytes(w, m) (K parts' FP32 partials; calls that overlap
+ * in time must not share it). */
+size_t tern_q4_workspace_bytes(const tern_q4 *w, int32_t m);
+tern_status tern_q4_gemm(const tern_q4 *w, const uint16_t *x, int32_t m, void *y, int32_t y_dtype, void *ws,
+                         size_t ws_bytes, void *stream);
+
+/* Routing of m tokens to experts.  For a row of logits l (FP16 or FP32
+ * [m][experts]; a NaN counts as minus infinity, plus infinity as FP32's
+ * largest value):
+ *   score  s_e = exp(l_e) / sum exp(l)  (TERN_SCORE_SOFTMAX) or
+ *          1 / (1 + exp(-l_e))          (TERN_SCORE_SIGMOID);
+ *   key    c_e = s_e + bias_e (FP32 [experts]; a NaN counts as minus
+ *          infinity), or, without a bias, s_e, in the order of l_e;
+ *   an expert whose logit or key is minus infinity is masked: never chosen;
+ *   groups the experts form `groups` runs of equal length, of which the
+ *          keep_groups with the largest sums of their group_best (1 or 2)
+ *          largest keys stay (a masked expert adds nothing, a group of
+ *          masked experts comes last); equal sums: the lower group;
+ *   ids    int32 [m][topk]: the experts with the topk largest keys, the
+ *          largest first, the lower expert among equals; -1 where none is
+ *          left;
+ *   weight FP32 [m][topk]: the chosen experts' scores s (without bias), 0 at
+ *          -1; with renorm divided by their sum (0 where it is 0); times
+ *          scale.
+ * Keys, their order and the weights are computed in FP64 (without a bias the
+ * order is the logits').  experts <= 1024, groups <= 64, topk <= 64
+ * (TERN_E_UNSUPPORTED above).  Async on stream. */
+typedef enum tern_score { TERN_SCORE_SOFTMAX = 0, TERN_SCORE_SIGMOID = 1 } tern_score;
+typedef struct tern_router {
+  int32_t experts, topk;
+  int32_t score;                             /* tern_score */
+  int32_t groups, group_best, keep_groups;   /* 1, 1, 1: no groups */
+  int32_t renorm;
+  float scale;
+  const float *bias;                         /* device [experts], or NULL */
+} tern_router;
+tern_status tern_route(const void *logits, int32_t l_dtype, int32_t m, const tern_router *r, int32_t *ids,
+                       float *weights, void *stream);
+
+/* The routed experts' feed-forward layer with 4-bit weights:
+ *   y[t] = sum_j weights[t][j] Wd_e (silu(Wg_e x[t]) * (Wu_e x[t])),
+ *   e = ids[t][j], j < topk, silu(v) = v / (1 + exp(-v)).
+ * gate_up: count = experts, n = 2 I rows, the gate's I and then the up
+ * projection's I; k = the width of x.  down: the same count, k = I, n = the
+ * width of y ([m][n]).  Slots whose id lies outside 0..count-1 are skipped
+ * (a token without any gets zeros); a token may name an expert twice.  The
+ * inner values silu(g) * u are held in FP16 (the down product's matrix
+ * operand); every sum is FP32, a token's slots are added in slot order, and
+ * results are bitwise reproducible.  count <= 1024, m * topk < 2^31
+ * (TERN_E_UNSUPPORTED).  ws: tern_q4_experts_workspace_bytes bytes, 16-byte
+ * aligned; calls that overlap in time must not share it.  ids and weights as
+ * tern_route leaves them (device).  Async on stream. */
+size_t tern_q4_experts_workspace_bytes(const tern_q4 *gate_up, const tern_q4 *down, int32_t m, int32_t topk);
+tern_status tern_q4_experts(const tern_q4 *gate_up, const tern_q4 *down, const uint16_t *x, int32_t m,
+                            const int32_t *ids, const float *weights, int32_t topk, void *y, int32_t y_dtype,
+                            void *ws, size_t ws_bytes, void *stream);
+
 /* Measurement aid, not part of the product: a plain streaming read of
  * `bytes` bytes (a multiple of 16) of device memory at `buf` (16-byte
  * aligned), the attainable-bandwidth reference for the products above.

@@ -19,7 +19,7 @@ LIB = os.path.join(PKG, "libtern.so")
 OBJDIR = os.path.join(PKG, "_build")
 
 SOURCES = ["tern_api.cpp", "pack.hip", "gemv.hip", "gemv_mfma.hip", "gemv_b3.hip", "gemm.hip", "quant.hip", "noalloc.hip",
-           "rotate.hip"]
+           "rotate.hip", "q4_api.cpp", "q4_rows.hip", "q4_tile.hip", "q4_experts.hip", "route.hip"]
 ARCH = os.environ.get("TERN_OFFLOAD_ARCH", "gfx950")
 
 

@@ -1,0 +1,107 @@
+// Declarations and device code shared by the 4-bit kernels (q4_*.hip).  Not
+// part of the public ABI.
+//
+// A 4-bit weight is W[n][k] = s[n][g] (q[n][k] - z[n][g]), g = k / G.  The
+// code q - z (0..15 minus 0..255) is an exact FP16 integer, so every kernel
+// here multiplies q - z with the FP16 activations on the matrix cores, sums
+// one group in FP32, and applies the group's scale to that FP32 sum: no
+// weight is ever rounded, and a scale's size costs neither range nor
+// precision.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "tern.h"
+
+namespace tern {
+
+typedef _Float16 h2_t __attribute__((ext_vector_type(2)));
+typedef _Float16 h8_t __attribute__((ext_vector_type(8)));
+typedef float f4_t __attribute__((ext_vector_type(4)));
+typedef float f16_t __attribute__((ext_vector_type(16)));
+typedef uint32_t w2_t __attribute__((ext_vector_type(2)));
+typedef uint32_t w4_t __attribute__((ext_vector_type(4)));
+
+// One product, or the products of the slots that were routed to experts.
+struct Q4Args {
+  const uint8_t* codes;
+  const uint16_t* scale;
+  const uint8_t* zero;  // NULL: 8 everywhere
+  const uint16_t* x;
+  void* y;
+  int32_t n, k, m;      // m: rows of x (plain product)
+  int32_t y_f32;
+  // split K (plain tiles): FP32 partials [splits][m][n], tiles of K per part
+  float* partial;
+  int32_t splits, tps;
+  // experts
+  const int4* tiles;     // {expert, first position, rows, 0}, sorted by expert
+  const int32_t* ntiles;
+  const int32_t* slots;  // position -> slot (token * topk + j)
+  const int32_t* ids;    // [m][topk]
+  const float* gates;    // [m][topk]
+  int32_t topk, experts;
+};
+
+enum Q4Mode {
+  kQ4Plain = 0,       // y[m][n]
+  kQ4Up = 1,          // h[position][n / 2] = silu(gate) * up, rows gathered from x
+  kQ4Down = 2,        // part[position][n] (FP32) from h[position][k]
+  kQ4UpSlot = 3,      // as kQ4Up, one slot per tile: position = slot, expert = ids[slot]
+  kQ4DownToken = 4    // y[token][n] = sum over its slots, in slot order
+};
+
+hipError_t launch_q4_rows(int mode, int group, const Q4Args& a, int max_tiles, hipStream_t s);
+hipError_t launch_q4_tile(int mode, int group, const Q4Args& a, int max_tiles, hipStream_t s);
+hipError_t launch_q4_reduce(const Q4Args& a, hipStream_t s);
+hipError_t launch_q4_plan(const int32_t* ids, int slots, int experts, int rows, int4* tiles, int32_t* ntiles,
+                          int32_t* order, int32_t* place, hipStream_t s);
+hipError_t launch_q4_combine(const float* part, const int32_t* place, const float* gates, int m, int topk, int n,
+                             void* y, int y_f32, hipStream_t s);
+hipError_t launch_q4_pack(const uint8_t* q, size_t words, uint8_t* codes, uint32_t* flag, hipStream_t s);
+hipError_t launch_q4_unpack(const uint8_t* codes, size_t words, uint8_t* q, hipStream_t s);
+
+struct RouteArgs {
+  const void* logits;
+  const float* bias;
+  int32_t* ids;
+  float* weights;
+  int32_t m, experts, topk, groups, best, keep, renorm, sigmoid;
+  float scale;
+};
+hipError_t launch_route(const RouteArgs& a, int f16, hipStream_t s);
+
+
+// ---------------------------------------------------------------- device code
+__device__ inline h2_t as_h2(uint32_t v) { return __builtin_bit_cast(h2_t, v); }
+
+// The constants that turn 1024 + q and 1024 + 16 q into q - z.
+struct Q4Bias {
+  h2_t lo, hi;  // -(1024 + z), -(64 + z)
+};
+__device__ inline Q4Bias q4_bias(int z) {
+  const _Float16 l = (_Float16)(-(1024 + z)), h = (_Float16)(-(64 + z));
+  return {h2_t{l, l}, h2_t{h, h}};
+}
+
+// Eight codes of a word to FP16 q - z, in k order.  A code ORed into the low
+// mantissa bits of 1024.0 is 1024 + q, into bits 4..7 1024 + 16 q; both
+// steps back are exact.  Nine VALU operations per word.
+__device__ inline h8_t q4_decode(uint32_t w, const Q4Bias& b) {
+  constexpr uint32_t kOne = 0x64006400u;
+  const h2_t six = {(_Float16)0.0625f, (_Float16)0.0625f};
+  const uint32_t v = w >> 8;
+  const h2_t p0 = as_h2((w & 0x000F000Fu) | kOne) + b.lo;
+  const h2_t p1 = as_h2((w & 0x00F000F0u) | kOne) * six + b.hi;
+  const h2_t p2 = as_h2((v & 0x000F000Fu) | kOne) + b.lo;
+  const h2_t p3 = as_h2((v & 0x00F000F0u) | kOne) * six + b.hi;
+  return h8_t{p0.x, p0.y, p1.x, p1.y, p2.x, p2.y, p3.x, p3.y};
+}
+
+__device__ inline float half_bits(uint16_t v) { return (float)__builtin_bit_cast(_Float16, v); }
+
+__device__ inline float q4_swiglu(float gate, float up) { return gate / (1.0f + __expf(-gate)) * up; }
+
+}  // namespace tern

@@ -1,0 +1,320 @@
+// Host half of the 4-bit layers' C ABI (tern_q4_*, tern_route in tern.h):
+// argument checks, workspace sizing, choice of kernel and launches.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cstdarg>
+#include <cstdio>
+
+#include "internal.h"
+#include "q4.h"
+
+namespace {
+
+tern_status fail(tern_status s, const char* fmt, ...) {
+  char msg[512];
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(msg, sizeof(msg), fmt, ap);
+  va_end(ap);
+  return tern::record_failure(s, msg);
+}
+
+#define Q4_HIP(call)                                                                       \
+  do {                                                                                     \
+    hipError_t e_ = (call);                                                                \
+    if (e_ != hipSuccess) return fail(TERN_E_HIP, "%s: %s", #call, hipGetErrorString(e_)); \
+  } while (0)
+
+#define Q4_TRY(expr)                  \
+  do {                                \
+    tern_status s_ = (expr);          \
+    if (s_ != TERN_OK) return s_;     \
+  } while (0)
+
+size_t round_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
+
+tern_status check_ptr(const void* p, bool needed, const char* name, size_t align) {
+  if (!p) return needed ? fail(TERN_E_INVAL, "%s is NULL", name) : TERN_OK;
+  if (reinterpret_cast<uintptr_t>(p) & (align - 1)) return fail(TERN_E_ALIGN, "%s is not %zu-byte aligned", name, align);
+  return TERN_OK;
+}
+
+tern_status check_shape(const tern_q4* w) {
+  if (!w) return fail(TERN_E_INVAL, "matrix descriptor is NULL");
+  if (w->n < 0 || w->k < 0 || w->count < 0)
+    return fail(TERN_E_INVAL, "negative shape n=%d k=%d count=%d", w->n, w->k, w->count);
+  if (w->group != 32 && w->group != 64 && w->group != 128)
+    return fail(TERN_E_UNSUPPORTED, "4-bit group %d is not 32, 64 or 128", w->group);
+  if (w->k % w->group) return fail(TERN_E_UNSUPPORTED, "k=%d must be a multiple of group %d", w->k, w->group);
+  // the kernels round k up to a step of 128 and n up to a tile
+  if (w->k > 0x7fffff00 || w->n > 0x7fffff00) return fail(TERN_E_UNSUPPORTED, "n=%d or k=%d is too large", w->n, w->k);
+  return TERN_OK;
+}
+
+tern_status check_q4(const tern_q4* w) {
+  Q4_TRY(check_shape(w));
+  const bool body = w->n > 0 && w->k > 0 && w->count > 0;
+  Q4_TRY(check_ptr(w->codes, body, "codes", 16));
+  Q4_TRY(check_ptr(w->scale, body, "scale", 2));
+  return TERN_OK;
+}
+
+size_t words_of(const tern_q4* w) { return (size_t)w->count * (size_t)w->n * (size_t)(w->k / 8); }
+
+// Up to this many activation rows the rows kernel, above it the tile kernel.
+constexpr int kRowsMost = 64;
+
+// K parts of a plain tile product: enough workgroups for two per CU, at
+// least four K steps each.
+int pick_splits(int m, int n, int k) {
+  const long long tiles = (long long)((m + 127) / 128) * ((n + 127) / 128);
+  const int steps = (k + 127) / 128;
+  if (tiles >= 256 || steps < 8) return 1;
+  const int splits = (int)std::min<long long>(512 / tiles, steps / 4);
+  const int tps = (steps + splits - 1) / splits;
+  return (steps + tps - 1) / tps;
+}
+
+size_t plain_ws(int m, int n, int k) {
+  if (m <= kRowsMost) return 0;
+  const int s = pick_splits(m, n, k);
+  return s > 1 ? (size_t)s * m * n * 4 : 0;
+}
+
+tern::Q4Args args_of(const tern_q4* w) {
+  tern::Q4Args a = {};
+  a.codes = w->codes;
+  a.scale = w->scale;
+  a.zero = w->zero;
+  a.n = w->n;
+  a.k = w->k;
+  a.splits = 1;
+  a.tps = (w->k + 127) / 128;
+  a.experts = w->count;
+  return a;
+}
+
+// ---- experts
+// Few slots: every slot is a tile of its own and a token's down products are
+// summed in its own workgroup; nothing has to be sorted.
+constexpr int kDirectSlots = 32;
+
+struct ExpertsPlan {
+  bool direct, tile;
+  int rows, max_tiles;
+  size_t h, part, tiles, ntiles, order, place, bytes;  // offsets in the workspace
+};
+
+ExpertsPlan plan_experts(int m, int topk, int experts, int inner, int n) {
+  ExpertsPlan p = {};
+  const size_t slots = (size_t)m * topk;
+  p.direct = slots <= (size_t)kDirectSlots;
+  p.tile = !p.direct && slots > (size_t)experts * 24;
+  p.rows = p.tile ? 128 : 16;
+  p.max_tiles = (int)std::min<size_t>(slots, slots / p.rows + experts);
+  if (!p.direct && !p.tile && p.max_tiles > 65535) {
+    p.tile = true;
+    p.rows = 128;
+    p.max_tiles = (int)std::min<size_t>(slots, slots / p.rows + experts);
+  }
+  size_t at = 0;
+  auto take = [&](size_t bytes) {
+    const size_t o = at;
+    at += round_up(bytes, 256);
+    return o;
+  };
+  p.h = take(slots * inner * 2);
+  if (!p.direct) {
+    p.part = take(slots * n * 4);
+    p.tiles = take((size_t)p.max_tiles * 16);
+    p.ntiles = take(4);
+    p.order = take(slots * 4);
+    p.place = take(slots * 4);
+  }
+  p.bytes = at;
+  return p;
+}
+
+tern_status check_experts(const tern_q4* up, const tern_q4* down, int m, int topk) {
+  Q4_TRY(check_shape(up));
+  Q4_TRY(check_shape(down));
+  if (m < 0) return fail(TERN_E_INVAL, "m=%d must not be negative", m);
+  if (up->count < 1 || up->count != down->count)
+    return fail(TERN_E_INVAL, "%d gate/up and %d down matrices", up->count, down->count);
+  if (up->count > 1024) return fail(TERN_E_UNSUPPORTED, "%d experts: 1024 at most", up->count);
+  if (up->n % 2 || up->n / 2 != down->k)
+    return fail(TERN_E_INVAL, "gate/up has %d rows, down k=%d: twice as many are wanted", up->n, down->k);
+  if (topk < 1) return fail(TERN_E_INVAL, "topk=%d must be positive", topk);
+  if ((long long)m * topk > 0x7fffffffll) return fail(TERN_E_UNSUPPORTED, "m=%d, topk=%d: too many slots", m, topk);
+  return TERN_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+tern_status tern_q4_check(const tern_q4* w) { return check_q4(w); }
+
+size_t tern_q4_workspace_bytes(const tern_q4* w, int32_t m) {
+  if (check_shape(w) != TERN_OK || m < 0) return 0;
+  return std::max<size_t>(256, plain_ws(m, w->n, w->k));
+}
+
+tern_status tern_q4_pack(const uint8_t* q, const tern_q4* dst, void* ws, size_t ws_bytes, void* stream) {
+  Q4_TRY(check_shape(dst));
+  const size_t words = words_of(dst);
+  if (!words) return TERN_OK;
+  Q4_TRY(check_ptr(q, true, "q", 8));
+  Q4_TRY(check_ptr(dst->codes, true, "codes", 16));
+  if (!ws || ws_bytes < 4) return fail(TERN_E_WORKSPACE, "workspace of %zu bytes, 4 are needed", ws_bytes);
+  Q4_TRY(check_ptr(ws, true, "workspace", 16));
+  const hipStream_t s = (hipStream_t)stream;
+  Q4_HIP(tern::launch_q4_pack(q, words, const_cast<uint8_t*>(dst->codes), (uint32_t*)ws, s));
+  uint32_t flag = 0;
+  Q4_HIP(hipMemcpyAsync(&flag, ws, 4, hipMemcpyDeviceToHost, s));
+  Q4_HIP(hipStreamSynchronize(s));
+  if (flag) return fail(TERN_E_INVAL, "code above 15");
+  return TERN_OK;
+}
+
+tern_status tern_q4_unpack(const tern_q4* src, uint8_t* q, void* stream) {
+  Q4_TRY(check_shape(src));
+  const size_t words = words_of(src);
+  if (!words) return TERN_OK;
+  Q4_TRY(check_ptr(src->codes, true, "codes", 16));
+  Q4_TRY(check_ptr(q, true, "q", 8));
+  Q4_HIP(tern::launch_q4_unpack(src->codes, words, q, (hipStream_t)stream));
+  return TERN_OK;
+}
+
+tern_status tern_q4_gemm(const tern_q4* w, const uint16_t* x, int32_t m, void* y, int32_t y_dtype, void* ws,
+                         size_t ws_bytes, void* stream) {
+  Q4_TRY(check_q4(w));
+  if (w->count != 1) return fail(TERN_E_INVAL, "tern_q4_gemm takes one matrix (count=%d)", w->count);
+  if (m < 0) return fail(TERN_E_INVAL, "m=%d must not be negative", m);
+  if (y_dtype != TERN_F16 && y_dtype != TERN_F32) return fail(TERN_E_UNSUPPORTED, "unknown output dtype %d", y_dtype);
+  if (m == 0 || w->n == 0) return TERN_OK;
+  Q4_TRY(check_ptr(x, w->k > 0, "x", 16));
+  Q4_TRY(check_ptr(y, true, "y", y_dtype == TERN_F32 ? 4 : 2));
+  const size_t need = plain_ws(m, w->n, w->k);
+  if (need && (!ws || ws_bytes < need))
+    return fail(TERN_E_WORKSPACE, "workspace of %zu bytes, %zu are needed", ws ? ws_bytes : (size_t)0, need);
+  if (need) Q4_TRY(check_ptr(ws, true, "workspace", 16));
+  tern::Q4Args a = args_of(w);
+  a.x = x;
+  a.y = y;
+  a.m = m;
+  a.y_f32 = y_dtype == TERN_F32;
+  const hipStream_t s = (hipStream_t)stream;
+  if (m <= kRowsMost) {
+    Q4_HIP(tern::launch_q4_rows(tern::kQ4Plain, w->group, a, 0, s));
+    return TERN_OK;
+  }
+  if ((long long)((m + 127) / 128) * ((w->n + 127) / 128) > 0x7fffffffll)
+    return fail(TERN_E_UNSUPPORTED, "m=%d, n=%d: too many tiles", m, w->n);
+  a.splits = pick_splits(m, w->n, w->k);
+  const int steps = (w->k + 127) / 128;
+  a.tps = (steps + a.splits - 1) / a.splits;
+  a.partial = (float*)ws;
+  Q4_HIP(tern::launch_q4_tile(tern::kQ4Plain, w->group, a, 0, s));
+  if (a.splits > 1) Q4_HIP(tern::launch_q4_reduce(a, s));
+  return TERN_OK;
+}
+
+size_t tern_q4_experts_workspace_bytes(const tern_q4* gate_up, const tern_q4* down, int32_t m, int32_t topk) {
+  if (check_experts(gate_up, down, m, topk) != TERN_OK) return 0;
+  return std::max<size_t>(256, plan_experts(m, topk, down->count, down->k, down->n).bytes);
+}
+
+tern_status tern_q4_experts(const tern_q4* gate_up, const tern_q4* down, const uint16_t* x, int32_t m,
+                            const int32_t* ids, const float* weights, int32_t topk, void* y, int32_t y_dtype, void* ws,
+                            size_t ws_bytes, void* stream) {
+  Q4_TRY(check_experts(gate_up, down, m, topk));
+  Q4_TRY(check_q4(gate_up));
+  Q4_TRY(check_q4(down));
+  if (y_dtype != TERN_F16 && y_dtype != TERN_F32) return fail(TERN_E_UNSUPPORTED, "unknown output dtype %d", y_dtype);
+  if (m == 0 || down->n == 0) return TERN_OK;
+  Q4_TRY(check_ptr(x, gate_up->k > 0, "x", 16));
+  Q4_TRY(check_ptr(ids, true, "ids", 4));
+  Q4_TRY(check_ptr(weights, true, "weights", 4));
+  Q4_TRY(check_ptr(y, true, "y", y_dtype == TERN_F32 ? 4 : 2));
+  const ExpertsPlan p = plan_experts(m, topk, down->count, down->k, down->n);
+  if (p.bytes && (!ws || ws_bytes < p.bytes))
+    return fail(TERN_E_WORKSPACE, "workspace of %zu bytes, %zu are needed", ws ? ws_bytes : (size_t)0, p.bytes);
+  Q4_TRY(check_ptr(ws, false, "workspace", 16));
+  const long long cols = std::max<long long>((gate_up->n / 2 + 63) / 64, (down->n + 127) / 128);
+  if (p.tile && cols * p.max_tiles > 0x7fffffffll) return fail(TERN_E_UNSUPPORTED, "m=%d, topk=%d: too many tiles", m, topk);
+  uint8_t* base = (uint8_t*)ws;
+  const hipStream_t s = (hipStream_t)stream;
+  tern::Q4Args u = args_of(gate_up), d = args_of(down);
+  u.x = x;
+  u.y = base + p.h;
+  d.x = (const uint16_t*)(base + p.h);
+  u.m = d.m = m;
+  u.ids = d.ids = ids;
+  u.gates = d.gates = weights;
+  u.topk = d.topk = topk;
+  if (p.direct) {
+    if (down->k) Q4_HIP(tern::launch_q4_rows(tern::kQ4UpSlot, gate_up->group, u, m * topk, s));
+    d.y = y;
+    d.y_f32 = y_dtype == TERN_F32;
+    Q4_HIP(tern::launch_q4_rows(tern::kQ4DownToken, down->group, d, m, s));
+    return TERN_OK;
+  }
+  u.tiles = d.tiles = (const int4*)(base + p.tiles);
+  u.ntiles = d.ntiles = (const int32_t*)(base + p.ntiles);
+  u.slots = d.slots = (const int32_t*)(base + p.order);
+  d.y = base + p.part;
+  Q4_HIP(tern::launch_q4_plan(ids, m * topk, down->count, p.rows, (int4*)(base + p.tiles), (int32_t*)(base + p.ntiles),
+                              (int32_t*)(base + p.order), (int32_t*)(base + p.place), s));
+  auto* launch = p.tile ? tern::launch_q4_tile : tern::launch_q4_rows;
+  if (down->k) Q4_HIP(launch(tern::kQ4Up, gate_up->group, u, p.max_tiles, s));
+  Q4_HIP(launch(tern::kQ4Down, down->group, d, p.max_tiles, s));
+  Q4_HIP(tern::launch_q4_combine((const float*)(base + p.part), (const int32_t*)(base + p.place), weights, m, topk,
+                                 down->n, y, y_dtype == TERN_F32, s));
+  return TERN_OK;
+}
+
+tern_status tern_route(const void* logits, int32_t l_dtype, int32_t m, const tern_router* r, int32_t* ids,
+                       float* weights, void* stream) {
+  if (!r) return fail(TERN_E_INVAL, "router descriptor is NULL");
+  if (m < 0) return fail(TERN_E_INVAL, "m=%d must not be negative", m);
+  if (l_dtype != TERN_F16 && l_dtype != TERN_F32) return fail(TERN_E_UNSUPPORTED, "unknown logits dtype %d", l_dtype);
+  if (r->score != TERN_SCORE_SOFTMAX && r->score != TERN_SCORE_SIGMOID)
+    return fail(TERN_E_UNSUPPORTED, "unknown score %d", r->score);
+  if (r->experts < 1 || r->groups < 1 || r->experts % r->groups)
+    return fail(TERN_E_INVAL, "%d experts in %d groups", r->experts, r->groups);
+  if (r->experts > 1024 || r->groups > 64)
+    return fail(TERN_E_UNSUPPORTED, "%d experts in %d groups: 1024 in 64 at most", r->experts, r->groups);
+  if (r->keep_groups < 1 || r->keep_groups > r->groups)
+    return fail(TERN_E_INVAL, "keep_groups=%d of %d groups", r->keep_groups, r->groups);
+  if (r->group_best != 1 && r->group_best != 2)
+    return fail(TERN_E_UNSUPPORTED, "group_best=%d is not 1 or 2", r->group_best);
+  if (r->topk < 1 || r->topk > r->keep_groups * (r->experts / r->groups))
+    return fail(TERN_E_INVAL, "topk=%d of %d experts", r->topk, r->keep_groups * (r->experts / r->groups));
+  if (r->topk > 64) return fail(TERN_E_UNSUPPORTED, "topk=%d: 64 at most", r->topk);
+  if (m == 0) return TERN_OK;
+  Q4_TRY(check_ptr(logits, true, "logits", l_dtype == TERN_F32 ? 4 : 2));
+  Q4_TRY(check_ptr(r->bias, false, "bias", 4));
+  Q4_TRY(check_ptr(ids, true, "ids", 4));
+  Q4_TRY(check_ptr(weights, true, "weights", 4));
+  tern::RouteArgs a = {};
+  a.logits = logits;
+  a.bias = r->bias;
+  a.ids = ids;
+  a.weights = weights;
+  a.m = m;
+  a.experts = r->experts;
+  a.topk = r->topk;
+  a.groups = r->groups;
+  a.best = r->group_best;
+  a.keep = r->keep_groups;
+  a.renorm = r->renorm != 0;
+  a.sigmoid = r->score == TERN_SCORE_SIGMOID;
+  a.scale = r->scale;
+  Q4_HIP(tern::launch_route(a, l_dtype == TERN_F16, (hipStream_t)stream));
+  return TERN_OK;
+}
+
+}  // extern "C"

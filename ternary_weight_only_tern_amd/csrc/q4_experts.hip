@@ -1,0 +1,131 @@
+// The routed experts' bookkeeping around the products of q4_rows.hip and
+// q4_tile.hip (which tile of rows belongs to which expert, the weighted sum
+// of a token's slots), and the packing of 4-bit codes.
+#include "q4.h"
+
+namespace tern {
+namespace {
+
+constexpr int kPlanThreads = 1024;
+
+// Sorts the slots by expert: order[position] = slot, place[slot] = position
+// (-1 for a slot that names no expert), and cuts every expert's positions
+// into tiles of at most `rows`.  One workgroup.  Where inside its expert a
+// slot lands depends on the order of the LDS atomics, but a row's result does
+// not depend on its place: the matrix instructions' rows are independent.
+__global__ __launch_bounds__(kPlanThreads) void q4_plan_kernel(const int32_t* ids, int slots, int experts, int rows,
+                                                               int4* tiles, int32_t* ntiles, int32_t* order,
+                                                               int32_t* place) {
+  __shared__ int count[kPlanThreads], first[kPlanThreads], tile0[kPlanThreads];
+  const int t = threadIdx.x;
+  count[t] = 0;
+  __syncthreads();
+  for (int s = t; s < slots; s += kPlanThreads) {
+    const int e = ids[s];
+    if ((unsigned)e < (unsigned)experts) atomicAdd(&count[e], 1);
+  }
+  __syncthreads();
+  const int mine = count[t], tl = (mine + rows - 1) / rows;
+  first[t] = mine;
+  tile0[t] = tl;
+  __syncthreads();
+  for (int d = 1; d < kPlanThreads; d <<= 1) {
+    const int a = t >= d ? first[t - d] : 0, b = t >= d ? tile0[t - d] : 0;
+    __syncthreads();
+    first[t] += a;
+    tile0[t] += b;
+    __syncthreads();
+  }
+  const int f = first[t] - mine, q = tile0[t] - tl;
+  if (t == kPlanThreads - 1) *ntiles = tile0[t];
+  __syncthreads();
+  count[t] = f;
+  for (int i = 0; i < tl; ++i) tiles[q + i] = make_int4(t, f + i * rows, min(rows, mine - i * rows), 0);
+  __syncthreads();
+  for (int s = t; s < slots; s += kPlanThreads) {
+    const int e = ids[s];
+    int p = -1;
+    if ((unsigned)e < (unsigned)experts) {
+      p = atomicAdd(&count[e], 1);
+      order[p] = s;
+    }
+    place[s] = p;
+  }
+}
+
+// y[token] = sum over its slots, in slot order, of gate * part[place].
+__global__ __launch_bounds__(256) void q4_combine_kernel(const float* part, const int32_t* place, const float* gates,
+                                                         int topk, int n, void* y, int y_f32) {
+  const int token = blockIdx.x;
+  for (int c = threadIdx.x; c < n; c += 256) {
+    float sum = 0.f;
+    for (int j = 0; j < topk; ++j) {
+      const int p = place[(size_t)token * topk + j];
+      if (p >= 0) sum += gates[(size_t)token * topk + j] * part[(size_t)p * n + c];
+    }
+    const size_t dst = (size_t)token * n + c;
+    if (y_f32)
+      reinterpret_cast<float*>(y)[dst] = sum;
+    else
+      reinterpret_cast<_Float16*>(y)[dst] = (_Float16)sum;
+  }
+}
+
+// Eight codes (one byte each) to a word: offset o in bits 16 (o % 2) + 4 (o / 2).
+__global__ __launch_bounds__(256) void q4_pack_kernel(const uint8_t* q, size_t words, uint8_t* codes, uint32_t* flag) {
+  const size_t step = (size_t)gridDim.x * 256;
+  for (size_t i = (size_t)blockIdx.x * 256 + threadIdx.x; i < words; i += step) {
+    const w2_t v = reinterpret_cast<const w2_t*>(q)[i];
+    uint32_t word = 0;
+#pragma unroll
+    for (int o = 0; o < 8; ++o) word |= ((((o < 4 ? v.x : v.y) >> (8 * (o % 4))) & 15u)) << (16 * (o % 2) + 4 * (o / 2));
+    if ((v.x | v.y) & 0xF0F0F0F0u) *flag = 1;
+    reinterpret_cast<uint32_t*>(codes)[i] = word;
+  }
+}
+
+__global__ __launch_bounds__(256) void q4_unpack_kernel(const uint8_t* codes, size_t words, uint8_t* q) {
+  const size_t step = (size_t)gridDim.x * 256;
+  for (size_t i = (size_t)blockIdx.x * 256 + threadIdx.x; i < words; i += step) {
+    const uint32_t word = reinterpret_cast<const uint32_t*>(codes)[i];
+    uint32_t v[2] = {0, 0};
+#pragma unroll
+    for (int o = 0; o < 8; ++o) v[o / 4] |= ((word >> (16 * (o % 2) + 4 * (o / 2))) & 15u) << (8 * (o % 4));
+    reinterpret_cast<w2_t*>(q)[i] = w2_t{v[0], v[1]};
+  }
+}
+
+__global__ void q4_clear_kernel(uint32_t* flag) { *flag = 0; }
+
+unsigned blocks_for(size_t items) {
+  const size_t b = (items + 255) / 256;
+  return (unsigned)(b < 8192 ? b : 8192);
+}
+
+}  // namespace
+
+hipError_t launch_q4_plan(const int32_t* ids, int slots, int experts, int rows, int4* tiles, int32_t* ntiles,
+                          int32_t* order, int32_t* place, hipStream_t s) {
+  hipLaunchKernelGGL(q4_plan_kernel, dim3(1), dim3(kPlanThreads), 0, s, ids, slots, experts, rows, tiles, ntiles, order,
+                     place);
+  return hipGetLastError();
+}
+
+hipError_t launch_q4_combine(const float* part, const int32_t* place, const float* gates, int m, int topk, int n,
+                             void* y, int y_f32, hipStream_t s) {
+  hipLaunchKernelGGL(q4_combine_kernel, dim3((unsigned)m), dim3(256), 0, s, part, place, gates, topk, n, y, y_f32);
+  return hipGetLastError();
+}
+
+hipError_t launch_q4_pack(const uint8_t* q, size_t words, uint8_t* codes, uint32_t* flag, hipStream_t s) {
+  hipLaunchKernelGGL(q4_clear_kernel, dim3(1), dim3(1), 0, s, flag);
+  if (words) hipLaunchKernelGGL(q4_pack_kernel, dim3(blocks_for(words)), dim3(256), 0, s, q, words, codes, flag);
+  return hipGetLastError();
+}
+
+hipError_t launch_q4_unpack(const uint8_t* codes, size_t words, uint8_t* q, hipStream_t s) {
+  if (words) hipLaunchKernelGGL(q4_unpack_kernel, dim3(blocks_for(words)), dim3(256), 0, s, codes, words, q);
+  return hipGetLastError();
+}
+
+}  // namespace tern

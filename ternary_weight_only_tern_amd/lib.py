@@ -9,7 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from ctypes import POINTER, c_double, c_int32, c_size_t, c_uint32, c_void_p
+from ctypes import POINTER, c_double, c_float, c_int32, c_size_t, c_uint32, c_void_p
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libtern.so")
@@ -29,6 +29,8 @@ TERN_OFF_ROW = 1
 TERN_OFF_GROUP = 2
 TERN_F16 = 0
 TERN_F32 = 1
+TERN_SCORE_SOFTMAX = 0
+TERN_SCORE_SIGMOID = 1
 
 (TERN_BUF_PLANE0, TERN_BUF_SCALE0, TERN_BUF_OFFSET, TERN_BUF_MASK, TERN_BUF_ROWPTR,
  TERN_BUF_BLOCKS1, TERN_BUF_BLOCKS2, TERN_BUF_RSCALE1, TERN_BUF_RSCALE2, TERN_NBUF) = range(10)
@@ -37,7 +39,9 @@ SYMBOLS = ["tern_row_stride", "tern_check", "tern_packed_sizes", "tern_workspace
            "tern_pack", "tern_unpack", "tern_gemv", "tern_gemm", "tern_batch_workspace_bytes",
            "tern_gemv_batched", "tern_plan_create", "tern_plan_run", "tern_plan_run_events", "tern_plan_launches", "tern_plan_destroy", "tern_b3_min_stages", "tern_gemv_noalloc",
            "tern_rotated_workspace_bytes", "tern_plan_create_rotated",
-           "tern_bits", "tern_quantize", "tern_rotate", "tern_rotate_batched", "tern_read_probe", "tern_status_str", "tern_last_error"]
+           "tern_bits", "tern_quantize", "tern_rotate", "tern_rotate_batched", "tern_q4_check", "tern_q4_pack", "tern_q4_unpack", "tern_q4_workspace_bytes", "tern_q4_gemm",
+           "tern_route", "tern_q4_experts_workspace_bytes", "tern_q4_experts",
+           "tern_read_probe", "tern_status_str", "tern_last_error"]
 
 
 class tern_matrix(ctypes.Structure):
@@ -46,6 +50,17 @@ class tern_matrix(ctypes.Structure):
                 ("plane0", c_void_p), ("scale0", c_void_p),
                 ("mask", c_void_p * 2), ("rowptr", c_void_p * 2), ("blocks", c_void_p * 2),
                 ("rscale", c_void_p * 2), ("offset", c_void_p), ("nnz", c_uint32 * 2)]
+
+
+class tern_q4(ctypes.Structure):
+    _fields_ = [("n", c_int32), ("k", c_int32), ("group", c_int32), ("count", c_int32),
+                ("codes", c_void_p), ("scale", c_void_p), ("zero", c_void_p)]
+
+
+class tern_router(ctypes.Structure):
+    _fields_ = [("experts", c_int32), ("topk", c_int32), ("score", c_int32), ("groups", c_int32),
+                ("group_best", c_int32), ("keep_groups", c_int32), ("renorm", c_int32), ("scale", c_float),
+                ("bias", c_void_p)]
 
 
 class TernError(RuntimeError):
@@ -93,6 +108,15 @@ def load() -> ctypes.CDLL:
         "tern_rotate": (c_int32, [c_void_p, c_int32, c_void_p, c_int32, c_int32, c_void_p, c_void_p]),
         "tern_rotate_batched": (c_int32, [c_int32, POINTER(c_void_p), c_int32, POINTER(c_void_p), POINTER(c_int32),
                                           c_int32, POINTER(c_void_p), c_void_p]),
+        "tern_q4_check": (c_int32, [c_void_p]),
+        "tern_q4_pack": (c_int32, [c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
+        "tern_q4_unpack": (c_int32, [c_void_p, c_void_p, c_void_p]),
+        "tern_q4_workspace_bytes": (c_size_t, [c_void_p, c_int32]),
+        "tern_q4_gemm": (c_int32, [c_void_p, c_void_p, c_int32, c_void_p, c_int32, c_void_p, c_size_t, c_void_p]),
+        "tern_route": (c_int32, [c_void_p, c_int32, c_int32, c_void_p, c_void_p, c_void_p, c_void_p]),
+        "tern_q4_experts_workspace_bytes": (c_size_t, [c_void_p, c_void_p, c_int32, c_int32]),
+        "tern_q4_experts": (c_int32, [c_void_p, c_void_p, c_void_p, c_int32, c_void_p, c_void_p, c_int32, c_void_p,
+                                      c_int32, c_void_p, c_size_t, c_void_p]),
         "tern_read_probe": (c_int32, [c_void_p, c_size_t, c_void_p, c_void_p]),
         "tern_status_str": (ctypes.c_char_p, [c_int32]),
         "tern_last_error": (ctypes.c_char_p, []),
@@ -381,6 +405,236 @@ def tern_rotate_batched(Rs, xs, outs=None, stream=None):
     kk = (c_int32 * max(n, 1))(*[x.shape[1] for x in xs])
     check(load().tern_rotate_batched(n, rp, block, xp, kk, m, op, _stream(stream)))
     return outs
+
+
+# ---------------------------------------------------------------- 4-bit weights, routing, experts
+def _refuse(what: str):
+    raise ValueError(what)
+
+
+def _tensor(t, name, dtypes, device, shape=None):
+    """Checks a device tensor argument: its type, device, layout and shape."""
+    if t.dtype not in dtypes:
+        _refuse(f"{name} is {t.dtype}, not {' or '.join(str(d) for d in dtypes)}")
+    if t.device != device:
+        _refuse(f"{name} is on {t.device}, not {device}")
+    if not t.is_contiguous():
+        _refuse(f"{name} is not contiguous")
+    if shape is not None and t.shape != shape:
+        _refuse(f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
+    return t
+
+
+class _On:
+    """The device of a call's tensors made current while it runs."""
+
+    def __init__(self, device):
+        import torch
+        self.other = device.index != torch.cuda.current_device()
+        self.guard = torch.cuda.device(device) if self.other else None
+
+    def __enter__(self):
+        if self.other:
+            self.guard.__enter__()
+
+    def __exit__(self, *exc):
+        if self.other:
+            self.guard.__exit__(*exc)
+
+
+def _fresh(shape, dtype, device, stream):
+    """An uninitialised tensor for a call on `stream`.  When that is a stream
+    of the caller's, it first waits for torch's current stream (where the
+    memory may still be in use), and the allocator is told that it uses the
+    tensor, so that the memory is not handed out again before the call is
+    done."""
+    import torch
+    t = torch.empty(shape, dtype=dtype, device=device)
+    if stream is not None:
+        ext = torch.cuda.ExternalStream(stream, device=t.device)
+        ext.wait_stream(torch.cuda.current_stream(t.device))
+        t.record_stream(ext)
+    return t
+
+
+def _scratch(nbytes, device, stream):
+    import torch
+    return _fresh(max(nbytes, 256), torch.uint8, device, stream)
+
+
+class Q4Matrix:
+    """4-bit weights on the device: codes uint8 [n][k/2] in tern_q4's word
+    order, scale fp16 [n][k/group], zero uint8 [n][k/group] or None (8
+    everywhere); or a stack of them, [count][n][...] in every array.  Keeps
+    the tensors; makes no copy."""
+
+    def __init__(self, codes, scale, zero=None):
+        import torch
+        if codes.dim() not in (2, 3) or scale.dim() != codes.dim() or codes.shape[:-1] != scale.shape[:-1]:
+            _refuse(f"codes {tuple(codes.shape)} and scale {tuple(scale.shape)} are no 4-bit matrix")
+        if codes.device.type != "cuda":
+            _refuse(f"codes are on {codes.device}, not on a GPU")
+        _tensor(codes, "codes", (torch.uint8,), codes.device)
+        _tensor(scale, "scale", (torch.float16,), codes.device)
+        if zero is not None:
+            _tensor(zero, "zero", (torch.uint8,), codes.device, scale.shape)
+        self.codes, self.scale, self.zero = codes, scale, zero
+        self.device = codes.device
+        self.n, self.k = codes.shape[-2], 2 * codes.shape[-1]
+        self.count = codes.shape[0] if codes.dim() == 3 else 1
+        ng = scale.shape[-1]
+        if self.k and (ng < 1 or self.k % ng):
+            _refuse(f"k={self.k} in {ng} groups")
+        self.group = self.k // ng if self.k else 128
+        self._desc = tern_q4(self.n, self.k, self.group, self.count, _ptr(codes), _ptr(scale), _ptr(zero))
+        self._at = ctypes.addressof(self._desc)
+        check(load().tern_q4_check(self._at))
+
+    @classmethod
+    def from_codes(cls, q, scale, zero=None, stream=None):
+        """tern_q4_pack: from codes 0..15 of one byte each, uint8 [n][k] (or
+        [count][n][k])."""
+        import torch
+        if q.device.type != "cuda":
+            _refuse(f"q is on {q.device}, not on a GPU")
+        if q.dim() not in (2, 3) or q.shape[-1] % 2:
+            _refuse(f"codes of shape {tuple(q.shape)}")
+        _tensor(q, "q", (torch.uint8,), q.device)
+        codes = _fresh((*q.shape[:-1], q.shape[-1] // 2), torch.uint8, q.device, stream)
+        self = cls(codes, scale, zero)
+        with _On(self.device):
+            ws = _scratch(256, self.device, stream)
+            check(load().tern_q4_pack(_ptr(q), self._at, _ptr(ws), ws.numel(), _stream_of(self.device, stream)))
+        return self
+
+    def unpack(self, stream=None):
+        """tern_q4_unpack: the codes, one byte each."""
+        import torch
+        q = _fresh((*self.codes.shape[:-1], self.k), torch.uint8, self.device, stream)
+        with _On(self.device):
+            check(load().tern_q4_unpack(self._at, _ptr(q), _stream_of(self.device, stream)))
+        return q
+
+
+def _stream_of(device, stream):
+    if stream is not None:
+        return stream
+    import torch
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+def _y_type(y_dtype):
+    import torch
+    if y_dtype not in (TERN_F16, TERN_F32):
+        _refuse(f"unknown output dtype {y_dtype}")
+    return torch.float32 if y_dtype == TERN_F32 else torch.float16
+
+
+def tern_q4_workspace(w: Q4Matrix, m: int):
+    """A workspace for tern_q4_gemm with m activation rows."""
+    return _scratch(load().tern_q4_workspace_bytes(w._at, m), w.device, None)
+
+
+def tern_q4_gemm(w: Q4Matrix, x, y_dtype=TERN_F16, out=None, stream=None, ws=None):
+    """y = x W^T (x fp16 [m][k], contiguous); returns y [m][n], fp16 or fp32
+    per y_dtype, in `out` if given."""
+    import torch
+    _tensor(x, "x", (torch.float16,), w.device)
+    if x.dim() != 2 or x.shape[1] != w.k:
+        _refuse(f"x has shape {tuple(x.shape)}, not [m][{w.k}]")
+    m = x.shape[0]
+    kind = _y_type(y_dtype)
+    with _On(w.device):
+        if out is None:
+            out = _fresh((m, w.n), kind, w.device, stream)
+        else:
+            _tensor(out, "out", (kind,), w.device, (m, w.n))
+        if ws is None:
+            ws = _scratch(load().tern_q4_workspace_bytes(w._at, m), w.device, stream)
+        check(load().tern_q4_gemm(w._at, _ptr(x), m, _ptr(out), y_dtype, _ptr(ws), ws.numel(),
+                                  _stream_of(w.device, stream)))
+    return out
+
+
+def tern_route(logits, topk, score=TERN_SCORE_SOFTMAX, bias=None, groups=1, group_best=1, keep_groups=1, renorm=True,
+               scale=1.0, ids=None, weights=None, stream=None):
+    """Routes tokens to experts: (ids int32 [m][topk], weights fp32
+    [m][topk]) from logits fp16 or fp32 [m][experts], contiguous."""
+    import torch
+    if logits.device.type != "cuda" or logits.dim() != 2:
+        _refuse(f"logits of shape {tuple(logits.shape)} on {logits.device}, not [m][experts] on a GPU")
+    device = logits.device
+    _tensor(logits, "logits", (torch.float16, torch.float32), device)
+    m, experts = logits.shape
+    if bias is not None:
+        _tensor(bias, "bias", (torch.float32,), device, (experts,))
+    with _On(device):
+        if ids is None:
+            ids = _fresh((m, max(topk, 0)), torch.int32, device, stream)
+        else:
+            _tensor(ids, "ids", (torch.int32,), device, (m, topk))
+        if weights is None:
+            weights = _fresh((m, max(topk, 0)), torch.float32, device, stream)
+        else:
+            _tensor(weights, "weights", (torch.float32,), device, (m, topk))
+        r = tern_router(experts, topk, score, groups, group_best, keep_groups, int(bool(renorm)), scale, _ptr(bias))
+        check(load().tern_route(_ptr(logits), TERN_F32 if logits.dtype == torch.float32 else TERN_F16, m,
+                                ctypes.addressof(r), _ptr(ids), _ptr(weights), _stream_of(device, stream)))
+    return ids, weights
+
+
+def tern_q4_experts_workspace(gate_up: Q4Matrix, down: Q4Matrix, m: int, topk: int):
+    """A workspace for tern_q4_experts with m tokens of topk slots."""
+    return _scratch(load().tern_q4_experts_workspace_bytes(gate_up._at, down._at, m, topk), down.device, None)
+
+
+def tern_q4_experts(gate_up: Q4Matrix, down: Q4Matrix, x, ids, weights, y_dtype=TERN_F16, out=None, stream=None,
+                    ws=None):
+    """The routed experts' layer: y [m][down.n] from x fp16 [m][gate_up.k],
+    ids int32 and weights fp32 [m][topk] (as tern_route returns them)."""
+    import torch
+    device = gate_up.device
+    _tensor(x, "x", (torch.float16,), device)
+    if down.device != device:
+        _refuse(f"down is on {down.device}, not {device}")
+    if x.dim() != 2 or x.shape[1] != gate_up.k:
+        _refuse(f"x has shape {tuple(x.shape)}, not [m][{gate_up.k}]")
+    m = x.shape[0]
+    _tensor(ids, "ids", (torch.int32,), device)
+    if ids.dim() != 2 or ids.shape[0] != m:
+        _refuse(f"ids have shape {tuple(ids.shape)}, not [{m}][topk]")
+    _tensor(weights, "weights", (torch.float32,), device, ids.shape)
+    topk = ids.shape[1]
+    kind = _y_type(y_dtype)
+    with _On(device):
+        if out is None:
+            out = _fresh((m, down.n), kind, device, stream)
+        else:
+            _tensor(out, "out", (kind,), device, (m, down.n))
+        if ws is None:
+            ws = _scratch(load().tern_q4_experts_workspace_bytes(gate_up._at, down._at, m, topk), device, stream)
+        check(load().tern_q4_experts(gate_up._at, down._at, _ptr(x), m, _ptr(ids), _ptr(weights), topk, _ptr(out),
+                                     y_dtype, _ptr(ws), ws.numel(), _stream_of(device, stream)))
+    return out
+
+
+class Q4Experts:
+    """A layer of experts with its router's settings: run() routes the tokens
+    by their logits (tern_route) and applies their experts
+    (tern_q4_experts)."""
+
+    def __init__(self, gate_up: Q4Matrix, down: Q4Matrix, topk, score=TERN_SCORE_SOFTMAX, bias=None, groups=1,
+                 group_best=1, keep_groups=1, renorm=True, scale=1.0):
+        self.gate_up, self.down, self.topk = gate_up, down, topk
+        self._route = dict(score=score, bias=bias, groups=groups, group_best=group_best, keep_groups=keep_groups,
+                           renorm=renorm, scale=scale)
+
+    def run(self, x, logits, y_dtype=TERN_F16, out=None, stream=None, ws=None):
+        """y [m][down.n] for x fp16 [m][k] and logits [m][experts]."""
+        if tuple(logits.shape) != (x.shape[0], self.down.count):
+            _refuse(f"logits have shape {tuple(logits.shape)}, not {(x.shape[0], self.down.count)}")
+        ids, weights = tern_route(logits, self.topk, stream=stream, **self._route)
+        return tern_q4_experts(self.gate_up, self.down, x, ids, weights, y_dtype, out, stream, ws)
 
 
 def tern_read_probe(buf, sink, stream=None) -> None:

@@ -1,0 +1,109 @@
+"""Argument errors of the 4-bit layers' C ABI, answered without a GPU."""
+import ctypes
+
+import pytest
+
+from ternary_weight_only_tern_amd import lib as L
+
+P = ctypes.c_void_p
+
+
+def q4(n=64, k=256, group=64, count=1, codes=0x10000, scale=0x20000, zero=None):
+    return L.tern_q4(n, k, group, count, codes, scale, zero)
+
+
+def at(d):
+    return ctypes.addressof(d)
+
+
+@pytest.mark.parametrize("kw,want", [
+    ({}, L.TERN_OK), (dict(group=32), L.TERN_OK), (dict(k=0, codes=None, scale=None), L.TERN_OK),
+    (dict(n=0, codes=None, scale=None), L.TERN_OK),
+    (dict(n=-1), L.TERN_E_INVAL), (dict(k=-64), L.TERN_E_INVAL), (dict(count=-1), L.TERN_E_INVAL),
+    (dict(group=16), L.TERN_E_UNSUPPORTED), (dict(group=96), L.TERN_E_UNSUPPORTED), (dict(group=0), L.TERN_E_UNSUPPORTED),
+    (dict(group=256), L.TERN_E_UNSUPPORTED), (dict(k=96), L.TERN_E_UNSUPPORTED), (dict(n=0x7fffffff), L.TERN_E_UNSUPPORTED),
+    (dict(codes=None), L.TERN_E_INVAL), (dict(scale=None), L.TERN_E_INVAL),
+    (dict(codes=0x10008), L.TERN_E_ALIGN), (dict(scale=0x20001), L.TERN_E_ALIGN)])
+def test_check(kw, want):
+    d = q4(**kw)
+    assert L.load().tern_q4_check(at(d)) == want
+
+
+def test_null_descriptor():
+    lib = L.load()
+    assert lib.tern_q4_check(None) == L.TERN_E_INVAL
+    assert lib.tern_q4_workspace_bytes(None, 1) == 0
+    assert lib.tern_route(P(16), 0, 1, None, P(16), P(16), None) == L.TERN_E_INVAL
+
+
+def test_gemm_refusals():
+    lib = L.load()
+    d = q4(n=64, k=4096)
+    g = lambda x=0x1000, m=1, y=0x2000, dt=0, ws=0x3000, nb=1 << 30, d=d: lib.tern_q4_gemm(at(d), x, m, y, dt, ws, nb, None)
+    assert g(m=-1) == L.TERN_E_INVAL
+    assert g(x=None) == L.TERN_E_INVAL and g(y=None) == L.TERN_E_INVAL
+    assert g(x=0x1008) == L.TERN_E_ALIGN and g(y=0x2001) == L.TERN_E_ALIGN and g(y=0x2002, dt=1) == L.TERN_E_ALIGN
+    assert g(dt=2) == L.TERN_E_UNSUPPORTED
+    assert g(d=q4(count=2)) == L.TERN_E_INVAL
+    assert g(m=0, x=None, y=None) == L.TERN_OK
+    assert g(d=q4(n=0), x=None, y=None) == L.TERN_OK
+    need = lib.tern_q4_workspace_bytes(at(d), 100)
+    assert need > 256
+    assert g(m=100, nb=need - 1) == L.TERN_E_WORKSPACE and g(m=100, ws=None) == L.TERN_E_WORKSPACE
+    assert g(m=100, ws=0x3008) == L.TERN_E_ALIGN
+
+
+def test_pack_refusals():
+    lib = L.load()
+    d = q4()
+    assert lib.tern_q4_pack(None, at(d), 0x1000, 256, None) == L.TERN_E_INVAL
+    assert lib.tern_q4_pack(0x1004, at(d), 0x1000, 256, None) == L.TERN_E_ALIGN
+    assert lib.tern_q4_pack(0x1000, at(d), None, 0, None) == L.TERN_E_WORKSPACE
+    assert lib.tern_q4_unpack(at(d), None, None) == L.TERN_E_INVAL
+    assert lib.tern_q4_unpack(at(q4(n=0)), None, None) == L.TERN_OK
+
+
+ROUTER = dict(experts=64, topk=8, score=1, groups=8, group_best=2, keep_groups=4, renorm=1, scale=1.0, bias=None)
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(experts=0), L.TERN_E_INVAL), (dict(experts=60), L.TERN_E_INVAL), (dict(groups=0), L.TERN_E_INVAL),
+    (dict(experts=2048), L.TERN_E_UNSUPPORTED), (dict(experts=256, groups=128), L.TERN_E_UNSUPPORTED),
+    (dict(keep_groups=0), L.TERN_E_INVAL), (dict(keep_groups=9), L.TERN_E_INVAL),
+    (dict(group_best=0), L.TERN_E_UNSUPPORTED), (dict(group_best=3), L.TERN_E_UNSUPPORTED),
+    (dict(topk=0), L.TERN_E_INVAL), (dict(topk=33), L.TERN_E_INVAL), (dict(score=2), L.TERN_E_UNSUPPORTED),
+    (dict(experts=1024, topk=65), L.TERN_E_UNSUPPORTED), (dict(bias=0x1002), L.TERN_E_ALIGN)])
+def test_route_refusals(kw, want):
+    r = L.tern_router(**{**ROUTER, **kw})
+    assert L.load().tern_route(0x1000, 1, 4, at(r), 0x2000, 0x3000, None) == want
+
+
+def test_route_pointers():
+    lib = L.load()
+    r = L.tern_router(**ROUTER)
+    f = lambda l=0x1000, dt=1, m=4, ids=0x2000, w=0x3000: lib.tern_route(l, dt, m, at(r), ids, w, None)
+    assert f(l=None) == L.TERN_E_INVAL and f(ids=None) == L.TERN_E_INVAL and f(w=None) == L.TERN_E_INVAL
+    assert f(l=0x1002) == L.TERN_E_ALIGN and f(ids=0x2002) == L.TERN_E_ALIGN and f(dt=5) == L.TERN_E_UNSUPPORTED
+    assert f(m=-1) == L.TERN_E_INVAL and f(m=0, l=None) == L.TERN_OK
+
+
+def test_experts_refusals():
+    lib = L.load()
+    up, down = q4(n=128, k=256, count=4), q4(n=96, k=64, count=4)
+    need = lib.tern_q4_experts_workspace_bytes(at(up), at(down), 10, 2)
+    assert need > 0
+
+    def f(up=up, down=down, x=0x1000, m=10, ids=0x2000, w=0x3000, topk=2, y=0x4000, dt=0, ws=0x5000, nb=need):
+        return lib.tern_q4_experts(at(up), at(down), x, m, ids, w, topk, y, dt, ws, nb, None)
+
+    assert f(m=-1) == L.TERN_E_INVAL and f(topk=0) == L.TERN_E_INVAL
+    assert f(up=q4(n=128, k=256, count=5)) == L.TERN_E_INVAL
+    assert f(up=q4(n=130, k=256, count=4)) == L.TERN_E_INVAL and f(up=q4(n=129, k=256, count=4)) == L.TERN_E_INVAL
+    assert f(up=q4(n=128, count=0), down=q4(k=64, count=0)) == L.TERN_E_INVAL
+    assert f(up=q4(n=128, count=2000), down=q4(k=64, count=2000)) == L.TERN_E_UNSUPPORTED
+    assert f(m=1 << 30, topk=2) == L.TERN_E_UNSUPPORTED
+    for kw in (dict(x=None), dict(ids=None), dict(w=None), dict(y=None)):
+        assert f(**kw) == L.TERN_E_INVAL
+    assert f(x=0x1008) == L.TERN_E_ALIGN and f(ids=0x2002) == L.TERN_E_ALIGN and f(ws=0x5008) == L.TERN_E_ALIGN
+    assert f(dt=9) == L.TERN_E_UNSUPPORTED and f(nb=need - 1) == L.TERN_E_WORKSPACE and f(ws=None) == L.TERN_E_WORKSPACE
+    assert f(m=0, x=None, ids=None, w=None, y=None, ws=None, nb=0) == L.TERN_OK
