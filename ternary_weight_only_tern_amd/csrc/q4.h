@@ -20,7 +20,7 @@ namespace tern {
 typedef _Float16 h2_t __attribute__((ext_vector_type(2)));
 typedef _Float16 h8_t __attribute__((ext_vector_type(8)));
 typedef float f4_t __attribute__((ext_vector_type(4)));
-typedef float f16_t __attribute__((ext_vector_type(16)));
+typedef float a16_t __attribute__((ext_vector_type(16)));
 typedef uint32_t w2_t __attribute__((ext_vector_type(2)));
 typedef uint32_t w4_t __attribute__((ext_vector_type(4)));
 
@@ -77,26 +77,31 @@ hipError_t launch_route(const RouteArgs& a, int f16, hipStream_t s);
 // ---------------------------------------------------------------- device code
 __device__ inline h2_t as_h2(uint32_t v) { return __builtin_bit_cast(h2_t, v); }
 
-// The constants that turn 1024 + q and 1024 + 16 q into q - z.
+// What turns 1024 + q and 1024 + 16 q into q - z, and the two bit patterns of
+// q4_decode, kept in registers: v_and_or_b32 takes no literal.
 struct Q4Bias {
   h2_t lo, hi;  // -(1024 + z), -(64 + z)
 };
-__device__ inline Q4Bias q4_bias(int z) {
-  const _Float16 l = (_Float16)(-(1024 + z)), h = (_Float16)(-(64 + z));
+__device__ inline Q4Bias q4_bias(uint32_t z) {  // 0..255
+  const _Float16 l = __builtin_bit_cast(_Float16, (uint16_t)(0xE400u | z));
+  const _Float16 h = l + (_Float16)960.0f;
   return {h2_t{l, l}, h2_t{h, h}};
 }
+struct Q4Masks {
+  uint32_t lo = 0x000F000Fu, hi = 0x00F000F0u, one = 0x64006400u;
+  __device__ inline Q4Masks() { asm("" : "+v"(lo), "+v"(hi), "+s"(one)); }
+};
 
 // Eight codes of a word to FP16 q - z, in k order.  A code ORed into the low
 // mantissa bits of 1024.0 is 1024 + q, into bits 4..7 1024 + 16 q; both
 // steps back are exact.  Nine VALU operations per word.
-__device__ inline h8_t q4_decode(uint32_t w, const Q4Bias& b) {
-  constexpr uint32_t kOne = 0x64006400u;
+__device__ inline h8_t q4_decode(uint32_t w, const Q4Bias& b, const Q4Masks& m) {
   const h2_t six = {(_Float16)0.0625f, (_Float16)0.0625f};
   const uint32_t v = w >> 8;
-  const h2_t p0 = as_h2((w & 0x000F000Fu) | kOne) + b.lo;
-  const h2_t p1 = as_h2((w & 0x00F000F0u) | kOne) * six + b.hi;
-  const h2_t p2 = as_h2((v & 0x000F000Fu) | kOne) + b.lo;
-  const h2_t p3 = as_h2((v & 0x00F000F0u) | kOne) * six + b.hi;
+  const h2_t p0 = as_h2((w & m.lo) | m.one) + b.lo;
+  const h2_t p1 = as_h2((w & m.hi) | m.one) * six + b.hi;
+  const h2_t p2 = as_h2((v & m.lo) | m.one) + b.lo;
+  const h2_t p3 = as_h2((v & m.hi) | m.one) * six + b.hi;
   return h8_t{p0.x, p0.y, p1.x, p1.y, p2.x, p2.y, p3.x, p3.y};
 }
 

@@ -47,8 +47,8 @@ tern_status check_shape(const tern_q4* w) {
   if (w->group != 32 && w->group != 64 && w->group != 128)
     return fail(TERN_E_UNSUPPORTED, "4-bit group %d is not 32, 64 or 128", w->group);
   if (w->k % w->group) return fail(TERN_E_UNSUPPORTED, "k=%d must be a multiple of group %d", w->k, w->group);
-  // the kernels round k up to a step of 128 and n up to a tile
-  if (w->k > 0x7fffff00 || w->n > 0x7fffff00) return fail(TERN_E_UNSUPPORTED, "n=%d or k=%d is too large", w->n, w->k);
+  // buffer descriptors hold 16 weight rows or 32 activation rows; n is rounded up to a tile
+  if (w->k > (1 << 24) || w->n > 0x7fffff00) return fail(TERN_E_UNSUPPORTED, "n=%d or k=%d is too large", w->n, w->k);
   return TERN_OK;
 }
 
@@ -63,7 +63,7 @@ tern_status check_q4(const tern_q4* w) {
 size_t words_of(const tern_q4* w) { return (size_t)w->count * (size_t)w->n * (size_t)(w->k / 8); }
 
 // Up to this many activation rows the rows kernel, above it the tile kernel.
-constexpr int kRowsMost = 64;
+constexpr int kRowsMost = 32;
 
 // K parts of a plain tile product: enough workgroups for two per CU, at
 // least four K steps each.
@@ -106,18 +106,15 @@ struct ExpertsPlan {
   size_t h, part, tiles, ntiles, order, place, bytes;  // offsets in the workspace
 };
 
-ExpertsPlan plan_experts(int m, int topk, int experts, int inner, int n) {
+ExpertsPlan plan_experts(int m, int topk, int experts, int hidden, int inner, int n) {
   ExpertsPlan p = {};
   const size_t slots = (size_t)m * topk;
   p.direct = slots <= (size_t)kDirectSlots;
-  p.tile = !p.direct && slots > (size_t)experts * 24;
+  // the rows kernel holds x in one buffer below 2 GiB and its tiles in a grid's y
+  const bool rows = slots <= (size_t)experts * 24 && (size_t)m * hidden * 2 < ((size_t)1 << 31) && slots / 16 + experts <= 65535;
+  p.tile = !p.direct && !rows;
   p.rows = p.tile ? 128 : 16;
   p.max_tiles = (int)std::min<size_t>(slots, slots / p.rows + experts);
-  if (!p.direct && !p.tile && p.max_tiles > 65535) {
-    p.tile = true;
-    p.rows = 128;
-    p.max_tiles = (int)std::min<size_t>(slots, slots / p.rows + experts);
-  }
   size_t at = 0;
   auto take = [&](size_t bytes) {
     const size_t o = at;
@@ -224,7 +221,7 @@ tern_status tern_q4_gemm(const tern_q4* w, const uint16_t* x, int32_t m, void* y
 
 size_t tern_q4_experts_workspace_bytes(const tern_q4* gate_up, const tern_q4* down, int32_t m, int32_t topk) {
   if (check_experts(gate_up, down, m, topk) != TERN_OK) return 0;
-  return std::max<size_t>(256, plan_experts(m, topk, down->count, down->k, down->n).bytes);
+  return std::max<size_t>(256, plan_experts(m, topk, down->count, gate_up->k, down->k, down->n).bytes);
 }
 
 tern_status tern_q4_experts(const tern_q4* gate_up, const tern_q4* down, const uint16_t* x, int32_t m,
@@ -239,7 +236,7 @@ tern_status tern_q4_experts(const tern_q4* gate_up, const tern_q4* down, const u
   Q4_TRY(check_ptr(ids, true, "ids", 4));
   Q4_TRY(check_ptr(weights, true, "weights", 4));
   Q4_TRY(check_ptr(y, true, "y", y_dtype == TERN_F32 ? 4 : 2));
-  const ExpertsPlan p = plan_experts(m, topk, down->count, down->k, down->n);
+  const ExpertsPlan p = plan_experts(m, topk, down->count, gate_up->k, down->k, down->n);
   if (p.bytes && (!ws || ws_bytes < p.bytes))
     return fail(TERN_E_WORKSPACE, "workspace of %zu bytes, %zu are needed", ws ? ws_bytes : (size_t)0, p.bytes);
   Q4_TRY(check_ptr(ws, false, "workspace", 16));

@@ -1,119 +1,55 @@
-// Products with 4-bit weights for few activation rows (up to 64; the routed
-// experts' 16-row tiles): y[m][n] = sum_g s[n][g] sum_{k in g} (q - z) x.
+// Products with 4-bit weights for up to 32 activation rows, and the routed
+// experts' 16-row tiles: y[m][n] = sum_g s[n][g] sum_{k in g} (q - z) x.
 //
-// A workgroup owns 16 weight rows (a panel, contiguous in memory; NB panels)
-// and its wavefronts share the panel's K: wavefront w takes the 128-wide K
-// tiles w, w + W, ...  A lane loads 16 bytes of one row (32 codes), decodes
-// them to FP16 and feeds four v_mfma_f32_16x16x32_f16 with the activations
-// as A (16 rows) and the weights as B (16 columns); a group's sum, FP32, is
-// scaled and added to the running FP32 sum.  At group 128 the four lanes
-// that hold one row's tile multiply 32 consecutive k each.  Smaller groups
-// need every instruction's 32 k inside one group, so the four lanes' words
-// are transposed first (v_permlane32_swap, v_permlane16_swap: four
-// operations per 16 bytes).  The wavefronts' sums are added in LDS in
-// wavefront order: results do not depend on timing.
+// A workgroup of W wavefronts owns NB panels of 16 weight rows (a panel is
+// contiguous in memory) and shares their K: wavefront w takes the 128-wide K
+// tiles w, w + W, ...  A tile's codes and activations are loaded straight
+// into the wavefront's own LDS in memory order (a load in the matrix
+// operand's order, lane = row, would touch a line per lane), read back in the
+// operands' order, and the next tile's loads are in flight while they are
+// decoded and fed to v_mfma_f32_16x16x32_f16 (activations as A, 16 rows;
+// weights as B, 16 columns).  A group's FP32 sum is scaled and added to the
+// running FP32 sum.  The panels' scales and zero points are staged once, for
+// the whole workgroup.  The wavefronts' sums are added in LDS in wavefront
+// order: results do not depend on timing.  Loads go through buffer
+// descriptors, whose bounds checks stand in for branches; what they leave in
+// LDS behind the last row or behind k reaches no stored output.
 //
 // At one row the bound is the reading of the codes from memory.
-#include "q4.h"
+#include "q4_rows.h"
 
 namespace tern {
 namespace {
 
-template <int G, int MT, int NB>
-struct Frag {
-  w4_t c[NB];
-  uint16_t s[NB][128 / G];
-  uint8_t z[NB][128 / G];
-  h8_t x[MT][4];
-};
+// LDS of a workgroup behind the wavefronts' staging: the scales and zero
+// points of `panels` panels over `ct` K tiles.
+constexpr size_t scale_bytes(int groups, int panels, bool z) { return (size_t)panels * 16 * groups * (z ? 3 : 2) + 32; }
+constexpr size_t kLdsMost = 64 * 1024, kScaleMost = 20 * 1024;
 
-// The rows a lane reads: weight rows (clamped into the matrix) and
-// activation rows (NULL: none, counted as zeros).
-template <int MT, int NB>
-struct Rows {
-  const uint8_t* c[NB];
-  const uint16_t* s[NB];
-  const uint8_t* z[NB];
-  const uint16_t* x[MT];
-};
-
-template <int G, int MT, int NB, bool Z>
-__device__ inline void load_tile(Frag<G, MT, NB>& f, const Rows<MT, NB>& r, int t, int k, int kq) {
-  constexpr int SG = 128 / G;
-  const int ng = k / G;
-  const bool in = t * 128 + kq * 32 < k;
-#pragma unroll
-  for (int b = 0; b < NB; ++b) {
-    f.c[b] = w4_t{0, 0, 0, 0};
-    if (in) f.c[b] = *reinterpret_cast<const w4_t*>(r.c[b] + (size_t)t * 64 + kq * 16);
-#pragma unroll
-    for (int j = 0; j < SG; ++j) {
-      const int g = min(t * SG + j, ng - 1);  // a tile past the end of K has zero activations there
-      f.s[b][j] = r.s[b][g];
-      f.z[b][j] = Z ? r.z[b][g] : (uint8_t)8;
-    }
-  }
-#pragma unroll
-  for (int a = 0; a < MT; ++a)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int kx = t * 128 + (G == 128 ? kq * 32 + i * 8 : i * 32 + kq * 8);
-      f.x[a][i] = h8_t{};
-      if (r.x[a] != nullptr && kx < k) f.x[a][i] = *reinterpret_cast<const h8_t*>(r.x[a] + kx);
-    }
-}
-
-template <int G, int MT, int NB, bool Z>
-__device__ inline void multiply_tile(const Frag<G, MT, NB>& f, float mul, f4_t (&acc)[MT][NB]) {
-  constexpr int SG = 128 / G;
-#pragma unroll
-  for (int b = 0; b < NB; ++b) {
-    uint32_t w[4] = {f.c[b].x, f.c[b].y, f.c[b].z, f.c[b].w};
-    if (G < 128) {  // word i of lane quarter q <- word q of lane quarter i
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const auto p = __builtin_amdgcn_permlane32_swap(w[i], w[i + 2], false, false);
-        w[i] = p[0];
-        w[i + 2] = p[1];
-      }
-#pragma unroll
-      for (int i = 0; i < 4; i += 2) {
-        const auto p = __builtin_amdgcn_permlane16_swap(w[i], w[i + 1], false, false);
-        w[i] = p[0];
-        w[i + 1] = p[1];
-      }
-    }
-#pragma unroll
-    for (int j = 0; j < SG; ++j) {
-      const Q4Bias bias = q4_bias(Z ? f.z[b][j] : 8);
-      f4_t sum[MT];
-#pragma unroll
-      for (int a = 0; a < MT; ++a) sum[a] = f4_t{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int i = 0; i < 4 / SG; ++i) {
-        const h8_t wv = q4_decode(w[j * (4 / SG) + i], bias);
-#pragma unroll
-        for (int a = 0; a < MT; ++a)
-          sum[a] = __builtin_amdgcn_mfma_f32_16x16x32_f16(f.x[a][j * (4 / SG) + i], wv, sum[a], 0, 0, 0);
-      }
-      const float s = half_bits(f.s[b][j]) * mul;
-#pragma unroll
-      for (int a = 0; a < MT; ++a) acc[a][b] += s * sum[a];
-    }
-  }
-}
-
-template <int G, int MT, int NB, bool Z, int W, int MODE>
-__global__ __launch_bounds__(W * 64) void q4_rows_kernel(const Q4Args a) {
-  __shared__ float red[W][MT * NB][4][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+// XR: rows of x at most (4, 16 or 32).  ct: K tiles whose scales are staged
+// at a time (all of them unless K is very long).
+template <int G, bool Z, int XR, int NB, int W, int MODE>
+__global__ __launch_bounds__(W * 64) void q4_rows_kernel(const Q4Args a, const int ct) {
+  constexpr bool up = MODE == kQ4Up || MODE == kQ4UpSlot, token = MODE == kQ4DownToken;
+  static_assert(!up || NB == 2, "gate and up panels go together");
+  static_assert(!token || NB == 1, "one panel");
+  constexpr int NBO = up ? 1 : NB;                    // panels of the output
+  constexpr int XI = XR / 4, MT = (XR + 15) / 16;     // staging loads and operands of a tile's x
+  constexpr int SG = 128 / G, S = (NB + XI) * 64;     // 16-byte chunks of a wavefront's staging
+  extern __shared__ w4_t lds[];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, kq = lane >> 4;
   const int k = a.k, ng = k / G, T = (k + 127) / 128;
-  constexpr bool up = MODE == kQ4Up || MODE == kQ4UpSlot;
   const int width = up ? a.n / 2 : a.n;  // output columns
-  const int n0 = blockIdx.x * 16 * (up ? 1 : NB);
+  const int n0 = blockIdx.x * 16 * NBO;
+  w4_t* const cl = lds + wave * S;
+  w4_t* const xl = cl + NB * 64;
+  // scales [panel][16][cg], then zero points alike
+  const int cg = min(ct * SG, ng), panels = token ? a.topk : NB;
+  uint16_t* const sl = reinterpret_cast<uint16_t*>(lds + W * S);
+  uint8_t* const zl = reinterpret_cast<uint8_t*>(sl + panels * 16 * cg);
 
-  int e = 0, rows = a.m, pos = 0;
+  int e = 0, rows = 1, pos = blockIdx.y;
   if (MODE == kQ4Up || MODE == kQ4Down) {
     if ((int)blockIdx.y >= *a.ntiles) return;
     const int4 tile = a.tiles[blockIdx.y];
@@ -123,91 +59,183 @@ __global__ __launch_bounds__(W * 64) void q4_rows_kernel(const Q4Args a) {
   } else if (MODE == kQ4UpSlot) {
     e = a.ids[blockIdx.y];
     if ((unsigned)e >= (unsigned)a.experts) return;
-    pos = blockIdx.y;
-    rows = 1;
   } else if (MODE == kQ4Plain) {
-    pos = blockIdx.y * 16 * MT;
-    rows = min(rows - pos, 16 * MT);
-  } else {
-    pos = blockIdx.y;
-    rows = 1;
+    rows = a.m;
+    pos = 0;
   }
 
-  Rows<MT, NB> at;
-  auto weights = [&](int expert) {
+  // panel b: 16 rows from row0(b), as many as exist
+  auto row0 = [&](int b) {
+    const int col = n0 + (up ? 0 : b * 16);
+    return (col < width ? col : 0) + (up && b ? width : 0);
+  };
+  auto count = [&](int b) { return max(0, min(16, width - n0 - (up ? 0 : b * 16))); };
+  __amdgpu_buffer_rsrc_t fc[NB], fx;
+  auto aim = [&](int expert) {
 #pragma unroll
-    for (int b = 0; b < NB; ++b) {
-      const int col = min(n0 + (up ? 0 : b * 16) + r, width - 1) + (up && b ? width : 0);
-      const size_t row = (size_t)expert * a.n + col;
-      at.c[b] = a.codes + row * (size_t)(k / 2);
-      at.s[b] = a.scale + row * ng;
-      at.z[b] = Z ? a.zero + row * ng : nullptr;
+    for (int b = 0; b < NB; ++b)
+      fc[b] = q4_buffer(a.codes + ((size_t)expert * a.n + row0(b)) * (size_t)(k / 2), (uint32_t)count(b) * (uint32_t)(k / 2));
+  };
+  // the scales of `expert`'s panel b, groups g0 .. g0 + cg - 1, to slot p
+  auto stage_scales = [&](int expert, int b, int p, int g0) {
+    const size_t at = ((size_t)expert * a.n + row0(b)) * ng;
+    const int rc = count(b), want = min(cg, ng - g0);
+    const uint16_t* s = a.scale + at;
+    const uint8_t* z = Z ? a.zero + at : nullptr;
+    uint16_t* sd = sl + p * 16 * cg;
+    uint8_t* zd = zl + p * 16 * cg;
+    if (rc == 16 && want == ng && !((uintptr_t)s & 15) && (!Z || !((uintptr_t)z & 15)) ) {  // contiguous
+      for (int i = threadIdx.x; i < 2 * ng; i += W * 64)  // 16 rows of 2 ng bytes, then of ng bytes
+        reinterpret_cast<w4_t*>(sd)[i] = reinterpret_cast<const w4_t*>(s)[i];
+      if (Z)
+        for (int i = threadIdx.x; i < ng; i += W * 64) reinterpret_cast<w4_t*>(zd)[i] = reinterpret_cast<const w4_t*>(z)[i];
+    } else {
+      for (int i = threadIdx.x; i < rc * want; i += W * 64) {
+        const int row = i / want, g = i - row * want;
+        sd[row * cg + g] = s[(size_t)row * ng + g0 + g];
+        if (Z) zd[row * cg + g] = z[(size_t)row * ng + g0 + g];
+      }
     }
   };
+
+  // the chunks of x this lane stages: row, chunk (swizzled by row like the codes)
+  uint32_t xo[XI];
+  if (MODE == kQ4Up) {
+    fx = q4_buffer(a.x, (uint32_t)a.m * (uint32_t)k * 2);  // below 2 GiB (host)
+  } else if (!token) {
+    const size_t first = MODE == kQ4UpSlot ? pos / a.topk : pos;
+    fx = q4_buffer(a.x + first * k, (uint32_t)rows * (uint32_t)k * 2);
+  }
+#pragma unroll
+  for (int j = 0; j < XI; ++j) {
+    const int row = j * 4 + (lane >> 4);
+    xo[j] = kFar;
+    if (row < rows)
+      xo[j] = (uint32_t)(MODE == kQ4Up ? a.slots[pos + row] / a.topk : row) * (uint32_t)k * 2 + ((lane ^ row) & 15) * 16;
+  }
+  const int cr = lane >> 2;  // the chunk of the codes this lane stages
+  const uint32_t co = (uint32_t)cr * (uint32_t)(k / 2) + (uint32_t)(code_chunk(cr, lane & 3) & 3) * 16;
+
+  const Q4Masks masks;
   f4_t acc[MT][NB];
 #pragma unroll
   for (int i = 0; i < MT; ++i)
 #pragma unroll
     for (int b = 0; b < NB; ++b) acc[i][b] = f4_t{0.f, 0.f, 0.f, 0.f};
+  if (!token) aim(e);
 
-  if (MODE == kQ4DownToken) {
-    // the token's slots one after another along the wavefronts' K tiles
-    for (int u = wave; u < a.topk * T; u += W) {
-      const int j = u / T, t = u - j * T;
-      const int slot = pos * a.topk + j;
-      const int ex = a.ids[slot];
-      if ((unsigned)ex >= (unsigned)a.experts) continue;
-      weights(ex);
-      at.x[0] = r == 0 ? a.x + (size_t)slot * k : nullptr;
-      Frag<G, MT, NB> f;
-      load_tile<G, MT, NB, Z>(f, at, t, k, kq);
-      multiply_tile<G, MT, NB, Z>(f, a.gates[slot], acc);
-    }
-  } else {
-    weights(e);
-#pragma unroll
-    for (int i = 0; i < MT; ++i) {
-      const int row = i * 16 + r;
-      at.x[i] = nullptr;
-      if (row < rows) {
-        size_t src = (size_t)pos + row;
-        if (MODE == kQ4Up) src = (size_t)(a.slots[pos + row] / a.topk);
-        if (MODE == kQ4UpSlot) src = (size_t)(pos / a.topk);
-        at.x[i] = a.x + src * k;
+  for (int c0 = 0; c0 < T || c0 == 0; c0 += ct) {
+    const int c1 = min(T, c0 + ct);
+    // work unit v: tile c0 + v (a token: its slots' tiles one after another)
+    const int tiles = c1 - c0, work = token ? a.topk * tiles : tiles;
+    int t = 0, p = 0;
+    float mul = 1.0f;
+    auto issue = [&](int v) {
+      t = c0 + v;
+      if (token) {
+        p = v / tiles;
+        t = c0 + v - p * tiles;
+        const size_t slot = (size_t)pos * a.topk + p;
+        const int ex = a.ids[slot];
+        if ((unsigned)ex >= (unsigned)a.experts) return false;
+        mul = a.gates[slot];
+        aim(ex);
+        fx = q4_buffer(a.x + slot * k, (uint32_t)k * 2);
       }
+#pragma unroll
+      for (int b = 0; b < NB; ++b) q4_stage16(fc[b], cl + b * 64, co + (uint32_t)t * 64);
+#pragma unroll
+      for (int j = 0; j < XI; ++j)
+        if (j == 0 || j * 4 < rows) q4_stage16(fx, xl + j * 64, xo[j] + (uint32_t)t * 256);
+      return true;
+    };
+    bool have = false;
+    int v = wave;
+    for (; v < work && !(have = issue(v)); v += W) {
     }
-    Frag<G, MT, NB> f, next;
-    if (wave < T) load_tile<G, MT, NB, Z>(f, at, wave, k, kq);
-    for (int t = wave; t < T; t += W) {
-      if (t + W < T) load_tile<G, MT, NB, Z>(next, at, t + W, k, kq);
-      multiply_tile<G, MT, NB, Z>(f, 1.0f, acc);
-      f = next;
+    if (c0) __syncthreads();  // the scales before these are in use until here
+    if (token) {
+      for (int j = 0; j < a.topk; ++j) {
+        const int ex = a.ids[(size_t)pos * a.topk + j];
+        if ((unsigned)ex < (unsigned)a.experts) stage_scales(ex, 0, j, c0 * SG);
+      }
+    } else {
+#pragma unroll
+      for (int b = 0; b < NB; ++b) stage_scales(e, b, b, c0 * SG);
+    }
+    __syncthreads();
+    while (have) {
+      q4_loads_done();
+      w4_t words[NB];
+      h8_t x[MT][4];
+#pragma unroll
+      for (int b = 0; b < NB; ++b) words[b] = cl[b * 64 + code_chunk(r, kq)];
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        const int row = min(i * 16 + r, rows - 1);  // rows behind the last: a copy, not stored
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[i][j] = __builtin_bit_cast(h8_t, xl[row * 16 + ((x_chunk<G>(j, kq) ^ row) & 15)]);
+      }
+      uint16_t s[NB][SG];
+      uint8_t z[NB][SG];
+      const int left = min(SG, (k - t * 128) / G);  // groups in this tile
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        const int at = ((token ? p : b) * 16 + r) * cg + (t - c0) * SG;
+#pragma unroll
+        for (int j = 0; j < SG; ++j) {
+          const int g = j < left ? j : 0;
+          s[b][j] = sl[at + g];
+          z[b][j] = Z ? zl[at + g] : (uint8_t)8;
+        }
+      }
+      const float factor = mul;
+      q4_reads_done();
+      have = false;
+      for (v += W; v < work && !(have = issue(v)); v += W) {
+      }
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        const w4_t w = in_order<G>(words[b]);
+#pragma unroll
+        for (int j = 0; j < SG; ++j) {
+          if (j && j >= left) break;
+          const Q4Bias bias = q4_bias(z[b][j]);
+          f4_t sum[MT];
+#pragma unroll
+          for (int i = 0; i < MT; ++i) sum[i] = f4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int q = j * (4 / SG); q < (j + 1) * (4 / SG); ++q) {
+            const h8_t wv = q4_decode(w[q], bias, masks);
+#pragma unroll
+            for (int i = 0; i < MT; ++i) sum[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(x[i][q], wv, sum[i], 0, 0, 0);
+          }
+          const float f = half_bits(s[b][j]) * factor;
+#pragma unroll
+          for (int i = 0; i < MT; ++i) acc[i][b] += f * sum[i];
+        }
+      }
     }
   }
 
+  // every wavefront's sums to its own staging, [operand][panel][lane]
+  f4_t* const red = reinterpret_cast<f4_t*>(lds);
 #pragma unroll
   for (int i = 0; i < MT; ++i)
 #pragma unroll
     for (int b = 0; b < NB; ++b)
-#pragma unroll
-      for (int v = 0; v < 4; ++v) red[wave][i * NB + b][v][lane] = acc[i][b][v];
+      if (i * 16 + kq * 4 < rows) red[wave * S + (i * NB + b) * 64 + lane] = acc[i][b];
   __syncthreads();
-  constexpr int OUT = MT * (up ? 1 : NB) * 256;
-  for (int o = threadIdx.x; o < OUT; o += W * 64) {
-    const int l = o & 63, v = (o >> 6) & 3, tile = o >> 8;
-    const int i = up ? tile : tile / NB, b = up ? 0 : tile % NB;
-    const int row = i * 16 + (l >> 4) * 4 + v, col = n0 + b * 16 + (l & 15);
+  for (int o = threadIdx.x; o < rows * NBO * 16; o += W * 64) {
+    const int row = o / (NBO * 16), c = o % (NBO * 16), b = c / 16;
+    const int l = (row / 16 * NB + b) * 64 + row % 16 / 4 * 16 + c % 16, col = n0 + c;
     float sum = 0.f, gate = 0.f;
 #pragma unroll
     for (int w = 0; w < W; ++w) {
-      if (up) {
-        gate += red[w][i * NB][v][l];
-        sum += red[w][i * NB + NB - 1][v][l];
-      } else {
-        sum += red[w][tile][v][l];
-      }
+      if (up) gate += red[w * S + l][row % 4];
+      sum += red[w * S + l + (up ? 64 : 0)][row % 4];
     }
-    if (row >= rows || col >= width) continue;
+    if (col >= width) continue;
     const size_t dst = ((size_t)pos + row) * width + col;
     if (up)
       reinterpret_cast<_Float16*>(a.y)[dst] = (_Float16)q4_swiglu(gate, sum);
@@ -218,29 +246,52 @@ __global__ __launch_bounds__(W * 64) void q4_rows_kernel(const Q4Args a) {
   }
 }
 
-template <int G, int MT, int NB, bool Z, int W, int MODE>
+template <int G, bool Z, int XR, int NB, int W, int MODE>
 hipError_t launch(const Q4Args& a, int tiles, hipStream_t s) {
   constexpr bool up = MODE == kQ4Up || MODE == kQ4UpSlot;
-  const int width = up ? a.n / 2 : a.n;
-  const int cols = 16 * (up ? 1 : NB);
-  const int gy = MODE == kQ4Plain ? (a.m + 16 * MT - 1) / (16 * MT) : tiles;
-  const dim3 grid((unsigned)((width + cols - 1) / cols), (unsigned)gy);
-  hipLaunchKernelGGL((q4_rows_kernel<G, MT, NB, Z, W, MODE>), grid, dim3(W * 64), 0, s, a);
+  constexpr int SG = 128 / G, S = (NB + XR / 4) * 64;
+  const int width = up ? a.n / 2 : a.n, cols = 16 * (up ? 1 : NB);
+  const int T = (a.k + 127) / 128, panels = MODE == kQ4DownToken ? a.topk : NB;
+  constexpr size_t staging = (size_t)W * S * 16;
+  const size_t most = kLdsMost - staging < kScaleMost ? kLdsMost - staging : kScaleMost;
+  int ct = T > 0 ? T : 1;
+  while (scale_bytes(ct * SG, panels, Z) > most && ct > 1) ct = (ct + 1) / 2;
+  const size_t bytes = staging + scale_bytes(ct * SG, panels, Z);
+  if (bytes > kLdsMost) return hipErrorInvalidValue;
+  const dim3 grid((unsigned)((width + cols - 1) / cols), (unsigned)(MODE == kQ4Plain ? 1 : tiles));
+  hipLaunchKernelGGL((q4_rows_kernel<G, Z, XR, NB, W, MODE>), grid, dim3(W * 64), bytes, s, a, ct);
   return hipGetLastError();
 }
 
 template <int G, bool Z>
 hipError_t pick(int mode, const Q4Args& a, int tiles, hipStream_t s) {
   switch (mode) {
-    case kQ4Up: return launch<G, 1, 2, Z, 8, kQ4Up>(a, tiles, s);
-    case kQ4Down: return launch<G, 1, 1, Z, 8, kQ4Down>(a, tiles, s);
-    case kQ4UpSlot: return launch<G, 1, 2, Z, 8, kQ4UpSlot>(a, tiles, s);
-    case kQ4DownToken: return launch<G, 1, 1, Z, 8, kQ4DownToken>(a, tiles, s);
+    case kQ4Up: return launch<G, Z, 16, 2, 8, kQ4Up>(a, tiles, s);
+    case kQ4Down: return launch<G, Z, 16, 1, 8, kQ4Down>(a, tiles, s);
+    case kQ4UpSlot: return launch<G, Z, 4, 2, 8, kQ4UpSlot>(a, tiles, s);
+    case kQ4DownToken: return launch<G, Z, 4, 1, 8, kQ4DownToken>(a, tiles, s);
     default: break;
   }
-  if (a.m <= 16) return launch<G, 1, 1, Z, 8, kQ4Plain>(a, tiles, s);
-  if (a.m <= 32) return launch<G, 2, 1, Z, 8, kQ4Plain>(a, tiles, s);
-  return launch<G, 4, 1, Z, 4, kQ4Plain>(a, tiles, s);
+  // Wavefronts a panel: 4 where there are panels enough to fill the card, 16
+  // where few panels have long rows.  us at W = 4, 8, 16 (m = 1, group 128):
+  // 12288 x 4096 6.5, 6.8, -; 131072 x 2560 36.7, 43, -; 4096 x 4096 4.3, 3.6,
+  // 3.9; 2560 x 9728 9.5, 6.2, 5.1; at W = 4, 8 (m = 16): 12288 x 4096 8.4,
+  // 9.4; 4096 x 12288 13.8, 9.7.
+  const int panels = (a.n + 15) / 16, T = (a.k + 127) / 128;
+  if (a.m <= 4) {
+    if (panels >= 512) return launch<G, Z, 4, 1, 4, kQ4Plain>(a, tiles, s);
+    if (panels < 256 && T >= 64) return launch<G, Z, 4, 1, 16, kQ4Plain>(a, tiles, s);
+    return launch<G, Z, 4, 1, 8, kQ4Plain>(a, tiles, s);
+  }
+  if (a.m <= 16) {
+    if (panels >= 512) return launch<G, Z, 16, 1, 4, kQ4Plain>(a, tiles, s);
+    return launch<G, Z, 16, 1, 8, kQ4Plain>(a, tiles, s);
+  }
+  // two operands of x: 9 KiB of staging a wavefront; two panels share them
+  // where panels abound (m = 24, 4096 x 4096: 6.4 against 8.0 us; m = 32,
+  // 12288 x 4096: 14.9 against 12.0)
+  if (panels >= 512) return launch<G, Z, 32, 2, 4, kQ4Plain>(a, tiles, s);
+  return launch<G, Z, 32, 1, 6, kQ4Plain>(a, tiles, s);
 }
 
 }  // namespace
