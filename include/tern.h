@@ -387,7 +387,7 @@ tern_status tern_rotate_batched(int32_t count, const uint16_t *const *R, int32_t
  * `count` matrices of one shape may be stacked ([count][n][...] in every
  * array): a layer's experts.  group 32, 64 or 128 and k a multiple of it
  * (TERN_E_UNSUPPORTED otherwise); any n.  codes 16-byte aligned, scale
- * 2-byte; k at most 2^24.  The conventions above hold: x is FP16 [m][k], 16-byte aligned;
+ * 2-byte; k at most 2^22.  The conventions above hold: x is FP16 [m][k], 16-byte aligned;
  * FP32 sums; y FP16 (nearest even) or FP32; n == 0 or m == 0 is a no-op,
  * k == 0 writes zeros; status codes, asynchronous, nothing kept between
  * calls, every call but tern_q4_pack may be captured into a HIP graph (as

@@ -47,8 +47,8 @@ tern_status check_shape(const tern_q4* w) {
   if (w->group != 32 && w->group != 64 && w->group != 128)
     return fail(TERN_E_UNSUPPORTED, "4-bit group %d is not 32, 64 or 128", w->group);
   if (w->k % w->group) return fail(TERN_E_UNSUPPORTED, "k=%d must be a multiple of group %d", w->k, w->group);
-  // buffer descriptors hold 16 weight rows or 32 activation rows; n is rounded up to a tile
-  if (w->k > (1 << 24) || w->n > 0x7fffff00) return fail(TERN_E_UNSUPPORTED, "n=%d or k=%d is too large", w->n, w->k);
+  // buffer descriptors hold 128 activation rows, their offsets 31 bits; n is rounded up to a tile
+  if (w->k > (1 << 22) || w->n > 0x7fffff00) return fail(TERN_E_UNSUPPORTED, "n=%d or k=%d is too large", w->n, w->k);
   return TERN_OK;
 }
 
@@ -62,24 +62,40 @@ tern_status check_q4(const tern_q4* w) {
 
 size_t words_of(const tern_q4* w) { return (size_t)w->count * (size_t)w->n * (size_t)(w->k / 8); }
 
-// Up to this many activation rows the rows kernel, above it the tile kernel.
-constexpr int kRowsMost = 32;
+long long tiles_of(int m, int n, int tile) {  // tiles of 64 x 128 or 128 x 256
+  return (long long)((m + tile - 1) / tile) * ((n + 2 * tile - 1) / (2 * tile));
+}
 
-// K parts of a plain tile product: enough workgroups for two per CU, at
-// least four K steps each.
-int pick_splits(int m, int n, int k) {
-  const long long tiles = (long long)((m + 127) / 128) * ((n + 127) / 128);
+// The tile kernel holds a matrix's scales in one buffer below 2 GiB.
+bool tile_scales_fit(int n, int k) { return (long long)n * (k / 32) * 2 < (1ll << 31); }
+
+// How a plain product runs.  Rows kernel: up to 160 activation rows, and up
+// to 320 where the tiles would not fill the card (us, rows against tiles: m =
+// 128, 4096 x 4096 13.5, 17.7; m = 256, 2560 x 9728 29.8, 30.2; m = 256, 12288
+// x 4096 41.6, 40.4).  Large tiles from one a CU (2048 x 4096 x 4096 74.4, 86.7
+// on small ones; 512 x 12288 x 4096 69.8, 61.5).  K parts where tiles are few:
+// some 512 workgroups, at least eight K steps each.
+struct Route {
+  bool rows;
+  int tile, splits, tps;
+};
+
+Route route_of(int m, int n, int k) {
+  Route r = {};
   const int steps = (k + 127) / 128;
-  if (tiles >= 256 || steps < 8) return 1;
-  const int splits = (int)std::min<long long>(512 / tiles, steps / 4);
-  const int tps = (steps + splits - 1) / splits;
-  return (steps + tps - 1) / tps;
+  const long long small = tiles_of(m, n, tern::kQ4TileSmall);
+  r.rows = m <= 160 || (m <= 320 && small < 256) || !tile_scales_fit(n, k);
+  r.tile = tiles_of(m, n, tern::kQ4TileLarge) >= 256 ? tern::kQ4TileLarge : tern::kQ4TileSmall;
+  r.splits = 1;
+  if (!r.rows && small < 256) r.splits = std::max(1, (int)std::min<long long>(512 / std::max(small, 1ll), steps / 8));
+  r.tps = std::max(1, (steps + r.splits - 1) / r.splits);
+  r.splits = std::max(1, (steps + r.tps - 1) / r.tps);
+  return r;
 }
 
 size_t plain_ws(int m, int n, int k) {
-  if (m <= kRowsMost) return 0;
-  const int s = pick_splits(m, n, k);
-  return s > 1 ? (size_t)s * m * n * 4 : 0;
+  const Route r = route_of(m, n, k);
+  return !r.rows && r.splits > 1 ? (size_t)r.splits * m * n * 4 : 0;
 }
 
 tern::Q4Args args_of(const tern_q4* w) {
@@ -106,14 +122,17 @@ struct ExpertsPlan {
   size_t h, part, tiles, ntiles, order, place, bytes;  // offsets in the workspace
 };
 
-ExpertsPlan plan_experts(int m, int topk, int experts, int hidden, int inner, int n) {
+ExpertsPlan plan_tokens(const tern_q4* up, const tern_q4* down, int m, int topk) {
   ExpertsPlan p = {};
+  const int experts = down->count, inner = down->k, n = down->n;
   const size_t slots = (size_t)m * topk;
   p.direct = slots <= (size_t)kDirectSlots;
-  // the rows kernel holds x in one buffer below 2 GiB and its tiles in a grid's y
-  const bool rows = slots <= (size_t)experts * 24 && (size_t)m * hidden * 2 < ((size_t)1 << 31) && slots / 16 + experts <= 65535;
-  p.tile = !p.direct && !rows;
-  p.rows = p.tile ? 128 : 16;
+  // Tiles of 4, 16 or 32 rows on the rows kernel (its tiles are a grid's y),
+  // of 64 or 128 on the tile kernel, by the rows an expert has on average.
+  const size_t mean = slots / experts;
+  p.rows = mean < 3 ? 4 : mean < 12 ? 16 : mean < 40 ? 32 : mean < 160 ? tern::kQ4TileSmall : tern::kQ4TileLarge;
+  if (!tile_scales_fit(up->n, up->k) || !tile_scales_fit(n, inner)) p.rows = std::min(p.rows, 32);
+  p.tile = p.rows > 32;
   p.max_tiles = (int)std::min<size_t>(slots, slots / p.rows + experts);
   size_t at = 0;
   auto take = [&](size_t bytes) {
@@ -131,6 +150,20 @@ ExpertsPlan plan_experts(int m, int topk, int experts, int hidden, int inner, in
   }
   p.bytes = at;
   return p;
+}
+
+// Tokens of one round: their x stays below a buffer's 2 GiB, their tiles
+// below a grid's y, and the workspace does not grow with m without end.
+int round_tokens(const tern_q4* up, int m, int topk) {
+  const long long by_x = up->k ? ((1ll << 31) - 1) / (2ll * up->k) : m;
+  return (int)std::max<long long>(1, std::min<long long>({(long long)m, by_x, (1ll << 20) / topk}));
+}
+
+size_t experts_ws(const tern_q4* up, const tern_q4* down, int m, int topk) {
+  if (m <= 0) return 0;
+  const int most = round_tokens(up, m, topk);
+  const size_t rest = m % most ? plan_tokens(up, down, m % most, topk).bytes : 0;
+  return std::max(plan_tokens(up, down, most, topk).bytes, rest);
 }
 
 tern_status check_experts(const tern_q4* up, const tern_q4* down, int m, int topk) {
@@ -204,24 +237,23 @@ tern_status tern_q4_gemm(const tern_q4* w, const uint16_t* x, int32_t m, void* y
   a.m = m;
   a.y_f32 = y_dtype == TERN_F32;
   const hipStream_t s = (hipStream_t)stream;
-  if (m <= kRowsMost) {
-    Q4_HIP(tern::launch_q4_rows(tern::kQ4Plain, w->group, a, 0, s));
+  const Route r = route_of(m, w->n, w->k);
+  if (r.rows) {
+    Q4_HIP(tern::launch_q4_rows(tern::kQ4Plain, w->group, a, 0, 0, s));
     return TERN_OK;
   }
-  if ((long long)((m + 127) / 128) * ((w->n + 127) / 128) > 0x7fffffffll)
-    return fail(TERN_E_UNSUPPORTED, "m=%d, n=%d: too many tiles", m, w->n);
-  a.splits = pick_splits(m, w->n, w->k);
-  const int steps = (w->k + 127) / 128;
-  a.tps = (steps + a.splits - 1) / a.splits;
+  if (tiles_of(m, w->n, r.tile) * r.splits > 0x7ffffff0ll) return fail(TERN_E_UNSUPPORTED, "m=%d, n=%d: too many tiles", m, w->n);
+  a.splits = r.splits;
+  a.tps = r.tps;
   a.partial = (float*)ws;
-  Q4_HIP(tern::launch_q4_tile(tern::kQ4Plain, w->group, a, 0, s));
+  Q4_HIP(tern::launch_q4_tile(tern::kQ4Plain, w->group, a, 0, r.tile, s));
   if (a.splits > 1) Q4_HIP(tern::launch_q4_reduce(a, s));
   return TERN_OK;
 }
 
 size_t tern_q4_experts_workspace_bytes(const tern_q4* gate_up, const tern_q4* down, int32_t m, int32_t topk) {
   if (check_experts(gate_up, down, m, topk) != TERN_OK) return 0;
-  return std::max<size_t>(256, plan_experts(m, topk, down->count, gate_up->k, down->k, down->n).bytes);
+  return std::max<size_t>(256, experts_ws(gate_up, down, m, topk));
 }
 
 tern_status tern_q4_experts(const tern_q4* gate_up, const tern_q4* down, const uint16_t* x, int32_t m,
@@ -236,40 +268,44 @@ tern_status tern_q4_experts(const tern_q4* gate_up, const tern_q4* down, const u
   Q4_TRY(check_ptr(ids, true, "ids", 4));
   Q4_TRY(check_ptr(weights, true, "weights", 4));
   Q4_TRY(check_ptr(y, true, "y", y_dtype == TERN_F32 ? 4 : 2));
-  const ExpertsPlan p = plan_experts(m, topk, down->count, gate_up->k, down->k, down->n);
-  if (p.bytes && (!ws || ws_bytes < p.bytes))
-    return fail(TERN_E_WORKSPACE, "workspace of %zu bytes, %zu are needed", ws ? ws_bytes : (size_t)0, p.bytes);
+  const size_t need = experts_ws(gate_up, down, m, topk);
+  if (need && (!ws || ws_bytes < need))
+    return fail(TERN_E_WORKSPACE, "workspace of %zu bytes, %zu are needed", ws ? ws_bytes : (size_t)0, need);
   Q4_TRY(check_ptr(ws, false, "workspace", 16));
-  const long long cols = std::max<long long>((gate_up->n / 2 + 63) / 64, (down->n + 127) / 128);
-  if (p.tile && cols * p.max_tiles > 0x7fffffffll) return fail(TERN_E_UNSUPPORTED, "m=%d, topk=%d: too many tiles", m, topk);
   uint8_t* base = (uint8_t*)ws;
   const hipStream_t s = (hipStream_t)stream;
-  tern::Q4Args u = args_of(gate_up), d = args_of(down);
-  u.x = x;
-  u.y = base + p.h;
-  d.x = (const uint16_t*)(base + p.h);
-  u.m = d.m = m;
-  u.ids = d.ids = ids;
-  u.gates = d.gates = weights;
-  u.topk = d.topk = topk;
-  if (p.direct) {
-    if (down->k) Q4_HIP(tern::launch_q4_rows(tern::kQ4UpSlot, gate_up->group, u, m * topk, s));
-    d.y = y;
-    d.y_f32 = y_dtype == TERN_F32;
-    Q4_HIP(tern::launch_q4_rows(tern::kQ4DownToken, down->group, d, m, s));
-    return TERN_OK;
+  const int most = round_tokens(gate_up, m, topk), f32 = y_dtype == TERN_F32;
+  for (int t = 0; t < m; t += most) {
+    const int mt = std::min(most, m - t);
+    const ExpertsPlan p = plan_tokens(gate_up, down, mt, topk);
+    uint8_t* yt = (uint8_t*)y + (size_t)t * down->n * (f32 ? 4 : 2);
+    tern::Q4Args u = args_of(gate_up), d = args_of(down);
+    u.x = x + (size_t)t * gate_up->k;
+    u.y = base + p.h;
+    d.x = (const uint16_t*)(base + p.h);
+    u.m = d.m = mt;
+    u.ids = d.ids = ids + (size_t)t * topk;
+    u.gates = d.gates = weights + (size_t)t * topk;
+    u.topk = d.topk = topk;
+    if (p.direct) {
+      if (down->k) Q4_HIP(tern::launch_q4_rows(tern::kQ4UpSlot, gate_up->group, u, mt * topk, 0, s));
+      d.y = yt;
+      d.y_f32 = f32;
+      Q4_HIP(tern::launch_q4_rows(tern::kQ4DownToken, down->group, d, mt, 0, s));
+      continue;
+    }
+    u.tiles = d.tiles = (const int4*)(base + p.tiles);
+    u.ntiles = d.ntiles = (const int32_t*)(base + p.ntiles);
+    u.slots = d.slots = (const int32_t*)(base + p.order);
+    d.y = base + p.part;
+    Q4_HIP(tern::launch_q4_plan(u.ids, mt * topk, down->count, p.rows, (int4*)(base + p.tiles),
+                                (int32_t*)(base + p.ntiles), (int32_t*)(base + p.order), (int32_t*)(base + p.place), s));
+    auto* launch = p.tile ? tern::launch_q4_tile : tern::launch_q4_rows;
+    if (down->k) Q4_HIP(launch(tern::kQ4Up, gate_up->group, u, p.max_tiles, p.rows, s));
+    Q4_HIP(launch(tern::kQ4Down, down->group, d, p.max_tiles, p.rows, s));
+    Q4_HIP(tern::launch_q4_combine((const float*)(base + p.part), (const int32_t*)(base + p.place), u.gates, mt, topk,
+                                   down->n, yt, f32, s));
   }
-  u.tiles = d.tiles = (const int4*)(base + p.tiles);
-  u.ntiles = d.ntiles = (const int32_t*)(base + p.ntiles);
-  u.slots = d.slots = (const int32_t*)(base + p.order);
-  d.y = base + p.part;
-  Q4_HIP(tern::launch_q4_plan(ids, m * topk, down->count, p.rows, (int4*)(base + p.tiles), (int32_t*)(base + p.ntiles),
-                              (int32_t*)(base + p.order), (int32_t*)(base + p.place), s));
-  auto* launch = p.tile ? tern::launch_q4_tile : tern::launch_q4_rows;
-  if (down->k) Q4_HIP(launch(tern::kQ4Up, gate_up->group, u, p.max_tiles, s));
-  Q4_HIP(launch(tern::kQ4Down, down->group, d, p.max_tiles, s));
-  Q4_HIP(tern::launch_q4_combine((const float*)(base + p.part), (const int32_t*)(base + p.place), weights, m, topk,
-                                 down->n, y, y_dtype == TERN_F32, s));
   return TERN_OK;
 }
 

@@ -6,7 +6,7 @@
 namespace tern {
 namespace {
 
-constexpr int kPlanThreads = 1024;
+constexpr int kPlanThreads = 1024, kBatch = 8;  // kBatch ids requested before any is used
 
 // Sorts the slots by expert: order[position] = slot, place[slot] = position
 // (-1 for a slot that names no expert), and cuts every expert's positions
@@ -20,9 +20,13 @@ __global__ __launch_bounds__(kPlanThreads) void q4_plan_kernel(const int32_t* id
   const int t = threadIdx.x;
   count[t] = 0;
   __syncthreads();
-  for (int s = t; s < slots; s += kPlanThreads) {
-    const int e = ids[s];
-    if ((unsigned)e < (unsigned)experts) atomicAdd(&count[e], 1);
+  for (int s0 = t; s0 < slots; s0 += kPlanThreads * kBatch) {
+    int e[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) e[i] = s0 + i * kPlanThreads < slots ? ids[s0 + i * kPlanThreads] : -1;
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i)
+      if ((unsigned)e[i] < (unsigned)experts) atomicAdd(&count[e[i]], 1);
   }
   __syncthreads();
   const int mine = count[t], tl = (mine + rows - 1) / rows;
@@ -42,32 +46,54 @@ __global__ __launch_bounds__(kPlanThreads) void q4_plan_kernel(const int32_t* id
   count[t] = f;
   for (int i = 0; i < tl; ++i) tiles[q + i] = make_int4(t, f + i * rows, min(rows, mine - i * rows), 0);
   __syncthreads();
-  for (int s = t; s < slots; s += kPlanThreads) {
-    const int e = ids[s];
-    int p = -1;
-    if ((unsigned)e < (unsigned)experts) {
-      p = atomicAdd(&count[e], 1);
-      order[p] = s;
+  for (int s0 = t; s0 < slots; s0 += kPlanThreads * kBatch) {
+    int e[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) e[i] = s0 + i * kPlanThreads < slots ? ids[s0 + i * kPlanThreads] : -1;
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int s = s0 + i * kPlanThreads;
+      int p = -1;
+      if ((unsigned)e[i] < (unsigned)experts) {
+        p = atomicAdd(&count[e[i]], 1);
+        order[p] = s;
+      }
+      if (s < slots) place[s] = p;
     }
-    place[s] = p;
   }
 }
 
-// y[token] = sum over its slots, in slot order, of gate * part[place].
+// y[token] = sum over its slots, in slot order, of gate * part[place]; four
+// columns a thread (V = 4: n a multiple of four).  Bound by the reading of
+// the partials.
+template <int V>
 __global__ __launch_bounds__(256) void q4_combine_kernel(const float* part, const int32_t* place, const float* gates,
                                                          int topk, int n, void* y, int y_f32) {
-  const int token = blockIdx.x;
-  for (int c = threadIdx.x; c < n; c += 256) {
-    float sum = 0.f;
+  const size_t first = (size_t)blockIdx.x * topk;
+  for (int c = (blockIdx.y * 256 + threadIdx.x) * V; c < n; c += gridDim.y * 256 * V) {
+    float sum[V] = {};
+#pragma unroll 4
     for (int j = 0; j < topk; ++j) {
-      const int p = place[(size_t)token * topk + j];
-      if (p >= 0) sum += gates[(size_t)token * topk + j] * part[(size_t)p * n + c];
+      const int p = place[first + j];
+      if (p < 0) continue;
+      const float g = gates[first + j];
+      const float* from = part + (size_t)p * n + c;
+      if (V == 4) {
+        const f4_t v = *reinterpret_cast<const f4_t*>(from);
+#pragma unroll
+        for (int i = 0; i < V; ++i) sum[i] += g * v[i];
+      } else {
+        sum[0] += g * from[0];
+      }
     }
-    const size_t dst = (size_t)token * n + c;
-    if (y_f32)
-      reinterpret_cast<float*>(y)[dst] = sum;
-    else
-      reinterpret_cast<_Float16*>(y)[dst] = (_Float16)sum;
+    const size_t dst = (size_t)blockIdx.x * n + c;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      if (y_f32)
+        reinterpret_cast<float*>(y)[dst + i] = sum[i];
+      else
+        reinterpret_cast<_Float16*>(y)[dst + i] = (_Float16)sum[i];
+    }
   }
 }
 
@@ -113,7 +139,12 @@ hipError_t launch_q4_plan(const int32_t* ids, int slots, int experts, int rows, 
 
 hipError_t launch_q4_combine(const float* part, const int32_t* place, const float* gates, int m, int topk, int n,
                              void* y, int y_f32, hipStream_t s) {
-  hipLaunchKernelGGL(q4_combine_kernel, dim3((unsigned)m), dim3(256), 0, s, part, place, gates, topk, n, y, y_f32);
+  const int v = n % 4 ? 1 : 4, blocks = (n + 256 * v - 1) / (256 * v);
+  const dim3 grid((unsigned)m, (unsigned)(blocks < 64 ? blocks : 64));
+  if (v == 4)
+    hipLaunchKernelGGL((q4_combine_kernel<4>), grid, dim3(256), 0, s, part, place, gates, topk, n, y, y_f32);
+  else
+    hipLaunchKernelGGL((q4_combine_kernel<1>), grid, dim3(256), 0, s, part, place, gates, topk, n, y, y_f32);
   return hipGetLastError();
 }
 

@@ -41,7 +41,12 @@ __global__ __launch_bounds__(W * 64) void q4_rows_kernel(const Q4Args a, const i
   const int r = lane & 15, kq = lane >> 4;
   const int k = a.k, ng = k / G, T = (k + 127) / 128;
   const int width = up ? a.n / 2 : a.n;  // output columns
-  const int n0 = blockIdx.x * 16 * NBO;
+  // Plain: the row chunks of one panel follow each other on one XCD
+  // (blockIdx % 8), whose L2 then reads the panel once.
+  const int chunks = MODE == kQ4Plain ? (a.m + XR - 1) / XR : 1;
+  const int panel = MODE == kQ4Plain ? (int)blockIdx.x / 8 / chunks * 8 + (int)blockIdx.x % 8 : (int)blockIdx.x;
+  const int n0 = panel * 16 * NBO;
+  if (MODE == kQ4Plain && n0 >= width) return;
   w4_t* const cl = lds + wave * S;
   w4_t* const xl = cl + NB * 64;
   // scales [panel][16][cg], then zero points alike
@@ -60,8 +65,8 @@ __global__ __launch_bounds__(W * 64) void q4_rows_kernel(const Q4Args a, const i
     e = a.ids[blockIdx.y];
     if ((unsigned)e >= (unsigned)a.experts) return;
   } else if (MODE == kQ4Plain) {
-    rows = a.m;
-    pos = 0;
+    pos = (int)blockIdx.x / 8 % chunks * XR;
+    rows = min(a.m - pos, XR);
   }
 
   // panel b: 16 rows from row0(b), as many as exist
@@ -258,19 +263,26 @@ hipError_t launch(const Q4Args& a, int tiles, hipStream_t s) {
   while (scale_bytes(ct * SG, panels, Z) > most && ct > 1) ct = (ct + 1) / 2;
   const size_t bytes = staging + scale_bytes(ct * SG, panels, Z);
   if (bytes > kLdsMost) return hipErrorInvalidValue;
-  const dim3 grid((unsigned)((width + cols - 1) / cols), (unsigned)(MODE == kQ4Plain ? 1 : tiles));
+  const unsigned panels_x = (unsigned)((width + cols - 1) / cols);
+  const dim3 grid = MODE == kQ4Plain ? dim3((panels_x + 7) / 8 * 8 * (unsigned)((a.m + XR - 1) / XR)) : dim3(panels_x, (unsigned)tiles);
   hipLaunchKernelGGL((q4_rows_kernel<G, Z, XR, NB, W, MODE>), grid, dim3(W * 64), bytes, s, a, ct);
   return hipGetLastError();
 }
 
+template <int G, bool Z, int XR>
+hipError_t pick_experts(int mode, const Q4Args& a, int tiles, hipStream_t s) {
+  if (mode == kQ4Up) return launch<G, Z, XR, 2, 4, kQ4Up>(a, tiles, s);
+  return launch<G, Z, XR, 1, 4, kQ4Down>(a, tiles, s);
+}
+
 template <int G, bool Z>
-hipError_t pick(int mode, const Q4Args& a, int tiles, hipStream_t s) {
-  switch (mode) {
-    case kQ4Up: return launch<G, Z, 16, 2, 8, kQ4Up>(a, tiles, s);
-    case kQ4Down: return launch<G, Z, 16, 1, 8, kQ4Down>(a, tiles, s);
-    case kQ4UpSlot: return launch<G, Z, 4, 2, 8, kQ4UpSlot>(a, tiles, s);
-    case kQ4DownToken: return launch<G, Z, 4, 1, 8, kQ4DownToken>(a, tiles, s);
-    default: break;
+hipError_t pick(int mode, const Q4Args& a, int tiles, int rows, hipStream_t s) {
+  if (mode == kQ4UpSlot) return launch<G, Z, 4, 2, 8, kQ4UpSlot>(a, tiles, s);
+  if (mode == kQ4DownToken) return launch<G, Z, 4, 1, 16, kQ4DownToken>(a, tiles, s);
+  if (mode != kQ4Plain) {
+    if (rows <= 4) return pick_experts<G, Z, 4>(mode, a, tiles, s);
+    if (rows <= 16) return pick_experts<G, Z, 16>(mode, a, tiles, s);
+    return pick_experts<G, Z, 32>(mode, a, tiles, s);
   }
   // Wavefronts a panel: 4 where there are panels enough to fill the card, 16
   // where few panels have long rows.  us at W = 4, 8, 16 (m = 1, group 128):
@@ -287,21 +299,22 @@ hipError_t pick(int mode, const Q4Args& a, int tiles, hipStream_t s) {
     if (panels >= 512) return launch<G, Z, 16, 1, 4, kQ4Plain>(a, tiles, s);
     return launch<G, Z, 16, 1, 8, kQ4Plain>(a, tiles, s);
   }
-  // two operands of x: 9 KiB of staging a wavefront; two panels share them
-  // where panels abound (m = 24, 4096 x 4096: 6.4 against 8.0 us; m = 32,
-  // 12288 x 4096: 14.9 against 12.0)
-  if (panels >= 512) return launch<G, Z, 32, 2, 4, kQ4Plain>(a, tiles, s);
+  // Chunks of 32 rows, 9 KiB of staging a wavefront; two panels share them
+  // where panels abound.  us with one panel (W = 6), two (W = 4): m = 24, 4096
+  // x 4096 6.3, 7.9; m = 64, 12288 x 4096 23.4, 17.0; m = 77, 2560 x 9728 at
+  // group 32 18.2, 23.7; m = 128, 4096 x 4096 at group 64 19, 13.5.
+  if ((long long)panels * ((a.m + 31) / 32) >= 512) return launch<G, Z, 32, 2, 4, kQ4Plain>(a, tiles, s);
   return launch<G, Z, 32, 1, 6, kQ4Plain>(a, tiles, s);
 }
 
 }  // namespace
 
-hipError_t launch_q4_rows(int mode, int group, const Q4Args& a, int tiles, hipStream_t s) {
+hipError_t launch_q4_rows(int mode, int group, const Q4Args& a, int tiles, int rows, hipStream_t s) {
   const bool z = a.zero != nullptr;
   switch (group) {
-    case 32: return z ? pick<32, true>(mode, a, tiles, s) : pick<32, false>(mode, a, tiles, s);
-    case 64: return z ? pick<64, true>(mode, a, tiles, s) : pick<64, false>(mode, a, tiles, s);
-    default: return z ? pick<128, true>(mode, a, tiles, s) : pick<128, false>(mode, a, tiles, s);
+    case 32: return z ? pick<32, true>(mode, a, tiles, rows, s) : pick<32, false>(mode, a, tiles, rows, s);
+    case 64: return z ? pick<64, true>(mode, a, tiles, rows, s) : pick<64, false>(mode, a, tiles, rows, s);
+    default: return z ? pick<128, true>(mode, a, tiles, rows, s) : pick<128, false>(mode, a, tiles, rows, s);
   }
 }
 

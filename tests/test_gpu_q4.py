@@ -15,7 +15,7 @@ SHAPES = [
     # m, n, k in groups of 128
     (1, 16, 1), (1, 1, 1), (1, 257, 9), (2, 48, 2), (3, 100, 33), (15, 31, 5), (16, 64, 8), (17, 33, 3), (32, 130, 4),
     (33, 65, 7), (48, 16, 17), (64, 129, 2), (65, 127, 1), (65, 300, 9), (128, 128, 8), (129, 257, 3), (300, 140, 20),
-    (70, 3, 96),
+    (70, 3, 96), (321, 129, 8), (400, 700, 17), (330, 33, 40), (513, 4400, 1), (2050, 4097, 2),
 ]
 
 
@@ -37,7 +37,7 @@ def test_gemm_matches_oracle(m, n, kg, group):
         assert (got == again).all(), "two runs differ"
 
 
-@pytest.mark.parametrize("m", [1, 20, 90])
+@pytest.mark.parametrize("m", [1, 20, 400])
 def test_gemm_scales_and_zero_points_of_any_size(m):
     """Scales from subnormal to 60000 and zero points up to 255: FP32 outputs
     keep their precision and their range."""
@@ -51,7 +51,7 @@ def test_gemm_scales_and_zero_points_of_any_size(m):
     check(L.tern_q4_gemm(upload((q, s, z)), half(x), L.TERN_F32), y, err, "f32", "wide scales")
 
 
-@pytest.mark.parametrize("m", [3, 40, 100])
+@pytest.mark.parametrize("m", [3, 40, 400])
 @pytest.mark.parametrize("group", [32, 128])
 def test_gemm_bad_rows_and_scales_stay_alone(m, group):
     """A NaN or infinity in a row of x reaches that row of y alone, one in a
@@ -77,7 +77,7 @@ def test_gemm_bad_rows_and_scales_stay_alone(m, group):
     assert got[:, 4].isnan().all() and not got[:, 5].isfinite().any()
 
 
-@pytest.mark.parametrize("m", [1, 33, 77])
+@pytest.mark.parametrize("m", [1, 33, 400])
 def test_gemm_writes_its_output_alone(m):
     import torch
     rng = np.random.default_rng(7)
@@ -92,7 +92,7 @@ def test_gemm_writes_its_output_alone(m):
     assert (ws[need:] == 77).all()
 
 
-@pytest.mark.parametrize("m", [0, 1, 80])
+@pytest.mark.parametrize("m", [0, 1, 400])
 def test_gemm_empty(m):
     import torch
     w = L.Q4Matrix(torch.empty((5, 0), dtype=torch.uint8, device="cuda"), torch.empty((5, 0), dtype=torch.float16, device="cuda"))
@@ -102,7 +102,7 @@ def test_gemm_empty(m):
     assert L.tern_q4_gemm(w, torch.ones((m, 128), dtype=torch.float16, device="cuda")).shape == (m, 0)
 
 
-@pytest.mark.parametrize("m", [1, 48, 70])
+@pytest.mark.parametrize("m", [1, 48, 400])
 def test_gemm_captured_and_on_another_stream(m):
     import torch
     rng = np.random.default_rng(8)
@@ -135,7 +135,7 @@ def test_gemm_offsets_past_32_bits():
     pick = [0, 1, n // 2, n - 20, n - 2, n - 1]
     q = np.stack([L.Q4Matrix(codes[r:r + 1].clone(), scale[r:r + 1].clone()).unpack().cpu().numpy()[0] for r in pick])
     s = scale[pick].cpu().numpy()
-    for m in (1, 66):
+    for m in (1, 66, 170):
         x = activations(rng, m, k)
         y, _, err = Q.gemm(q, s, None, group, x)
         got = L.tern_q4_gemm(w, half(x), L.TERN_F32)
@@ -173,7 +173,7 @@ def test_gemm_refusals_of_tensors():
         L.tern_q4_gemm(w, torch.ones(2 * 128 + 1, dtype=torch.float16, **dev)[1:].view(2, 128))
     assert e.value.status == L.TERN_E_ALIGN
     with pytest.raises(L.TernError) as e:
-        big = torch.ones((70, 4096), dtype=torch.float16, **dev)
+        big = torch.ones((400, 4096), dtype=torch.float16, **dev)
         wide = L.Q4Matrix(torch.zeros((8, 2048), dtype=torch.uint8, **dev), torch.ones((8, 32), dtype=torch.float16, **dev))
         L.tern_q4_gemm(wide, big, ws=torch.empty(16, dtype=torch.uint8, **dev))
     assert e.value.status == L.TERN_E_WORKSPACE

@@ -21,7 +21,7 @@ def at(d):
     (dict(n=0, codes=None, scale=None), L.TERN_OK),
     (dict(n=-1), L.TERN_E_INVAL), (dict(k=-64), L.TERN_E_INVAL), (dict(count=-1), L.TERN_E_INVAL),
     (dict(group=16), L.TERN_E_UNSUPPORTED), (dict(group=96), L.TERN_E_UNSUPPORTED), (dict(group=0), L.TERN_E_UNSUPPORTED),
-    (dict(group=256), L.TERN_E_UNSUPPORTED), (dict(k=96), L.TERN_E_UNSUPPORTED), (dict(n=0x7fffffff), L.TERN_E_UNSUPPORTED),
+    (dict(group=256), L.TERN_E_UNSUPPORTED), (dict(k=96), L.TERN_E_UNSUPPORTED), (dict(n=0x7fffffff), L.TERN_E_UNSUPPORTED), (dict(k=(1 << 22) + 64), L.TERN_E_UNSUPPORTED),
     (dict(codes=None), L.TERN_E_INVAL), (dict(scale=None), L.TERN_E_INVAL),
     (dict(codes=0x10008), L.TERN_E_ALIGN), (dict(scale=0x20001), L.TERN_E_ALIGN)])
 def test_check(kw, want):
@@ -47,10 +47,10 @@ def test_gemm_refusals():
     assert g(d=q4(count=2)) == L.TERN_E_INVAL
     assert g(m=0, x=None, y=None) == L.TERN_OK
     assert g(d=q4(n=0), x=None, y=None) == L.TERN_OK
-    need = lib.tern_q4_workspace_bytes(at(d), 100)
+    need = lib.tern_q4_workspace_bytes(at(d), 400)
     assert need > 256
-    assert g(m=100, nb=need - 1) == L.TERN_E_WORKSPACE and g(m=100, ws=None) == L.TERN_E_WORKSPACE
-    assert g(m=100, ws=0x3008) == L.TERN_E_ALIGN
+    assert g(m=400, nb=need - 1) == L.TERN_E_WORKSPACE and g(m=400, ws=None) == L.TERN_E_WORKSPACE
+    assert g(m=400, ws=0x3008) == L.TERN_E_ALIGN
 
 
 def test_pack_refusals():
