@@ -2,18 +2,25 @@
 // (score + bias), selection of groups, top-k, weights.  The definition
 // stands at tern_route in tern.h.
 //
-// One wavefront per token; lane l holds the experts l, l + 64, ...  What is
-// chosen hangs on the order of the keys alone, so they are FP64: FP32 scores
-// near 1 (sigmoid) or tiny ones (softmax) tie where the exact ones do not.
-// Without a bias both scores grow with the logit and the logit itself is the
-// key.  A round of the top-k takes the largest key of the wavefront, the
-// lowest expert among equals.
+// What is chosen hangs on the order of the keys alone, so their order is
+// that of the FP64 keys: FP32 scores near 1 (sigmoid) or tiny ones (softmax)
+// tie where the exact ones do not.  Without a bias both scores grow with the
+// logit and the logit itself is the key.
+//
+// Most rows need no FP64 keys.  route_kernel packs an FP32 key, rounded down
+// by at most 256 steps, and its expert into one word, lets 16 or 32 lanes a
+// token take the largest word topk + 1 times (a lane keeps its words sorted,
+// the lanes' heads meet in four or five DPP steps), and looks at the gaps
+// between the keys taken: where every gap is wider than the keys' errors, the
+// order is the exact one.  A token with a gap in doubt (FP16 logits as keys
+// have none: they are exact in the word) is routed again by exact_row, 64
+// lanes and FP64 keys.
 #include "q4.h"
 
 namespace tern {
 namespace {
 
-constexpr int kRowsPerWg = 4;
+constexpr int kWaves = 4;  // of a workgroup
 
 __device__ inline double wave_sum(double v) {
 #pragma unroll
@@ -38,12 +45,10 @@ __device__ inline double score_of(float l, int sigmoid, float top, double total)
   return sigmoid ? 1.0 / (1.0 + exp(-(double)l)) : exp((double)l - (double)top) / total;
 }
 
+// One token by one wavefront, keys in FP64; keys: its LDS, EPL * 64.
 template <int EPL, int F16>
-__global__ __launch_bounds__(kRowsPerWg * 64) void route_kernel(const RouteArgs a) {
-  __shared__ double keys[kRowsPerWg][EPL * 64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int row = blockIdx.x * kRowsPerWg + wave;
-  if (row >= a.m) return;  // no barrier below: a wavefront works alone
+__device__ inline void exact_row(const RouteArgs& a, int row, double* keys) {
+  const int lane = threadIdx.x & 63;
   const size_t base = (size_t)row * a.experts;
 
   float l[EPL];
@@ -85,13 +90,13 @@ __global__ __launch_bounds__(kRowsPerWg * 64) void route_kernel(const RouteArgs 
   if (a.groups > 1) {
     const int size = a.experts / a.groups;
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) keys[wave][i * 64 + lane] = key[i];
+    for (int i = 0; i < EPL; ++i) keys[i * 64 + lane] = key[i];
     __builtin_amdgcn_wave_barrier();
     __threadfence_block();
     double one = -INFINITY, two = -INFINITY;
     if (lane < a.groups)
       for (int i = 0; i < size; ++i) {
-        const double v = keys[wave][lane * size + i];
+        const double v = keys[lane * size + i];
         if (v > one) {
           two = one;
           one = v;
@@ -152,20 +157,227 @@ __global__ __launch_bounds__(kRowsPerWg * 64) void route_kernel(const RouteArgs 
   }
 }
 
+template <int EPL, int F16>
+__global__ __launch_bounds__(kWaves * 64) void route_exact_kernel(const RouteArgs a) {
+  __shared__ double keys[kWaves][EPL * 64];
+  const int wave = threadIdx.x >> 6, row = blockIdx.x * kWaves + wave;
+  if (row < a.m) exact_row<EPL, F16>(a, row, keys[wave]);  // no barrier inside
+}
+
+// ---- packed keys
+// Sortable words, expert in the low eight bits (the lower expert larger), 0
+// for a masked one.  Keys that are logits: FP32's bits in order.  Scores plus
+// bias: fixed point, 2^-29, for |key| < 2 (others are in doubt).
+__device__ inline uint32_t pack_float(float v, int e) {
+  const uint32_t b = __builtin_bit_cast(uint32_t, v);
+  return (((int32_t)b < 0 ? ~b : b | 0x80000000u) & ~255u) | (uint32_t)(255 - e);
+}
+__device__ inline float unpack_float(uint32_t w) {
+  w &= ~255u;
+  return __builtin_bit_cast(float, w & 0x80000000u ? w & 0x7FFFFFFFu : ~w);
+}
+__device__ inline uint32_t pack_fixed(float v, int e) {
+  return (((uint32_t)(int32_t)(v * 0x1p29f) ^ 0x80000000u) & ~255u) | (uint32_t)(255 - e);
+}
+__device__ inline float unpack_fixed(uint32_t w) { return (float)(int32_t)((w & ~255u) ^ 0x80000000u) * 0x1p-29f; }
+
+template <int CTRL>
+__device__ inline uint32_t dpp(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, CTRL, 0xF, 0xF, false);
+}
+
+// The largest word of a token's LPR lanes, in all of them.
+template <int LPR>
+__device__ inline uint32_t lanes_max(uint32_t v) {
+  v = max(v, dpp<0x128>(v));  // row_ror 8, 4, 2, 1: the 16 lanes of a DPP row
+  v = max(v, dpp<0x124>(v));
+  v = max(v, dpp<0x122>(v));
+  v = max(v, dpp<0x121>(v));
+  if (LPR == 32) {
+    const auto p = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    v = max(p[0], p[1]);
+  }
+  return v;
+}
+
+// Errors of an FP32 score: the exponential (argument and result) and the
+// reciprocal or the sum, below 2^-20 for both scores; 2^-18 covers two of
+// them twice over.
+constexpr float kScoreDoubt = 0x1p-18f;
+
+// LPR lanes a token, EPL consecutive experts each.  Takes topk <= LPR and, if
+// there are groups, whole runs of a power of two of lanes.
+template <int LPR, int EPL, int F16>
+__global__ __launch_bounds__(kWaves * 64) void route_kernel(const RouteArgs a) {
+  constexpr int RPW = 64 / LPR;                       // tokens of a wavefront
+  constexpr int XPL = (LPR * EPL + 63) / 64;          // experts per lane of exact_row
+  __shared__ double keys[kWaves][XPL * 64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int in = lane % LPR;                          // lane among the token's
+  const int first = (blockIdx.x * kWaves + wave) * RPW, row = first + lane / LPR;
+  if (first >= a.m) return;  // no barrier below: a wavefront works alone
+  const size_t base = (size_t)min(row, a.m - 1) * a.experts;
+  const bool plain_key = a.bias == nullptr && (a.groups == 1 || a.best == 1);
+
+  float l[EPL];
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) {
+    const int e = in * EPL + i;
+    l[i] = -INFINITY;
+    if (e < a.experts) l[i] = load_logit<F16>(a.logits, base + e);
+  }
+  // softmax: the largest logit, and the sum where it is needed: FP64 for the
+  // weights, FP32 for packed keys
+  float top = 0.f;
+  double total = 1.0;
+  if (!a.sigmoid) {
+    float most = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) most = fmaxf(most, l[i]);
+    const uint32_t b = __builtin_bit_cast(uint32_t, most);
+    const uint32_t w = lanes_max<LPR>((int32_t)b < 0 ? ~b : b | 0x80000000u);
+    top = __builtin_bit_cast(float, w & 0x80000000u ? w & 0x7FFFFFFFu : ~w);
+    if (top == -INFINITY) top = 0.f;
+    if (!a.renorm || !plain_key) {
+      double sum = 0.0;
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) {
+        if (a.renorm)
+          sum += (double)__expf(l[i] - top);
+        else if (l[i] != -INFINITY)
+          sum += exp((double)l[i] - (double)top);
+      }
+#pragma unroll
+      for (int d = 1; d < LPR; d <<= 1) sum += __shfl_xor(sum, d);
+      total = fmax(sum, 1.0);
+    }
+  }
+
+  uint32_t q[EPL];
+  bool doubt = false;
+  const float share = (float)(1.0 / total);
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) {
+    const int e = in * EPL + i;
+    float c = l[i];
+    if (!plain_key) {
+      c = a.sigmoid ? __builtin_amdgcn_rcpf(1.0f + __expf(-l[i])) : __expf(l[i] - top) * share;
+      if (a.bias && e < a.experts) c += a.bias[e];
+      if (l[i] == -INFINITY || !(c == c)) c = -INFINITY;
+      if (c != -INFINITY && !(fabsf(c) < 2.0f)) doubt = true;
+    }
+    q[i] = c == -INFINITY ? 0u : plain_key ? pack_float(c, e) : pack_fixed(fabsf(c) < 2.0f ? c : 0.0f, e);
+  }
+  // the lane's words, largest first
+  auto order = [&](int i, int j) {
+    const uint32_t hi = max(q[i], q[j]), lo = min(q[i], q[j]);
+    q[i] = hi;
+    q[j] = lo;
+  };
+  if (EPL == 8) {
+    order(0, 1), order(2, 3), order(4, 5), order(6, 7);
+    order(0, 2), order(1, 3), order(4, 6), order(5, 7);
+    order(1, 2), order(5, 6), order(0, 4), order(3, 7);
+    order(1, 5), order(2, 6);
+    order(1, 4), order(3, 6);
+    order(2, 4), order(3, 5);
+    order(3, 4);
+  } else {
+    order(0, 1), order(2, 3), order(0, 2), order(1, 3), order(1, 2);
+  }
+  auto value = [&](uint32_t w) { return plain_key ? unpack_float(w) : unpack_fixed(w); };
+  // how far apart two packed keys must be for their order to be certain
+  const bool exact_keys = plain_key && F16;
+  auto margin = [&](float v) { return plain_key ? fabsf(v) * 0x1p-14f : kScoreDoubt; };
+
+  if (a.groups > 1) {
+    const int span = a.experts / a.groups / EPL;  // lanes of a group, a power of two
+    uint32_t one = q[0], two = q[1];
+    for (int d = 1; d < span; d <<= 1) {
+      const uint32_t o1 = __shfl_xor(one, d), o2 = __shfl_xor(two, d);
+      two = max(min(one, o1), max(two, o2));
+      one = max(one, o1);
+    }
+    float sum = one ? value(one) : -INFINITY;
+    if (a.best == 2 && two) sum += value(two);
+    const int mine = in / span;
+    int rank = 0;
+    for (int g = 0; g < a.groups; ++g) {
+      const float v = __shfl(sum, lane - in + g * span);
+      if (v > sum || (v == sum && g < mine)) ++rank;
+      if (!exact_keys && g != mine && sum != -INFINITY && fabsf(v - sum) <= 2.0f * margin(sum)) doubt = true;
+    }
+    if (rank >= a.keep) {
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) q[i] = 0;
+    }
+  }
+
+  int mine = -1;
+  uint32_t last = 0;
+  for (int j = 0; j <= a.topk; ++j) {
+    const uint32_t w = lanes_max<LPR>(q[0]);
+    if (!exact_keys && j && w) {  // beside the one before: certainly smaller?
+      const float v = value(last);
+      if (!(v - value(w) > margin(v))) doubt = true;
+    }
+    if (j == a.topk) break;
+    if (in == j && w) mine = 255 - (int)(w & 255u);
+    const bool taken = w && q[0] == w;
+#pragma unroll
+    for (int i = 0; i + 1 < EPL; ++i) q[i] = taken ? q[i + 1] : q[i];
+    q[EPL - 1] = taken ? 0u : q[EPL - 1];
+    last = w;
+  }
+
+  double g = 0.0;
+  if (mine >= 0) g = score_of(load_logit<F16>(a.logits, base + mine), a.sigmoid, top, a.renorm ? 1.0 : total);
+  if (a.renorm) {
+    double sum = g;
+#pragma unroll
+    for (int d = 1; d < LPR; d <<= 1) sum += __shfl_xor(sum, d);
+    g = sum > 0.0 ? g / sum : 0.0;
+  }
+  const unsigned long long again = __ballot(doubt);
+  constexpr unsigned long long kMine = LPR == 32 ? 0xFFFFFFFFull : 0xFFFFull;
+  if (row < a.m && in < a.topk && !(again & (kMine << (lane - in)))) {
+    a.ids[(size_t)row * a.topk + in] = mine;
+    a.weights[(size_t)row * a.topk + in] = (float)(g * (double)a.scale);
+  }
+  if (again) {
+    for (int t = 0; t < RPW; ++t)
+      if (first + t < a.m && (again & (kMine << (t * LPR)))) exact_row<XPL, F16>(a, first + t, keys[wave]);
+  }
+}
+
+template <int LPR, int EPL, int F16>
+hipError_t launch(const RouteArgs& a, hipStream_t s) {
+  constexpr int rows = kWaves * (64 / LPR);
+  hipLaunchKernelGGL((route_kernel<LPR, EPL, F16>), dim3((unsigned)((a.m + rows - 1) / rows)), dim3(kWaves * 64), 0, s, a);
+  return hipGetLastError();
+}
+
+template <int EPL, int F16>
+hipError_t launch_exact(const RouteArgs& a, hipStream_t s) {
+  hipLaunchKernelGGL((route_exact_kernel<EPL, F16>), dim3((unsigned)((a.m + kWaves - 1) / kWaves)), dim3(kWaves * 64), 0, s, a);
+  return hipGetLastError();
+}
+
 template <int F16>
 hipError_t pick(const RouteArgs& a, hipStream_t s) {
-  const dim3 grid((unsigned)((a.m + kRowsPerWg - 1) / kRowsPerWg)), block(kRowsPerWg * 64);
-  if (a.experts <= 64)
-    hipLaunchKernelGGL((route_kernel<1, F16>), grid, block, 0, s, a);
-  else if (a.experts <= 128)
-    hipLaunchKernelGGL((route_kernel<2, F16>), grid, block, 0, s, a);
-  else if (a.experts <= 256)
-    hipLaunchKernelGGL((route_kernel<4, F16>), grid, block, 0, s, a);
-  else if (a.experts <= 512)
-    hipLaunchKernelGGL((route_kernel<8, F16>), grid, block, 0, s, a);
-  else
-    hipLaunchKernelGGL((route_kernel<16, F16>), grid, block, 0, s, a);
-  return hipGetLastError();
+  const int lpr = a.experts <= 128 ? 16 : 32, epl = a.experts <= 64 ? 4 : 8;
+  const int size = a.experts / a.groups, span = size / epl;
+  const bool packed = a.experts <= 256 && a.topk <= lpr && (a.groups == 1 || (size % epl == 0 && (span & (span - 1)) == 0));
+  if (packed) {
+    if (a.experts <= 64) return launch<16, 4, F16>(a, s);
+    if (a.experts <= 128) return launch<16, 8, F16>(a, s);
+    return launch<32, 8, F16>(a, s);
+  }
+  if (a.experts <= 64) return launch_exact<1, F16>(a, s);
+  if (a.experts <= 128) return launch_exact<2, F16>(a, s);
+  if (a.experts <= 256) return launch_exact<4, F16>(a, s);
+  if (a.experts <= 512) return launch_exact<8, F16>(a, s);
+  return launch_exact<16, F16>(a, s);
 }
 
 }  // namespace

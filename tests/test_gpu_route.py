@@ -81,6 +81,22 @@ def test_route_keys_that_fp32_cannot_tell_apart():
     run(np.full((2, 32), -120, np.float32) - np.arange(32, dtype=np.float32), 4, "sigmoid", None, 4, 2, 2)
 
 
+@pytest.mark.parametrize("experts,groups,topk", [(64, 4, 6), (128, 2, 8), (256, 8, 8), (200, 5, 12)])
+def test_route_near_ties(experts, groups, topk):
+    """Keys a few FP32 steps apart, in any order, beside clear ones; biases
+    that cancel the scores' differences; biases far out."""
+    rng = np.random.default_rng(experts)
+    for score in ("softmax", "sigmoid"):
+        l = rng.standard_normal((40, experts)).astype(np.float32)
+        l[::2] = np.float32(1.25) + rng.integers(-6, 7, l[::2].shape).astype(np.float32) * np.float32(2.0 ** -23)
+        run(l, topk, score)
+        run(l, topk, score, np.zeros(experts, np.float32), groups, 2, max(1, groups // 2))
+        run(l, topk, score, (rng.integers(-3, 4, experts) * 2.0 ** -24).astype(np.float32), groups, 1, groups)
+        run(l, topk, score, (10 * rng.standard_normal(experts)).astype(np.float32), groups, 2, groups)
+        run(l, topk, score, None, groups, 2, 1 if topk <= experts // groups else 2, renorm=False)
+        run((1e-30 * l).astype(np.float32), topk, score)
+
+
 def test_route_captured():
     import torch
     l = torch.randn((33, 64), device="cuda")
