@@ -7,14 +7,18 @@
 // tie where the exact ones do not.  Without a bias both scores grow with the
 // logit and the logit itself is the key.
 //
-// Most rows need no FP64 keys.  route_kernel packs an FP32 key, rounded down
+// Most rows need few FP64 keys.  route_kernel packs an FP32 key, rounded down
 // by at most 256 steps, and its expert into one word, lets 16 or 32 lanes a
 // token take the largest word topk + 1 times (a lane keeps its words sorted,
 // the lanes' heads meet in four or five DPP steps), and looks at the gaps
-// between the keys taken: where every gap is wider than the keys' errors, the
-// order is the exact one.  A token with a gap in doubt (FP16 logits as keys
-// have none: they are exact in the word) is routed again by exact_row, 64
-// lanes and FP64 keys.
+// between the words taken: where every gap is wider than the keys' errors,
+// the order is the exact one (logits from FP16 are exact in the word).
+// Otherwise the FP64 keys of the words up to the next wide gap put these in
+// order; groups in doubt are told apart by their FP64 sums.  A token that
+// finds no such gap, or a softmax with a bias and a doubt, is routed again by
+// exact_row, 64 lanes and FP64 keys for every expert.
+// 16384 tokens, 256 experts, sigmoid, bias, 4 of 8 groups, top 8: bound by
+// the vector instructions, some 300 a token.
 #include "q4.h"
 
 namespace tern {
@@ -33,16 +37,50 @@ __device__ inline float wave_max(float v) {
   return v;
 }
 
+// NaN counts as minus infinity, plus infinity as the largest value, -0 as 0.
+__device__ inline float clean_logit(float v) {
+  if (!(v == v)) v = -INFINITY;
+  return fminf(v, 3.4028234663852886e38f) + 0.0f;
+}
+
 template <int F16>
 __device__ inline float load_logit(const void* logits, size_t i) {
   float v = F16 ? (float)reinterpret_cast<const _Float16*>(logits)[i] : reinterpret_cast<const float*>(logits)[i];
-  if (!(v == v)) v = -INFINITY;
-  return fminf(v, 3.4028234663852886e38f);
+  return clean_logit(v);
 }
 
 // The score of a logit that is not minus infinity (top, total: softmax's).
 __device__ inline double score_of(float l, int sigmoid, float top, double total) {
   return sigmoid ? 1.0 / (1.0 + exp(-(double)l)) : exp((double)l - (double)top) / total;
+}
+
+template <int CTRL>
+__device__ inline uint32_t dpp(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, CTRL, 0xF, 0xF, false);
+}
+
+// The largest word of LPR consecutive lanes (16, 32 or 64), in all of them.
+template <int LPR>
+__device__ inline uint32_t lanes_max(uint32_t v) {
+  v = max(v, dpp<0x128>(v));  // row_ror 8, 4, 2, 1: the 16 lanes of a DPP row
+  v = max(v, dpp<0x124>(v));
+  v = max(v, dpp<0x122>(v));
+  v = max(v, dpp<0x121>(v));
+  if (LPR >= 32) {
+    const auto p = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    v = max(p[0], p[1]);
+  }
+  if (LPR == 64) {
+    const auto p = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    v = max(p[0], p[1]);
+  }
+  return v;
+}
+
+// FP64's bits in order; 0 for a masked expert.
+__device__ inline uint64_t sortable(double v) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v + 0.0);  // no -0: it ties with 0
+  return v == -INFINITY ? 0 : (int64_t)b < 0 ? ~b : b | 0x8000000000000000ull;
 }
 
 // One token by one wavefront, keys in FP64; keys: its LDS, EPL * 64.
@@ -119,30 +157,28 @@ __device__ inline void exact_row(const RouteArgs& a, int row, double* keys) {
     }
   }
 
+  uint64_t q[EPL];
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) q[i] = sortable(key[i]);
   int mine = -1;
   for (int j = 0; j < a.topk; ++j) {
-    double best = -INFINITY;
-    int at = 0x7fffffff;
+    uint64_t best = 0;
+    uint32_t at = 0;  // 1024 - expert: the lowest expert among equals
 #pragma unroll
     for (int i = 0; i < EPL; ++i)
-      if (key[i] > best) {
-        best = key[i];
-        at = i * 64 + lane;
+      if (q[i] > best) {
+        best = q[i];
+        at = 1024 - (i * 64 + lane);
       }
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-      const double v = __shfl_xor(best, d);
-      const int w = __shfl_xor(at, d);
-      if (v > best || (v == best && w < at)) {
-        best = v;
-        at = w;
-      }
-    }
-    if (best == -INFINITY) break;
-    if (lane == j) mine = at;
+    const uint32_t hi = lanes_max<64>((uint32_t)(best >> 32));
+    if (hi == 0) break;  // only masked ones are left (an unmasked word has bits there)
+    const uint32_t lo = lanes_max<64>((uint32_t)(best >> 32) == hi ? (uint32_t)best : 0u);
+    const uint32_t who = lanes_max<64>((uint32_t)(best >> 32) == hi && (uint32_t)best == lo ? at : 0u);
+    const int e = 1024 - (int)who;
+    if (lane == j) mine = e;
 #pragma unroll
     for (int i = 0; i < EPL; ++i)
-      if (at == i * 64 + lane) key[i] = -INFINITY;
+      if (e == i * 64 + lane) q[i] = 0;
   }
 
   double g = 0.0;
@@ -181,36 +217,22 @@ __device__ inline uint32_t pack_fixed(float v, int e) {
 }
 __device__ inline float unpack_fixed(uint32_t w) { return (float)(int32_t)((w & ~255u) ^ 0x80000000u) * 0x1p-29f; }
 
-template <int CTRL>
-__device__ inline uint32_t dpp(uint32_t v) {
-  return (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, CTRL, 0xF, 0xF, false);
-}
+// Two packed keys nearer than this are in doubt: an FP32 sigmoid is off by
+// 2^-22 at most (|l| 2^-23 + 2^-23 from the exponential, times a slope of 1/4
+// and at most 0.23 / |l|; the sum and the reciprocal), a softmax score by
+// 2^-20.5 (its sum's error among them), a bias's addition by 2^-23, and a
+// word drops up to 2^-21.
+constexpr int kMore = 4;  // words beyond the topk-th that settle a doubt about it
+constexpr float kSigmoidDoubt = 0x1p-19f, kSoftmaxDoubt = 0x1p-18f;
 
-// The largest word of a token's LPR lanes, in all of them.
-template <int LPR>
-__device__ inline uint32_t lanes_max(uint32_t v) {
-  v = max(v, dpp<0x128>(v));  // row_ror 8, 4, 2, 1: the 16 lanes of a DPP row
-  v = max(v, dpp<0x124>(v));
-  v = max(v, dpp<0x122>(v));
-  v = max(v, dpp<0x121>(v));
-  if (LPR == 32) {
-    const auto p = __builtin_amdgcn_permlane16_swap(v, v, false, false);
-    v = max(p[0], p[1]);
-  }
-  return v;
-}
 
-// Errors of an FP32 score: the exponential (argument and result) and the
-// reciprocal or the sum, below 2^-20 for both scores; 2^-18 covers two of
-// them twice over.
-constexpr float kScoreDoubt = 0x1p-18f;
-
-// LPR lanes a token, EPL consecutive experts each.  Takes topk <= LPR and, if
+// LPR lanes a token, EPL consecutive experts each.  Takes topk + kMore <= LPR and, if
 // there are groups, whole runs of a power of two of lanes.
 template <int LPR, int EPL, int F16>
-__global__ __launch_bounds__(kWaves * 64) void route_kernel(const RouteArgs a) {
+__global__ __launch_bounds__(kWaves * 64, 8) void route_kernel(const RouteArgs a) {
   constexpr int RPW = 64 / LPR;                       // tokens of a wavefront
   constexpr int XPL = (LPR * EPL + 63) / 64;          // experts per lane of exact_row
+  constexpr unsigned long long kMine = LPR == 32 ? 0xFFFFFFFFull : 0xFFFFull;
   __shared__ double keys[kWaves][XPL * 64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int in = lane % LPR;                          // lane among the token's
@@ -219,12 +241,47 @@ __global__ __launch_bounds__(kWaves * 64) void route_kernel(const RouteArgs a) {
   const size_t base = (size_t)min(row, a.m - 1) * a.experts;
   const bool plain_key = a.bias == nullptr && (a.groups == 1 || a.best == 1);
 
-  float l[EPL];
+  // this lane's logits and biases: 16 bytes a load where rows allow it
+  float l[EPL], bias[EPL] = {};
+  const bool whole = a.experts % EPL == 0 && !((uintptr_t)a.logits & 15) && !((uintptr_t)a.bias & 15);
+  if (whole) {
 #pragma unroll
-  for (int i = 0; i < EPL; ++i) {
-    const int e = in * EPL + i;
-    l[i] = -INFINITY;
-    if (e < a.experts) l[i] = load_logit<F16>(a.logits, base + e);
+    for (int i = 0; i < EPL; ++i) l[i] = -INFINITY;
+    if (in * EPL < a.experts) {
+      if (F16) {
+        typedef _Float16 hv_t __attribute__((ext_vector_type(EPL)));
+        const hv_t v = *reinterpret_cast<const hv_t*>(reinterpret_cast<const _Float16*>(a.logits) + base + in * EPL);
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) l[i] = (float)v[i];
+      } else {
+#pragma unroll
+        for (int i = 0; i < EPL; i += 4) {
+          const f4_t v = *reinterpret_cast<const f4_t*>(reinterpret_cast<const float*>(a.logits) + base + in * EPL + i);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) l[i + j] = v[j];
+        }
+      }
+      if (a.bias) {
+#pragma unroll
+        for (int i = 0; i < EPL; i += 4) {
+          const f4_t v = *reinterpret_cast<const f4_t*>(a.bias + in * EPL + i);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) bias[i + j] = v[j];
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) l[i] = clean_logit(l[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+      const int e = in * EPL + i;
+      l[i] = -INFINITY;
+      if (e < a.experts) {
+        l[i] = load_logit<F16>(a.logits, base + e);
+        if (a.bias) bias[i] = a.bias[e];
+      }
+    }
   }
   // softmax: the largest logit, and the sum where it is needed: FP64 for the
   // weights, FP32 for packed keys
@@ -262,7 +319,7 @@ __global__ __launch_bounds__(kWaves * 64) void route_kernel(const RouteArgs a) {
     float c = l[i];
     if (!plain_key) {
       c = a.sigmoid ? __builtin_amdgcn_rcpf(1.0f + __expf(-l[i])) : __expf(l[i] - top) * share;
-      if (a.bias && e < a.experts) c += a.bias[e];
+      c += bias[i];
       if (l[i] == -INFINITY || !(c == c)) c = -INFINITY;
       if (c != -INFINITY && !(fabsf(c) < 2.0f)) doubt = true;
     }
@@ -288,7 +345,7 @@ __global__ __launch_bounds__(kWaves * 64) void route_kernel(const RouteArgs a) {
   auto value = [&](uint32_t w) { return plain_key ? unpack_float(w) : unpack_fixed(w); };
   // how far apart two packed keys must be for their order to be certain
   const bool exact_keys = plain_key && F16;
-  auto margin = [&](float v) { return plain_key ? fabsf(v) * 0x1p-14f : kScoreDoubt; };
+  auto margin = [&](float v) { return plain_key ? fabsf(v) * 0x1p-14f : a.sigmoid ? kSigmoidDoubt : kSoftmaxDoubt; };
 
   if (a.groups > 1) {
     const int span = a.experts / a.groups / EPL;  // lanes of a group, a power of two
@@ -301,11 +358,48 @@ __global__ __launch_bounds__(kWaves * 64) void route_kernel(const RouteArgs a) {
     float sum = one ? value(one) : -INFINITY;
     if (a.best == 2 && two) sum += value(two);
     const int mine = in / span;
-    int rank = 0;
+    int rank = 0;  // groups before this one
     for (int g = 0; g < a.groups; ++g) {
       const float v = __shfl(sum, lane - in + g * span);
       if (v > sum || (v == sum && g < mine)) ++rank;
-      if (!exact_keys && g != mine && sum != -INFINITY && fabsf(v - sum) <= 2.0f * margin(sum)) doubt = true;
+    }
+    if (!exact_keys) {  // the last group kept, certainly before the next?
+      const uint32_t b = __builtin_bit_cast(uint32_t, sum), w = (int32_t)b < 0 ? ~b : b | 0x80000000u;
+      const bool kept = rank < a.keep && in < a.groups * span;
+      const uint32_t least = ~lanes_max<LPR>(kept ? ~w : 0u), most = lanes_max<LPR>(kept || in >= a.groups * span ? 0u : w);
+      auto back = [](uint32_t v) { return __builtin_bit_cast(float, v & 0x80000000u ? v & 0x7FFFFFFFu : ~v); };
+      const float x = back(least), y = back(most);
+      const bool unsure = most && y != -INFINITY && !(x - y > 2.0f * margin(x));
+      if (__ballot(unsure)) {
+        if (!plain_key && !a.sigmoid) {
+          doubt = doubt || unsure;
+        } else {  // the groups' FP64 sums
+          double first_key = -INFINITY, second_key = -INFINITY;
+          for (int i = 0; i < EPL; ++i) {
+            const int e = in * EPL + i;
+            const float v = e < a.experts ? load_logit<F16>(a.logits, base + e) : -INFINITY;
+            double k = v;
+            if (!plain_key && v != -INFINITY) {
+              k = score_of(v, 1, 0.f, 1.0) + (a.bias ? (double)a.bias[e] : 0.0);
+              if (!(k == k)) k = -INFINITY;
+            }
+            second_key = fmax(second_key, fmin(first_key, k));
+            first_key = fmax(first_key, k);
+          }
+          for (int d = 1; d < span; d <<= 1) {
+            const double o1 = __shfl_xor(first_key, d), o2 = __shfl_xor(second_key, d);
+            second_key = fmax(fmin(first_key, o1), fmax(second_key, o2));
+            first_key = fmax(first_key, o1);
+          }
+          double total_key = first_key;
+          if (a.best == 2 && second_key != -INFINITY) total_key += second_key;
+          rank = 0;
+          for (int g = 0; g < a.groups; ++g) {
+            const double v = __shfl(total_key, lane - in + g * span);
+            if (v > total_key || (v == total_key && g < mine)) ++rank;
+          }
+        }
+      }
     }
     if (rank >= a.keep) {
 #pragma unroll
@@ -313,36 +407,61 @@ __global__ __launch_bounds__(kWaves * 64) void route_kernel(const RouteArgs a) {
     }
   }
 
-  int mine = -1;
-  uint32_t last = 0;
-  for (int j = 0; j <= a.topk; ++j) {
+  // lane j keeps the j-th word taken, topk + 1 of them
+  uint32_t kept = 0;
+  auto take = [&](int j) {
     const uint32_t w = lanes_max<LPR>(q[0]);
-    if (!exact_keys && j && w) {  // beside the one before: certainly smaller?
-      const float v = value(last);
-      if (!(v - value(w) > margin(v))) doubt = true;
-    }
-    if (j == a.topk) break;
-    if (in == j && w) mine = 255 - (int)(w & 255u);
-    const bool taken = w && q[0] == w;
+    if (in == j) kept = w;
+    const bool taken = q[0] == w;  // words differ, but for the zeros at the end
 #pragma unroll
     for (int i = 0; i + 1 < EPL; ++i) q[i] = taken ? q[i + 1] : q[i];
     q[EPL - 1] = taken ? 0u : q[EPL - 1];
-    last = w;
+  };
+  for (int j = 0; j <= a.topk; ++j) take(j);
+  auto certain = [&]() {  // this lane's word is larger than the next in FP64 too
+    const uint32_t next = __shfl_down(kept, 1);
+    const float v = value(kept);
+    return exact_keys || !next || v - value(next) > margin(v);
+  };
+  int at = in;  // where this lane's expert goes
+  bool sure = certain();  // by every lane: a lane reads its neighbour's word
+  if (__ballot(in < a.topk && !sure)) {
+    // A few more words, up to a certain gap; the FP64 keys of those before it
+    // give the order.
+    for (int j = a.topk + 1; j < a.topk + kMore; ++j) take(j);
+    sure = certain();
+    const unsigned long long gap = __ballot(in >= a.topk - 1 && in < a.topk + kMore - 1 && sure) >> (lane - in) & kMine;
+    if (!gap || (!plain_key && !a.sigmoid)) doubt = true;
+    const int count = gap ? __ffsll(gap) : 0;  // words before the gap
+    if (in >= count) kept = 0;
+    const int e = kept ? 255 - (int)(kept & 255u) : -1;
+    double key = -INFINITY;
+    if (e >= 0) {
+      const float v = load_logit<F16>(a.logits, base + e);
+      key = plain_key ? (double)v : score_of(v, 1, 0.f, 1.0) + (a.bias ? (double)a.bias[e] : 0.0);
+      at = 0;
+    }
+    for (int i = 0; i < a.topk + kMore; ++i) {
+      const double k = __shfl(key, lane - in + i);
+      const int o = __shfl(e, lane - in + i);
+      if (e >= 0 && o >= 0 && (k > key || (k == key && o < e))) ++at;
+    }
+  } else if (in >= a.topk) {
+    kept = 0;
   }
+  const int mine = at < a.topk && kept ? 255 - (int)(kept & 255u) : -1;
 
   double g = 0.0;
   if (mine >= 0) g = score_of(load_logit<F16>(a.logits, base + mine), a.sigmoid, top, a.renorm ? 1.0 : total);
   if (a.renorm) {
-    double sum = g;
-#pragma unroll
-    for (int d = 1; d < LPR; d <<= 1) sum += __shfl_xor(sum, d);
+    double sum = g;  // of the first lanes, a power of two of them
+    for (int d = 1; d < a.topk + kMore; d <<= 1) sum += __shfl_xor(sum, d);
     g = sum > 0.0 ? g / sum : 0.0;
   }
   const unsigned long long again = __ballot(doubt);
-  constexpr unsigned long long kMine = LPR == 32 ? 0xFFFFFFFFull : 0xFFFFull;
-  if (row < a.m && in < a.topk && !(again & (kMine << (lane - in)))) {
-    a.ids[(size_t)row * a.topk + in] = mine;
-    a.weights[(size_t)row * a.topk + in] = (float)(g * (double)a.scale);
+  if (row < a.m && at < a.topk && !(again & (kMine << (lane - in)))) {
+    a.ids[(size_t)row * a.topk + at] = mine;
+    a.weights[(size_t)row * a.topk + at] = (float)(g * (double)a.scale);
   }
   if (again) {
     for (int t = 0; t < RPW; ++t)
@@ -367,7 +486,7 @@ template <int F16>
 hipError_t pick(const RouteArgs& a, hipStream_t s) {
   const int lpr = a.experts <= 128 ? 16 : 32, epl = a.experts <= 64 ? 4 : 8;
   const int size = a.experts / a.groups, span = size / epl;
-  const bool packed = a.experts <= 256 && a.topk <= lpr && (a.groups == 1 || (size % epl == 0 && (span & (span - 1)) == 0));
+  const bool packed = a.experts <= 256 && a.topk + kMore <= lpr && (a.groups == 1 || (size % epl == 0 && (span & (span - 1)) == 0));
   if (packed) {
     if (a.experts <= 64) return launch<16, 4, F16>(a, s);
     if (a.experts <= 128) return launch<16, 8, F16>(a, s);

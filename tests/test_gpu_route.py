@@ -62,10 +62,12 @@ def test_route_masked_and_odd_logits(score):
 def test_route_ties_go_to_the_lowest(score):
     rng = np.random.default_rng(2)
     l = rng.integers(-2, 3, (60, 128)).astype(np.float16)
+    l[l == 0] *= rng.choice([-1, 1], (l == 0).sum()).astype(np.float16)  # -0 ties with 0
     flat = np.zeros(128, np.float32)
     for b in (None, flat):
         for groups, best, keep in ((1, 1, 1), (8, 2, 3)):
             run(l, 16, score, b, groups, best, keep)
+            run(l.astype(np.float32), 16, score, b, groups, best, keep)
 
 
 def test_route_keys_that_fp32_cannot_tell_apart():
