@@ -127,6 +127,11 @@ __global__ __launch_bounds__(W * 64) void q4_rows_kernel(const Q4Args a, const i
   for (int i = 0; i < MT; ++i)
 #pragma unroll
     for (int b = 0; b < NB; ++b) acc[i][b] = f4_t{0.f, 0.f, 0.f, 0.f};
+  int slot_id = -1, slot_gate = 0;  // token: lane j holds slot j's expert and gate (topk <= 64, host)
+  if (token && lane < a.topk) {
+    slot_id = a.ids[(size_t)pos * a.topk + lane];
+    slot_gate = __builtin_bit_cast(int, a.gates[(size_t)pos * a.topk + lane]);
+  }
   if (!token) aim(e);
 
   for (int c0 = 0; c0 < T || c0 == 0; c0 += ct) {
@@ -141,9 +146,9 @@ __global__ __launch_bounds__(W * 64) void q4_rows_kernel(const Q4Args a, const i
         p = v / tiles;
         t = c0 + v - p * tiles;
         const size_t slot = (size_t)pos * a.topk + p;
-        const int ex = a.ids[slot];
+        const int ex = __builtin_amdgcn_readlane(slot_id, p);
         if ((unsigned)ex >= (unsigned)a.experts) return false;
-        mul = a.gates[slot];
+        mul = __builtin_bit_cast(float, __builtin_amdgcn_readlane(slot_gate, p));
         aim(ex);
         fx = q4_buffer(a.x + slot * k, (uint32_t)k * 2);
       }
@@ -160,9 +165,24 @@ __global__ __launch_bounds__(W * 64) void q4_rows_kernel(const Q4Args a, const i
     }
     if (c0) __syncthreads();  // the scales before these are in use until here
     if (token) {
-      for (int j = 0; j < a.topk; ++j) {
+      // every slot's scales in one pass: one after another, their latencies would add up
+      const int g0 = c0 * SG, want = min(cg, ng - g0), rc = count(0);
+      const bool whole = rc == 16 && want == ng && !((uintptr_t)a.scale & 15) && (size_t)a.n * ng % 8 == 0 &&
+                         (!Z || (!((uintptr_t)a.zero & 15) && (size_t)a.n * ng % 16 == 0));
+      const int per = whole ? 2 * ng : rc * want;
+      for (int i = threadIdx.x; i < a.topk * per; i += W * 64) {
+        const int j = i / per, c = i - j * per;
         const int ex = a.ids[(size_t)pos * a.topk + j];
-        if ((unsigned)ex < (unsigned)a.experts) stage_scales(ex, 0, j, c0 * SG);
+        if ((unsigned)ex >= (unsigned)a.experts) continue;
+        const size_t at = ((size_t)ex * a.n + n0) * ng;
+        if (whole) {  // 16-byte chunks of 16 rows' scales, and of their zero points
+          reinterpret_cast<w4_t*>(sl + j * 16 * cg)[c] = reinterpret_cast<const w4_t*>(a.scale + at)[c];
+          if (Z && c < ng) reinterpret_cast<w4_t*>(zl + j * 16 * cg)[c] = reinterpret_cast<const w4_t*>(a.zero + at)[c];
+        } else {
+          const int row = c / want, g = c - row * want;
+          sl[(j * 16 + row) * cg + g] = a.scale[at + (size_t)row * ng + g0 + g];
+          if (Z) zl[(j * 16 + row) * cg + g] = a.zero[at + (size_t)row * ng + g0 + g];
+        }
       }
     } else {
 #pragma unroll

@@ -425,21 +425,26 @@ def _tensor(t, name, dtypes, device, shape=None):
     return t
 
 
-class _On:
-    """The device of a call's tensors made current while it runs."""
+_torch = _raw_stream = _current_device = None
 
-    def __init__(self, device):
-        import torch
-        self.other = device.index != torch.cuda.current_device()
-        self.guard = torch.cuda.device(device) if self.other else None
 
-    def __enter__(self):
-        if self.other:
-            self.guard.__enter__()
+def _use_torch():
+    """Looks torch's calls up once: a product of a few microseconds notices
+    what its wrapper costs.  The stream handle comes without a Stream object
+    where torch offers that."""
+    global _torch, _raw_stream, _current_device
+    import torch
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    _raw_stream = raw or (lambda index: torch.cuda.current_stream(index).cuda_stream)
+    _current_device = torch.cuda.current_device
+    _torch = torch
+    return torch
 
-    def __exit__(self, *exc):
-        if self.other:
-            self.guard.__exit__(*exc)
+
+def _elsewhere(device):
+    """Whether `device` is not the current one (then the call is made again
+    with it current)."""
+    return device.index != _current_device()
 
 
 def _fresh(shape, dtype, device, stream):
@@ -478,6 +483,7 @@ class Q4Matrix:
         _tensor(scale, "scale", (torch.float16,), codes.device)
         if zero is not None:
             _tensor(zero, "zero", (torch.uint8,), codes.device, scale.shape)
+        _use_torch()
         self.codes, self.scale, self.zero = codes, scale, zero
         self.device = codes.device
         self.n, self.k = codes.shape[-2], 2 * codes.shape[-1]
@@ -502,7 +508,7 @@ class Q4Matrix:
         _tensor(q, "q", (torch.uint8,), q.device)
         codes = _fresh((*q.shape[:-1], q.shape[-1] // 2), torch.uint8, q.device, stream)
         self = cls(codes, scale, zero)
-        with _On(self.device):
+        with torch.cuda.device(self.device):
             ws = _scratch(256, self.device, stream)
             check(load().tern_q4_pack(_ptr(q), self._at, _ptr(ws), ws.numel(), _stream_of(self.device, stream)))
         return self
@@ -511,23 +517,21 @@ class Q4Matrix:
         """tern_q4_unpack: the codes, one byte each."""
         import torch
         q = _fresh((*self.codes.shape[:-1], self.k), torch.uint8, self.device, stream)
-        with _On(self.device):
+        with torch.cuda.device(self.device):
             check(load().tern_q4_unpack(self._at, _ptr(q), _stream_of(self.device, stream)))
         return q
 
 
 def _stream_of(device, stream):
-    if stream is not None:
-        return stream
-    import torch
-    return torch.cuda.current_stream(device).cuda_stream
+    return stream if stream is not None else _raw_stream(device.index)
 
 
 def _y_type(y_dtype):
-    import torch
-    if y_dtype not in (TERN_F16, TERN_F32):
-        _refuse(f"unknown output dtype {y_dtype}")
-    return torch.float32 if y_dtype == TERN_F32 else torch.float16
+    if y_dtype == TERN_F16:
+        return _torch.float16
+    if y_dtype == TERN_F32:
+        return _torch.float32
+    _refuse(f"unknown output dtype {y_dtype}")
 
 
 def tern_q4_workspace(w: Q4Matrix, m: int):
@@ -538,21 +542,23 @@ def tern_q4_workspace(w: Q4Matrix, m: int):
 def tern_q4_gemm(w: Q4Matrix, x, y_dtype=TERN_F16, out=None, stream=None, ws=None):
     """y = x W^T (x fp16 [m][k], contiguous); returns y [m][n], fp16 or fp32
     per y_dtype, in `out` if given."""
-    import torch
-    _tensor(x, "x", (torch.float16,), w.device)
-    if x.dim() != 2 or x.shape[1] != w.k:
+    device = w.device
+    if _elsewhere(device):
+        with _torch.cuda.device(device):
+            return tern_q4_gemm(w, x, y_dtype, out, stream, ws)
+    _tensor(x, "x", (_torch.float16,), device)
+    if x.dim() != 2 or x.size(1) != w.k:
         _refuse(f"x has shape {tuple(x.shape)}, not [m][{w.k}]")
-    m = x.shape[0]
+    m = x.size(0)
     kind = _y_type(y_dtype)
-    with _On(w.device):
-        if out is None:
-            out = _fresh((m, w.n), kind, w.device, stream)
-        else:
-            _tensor(out, "out", (kind,), w.device, (m, w.n))
-        if ws is None:
-            ws = _scratch(load().tern_q4_workspace_bytes(w._at, m), w.device, stream)
-        check(load().tern_q4_gemm(w._at, _ptr(x), m, _ptr(out), y_dtype, _ptr(ws), ws.numel(),
-                                  _stream_of(w.device, stream)))
+    if out is None:
+        out = _fresh((m, w.n), kind, device, stream)
+    else:
+        _tensor(out, "out", (kind,), device, (m, w.n))
+    if ws is None:
+        ws = _scratch(load().tern_q4_workspace_bytes(w._at, m), device, stream)
+    check(load().tern_q4_gemm(w._at, x.data_ptr(), m, out.data_ptr(), y_dtype, ws.data_ptr(), ws.nbytes,
+                              _stream_of(device, stream)))
     return out
 
 
@@ -560,26 +566,29 @@ def tern_route(logits, topk, score=TERN_SCORE_SOFTMAX, bias=None, groups=1, grou
                scale=1.0, ids=None, weights=None, stream=None):
     """Routes tokens to experts: (ids int32 [m][topk], weights fp32
     [m][topk]) from logits fp16 or fp32 [m][experts], contiguous."""
-    import torch
-    if logits.device.type != "cuda" or logits.dim() != 2:
-        _refuse(f"logits of shape {tuple(logits.shape)} on {logits.device}, not [m][experts] on a GPU")
+    torch = _torch or _use_torch()
     device = logits.device
+    if device.type != "cuda" or logits.dim() != 2:
+        _refuse(f"logits of shape {tuple(logits.shape)} on {device}, not [m][experts] on a GPU")
+    if _elsewhere(device):
+        with torch.cuda.device(device):
+            return tern_route(logits, topk, score, bias, groups, group_best, keep_groups, renorm, scale, ids, weights,
+                              stream)
     _tensor(logits, "logits", (torch.float16, torch.float32), device)
     m, experts = logits.shape
     if bias is not None:
         _tensor(bias, "bias", (torch.float32,), device, (experts,))
-    with _On(device):
-        if ids is None:
-            ids = _fresh((m, max(topk, 0)), torch.int32, device, stream)
-        else:
-            _tensor(ids, "ids", (torch.int32,), device, (m, topk))
-        if weights is None:
-            weights = _fresh((m, max(topk, 0)), torch.float32, device, stream)
-        else:
-            _tensor(weights, "weights", (torch.float32,), device, (m, topk))
-        r = tern_router(experts, topk, score, groups, group_best, keep_groups, int(bool(renorm)), scale, _ptr(bias))
-        check(load().tern_route(_ptr(logits), TERN_F32 if logits.dtype == torch.float32 else TERN_F16, m,
-                                ctypes.addressof(r), _ptr(ids), _ptr(weights), _stream_of(device, stream)))
+    if ids is None:
+        ids = _fresh((m, max(topk, 0)), torch.int32, device, stream)
+    else:
+        _tensor(ids, "ids", (torch.int32,), device, (m, topk))
+    if weights is None:
+        weights = _fresh((m, max(topk, 0)), torch.float32, device, stream)
+    else:
+        _tensor(weights, "weights", (torch.float32,), device, (m, topk))
+    r = tern_router(experts, topk, score, groups, group_best, keep_groups, 1 if renorm else 0, scale, _ptr(bias))
+    check(load().tern_route(logits.data_ptr(), TERN_F32 if logits.dtype == torch.float32 else TERN_F16, m,
+                            ctypes.addressof(r), ids.data_ptr(), weights.data_ptr(), _stream_of(device, stream)))
     return ids, weights
 
 
@@ -592,29 +601,30 @@ def tern_q4_experts(gate_up: Q4Matrix, down: Q4Matrix, x, ids, weights, y_dtype=
                     ws=None):
     """The routed experts' layer: y [m][down.n] from x fp16 [m][gate_up.k],
     ids int32 and weights fp32 [m][topk] (as tern_route returns them)."""
-    import torch
-    device = gate_up.device
+    torch, device = _torch, gate_up.device
+    if _elsewhere(device):
+        with torch.cuda.device(device):
+            return tern_q4_experts(gate_up, down, x, ids, weights, y_dtype, out, stream, ws)
     _tensor(x, "x", (torch.float16,), device)
     if down.device != device:
         _refuse(f"down is on {down.device}, not {device}")
-    if x.dim() != 2 or x.shape[1] != gate_up.k:
+    if x.dim() != 2 or x.size(1) != gate_up.k:
         _refuse(f"x has shape {tuple(x.shape)}, not [m][{gate_up.k}]")
-    m = x.shape[0]
+    m = x.size(0)
     _tensor(ids, "ids", (torch.int32,), device)
-    if ids.dim() != 2 or ids.shape[0] != m:
+    if ids.dim() != 2 or ids.size(0) != m:
         _refuse(f"ids have shape {tuple(ids.shape)}, not [{m}][topk]")
     _tensor(weights, "weights", (torch.float32,), device, ids.shape)
-    topk = ids.shape[1]
+    topk = ids.size(1)
     kind = _y_type(y_dtype)
-    with _On(device):
-        if out is None:
-            out = _fresh((m, down.n), kind, device, stream)
-        else:
-            _tensor(out, "out", (kind,), device, (m, down.n))
-        if ws is None:
-            ws = _scratch(load().tern_q4_experts_workspace_bytes(gate_up._at, down._at, m, topk), device, stream)
-        check(load().tern_q4_experts(gate_up._at, down._at, _ptr(x), m, _ptr(ids), _ptr(weights), topk, _ptr(out),
-                                     y_dtype, _ptr(ws), ws.numel(), _stream_of(device, stream)))
+    if out is None:
+        out = _fresh((m, down.n), kind, device, stream)
+    else:
+        _tensor(out, "out", (kind,), device, (m, down.n))
+    if ws is None:
+        ws = _scratch(load().tern_q4_experts_workspace_bytes(gate_up._at, down._at, m, topk), device, stream)
+    check(load().tern_q4_experts(gate_up._at, down._at, x.data_ptr(), m, ids.data_ptr(), weights.data_ptr(), topk,
+                                 out.data_ptr(), y_dtype, ws.data_ptr(), ws.nbytes, _stream_of(device, stream)))
     return out
 
 
