@@ -56,9 +56,10 @@ enum Q4Mode {
 // Output tiles of the tile kernel: 128 x 256 (one workgroup a CU) and 64 x 128
 // (three).
 constexpr int kQ4TileLarge = 128, kQ4TileSmall = 64;
-// rows: the most rows of a tile, 4, 16 or 32 (rows kernel; expert modes only)
-// or one of the two above (tile kernel).
-hipError_t launch_q4_rows(int mode, int group, const Q4Args& a, int max_tiles, int rows, hipStream_t s);
+// Rows of an experts' tile on the rows kernel.
+constexpr int kQ4TileRows = 16;
+// max_tiles: experts' tiles at most (expert modes); rows: one of the first two.
+hipError_t launch_q4_rows(int mode, int group, const Q4Args& a, int max_tiles, hipStream_t s);
 hipError_t launch_q4_tile(int mode, int group, const Q4Args& a, int max_tiles, int rows, hipStream_t s);
 hipError_t launch_q4_reduce(const Q4Args& a, hipStream_t s);
 hipError_t launch_q4_plan(const int32_t* ids, int slots, int experts, int rows, int4* tiles, int32_t* ntiles,

@@ -127,12 +127,15 @@ ExpertsPlan plan_tokens(const tern_q4* up, const tern_q4* down, int m, int topk)
   const int experts = down->count, inner = down->k, n = down->n;
   const size_t slots = (size_t)m * topk;
   p.direct = slots <= (size_t)kDirectSlots;
-  // Tiles of 4, 16 or 32 rows on the rows kernel (its tiles are a grid's y),
-  // of 64 or 128 on the tile kernel, by the rows an expert has on average.
+  // Tiles of 16 rows on the rows kernel (its tiles are a grid's y), of 64 or
+  // 128 on the tile kernel, by the rows an expert has on average.  us, 64
+  // experts of 2560 x 1024, up and down, 16 / 64 / 128: 8 rows an expert 47 +
+  // 19 / 53 + 25 / 76 + 49; 25 rows 77 + 35 / 62 + 33 / 83 + 51; 100 rows 204 +
+  // 104 / 109 + 57 / 129 + 76; 256 rows 470 + 239 / 231 + 123 / 236 + 139.
   const size_t mean = slots / experts;
-  p.rows = mean < 3 ? 4 : mean < 12 ? 16 : mean < 40 ? 32 : mean < 160 ? tern::kQ4TileSmall : tern::kQ4TileLarge;
-  if (!tile_scales_fit(up->n, up->k) || !tile_scales_fit(n, inner)) p.rows = std::min(p.rows, 32);
-  p.tile = p.rows > 32;
+  p.rows = mean < 20 ? tern::kQ4TileRows : mean < 384 ? tern::kQ4TileSmall : tern::kQ4TileLarge;
+  if (!tile_scales_fit(up->n, up->k) || !tile_scales_fit(n, inner)) p.rows = tern::kQ4TileRows;
+  p.tile = p.rows != tern::kQ4TileRows;
   p.max_tiles = (int)std::min<size_t>(slots, slots / p.rows + experts);
   size_t at = 0;
   auto take = [&](size_t bytes) {
@@ -156,7 +159,7 @@ ExpertsPlan plan_tokens(const tern_q4* up, const tern_q4* down, int m, int topk)
 // below a grid's y, and the workspace does not grow with m without end.
 int round_tokens(const tern_q4* up, int m, int topk) {
   const long long by_x = up->k ? ((1ll << 31) - 1) / (2ll * up->k) : m;
-  return (int)std::max<long long>(1, std::min<long long>({(long long)m, by_x, (1ll << 20) / topk}));
+  return (int)std::max<long long>(1, std::min<long long>({(long long)m, by_x, (1ll << 19) / topk}));
 }
 
 size_t experts_ws(const tern_q4* up, const tern_q4* down, int m, int topk) {
@@ -239,7 +242,7 @@ tern_status tern_q4_gemm(const tern_q4* w, const uint16_t* x, int32_t m, void* y
   const hipStream_t s = (hipStream_t)stream;
   const Route r = route_of(m, w->n, w->k);
   if (r.rows) {
-    Q4_HIP(tern::launch_q4_rows(tern::kQ4Plain, w->group, a, 0, 0, s));
+    Q4_HIP(tern::launch_q4_rows(tern::kQ4Plain, w->group, a, 0, s));
     return TERN_OK;
   }
   if (tiles_of(m, w->n, r.tile) * r.splits > 0x7ffffff0ll) return fail(TERN_E_UNSUPPORTED, "m=%d, n=%d: too many tiles", m, w->n);
@@ -288,10 +291,10 @@ tern_status tern_q4_experts(const tern_q4* gate_up, const tern_q4* down, const u
     u.gates = d.gates = weights + (size_t)t * topk;
     u.topk = d.topk = topk;
     if (p.direct) {
-      if (down->k) Q4_HIP(tern::launch_q4_rows(tern::kQ4UpSlot, gate_up->group, u, mt * topk, 0, s));
+      if (down->k) Q4_HIP(tern::launch_q4_rows(tern::kQ4UpSlot, gate_up->group, u, mt * topk, s));
       d.y = yt;
       d.y_f32 = f32;
-      Q4_HIP(tern::launch_q4_rows(tern::kQ4DownToken, down->group, d, mt, 0, s));
+      Q4_HIP(tern::launch_q4_rows(tern::kQ4DownToken, down->group, d, mt, s));
       continue;
     }
     u.tiles = d.tiles = (const int4*)(base + p.tiles);
@@ -300,9 +303,12 @@ tern_status tern_q4_experts(const tern_q4* gate_up, const tern_q4* down, const u
     d.y = base + p.part;
     Q4_HIP(tern::launch_q4_plan(u.ids, mt * topk, down->count, p.rows, (int4*)(base + p.tiles),
                                 (int32_t*)(base + p.ntiles), (int32_t*)(base + p.order), (int32_t*)(base + p.place), s));
-    auto* launch = p.tile ? tern::launch_q4_tile : tern::launch_q4_rows;
-    if (down->k) Q4_HIP(launch(tern::kQ4Up, gate_up->group, u, p.max_tiles, p.rows, s));
-    Q4_HIP(launch(tern::kQ4Down, down->group, d, p.max_tiles, p.rows, s));
+    auto product = [&](int mode, int group, const tern::Q4Args& a) {
+      return p.tile ? tern::launch_q4_tile(mode, group, a, p.max_tiles, p.rows, s)
+                    : tern::launch_q4_rows(mode, group, a, p.max_tiles, s);
+    };
+    if (down->k) Q4_HIP(product(tern::kQ4Up, gate_up->group, u));
+    Q4_HIP(product(tern::kQ4Down, down->group, d));
     Q4_HIP(tern::launch_q4_combine((const float*)(base + p.part), (const int32_t*)(base + p.place), u.gates, mt, topk,
                                    down->n, yt, f32, s));
   }

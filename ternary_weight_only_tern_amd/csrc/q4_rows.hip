@@ -22,8 +22,13 @@ namespace tern {
 namespace {
 
 // LDS of a workgroup behind the wavefronts' staging: the scales and zero
-// points of `panels` panels over `ct` K tiles.
-constexpr size_t scale_bytes(int groups, int panels, bool z) { return (size_t)panels * 16 * groups * (z ? 3 : 2) + 32; }
+// points of `panels` panels over `groups` groups.  Rows are padded to an odd
+// number of dwords: a tile's 16 rows are read at once.
+__host__ __device__ constexpr int scale_pitch(int groups) { return (groups + 7) / 8 * 8 + 2; }  // halves
+__host__ __device__ constexpr int zero_pitch(int groups) { return (groups + 7) / 8 * 8 + 4; }   // bytes
+constexpr size_t scale_bytes(int groups, int panels, bool z) {
+  return (size_t)panels * 16 * (scale_pitch(groups) * 2 + (z ? zero_pitch(groups) : 0)) + 16;
+}
 constexpr size_t kLdsMost = 64 * 1024, kScaleMost = 20 * 1024;
 
 // XR: rows of x at most (4, 16 or 32).  ct: K tiles whose scales are staged
@@ -49,10 +54,10 @@ __global__ __launch_bounds__(W * 64) void q4_rows_kernel(const Q4Args a, const i
   if (MODE == kQ4Plain && n0 >= width) return;
   w4_t* const cl = lds + wave * S;
   w4_t* const xl = cl + NB * 64;
-  // scales [panel][16][cg], then zero points alike
-  const int cg = min(ct * SG, ng), panels = token ? a.topk : NB;
+  // scales [panel][16][sp], then zero points [panel][16][zp], of cg groups
+  const int cg = min(ct * SG, ng), sp = scale_pitch(cg), zp = zero_pitch(cg), panels = token ? a.topk : NB;
   uint16_t* const sl = reinterpret_cast<uint16_t*>(lds + W * S);
-  uint8_t* const zl = reinterpret_cast<uint8_t*>(sl + panels * 16 * cg);
+  uint8_t* const zl = reinterpret_cast<uint8_t*>(sl + panels * 16 * sp);
 
   int e = 0, rows = 1, pos = blockIdx.y;
   if (MODE == kQ4Up || MODE == kQ4Down) {
@@ -81,26 +86,60 @@ __global__ __launch_bounds__(W * 64) void q4_rows_kernel(const Q4Args a, const i
     for (int b = 0; b < NB; ++b)
       fc[b] = q4_buffer(a.codes + ((size_t)expert * a.n + row0(b)) * (size_t)(k / 2), (uint32_t)count(b) * (uint32_t)(k / 2));
   };
-  // the scales of `expert`'s panel b, groups g0 .. g0 + cg - 1, to slot p
-  auto stage_scales = [&](int expert, int b, int p, int g0) {
-    const size_t at = ((size_t)expert * a.n + row0(b)) * ng;
-    const int rc = count(b), want = min(cg, ng - g0);
-    const uint16_t* s = a.scale + at;
-    const uint8_t* z = Z ? a.zero + at : nullptr;
-    uint16_t* sd = sl + p * 16 * cg;
-    uint8_t* zd = zl + p * 16 * cg;
-    if (rc == 16 && want == ng && !((uintptr_t)s & 15) && (!Z || !((uintptr_t)z & 15)) ) {  // contiguous
-      for (int i = threadIdx.x; i < 2 * ng; i += W * 64)  // 16 rows of 2 ng bytes, then of ng bytes
-        reinterpret_cast<w4_t*>(sd)[i] = reinterpret_cast<const w4_t*>(s)[i];
-      if (Z)
-        for (int i = threadIdx.x; i < ng; i += W * 64) reinterpret_cast<w4_t*>(zd)[i] = reinterpret_cast<const w4_t*>(z)[i];
-    } else {
-      for (int i = threadIdx.x; i < rc * want; i += W * 64) {
-        const int row = i / want, g = i - row * want;
-        sd[row * cg + g] = s[(size_t)row * ng + g0 + g];
-        if (Z) zd[row * cg + g] = z[(size_t)row * ng + g0 + g];
+  // The scales (zero points) of the workgroup's panels, groups g0 and on.  A
+  // panel's 16 rows lie one behind the other: 16 bytes a load where they
+  // start on a multiple of 16.  All panels (a
+  // token: its slots') in one pass; one after another, their latencies would
+  // add up.
+  auto stage_scales = [&](int expert, int g0) {
+    const int want = min(cg, ng - g0);
+    auto first = [&](int p) {  // the panel's first row's offset, or -1
+      int ex = expert;
+      if (token) {
+        ex = a.ids[(size_t)pos * a.topk + p];
+        if ((unsigned)ex >= (unsigned)a.experts) return (int64_t)-1;
       }
-    }
+      return ((int64_t)ex * a.n + row0(token ? 0 : p)) * ng;
+    };
+    auto quotient = [](int i, int d) { return (int)(((float)i + 0.5f) / (float)d); };  // below 2^20, exact
+    auto copy = [&](auto* dst, const auto* src, int pitch) {
+      constexpr int E = 16 / sizeof(*src), D = E / 4;  // elements in 16 bytes, in a dword
+      const bool full = count(0) == 16 && count(token ? 0 : panels - 1) == 16;
+      if (full && want == ng && !((uintptr_t)src & 15) && (size_t)a.n * ng % E == 0) {
+        const int per = 16 * ng / E;
+        const float inv = 1.0f / (float)ng;
+        for (int i = threadIdx.x; i < panels * per; i += W * 64) {
+          const int p = token ? quotient(i, per) : NB == 1 ? 0 : (int)(i >= per), c = (i - p * per) * E;
+          const int64_t at = first(p);
+          if (at < 0) continue;
+          const w4_t v = *reinterpret_cast<const w4_t*>(src + at + c);
+          int row = (int)(((float)c + 0.5f) * inv), col = c - row * ng;
+          row += p * 16;
+          if (ng % D == 0) {
+#pragma unroll
+            for (int d = 0; d < 4; ++d) {
+              *reinterpret_cast<uint32_t*>(dst + row * pitch + col) = v[d];
+              if ((col += D) == ng) col = 0, ++row;
+            }
+          } else {  // dwords straddle rows
+#pragma unroll
+            for (int d = 0; d < E; ++d) {
+              dst[row * pitch + col] = v[d / D] >> (32 / D * (d % D));
+              if (++col == ng) col = 0, ++row;
+            }
+          }
+        }
+      } else {
+        const int per = 16 * want;
+        for (int i = threadIdx.x; i < panels * per; i += W * 64) {
+          const int p = i / per, row = i % per / want, g = i % want;
+          const int64_t at = first(p);
+          if (at >= 0 && row < count(token ? 0 : p)) dst[(p * 16 + row) * pitch + g] = src[at + (int64_t)row * ng + g0 + g];
+        }
+      }
+    };
+    copy(sl, a.scale, sp);
+    if (Z) copy(zl, a.zero, zp);
   };
 
   // the chunks of x this lane stages: row, chunk (swizzled by row like the codes)
@@ -164,30 +203,7 @@ __global__ __launch_bounds__(W * 64) void q4_rows_kernel(const Q4Args a, const i
     for (; v < work && !(have = issue(v)); v += W) {
     }
     if (c0) __syncthreads();  // the scales before these are in use until here
-    if (token) {
-      // every slot's scales in one pass: one after another, their latencies would add up
-      const int g0 = c0 * SG, want = min(cg, ng - g0), rc = count(0);
-      const bool whole = rc == 16 && want == ng && !((uintptr_t)a.scale & 15) && (size_t)a.n * ng % 8 == 0 &&
-                         (!Z || (!((uintptr_t)a.zero & 15) && (size_t)a.n * ng % 16 == 0));
-      const int per = whole ? 2 * ng : rc * want;
-      for (int i = threadIdx.x; i < a.topk * per; i += W * 64) {
-        const int j = i / per, c = i - j * per;
-        const int ex = a.ids[(size_t)pos * a.topk + j];
-        if ((unsigned)ex >= (unsigned)a.experts) continue;
-        const size_t at = ((size_t)ex * a.n + n0) * ng;
-        if (whole) {  // 16-byte chunks of 16 rows' scales, and of their zero points
-          reinterpret_cast<w4_t*>(sl + j * 16 * cg)[c] = reinterpret_cast<const w4_t*>(a.scale + at)[c];
-          if (Z && c < ng) reinterpret_cast<w4_t*>(zl + j * 16 * cg)[c] = reinterpret_cast<const w4_t*>(a.zero + at)[c];
-        } else {
-          const int row = c / want, g = c - row * want;
-          sl[(j * 16 + row) * cg + g] = a.scale[at + (size_t)row * ng + g0 + g];
-          if (Z) zl[(j * 16 + row) * cg + g] = a.zero[at + (size_t)row * ng + g0 + g];
-        }
-      }
-    } else {
-#pragma unroll
-      for (int b = 0; b < NB; ++b) stage_scales(e, b, b, c0 * SG);
-    }
+    stage_scales(e, c0 * SG);
     __syncthreads();
     while (have) {
       q4_loads_done();
@@ -201,18 +217,30 @@ __global__ __launch_bounds__(W * 64) void q4_rows_kernel(const Q4Args a, const i
 #pragma unroll
         for (int j = 0; j < 4; ++j) x[i][j] = __builtin_bit_cast(h8_t, xl[row * 16 + ((x_chunk<G>(j, kq) ^ row) & 15)]);
       }
+      // this tile's scales and zero points of the lane's row; behind the last
+      // group whatever lies there, not used
       uint16_t s[NB][SG];
       uint8_t z[NB][SG];
       const int left = min(SG, (k - t * 128) / G);  // groups in this tile
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
-        const int at = ((token ? p : b) * 16 + r) * cg + (t - c0) * SG;
+        const int row = (token ? p : b) * 16 + r;
+        const uint16_t* from = sl + row * sp + (t - c0) * SG;
+        const uint8_t* zero = zl + row * zp + (t - c0) * SG;
 #pragma unroll
-        for (int j = 0; j < SG; ++j) {
-          const int g = j < left ? j : 0;
-          s[b][j] = sl[at + g];
-          z[b][j] = Z ? zl[at + g] : (uint8_t)8;
+        for (int j = 0; j < SG; j += 2) {
+          if (SG == 1) {
+            s[b][0] = from[0];
+          } else {
+            const uint32_t v = reinterpret_cast<const uint32_t*>(from)[j / 2];
+            s[b][j] = (uint16_t)v;
+            s[b][j + (SG > 1 ? 1 : 0)] = (uint16_t)(v >> 16);
+          }
         }
+        uint32_t v = 0x08080808u;
+        if (Z) v = SG == 4 ? *reinterpret_cast<const uint32_t*>(zero) : SG == 2 ? *reinterpret_cast<const uint16_t*>(zero) : *zero;
+#pragma unroll
+        for (int j = 0; j < SG; ++j) z[b][j] = (uint8_t)(v >> (8 * j));
       }
       const float factor = mul;
       q4_reads_done();
@@ -289,20 +317,19 @@ hipError_t launch(const Q4Args& a, int tiles, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <int G, bool Z, int XR>
-hipError_t pick_experts(int mode, const Q4Args& a, int tiles, hipStream_t s) {
-  if (mode == kQ4Up) return launch<G, Z, XR, 2, 4, kQ4Up>(a, tiles, s);
-  return launch<G, Z, XR, 1, 4, kQ4Down>(a, tiles, s);
-}
-
 template <int G, bool Z>
-hipError_t pick(int mode, const Q4Args& a, int tiles, int rows, hipStream_t s) {
+hipError_t pick(int mode, const Q4Args& a, int tiles, hipStream_t s) {
   if (mode == kQ4UpSlot) return launch<G, Z, 4, 2, 8, kQ4UpSlot>(a, tiles, s);
-  if (mode == kQ4DownToken) return launch<G, Z, 4, 1, 16, kQ4DownToken>(a, tiles, s);
-  if (mode != kQ4Plain) {
-    if (rows <= 4) return pick_experts<G, Z, 4>(mode, a, tiles, s);
-    if (rows <= 16) return pick_experts<G, Z, 16>(mode, a, tiles, s);
-    return pick_experts<G, Z, 32>(mode, a, tiles, s);
+  if (mode == kQ4DownToken) {
+    if (tiles == 1) return launch<G, Z, 4, 1, 16, kQ4DownToken>(a, tiles, s);
+    return launch<G, Z, 4, 1, 8, kQ4DownToken>(a, tiles, s);
+  }
+  if (mode == kQ4Up) return launch<G, Z, 16, 2, 4, kQ4Up>(a, tiles, s);
+  // us, one panel of four wavefronts against two of two: 14 tiles 12.9, 14; 67
+  // tiles 26, 19.4; 130 tiles 49, 35 (2560 x 1024, group 128)
+  if (mode == kQ4Down) {
+    if (tiles < 64) return launch<G, Z, 16, 1, 4, kQ4Down>(a, tiles, s);
+    return launch<G, Z, 16, 2, 2, kQ4Down>(a, tiles, s);
   }
   // Wavefronts a panel: 4 where there are panels enough to fill the card, 16
   // where few panels have long rows.  us at W = 4, 8, 16 (m = 1, group 128):
@@ -329,12 +356,12 @@ hipError_t pick(int mode, const Q4Args& a, int tiles, int rows, hipStream_t s) {
 
 }  // namespace
 
-hipError_t launch_q4_rows(int mode, int group, const Q4Args& a, int tiles, int rows, hipStream_t s) {
+hipError_t launch_q4_rows(int mode, int group, const Q4Args& a, int tiles, hipStream_t s) {
   const bool z = a.zero != nullptr;
   switch (group) {
-    case 32: return z ? pick<32, true>(mode, a, tiles, rows, s) : pick<32, false>(mode, a, tiles, rows, s);
-    case 64: return z ? pick<64, true>(mode, a, tiles, rows, s) : pick<64, false>(mode, a, tiles, rows, s);
-    default: return z ? pick<128, true>(mode, a, tiles, rows, s) : pick<128, false>(mode, a, tiles, rows, s);
+    case 32: return z ? pick<32, true>(mode, a, tiles, s) : pick<32, false>(mode, a, tiles, s);
+    case 64: return z ? pick<64, true>(mode, a, tiles, s) : pick<64, false>(mode, a, tiles, s);
+    default: return z ? pick<128, true>(mode, a, tiles, s) : pick<128, false>(mode, a, tiles, s);
   }
 }
 

@@ -34,11 +34,11 @@ def compare(up, down, group, x, ids, g, what, outs=("f16", "f32")):
 @pytest.mark.parametrize("group", [32, 64, 128])
 @pytest.mark.parametrize("m,topk,count,hidden,inner,width", [
     (1, 1, 1, 1, 1, 1), (1, 8, 16, 3, 2, 130), (4, 8, 8, 5, 1, 33), (1, 2, 60, 2, 3, 65),     # slot by slot
-    (11, 3, 20, 3, 2, 100), (25, 8, 100, 1, 1, 16),                                            # tiles of 4 rows
-    (11, 3, 5, 3, 2, 100), (40, 2, 8, 2, 5, 47),                                               # of 16
-    (60, 2, 4, 3, 3, 129), (90, 1, 3, 5, 1, 20),                                               # of 32
+    (11, 3, 20, 3, 2, 100), (25, 8, 100, 1, 1, 16),                                            # tiles of 16 rows
+    (11, 3, 5, 3, 2, 100), (40, 2, 8, 2, 5, 47),
+    (60, 2, 7, 3, 3, 129), (50, 1, 3, 5, 1, 20),
     (150, 1, 2, 2, 1, 70), (130, 4, 4, 1, 3, 260),                                             # of 64
-    (330, 1, 2, 2, 1, 70), (100, 5, 3, 4, 3, 300),                                             # of 128
+    (900, 1, 2, 2, 1, 70), (170, 5, 2, 4, 3, 300),                                             # of 128
 ])
 def test_experts_match_oracle(m, topk, count, hidden, inner, width, group):
     say("experts", m, topk, count, hidden, inner, width, group)
@@ -48,7 +48,7 @@ def test_experts_match_oracle(m, topk, count, hidden, inner, width, group):
     compare(up, down, group, activations(rng, m, hidden * group), ids, g, "experts")
 
 
-@pytest.mark.parametrize("m,topk,count", [(3, 4, 4), (20, 2, 20), (30, 2, 8), (60, 2, 4), (150, 2, 4), (400, 2, 3)])
+@pytest.mark.parametrize("m,topk,count", [(3, 4, 4), (20, 2, 20), (30, 2, 8), (60, 2, 4), (150, 2, 4), (600, 2, 3)])
 def test_experts_skipped_repeated_and_lopsided(m, topk, count):
     """Ids outside the range, tokens with none, one expert for all, the same
     expert twice."""
@@ -69,7 +69,7 @@ def test_experts_skipped_repeated_and_lopsided(m, topk, count):
 def test_experts_bad_rows_stay_alone():
     import torch
     rng = np.random.default_rng(5)
-    for m, count in ((3, 4), (30, 20), (30, 8), (60, 4), (120, 2), (300, 2)):
+    for m, count in ((3, 4), (30, 20), (30, 8), (120, 2), (420, 2)):
         up, down = (upload(w) for w in layer(rng, count, 128, 64, 50, 64, False))
         x = activations(rng, m, 128)
         ids, g = slots(rng, m, 2, count)
@@ -83,7 +83,7 @@ def test_experts_bad_rows_stay_alone():
 def test_experts_write_their_output_alone():
     import torch
     rng = np.random.default_rng(6)
-    for m, count in ((2, 4), (30, 20), (30, 8), (60, 4), (120, 2), (300, 2)):
+    for m, count in ((2, 4), (30, 20), (30, 8), (120, 2), (420, 2)):
         up, down = (upload(w) for w in layer(rng, count, 64, 32, 33, 32, False))
         ids, g = slots(rng, m, 2, count)
         buf = torch.full((m + 2, 33), -7.0, dtype=torch.float16, device="cuda")
