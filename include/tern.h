@@ -387,8 +387,10 @@ tern_status tern_rotate_batched(int32_t count, const uint16_t *const *R, int32_t
  * `count` matrices of one shape may be stacked ([count][n][...] in every
  * array): a layer's experts.  group 32, 64 or 128 and k a multiple of it
  * (TERN_E_UNSUPPORTED otherwise); any n.  codes 16-byte aligned, scale
- * 2-byte; k at most 2^22.  The conventions above hold: x is FP16 [m][k], 16-byte aligned;
- * FP32 sums; y FP16 (nearest even) or FP32; n == 0 or m == 0 is a no-op,
+ * 2-byte.  k at most 2^22; a product whose grid would pass 2^32 threads is
+ * refused (TERN_E_UNSUPPORTED, nothing launched).  The conventions above
+ * hold: x is FP16 [m][k], 16-byte aligned; FP32 sums; y FP16 (nearest even)
+ * or FP32; y and the workspace overlap no input; n == 0 or m == 0 is a no-op,
  * k == 0 writes zeros; status codes, asynchronous, nothing kept between
  * calls, every call but tern_q4_pack may be captured into a HIP graph (as
  * long as its workspace stays its own).  A row of x that holds a NaN or an
@@ -414,7 +416,8 @@ tern_status tern_q4_unpack(const tern_q4 *src, uint8_t *q, void *stream);
  * row, bound by the reading of the codes, to prefill batches on tiles.  The
  * integers q - zero meet x on the matrix cores, a group's FP32 sum is then
  * scaled in FP32: the weights are not rounded, and scales of any size lose
- * neither range nor precision.  Results are bitwise reproducible.  ws:
+ * neither range nor precision.  Results are bitwise reproducible (the same
+ * call; another m may add in another order).  ws:
  * tern_q4_workspace_bytes(w, m) (K parts' FP32 partials; calls that overlap
  * in time must not share it). */
 size_t tern_q4_workspace_bytes(const tern_q4 *w, int32_t m);
@@ -463,8 +466,8 @@ tern_status tern_route(const void *logits, int32_t l_dtype, int32_t m, const ter
  * (a token without any gets zeros); a token may name an expert twice.  The
  * inner values silu(g) * u are held in FP16 (the down product's matrix
  * operand); every sum is FP32, a token's slots are added in slot order, and
- * results are bitwise reproducible.  count <= 1024, m * topk < 2^31
- * (TERN_E_UNSUPPORTED).  ws: tern_q4_experts_workspace_bytes bytes, 16-byte
+ * results are bitwise reproducible.  count <= 1024, topk <= 2^19, m * topk
+ * < 2^31 (TERN_E_UNSUPPORTED).  ws: tern_q4_experts_workspace_bytes bytes, 16-byte
  * aligned; calls that overlap in time must not share it.  ids and weights as
  * tern_route leaves them (device).  Async on stream. */
 size_t tern_q4_experts_workspace_bytes(const tern_q4 *gate_up, const tern_q4 *down, int32_t m, int32_t topk);

@@ -20,10 +20,12 @@ tern_status fail(tern_status s, const char* fmt, ...) {
   return tern::record_failure(s, msg);
 }
 
-#define Q4_HIP(call)                                                                       \
-  do {                                                                                     \
-    hipError_t e_ = (call);                                                                \
-    if (e_ != hipSuccess) return fail(TERN_E_HIP, "%s: %s", #call, hipGetErrorString(e_)); \
+// A launch that would need too large a grid is not made, and says so.
+#define Q4_HIP(call)                                                                                                   \
+  do {                                                                                                                 \
+    hipError_t e_ = (call);                                                                                            \
+    if (e_ == hipErrorInvalidConfiguration) return fail(TERN_E_UNSUPPORTED, "the product needs too many workgroups"); \
+    if (e_ != hipSuccess) return fail(TERN_E_HIP, "%s: %s", #call, hipGetErrorString(e_));                             \
   } while (0)
 
 #define Q4_TRY(expr)                  \
@@ -60,10 +62,41 @@ tern_status check_q4(const tern_q4* w) {
   return TERN_OK;
 }
 
+tern_status check_rows(int m) {
+  if (m < 0) return fail(TERN_E_INVAL, "m=%d must not be negative", m);
+  if (m > 0x7fffff00) return fail(TERN_E_UNSUPPORTED, "m=%d is too large", m);  // rounded up to a tile
+  return TERN_OK;
+}
+
 size_t words_of(const tern_q4* w) { return (size_t)w->count * (size_t)w->n * (size_t)(w->k / 8); }
 
-long long tiles_of(int m, int n, int tile) {  // tiles of 64 x 128 or 128 x 256
-  return (long long)((m + tile - 1) / tile) * ((n + 2 * tile - 1) / (2 * tile));
+int tile_cols(int tile) { return tile == tern::kQ4TileSmall ? 128 : 256; }
+
+long long tiles_of(int m, int n, int tile) {
+  return (long long)((m + tile - 1) / tile) * ((n + tile_cols(tile) - 1) / tile_cols(tile));
+}
+
+// The tile size of a plain product: the one whose busiest CU is done first,
+// where a tile costs its 32 x 32 blocks times the tenths below.  Every tile
+// decodes its own codes, so few rows make a block dear, dearest where a group
+// is short.  us, 64 / 96 / 128 rows: 512 x 12288 x 4096 59.7 / 74 / 59.5 (group
+// 32 with zero points 97 / - / 86), 400 x 12288 x 4096 57.8 / 51.0 / 60, 1024 x
+// 5120 x 2560 38.5 / 34.4 / -, 4096 x 2560 x 9728 (group 64) 303 / 274 / 327,
+// 2048 x 4096 x 4096 88 / - / 71.9, 512 x 4096 x 4096 29.7 / - / -.
+int pick_tile(int m, int n, int group) {
+  const int tile[] = {tern::kQ4TileSmall, tern::kQ4TileMid, tern::kQ4TileLarge};
+  const int tenths[] = {group < 128 ? 30 : 28, 23, 21};
+  int best = 0;
+  long long least = 0;
+  for (int i = 0; i < 3; ++i) {
+    const long long blocks = (long long)(tile[i] / 32) * (tile_cols(tile[i]) / 32);
+    const long long cost = (tiles_of(m, n, tile[i]) + 255) / 256 * blocks * tenths[i];
+    if (!best || cost < least) {
+      best = tile[i];
+      least = cost;
+    }
+  }
+  return best;
 }
 
 // The tile kernel holds a matrix's scales in one buffer below 2 GiB.
@@ -72,20 +105,19 @@ bool tile_scales_fit(int n, int k) { return (long long)n * (k / 32) * 2 < (1ll <
 // How a plain product runs.  Rows kernel: up to 160 activation rows, and up
 // to 320 where the tiles would not fill the card (us, rows against tiles: m =
 // 128, 4096 x 4096 13.5, 17.7; m = 256, 2560 x 9728 29.8, 30.2; m = 256, 12288
-// x 4096 41.6, 40.4).  Large tiles from one a CU (2048 x 4096 x 4096 74.4, 86.7
-// on small ones; 512 x 12288 x 4096 69.8, 61.5).  K parts where tiles are few:
-// some 512 workgroups, at least eight K steps each.
+// x 4096 41.6, 40.4).  K parts where tiles are few: some 512 workgroups, at
+// least eight K steps each.
 struct Route {
   bool rows;
   int tile, splits, tps;
 };
 
-Route route_of(int m, int n, int k) {
+Route route_of(int m, int n, int k, int group) {
   Route r = {};
   const int steps = (k + 127) / 128;
   const long long small = tiles_of(m, n, tern::kQ4TileSmall);
   r.rows = m <= 160 || (m <= 320 && small < 256) || !tile_scales_fit(n, k);
-  r.tile = tiles_of(m, n, tern::kQ4TileLarge) >= 256 ? tern::kQ4TileLarge : tern::kQ4TileSmall;
+  r.tile = pick_tile(m, n, group);
   r.splits = 1;
   if (!r.rows && small < 256) r.splits = std::max(1, (int)std::min<long long>(512 / std::max(small, 1ll), steps / 8));
   r.tps = std::max(1, (steps + r.splits - 1) / r.splits);
@@ -93,9 +125,9 @@ Route route_of(int m, int n, int k) {
   return r;
 }
 
-size_t plain_ws(int m, int n, int k) {
-  const Route r = route_of(m, n, k);
-  return !r.rows && r.splits > 1 ? (size_t)r.splits * m * n * 4 : 0;
+size_t plain_ws(int m, const tern_q4* w) {
+  const Route r = route_of(m, w->n, w->k, w->group);
+  return !r.rows && r.splits > 1 ? (size_t)r.splits * m * w->n * 4 : 0;
 }
 
 tern::Q4Args args_of(const tern_q4* w) {
@@ -115,6 +147,8 @@ tern::Q4Args args_of(const tern_q4* w) {
 // Few slots: every slot is a tile of its own and a token's down products are
 // summed in its own workgroup; nothing has to be sorted.
 constexpr int kDirectSlots = 32;
+// Slots of one round.
+constexpr int kRoundSlots = 1 << 19;
 
 struct ExpertsPlan {
   bool direct, tile;
@@ -127,13 +161,14 @@ ExpertsPlan plan_tokens(const tern_q4* up, const tern_q4* down, int m, int topk)
   const int experts = down->count, inner = down->k, n = down->n;
   const size_t slots = (size_t)m * topk;
   p.direct = slots <= (size_t)kDirectSlots;
-  // Tiles of 16 rows on the rows kernel (its tiles are a grid's y), of 64 or
-  // 128 on the tile kernel, by the rows an expert has on average.  us, 64
-  // experts of 2560 x 1024, up and down, 16 / 64 / 128: 8 rows an expert 47 +
-  // 19 / 53 + 25 / 76 + 49; 25 rows 77 + 35 / 62 + 33 / 83 + 51; 100 rows 204 +
-  // 104 / 109 + 57 / 129 + 76; 256 rows 470 + 239 / 231 + 123 / 236 + 139.
+  // Tiles of 16 rows on the rows kernel (its tiles are a grid's y) or of 64 on
+  // the tile kernel, by the rows an expert has on average.  us, 64 experts of
+  // 2560 x 1024, up and down, 16 / 64: 8 rows an expert 47 + 19 / 53 + 25; 25
+  // rows 76 + 35 / 66 + 30; 100 rows 198 + 99 / 110 + 57; 512 rows 875 + 468 /
+  // 421 + 237.  Tiles of 96 or 128 rows gain nothing: an expert's last tile is
+  // half empty (100 rows 121 + 72, 512 rows 412 + 237 with 128).
   const size_t mean = slots / experts;
-  p.rows = mean < 20 ? tern::kQ4TileRows : mean < 384 ? tern::kQ4TileSmall : tern::kQ4TileLarge;
+  p.rows = mean < 20 ? tern::kQ4TileRows : tern::kQ4TileSmall;
   if (!tile_scales_fit(up->n, up->k) || !tile_scales_fit(n, inner)) p.rows = tern::kQ4TileRows;
   p.tile = p.rows != tern::kQ4TileRows;
   p.max_tiles = (int)std::min<size_t>(slots, slots / p.rows + experts);
@@ -159,7 +194,7 @@ ExpertsPlan plan_tokens(const tern_q4* up, const tern_q4* down, int m, int topk)
 // below a grid's y, and the workspace does not grow with m without end.
 int round_tokens(const tern_q4* up, int m, int topk) {
   const long long by_x = up->k ? ((1ll << 31) - 1) / (2ll * up->k) : m;
-  return (int)std::max<long long>(1, std::min<long long>({(long long)m, by_x, (1ll << 19) / topk}));
+  return (int)std::max<long long>(1, std::min<long long>({(long long)m, by_x, (long long)kRoundSlots / topk}));
 }
 
 size_t experts_ws(const tern_q4* up, const tern_q4* down, int m, int topk) {
@@ -167,6 +202,15 @@ size_t experts_ws(const tern_q4* up, const tern_q4* down, int m, int topk) {
   const int most = round_tokens(up, m, topk);
   const size_t rest = m % most ? plan_tokens(up, down, m % most, topk).bytes : 0;
   return std::max(plan_tokens(up, down, most, topk).bytes, rest);
+}
+
+// Whether a round's grids can be launched (the kernels' widest workgroups on
+// the rows kernel).
+bool plan_fits(const tern_q4* down, const ExpertsPlan& p) {
+  auto fits = [&](long long width, int cols) {
+    return p.tile ? tern::grid_fits((width + cols - 1) / cols * p.max_tiles, 256) : tern::grid_fits((width + 15) / 16, 1024);
+  };
+  return fits(down->k, 64) && fits(down->n, 128);
 }
 
 tern_status check_experts(const tern_q4* up, const tern_q4* down, int m, int topk) {
@@ -179,6 +223,7 @@ tern_status check_experts(const tern_q4* up, const tern_q4* down, int m, int top
   if (up->n % 2 || up->n / 2 != down->k)
     return fail(TERN_E_INVAL, "gate/up has %d rows, down k=%d: twice as many are wanted", up->n, down->k);
   if (topk < 1) return fail(TERN_E_INVAL, "topk=%d must be positive", topk);
+  if (topk > kRoundSlots) return fail(TERN_E_UNSUPPORTED, "topk=%d: %d at most", topk, kRoundSlots);
   if ((long long)m * topk > 0x7fffffffll) return fail(TERN_E_UNSUPPORTED, "m=%d, topk=%d: too many slots", m, topk);
   return TERN_OK;
 }
@@ -190,8 +235,8 @@ extern "C" {
 tern_status tern_q4_check(const tern_q4* w) { return check_q4(w); }
 
 size_t tern_q4_workspace_bytes(const tern_q4* w, int32_t m) {
-  if (check_shape(w) != TERN_OK || m < 0) return 0;
-  return std::max<size_t>(256, plain_ws(m, w->n, w->k));
+  if (check_shape(w) != TERN_OK || check_rows(m) != TERN_OK) return 0;
+  return std::max<size_t>(256, plain_ws(m, w));
 }
 
 tern_status tern_q4_pack(const uint8_t* q, const tern_q4* dst, void* ws, size_t ws_bytes, void* stream) {
@@ -225,12 +270,12 @@ tern_status tern_q4_gemm(const tern_q4* w, const uint16_t* x, int32_t m, void* y
                          size_t ws_bytes, void* stream) {
   Q4_TRY(check_q4(w));
   if (w->count != 1) return fail(TERN_E_INVAL, "tern_q4_gemm takes one matrix (count=%d)", w->count);
-  if (m < 0) return fail(TERN_E_INVAL, "m=%d must not be negative", m);
+  Q4_TRY(check_rows(m));
   if (y_dtype != TERN_F16 && y_dtype != TERN_F32) return fail(TERN_E_UNSUPPORTED, "unknown output dtype %d", y_dtype);
   if (m == 0 || w->n == 0) return TERN_OK;
   Q4_TRY(check_ptr(x, w->k > 0, "x", 16));
   Q4_TRY(check_ptr(y, true, "y", y_dtype == TERN_F32 ? 4 : 2));
-  const size_t need = plain_ws(m, w->n, w->k);
+  const size_t need = plain_ws(m, w);
   if (need && (!ws || ws_bytes < need))
     return fail(TERN_E_WORKSPACE, "workspace of %zu bytes, %zu are needed", ws ? ws_bytes : (size_t)0, need);
   if (need) Q4_TRY(check_ptr(ws, true, "workspace", 16));
@@ -240,12 +285,11 @@ tern_status tern_q4_gemm(const tern_q4* w, const uint16_t* x, int32_t m, void* y
   a.m = m;
   a.y_f32 = y_dtype == TERN_F32;
   const hipStream_t s = (hipStream_t)stream;
-  const Route r = route_of(m, w->n, w->k);
+  const Route r = route_of(m, w->n, w->k, w->group);
   if (r.rows) {
     Q4_HIP(tern::launch_q4_rows(tern::kQ4Plain, w->group, a, 0, s));
     return TERN_OK;
   }
-  if (tiles_of(m, w->n, r.tile) * r.splits > 0x7ffffff0ll) return fail(TERN_E_UNSUPPORTED, "m=%d, n=%d: too many tiles", m, w->n);
   a.splits = r.splits;
   a.tps = r.tps;
   a.partial = (float*)ws;
@@ -278,8 +322,11 @@ tern_status tern_q4_experts(const tern_q4* gate_up, const tern_q4* down, const u
   uint8_t* base = (uint8_t*)ws;
   const hipStream_t s = (hipStream_t)stream;
   const int most = round_tokens(gate_up, m, topk), f32 = y_dtype == TERN_F32;
-  for (int t = 0; t < m; t += most) {
-    const int mt = std::min(most, m - t);
+  for (int mt : {most, m % most ? m % most : most})
+    if (!plan_fits(down, plan_tokens(gate_up, down, mt, topk)))
+      return fail(TERN_E_UNSUPPORTED, "m=%d, n=%d: the products need too many workgroups", m, down->n);
+  for (int t = 0, mt; t < m; t += mt) {
+    mt = std::min(most, m - t);
     const ExpertsPlan p = plan_tokens(gate_up, down, mt, topk);
     uint8_t* yt = (uint8_t*)y + (size_t)t * down->n * (f32 ? 4 : 2);
     tern::Q4Args u = args_of(gate_up), d = args_of(down);
@@ -304,7 +351,7 @@ tern_status tern_q4_experts(const tern_q4* gate_up, const tern_q4* down, const u
     Q4_HIP(tern::launch_q4_plan(u.ids, mt * topk, down->count, p.rows, (int4*)(base + p.tiles),
                                 (int32_t*)(base + p.ntiles), (int32_t*)(base + p.order), (int32_t*)(base + p.place), s));
     auto product = [&](int mode, int group, const tern::Q4Args& a) {
-      return p.tile ? tern::launch_q4_tile(mode, group, a, p.max_tiles, p.rows, s)
+      return p.tile ? tern::launch_q4_tile(mode, group, a, p.max_tiles, tern::kQ4TileSmall, s)
                     : tern::launch_q4_rows(mode, group, a, p.max_tiles, s);
     };
     if (down->k) Q4_HIP(product(tern::kQ4Up, gate_up->group, u));
@@ -339,11 +386,7 @@ tern_status tern_route(const void* logits, int32_t l_dtype, int32_t m, const ter
   Q4_TRY(check_ptr(ids, true, "ids", 4));
   Q4_TRY(check_ptr(weights, true, "weights", 4));
   tern::RouteArgs a = {};
-  a.logits = logits;
   a.bias = r->bias;
-  a.ids = ids;
-  a.weights = weights;
-  a.m = m;
   a.experts = r->experts;
   a.topk = r->topk;
   a.groups = r->groups;
@@ -352,7 +395,14 @@ tern_status tern_route(const void* logits, int32_t l_dtype, int32_t m, const ter
   a.renorm = r->renorm != 0;
   a.sigmoid = r->score == TERN_SCORE_SIGMOID;
   a.scale = r->scale;
-  Q4_HIP(tern::launch_route(a, l_dtype == TERN_F16, (hipStream_t)stream));
+  constexpr int most = 1 << 24;  // tokens of a launch
+  for (int t = 0; t < m; t += std::min(most, m - t)) {
+    a.m = std::min(most, m - t);
+    a.logits = (const uint8_t*)logits + (size_t)t * r->experts * (l_dtype == TERN_F32 ? 4 : 2);
+    a.ids = ids + (size_t)t * r->topk;
+    a.weights = weights + (size_t)t * r->topk;
+    Q4_HIP(tern::launch_route(a, l_dtype == TERN_F16, (hipStream_t)stream));
+  }
   return TERN_OK;
 }
 

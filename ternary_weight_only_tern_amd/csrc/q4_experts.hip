@@ -70,7 +70,7 @@ template <int V>
 __global__ __launch_bounds__(256) void q4_combine_kernel(const float* part, const int32_t* place, const float* gates,
                                                          int topk, int n, void* y, int y_f32) {
   const size_t first = (size_t)blockIdx.x * topk;
-  for (int c = (blockIdx.y * 256 + threadIdx.x) * V; c < n; c += gridDim.y * 256 * V) {
+  for (uint32_t c = (blockIdx.y * 256 + threadIdx.x) * V; c < (uint32_t)n; c += gridDim.y * 256 * V) {
     float sum[V] = {};
 #pragma unroll 4
     for (int j = 0; j < topk; ++j) {

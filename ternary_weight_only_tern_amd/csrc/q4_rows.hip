@@ -311,8 +311,10 @@ hipError_t launch(const Q4Args& a, int tiles, hipStream_t s) {
   while (scale_bytes(ct * SG, panels, Z) > most && ct > 1) ct = (ct + 1) / 2;
   const size_t bytes = staging + scale_bytes(ct * SG, panels, Z);
   if (bytes > kLdsMost) return hipErrorInvalidValue;
-  const unsigned panels_x = (unsigned)((width + cols - 1) / cols);
-  const dim3 grid = MODE == kQ4Plain ? dim3((panels_x + 7) / 8 * 8 * (unsigned)((a.m + XR - 1) / XR)) : dim3(panels_x, (unsigned)tiles);
+  long long blocks = (width + cols - 1) / cols;
+  if (MODE == kQ4Plain) blocks = (blocks + 7) / 8 * 8 * ((a.m + XR - 1) / XR);
+  if (!grid_fits(blocks, W * 64)) return hipErrorInvalidConfiguration;
+  const dim3 grid((unsigned)blocks, MODE == kQ4Plain ? 1u : (unsigned)tiles);
   hipLaunchKernelGGL((q4_rows_kernel<G, Z, XR, NB, W, MODE>), grid, dim3(W * 64), bytes, s, a, ct);
   return hipGetLastError();
 }
@@ -332,12 +334,14 @@ hipError_t pick(int mode, const Q4Args& a, int tiles, hipStream_t s) {
     return launch<G, Z, 16, 2, 2, kQ4Down>(a, tiles, s);
   }
   // Wavefronts a panel: 4 where there are panels enough to fill the card, 16
-  // where few panels have long rows.  us at W = 4, 8, 16 (m = 1, group 128):
-  // 12288 x 4096 6.5, 6.8, -; 131072 x 2560 36.7, 43, -; 4096 x 4096 4.3, 3.6,
-  // 3.9; 2560 x 9728 9.5, 6.2, 5.1; at W = 4, 8 (m = 16): 12288 x 4096 8.4,
-  // 9.4; 4096 x 12288 13.8, 9.7.
+  // where few panels have long rows; two panels at a time where there are
+  // thousands.  us at W = 4, 8, 16 (m = 1, group 128): 12288 x 4096 6.9, 7.0,
+  // 8.5; 4096 x 4096 4.3, 3.7, 4.2; 2560 x 9728 9.8, 6.6, 5.6; 131072 x 2560
+  // 38.9, 51.6, 95.9, with two panels at W = 4 34.9; at W = 4, 8 (m = 16):
+  // 12288 x 4096 8.4, 9.5; 4096 x 12288 13.7, 9.6.
   const int panels = (a.n + 15) / 16, T = (a.k + 127) / 128;
   if (a.m <= 4) {
+    if (panels >= 2048) return launch<G, Z, 4, 2, 4, kQ4Plain>(a, tiles, s);
     if (panels >= 512) return launch<G, Z, 4, 1, 4, kQ4Plain>(a, tiles, s);
     if (panels < 256 && T >= 64) return launch<G, Z, 4, 1, 16, kQ4Plain>(a, tiles, s);
     return launch<G, Z, 4, 1, 8, kQ4Plain>(a, tiles, s);

@@ -290,14 +290,17 @@ hipError_t launch(const Q4Args& a, int tiles, hipStream_t s) {
   const long long tn = (width + cols - 1) / cols;
   const long long tm = MODE == kQ4Plain ? (long long)((a.m + BM - 1) / BM) * a.splits : tiles;
   const long long grid = (tn * tm + kXcds - 1) / kXcds * kXcds;
-  if (grid > 0x7fffffffll) return hipErrorInvalidValue;
+  if (!grid_fits(grid, WM * WN * 64)) return hipErrorInvalidConfiguration;
   hipLaunchKernelGGL((q4_tile_kernel<G, Z, MODE, WM, WN, MW, NW>), dim3((unsigned)grid), dim3(WM * WN * 64), 0, s, a);
   return hipGetLastError();
 }
 
 template <int G, bool Z, int MODE>
 hipError_t pick(const Q4Args& a, int tiles, int rows, hipStream_t s) {
-  if (rows == kQ4TileLarge) return launch<G, Z, MODE, 2, 4, 2, 2>(a, tiles, s);
+  if constexpr (MODE == kQ4Plain) {
+    if (rows == kQ4TileLarge) return launch<G, Z, MODE, 1, 8, 4, 1>(a, tiles, s);
+    if (rows == kQ4TileMid) return launch<G, Z, MODE, 1, 8, 3, 1>(a, tiles, s);
+  }
   return launch<G, Z, MODE, 1, 4, 2, 1>(a, tiles, s);
 }
 

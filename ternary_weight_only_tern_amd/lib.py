@@ -467,6 +467,11 @@ def _scratch(nbytes, device, stream):
     return _fresh(max(nbytes, 256), torch.uint8, device, stream)
 
 
+def _count(v):
+    """A size that the C interface's 32 bits hold."""
+    return v if v < 2 ** 31 else _refuse(f"a size of {v} is too large")
+
+
 class Q4Matrix:
     """4-bit weights on the device: codes uint8 [n][k/2] in tern_q4's word
     order, scale fp16 [n][k/group], zero uint8 [n][k/group] or None (8
@@ -486,7 +491,7 @@ class Q4Matrix:
         _use_torch()
         self.codes, self.scale, self.zero = codes, scale, zero
         self.device = codes.device
-        self.n, self.k = codes.shape[-2], 2 * codes.shape[-1]
+        self.n, self.k = _count(codes.shape[-2]), _count(2 * codes.shape[-1])
         self.count = codes.shape[0] if codes.dim() == 3 else 1
         ng = scale.shape[-1]
         if self.k and (ng < 1 or self.k % ng):
@@ -549,7 +554,7 @@ def tern_q4_gemm(w: Q4Matrix, x, y_dtype=TERN_F16, out=None, stream=None, ws=Non
     _tensor(x, "x", (_torch.float16,), device)
     if x.dim() != 2 or x.size(1) != w.k:
         _refuse(f"x has shape {tuple(x.shape)}, not [m][{w.k}]")
-    m = x.size(0)
+    m = _count(x.size(0))
     kind = _y_type(y_dtype)
     if out is None:
         out = _fresh((m, w.n), kind, device, stream)
@@ -557,6 +562,8 @@ def tern_q4_gemm(w: Q4Matrix, x, y_dtype=TERN_F16, out=None, stream=None, ws=Non
         _tensor(out, "out", (kind,), device, (m, w.n))
     if ws is None:
         ws = _scratch(load().tern_q4_workspace_bytes(w._at, m), device, stream)
+    elif ws.device != device or not ws.is_contiguous():
+        _refuse(f"a workspace on {ws.device}, or with gaps; contiguous on {device} is wanted")
     check(load().tern_q4_gemm(w._at, x.data_ptr(), m, out.data_ptr(), y_dtype, ws.data_ptr(), ws.nbytes,
                               _stream_of(device, stream)))
     return out
@@ -575,7 +582,7 @@ def tern_route(logits, topk, score=TERN_SCORE_SOFTMAX, bias=None, groups=1, grou
             return tern_route(logits, topk, score, bias, groups, group_best, keep_groups, renorm, scale, ids, weights,
                               stream)
     _tensor(logits, "logits", (torch.float16, torch.float32), device)
-    m, experts = logits.shape
+    m, experts = _count(logits.size(0)), _count(logits.size(1))
     if bias is not None:
         _tensor(bias, "bias", (torch.float32,), device, (experts,))
     if ids is None:
@@ -610,12 +617,12 @@ def tern_q4_experts(gate_up: Q4Matrix, down: Q4Matrix, x, ids, weights, y_dtype=
         _refuse(f"down is on {down.device}, not {device}")
     if x.dim() != 2 or x.size(1) != gate_up.k:
         _refuse(f"x has shape {tuple(x.shape)}, not [m][{gate_up.k}]")
-    m = x.size(0)
+    m = _count(x.size(0))
     _tensor(ids, "ids", (torch.int32,), device)
     if ids.dim() != 2 or ids.size(0) != m:
         _refuse(f"ids have shape {tuple(ids.shape)}, not [{m}][topk]")
     _tensor(weights, "weights", (torch.float32,), device, ids.shape)
-    topk = ids.size(1)
+    topk = _count(ids.size(1))
     kind = _y_type(y_dtype)
     if out is None:
         out = _fresh((m, down.n), kind, device, stream)
@@ -623,6 +630,8 @@ def tern_q4_experts(gate_up: Q4Matrix, down: Q4Matrix, x, ids, weights, y_dtype=
         _tensor(out, "out", (kind,), device, (m, down.n))
     if ws is None:
         ws = _scratch(load().tern_q4_experts_workspace_bytes(gate_up._at, down._at, m, topk), device, stream)
+    elif ws.device != device or not ws.is_contiguous():
+        _refuse(f"a workspace on {ws.device}, or with gaps; contiguous on {device} is wanted")
     check(load().tern_q4_experts(gate_up._at, down._at, x.data_ptr(), m, ids.data_ptr(), weights.data_ptr(), topk,
                                  out.data_ptr(), y_dtype, ws.data_ptr(), ws.nbytes, _stream_of(device, stream)))
     return out

@@ -37,6 +37,31 @@ def test_gemm_matches_oracle(m, n, kg, group):
         assert (got == again).all(), "two runs differ"
 
 
+@pytest.mark.parametrize("m,n,k,group,zero", [
+    (1, 40, 20512, 32, True), (3, 9000, 2560, 32, True), (4, 32773, 64, 64, False), (2, 33000, 1280, 32, True),
+    (12, 40, 20512, 32, True), (20, 40, 20512, 32, True), (160, 1640, 10240, 32, True), (33, 70, 33024, 128, False)])
+def test_gemm_long_rows_and_many_panels(m, n, k, group, zero):
+    """Rows whose scales are staged in parts, and as many panels as change
+    the kernel's shape."""
+    say("q4 gemm", m, n, k, group)
+    rng = np.random.default_rng(n + k)
+    w = weights(rng, (), n, k, group, zero)
+    x = activations(rng, m, k)
+    y, _, err = Q.gemm(*w, group, x)
+    check(L.tern_q4_gemm(upload(w), half(x), L.TERN_F32), y, err, "f32", f"{m}x{n}x{k} group {group}")
+
+
+@pytest.mark.parametrize("m,n", [(700, 9728), (1500, 4096), (900, 5120), (512, 12300)])
+def test_gemm_tile_sizes(m, n):
+    """Each output tile of the tile kernel, by the sizes that choose it."""
+    say("q4 gemm", m, n)
+    rng = np.random.default_rng(m)
+    w = weights(rng, (), n, 192, 64, True)
+    x = activations(rng, m, 192)
+    y, _, err = Q.gemm(*w, 64, x)
+    check(L.tern_q4_gemm(upload(w), half(x), L.TERN_F32), y, err, "f32", f"{m}x{n}")
+
+
 @pytest.mark.parametrize("m", [1, 20, 400])
 def test_gemm_scales_and_zero_points_of_any_size(m):
     """Scales from subnormal to 60000 and zero points up to 255: FP32 outputs
@@ -167,6 +192,9 @@ def test_gemm_refusals_of_tensors():
             L.tern_q4_gemm(w, bad)
     with pytest.raises(ValueError):
         L.tern_q4_gemm(w, x, out=torch.empty((2, 8), **dev))
+    for ws in (torch.empty(1024, dtype=torch.uint8), torch.empty(2048, dtype=torch.uint8, **dev)[::2]):
+        with pytest.raises(ValueError):
+            L.tern_q4_gemm(w, x, ws=ws)
     with pytest.raises(ValueError):
         L.tern_q4_gemm(w, x, 7)
     with pytest.raises(L.TernError) as e:

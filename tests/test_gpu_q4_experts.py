@@ -1,5 +1,5 @@
 """tern_q4_experts on the GPU against the oracle, on each of its routes (slot
-by slot, 16-row tiles, 128-row tiles), and with tern_route before it."""
+by slot, tiles of 16 rows and of 64), and with tern_route before it."""
 import numpy as np
 import pytest
 
@@ -38,7 +38,7 @@ def compare(up, down, group, x, ids, g, what, outs=("f16", "f32")):
     (11, 3, 5, 3, 2, 100), (40, 2, 8, 2, 5, 47),
     (60, 2, 7, 3, 3, 129), (50, 1, 3, 5, 1, 20),
     (150, 1, 2, 2, 1, 70), (130, 4, 4, 1, 3, 260),                                             # of 64
-    (900, 1, 2, 2, 1, 70), (170, 5, 2, 4, 3, 300),                                             # of 128
+    (900, 1, 2, 2, 1, 70), (170, 5, 2, 4, 3, 300),                                             # several an expert
 ])
 def test_experts_match_oracle(m, topk, count, hidden, inner, width, group):
     say("experts", m, topk, count, hidden, inner, width, group)
@@ -46,6 +46,48 @@ def test_experts_match_oracle(m, topk, count, hidden, inner, width, group):
     up, down = layer(rng, count, hidden * group, inner * group, width, group, zero=m % 2 == 0)
     ids, g = slots(rng, m, topk, count)
     compare(up, down, group, activations(rng, m, hidden * group), ids, g, "experts")
+
+
+@pytest.mark.parametrize("m,topk,count,hidden,inner,width", [
+    (1, 32, 8, 64, 384, 20), (2, 16, 8, 10240, 1024, 17), (1, 1, 1, 20480, 32, 5),              # slot by slot
+    (30, 2, 20, 10240, 64, 18), (30, 2, 20, 64, 8192, 18), (70, 1, 64, 32, 10240, 40)])         # tiles of 16 rows
+def test_experts_long_rows(m, topk, count, hidden, inner, width):
+    """Rows whose scales are staged in parts."""
+    say("experts", m, topk, count, hidden, inner, width)
+    rng = np.random.default_rng(hidden + inner)
+    up, down = layer(rng, count, hidden, inner, width, 32, True)
+    ids, g = slots(rng, m, topk, count)
+    # small activations: the inner values stay in FP16's range
+    x = (activations(rng, m, hidden).astype(np.float64) / 64).astype(np.float16)
+    compare(up, down, 32, x, ids, g, "long rows", outs=("f32",))
+
+
+def test_experts_of_more_slots_than_a_round():
+    """Tokens in several rounds: the same rows as calls on parts of them, and
+    the oracle's at the rounds' ends."""
+    import torch
+    rng = np.random.default_rng(11)
+    m, topk, count = (1 << 19) + 1000, 2, 3
+    up, down = layer(rng, count, 32, 32, 8, 32, False)
+    u, d = upload(up), upload(down)
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    x = torch.randn((m, 32), device="cuda", generator=gen).half()
+    ids = torch.randint(-1, count, (m, topk), device="cuda", generator=gen, dtype=torch.int32)
+    g = torch.rand((m, topk), device="cuda", generator=gen)
+    got = L.tern_q4_experts(u, d, x, ids, g, L.TERN_F32)
+    edge = 1 << 18
+    for a, b in ((0, 40), (edge - 300, edge + 300), (2 * edge - 5, 2 * edge + 11), (m - 1000, m)):
+        part = L.tern_q4_experts(u, d, x[a:b], ids[a:b].contiguous(), g[a:b].contiguous(), L.TERN_F32)
+        if (b - a) * topk > 32:
+            assert torch.equal(got[a:b], part)
+        else:  # slot by slot: gates go into the FP32 sums, in another order than on tiles, so both meet the oracle
+            y, err = Q.experts(up, down, 32, x[a:b].cpu().numpy(), ids[a:b].cpu().numpy(), g[a:b].cpu().numpy())
+            check(got[a:b], y, err, "f32", "tiles")
+            check(part, y, err, "f32", "slot by slot")
+    for a in (0, edge - 8, 2 * edge - 8, m - 16):
+        part = slice(a, a + 16)
+        y, err = Q.experts(up, down, 32, x[part].cpu().numpy(), ids[part].cpu().numpy(), g[part].cpu().numpy())
+        check(got[part], y, err, "f32", f"tokens from {a}")
 
 
 @pytest.mark.parametrize("m,topk,count", [(3, 4, 4), (20, 2, 20), (30, 2, 8), (60, 2, 4), (150, 2, 4), (600, 2, 3)])
@@ -169,7 +211,7 @@ def test_experts_refusals_of_tensors():
     ids, g = (to_dev(a) for a in slots(rng, 3, 2, 4))
     call = lambda **kw: L.tern_q4_experts(**{**dict(gate_up=up, down=down, x=x, ids=ids, weights=g), **kw})
     for kw in (dict(x=x[:, :32]), dict(x=x[:2]), dict(ids=ids.long()), dict(ids=ids.t().contiguous()), dict(ids=ids.cpu()),
-               dict(weights=g[:, :1]), dict(weights=g.half()), dict(out=torch.empty((3, 33), device="cuda"))):
+               dict(weights=g[:, :1]), dict(weights=g.half()), dict(ws=torch.empty(1 << 20, dtype=torch.uint8)), dict(out=torch.empty((3, 33), device="cuda"))):
         with pytest.raises(ValueError):
             call(**kw)
     for kw in (dict(down=up), dict(ws=torch.empty(16, dtype=torch.uint8, device="cuda"))):

@@ -99,6 +99,14 @@ def test_route_near_ties(experts, groups, topk):
         run((1e-30 * l).astype(np.float32), topk, score)
 
 
+def test_route_of_more_tokens_than_a_launch():
+    import torch
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    l = torch.randn(((1 << 24) + 777, 2), device="cuda", generator=gen).half()
+    ids, w = L.tern_route(l, 1, scale=0.5)
+    assert torch.equal(ids[:, 0], (l[:, 1] > l[:, 0]).int()) and (w == 0.5).all()
+
+
 def test_route_captured():
     import torch
     l = torch.randn((33, 64), device="cuda")

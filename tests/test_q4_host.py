@@ -60,7 +60,8 @@ def test_pack_refusals():
     assert lib.tern_q4_pack(0x1004, at(d), 0x1000, 256, None) == L.TERN_E_ALIGN
     assert lib.tern_q4_pack(0x1000, at(d), None, 0, None) == L.TERN_E_WORKSPACE
     assert lib.tern_q4_unpack(at(d), None, None) == L.TERN_E_INVAL
-    assert lib.tern_q4_unpack(at(q4(n=0)), None, None) == L.TERN_OK
+    empty = q4(n=0)
+    assert lib.tern_q4_unpack(at(empty), None, None) == L.TERN_OK
 
 
 ROUTER = dict(experts=64, topk=8, score=1, groups=8, group_best=2, keep_groups=4, renorm=1, scale=1.0, bias=None)
@@ -101,9 +102,36 @@ def test_experts_refusals():
     assert f(up=q4(n=130, k=256, count=4)) == L.TERN_E_INVAL and f(up=q4(n=129, k=256, count=4)) == L.TERN_E_INVAL
     assert f(up=q4(n=128, count=0), down=q4(k=64, count=0)) == L.TERN_E_INVAL
     assert f(up=q4(n=128, count=2000), down=q4(k=64, count=2000)) == L.TERN_E_UNSUPPORTED
-    assert f(m=1 << 30, topk=2) == L.TERN_E_UNSUPPORTED
+    assert f(m=1 << 30, topk=2) == L.TERN_E_UNSUPPORTED and f(m=1, topk=(1 << 19) + 1) == L.TERN_E_UNSUPPORTED
     for kw in (dict(x=None), dict(ids=None), dict(w=None), dict(y=None)):
         assert f(**kw) == L.TERN_E_INVAL
     assert f(x=0x1008) == L.TERN_E_ALIGN and f(ids=0x2002) == L.TERN_E_ALIGN and f(ws=0x5008) == L.TERN_E_ALIGN
     assert f(dt=9) == L.TERN_E_UNSUPPORTED and f(nb=need - 1) == L.TERN_E_WORKSPACE and f(ws=None) == L.TERN_E_WORKSPACE
     assert f(m=0, x=None, ids=None, w=None, y=None, ws=None, nb=0) == L.TERN_OK
+
+
+def test_grids_past_32_bits_are_refused():
+    """Sizes whose product would need more threads than a launch counts are
+    refused before anything is launched."""
+    lib = L.load()
+
+    def g(m, n, k):
+        d = q4(n=n, k=k)
+        return lib.tern_q4_gemm(at(d), 0x1000, m, 0x2000, 0, 0x3000, 1 << 62, None)
+
+    assert g(0x7fffffff, 16, 64) == L.TERN_E_UNSUPPORTED and b"too large" in lib.tern_last_error()
+    for m, n, k in ((0x7fffff00, 16, 64), (1 << 20, 1 << 20, 64), (1, 0x7fffff00, 64), (40, 1 << 28, 256)):
+        assert g(m, n, k) == L.TERN_E_UNSUPPORTED and b"too many workgroups" in lib.tern_last_error(), (m, n, k)
+
+    def e(m, n, count):
+        up, down = q4(n=64, k=64, group=32, count=count), q4(n=n, k=32, group=32, count=count)
+        return lib.tern_q4_experts(at(up), at(down), 0x1000, m, 0x2000, 0x3000, 1, 0x4000, 0, 0x5000, 1 << 62, None)
+
+    assert e(1 << 15, 1 << 22, 1024) == L.TERN_E_UNSUPPORTED and b"too many workgroups" in lib.tern_last_error()
+    assert e(1, 1 << 27, 8) == L.TERN_E_UNSUPPORTED
+
+
+def test_sizes_past_32_bits_are_refused():
+    assert L._count(2 ** 31 - 1) == 2 ** 31 - 1
+    with pytest.raises(ValueError):
+        L._count(2 ** 31)
