@@ -16,40 +16,43 @@ constexpr int kPlanThreads = 1024, kBatch = 8;  // kBatch ids requested before a
 __global__ __launch_bounds__(kPlanThreads) void q4_plan_kernel(const int32_t* ids, int slots, int experts, int rows,
                                                                int4* tiles, int32_t* ntiles, int32_t* order,
                                                                int32_t* place) {
-  __shared__ int count[kPlanThreads], first[kPlanThreads], tile0[kPlanThreads];
-  const int t = threadIdx.x;
+  __shared__ int count[kPlanThreads], wave_rows[kPlanThreads / 64], wave_tiles[kPlanThreads / 64];
+  const int t = threadIdx.x, lane = t & 63, wave = t >> 6;
+  int e[kBatch];  // the batch at hand; the last one counted is kept
+  int s0 = t;
+  auto fetch = [&](int from) {
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) e[i] = from + i * kPlanThreads < slots ? ids[from + i * kPlanThreads] : -1;
+  };
+  fetch(s0);
   count[t] = 0;
   __syncthreads();
-  for (int s0 = t; s0 < slots; s0 += kPlanThreads * kBatch) {
-    int e[kBatch];
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i) e[i] = s0 + i * kPlanThreads < slots ? ids[s0 + i * kPlanThreads] : -1;
+  while (true) {
 #pragma unroll
     for (int i = 0; i < kBatch; ++i)
       if ((unsigned)e[i] < (unsigned)experts) atomicAdd(&count[e[i]], 1);
+    if (s0 + kPlanThreads * kBatch >= slots) break;
+    fetch(s0 += kPlanThreads * kBatch);
   }
   __syncthreads();
+  // running sums over the experts: inside a wavefront, then over wavefronts
   const int mine = count[t], tl = (mine + rows - 1) / rows;
-  first[t] = mine;
-  tile0[t] = tl;
-  __syncthreads();
-  for (int d = 1; d < kPlanThreads; d <<= 1) {
-    const int a = t >= d ? first[t - d] : 0, b = t >= d ? tile0[t - d] : 0;
-    __syncthreads();
-    first[t] += a;
-    tile0[t] += b;
-    __syncthreads();
+  int f = mine, q = tl;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int a = __shfl_up(f, d), b = __shfl_up(q, d);
+    if (lane >= d) f += a, q += b;
   }
-  const int f = first[t] - mine, q = tile0[t] - tl;
-  if (t == kPlanThreads - 1) *ntiles = tile0[t];
+  if (lane == 63) wave_rows[wave] = f, wave_tiles[wave] = q;
   __syncthreads();
+  for (int w = 0; w < wave; ++w) f += wave_rows[w], q += wave_tiles[w];
+  if (t == kPlanThreads - 1) *ntiles = q;
+  f -= mine;
+  q -= tl;
   count[t] = f;
   for (int i = 0; i < tl; ++i) tiles[q + i] = make_int4(t, f + i * rows, min(rows, mine - i * rows), 0);
   __syncthreads();
-  for (int s0 = t; s0 < slots; s0 += kPlanThreads * kBatch) {
-    int e[kBatch];
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i) e[i] = s0 + i * kPlanThreads < slots ? ids[s0 + i * kPlanThreads] : -1;
+  for (;; fetch(s0 -= kPlanThreads * kBatch)) {
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
       const int s = s0 + i * kPlanThreads;
@@ -60,6 +63,7 @@ __global__ __launch_bounds__(kPlanThreads) void q4_plan_kernel(const int32_t* id
       }
       if (s < slots) place[s] = p;
     }
+    if (s0 < kPlanThreads * kBatch) break;
   }
 }
 

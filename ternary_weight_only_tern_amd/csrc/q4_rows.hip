@@ -29,7 +29,7 @@ __host__ __device__ constexpr int zero_pitch(int groups) { return (groups + 7) /
 constexpr size_t scale_bytes(int groups, int panels, bool z) {
   return (size_t)panels * 16 * (scale_pitch(groups) * 2 + (z ? zero_pitch(groups) : 0)) + 16;
 }
-constexpr size_t kLdsMost = 64 * 1024, kScaleMost = 20 * 1024;
+constexpr size_t kLdsMost = 80 * 1024, kScaleMost = 32 * 1024;  // two workgroups a CU
 
 // XR: rows of x at most (4, 16 or 32).  ct: K tiles whose scales are staged
 // at a time (all of them unless K is very long).
@@ -315,6 +315,11 @@ hipError_t launch(const Q4Args& a, int tiles, hipStream_t s) {
   if (MODE == kQ4Plain) blocks = (blocks + 7) / 8 * 8 * ((a.m + XR - 1) / XR);
   if (!grid_fits(blocks, W * 64)) return hipErrorInvalidConfiguration;
   const dim3 grid((unsigned)blocks, MODE == kQ4Plain ? 1u : (unsigned)tiles);
+  if (bytes > 64 * 1024) {
+    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(q4_rows_kernel<G, Z, XR, NB, W, MODE>),
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, (int)kLdsMost);
+    if (e != hipSuccess) return e;
+  }
   hipLaunchKernelGGL((q4_rows_kernel<G, Z, XR, NB, W, MODE>), grid, dim3(W * 64), bytes, s, a, ct);
   return hipGetLastError();
 }
@@ -350,12 +355,15 @@ hipError_t pick(int mode, const Q4Args& a, int tiles, hipStream_t s) {
     if (panels >= 512) return launch<G, Z, 16, 1, 4, kQ4Plain>(a, tiles, s);
     return launch<G, Z, 16, 1, 8, kQ4Plain>(a, tiles, s);
   }
-  // Chunks of 32 rows, 9 KiB of staging a wavefront; two panels share them
-  // where panels abound.  us with one panel (W = 6), two (W = 4): m = 24, 4096
-  // x 4096 6.3, 7.9; m = 64, 12288 x 4096 23.4, 17.0; m = 77, 2560 x 9728 at
-  // group 32 18.2, 23.7; m = 128, 4096 x 4096 at group 64 19, 13.5.
-  if ((long long)panels * ((a.m + 31) / 32) >= 512) return launch<G, Z, 32, 2, 4, kQ4Plain>(a, tiles, s);
-  return launch<G, Z, 32, 1, 6, kQ4Plain>(a, tiles, s);
+  // Chunks of 32 rows decode the codes least often, chunks of 16 give more
+  // wavefronts.  us at 32 rows with two panels (W = 4), one (W = 6), at 16 rows
+  // with two (W = 8): m = 24, 2560 x 9728 at group 32 22.6, 11.1, 11.8; m = 48
+  // 23.4, 18.1, 12.3; m = 77 24.9, 20.1, 18.0; m = 100, 2560 x 2560 8.0, 9.5,
+  // 7.4; m = 64, 12288 x 4096 16.8, 28, 19.0; m = 128, 4096 x 4096 at group 64
+  // 14.8, 23.5, 17.1.
+  if ((long long)panels * ((a.m + 31) / 32) >= 768) return launch<G, Z, 32, 2, 4, kQ4Plain>(a, tiles, s);
+  if (a.m <= 32) return launch<G, Z, 32, 1, 6, kQ4Plain>(a, tiles, s);
+  return launch<G, Z, 16, 2, 8, kQ4Plain>(a, tiles, s);
 }
 
 }  // namespace
