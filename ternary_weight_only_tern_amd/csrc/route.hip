@@ -17,8 +17,9 @@
 // order; groups in doubt are told apart by their FP64 sums.  A token that
 // finds no such gap, or a softmax with a bias and a doubt, is routed again by
 // exact_row, 64 lanes and FP64 keys for every expert.
-// 16384 tokens, 256 experts, sigmoid, bias, 4 of 8 groups, top 8: bound by
-// the vector instructions, some 300 a token.
+// 16384 tokens, 256 experts, sigmoid, bias, 4 of 8 groups, top 8: 15.0 us,
+// bound by the vector instructions (37 tokens of it 6.3 us, one token of 64
+// experts 2.9 us: latency).
 #include "q4.h"
 
 namespace tern {
