@@ -102,10 +102,12 @@ int pick_tile(int m, int n, int group) {
 // The tile kernel holds a matrix's scales in one buffer below 2 GiB.
 bool tile_scales_fit(int n, int k) { return (long long)n * (k / 32) * 2 < (1ll << 31); }
 
-// How a plain product runs.  Rows kernel: up to 160 activation rows, and up
-// to 320 where the tiles would not fill the card (us, rows against tiles: m =
-// 128, 4096 x 4096 13.5, 17.7; m = 256, 2560 x 9728 29.8, 30.2; m = 256, 12288
-// x 4096 41.6, 40.4).  K parts where tiles are few: some 512 workgroups, at
+// How a plain product runs.  Rows kernel: up to 24 activation rows, up to 160
+// unless tiles abound, and up to 320 where tiles would not fill the card (us,
+// rows against tiles: m = 24, 131072 x 2560 57, 61; m = 64 94, 66; m = 64,
+// 32768 x 2560 22.8, 21.9; m = 128, 12288 x 4096 23.6, 27.6; m = 160, 19456 x
+// 2560 29.8, 28.4; m = 128, 4096 x 4096 13.9, 17.7; m = 256, 2560 x 9728 29.8,
+// 30.2; m = 256, 12288 x 4096 41.6, 40.4).  K parts where tiles are few: some 512 workgroups, at
 // least eight K steps each.
 struct Route {
   bool rows;
@@ -116,7 +118,7 @@ Route route_of(int m, int n, int k, int group) {
   Route r = {};
   const int steps = (k + 127) / 128;
   const long long small = tiles_of(m, n, tern::kQ4TileSmall);
-  r.rows = m <= 160 || (m <= 320 && small < 256) || !tile_scales_fit(n, k);
+  r.rows = m <= 24 || (m <= 160 && small < 384) || (m <= 320 && small < 256) || !tile_scales_fit(n, k);
   r.tile = pick_tile(m, n, group);
   r.splits = 1;
   if (!r.rows && small < 256) r.splits = std::max(1, (int)std::min<long long>(512 / std::max(small, 1ll), steps / 8));

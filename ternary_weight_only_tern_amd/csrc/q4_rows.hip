@@ -21,7 +21,7 @@
 // the plain read 2.5 us).  From some ten rows on the waits of each wavefront's
 // K tiles for the next, and then the decoding, repeated for every 16 or 32
 // rows, bound it (13 x 12288 x 4096, group 64, zero points 8.8 us, 3.1 TB/s; 77
-// x 2560 x 9728, group 32 17.4 us).
+// x 2560 x 9728, group 32 16.3 us).
 #include "q4_rows.h"
 
 namespace tern {
@@ -35,7 +35,7 @@ __host__ __device__ constexpr int zero_pitch(int groups) { return (groups + 7) /
 constexpr size_t scale_bytes(int groups, int panels, bool z) {
   return (size_t)panels * 16 * (scale_pitch(groups) * 2 + (z ? zero_pitch(groups) : 0)) + 16;
 }
-constexpr size_t kLdsMost = 80 * 1024, kScaleMost = 32 * 1024;  // two workgroups a CU
+constexpr size_t kLdsMost = 100 * 1024, kScaleMost = 32 * 1024;
 
 // XR: rows of x at most (4, 16 or 32).  ct: K tiles whose scales are staged
 // at a time (all of them unless K is very long).
@@ -344,11 +344,12 @@ hipError_t pick(int mode, const Q4Args& a, int tiles, hipStream_t s) {
     return launch<G, Z, 16, 2, 2, kQ4Down>(a, tiles, s);
   }
   // Wavefronts a panel: 4 where there are panels enough to fill the card, 16
-  // where few panels have long rows; two panels at a time where there are
-  // thousands.  us at W = 4, 8, 16 (m = 1, group 128): 12288 x 4096 6.9, 7.0,
+  // where few panels have long rows; two or four panels at a time where there
+  // are thousands.  us at W = 4, 8, 16 (m = 1, group 128): 12288 x 4096 6.9, 7.0,
   // 8.5; 4096 x 4096 4.3, 3.7, 4.2; 2560 x 9728 9.8, 6.6, 5.6; 131072 x 2560
   // 38.9, 51.6, 95.9, with two panels at W = 4 34.9; at W = 4, 8 (m = 16):
-  // 12288 x 4096 8.4, 9.5; 4096 x 12288 13.7, 9.6.
+  // 12288 x 4096 8.4, 9.5; 4096 x 12288 13.7, 9.6; 131072 x 2560 with two, four
+  // panels at W = 4 52, 43.
   const int panels = (a.n + 15) / 16, T = (a.k + 127) / 128;
   if (a.m <= 4) {
     if (panels >= 2048) return launch<G, Z, 4, 2, 4, kQ4Plain>(a, tiles, s);
@@ -357,16 +358,24 @@ hipError_t pick(int mode, const Q4Args& a, int tiles, hipStream_t s) {
     return launch<G, Z, 4, 1, 8, kQ4Plain>(a, tiles, s);
   }
   if (a.m <= 16) {
+    if (panels >= 2048) return launch<G, Z, 16, 4, 4, kQ4Plain>(a, tiles, s);
     if (panels >= 512) return launch<G, Z, 16, 1, 4, kQ4Plain>(a, tiles, s);
     return launch<G, Z, 16, 1, 8, kQ4Plain>(a, tiles, s);
   }
-  // Chunks of 32 rows decode the codes least often, chunks of 16 give more
-  // wavefronts.  us at 32 rows with two panels (W = 4), one (W = 6), at 16 rows
-  // with two (W = 8): m = 24, 2560 x 9728 at group 32 22.6, 11.1, 11.8; m = 48
-  // 23.4, 18.1, 12.3; m = 77 24.9, 20.1, 18.0; m = 100, 2560 x 2560 8.0, 9.5,
-  // 7.4; m = 64, 12288 x 4096 16.8, 28, 19.0; m = 128, 4096 x 4096 at group 64
-  // 14.8, 23.5, 17.1.
-  if ((long long)panels * ((a.m + 31) / 32) >= 768) return launch<G, Z, 32, 2, 4, kQ4Plain>(a, tiles, s);
+  // Chunks of 32 rows decode the codes least often, several panels share the
+  // activations' way from the L2; both leave fewer wavefronts.  us at 32 rows
+  // with four panels (W = 4), two (W = 4, 7), one (W = 6), at 16 rows with two
+  // (W = 8), by panels x chunks: m = 128, 12288 x 4096 (3.1 thousand) 23.6,
+  // 27.8, 33.1, -, 33.7; m = 96, 9728 x 2560 (1824) 13.1, 15.2, 16.1, -, 17.6;
+  // m = 64, 12288 x 4096 (1536) 17.2, 16.3, 16.9, -, 18.6; m = 128, 4096 x 4096
+  // at group 64 (1024) 16.6, 15.3, 13.9, 23.5, 17.1; m = 64, 4096 x 12288 (512)
+  // -, 18.8, 16.6, 23.5, 18.7; at group 32, 2560 x 9728: m = 77 (480) -, 24.9,
+  // 17.9, 20.1, 18.7; m = 48 (320) -, 23.4, 16.5, 17.7, 12.2; m = 24 (160) -,
+  // 22.6, -, 11.1, 11.8.
+  const long long work = (long long)panels * ((a.m + 31) / 32);
+  if (work >= 1792) return launch<G, Z, 32, 4, 4, kQ4Plain>(a, tiles, s);
+  if (work >= 1152) return launch<G, Z, 32, 2, 4, kQ4Plain>(a, tiles, s);
+  if (work >= 448) return launch<G, Z, 32, 2, 7, kQ4Plain>(a, tiles, s);
   if (a.m <= 32) return launch<G, Z, 32, 1, 6, kQ4Plain>(a, tiles, s);
   return launch<G, Z, 16, 2, 8, kQ4Plain>(a, tiles, s);
 }

@@ -39,6 +39,7 @@ def test_gemm_matches_oracle(m, n, kg, group):
 
 @pytest.mark.parametrize("m,n,k,group,zero", [
     (1, 40, 20512, 32, True), (3, 9000, 2560, 32, True), (4, 32773, 64, 64, False), (2, 33000, 1280, 32, True),
+    (13, 33000, 320, 64, True), (20, 28700, 96, 32, False), (40, 4100, 10240, 32, True), (31, 49300, 64, 64, True),
     (12, 40, 20512, 32, True), (20, 40, 20512, 32, True), (160, 1640, 10240, 32, True), (33, 70, 33024, 128, False)])
 def test_gemm_long_rows_and_many_panels(m, n, k, group, zero):
     """Rows whose scales are staged in parts, and as many panels as change
