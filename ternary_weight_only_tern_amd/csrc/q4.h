@@ -57,12 +57,12 @@ enum Q4Mode {
 inline bool grid_fits(long long blocks, int threads) { return blocks * threads < (1ll << 32); }
 
 // Rows of the tile kernel's output tiles: 128 x 256 (one workgroup a CU), 96 x
-// 256 (two) and 64 x 128 (three).
-constexpr int kQ4TileLarge = 128, kQ4TileMid = 96, kQ4TileSmall = 64;
+// 256 (two), 64 x 128 (three) and 32 x 128 (five).
+constexpr int kQ4TileLarge = 128, kQ4TileMid = 96, kQ4TileSmall = 64, kQ4TileTiny = 32;
 // Rows of an experts' tile on the rows kernel.
 constexpr int kQ4TileRows = 16;
 // max_tiles: experts' tiles at most (expert modes); rows: one of the
-// three above, kQ4TileSmall in the expert modes.
+// four above, kQ4TileTiny or kQ4TileSmall in the expert modes.
 hipError_t launch_q4_rows(int mode, int group, const Q4Args& a, int max_tiles, hipStream_t s);
 hipError_t launch_q4_tile(int mode, int group, const Q4Args& a, int max_tiles, int rows, hipStream_t s);
 hipError_t launch_q4_reduce(const Q4Args& a, hipStream_t s);

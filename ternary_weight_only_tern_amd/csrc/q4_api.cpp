@@ -70,7 +70,7 @@ tern_status check_rows(int m) {
 
 size_t words_of(const tern_q4* w) { return (size_t)w->count * (size_t)w->n * (size_t)(w->k / 8); }
 
-int tile_cols(int tile) { return tile == tern::kQ4TileSmall ? 128 : 256; }
+int tile_cols(int tile) { return tile <= tern::kQ4TileSmall ? 128 : 256; }
 
 long long tiles_of(int m, int n, int tile) {
   return (long long)((m + tile - 1) / tile) * ((n + tile_cols(tile) - 1) / tile_cols(tile));
@@ -83,7 +83,9 @@ long long tiles_of(int m, int n, int tile) {
 // 32 with zero points 97 / - / 86), 400 x 12288 x 4096 57.8 / 51.0 / 60, 1024 x
 // 5120 x 2560 38.5 / 34.4 / -, 4096 x 2560 x 9728 (group 64) 303 / 274 / 327,
 // 2048 x 4096 x 4096 88 / - / 71.9, 512 x 4096 x 4096 29.7 / - / -.
+// Up to 32 rows a tile of 32 (24 x 131072 x 2560 47 us, 61 with 64 rows).
 int pick_tile(int m, int n, int group) {
+  if (m <= 32) return tern::kQ4TileTiny;
   const int tile[] = {tern::kQ4TileSmall, tern::kQ4TileMid, tern::kQ4TileLarge};
   const int tenths[] = {group < 128 ? 30 : 28, 23, 21};
   int best = 0;
@@ -102,9 +104,9 @@ int pick_tile(int m, int n, int group) {
 // The tile kernel holds a matrix's scales in one buffer below 2 GiB.
 bool tile_scales_fit(int n, int k) { return (long long)n * (k / 32) * 2 < (1ll << 31); }
 
-// How a plain product runs.  Rows kernel: up to 24 activation rows, up to 160
+// How a plain product runs.  Rows kernel: up to 16 activation rows, up to 160
 // unless tiles abound, and up to 320 where tiles would not fill the card (us,
-// rows against tiles: m = 24, 131072 x 2560 57, 61; m = 64 94, 66; m = 64,
+// rows against tiles: m = 24, 131072 x 2560 57, 47; m = 64 94, 66; m = 64,
 // 32768 x 2560 22.8, 21.9; m = 128, 12288 x 4096 23.6, 27.6; m = 160, 19456 x
 // 2560 29.8, 28.4; m = 128, 4096 x 4096 13.9, 17.7; m = 256, 2560 x 9728 29.8,
 // 30.2; m = 256, 12288 x 4096 41.6, 40.4).  K parts where tiles are few: some 512 workgroups, at
@@ -118,7 +120,7 @@ Route route_of(int m, int n, int k, int group) {
   Route r = {};
   const int steps = (k + 127) / 128;
   const long long small = tiles_of(m, n, tern::kQ4TileSmall);
-  r.rows = m <= 24 || (m <= 160 && small < 384) || (m <= 320 && small < 256) || !tile_scales_fit(n, k);
+  r.rows = m <= 16 || (m <= 160 && small < 384) || (m <= 320 && small < 256) || !tile_scales_fit(n, k);
   r.tile = pick_tile(m, n, group);
   r.splits = 1;
   if (!r.rows && small < 256) r.splits = std::max(1, (int)std::min<long long>(512 / std::max(small, 1ll), steps / 8));
@@ -163,14 +165,17 @@ ExpertsPlan plan_tokens(const tern_q4* up, const tern_q4* down, int m, int topk)
   const int experts = down->count, inner = down->k, n = down->n;
   const size_t slots = (size_t)m * topk;
   p.direct = slots <= (size_t)kDirectSlots;
-  // Tiles of 16 rows on the rows kernel (its tiles are a grid's y) or of 64 on
-  // the tile kernel, by the rows an expert has on average.  us, 64 experts of
-  // 2560 x 1024, up and down, 16 / 64: 8 rows an expert 47 + 19 / 53 + 25; 25
-  // rows 76 + 35 / 66 + 30; 100 rows 198 + 99 / 110 + 57; 512 rows 875 + 468 /
-  // 421 + 237.  Tiles of 96 or 128 rows gain nothing: an expert's last tile is
-  // half empty (100 rows 121 + 72, 512 rows 412 + 237 with 128).
+  // Tiles of 16 rows on the rows kernel (its tiles are a grid's y) or of 32 or
+  // 64 on the tile kernel, by the rows an expert has on average.  us, 64
+  // experts of 2560 x 1024, up and down, 16 / 32 / 64: 8 rows an expert 45 + 20
+  // / 43 + 20 / 55 + 23; 16 rows 58 + 26 / 54 + 22 / 60 + 26; 25 rows 73 + 34 /
+  // 56 + 26 / 64 + 30; 37 rows 96 + 46 / 66 + 32 / 67 + 32; 62 rows 138 + 67 /
+  // 85 + 43 / 83 + 42; 16 experts of 4096 x 1056 at group 32, 25 rows 39 + 26 /
+  // 46 + 26 / 66 + 27.  Tiles of 96 or 128 rows gain nothing: an expert's last
+  // tile is half empty (100 rows 110 + 57 with 64, 121 + 72 with 128; 512 rows
+  // 421 + 237, 412 + 237).
   const size_t mean = slots / experts;
-  p.rows = mean < 20 ? tern::kQ4TileRows : tern::kQ4TileSmall;
+  p.rows = mean < 12 ? tern::kQ4TileRows : mean < 40 ? tern::kQ4TileTiny : tern::kQ4TileSmall;
   if (!tile_scales_fit(up->n, up->k) || !tile_scales_fit(n, inner)) p.rows = tern::kQ4TileRows;
   p.tile = p.rows != tern::kQ4TileRows;
   p.max_tiles = (int)std::min<size_t>(slots, slots / p.rows + experts);
@@ -353,7 +358,7 @@ tern_status tern_q4_experts(const tern_q4* gate_up, const tern_q4* down, const u
     Q4_HIP(tern::launch_q4_plan(u.ids, mt * topk, down->count, p.rows, (int4*)(base + p.tiles),
                                 (int32_t*)(base + p.ntiles), (int32_t*)(base + p.order), (int32_t*)(base + p.place), s));
     auto product = [&](int mode, int group, const tern::Q4Args& a) {
-      return p.tile ? tern::launch_q4_tile(mode, group, a, p.max_tiles, tern::kQ4TileSmall, s)
+      return p.tile ? tern::launch_q4_tile(mode, group, a, p.max_tiles, p.rows, s)
                     : tern::launch_q4_rows(mode, group, a, p.max_tiles, s);
     };
     if (down->k) Q4_HIP(product(tern::kQ4Up, gate_up->group, u));

@@ -307,6 +307,7 @@ hipError_t pick(const Q4Args& a, int tiles, int rows, hipStream_t s) {
     if (rows == kQ4TileLarge) return launch<G, Z, MODE, 1, 8, 4, 1>(a, tiles, s);
     if (rows == kQ4TileMid) return launch<G, Z, MODE, 1, 8, 3, 1>(a, tiles, s);
   }
+  if (rows == kQ4TileTiny) return launch<G, Z, MODE, 1, 4, 1, 1>(a, tiles, s);
   return launch<G, Z, MODE, 1, 4, 2, 1>(a, tiles, s);
 }
 

@@ -1,5 +1,5 @@
 """tern_q4_experts on the GPU against the oracle, on each of its routes (slot
-by slot, tiles of 16 rows and of 64), and with tern_route before it."""
+by slot, tiles of 16, 32 and 64 rows), and with tern_route before it."""
 import numpy as np
 import pytest
 
@@ -37,6 +37,7 @@ def compare(up, down, group, x, ids, g, what, outs=("f16", "f32")):
     (11, 3, 20, 3, 2, 100), (25, 8, 100, 1, 1, 16),                                            # tiles of 16 rows
     (11, 3, 5, 3, 2, 100), (40, 2, 8, 2, 5, 47),
     (60, 2, 7, 3, 3, 129), (50, 1, 3, 5, 1, 20),
+    (70, 2, 7, 2, 2, 130), (36, 3, 3, 5, 3, 129),                                              # of 32
     (150, 1, 2, 2, 1, 70), (130, 4, 4, 1, 3, 260),                                             # of 64
     (900, 1, 2, 2, 1, 70), (170, 5, 2, 4, 3, 300),                                             # several an expert
 ])
