@@ -425,18 +425,25 @@ def _tensor(t, name, dtypes, device, shape=None):
     return t
 
 
-_torch = _raw_stream = _current_device = None
+def _space(ws, device):
+    """Checks a caller's workspace; its size and alignment the library checks."""
+    if ws.get_device() != device.index or not ws.is_contiguous():
+        _refuse(f"a workspace on {ws.device}, or with gaps; contiguous on {device} is wanted")
+
+
+_torch = _raw_stream = _current_device = _halves = None
 
 
 def _use_torch():
     """Looks torch's calls up once: a product of a few microseconds notices
     what its wrapper costs.  The stream handle comes without a Stream object
     where torch offers that."""
-    global _torch, _raw_stream, _current_device
+    global _torch, _raw_stream, _current_device, _halves
     import torch
     raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
     _raw_stream = raw or (lambda index: torch.cuda.current_stream(index).cuda_stream)
     _current_device = torch.cuda.current_device
+    _halves = (torch.float16,)
     _torch = torch
     return torch
 
@@ -551,10 +558,11 @@ def tern_q4_gemm(w: Q4Matrix, x, y_dtype=TERN_F16, out=None, stream=None, ws=Non
     if _elsewhere(device):
         with _torch.cuda.device(device):
             return tern_q4_gemm(w, x, y_dtype, out, stream, ws)
-    _tensor(x, "x", (_torch.float16,), device)
-    if x.dim() != 2 or x.size(1) != w.k:
-        _refuse(f"x has shape {tuple(x.shape)}, not [m][{w.k}]")
-    m = _count(x.size(0))
+    _tensor(x, "x", _halves, device)
+    shape = x.shape
+    if len(shape) != 2 or shape[1] != w.k:
+        _refuse(f"x has shape {tuple(shape)}, not [m][{w.k}]")
+    m = _count(shape[0])
     kind = _y_type(y_dtype)
     if out is None:
         out = _fresh((m, w.n), kind, device, stream)
@@ -562,8 +570,8 @@ def tern_q4_gemm(w: Q4Matrix, x, y_dtype=TERN_F16, out=None, stream=None, ws=Non
         _tensor(out, "out", (kind,), device, (m, w.n))
     if ws is None:
         ws = _scratch(load().tern_q4_workspace_bytes(w._at, m), device, stream)
-    elif ws.device != device or not ws.is_contiguous():
-        _refuse(f"a workspace on {ws.device}, or with gaps; contiguous on {device} is wanted")
+    else:
+        _space(ws, device)
     check(load().tern_q4_gemm(w._at, x.data_ptr(), m, out.data_ptr(), y_dtype, ws.data_ptr(), ws.nbytes,
                               _stream_of(device, stream)))
     return out
@@ -630,8 +638,8 @@ def tern_q4_experts(gate_up: Q4Matrix, down: Q4Matrix, x, ids, weights, y_dtype=
         _tensor(out, "out", (kind,), device, (m, down.n))
     if ws is None:
         ws = _scratch(load().tern_q4_experts_workspace_bytes(gate_up._at, down._at, m, topk), device, stream)
-    elif ws.device != device or not ws.is_contiguous():
-        _refuse(f"a workspace on {ws.device}, or with gaps; contiguous on {device} is wanted")
+    else:
+        _space(ws, device)
     check(load().tern_q4_experts(gate_up._at, down._at, x.data_ptr(), m, ids.data_ptr(), weights.data_ptr(), topk,
                                  out.data_ptr(), y_dtype, ws.data_ptr(), ws.nbytes, _stream_of(device, stream)))
     return out

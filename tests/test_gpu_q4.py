@@ -149,6 +149,19 @@ def test_gemm_captured_and_on_another_stream(m):
         assert torch.equal(got, want)
 
 
+@pytest.mark.parametrize("m,n,k", [(40, 3600, 640), (64, 9000, 320), (30, 49300, 64)])
+def test_gemm_captured_on_the_wide_kernels(m, n, k):
+    """Workgroups of over 64 KiB of LDS, four panels, 32-row tiles."""
+    import torch
+    rng = np.random.default_rng(12)
+    wd = upload(weights(rng, (), n, k, 64, False))
+    x = half(activations(rng, m, k))
+    y = torch.empty((m, n), device="cuda")
+    ws = L.tern_q4_workspace(wd, m)
+    replay_checks(lambda s: L.tern_q4_gemm(wd, x, L.TERN_F32, out=y, stream=s, ws=ws),
+                  lambda r: x.copy_(half(activations(rng, m, k))), [y])
+
+
 def test_gemm_offsets_past_32_bits():
     """Codes of over 4 GiB: rows at both ends against the oracle."""
     import torch
