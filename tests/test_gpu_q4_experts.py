@@ -187,6 +187,54 @@ def test_routed_layer_captured(m, topk, count):
     check(y, out, err + 2.0 ** -23 * np.abs(out), "f32", "routed layer")
 
 
+@pytest.mark.parametrize("m,count", [(2, 4), (30, 20), (60, 8), (150, 4)])
+def test_skipped_slots_weights_are_not_looked_at(m, count):
+    import torch
+    rng = np.random.default_rng(13)
+    up, down = (upload(w) for w in layer(rng, count, 64, 32, 33, 32, False))
+    x = half(activations(rng, m, 64))
+    ids, g = slots(rng, m, 2, count)
+    ids[::2, 1] = -1
+    g[::2, 1] = 0.5
+    want = L.tern_q4_experts(up, down, x, to_dev(ids), to_dev(g))
+    g[::4, 1], g[2::4, 1] = np.nan, np.inf
+    assert torch.equal(L.tern_q4_experts(up, down, x, to_dev(ids), to_dev(g)), want) and want.isfinite().all()
+
+
+@pytest.mark.parametrize("m,topk,count", [(1, 4, 8), (30, 4, 16), (100, 2, 4)])
+def test_layer_captured_with_its_own_buffers(m, topk, count):
+    """Q4Experts.run and tern_q4_gemm in a graph, their outputs and workspaces
+    from the graph's pool; another graph of the same layer beside it."""
+    import torch
+    rng = np.random.default_rng(14)
+    up, down = (upload(w) for w in layer(rng, count, 128, 64, 72, 64, False))
+    head = upload(weights(rng, (), 200, 128, 64, True))
+    e = L.Q4Experts(up, down, topk)
+    x, l = half(activations(rng, m, 128)), to_dev(rng.standard_normal((m, count)).astype(np.float32))
+    big = half(activations(rng, 400, 128))
+
+    def step():
+        return e.run(x, l), L.tern_q4_gemm(head, big)
+
+    step()
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for _ in range(2):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            outs.append(step())
+    for _ in range(3):
+        x.copy_(half(activations(rng, m, 128)))
+        l.normal_()
+        want = step()
+        torch.cuda.synchronize()
+        for graph in graphs:
+            graph.replay()
+        torch.cuda.synchronize()
+        for out in outs:
+            assert torch.equal(out[0], want[0]) and torch.equal(out[1], want[1])
+
+
 def test_two_calls_at_once_on_two_streams():
     import torch
     rng = np.random.default_rng(9)
