@@ -465,7 +465,8 @@ tern_status tern_route(const void *logits, int32_t l_dtype, int32_t m, const ter
  * width of y ([m][n]).  Slots whose id lies outside 0..count-1 are skipped
  * (a token without any gets zeros); a token may name an expert twice.  The
  * inner values silu(g) * u are held in FP16 (the down product's matrix
- * operand; beyond 65504 they are infinite); a skipped slot's weight is not
+ * operand; beyond 65504 they are infinite), for up to 32 slots as the sum of
+ * two FP16 values; a skipped slot's weight is not
  * looked at; every sum is FP32, a token's slots are added in slot order, and
  * results are bitwise reproducible.  count <= 1024, topk <= 2^19, m * topk
  * < 2^31 (TERN_E_UNSUPPORTED).  ws: tern_q4_experts_workspace_bytes bytes, 16-byte

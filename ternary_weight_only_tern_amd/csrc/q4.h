@@ -49,8 +49,9 @@ enum Q4Mode {
   kQ4Plain = 0,       // y[m][n]
   kQ4Up = 1,          // h[position][n / 2] = silu(gate) * up, rows gathered from x
   kQ4Down = 2,        // part[position][n] (FP32) from h[position][k]
-  kQ4UpSlot = 3,      // as kQ4Up, one slot per tile: position = slot, expert = ids[slot]
-  kQ4DownToken = 4    // y[token][n] = sum over its slots, in slot order
+  kQ4UpSlot = 3,      // as kQ4Up, one slot per tile: position = slot, expert = ids[slot]; h[slot][2][n / 2]:
+                      // the FP16 value and, in FP16 again, what it leaves
+  kQ4DownToken = 4    // y[token][n] = sum over its slots, in slot order, from kQ4UpSlot's h
 };
 
 // A grid's threads have to be countable in 32 bits.

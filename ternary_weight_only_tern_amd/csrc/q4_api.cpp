@@ -171,11 +171,14 @@ ExpertsPlan plan_tokens(const tern_q4* up, const tern_q4* down, int m, int topk)
   // / 43 + 20 / 55 + 23; 16 rows 58 + 26 / 54 + 22 / 60 + 26; 25 rows 73 + 34 /
   // 56 + 26 / 64 + 30; 37 rows 96 + 46 / 66 + 32 / 67 + 32; 62 rows 138 + 67 /
   // 85 + 43 / 83 + 42; 16 experts of 4096 x 1056 at group 32, 25 rows 39 + 26 /
-  // 46 + 26 / 66 + 27.  Tiles of 96 or 128 rows gain nothing: an expert's last
+  // 46 + 26 / 66 + 27.  Few slots fill the card longer with tiles of 32: 8
+  // experts of 4096 x 2048 at group 64, 50 rows - / 37 + 20 / 48 + 25, 100 rows -
+  // / 58 + 30 / 58 + 30, 225 rows - / 111 + 57 / 96 + 50; 16 experts of 2560 x
+  // 1024, 75 rows - / 28 + 18 / 31 + 18.  Tiles of 96 or 128 rows gain nothing: an expert's last
   // tile is half empty (100 rows 110 + 57 with 64, 121 + 72 with 128; 512 rows
   // 421 + 237, 412 + 237).
   const size_t mean = slots / experts;
-  p.rows = mean < 12 ? tern::kQ4TileRows : mean < 40 ? tern::kQ4TileTiny : tern::kQ4TileSmall;
+  p.rows = mean < 12 ? tern::kQ4TileRows : mean < (slots < 2048 ? 100 : 40) ? tern::kQ4TileTiny : tern::kQ4TileSmall;
   if (!tile_scales_fit(up->n, up->k) || !tile_scales_fit(n, inner)) p.rows = tern::kQ4TileRows;
   p.tile = p.rows != tern::kQ4TileRows;
   p.max_tiles = (int)std::min<size_t>(slots, slots / p.rows + experts);
@@ -185,7 +188,7 @@ ExpertsPlan plan_tokens(const tern_q4* up, const tern_q4* down, int m, int topk)
     at += round_up(bytes, 256);
     return o;
   };
-  p.h = take(slots * inner * 2);
+  p.h = take(slots * inner * (p.direct ? 4 : 2));  // direct: a value's rounding and the rest
   if (!p.direct) {
     p.part = take(slots * n * 4);
     p.tiles = take((size_t)p.max_tiles * 16);

@@ -65,7 +65,7 @@ __global__ __launch_bounds__(W * 64) void q4_rows_kernel(const Q4Args a, const i
   uint16_t* const sl = reinterpret_cast<uint16_t*>(lds + W * S);
   uint8_t* const zl = reinterpret_cast<uint8_t*>(sl + panels * 16 * sp);
 
-  int e = 0, rows = 1, pos = blockIdx.y;
+  int e = 0, rows = token ? 2 : 1, pos = blockIdx.y;  // a token's x: a value's rounding and the rest of it
   if (MODE == kQ4Up || MODE == kQ4Down) {
     if ((int)blockIdx.y >= *a.ntiles) return;
     const int4 tile = a.tiles[blockIdx.y];
@@ -194,7 +194,7 @@ __global__ __launch_bounds__(W * 64) void q4_rows_kernel(const Q4Args a, const i
         if ((unsigned)ex >= (unsigned)a.experts) return false;
         mul = __builtin_bit_cast(float, __builtin_amdgcn_readlane(slot_gate, p));
         aim(ex);
-        fx = q4_buffer(a.x + slot * k, (uint32_t)k * 2);
+        fx = q4_buffer(a.x + slot * 2 * k, (uint32_t)k * 4);
       }
 #pragma unroll
       for (int b = 0; b < NB; ++b) q4_stage16(fc[b], cl + b * 64, co + (uint32_t)t * 64);
@@ -284,18 +284,27 @@ __global__ __launch_bounds__(W * 64) void q4_rows_kernel(const Q4Args a, const i
     for (int b = 0; b < NB; ++b)
       if (i * 16 + kq * 4 < rows) red[wave * S + (i * NB + b) * 64 + lane] = acc[i][b];
   __syncthreads();
-  for (int o = threadIdx.x; o < rows * NBO * 16; o += W * 64) {
+  for (int o = threadIdx.x; o < (token ? 1 : rows) * NBO * 16; o += W * 64) {
     const int row = o / (NBO * 16), c = o % (NBO * 16), b = c / 16;
     const int l = (row / 16 * NB + b) * 64 + row % 16 / 4 * 16 + c % 16, col = n0 + c;
-    float sum = 0.f, gate = 0.f;
+    float sum = 0.f, gate = 0.f, rest = 0.f;
 #pragma unroll
     for (int w = 0; w < W; ++w) {
       if (up) gate += red[w * S + l][row % 4];
+      if (token) rest += red[w * S + l][1];
       sum += red[w * S + l + (up ? 64 : 0)][row % 4];
     }
+    sum += rest;
     if (col >= width) continue;
     const size_t dst = ((size_t)pos + row) * width + col;
-    if (up)
+    if (MODE == kQ4UpSlot) {
+      // one slot fills one of the operand's rows: a second one costs the down
+      // product nothing and holds what rounding to FP16 leaves
+      const float h = q4_swiglu(gate, sum), high = (float)(_Float16)h;
+      _Float16* const to = reinterpret_cast<_Float16*>(a.y) + (size_t)pos * 2 * width + col;
+      to[0] = (_Float16)high;
+      to[width] = fabsf(high) < INFINITY ? (_Float16)(h - high) : (_Float16)0.0f;
+    } else if (up)
       reinterpret_cast<_Float16*>(a.y)[dst] = (_Float16)q4_swiglu(gate, sum);
     else if (MODE == kQ4Down || a.y_f32)
       reinterpret_cast<float*>(a.y)[dst] = sum;

@@ -39,7 +39,7 @@ def compare(up, down, group, x, ids, g, what, outs=("f16", "f32")):
     (60, 2, 7, 3, 3, 129), (50, 1, 3, 5, 1, 20),
     (70, 2, 7, 2, 2, 130), (36, 3, 3, 5, 3, 129),                                              # of 32
     (150, 1, 2, 2, 1, 70), (130, 4, 4, 1, 3, 260),                                             # of 64
-    (900, 1, 2, 2, 1, 70), (170, 5, 2, 4, 3, 300),                                             # several an expert
+    (900, 1, 2, 2, 1, 70), (170, 5, 2, 4, 3, 300), (1100, 2, 30, 1, 1, 65),                                             # several an expert
 ])
 def test_experts_match_oracle(m, topk, count, hidden, inner, width, group):
     say("experts", m, topk, count, hidden, inner, width, group)
