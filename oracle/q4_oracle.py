@@ -85,11 +85,12 @@ def route(logits, topk, score="softmax", bias=None, groups=1, best=1, keep=1, re
     return ids, weights
 
 
-def experts(up, down, group, x, ids, gates):
+def experts(up, down, group, x, ids, gates, parts=1):
     """up, down: (q, scale, zero) stacks.  (y, bound without the output's own
     rounding.)  The inner values' error: the FP32 sums of gate and up (silu's
     slope is below 1.1), the exponential ((|g| + 4) 2^-22 relative), their
-    rounding to FP16; it reaches y through |Wd|; the down product's and the
+    rounding to `parts` FP16 values (a second one leaves half a step of the
+    first one's rounding, and subnormals' 2^-25); it reaches y through |Wd|; the down product's and the
     slots' FP32 sums add theirs."""
     m, topk = ids.shape
     count = up[0].shape[0]
@@ -108,10 +109,10 @@ def experts(up, down, group, x, ids, gates):
                 silu = g / (1 + np.exp(-g))
             h = silu * u
             dh = 1.1 * dg * (np.abs(u) + du) + np.abs(silu) * du + np.abs(h) * (np.abs(g) + 4) * 2.0 ** -22
-            dh = dh + (np.abs(h) + dh) * 2.0 ** -11 + 2.0 ** -25
+            dh = dh + (np.abs(h) + dh) * 2.0 ** (-11 * parts) + 2.0 ** -25
             w = dequant(*of(down), group)
             gate = float(gates[t, j])
             y[t] += gate * (w @ h)
             b = np.abs(w) @ (np.abs(h) + dh)
-            err[t] += abs(gate) * (np.abs(w) @ dh + (adds(w.shape[1], group) + topk + 2) * ADD * b)
+            err[t] += abs(gate) * (np.abs(w) @ dh + (adds(w.shape[1], group) + topk + 1 + parts) * ADD * b)
     return y, err

@@ -109,6 +109,33 @@ def test_experts_skipped_repeated_and_lopsided(m, topk, count):
     assert (got == 0).all()
 
 
+@pytest.mark.parametrize("m,topk,count,hidden,inner,group", [
+    (1, 1, 4, 256, 128, 128), (1, 8, 64, 2560, 1024, 128), (4, 8, 8, 320, 96, 32), (32, 1, 5, 128, 64, 64)])
+def test_few_slots_keep_their_inner_values(m, topk, count, hidden, inner, group):
+    """Up to 32 slots the inner values come as two FP16 values each: the bound
+    has their rounding squared."""
+    rng = np.random.default_rng(15)
+    up, down = layer(rng, count, hidden, inner, 40, group, True)
+    ids, g = slots(rng, m, topk, count)
+    x = (activations(rng, m, hidden).astype(np.float64) / 16).astype(np.float16)
+    y, err = Q.experts(up, down, group, x, ids, g, parts=2)
+    check(L.tern_q4_experts(upload(up), upload(down), half(x), to_dev(ids), to_dev(g), L.TERN_F32), y, err, "f32", "few slots")
+
+
+def test_few_slots_past_fp16_are_infinite():
+    """An inner value beyond FP16 is infinite, its rest nothing: no NaN."""
+    import torch
+    rng = np.random.default_rng(16)
+    up, down = layer(rng, 1, 64, 32, 3, 32, False)
+    q = np.full_like(up[0], 15)
+    up = (q, np.full_like(up[1], np.float16(4.0)), None)
+    down = (np.full_like(down[0], 9), np.ones_like(down[1]), None)  # weights 1
+    x = half(np.ones((1, 64), np.float16))
+    got = L.tern_q4_experts(upload(up), upload(down), x, to_dev(np.zeros((1, 1), np.int32)), to_dev(np.ones((1, 1), np.float32)),
+                            L.TERN_F32)
+    assert torch.isinf(got).all() and (got > 0).all()
+
+
 def test_experts_bad_rows_stay_alone():
     import torch
     rng = np.random.default_rng(5)
