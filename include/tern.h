@@ -464,11 +464,13 @@ tern_status tern_route(const void *logits, int32_t l_dtype, int32_t m, const ter
  * projection's I; k = the width of x.  down: the same count, k = I, n = the
  * width of y ([m][n]).  Slots whose id lies outside 0..count-1 are skipped
  * (a token without any gets zeros); a token may name an expert twice.  The
- * inner values silu(g) * u are held in FP16 (the down product's matrix
- * operand; beyond 65504 they are infinite), for up to 32 slots as the sum of
- * two FP16 values; a skipped slot's weight is not
- * looked at; every sum is FP32, a token's slots are added in slot order, and
- * results are bitwise reproducible.  count <= 1024, topk <= 2^19, m * topk
+ * inner values silu(g) * u are held as sums of BF16 values, the down
+ * product's matrix operands: two (17 bits) above 32 slots, three (FP32's 24)
+ * where a call of few slots is computed slot by slot; from 2^-50 to 2^71 in
+ * size, beyond which they are infinite.  A skipped slot's weight is not
+ * looked at; every sum is FP32 (a token's slots in slot order, or, slot by
+ * slot, as its workgroup's wavefronts share their products), and results are
+ * bitwise reproducible (the same call; another m may add in another order).  count <= 1024, topk <= 2^19, m * topk
  * < 2^31 (TERN_E_UNSUPPORTED).  ws: tern_q4_experts_workspace_bytes bytes, 16-byte
  * aligned; calls that overlap in time must not share it.  ids and weights as
  * tern_route leaves them (device).  Async on stream. */

@@ -88,10 +88,13 @@ def route(logits, topk, score="softmax", bias=None, groups=1, best=1, keep=1, re
 def experts(up, down, group, x, ids, gates, parts=1):
     """up, down: (q, scale, zero) stacks.  (y, bound without the output's own
     rounding.)  The inner values' error: the FP32 sums of gate and up (silu's
-    slope is below 1.1), the exponential ((|g| + 4) 2^-22 relative), their
-    rounding to `parts` FP16 values (a second one leaves half a step of the
-    first one's rounding, and subnormals' 2^-25); it reaches y through |Wd|; the down product's and the
-    slots' FP32 sums add theirs."""
+    slope is below 1.1), the exponential ((|g| + 4) 2^-22 relative), and their
+    rounding to a BF16 value and `parts` more (1, or 2 for up to 32 slots),
+    each of what the ones before leave: the first is off by 2^-8, and a rest
+    lies a binade lower than what it may be off by, so each one more brings
+    nine bits.  A product of a value and a code that FP32 cannot hold is lost
+    (2^-69 of a code's step).  This reaches y through |Wd|; the down product's
+    sums (every value's parts are added) and the slots' add theirs."""
     m, topk = ids.shape
     count = up[0].shape[0]
     y = np.zeros((m, down[0].shape[1]))
@@ -109,10 +112,10 @@ def experts(up, down, group, x, ids, gates, parts=1):
                 silu = g / (1 + np.exp(-g))
             h = silu * u
             dh = 1.1 * dg * (np.abs(u) + du) + np.abs(silu) * du + np.abs(h) * (np.abs(g) + 4) * 2.0 ** -22
-            dh = dh + (np.abs(h) + dh) * 2.0 ** (-11 * parts) + 2.0 ** -25
+            dh = dh + (np.abs(h) + dh) * 2.0 ** (-8 - 9 * parts) + 2.0 ** -69
             w = dequant(*of(down), group)
             gate = float(gates[t, j])
             y[t] += gate * (w @ h)
-            b = np.abs(w) @ (np.abs(h) + dh)
-            err[t] += abs(gate) * (np.abs(w) @ dh + (adds(w.shape[1], group) + topk + 1 + parts) * ADD * b)
+            b = np.abs(w) @ (np.abs(h) + dh) * (1 + 2.0 ** -7)
+            err[t] += abs(gate) * (np.abs(w) @ dh + (adds(w.shape[1], group) + parts * group + topk + 1 + parts) * ADD * b)
     return y, err

@@ -19,6 +19,8 @@ namespace tern {
 
 typedef _Float16 h2_t __attribute__((ext_vector_type(2)));
 typedef _Float16 h8_t __attribute__((ext_vector_type(8)));
+typedef __bf16 b8_t __attribute__((ext_vector_type(8)));
+typedef short s2_t __attribute__((ext_vector_type(2)));
 typedef float f4_t __attribute__((ext_vector_type(4)));
 typedef float a16_t __attribute__((ext_vector_type(16)));
 typedef uint32_t w2_t __attribute__((ext_vector_type(2)));
@@ -47,12 +49,19 @@ struct Q4Args {
 
 enum Q4Mode {
   kQ4Plain = 0,       // y[m][n]
-  kQ4Up = 1,          // h[position][n / 2] = silu(gate) * up, rows gathered from x
-  kQ4Down = 2,        // part[position][n] (FP32) from h[position][k]
-  kQ4UpSlot = 3,      // as kQ4Up, one slot per tile: position = slot, expert = ids[slot]; h[slot][2][n / 2]:
-                      // the FP16 value and, in FP16 again, what it leaves
-  kQ4DownToken = 4    // y[token][n] = sum over its slots, in slot order, from kQ4UpSlot's h
+  kQ4Up = 1,          // h[position][kInnerTile][n / 2] = silu(gate) * up, rows gathered from x
+  kQ4Down = 2,        // part[position][n] (FP32) from h[position][kInnerTile][k]
+  kQ4UpSlot = 3,      // as kQ4Up, one slot per tile: position = slot, expert = ids[slot]; h[slot][kInnerSlot][n / 2]
+  kQ4DownToken = 4    // y[token][n] = sum over its slots from kQ4UpSlot's h
 };
+
+// An inner value is held as the sum of BF16 values, each what the ones before
+// leave (q4_store_inner): two have 17 bits and cost the down product twice the
+// matrix instructions; three have FP32's bits and are free for single slots,
+// which fill three rows of an operand of sixteen.  BF16 because it has FP32's
+// range: inner values are products of two projections, whose size a model
+// bounds nowhere.
+constexpr int kInnerTile = 2, kInnerSlot = 3;
 
 // A grid's threads have to be countable in 32 bits.
 inline bool grid_fits(long long blocks, int threads) { return blocks * threads < (1ll << 32); }
@@ -61,10 +70,11 @@ inline bool grid_fits(long long blocks, int threads) { return blocks * threads <
 // 256 (two), 64 x 128 (three) and 32 x 128 (five).
 constexpr int kQ4TileLarge = 128, kQ4TileMid = 96, kQ4TileSmall = 64, kQ4TileTiny = 32;
 // Rows of an experts' tile on the rows kernel.
-constexpr int kQ4TileRows = 16;
+constexpr int kQ4TileRows = 16, kQ4TileFew = 8;
 // max_tiles: experts' tiles at most (expert modes); rows: one of the
-// four above, kQ4TileTiny or kQ4TileSmall in the expert modes.
-hipError_t launch_q4_rows(int mode, int group, const Q4Args& a, int max_tiles, hipStream_t s);
+// four above, kQ4TileTiny or kQ4TileSmall in the expert modes; one of the two
+// above on the rows kernel's tiles.
+hipError_t launch_q4_rows(int mode, int group, const Q4Args& a, int max_tiles, int rows, hipStream_t s);
 hipError_t launch_q4_tile(int mode, int group, const Q4Args& a, int max_tiles, int rows, hipStream_t s);
 hipError_t launch_q4_reduce(const Q4Args& a, hipStream_t s);
 hipError_t launch_q4_plan(const int32_t* ids, int slots, int experts, int rows, int4* tiles, int32_t* ntiles,
@@ -114,6 +124,57 @@ __device__ inline h8_t q4_decode(uint32_t w, const Q4Bias& b, const Q4Masks& m) 
   const h2_t p2 = as_h2((v & m.lo) | m.one) + b.lo;
   const h2_t p3 = as_h2((v & m.hi) | m.one) * six + b.hi;
   return h8_t{p0.x, p0.y, p1.x, p1.y, p2.x, p2.y, p3.x, p3.y};
+}
+
+// The same as BF16 (q - z) 2^-112, the down product's operand: FP16's bits of
+// an integer below 256 end in three zeros, so that a shift by three leaves
+// BF16's seven bits of mantissa and FP16's exponent where BF16's is read, its
+// bias 112 larger.  The inner values are held 2^56 times as large, the sums'
+// scales too: products lie 2^-56 below their value, in FP32's range for inner
+// values from 2^-50 to 2^71, and every factor is exact.  Eight more operations
+// per word.
+constexpr float kInnerScale = 0x1p56f;
+__device__ inline b8_t q4_decode_inner(uint32_t w, const Q4Bias& b, const Q4Masks& m) {
+  w4_t v = __builtin_bit_cast(w4_t, q4_decode(w, b, m));
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t pair = v[i];  // a bit cast of v[i] itself would read v[0]
+    v[i] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(s2_t, pair) >> 3) & 0x8FFF8FFFu;
+  }
+  return __builtin_bit_cast(b8_t, v);
+}
+
+// Weights of a word as the B operand and its product with A, 16 bytes of x
+// (FP16) or of inner values (BF16).
+template <bool INNER>
+__device__ inline w4_t q4_weights(uint32_t w, const Q4Bias& b, const Q4Masks& m) {
+  if constexpr (INNER) return __builtin_bit_cast(w4_t, q4_decode_inner(w, b, m));
+  return __builtin_bit_cast(w4_t, q4_decode(w, b, m));
+}
+template <bool INNER>
+__device__ inline f4_t q4_mfma16(w4_t x, w4_t w, f4_t c) {
+  if constexpr (INNER)
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(b8_t, x), __builtin_bit_cast(b8_t, w), c, 0, 0, 0);
+  return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(h8_t, x), __builtin_bit_cast(h8_t, w), c, 0, 0, 0);
+}
+template <bool INNER>
+__device__ inline a16_t q4_mfma32(w4_t x, w4_t w, a16_t c) {
+  if constexpr (INNER)
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(b8_t, x), __builtin_bit_cast(b8_t, w), c, 0, 0, 0);
+  return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(h8_t, x), __builtin_bit_cast(h8_t, w), c, 0, 0, 0);
+}
+
+// An inner value to PARTS rows of BF16 values, `pitch` apart.
+template <int PARTS>
+__device__ inline void q4_store_inner(void* y, size_t at, size_t pitch, float h) {
+  __bf16* const to = reinterpret_cast<__bf16*>(y) + at;
+  float rest = h * kInnerScale;
+#pragma unroll
+  for (int i = 0; i < PARTS; ++i) {
+    const __bf16 v = (__bf16)rest;
+    to[i * pitch] = v;
+    rest = fabsf((float)v) < INFINITY ? rest - (float)v : 0.0f;  // exact; nothing beside an infinity or a NaN
+  }
 }
 
 __device__ inline float half_bits(uint16_t v) { return (float)__builtin_bit_cast(_Float16, v); }

@@ -165,22 +165,25 @@ ExpertsPlan plan_tokens(const tern_q4* up, const tern_q4* down, int m, int topk)
   const int experts = down->count, inner = down->k, n = down->n;
   const size_t slots = (size_t)m * topk;
   p.direct = slots <= (size_t)kDirectSlots;
-  // Tiles of 16 rows on the rows kernel (its tiles are a grid's y) or of 32 or
-  // 64 on the tile kernel, by the rows an expert has on average.  us, 64
-  // experts of 2560 x 1024, up and down, 16 / 32 / 64: 8 rows an expert 45 + 20
-  // / 43 + 20 / 55 + 23; 16 rows 58 + 26 / 54 + 22 / 60 + 26; 25 rows 73 + 34 /
-  // 56 + 26 / 64 + 30; 37 rows 96 + 46 / 66 + 32 / 67 + 32; 62 rows 138 + 67 /
-  // 85 + 43 / 83 + 42; 16 experts of 4096 x 1056 at group 32, 25 rows 39 + 26 /
-  // 46 + 26 / 66 + 27.  Few slots fill the card longer with tiles of 32: 8
-  // experts of 4096 x 2048 at group 64, 50 rows - / 37 + 20 / 48 + 25, 100 rows -
-  // / 58 + 30 / 58 + 30, 225 rows - / 111 + 57 / 96 + 50; 16 experts of 2560 x
-  // 1024, 75 rows - / 28 + 18 / 31 + 18.  Tiles of 96 or 128 rows gain nothing: an expert's last
-  // tile is half empty (100 rows 110 + 57 with 64, 121 + 72 with 128; 512 rows
-  // 421 + 237, 412 + 237).
+  // Tiles of 8 or 16 rows on the rows kernel (its tiles are a grid's y) or of
+  // 32 or 64 on the tile kernel, by the rows an expert has on average; short
+  // groups make the tile kernel's decoding dear.  us of a whole call, 8 / 16 /
+  // 32 / 64: 64 experts of 2560 x 1024 at group 128, 2 rows an expert 57 / 62 /
+  // 63 / -, 4 rows 72 / 76 / 76 / -, 6 rows 81 / 83 / 79 / 103, 12 rows 114 / 105
+  // / 92 / 110, 25 rows - / 150 / 106 / 123, 37 rows - / 197 / 127 / 133, 62 rows
+  // - / - / 180 / 177, 125 rows - / - / 303 / 278; 128 of 2048 x 768, 2 rows 64 /
+  // 70 / 74 / -, 8 rows 108 / 106 / 95 / 120; 8 of 4096 x 2048 at group 64, 5
+  // rows 41 / 40 / 49 / -, 10 rows 55 / 51 / 50 / 63, 20 rows 76 / 66 / 62 / 64,
+  // 50 rows - / - / 77 / 92, 100 rows - / - / 122 / 114; 16 of 4096 x 1056 at
+  // group 32, 2.6 rows 47 / 48 / 62 / -, 8 rows 63 / 61 / 69 / 90, 12 rows 76 / 69
+  // / 84 / 105, 20 rows 102 / 82 / 88 / 111, 32 rows - / 107 / 90 / 123, 50 rows -
+  // / - / 124 / 126, 100 rows - / - / 176 / 173.
   const size_t mean = slots / experts;
-  p.rows = mean < 12 ? tern::kQ4TileRows : mean < (slots < 2048 ? 100 : 40) ? tern::kQ4TileTiny : tern::kQ4TileSmall;
+  p.rows = mean < 5 ? tern::kQ4TileFew
+           : mean * up->group < 768 ? tern::kQ4TileRows
+           : mean < 60 ? tern::kQ4TileTiny : tern::kQ4TileSmall;
   if (!tile_scales_fit(up->n, up->k) || !tile_scales_fit(n, inner)) p.rows = tern::kQ4TileRows;
-  p.tile = p.rows != tern::kQ4TileRows;
+  p.tile = p.rows > tern::kQ4TileRows;
   p.max_tiles = (int)std::min<size_t>(slots, slots / p.rows + experts);
   size_t at = 0;
   auto take = [&](size_t bytes) {
@@ -188,7 +191,7 @@ ExpertsPlan plan_tokens(const tern_q4* up, const tern_q4* down, int m, int topk)
     at += round_up(bytes, 256);
     return o;
   };
-  p.h = take(slots * inner * (p.direct ? 4 : 2));  // direct: a value's rounding and the rest
+  p.h = take(slots * inner * 2 * (p.direct ? tern::kInnerSlot : tern::kInnerTile));
   if (!p.direct) {
     p.part = take(slots * n * 4);
     p.tiles = take((size_t)p.max_tiles * 16);
@@ -297,7 +300,7 @@ tern_status tern_q4_gemm(const tern_q4* w, const uint16_t* x, int32_t m, void* y
   const hipStream_t s = (hipStream_t)stream;
   const Route r = route_of(m, w->n, w->k, w->group);
   if (r.rows) {
-    Q4_HIP(tern::launch_q4_rows(tern::kQ4Plain, w->group, a, 0, s));
+    Q4_HIP(tern::launch_q4_rows(tern::kQ4Plain, w->group, a, 0, 0, s));
     return TERN_OK;
   }
   a.splits = r.splits;
@@ -348,10 +351,10 @@ tern_status tern_q4_experts(const tern_q4* gate_up, const tern_q4* down, const u
     u.gates = d.gates = weights + (size_t)t * topk;
     u.topk = d.topk = topk;
     if (p.direct) {
-      if (down->k) Q4_HIP(tern::launch_q4_rows(tern::kQ4UpSlot, gate_up->group, u, mt * topk, s));
+      if (down->k) Q4_HIP(tern::launch_q4_rows(tern::kQ4UpSlot, gate_up->group, u, mt * topk, 0, s));
       d.y = yt;
       d.y_f32 = f32;
-      Q4_HIP(tern::launch_q4_rows(tern::kQ4DownToken, down->group, d, mt, s));
+      Q4_HIP(tern::launch_q4_rows(tern::kQ4DownToken, down->group, d, mt, 0, s));
       continue;
     }
     u.tiles = d.tiles = (const int4*)(base + p.tiles);
@@ -362,7 +365,7 @@ tern_status tern_q4_experts(const tern_q4* gate_up, const tern_q4* down, const u
                                 (int32_t*)(base + p.ntiles), (int32_t*)(base + p.order), (int32_t*)(base + p.place), s));
     auto product = [&](int mode, int group, const tern::Q4Args& a) {
       return p.tile ? tern::launch_q4_tile(mode, group, a, p.max_tiles, p.rows, s)
-                    : tern::launch_q4_rows(mode, group, a, p.max_tiles, s);
+                    : tern::launch_q4_rows(mode, group, a, p.max_tiles, p.rows, s);
     };
     if (down->k) Q4_HIP(product(tern::kQ4Up, gate_up->group, u));
     Q4_HIP(product(tern::kQ4Down, down->group, d));

@@ -8,7 +8,8 @@
 // operand's order, lane = row, would touch a line per lane), read back in the
 // operands' order, and the next tile's loads are in flight while they are
 // decoded and fed to v_mfma_f32_16x16x32_f16 (activations as A, 16 rows;
-// weights as B, 16 columns).  A group's FP32 sum is scaled and added to the
+// weights as B, 16 columns; the experts' down products to the BF16 form, an
+// inner value's parts in rows of their own).  A group's FP32 sum is scaled and added to the
 // running FP32 sum.  The panels' scales and zero points are staged once, for
 // the whole workgroup.  The wavefronts' sums are added in LDS in wavefront
 // order: results do not depend on timing.  Loads go through buffer
@@ -37,13 +38,16 @@ constexpr size_t scale_bytes(int groups, int panels, bool z) {
 }
 constexpr size_t kLdsMost = 100 * 1024, kScaleMost = 32 * 1024;
 
-// XR: rows of x at most (4, 16 or 32).  ct: K tiles whose scales are staged
+// XR: rows of x at most (4, 16 or 32; kQ4Down: of inner values' parts).  ct: K tiles whose scales are staged
 // at a time (all of them unless K is very long).
 template <int G, bool Z, int XR, int NB, int W, int MODE>
 __global__ __launch_bounds__(W * 64) void q4_rows_kernel(const Q4Args a, const int ct) {
   constexpr bool up = MODE == kQ4Up || MODE == kQ4UpSlot, token = MODE == kQ4DownToken;
   static_assert(!up || NB == 2, "gate and up panels go together");
   static_assert(!token || NB == 1, "one panel");
+  constexpr bool inner = MODE == kQ4Down || token;    // x holds inner values in BF16
+  // rows of x (of the operands) whose products make one row of the output
+  constexpr int P = MODE == kQ4Down ? kInnerTile : token ? kInnerSlot : 1;
   constexpr int NBO = up ? 1 : NB;                    // panels of the output
   constexpr int XI = XR / 4, MT = (XR + 15) / 16;     // staging loads and operands of a tile's x
   constexpr int SG = 128 / G, S = (NB + XI) * 64;     // 16-byte chunks of a wavefront's staging
@@ -65,7 +69,7 @@ __global__ __launch_bounds__(W * 64) void q4_rows_kernel(const Q4Args a, const i
   uint16_t* const sl = reinterpret_cast<uint16_t*>(lds + W * S);
   uint8_t* const zl = reinterpret_cast<uint8_t*>(sl + panels * 16 * sp);
 
-  int e = 0, rows = token ? 2 : 1, pos = blockIdx.y;  // a token's x: a value's rounding and the rest of it
+  int e = 0, rows = 1, pos = blockIdx.y;  // output rows
   if (MODE == kQ4Up || MODE == kQ4Down) {
     if ((int)blockIdx.y >= *a.ntiles) return;
     const int4 tile = a.tiles[blockIdx.y];
@@ -79,6 +83,8 @@ __global__ __launch_bounds__(W * 64) void q4_rows_kernel(const Q4Args a, const i
     pos = (int)blockIdx.x / 8 % chunks * XR;
     rows = min(a.m - pos, XR);
   }
+
+  const int xrows = rows * P;
 
   // panel b: 16 rows from row0(b), as many as exist
   auto row0 = [&](int b) {
@@ -153,13 +159,13 @@ __global__ __launch_bounds__(W * 64) void q4_rows_kernel(const Q4Args a, const i
     fx = q4_buffer(a.x, (uint32_t)a.m * (uint32_t)k * 2);  // below 2 GiB (host)
   } else if (!token) {
     const size_t first = MODE == kQ4UpSlot ? pos / a.topk : pos;
-    fx = q4_buffer(a.x + first * k, (uint32_t)rows * (uint32_t)k * 2);
+    fx = q4_buffer(a.x + first * P * k, (uint32_t)xrows * (uint32_t)k * 2);
   }
 #pragma unroll
   for (int j = 0; j < XI; ++j) {
     const int row = j * 4 + (lane >> 4);
     xo[j] = kFar;
-    if (row < rows)
+    if (row < xrows)
       xo[j] = (uint32_t)(MODE == kQ4Up ? a.slots[pos + row] / a.topk : row) * (uint32_t)k * 2 + ((lane ^ row) & 15) * 16;
   }
   const int cr = lane >> 2;  // the chunk of the codes this lane stages
@@ -171,7 +177,7 @@ __global__ __launch_bounds__(W * 64) void q4_rows_kernel(const Q4Args a, const i
   for (int i = 0; i < MT; ++i)
 #pragma unroll
     for (int b = 0; b < NB; ++b) acc[i][b] = f4_t{0.f, 0.f, 0.f, 0.f};
-  int slot_id = -1, slot_gate = 0;  // token: lane j holds slot j's expert and gate (topk <= 64, host)
+  int slot_id = -1, slot_gate = 0;  // token: lane j holds slot j's expert and gate (topk <= 32, host)
   if (token && lane < a.topk) {
     slot_id = a.ids[(size_t)pos * a.topk + lane];
     slot_gate = __builtin_bit_cast(int, a.gates[(size_t)pos * a.topk + lane]);
@@ -194,13 +200,13 @@ __global__ __launch_bounds__(W * 64) void q4_rows_kernel(const Q4Args a, const i
         if ((unsigned)ex >= (unsigned)a.experts) return false;
         mul = __builtin_bit_cast(float, __builtin_amdgcn_readlane(slot_gate, p));
         aim(ex);
-        fx = q4_buffer(a.x + slot * 2 * k, (uint32_t)k * 4);
+        fx = q4_buffer(a.x + slot * P * k, (uint32_t)P * (uint32_t)k * 2);
       }
 #pragma unroll
       for (int b = 0; b < NB; ++b) q4_stage16(fc[b], cl + b * 64, co + (uint32_t)t * 64);
 #pragma unroll
       for (int j = 0; j < XI; ++j)
-        if (j == 0 || j * 4 < rows) q4_stage16(fx, xl + j * 64, xo[j] + (uint32_t)t * 256);
+        if (j == 0 || j * 4 < xrows) q4_stage16(fx, xl + j * 64, xo[j] + (uint32_t)t * 256);
       return true;
     };
     bool have = false;
@@ -213,14 +219,14 @@ __global__ __launch_bounds__(W * 64) void q4_rows_kernel(const Q4Args a, const i
     while (have) {
       q4_loads_done();
       w4_t words[NB];
-      h8_t x[MT][4];
+      w4_t x[MT][4];
 #pragma unroll
       for (int b = 0; b < NB; ++b) words[b] = cl[b * 64 + code_chunk(r, kq)];
 #pragma unroll
       for (int i = 0; i < MT; ++i) {
-        const int row = min(i * 16 + r, rows - 1);  // rows behind the last: a copy, not stored
+        const int row = min(i * 16 + r, xrows - 1);  // rows behind the last: a copy, not stored
 #pragma unroll
-        for (int j = 0; j < 4; ++j) x[i][j] = __builtin_bit_cast(h8_t, xl[row * 16 + ((x_chunk<G>(j, kq) ^ row) & 15)]);
+        for (int j = 0; j < 4; ++j) x[i][j] = xl[row * 16 + ((x_chunk<G>(j, kq) ^ row) & 15)];
       }
       // this tile's scales and zero points of the lane's row; behind the last
       // group whatever lies there, not used
@@ -264,11 +270,14 @@ __global__ __launch_bounds__(W * 64) void q4_rows_kernel(const Q4Args a, const i
           for (int i = 0; i < MT; ++i) sum[i] = f4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
           for (int q = j * (4 / SG); q < (j + 1) * (4 / SG); ++q) {
-            const h8_t wv = q4_decode(w[q], bias, masks);
+            const w4_t wv = q4_weights<inner>(w[q], bias, masks);
 #pragma unroll
-            for (int i = 0; i < MT; ++i) sum[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(x[i][q], wv, sum[i], 0, 0, 0);
+            for (int i = 0; i < MT; ++i) {
+              if (MODE == kQ4Down && i * 16 >= xrows) break;
+              sum[i] = q4_mfma16<inner>(x[i][q], wv, sum[i]);
+            }
           }
-          const float f = half_bits(s[b][j]) * factor;
+          const float f = half_bits(s[b][j]) * (inner ? kInnerScale : 1.0f) * factor;
 #pragma unroll
           for (int i = 0; i < MT; ++i) acc[i][b] += f * sum[i];
         }
@@ -282,30 +291,26 @@ __global__ __launch_bounds__(W * 64) void q4_rows_kernel(const Q4Args a, const i
   for (int i = 0; i < MT; ++i)
 #pragma unroll
     for (int b = 0; b < NB; ++b)
-      if (i * 16 + kq * 4 < rows) red[wave * S + (i * NB + b) * 64 + lane] = acc[i][b];
+      if (i * 16 + kq * 4 < xrows) red[wave * S + (i * NB + b) * 64 + lane] = acc[i][b];
   __syncthreads();
-  for (int o = threadIdx.x; o < (token ? 1 : rows) * NBO * 16; o += W * 64) {
-    const int row = o / (NBO * 16), c = o % (NBO * 16), b = c / 16;
-    const int l = (row / 16 * NB + b) * 64 + row % 16 / 4 * 16 + c % 16, col = n0 + c;
-    float sum = 0.f, gate = 0.f, rest = 0.f;
+  for (int o = threadIdx.x; o < rows * NBO * 16; o += W * 64) {
+    const int row = o / (NBO * 16), c = o % (NBO * 16), b = c / 16, col = n0 + c;
+    float sum = 0.f, gate = 0.f;
 #pragma unroll
-    for (int w = 0; w < W; ++w) {
-      if (up) gate += red[w * S + l][row % 4];
-      if (token) rest += red[w * S + l][1];
-      sum += red[w * S + l + (up ? 64 : 0)][row % 4];
+    for (int i = P - 1; i >= 0; --i) {  // the smallest parts first
+      const int xr = row * P + i, l = (xr / 16 * NB + b) * 64 + xr % 16 / 4 * 16 + c % 16;
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        if (up) gate += red[w * S + l][xr % 4];
+        sum += red[w * S + l + (up ? 64 : 0)][xr % 4];
+      }
     }
-    sum += rest;
     if (col >= width) continue;
-    const size_t dst = ((size_t)pos + row) * width + col;
-    if (MODE == kQ4UpSlot) {
-      // one slot fills one of the operand's rows: a second one costs the down
-      // product nothing and holds what rounding to FP16 leaves
-      const float h = q4_swiglu(gate, sum), high = (float)(_Float16)h;
-      _Float16* const to = reinterpret_cast<_Float16*>(a.y) + (size_t)pos * 2 * width + col;
-      to[0] = (_Float16)high;
-      to[width] = fabsf(high) < INFINITY ? (_Float16)(h - high) : (_Float16)0.0f;
-    } else if (up)
-      reinterpret_cast<_Float16*>(a.y)[dst] = (_Float16)q4_swiglu(gate, sum);
+    const size_t at = (size_t)pos + row, dst = at * width + col;
+    if (MODE == kQ4UpSlot)
+      q4_store_inner<kInnerSlot>(a.y, at * kInnerSlot * width + col, width, q4_swiglu(gate, sum));
+    else if (MODE == kQ4Up)
+      q4_store_inner<kInnerTile>(a.y, at * kInnerTile * width + col, width, q4_swiglu(gate, sum));
     else if (MODE == kQ4Down || a.y_f32)
       reinterpret_cast<float*>(a.y)[dst] = sum;
     else
@@ -339,18 +344,18 @@ hipError_t launch(const Q4Args& a, int tiles, hipStream_t s) {
 }
 
 template <int G, bool Z>
-hipError_t pick(int mode, const Q4Args& a, int tiles, hipStream_t s) {
+hipError_t pick(int mode, const Q4Args& a, int tiles, int rows, hipStream_t s) {
   if (mode == kQ4UpSlot) return launch<G, Z, 4, 2, 8, kQ4UpSlot>(a, tiles, s);
   if (mode == kQ4DownToken) {
     if (tiles == 1) return launch<G, Z, 4, 1, 16, kQ4DownToken>(a, tiles, s);
     return launch<G, Z, 4, 1, 8, kQ4DownToken>(a, tiles, s);
   }
   if (mode == kQ4Up) return launch<G, Z, 16, 2, 4, kQ4Up>(a, tiles, s);
-  // us, one panel of four wavefronts against two of two: 14 tiles 12.9, 14; 67
-  // tiles 26, 19.4; 130 tiles 49, 35 (2560 x 1024, group 128)
+  // Two panels of two wavefronts; one of four was slower (us of whole calls:
+  // 64 experts of 2560 x 1024, 64 slots 52 against 49, 512 slots 103 against 90).
   if (mode == kQ4Down) {
-    if (tiles < 64) return launch<G, Z, 16, 1, 4, kQ4Down>(a, tiles, s);
-    return launch<G, Z, 16, 2, 2, kQ4Down>(a, tiles, s);
+    if (rows == kQ4TileFew) return launch<G, Z, 16, 2, 2, kQ4Down>(a, tiles, s);
+    return launch<G, Z, 32, 2, 2, kQ4Down>(a, tiles, s);
   }
   // Wavefronts a panel: 4 where there are panels enough to fill the card, 16
   // where few panels have long rows; two or four panels at a time where there
@@ -391,12 +396,12 @@ hipError_t pick(int mode, const Q4Args& a, int tiles, hipStream_t s) {
 
 }  // namespace
 
-hipError_t launch_q4_rows(int mode, int group, const Q4Args& a, int tiles, hipStream_t s) {
+hipError_t launch_q4_rows(int mode, int group, const Q4Args& a, int tiles, int rows, hipStream_t s) {
   const bool z = a.zero != nullptr;
   switch (group) {
-    case 32: return z ? pick<32, true>(mode, a, tiles, s) : pick<32, false>(mode, a, tiles, s);
-    case 64: return z ? pick<64, true>(mode, a, tiles, s) : pick<64, false>(mode, a, tiles, s);
-    default: return z ? pick<128, true>(mode, a, tiles, s) : pick<128, false>(mode, a, tiles, s);
+    case 32: return z ? pick<32, true>(mode, a, tiles, rows, s) : pick<32, false>(mode, a, tiles, rows, s);
+    case 64: return z ? pick<64, true>(mode, a, tiles, rows, s) : pick<64, false>(mode, a, tiles, rows, s);
+    default: return z ? pick<128, true>(mode, a, tiles, rows, s) : pick<128, false>(mode, a, tiles, rows, s);
   }
 }
 

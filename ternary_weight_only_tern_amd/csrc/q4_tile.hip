@@ -6,8 +6,11 @@
 // other half of LDS meanwhile; 16-byte chunks are XOR-swizzled by row, so
 // that the 32 rows of an operand read fall in distinct banks.  Only codes are
 // staged, never decoded weights: a wavefront decodes its weight rows in
-// registers and feeds v_mfma_f32_32x32x16_f16 as the B operand.  It keeps one
-// FP32 sum of the current group, which is scaled and added to the running
+// registers and feeds v_mfma_f32_32x32x16_f16 as the B operand (the experts'
+// down products the BF16 form, once for each of an inner value's two parts: as
+// many operations as the gate and up products, 215 against 239 us at 2048
+// tokens, 8 of 64 experts of 2560 x 1024; with one part, in FP16, 117 us, but
+// FP16's range and 11 bits).  It keeps one FP32 sum of the current group, which is scaled and added to the running
 // FP32 sum when the group ends (at group 128 one FMA per lane for every 16
 // matrix cycles).  Workgroups of one XCD take consecutive tiles, so that its
 // L2 reads each weight once.
@@ -30,12 +33,13 @@ template <int G, bool Z, int MODE, int WM, int WN, int MW, int NW>
 __global__ __launch_bounds__(WM * WN * 64) void q4_tile_kernel(const Q4Args a) {
 #ifdef __HIP_DEVICE_COMPILE__  // the host pass drops the kernel's stub when it has to look at the LDS loads
   constexpr int BM = 32 * WM * MW, BN = 32 * WN * NW, WAVES = WM * WN;
-  constexpr bool up = MODE == kQ4Up;
+  constexpr bool up = MODE == kQ4Up, inner = MODE == kQ4Down;
+  constexpr int P = inner ? kInnerTile : 1;  // rows of x that make an operand's row
   constexpr int NS = BK / G, SPG = G / 16;  // groups in a step, instructions (16 k) in a group
   // Two steps' staging, in separate arrays: the compiler then knows that
   // reading one does not wait for loads into the other.  (A third step in
   // flight gained nothing: 2048 x 4096 x 4096 77.7 against 74.4 us.)
-  __shared__ w4_t xs0[BM * 16], xs1[BM * 16], cs0[BN * 4], cs1[BN * 4];
+  __shared__ w4_t xs0[BM * P * 16], xs1[BM * P * 16], cs0[BN * 4], cs1[BN * 4];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / WN, wn = wave % WN;
   const int c32 = lane & 31, kq = lane >> 5;
@@ -69,8 +73,8 @@ __global__ __launch_bounds__(WM * WN * 64) void q4_tile_kernel(const Q4Args a) {
   // 16 CJ w + 16 j + (lane >> 2) of the codes.  Columns come in blocks of 32;
   // up: 16 of the gate, then the same 16 of the up projection.  Rows behind
   // the last lie past the buffers' ends.
-  constexpr int XJ = BM / 4 / WAVES, CJ = BN / 16 / WAVES;
-  static_assert(XJ > 0 && CJ > 0 && XJ * 4 * WAVES == BM && CJ * 16 * WAVES == BN, "every wavefront stages");
+  constexpr int XJ = BM * P / 4 / WAVES, CJ = BN / 16 / WAVES;
+  static_assert(XJ > 0 && CJ > 0 && XJ * 4 * WAVES == BM * P && CJ * 16 * WAVES == BN, "every wavefront stages");
   // half blocks of 16 rows: first row, and how many exist
   auto half_row = [&](int h) {
     const int col = n0 + (up ? h / 2 : h) * 16;
@@ -79,14 +83,14 @@ __global__ __launch_bounds__(WM * WN * 64) void q4_tile_kernel(const Q4Args a) {
   auto half_rows = [&](int h) { return max(0, min(16, width - n0 - (up ? h / 2 : h) * 16)); };
   const size_t row_bytes = (size_t)k * 2;
   const __amdgpu_buffer_rsrc_t fx = MODE == kQ4Up ? q4_buffer(a.x, (uint32_t)(a.m * row_bytes))
-                                                  : q4_buffer(a.x + (size_t)pos * k, (uint32_t)(rows * row_bytes));
+                                                  : q4_buffer(a.x + (size_t)pos * P * k, (uint32_t)(rows * P * row_bytes));
   uint32_t xo[XJ];
 #pragma unroll
   for (int j = 0; j < XJ; ++j) {
     const int row = wave * 4 * XJ + j * 4 + (lane >> 4);
     xo[j] = kFar;
-    if (row < rows)
-      xo[j] = (uint32_t)(MODE == kQ4Up ? a.slots[pos + row] / a.topk : row) * (uint32_t)row_bytes + ((lane ^ row) & 15) * 16;
+    if (row < rows * P)
+      xo[j] = (uint32_t)(MODE == kQ4Up ? a.slots[pos + row] / a.topk : row) * (uint32_t)row_bytes + ((lane ^ (row / P)) & 15) * 16;
   }
   __amdgpu_buffer_rsrc_t fc[CJ];
   uint32_t co[CJ];
@@ -159,7 +163,7 @@ __global__ __launch_bounds__(WM * WN * 64) void q4_tile_kernel(const Q4Args a) {
     const int left = min(NS, ng - t * NS);  // groups in this step
     const int at = vec ? t * NS % 4 : 0;
     w4_t w[2][NW];
-    h8_t xa[2][MW];
+    w4_t xa[2][P][MW];
     a16_t sum[MW][NW];
     auto read_x = [&](int step) {
       const int c = step / 4, i = step % 4;  // 64 k chunk, instruction in it
@@ -167,7 +171,8 @@ __global__ __launch_bounds__(WM * WN * 64) void q4_tile_kernel(const Q4Args a) {
 #pragma unroll
       for (int x = 0; x < MW; ++x) {
         const int row = (wm * MW + x) * 32 + c32;
-        xa[step % 2][x] = __builtin_bit_cast(h8_t, xd[row * 16 + ((chunk ^ row) & 15)]);
+#pragma unroll
+        for (int o = 0; o < P; ++o) xa[step % 2][o][x] = xd[(row * P + o) * 16 + ((chunk ^ row) & 15)];
       }
     };
 #pragma unroll
@@ -192,7 +197,7 @@ __global__ __launch_bounds__(WM * WN * 64) void q4_tile_kernel(const Q4Args a) {
       Q4Bias bias[NW];
 #pragma unroll
       for (int b = 0; b < NW; ++b) {
-        sc[b] = half_bits((uint16_t)((at + j < 2 ? sv[b].x : sv[b].y) >> (16 * ((at + j) & 1))));
+        sc[b] = half_bits((uint16_t)((at + j < 2 ? sv[b].x : sv[b].y) >> (16 * ((at + j) & 1)))) * (inner ? kInnerScale : 1.0f);
         bias[b] = q4_bias(Z ? (zv[b] >> (8 * (at + j))) & 255u : 8u);
 #pragma unroll
         for (int x = 0; x < MW; ++x)
@@ -206,10 +211,11 @@ __global__ __launch_bounds__(WM * WN * 64) void q4_tile_kernel(const Q4Args a) {
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int b = 0; b < NW; ++b) {
-          const h8_t wv = q4_decode(w[step / 4][b][step % 4], bias[b], masks);
+          const w4_t wv = q4_weights<inner>(w[step / 4][b][step % 4], bias[b], masks);
 #pragma unroll
-          for (int x = 0; x < MW; ++x)
-            sum[x][b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(xa[step % 2][x], wv, sum[x][b], 0, 0, 0);
+          for (int o = 0; o < P; ++o)
+#pragma unroll
+            for (int x = 0; x < MW; ++x) sum[x][b] = q4_mfma32<inner>(xa[step % 2][o][x], wv, sum[x][b]);
         }
       }
 #pragma unroll
@@ -260,7 +266,7 @@ __global__ __launch_bounds__(WM * WN * 64) void q4_tile_kernel(const Q4Args a) {
           const float other = __shfl_xor(value, 16);
           const int col = n0 + (wn * NW + b) * 16 + c32;
           if (c32 < 16 && row < rows && col < width)
-            reinterpret_cast<_Float16*>(a.y)[((size_t)pos + row) * width + col] = (_Float16)q4_swiglu(value, other);
+            q4_store_inner<kInnerTile>(a.y, ((size_t)pos + row) * kInnerTile * width + col, width, q4_swiglu(value, other));
           continue;
         }
         const int col = n0 + (wn * NW + b) * 32 + c32;
