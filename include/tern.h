@@ -430,7 +430,9 @@ tern_status tern_q4_gemm(const tern_q4 *w, const uint16_t *x, int32_t m, void *y
  *   score  s_e = exp(l_e) / sum exp(l)  (TERN_SCORE_SOFTMAX) or
  *          1 / (1 + exp(-l_e))          (TERN_SCORE_SIGMOID);
  *   key    c_e = s_e + bias_e (FP32 [experts]; a NaN counts as minus
- *          infinity), or, without a bias, s_e, in the order of l_e;
+ *          infinity), or, without a bias, s_e: experts then go in the order
+ *          of their logits l_e, groups judged by two keys by their sums of
+ *          scores;
  *   an expert whose logit or key is minus infinity is masked: never chosen;
  *   groups the experts form `groups` runs of equal length, of which the
  *          keep_groups with the largest sums of their group_best (1 or 2)
@@ -442,8 +444,8 @@ tern_status tern_q4_gemm(const tern_q4 *w, const uint16_t *x, int32_t m, void *y
  *   weight FP32 [m][topk]: the chosen experts' scores s (without bias), 0 at
  *          -1; with renorm divided by their sum (0 where it is 0); times
  *          scale.
- * Keys, their order and the weights are computed in FP64 (without a bias the
- * order is the logits').  experts <= 1024, groups <= 64, topk <= 64
+ * Keys, their order and sums and the weights are computed in FP64 (without a
+ * bias the experts' order is the logits', however close their scores).  experts <= 1024, groups <= 64, topk <= 64
  * (TERN_E_UNSUPPORTED above).  Async on stream. */
 typedef enum tern_score { TERN_SCORE_SOFTMAX = 0, TERN_SCORE_SIGMOID = 1 } tern_score;
 typedef struct tern_router {

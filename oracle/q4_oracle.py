@@ -64,15 +64,14 @@ def route(logits, topk, score="softmax", bias=None, groups=1, best=1, keep=1, re
             top = max(l)
             total = sum(np.exp(l[e] - top) for e in live)
             s = {e: np.exp(l[e] - top) / total for e in live}
-        if bias is None and (groups == 1 or best == 1):
-            key = {e: l[e] for e in live}
-        else:
-            key = {e: s[e] + (0.0 if bias is None else float(bias[e])) for e in live}
-        key = {e: v for e, v in key.items() if v == v and v > -np.inf}
+        # without a bias the order is the logits'; two experts' scores are summed as such
+        key = l if bias is None else {e: s[e] + float(bias[e]) for e in live}
+        key = {e: key[e] for e in live if key[e] == key[e] and key[e] > -np.inf}
         if groups > 1:
+            judged = s if bias is None and best == 2 else key
             sums = []
             for g in range(groups):
-                mine = sorted((v for e, v in key.items() if e // size == g), reverse=True)[:best]
+                mine = sorted((judged[e] for e in key if e // size == g), reverse=True)[:best]
                 sums.append(sum(mine) if mine else -np.inf)
             kept = sorted(range(groups), key=lambda g: (-sums[g], g))[:keep]
             key = {e: v for e, v in key.items() if e // size in kept}

@@ -5,7 +5,9 @@
 // What is chosen hangs on the order of the keys alone, so their order is
 // that of the FP64 keys: FP32 scores near 1 (sigmoid) or tiny ones (softmax)
 // tie where the exact ones do not.  Without a bias both scores grow with the
-// logit and the logit itself is the key.
+// logit and the logit itself is the key: where FP64 scores tie too (sigmoids
+// of logits past 36, softmax scores 745 below the largest), it does not.
+// Groups judged by two such experts go by the FP64 sums of their scores.
 //
 // Most rows need few FP64 keys.  route_kernel packs an FP32 key, rounded down
 // by at most 256 steps, and its expert into one word, lets 16 or 32 lanes a
@@ -97,7 +99,8 @@ __device__ inline void exact_row(const RouteArgs& a, int row, double* keys) {
     l[i] = -INFINITY;
     if (e < a.experts) l[i] = load_logit<F16>(a.logits, base + e);
   }
-  const bool plain_key = a.bias == nullptr && (a.groups == 1 || a.best == 1);
+  const bool plain_key = a.bias == nullptr;                          // the logit is the key
+  const bool score_sums = plain_key && a.groups > 1 && a.best == 2;  // but groups go by scores
   float top = 0.f;
   double total = 1.0;
   if (!a.sigmoid) {
@@ -106,7 +109,7 @@ __device__ inline void exact_row(const RouteArgs& a, int row, double* keys) {
     for (int i = 0; i < EPL; ++i) top = fmaxf(top, l[i]);
     top = wave_max(top);
     if (top == -INFINITY) top = 0.f;
-    if (!plain_key || !a.renorm) {
+    if (!plain_key || score_sums || !a.renorm) {
       double sum = 0.0;
 #pragma unroll
       for (int i = 0; i < EPL; ++i)
@@ -129,7 +132,8 @@ __device__ inline void exact_row(const RouteArgs& a, int row, double* keys) {
   if (a.groups > 1) {
     const int size = a.experts / a.groups;
 #pragma unroll
-    for (int i = 0; i < EPL; ++i) keys[i * 64 + lane] = key[i];
+    for (int i = 0; i < EPL; ++i)
+      keys[i * 64 + lane] = score_sums && l[i] != -INFINITY ? score_of(l[i], a.sigmoid, top, total) : key[i];
     __builtin_amdgcn_wave_barrier();
     __threadfence_block();
     double one = -INFINITY, two = -INFINITY;
@@ -240,7 +244,8 @@ __global__ __launch_bounds__(kWaves * 64, 8) void route_kernel(const RouteArgs a
   const int first = (blockIdx.x * kWaves + wave) * RPW, row = first + lane / LPR;
   if (first >= a.m) return;  // no barrier below: a wavefront works alone
   const size_t base = (size_t)min(row, a.m - 1) * a.experts;
-  const bool plain_key = a.bias == nullptr && (a.groups == 1 || a.best == 1);
+  const bool plain_key = a.bias == nullptr;                          // the logit is the key
+  const bool score_sums = plain_key && a.groups > 1 && a.best == 2;  // but groups go by scores
 
   // this lane's logits and biases: 16 bytes a load where rows allow it
   float l[EPL], bias[EPL] = {};
@@ -296,7 +301,7 @@ __global__ __launch_bounds__(kWaves * 64, 8) void route_kernel(const RouteArgs a
     const uint32_t w = lanes_max<LPR>((int32_t)b < 0 ? ~b : b | 0x80000000u);
     top = __builtin_bit_cast(float, w & 0x80000000u ? w & 0x7FFFFFFFu : ~w);
     if (top == -INFINITY) top = 0.f;
-    if (!a.renorm || !plain_key) {
+    if (!a.renorm || !plain_key || score_sums) {
       double sum = 0.0;
 #pragma unroll
       for (int i = 0; i < EPL; ++i) {
@@ -314,13 +319,15 @@ __global__ __launch_bounds__(kWaves * 64, 8) void route_kernel(const RouteArgs a
   uint32_t q[EPL];
   bool doubt = false;
   const float share = (float)(1.0 / total);
+  auto fast_score = [&](float v) {
+    return a.sigmoid ? __builtin_amdgcn_rcpf(1.0f + __expf(-v)) : __expf(v - top) * share;
+  };
 #pragma unroll
   for (int i = 0; i < EPL; ++i) {
     const int e = in * EPL + i;
     float c = l[i];
     if (!plain_key) {
-      c = a.sigmoid ? __builtin_amdgcn_rcpf(1.0f + __expf(-l[i])) : __expf(l[i] - top) * share;
-      c += bias[i];
+      c = fast_score(l[i]) + bias[i];
       if (l[i] == -INFINITY || !(c == c)) c = -INFINITY;
       if (c != -INFINITY && !(fabsf(c) < 2.0f)) doubt = true;
     }
@@ -346,7 +353,8 @@ __global__ __launch_bounds__(kWaves * 64, 8) void route_kernel(const RouteArgs a
   auto value = [&](uint32_t w) { return plain_key ? unpack_float(w) : unpack_fixed(w); };
   // how far apart two packed keys must be for their order to be certain
   const bool exact_keys = plain_key && F16;
-  auto margin = [&](float v) { return plain_key ? fabsf(v) * 0x1p-14f : a.sigmoid ? kSigmoidDoubt : kSoftmaxDoubt; };
+  const float score_margin = a.sigmoid ? kSigmoidDoubt : kSoftmaxDoubt;
+  auto margin = [&](float v) { return plain_key ? fabsf(v) * 0x1p-14f : score_margin; };
 
   if (a.groups > 1) {
     const int span = a.experts / a.groups / EPL;  // lanes of a group, a power of two
@@ -357,22 +365,38 @@ __global__ __launch_bounds__(kWaves * 64, 8) void route_kernel(const RouteArgs a
       one = max(one, o1);
     }
     float sum = one ? value(one) : -INFINITY;
-    if (a.best == 2 && two) sum += value(two);
+    if (score_sums) {  // from the logits themselves: a word has dropped bits that a score may hang on
+      float first_score = -INFINITY, second_score = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) {
+        const float v = l[i] == -INFINITY ? -INFINITY : fast_score(l[i]);
+        second_score = fmaxf(second_score, fminf(first_score, v));
+        first_score = fmaxf(first_score, v);
+      }
+      for (int d = 1; d < span; d <<= 1) {
+        const float o1 = __shfl_xor(first_score, d), o2 = __shfl_xor(second_score, d);
+        second_score = fmaxf(fminf(first_score, o1), fmaxf(second_score, o2));
+        first_score = fmaxf(first_score, o1);
+      }
+      sum = second_score == -INFINITY ? first_score : first_score + second_score;
+    } else if (a.best == 2 && two) {
+      sum += value(two);
+    }
     const int mine = in / span;
     int rank = 0;  // groups before this one
     for (int g = 0; g < a.groups; ++g) {
       const float v = __shfl(sum, lane - in + g * span);
       if (v > sum || (v == sum && g < mine)) ++rank;
     }
-    if (!exact_keys) {  // the last group kept, certainly before the next?
+    if (!exact_keys || score_sums) {  // the last group kept, certainly before the next?
       const uint32_t b = __builtin_bit_cast(uint32_t, sum), w = (int32_t)b < 0 ? ~b : b | 0x80000000u;
       const bool kept = rank < a.keep && in < a.groups * span;
       const uint32_t least = ~lanes_max<LPR>(kept ? ~w : 0u), most = lanes_max<LPR>(kept || in >= a.groups * span ? 0u : w);
       auto back = [](uint32_t v) { return __builtin_bit_cast(float, v & 0x80000000u ? v & 0x7FFFFFFFu : ~v); };
       const float x = back(least), y = back(most);
-      const bool unsure = most && y != -INFINITY && !(x - y > 2.0f * margin(x));
+      const bool unsure = most && y != -INFINITY && !(x - y > 2.0f * (score_sums ? score_margin : margin(x)));
       if (__ballot(unsure)) {
-        if (!plain_key && !a.sigmoid) {
+        if ((!plain_key || score_sums) && !a.sigmoid) {
           doubt = doubt || unsure;
         } else {  // the groups' FP64 sums
           double first_key = -INFINITY, second_key = -INFINITY;
@@ -380,7 +404,7 @@ __global__ __launch_bounds__(kWaves * 64, 8) void route_kernel(const RouteArgs a
             const int e = in * EPL + i;
             const float v = e < a.experts ? load_logit<F16>(a.logits, base + e) : -INFINITY;
             double k = v;
-            if (!plain_key && v != -INFINITY) {
+            if ((!plain_key || score_sums) && v != -INFINITY) {
               k = score_of(v, 1, 0.f, 1.0) + (a.bias ? (double)a.bias[e] : 0.0);
               if (!(k == k)) k = -INFINITY;
             }

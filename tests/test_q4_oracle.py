@@ -76,3 +76,16 @@ def test_experts_by_hand():
     want = -0.75 * (1 / (1 + math.exp(-1))) * 1.5
     assert math.isclose(y[0, 0], want, rel_tol=1e-12)
     assert 0 < err[0, 0] < 2e-3
+
+
+def test_route_without_a_bias_goes_by_the_logits():
+    """Scores that FP64 cannot tell apart: the larger logit is chosen first,
+    and groups judged by two such experts tie, so that the lower one stays."""
+    l = np.zeros((1, 8), np.float32)
+    l[0, 1], l[0, 5] = 40, 50
+    assert Q.route(l, 2, "sigmoid", None, 2, 2, 2)[0].tolist() == [[5, 1]]
+    l[0, 0:2], l[0, 4:6] = (40, 41), (50, 51)
+    assert Q.route(l, 1, "sigmoid", None, 2, 2, 1)[0].tolist() == [[1]]
+    l = np.full((1, 8), -1000, np.float32)
+    l[0, 2], l[0, 7] = 0, -900
+    assert Q.route(l, 2, "softmax", None, 2, 2, 2)[0].tolist() == [[2, 7]]
