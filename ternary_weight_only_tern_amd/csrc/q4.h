@@ -71,6 +71,9 @@ inline bool grid_fits(long long blocks, int threads) { return blocks * threads <
 constexpr int kQ4TileLarge = 128, kQ4TileMid = 96, kQ4TileSmall = 64, kQ4TileTiny = 32;
 // Rows of an experts' tile on the rows kernel.
 constexpr int kQ4TileRows = 16, kQ4TileFew = 8;
+// Wavefronts of its workgroups in the expert modes (their choice: q4_rows.hip),
+// and the down tiles' panels of 16 columns.
+constexpr int kUpSlotWaves = 8, kDownTokenWaves = 8, kDownOneTokenWaves = 16, kUpWaves = 4, kDownWaves = 2, kDownPanels = 2;
 // max_tiles: experts' tiles at most (expert modes); rows: one of the
 // four above, kQ4TileTiny or kQ4TileSmall in the expert modes; one of the two
 // above on the rows kernel's tiles.

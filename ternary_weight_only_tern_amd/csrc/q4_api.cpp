@@ -217,13 +217,16 @@ size_t experts_ws(const tern_q4* up, const tern_q4* down, int m, int topk) {
   return std::max(plan_tokens(up, down, most, topk).bytes, rest);
 }
 
-// Whether a round's grids can be launched (the kernels' widest workgroups on
-// the rows kernel).
-bool plan_fits(const tern_q4* down, const ExpertsPlan& p) {
-  auto fits = [&](long long width, int cols) {
-    return p.tile ? tern::grid_fits((width + cols - 1) / cols * p.max_tiles, 256) : tern::grid_fits((width + 15) / 16, 1024);
+// Whether a round's grids can be launched, those of the kernels it runs on.
+bool plan_fits(const tern_q4* down, const ExpertsPlan& p, int m) {
+  auto fits = [](long long width, int cols, long long rows, int threads) {
+    return tern::grid_fits((width + cols - 1) / cols * rows, threads);
   };
-  return fits(down->k, 64) && fits(down->n, 128);
+  if (p.direct)
+    return fits(down->k, 16, 1, 64 * tern::kUpSlotWaves) &&
+           fits(down->n, 16, 1, 64 * (m == 1 ? tern::kDownOneTokenWaves : tern::kDownTokenWaves));
+  if (p.tile) return fits(down->k, 64, p.max_tiles, 256) && fits(down->n, 128, p.max_tiles, 256);
+  return fits(down->k, 16, 1, 64 * tern::kUpWaves) && fits(down->n, 16 * tern::kDownPanels, 1, 64 * tern::kDownWaves);
 }
 
 tern_status check_experts(const tern_q4* up, const tern_q4* down, int m, int topk) {
@@ -336,7 +339,7 @@ tern_status tern_q4_experts(const tern_q4* gate_up, const tern_q4* down, const u
   const hipStream_t s = (hipStream_t)stream;
   const int most = round_tokens(gate_up, m, topk), f32 = y_dtype == TERN_F32;
   for (int mt : {most, m % most ? m % most : most})
-    if (!plan_fits(down, plan_tokens(gate_up, down, mt, topk)))
+    if (!plan_fits(down, plan_tokens(gate_up, down, mt, topk), mt))
       return fail(TERN_E_UNSUPPORTED, "m=%d, n=%d: the products need too many workgroups", m, down->n);
   for (int t = 0, mt; t < m; t += mt) {
     mt = std::min(most, m - t);

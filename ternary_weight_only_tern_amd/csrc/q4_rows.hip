@@ -345,17 +345,17 @@ hipError_t launch(const Q4Args& a, int tiles, hipStream_t s) {
 
 template <int G, bool Z>
 hipError_t pick(int mode, const Q4Args& a, int tiles, int rows, hipStream_t s) {
-  if (mode == kQ4UpSlot) return launch<G, Z, 4, 2, 8, kQ4UpSlot>(a, tiles, s);
+  if (mode == kQ4UpSlot) return launch<G, Z, 4, 2, kUpSlotWaves, kQ4UpSlot>(a, tiles, s);
   if (mode == kQ4DownToken) {
-    if (tiles == 1) return launch<G, Z, 4, 1, 16, kQ4DownToken>(a, tiles, s);
-    return launch<G, Z, 4, 1, 8, kQ4DownToken>(a, tiles, s);
+    if (tiles == 1) return launch<G, Z, 4, 1, kDownOneTokenWaves, kQ4DownToken>(a, tiles, s);
+    return launch<G, Z, 4, 1, kDownTokenWaves, kQ4DownToken>(a, tiles, s);
   }
-  if (mode == kQ4Up) return launch<G, Z, 16, 2, 4, kQ4Up>(a, tiles, s);
+  if (mode == kQ4Up) return launch<G, Z, 16, 2, kUpWaves, kQ4Up>(a, tiles, s);
   // Two panels of two wavefronts; one of four was slower (us of whole calls:
   // 64 experts of 2560 x 1024, 64 slots 52 against 49, 512 slots 103 against 90).
   if (mode == kQ4Down) {
-    if (rows == kQ4TileFew) return launch<G, Z, 16, 2, 2, kQ4Down>(a, tiles, s);
-    return launch<G, Z, 32, 2, 2, kQ4Down>(a, tiles, s);
+    if (rows == kQ4TileFew) return launch<G, Z, 16, kDownPanels, kDownWaves, kQ4Down>(a, tiles, s);
+    return launch<G, Z, 32, kDownPanels, kDownWaves, kQ4Down>(a, tiles, s);
   }
   // Wavefronts a panel: 4 where there are panels enough to fill the card, 16
   // where few panels have long rows; two or four panels at a time where there

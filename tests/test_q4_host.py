@@ -135,3 +135,18 @@ def test_sizes_past_32_bits_are_refused():
     assert L._count(2 ** 31 - 1) == 2 ** 31 - 1
     with pytest.raises(ValueError):
         L._count(2 ** 31)
+
+
+@pytest.mark.parametrize("m,topk,count,n", [
+    (1, 1, 8, 1 << 26), (16, 1, 1, 1 << 27), (32, 1, 2, 1 << 27), (2, 16, 1, 1 << 27), (400, 1, 1024, 1 << 30),
+    (1 << 15, 1, 64, 1 << 24)])
+def test_experts_grids_are_checked_before_any_launch(m, topk, count, n):
+    """A down product that needs too large a grid is refused before the gate
+    and up product runs: slot by slot (however few experts share the slots)
+    and on tiles."""
+    lib = L.load()
+    up, down = q4(n=64, k=64, group=32, count=count), q4(n=n, k=32, group=32, count=count)
+    need = lib.tern_q4_experts_workspace_bytes(at(up), at(down), m, topk)
+    got = lib.tern_q4_experts(at(up), at(down), 0x1000, m, 0x2000, 0x3000, topk, 0x4000, 0, 0x5000, need, None)
+    assert got == L.TERN_E_UNSUPPORTED
+    assert lib.tern_last_error().startswith(b"m=%d, n=" % m), lib.tern_last_error()
