@@ -473,8 +473,8 @@ tern_status tern_route(const void *logits, int32_t l_dtype, int32_t m, const ter
  * looked at; every sum is FP32 (a token's slots in slot order, or, slot by
  * slot, as its workgroup's wavefronts share their products), and results are
  * bitwise reproducible (the same call; another m may add in another order).  count <= 1024, topk <= 2^19, m * topk
- * < 2^31 (TERN_E_UNSUPPORTED).  ws: tern_q4_experts_workspace_bytes bytes, 16-byte
- * aligned; calls that overlap in time must not share it.  ids and weights as
+ * < 2^31 (TERN_E_UNSUPPORTED).  ws: tern_q4_experts_workspace_bytes bytes (tokens are
+ * taken in rounds of 1 GiB or of one token), 16-byte aligned; calls that overlap in time must not share it.  ids and weights as
  * tern_route leaves them (device).  Async on stream. */
 size_t tern_q4_experts_workspace_bytes(const tern_q4 *gate_up, const tern_q4 *down, int32_t m, int32_t topk);
 tern_status tern_q4_experts(const tern_q4 *gate_up, const tern_q4 *down, const uint16_t *x, int32_t m,

@@ -150,3 +150,12 @@ def test_experts_grids_are_checked_before_any_launch(m, topk, count, n):
     got = lib.tern_q4_experts(at(up), at(down), 0x1000, m, 0x2000, 0x3000, topk, 0x4000, 0, 0x5000, need, None)
     assert got == L.TERN_E_UNSUPPORTED
     assert lib.tern_last_error().startswith(b"m=%d, n=" % m), lib.tern_last_error()
+
+
+@pytest.mark.parametrize("hidden,inner,count,topk", [(7168, 2048, 256, 8), (4096, 2048, 64, 8), (65536, 32, 4, 1)])
+def test_experts_workspace_does_not_grow_without_end(hidden, inner, count, topk):
+    """Tokens are taken in rounds of about 1 GiB of partials and inner values."""
+    lib = L.load()
+    up, down = q4(n=2 * inner, k=512, count=count), q4(n=hidden, k=inner, group=32, count=count)
+    sizes = [lib.tern_q4_experts_workspace_bytes(at(up), at(down), m, topk) for m in (65536, 1 << 17, 1 << 20)]
+    assert 1 << 29 < min(sizes) and max(sizes) <= (1 << 30) + (1 << 24), sizes
