@@ -419,7 +419,8 @@ tern_status tern_q4_unpack(const tern_q4 *src, uint8_t *q, void *stream);
  * neither range nor precision.  Results are bitwise reproducible (the same
  * call; another m may add in another order).  ws:
  * tern_q4_workspace_bytes(w, m) (K parts' FP32 partials; calls that overlap
- * in time must not share it). */
+ * in time must not share it), enough for calls with fewer rows too; 0 for
+ * arguments that tern_q4_gemm refuses. */
 size_t tern_q4_workspace_bytes(const tern_q4 *w, int32_t m);
 tern_status tern_q4_gemm(const tern_q4 *w, const uint16_t *x, int32_t m, void *y, int32_t y_dtype, void *ws,
                          size_t ws_bytes, void *stream);
@@ -474,7 +475,8 @@ tern_status tern_route(const void *logits, int32_t l_dtype, int32_t m, const ter
  * slot, as its workgroup's wavefronts share their products), and results are
  * bitwise reproducible (the same call; another m may add in another order).  count <= 1024, topk <= 2^19, m * topk
  * < 2^31 (TERN_E_UNSUPPORTED).  ws: tern_q4_experts_workspace_bytes bytes (tokens are
- * taken in rounds of 1 GiB or of one token), 16-byte aligned; calls that overlap in time must not share it.  ids and weights as
+ * taken in rounds of 1 GiB or of one token; enough for fewer tokens too; 0 for
+ * arguments that are refused), 16-byte aligned; calls that overlap in time must not share it.  ids and weights as
  * tern_route leaves them (device).  Async on stream. */
 size_t tern_q4_experts_workspace_bytes(const tern_q4 *gate_up, const tern_q4 *down, int32_t m, int32_t topk);
 tern_status tern_q4_experts(const tern_q4 *gate_up, const tern_q4 *down, const uint16_t *x, int32_t m,

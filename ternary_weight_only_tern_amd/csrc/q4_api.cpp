@@ -134,6 +134,17 @@ size_t plain_ws(int m, const tern_q4* w) {
   return !r.rows && r.splits > 1 ? (size_t)r.splits * m * w->n * 4 : 0;
 }
 
+// The most that any call with up to m rows needs.  K parts come with more than
+// 320 rows, five of the tiles that route_of counts; the most of a tile's rows
+// takes the most.
+size_t plain_ws_upto(int m, const tern_q4* w) {
+  size_t most = plain_ws(m, w);
+  const int tile = tern::kQ4TileSmall;
+  for (long long r = 6 * tile; r < m && tiles_of((int)r, w->n, tile) < 256; r += tile)
+    most = std::max(most, plain_ws((int)r, w));
+  return most;
+}
+
 tern::Q4Args args_of(const tern_q4* w) {
   tern::Q4Args a = {};
   a.codes = w->codes;
@@ -197,7 +208,7 @@ ExpertsPlan plan_tokens(const tern_q4* up, const tern_q4* down, int m, int topk)
   p.h = take(slots * inner * 2 * (p.direct ? tern::kInnerSlot : tern::kInnerTile));
   if (!p.direct) {
     p.part = take(slots * n * 4);
-    p.tiles = take((size_t)p.max_tiles * 16);
+    p.tiles = take(std::min(slots, slots / tern::kQ4TileFew + experts) * 16);  // whatever the rows: it grows with the slots
     p.ntiles = take(4);
     p.order = take(slots * 4);
     p.place = take(slots * 4);
@@ -219,11 +230,18 @@ int round_tokens(const tern_q4* up, const tern_q4* down, int m, int topk) {
   return (int)std::max<long long>(1, std::min<long long>(launch_tokens(up, m, topk), by_bytes));
 }
 
+// What a call with m tokens needs, and what any with up to m does.
 size_t experts_ws(const tern_q4* up, const tern_q4* down, int m, int topk) {
   if (m <= 0) return 0;
   const int most = round_tokens(up, down, m, topk);
   const size_t rest = m % most ? plan_tokens(up, down, m % most, topk).bytes : 0;
   return std::max(plan_tokens(up, down, most, topk).bytes, rest);
+}
+size_t experts_ws_upto(const tern_q4* up, const tern_q4* down, int m, int topk) {
+  size_t most = experts_ws(up, down, m, topk);  // on tiles it grows with the tokens
+  for (int t = 1; t < m && (long long)t * topk <= kDirectSlots; ++t)
+    most = std::max(most, plan_tokens(up, down, t, topk).bytes);
+  return most;
 }
 
 // Whether a round's grids can be launched, those of the kernels it runs on.
@@ -261,7 +279,7 @@ tern_status tern_q4_check(const tern_q4* w) { return check_q4(w); }
 
 size_t tern_q4_workspace_bytes(const tern_q4* w, int32_t m) {
   if (check_shape(w) != TERN_OK || check_rows(m) != TERN_OK) return 0;
-  return std::max<size_t>(256, plain_ws(m, w));
+  return std::max<size_t>(256, plain_ws_upto(m, w));
 }
 
 tern_status tern_q4_pack(const uint8_t* q, const tern_q4* dst, void* ws, size_t ws_bytes, void* stream) {
@@ -325,7 +343,7 @@ tern_status tern_q4_gemm(const tern_q4* w, const uint16_t* x, int32_t m, void* y
 
 size_t tern_q4_experts_workspace_bytes(const tern_q4* gate_up, const tern_q4* down, int32_t m, int32_t topk) {
   if (check_experts(gate_up, down, m, topk) != TERN_OK) return 0;
-  return std::max<size_t>(256, experts_ws(gate_up, down, m, topk));
+  return std::max<size_t>(256, experts_ws_upto(gate_up, down, m, topk));
 }
 
 tern_status tern_q4_experts(const tern_q4* gate_up, const tern_q4* down, const uint16_t* x, int32_t m,

@@ -159,3 +159,26 @@ def test_experts_workspace_does_not_grow_without_end(hidden, inner, count, topk)
     up, down = q4(n=2 * inner, k=512, count=count), q4(n=hidden, k=inner, group=32, count=count)
     sizes = [lib.tern_q4_experts_workspace_bytes(at(up), at(down), m, topk) for m in (65536, 1 << 17, 1 << 20)]
     assert 1 << 29 < min(sizes) and max(sizes) <= (1 << 30) + (1 << 24), sizes
+
+
+@pytest.mark.parametrize("n,k,group", [(4096, 4096, 128), (64, 4096, 64), (1000, 9728, 32), (12288, 4096, 128), (33, 128, 64)])
+def test_gemm_workspace_grows_with_the_rows(n, k, group):
+    """A workspace for some rows serves every call with fewer."""
+    lib = L.load()
+    d = q4(n=n, k=k, group=group)
+    rows = [*range(1, 700), 1023, 1024, 1025, 4096, 20000]
+    sizes = [lib.tern_q4_workspace_bytes(at(d), m) for m in rows]
+    assert sizes == sorted(sizes)
+    assert sizes[0] == 256 and (sizes[-1] > 256) == (k > 2048 and n < 12288)  # K parts: long rows, few tiles
+
+
+@pytest.mark.parametrize("hidden,inner,count,topk", [(4096, 14336, 8, 2), (2560, 1024, 64, 8), (64, 32, 4, 1), (60000, 32, 3, 40), (4096, 2048, 1, 2)])
+def test_experts_workspace_grows_with_the_tokens(hidden, inner, count, topk):
+    lib = L.load()
+    up, down = q4(n=2 * inner, k=512, count=count), q4(n=hidden, k=inner, group=32, count=count)
+    rows = [*range(1, 900), 2047, 2048, 2049, 5000, 20000, 65536, 1 << 17]
+    sizes = [lib.tern_q4_experts_workspace_bytes(at(up), at(down), m, topk) for m in rows]
+    assert sizes == sorted(sizes)
+    for m, size in zip(rows, sizes):  # each is enough, and checked before the workspace's alignment
+        call = lambda nb: lib.tern_q4_experts(at(up), at(down), 0x1000, m, 0x2000, 0x3000, topk, 0x4000, 0, 0x5008, nb, None)
+        assert call(size) == L.TERN_E_ALIGN and call(255) == L.TERN_E_WORKSPACE
