@@ -479,6 +479,11 @@ def _count(v):
     return v if v < 2 ** 31 else _refuse(f"a size of {v} is too large")
 
 
+def _bytes(size):
+    """A workspace's size; the library's is 0 for sizes that it refuses."""
+    return size or _refuse(last_error())
+
+
 class Q4Matrix:
     """4-bit weights on the device: codes uint8 [n][k/2] in tern_q4's word
     order, scale fp16 [n][k/group], zero uint8 [n][k/group] or None (8
@@ -547,8 +552,8 @@ def _y_type(y_dtype):
 
 
 def tern_q4_workspace(w: Q4Matrix, m: int):
-    """A workspace for tern_q4_gemm with m activation rows."""
-    return _scratch(load().tern_q4_workspace_bytes(w._at, m), w.device, None)
+    """A workspace for tern_q4_gemm with up to m activation rows."""
+    return _scratch(_bytes(load().tern_q4_workspace_bytes(w._at, _count(m))), w.device, None)
 
 
 def tern_q4_gemm(w: Q4Matrix, x, y_dtype=TERN_F16, out=None, stream=None, ws=None):
@@ -591,6 +596,7 @@ def tern_route(logits, topk, score=TERN_SCORE_SOFTMAX, bias=None, groups=1, grou
                               stream)
     _tensor(logits, "logits", (torch.float16, torch.float32), device)
     m, experts = _count(logits.size(0)), _count(logits.size(1))
+    _count(max(topk, groups, group_best, keep_groups))
     if bias is not None:
         _tensor(bias, "bias", (torch.float32,), device, (experts,))
     if ids is None:
@@ -608,8 +614,8 @@ def tern_route(logits, topk, score=TERN_SCORE_SOFTMAX, bias=None, groups=1, grou
 
 
 def tern_q4_experts_workspace(gate_up: Q4Matrix, down: Q4Matrix, m: int, topk: int):
-    """A workspace for tern_q4_experts with m tokens of topk slots."""
-    return _scratch(load().tern_q4_experts_workspace_bytes(gate_up._at, down._at, m, topk), down.device, None)
+    """A workspace for tern_q4_experts with up to m tokens of topk slots."""
+    return _scratch(_bytes(load().tern_q4_experts_workspace_bytes(gate_up._at, down._at, _count(m), _count(topk))), down.device, None)
 
 
 def tern_q4_experts(gate_up: Q4Matrix, down: Q4Matrix, x, ids, weights, y_dtype=TERN_F16, out=None, stream=None,

@@ -51,3 +51,13 @@ def test_the_larger_of_two_saturated_scores_comes_first():
     l = np.full((1, 8), -1000, np.float32)
     l[0, 2], l[0, 7] = 0, -900
     assert run(l, 2, "softmax", None, 2, 2, 2).tolist() == [[2, 7]]
+
+
+def test_settings_past_32_bits_are_refused():
+    import torch
+    from ternary_weight_only_tern_amd import lib as L
+    l = torch.randn((4, 8), device="cuda")
+    far = 1 << 32
+    for kw in (dict(topk=far + 2), dict(groups=far + 1), dict(groups=2, keep_groups=far + 1), dict(group_best=far + 1)):
+        with pytest.raises(ValueError):
+            L.tern_route(l, **{**dict(topk=2), **kw})

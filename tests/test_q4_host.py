@@ -182,3 +182,19 @@ def test_experts_workspace_grows_with_the_tokens(hidden, inner, count, topk):
     for m, size in zip(rows, sizes):  # each is enough, and checked before the workspace's alignment
         call = lambda nb: lib.tern_q4_experts(at(up), at(down), 0x1000, m, 0x2000, 0x3000, topk, 0x4000, 0, 0x5008, nb, None)
         assert call(size) == L.TERN_E_ALIGN and call(255) == L.TERN_E_WORKSPACE
+
+
+def test_workspaces_of_refused_sizes_are_refused():
+    """The binding makes no workspace for a call that would be refused."""
+    from types import SimpleNamespace
+    descs = [q4(n=64, k=256), q4(n=128, k=256, count=4), q4(n=96, k=64, count=4)]
+    w, up, down = (SimpleNamespace(_at=at(d), device="cpu") for d in descs)
+    assert L.tern_q4_workspace(w, 0).numel() == 256 and L.tern_q4_experts_workspace(up, down, 0, 2).numel() >= 256
+    assert L.tern_q4_experts_workspace(up, down, 100, 2).numel() > 256
+    for m in (-1, 0x7fffffff, 1 << 31, (1 << 32) + 5):
+        with pytest.raises(ValueError):
+            L.tern_q4_workspace(w, m)
+    for u, d, m, topk in ((up, down, -1, 2), (up, down, 10, 0), (up, up, 10, 2), (up, down, 1 << 30, 2), (up, down, 1 << 32, 2),
+                          (up, down, 10, (1 << 32) + 2)):
+        with pytest.raises(ValueError):
+            L.tern_q4_experts_workspace(u, d, m, topk)
