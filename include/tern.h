@@ -483,6 +483,13 @@ tern_status tern_q4_experts(const tern_q4 *gate_up, const tern_q4 *down, const u
                             const int32_t *ids, const float *weights, int32_t topk, void *y, int32_t y_dtype,
                             void *ws, size_t ws_bytes, void *stream);
 
+/* Which kernels a call takes, for tests and measurements (host-only, no HIP
+ * call): the rows of the output tiles of tern_q4_gemm with m rows (0: the
+ * kernel for few rows), and of an expert's tiles in tern_q4_experts' first
+ * round (0: slot by slot).  -1 for arguments that the calls refuse. */
+int32_t tern_q4_tile_rows(const tern_q4 *w, int32_t m);
+int32_t tern_q4_experts_tile_rows(const tern_q4 *gate_up, const tern_q4 *down, int32_t m, int32_t topk);
+
 /* Measurement aid, not part of the product: a plain streaming read of
  * `bytes` bytes (a multiple of 16) of device memory at `buf` (16-byte
  * aligned), the attainable-bandwidth reference for the products above.

@@ -282,6 +282,19 @@ size_t tern_q4_workspace_bytes(const tern_q4* w, int32_t m) {
   return std::max<size_t>(256, plain_ws_upto(m, w));
 }
 
+int32_t tern_q4_tile_rows(const tern_q4* w, int32_t m) {
+  if (check_shape(w) != TERN_OK || check_rows(m) != TERN_OK) return -1;
+  const Route r = route_of(m, w->n, w->k, w->group);
+  return r.rows ? 0 : r.tile;
+}
+
+int32_t tern_q4_experts_tile_rows(const tern_q4* gate_up, const tern_q4* down, int32_t m, int32_t topk) {
+  if (check_experts(gate_up, down, m, topk) != TERN_OK) return -1;
+  if (m == 0) return 0;
+  const ExpertsPlan p = plan_tokens(gate_up, down, round_tokens(gate_up, down, m, topk), topk);
+  return p.direct ? 0 : p.rows;
+}
+
 tern_status tern_q4_pack(const uint8_t* q, const tern_q4* dst, void* ws, size_t ws_bytes, void* stream) {
   Q4_TRY(check_shape(dst));
   const size_t words = words_of(dst);

@@ -40,7 +40,7 @@ SYMBOLS = ["tern_row_stride", "tern_check", "tern_packed_sizes", "tern_workspace
            "tern_gemv_batched", "tern_plan_create", "tern_plan_run", "tern_plan_run_events", "tern_plan_launches", "tern_plan_destroy", "tern_b3_min_stages", "tern_gemv_noalloc",
            "tern_rotated_workspace_bytes", "tern_plan_create_rotated",
            "tern_bits", "tern_quantize", "tern_rotate", "tern_rotate_batched", "tern_q4_check", "tern_q4_pack", "tern_q4_unpack", "tern_q4_workspace_bytes", "tern_q4_gemm",
-           "tern_route", "tern_q4_experts_workspace_bytes", "tern_q4_experts",
+           "tern_route", "tern_q4_experts_workspace_bytes", "tern_q4_experts", "tern_q4_tile_rows", "tern_q4_experts_tile_rows",
            "tern_read_probe", "tern_status_str", "tern_last_error"]
 
 
@@ -117,6 +117,8 @@ def load() -> ctypes.CDLL:
         "tern_q4_experts_workspace_bytes": (c_size_t, [c_void_p, c_void_p, c_int32, c_int32]),
         "tern_q4_experts": (c_int32, [c_void_p, c_void_p, c_void_p, c_int32, c_void_p, c_void_p, c_int32, c_void_p,
                                       c_int32, c_void_p, c_size_t, c_void_p]),
+        "tern_q4_tile_rows": (c_int32, [c_void_p, c_int32]),
+        "tern_q4_experts_tile_rows": (c_int32, [c_void_p, c_void_p, c_int32, c_int32]),
         "tern_read_probe": (c_int32, [c_void_p, c_size_t, c_void_p, c_void_p]),
         "tern_status_str": (ctypes.c_char_p, [c_int32]),
         "tern_last_error": (ctypes.c_char_p, []),

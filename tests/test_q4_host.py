@@ -198,3 +198,29 @@ def test_workspaces_of_refused_sizes_are_refused():
                           (up, down, 10, (1 << 32) + 2)):
         with pytest.raises(ValueError):
             L.tern_q4_experts_workspace(u, d, m, topk)
+
+
+def test_kernels_a_call_takes():
+    """The tiles of the products and of the experts, and -1 for what is refused."""
+    lib = L.load()
+    w = q4(n=12288, k=4096, group=128)
+    assert [lib.tern_q4_tile_rows(at(w), m) for m in (0, 1, 16, 160, 400, 512)] == [0, 0, 0, 0, 96, 64]
+    tall = q4(n=131072, k=2560, group=128)
+    assert [lib.tern_q4_tile_rows(at(tall), m) for m in (1, 24, 2048)] == [0, 32, 128]
+    assert lib.tern_q4_tile_rows(at(w), -1) == -1 and lib.tern_q4_tile_rows(None, 1) == -1
+    up, down = q4(n=2048, k=2560, group=128, count=64), q4(n=2560, k=1024, group=128, count=64)
+    rows = [lib.tern_q4_experts_tile_rows(at(up), at(down), m, 8) for m in (1, 4, 8, 41, 100, 2048)]
+    assert rows == [0, 0, 8, 16, 32, 64]
+    assert lib.tern_q4_experts_tile_rows(at(up), at(up), 1, 8) == -1
+
+
+def test_matrices_past_the_tiles_buffers_stay_on_the_rows_kernel():
+    """The tile kernel holds a matrix's scales in one buffer below 2 GiB at
+    the shortest groups."""
+    lib = L.load()
+    for n, k, rows in ((1 << 20, 32640, 128), (1 << 20, 32768, 0), ((1 << 20) + 64, 32768, 0)):
+        w = q4(n=n, k=k, group=128)
+        assert lib.tern_q4_tile_rows(at(w), 2048) == rows
+    for inner, width, want in ((1 << 20, 16, 64), (1 << 20, 32736, 64), (1 << 20, 32768, 16), (1 << 14, 1 << 20, 64), (1 << 15, 1 << 20, 16)):
+        up, down = q4(n=2 * inner, k=512, group=128), q4(n=width, k=inner, group=128)
+        assert lib.tern_q4_experts_tile_rows(at(up), at(down), 100, 1) == want, (inner, width)
