@@ -468,8 +468,8 @@ tern_status tern_route(const void *logits, int32_t l_dtype, int32_t m, const ter
  * width of y ([m][n]).  Slots whose id lies outside 0..count-1 are skipped
  * (a token without any gets zeros); a token may name an expert twice.  The
  * inner values silu(g) * u are held as sums of BF16 values, the down
- * product's matrix operands: two (17 bits) above 32 slots, three (FP32's 24)
- * where a call of few slots is computed slot by slot; from 2^-50 to 2^71 in
+ * product's matrix operands: two (17 bits), or three (FP32's 24) where a call
+ * of up to 32 slots is computed slot by slot; from 2^-50 to 2^71 in
  * size, beyond which they are infinite.  A skipped slot's weight is not
  * looked at; every sum is FP32 (a token's slots in slot order, or, slot by
  * slot, as its workgroup's wavefronts share their products), and results are

@@ -160,8 +160,27 @@ tern::Q4Args args_of(const tern_q4* w) {
 
 // ---- experts
 // Few slots: every slot is a tile of its own and a token's down products are
-// summed in its own workgroup; nothing has to be sorted.
+// summed in its own workgroup; nothing has to be sorted, which saves two
+// launches, but slots that share an expert read it once each.  Taken up to 32
+// slots while what is read again, with slots spread evenly over the experts,
+// stays below 32 MB.  us slot by slot / on tiles (MB read again): 64 experts of
+// 2560 x 1024, top 8, 1 token 15 / 24 (0), 2 tokens 23 / 31 (4), 4 tokens 35 / 41
+// (22); 128 of 2048 x 768, 4 tokens 23 / 35 (7); 16 of 4096 x 1056 at group 32,
+// top 2, 4 tokens 26 / 32 (9), 8 tokens 39 / 39 (36), 16 tokens 68 / 47 (116); 8
+// of 4096 x 2048, 4 tokens 27 / 29 (32), 8 tokens 45 / 34 (111); 8 of 4096 x
+// 14336, 1 token 49 / 59 (0), 2 tokens 84 / 81 (44), 16 tokens 498 / 180 (1600); 4
+// of 1024 x 512, top 1, 16 tokens 11 / 15 (10), 32 tokens 16 / 15 (22).
 constexpr int kDirectSlots = 32;
+constexpr double kDirectAgain = 32e6;
+
+bool slot_by_slot(const tern_q4* up, const tern_q4* down, int m, int topk) {
+  const long long slots = (long long)m * topk;
+  if (slots > kDirectSlots) return false;
+  double missed = 1.0;  // the share of the experts that no token names
+  for (int t = 0; t < m; ++t) missed *= 1.0 - std::min(1.0, (double)topk / down->count);
+  const double bytes = ((double)up->n * up->k + (double)down->n * down->k) / 2;
+  return (slots - down->count * (1.0 - missed)) * bytes <= kDirectAgain || m == 1;
+}
 // Slots of one round, and bytes of its inner values and partials (but for a
 // single token's).  16384 tokens, 8 of 64 experts of 2560 x 1024: 3.62 ms in two
 // rounds, 3.61 in one of 1.8 GiB.
@@ -178,7 +197,7 @@ ExpertsPlan plan_tokens(const tern_q4* up, const tern_q4* down, int m, int topk)
   ExpertsPlan p = {};
   const int experts = down->count, inner = down->k, n = down->n;
   const size_t slots = (size_t)m * topk;
-  p.direct = slots <= (size_t)kDirectSlots;
+  p.direct = slot_by_slot(up, down, m, topk);
   // Tiles of 8 or 16 rows on the rows kernel (its tiles are a grid's y) or of
   // 32 or 64 on the tile kernel, by the rows an expert has on average; short
   // groups make the tile kernel's decoding dear.  us of a whole call, 8 / 16 /

@@ -224,3 +224,14 @@ def test_matrices_past_the_tiles_buffers_stay_on_the_rows_kernel():
     for inner, width, want in ((1 << 20, 16, 64), (1 << 20, 32736, 64), (1 << 20, 32768, 16), (1 << 14, 1 << 20, 64), (1 << 15, 1 << 20, 16)):
         up, down = q4(n=2 * inner, k=512, group=128), q4(n=width, k=inner, group=128)
         assert lib.tern_q4_experts_tile_rows(at(up), at(down), 100, 1) == want, (inner, width)
+
+
+@pytest.mark.parametrize("hidden,inner,count,topk,most", [(2560, 1024, 64, 8, 4), (4096, 14336, 8, 2, 1), (4096, 2048, 8, 2, 4), (1024, 512, 4, 1, 32),
+                                                          (65536, 65536, 1, 1, 1), (64, 64, 1024, 16, 2)])
+def test_few_slots_that_share_experts_go_to_tiles(hidden, inner, count, topk, most):
+    """Up to `most` tokens slot by slot; from there on what would be read again
+    counts for more than the launches that sorting costs."""
+    lib = L.load()
+    up, down = q4(n=2 * inner, k=hidden, group=64, count=count), q4(n=hidden, k=inner, group=64, count=count)
+    rows = [lib.tern_q4_experts_tile_rows(at(up), at(down), m, topk) for m in range(1, 50)]
+    assert not any(rows[:most]) and all(rows[most:]), rows
