@@ -391,9 +391,18 @@ hipError_t pick(int mode, const Q4Args& a, int tiles, int rows, hipStream_t s) {
   // -, 18.8, 16.6, 23.5, 18.7; at group 32, 2560 x 9728: m = 77 (480) -, 24.9,
   // 17.9, 20.1, 18.7; m = 48 (320) -, 23.4, 16.5, 17.7, 12.2; m = 24 (160) -,
   // 22.6, -, 11.1, 11.8.
+  // Seven wavefronts want K tiles: below two each four of 16 rows take less (7
+  // of 32 rows / 4 of 16, group 128, group 32: m = 32, 12288 x 256 5.4 / 4.4, 6.0
+  // / 4.6, x 1024 6.9 / 5.5, 7.4 / 6.4; m = 128, 4096 x 128 5.5 / 4.7, 5.7 / 4.9, x
+  // 1024 7.0 / 6.3, 7.3 / 7.0; m = 64, 4096 x 512 4.7 / 4.2, 5.0 / 4.4).  The
+  // other choices lie within 1.3 us of the best shape measured at K from 128 to
+  // 2048, but for m = 64, 32768 rows, where four panels of two wavefronts take 7.2
+  // against 9.4 at K = 128 and 26.2 against 29.4 at K = 2048 of group 32, and m =
+  // 128, 12288 x 2048 of group 32 (two panels of four 20.8 against 23.6).
   const long long work = (long long)panels * ((a.m + 31) / 32);
   if (work >= 1792) return launch<G, Z, 32, 4, 4, kQ4Plain>(a, tiles, s);
   if (work >= 1152) return launch<G, Z, 32, 2, 4, kQ4Plain>(a, tiles, s);
+  if (work >= 448 && T < 14) return launch<G, Z, 16, 2, 4, kQ4Plain>(a, tiles, s);
   if (work >= 448) return launch<G, Z, 32, 2, 7, kQ4Plain>(a, tiles, s);
   if (a.m <= 32) return launch<G, Z, 32, 1, 6, kQ4Plain>(a, tiles, s);
   return launch<G, Z, 16, 2, 8, kQ4Plain>(a, tiles, s);

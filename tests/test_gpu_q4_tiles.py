@@ -84,6 +84,21 @@ def test_experts_tiles(rows, group, hidden, inner, zero):
     assert (got == L.tern_q4_experts(u, d, half(x), to_dev(ids), to_dev(g), L.TERN_F32)).all(), "two runs differ"
 
 
+@pytest.mark.parametrize("zero", [False, True])
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("m,n,k", [(20, 7200, 128), (32, 12293, 896), (77, 2561, 1664), (77, 2561, 1792), (130, 1700, 512)])
+def test_short_rows_of_some_tens_of_activations(m, n, k, group, zero):
+    """Few K tiles for the wavefronts that share them: on both sides of the rule."""
+    say("short", m, n, k, group, zero)
+    rng = np.random.default_rng(m + k)
+    w = weights(rng, (), n, k, group, zero)
+    wd, x = upload(w), activations(rng, m, k)
+    assert L.load().tern_q4_tile_rows(wd._at, m) == 0
+    y, _, err = Q.gemm(*w, group, x)
+    for out in ("f32", "f16"):
+        check_rows(L.tern_q4_gemm(wd, half(x), kind_of(out)), y, err, out, "short rows")
+
+
 def far_codes(n, k, group):
     """Random codes of over 16 GiB, and rows of them as the oracle takes them."""
     import torch
