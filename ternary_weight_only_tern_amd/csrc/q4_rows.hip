@@ -277,9 +277,14 @@ __global__ __launch_bounds__(W * 64) void q4_rows_kernel(const Q4Args a, const i
               sum[i] = q4_mfma16<inner>(x[i][q], wv, sum[i]);
             }
           }
-          const float f = half_bits(s[b][j]) * (inner ? kInnerScale : 1.0f) * factor;
+          const float f = half_bits(s[b][j]) * (inner ? kInnerScale : 1.0f);
 #pragma unroll
-          for (int i = 0; i < MT; ++i) acc[i][b] += f * sum[i];
+          for (int i = 0; i < MT; ++i) {
+            if (token)  // the slot's weight last: with kInnerScale alone it could leave FP32's range
+              acc[i][b] += factor * (f * sum[i]);
+            else
+              acc[i][b] += f * sum[i];
+          }
         }
       }
     }

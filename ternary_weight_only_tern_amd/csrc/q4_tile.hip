@@ -10,10 +10,10 @@
 // down products the BF16 form, once for each of an inner value's two parts: as
 // many operations as the gate and up products, 226 against 251 us at 2048
 // tokens, 8 of 64 experts of 2560 x 1024; with one part, in FP16, 128 us, but
-// FP16's range and 11 bits).  It keeps one FP32 sum of the current group, which is scaled and added to the running
-// FP32 sum when the group ends (at group 128 one FMA per lane for every 16
-// matrix cycles).  Workgroups of one XCD take consecutive tiles, so that its
-// L2 reads each weight once.
+// FP16's range and 11 bits).  It keeps one FP32 sum of the current group, which
+// is scaled and added to the running FP32 sum when the group ends (at group 128
+// one FMA per lane for every 16 matrix cycles).  Workgroups of one XCD take
+// consecutive tiles, so that its L2 reads each weight once.
 //
 // Bound by the matrix and vector instructions together, and by what the power
 // leaves of the clock: 512 x 12288 x 4096 62.8 us, 820 TFLOP/s (the library's

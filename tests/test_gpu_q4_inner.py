@@ -72,3 +72,14 @@ def test_inner_values_past_range_are_infinite(m, topk, count):
     x = np.full((m, 128), -60000.0, np.float16)  # gate and up 1.2e14 each: inner 1.4e28
     ids = (np.arange(m * topk, dtype=np.int32) % count).reshape(m, topk)
     assert torch.isposinf(run(up, down, x, ids, np.ones((m, topk), np.float32), "f32")).all()
+
+
+@pytest.mark.parametrize("m,topk,count", ROUTES)
+@pytest.mark.parametrize("gate", [1e-30, 1e30])
+def test_weights_of_any_size(gate, m, topk, count):
+    """A slot's weight far from 1: outputs keep FP32's range."""
+    rng = np.random.default_rng(m)
+    up, down, ids, g, x = setting(rng, m, topk, count, 64, True)
+    x, g = x.astype(np.float16), (g * gate).astype(np.float32)
+    y, err = Q.experts(up, down, 64, x, ids, g, parts=2 if m * topk <= 32 else 1)
+    check(run(up, down, x, ids, g, "f32"), y, err, "f32", f"weights near {gate}")
