@@ -490,6 +490,134 @@ tern_status tern_q4_experts(const tern_q4 *gate_up, const tern_q4 *down, const u
 int32_t tern_q4_tile_rows(const tern_q4 *w, int32_t m);
 int32_t tern_q4_experts_tile_rows(const tern_q4 *gate_up, const tern_q4 *down, int32_t m, int32_t topk);
 
+/* ---- Rotary positions, an 8-bit cache of keys and values, attention over
+ * it: what stands between a decoder layer's q, k and v products and its o
+ * product, so that a layer runs through this library (tern_plan_run for q, k
+ * and v; tern_kv_write; tern_kv_attention; tern_plan_run for o).
+ *
+ * The conventions above hold: device pointers and a stream, asynchronous,
+ * status codes, no allocation, nothing kept between calls, bitwise
+ * reproducible, capturable into HIP graphs.  Rows of q, k, v and x are FP16
+ * [heads][dim], the rows `stride` elements apart (a multiple of 8, so that
+ * they may be columns of one product's output), pointers 16-byte aligned.
+ * Sums, scores, norms and angles' sines have 32 bits or more. */
+
+/* Rotary positions of a head's first `rot` elements (even; the others pass
+ * unchanged): pair i turns by the angle pos * freq[i],
+ *   (a, b) -> amp (a cos - b sin, b cos + a sin),
+ * pairs (2i, 2i+1) if interleaved, else (i, i + rot/2).  freq: device FP64
+ * [rot/2], radians per token; angles are taken to a turn in FP64.  norm: FP16
+ * [dim] or NULL; if given, x is first replaced by x norm / sqrt(mean(x^2) +
+ * eps) over the head's dim elements (any rot, also 0).  FP32 arithmetic, one
+ * rounding to FP16. */
+typedef struct tern_rotary {
+  int32_t rot, interleaved;
+  const double *freq;
+  float amp, eps;
+  const uint16_t *norm;
+} tern_rotary;
+
+/* Frequencies for tern_rotary (host arithmetic, no HIP call): writes host
+ * freq [rot/2] and *amp.  PLAIN: base^(-2i/rot).  For contexts that are
+ * `factor` times longer than the trained ones: LINEAR divides all by factor;
+ * BASE multiplies base with factor^(rot/(rot-2)); RAMP keeps the pairs that
+ * turn more than `high` times in `trained` tokens, divides those that turn
+ * less than `low` times, blends linearly by the pair's index between them
+ * (Peng et al., "YaRN", 2023), and sets amp = 0.1 ln(factor) + 1; WAVES does
+ * so linearly by the number of turns, with amp 1.  Arguments that a scaling
+ * does not name are not looked at. */
+typedef enum tern_rope_scaling {
+  TERN_ROPE_PLAIN = 0, TERN_ROPE_LINEAR = 1, TERN_ROPE_BASE = 2, TERN_ROPE_RAMP = 3, TERN_ROPE_WAVES = 4
+} tern_rope_scaling;
+tern_status tern_rope_frequencies(int32_t rot, double base, int32_t scaling, double factor, double low, double high,
+                                  int32_t trained, double *freq, float *amp);
+
+/* out = x [m][heads][dim] turned, row r by pos[r] (int32 [m], any value).
+ * dim a multiple of 8, at most 512 (TERN_E_UNSUPPORTED).  out may equal x
+ * (with the same stride). */
+tern_status tern_rope(const uint16_t *x, int64_t x_stride, int32_t m, int32_t heads, int32_t dim, const int32_t *pos,
+                      const tern_rotary *r, uint16_t *out, int64_t out_stride, void *stream);
+
+/* A cache of keys and values: pages of 64 tokens, 8-bit codes of -127..127
+ * with one FP32 scale for the 64 tokens of a (page, head), keys and values
+ * apart; a value is code * scale.  A byte is code + 128, the bytes of a (page,
+ * head) in the order of the matrix instructions' operands:
+ *   k: token 16a + 4t + i, dimension 64c + 16r + b at ((4c + t) 64 + 16r + 4a + i) 16 + b
+ *   v: token 16a + j, dimension 16c + e            at ((4c + a) 16 + e) 16 + j.
+ * dim 64, 128 or 256 (TERN_E_UNSUPPORTED).  k, v 16-byte aligned.  Scales are
+ * 0, NaN or in 2^-60 .. 2^60 (tern_kv_write's are). */
+#define TERN_KV_PAGE 64
+typedef struct tern_kv {
+  int32_t heads, dim, pages;
+  uint8_t *k, *v;           /* [pages][heads][64 * dim] */
+  float *k_scale, *v_scale; /* [pages][heads] */
+} tern_kv;
+
+/* Host-only check of a descriptor.  Makes no HIP call. */
+tern_status tern_kv_check(const tern_kv *c);
+
+/* The rows of a call and the sequences they belong to.  Sequence s has the
+ * rows start[s] .. start[s+1]-1 (start NULL: max_rows each, rows = count *
+ * max_rows), n of them, and len[s] tokens, its n last ones being those rows:
+ * row j stands at position len[s] - n + j.  Token t lies in page pages[s][t /
+ * 64].  A number outside 0 .. (the cache's pages) - 1 names no page, and so do
+ * tokens behind the table's end: their rows are not written, read as zeros,
+ * and attention passes over them.  len may be less than n (an unused place of a batch):
+ * a row whose position is negative is not written, reads as zeros and attends
+ * to nothing.  len, start and pages are device arrays, so that a captured
+ * call may be replayed for other lengths; max_rows (rows of a sequence beyond
+ * it are left out) and max_len (for the choice of kernels only) are bounds that
+ * the host knows.  Outputs' rows that belong to no sequence are left as they
+ * were.  rows and max_rows at most 2^29, len at most 2^30. */
+typedef struct tern_kv_batch {
+  int32_t count, rows, max_rows, max_len, max_pages;
+  const int32_t *start; /* [count+1], or NULL */
+  const int32_t *len;   /* [count] */
+  const int32_t *pages; /* [count][max_pages] */
+} tern_kv_batch;
+
+/* Writes rows of k and v ([rows][heads][dim]) at their positions, k turned
+ * first where rope is given (and rounded to FP16, as by tern_rope).  A (page,
+ * head) whose first token is among the rows, or whose scale is 0, takes the
+ * scale max|x| / 127 over the rows in it, rounded up to 8 significant bits; any
+ * other doubles its scale until the rows fit and rounds the codes it holds
+ * again (all roundings of a value together stay below one step of its last
+ * scale).  A code is x / scale, rounded to nearest even.  An infinity or a
+ * NaN among the rows makes the scale NaN: the page's tokens of that head read
+ * as NaN until its first token is written again.  A sequence's tokens are
+ * written in order from the first of a page on; a page that is written belongs to
+ * one sequence.  q: NULL, or rows that are turned in the same launch,
+ * q_out [rows][q_heads][dim], by q_rope at the same positions; q_out may equal
+ * q. */
+tern_status tern_kv_write(const tern_kv *c, const tern_kv_batch *b, const uint16_t *k, int64_t k_stride,
+                          const uint16_t *v, int64_t v_stride, const tern_rotary *rope, const uint16_t *q,
+                          int64_t q_stride, int32_t q_heads, const tern_rotary *q_rope, uint16_t *q_out, void *stream);
+
+/* The values of the rows' tokens back, [rows][heads][dim] in FP16 (nearest
+ * even) or FP32 (exact); k or v NULL: not wanted. */
+tern_status tern_kv_read(const tern_kv *c, const tern_kv_batch *b, void *k, void *v, int32_t dtype, void *stream);
+
+/* y[r][h] = sum_t softmax_t(scale q[r][h] . k_t) v_t over the tokens that row r
+ * sees: causal, those up to its own position, with a window the last `window`
+ * of them (0: all); not causal, all len of its sequence (an encoder's states,
+ * say; the rows then need no place in the cache).  Query heads h * g .. h * g +
+ * g - 1 share cache head h, g = q_heads / heads.  y FP16 [rows][q_heads][dim];
+ * a row that sees nothing is 0.  Tokens that a row does not see do not reach
+ * it, whatever they or their scales hold.  Scores and sums are FP32; the
+ * softmax's weights meet the codes of v in FP16 (11 bits each).  scale finite,
+ * not negative.  ws: tern_kv_attention_workspace_bytes (0 for arguments that
+ * are refused), 16-byte aligned, enough for every batch with no more rows and
+ * no larger max_len too; calls that overlap in time must not share it. */
+size_t tern_kv_attention_workspace_bytes(const tern_kv *c, const tern_kv_batch *b, int32_t q_heads);
+tern_status tern_kv_attention(const tern_kv *c, const tern_kv_batch *b, const uint16_t *q, int64_t q_stride,
+                              int32_t q_heads, float scale, int32_t window, int32_t causal, uint16_t *y, void *ws,
+                              size_t ws_bytes, void *stream);
+
+/* Which way an attention call goes, for tests and measurements (host-only):
+ * the parts the context is cut into, P, on the kernel for few rows, -1 - P on
+ * tiles; 0: nothing to do; -1: refused. */
+int32_t tern_kv_attention_parts(const tern_kv *c, const tern_kv_batch *b, int32_t q_heads, int32_t window);
+
 /* Measurement aid, not part of the product: a plain streaming read of
  * `bytes` bytes (a multiple of 16) of device memory at `buf` (16-byte
  * aligned), the attainable-bandwidth reference for the products above.

@@ -1,0 +1,252 @@
+// Declarations and device code shared by the kernels of rotary positions, the
+// 8-bit cache and attention over it (rope.hip, kv_*.hip).  Not part of the
+// public ABI.
+//
+// A page holds 64 tokens of one head, 64 D bytes of keys and as many of
+// values, in the order in which the matrix cores' operands take them: a
+// wavefront that loads 16 consecutive bytes a lane has the operand of
+// v_mfma_f32_16x16x32_f16 in its registers, without LDS or shuffles.
+//   keys    token 16a + 4t + i, dimension 64c + 16r + b  at  ((4c + t) 64 + 16r + 4a + i) 16 + b
+//   values  token 16a + j, dimension 16c + e             at  ((4c + a) 16 + e) 16 + j
+// (c for a chunk of dimensions).  The product of keys and queries leaves lane
+// group a of a row with the scores of tokens 16a + 4t + i, and the same lane
+// group holds the values of tokens 16a .. 16a + 15: the weights go from the
+// first product into the second without leaving their lane.
+// A byte is code + 128, so that 0x6400 | byte is the FP16 number 1024 + 128 +
+// code: decoding is one byte permutation and one packed subtraction for two
+// codes, exact.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "tern.h"
+
+namespace tern {
+
+constexpr int kPage = TERN_KV_PAGE;
+// Positions and rows stay below these, so that their sums fit 32 bits.
+constexpr int kMaxTokens = 1 << 30, kMaxRows = 1 << 29;
+
+// Turning and norm of a head's values (tern_rotary).
+struct Rotary {
+  const double* freq;
+  const uint16_t* norm;
+  float amp, eps;
+  int32_t rot, inter;
+  int32_t on;  // 0: values pass unchanged
+};
+
+struct RopeArgs {
+  const uint16_t* x;
+  uint16_t* out;
+  int64_t x_stride, out_stride;
+  const int32_t* pos;
+  Rotary r;
+  int32_t m, heads, dim;
+};
+
+// Which rows belong to which sequence (tern_kv_batch).
+struct Batch {
+  const int32_t *start, *len, *pages;
+  int32_t count, rows, max_rows, max_pages;
+};
+
+struct Cache {
+  uint8_t *k, *v;
+  float *ks, *vs;
+  int32_t heads, pages;
+};
+
+struct WriteArgs {
+  Cache c;
+  Batch b;
+  const uint16_t *k, *v, *q;
+  uint16_t* q_out;
+  int64_t k_stride, v_stride, q_stride;
+  Rotary rk, rq;
+  int32_t q_heads;
+  int32_t items;       // pages that a sequence's rows may lie in
+  int32_t kv_blocks;   // workgroups before those of q
+};
+
+struct ReadArgs {
+  Cache c;
+  Batch b;
+  void *k, *v;
+  int32_t f32, items;
+};
+
+struct AttnArgs {
+  Cache c;
+  Batch b;
+  const uint16_t* q;
+  int64_t q_stride;
+  uint16_t* y;         // [rows][q_heads][dim]
+  float* part;         // [splits][rows][q_heads][dim], then [splits][rows][q_heads][2]
+  float scale;         // times log2(e)
+  int32_t q_heads, group, window, causal;
+  int32_t splits, tiles;
+};
+
+// Rows (of a sequence, times the query heads of one cache head) of one
+// workgroup: the kernel for few rows, by blocks of 16, and the tiles.
+constexpr int kAttnFew = 16, kAttnTile = 128;
+
+hipError_t launch_rope(const RopeArgs& a, hipStream_t s);
+hipError_t launch_kv_write(const WriteArgs& a, int dim, hipStream_t s);
+hipError_t launch_kv_read(const ReadArgs& a, int dim, hipStream_t s);
+// blocks: of 16 rows, 1, 2 or 4 (2 at most at dim 256)
+hipError_t launch_attn_rows(const AttnArgs& a, int dim, int blocks, hipStream_t s);
+hipError_t launch_attn_tile(const AttnArgs& a, int dim, hipStream_t s);
+hipError_t launch_attn_join(const AttnArgs& a, int dim, hipStream_t s);
+
+// A grid's threads have to be countable in 32 bits.
+inline bool kv_grid_fits(long long blocks, int threads) { return blocks * threads < (1ll << 32); }
+
+// ---------------------------------------------------------------- device code
+#ifdef __HIPCC__
+typedef _Float16 kh2_t __attribute__((ext_vector_type(2)));
+typedef _Float16 kh4_t __attribute__((ext_vector_type(4)));
+typedef _Float16 kh8_t __attribute__((ext_vector_type(8)));
+typedef float kf4_t __attribute__((ext_vector_type(4)));
+typedef float kf16_t __attribute__((ext_vector_type(16)));
+typedef uint32_t kw2_t __attribute__((ext_vector_type(2)));
+typedef uint32_t kw4_t __attribute__((ext_vector_type(4)));
+
+// A sequence's rows in the arrays of rows and its place in the cache.  Rows
+// beyond max_rows or behind the arrays' end are left out, whatever start says.
+struct Span {
+  int first, n;  // rows that are there
+  int from;      // position of the first row; negative: rows before the sequence's beginning
+  int len;       // tokens, 0 at least
+};
+__device__ inline Span span_of(const Batch& b, int s) {
+  Span r;
+  int n = b.max_rows;
+  r.first = s * b.max_rows;
+  if (b.start) {
+    r.first = min(max(b.start[s], 0), b.rows);
+    n = min(max(b.start[s + 1] - r.first, 0), b.rows - r.first);
+  }
+  r.n = min(n, b.max_rows);
+  r.len = min(max(b.len[s], 0), kMaxTokens);
+  r.from = r.len - n;
+  return r;
+}
+
+// The page of a sequence's tokens 64 p ..; -1: none.
+__device__ inline int page_of(const Batch& b, const Cache& c, int s, int p) {
+  if (p >= b.max_pages) return -1;
+  const int id = b.pages[(size_t)s * b.max_pages + p];
+  return id >= 0 && id < c.pages ? id : -1;
+}
+
+// Four bytes code + 128 to FP16 codes.
+__device__ inline void codes4(uint32_t w, kh2_t& lo, kh2_t& hi) {
+  const kh2_t bias = {(_Float16)-1152.0f, (_Float16)-1152.0f};
+  lo = __builtin_bit_cast(kh2_t, __builtin_amdgcn_perm(0x64646464u, w, 0x04010400u)) + bias;
+  hi = __builtin_bit_cast(kh2_t, __builtin_amdgcn_perm(0x64646464u, w, 0x04030402u)) + bias;
+}
+__device__ inline kh8_t codes8(uint32_t w0, uint32_t w1) {
+  kh2_t a, b, c, d;
+  codes4(w0, a, b);
+  codes4(w1, c, d);
+  return kh8_t{a.x, a.y, b.x, b.y, c.x, c.y, d.x, d.y};
+}
+
+__device__ inline float kv_half(uint16_t v) { return (float)__builtin_bit_cast(_Float16, v); }
+
+// cos and sin of the angle pos * freq, times amp.  The angle is taken to a
+// turn in FP64 (2^31 turns would still leave 2^-22 of a turn).
+__device__ inline void angle_of(double pos, double freq, float amp, float& c, float& s) {
+  const double turns = pos * freq * 0.15915494309189533577;
+  const float t = (float)(turns - rint(turns));
+  c = amp * __builtin_amdgcn_cosf(t);
+  s = amp * __builtin_amdgcn_sinf(t);
+}
+
+// N (8 or 16) consecutive values of a head from dimension d0 on, normed and
+// turned, in FP32, the same bits for either N (the norm's sum is a tree over
+// eights, and every product and sum is spelled out).  All lanes of the head (`lanes` of them, a power of two,
+// neighbours) call it together; those without values have live false.  x is
+// 16-byte aligned.
+template <int N>
+__device__ inline void turned(const uint16_t* x, int d0, int dim, bool live, int lanes, const Rotary& r, int pos, float* y) {
+  union Row {
+    kw4_t w[N / 8];
+    uint16_t h[N];
+  };
+  Row v = {}, w = {};
+  if (live)
+    for (int i = 0; i < N / 8; ++i) v.w[i] = *reinterpret_cast<const kw4_t*>(x + d0 + 8 * i);
+#pragma unroll
+  for (int e = 0; e < N; ++e) y[e] = kv_half(v.h[e]);
+  if (!r.on) return;
+  float inv = 1.0f;
+  if (r.norm) {
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < N; i += 8) {
+      float eight = 0.f;
+#pragma unroll
+      for (int e = i; e < i + 8; ++e) eight = __builtin_fmaf(y[e], y[e], eight);
+      sum += eight;
+    }
+    for (int o = 1; o < lanes; o <<= 1) sum += __shfl_xor(sum, o);
+    inv = 1.0f / sqrtf(sum / dim + r.eps);
+    if (live)
+      for (int i = 0; i < N / 8; ++i) w.w[i] = *reinterpret_cast<const kw4_t*>(r.norm + d0 + 8 * i);
+#pragma unroll
+    for (int e = 0; e < N; ++e) y[e] = (inv * kv_half(w.h[e])) * y[e];
+  }
+  if (!live || d0 >= r.rot) return;
+  const double at = (double)pos;
+  float c, s;
+  if (r.inter) {
+#pragma unroll
+    for (int e = 0; e < N; e += 2) {
+      if (d0 + e >= r.rot) break;
+      angle_of(at, r.freq[(d0 + e) / 2], r.amp, c, s);
+      const float a = y[e], b = y[e + 1];
+      y[e] = __builtin_fmaf(a, c, -(b * s));
+      y[e + 1] = __builtin_fmaf(b, c, a * s);
+    }
+    return;
+  }
+  // pairs (i, i + rot / 2): the other one is another lane's
+  const int half = r.rot / 2;
+  if (half % N == 0) {
+    const bool low = d0 < half;
+    const int other = low ? d0 + half : d0 - half, i0 = low ? d0 : d0 - half;
+    for (int i = 0; i < N / 8; ++i) v.w[i] = *reinterpret_cast<const kw4_t*>(x + other + 8 * i);
+    if (r.norm)
+      for (int i = 0; i < N / 8; ++i) w.w[i] = *reinterpret_cast<const kw4_t*>(r.norm + other + 8 * i);
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+      float o = kv_half(v.h[e]);
+      if (r.norm) o = (inv * kv_half(w.h[e])) * o;
+      angle_of(at, r.freq[i0 + e], r.amp, c, s);
+      y[e] = low ? __builtin_fmaf(y[e], c, -(o * s)) : __builtin_fmaf(y[e], c, o * s);
+    }
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < N; ++e) {
+    const int d = d0 + e;
+    if (d >= r.rot) break;
+    const bool low = d < half;
+    const int other = low ? d + half : d - half;
+    float o = kv_half(x[other]);
+    if (r.norm) o = (inv * kv_half(r.norm[other])) * o;
+    angle_of(at, r.freq[low ? d : d - half], r.amp, c, s);
+    y[e] = low ? __builtin_fmaf(y[e], c, -(o * s)) : __builtin_fmaf(y[e], c, o * s);
+  }
+}
+
+// Bits of the FP16 value nearest to v.
+__device__ inline uint16_t kv_bits(float v) { return __builtin_bit_cast(uint16_t, (_Float16)v); }
+#endif
+
+}  // namespace tern

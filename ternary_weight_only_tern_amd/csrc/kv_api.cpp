@@ -1,0 +1,349 @@
+// Host half of the C ABI of rotary positions, the 8-bit cache and attention
+// over it (tern_rope*, tern_kv_* in tern.h): argument checks, workspace
+// sizing, choice of kernel and launches.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdarg>
+#include <cstdio>
+
+#include "internal.h"
+#include "kv.h"
+
+namespace {
+
+tern_status fail(tern_status s, const char* fmt, ...) {
+  char msg[512];
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(msg, sizeof(msg), fmt, ap);
+  va_end(ap);
+  return tern::record_failure(s, msg);
+}
+
+// A launch that would need too large a grid is not made, and says so.
+#define KV_HIP(call)                                                                                                \
+  do {                                                                                                              \
+    hipError_t e_ = (call);                                                                                         \
+    if (e_ == hipErrorInvalidConfiguration) return fail(TERN_E_UNSUPPORTED, "the call needs too many workgroups"); \
+    if (e_ != hipSuccess) return fail(TERN_E_HIP, "%s: %s", #call, hipGetErrorString(e_));                          \
+  } while (0)
+
+#define KV_TRY(expr)              \
+  do {                            \
+    tern_status s_ = (expr);      \
+    if (s_ != TERN_OK) return s_; \
+  } while (0)
+
+tern_status check_ptr(const void* p, const char* name, size_t align) {
+  if (!p) return fail(TERN_E_INVAL, "%s is NULL", name);
+  if (reinterpret_cast<uintptr_t>(p) & (align - 1)) return fail(TERN_E_ALIGN, "%s is not %zu-byte aligned", name, align);
+  return TERN_OK;
+}
+
+// Rows of heads, `stride` elements apart.
+tern_status check_rows(const void* p, int64_t stride, const char* name) {
+  KV_TRY(check_ptr(p, name, 16));
+  if (stride < 0) return fail(TERN_E_INVAL, "%s has the row stride %lld", name, (long long)stride);
+  if (stride % 8) return fail(TERN_E_ALIGN, "%s has the row stride %lld, not a multiple of 8", name, (long long)stride);
+  return TERN_OK;
+}
+
+tern_status check_rotary(const tern_rotary* r, int dim, const char* name) {
+  if (r->rot < 0 || r->rot > dim || r->rot % 2)
+    return fail(TERN_E_INVAL, "%s turns %d of %d elements", name, r->rot, dim);
+  if (r->rot) KV_TRY(check_ptr(r->freq, "freq", 8));
+  if (r->norm) KV_TRY(check_ptr(r->norm, "norm", 16));
+  return TERN_OK;
+}
+
+tern::Rotary rotary_of(const tern_rotary* r) {
+  tern::Rotary o = {};
+  if (!r) return o;
+  o.freq = r->freq;
+  o.norm = r->norm;
+  o.amp = r->amp;
+  o.eps = r->eps;
+  o.rot = r->rot;
+  o.inter = r->interleaved != 0;
+  o.on = 1;
+  return o;
+}
+
+tern_status check_shape(const tern_kv* c) {
+  if (!c) return fail(TERN_E_INVAL, "cache descriptor is NULL");
+  if (c->heads < 1 || c->pages < 0) return fail(TERN_E_INVAL, "cache of %d heads, %d pages", c->heads, c->pages);
+  if (c->dim != 64 && c->dim != 128 && c->dim != 256)
+    return fail(TERN_E_UNSUPPORTED, "head size %d is not 64, 128 or 256", c->dim);
+  if (c->heads > 65535) return fail(TERN_E_UNSUPPORTED, "%d heads: 65535 at most", c->heads);
+  return TERN_OK;
+}
+
+tern_status check_cache(const tern_kv* c) {
+  KV_TRY(check_shape(c));
+  if (!c->pages) return TERN_OK;
+  KV_TRY(check_ptr(c->k, "k", 16));
+  KV_TRY(check_ptr(c->v, "v", 16));
+  KV_TRY(check_ptr(c->k_scale, "k_scale", 4));
+  return check_ptr(c->v_scale, "v_scale", 4);
+}
+
+tern_status check_sizes(const tern_kv_batch* b) {
+  if (!b) return fail(TERN_E_INVAL, "batch descriptor is NULL");
+  if (b->count < 0 || b->rows < 0 || b->max_rows < 0 || b->max_len < 0 || b->max_pages < 0)
+    return fail(TERN_E_INVAL, "batch of count=%d rows=%d max_rows=%d max_len=%d max_pages=%d", b->count, b->rows,
+                b->max_rows, b->max_len, b->max_pages);
+  if (b->rows > tern::kMaxRows || b->max_rows > tern::kMaxRows)
+    return fail(TERN_E_UNSUPPORTED, "%d rows, %d of a sequence: %d at most", b->rows, b->max_rows, tern::kMaxRows);
+  return TERN_OK;
+}
+
+tern_status check_batch(const tern_kv_batch* b) {
+  KV_TRY(check_sizes(b));
+  if (!b->start && (long long)b->count * b->max_rows != b->rows)
+    return fail(TERN_E_INVAL, "%d sequences of %d rows are not %d rows", b->count, b->max_rows, b->rows);
+  return TERN_OK;
+}
+
+// Whether a call has nothing to do.
+bool nothing(const tern_kv_batch* b) { return !b->count || !b->rows || !b->max_rows; }
+
+// The arrays of a batch with rows.
+tern_status check_arrays(const tern_kv* c, const tern_kv_batch* b) {
+  if (!c->pages) return fail(TERN_E_INVAL, "the cache has no pages");
+  KV_TRY(check_cache(c));
+  KV_TRY(check_ptr(b->len, "len", 4));
+  if (b->start) KV_TRY(check_ptr(b->start, "start", 4));
+  if (b->max_pages) KV_TRY(check_ptr(b->pages, "pages", 4));
+  return TERN_OK;
+}
+
+tern::Cache cache_of(const tern_kv* c) { return {c->k, c->v, c->k_scale, c->v_scale, c->heads, c->pages}; }
+tern::Batch batch_of(const tern_kv_batch* b) {
+  return {b->start, b->len, b->pages, b->count, b->rows, b->max_rows, b->max_pages};
+}
+
+// Pages that a sequence's rows may lie in.
+int items_of(const tern_kv_batch* b) { return (b->max_rows + 2 * (tern::kPage - 1)) / tern::kPage; }
+
+// How attention runs.
+struct AttnPlan {
+  int blocks;  // of 16 rows in the kernel for few rows; 0: tiles
+  int tiles, splits;
+};
+constexpr int kPartPages = 4;       // the least of a part
+constexpr int kRowsTarget = 1024;   // workgroups
+constexpr int kTileTarget = 512;
+constexpr int kPartRows = 2 * kRowsTarget * 64;  // rows of all parts at most, either way (plan_of)
+
+int pages_of(const tern_kv_batch* b, int window) {
+  long long tokens = b->max_len;
+  if (window > 0) tokens = std::min<long long>(tokens, (long long)window + b->max_rows + tern::kPage);
+  return (int)((tokens + tern::kPage - 1) / tern::kPage);
+}
+
+AttnPlan plan_of(const tern_kv* c, const tern_kv_batch* b, int group, int window) {
+  AttnPlan p = {};
+  const long long rows = (long long)b->max_rows * group;
+  const int most = c->dim == 256 ? 32 : 64;
+  if (rows <= most) p.blocks = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
+  p.tiles = p.blocks ? 1 : (int)((rows + tern::kAttnTile - 1) / tern::kAttnTile);
+  const long long groups = (long long)p.tiles * c->heads * b->count;
+  const int target = p.blocks ? kRowsTarget : kTileTarget;
+  p.splits = 1;
+  if (groups < target / 2)
+    p.splits = (int)std::max<long long>(1, std::min<long long>((target + groups - 1) / groups, pages_of(b, window) / kPartPages));
+  return p;
+}
+
+size_t attn_need(const AttnPlan& p, const tern_kv* c, const tern_kv_batch* b, int q_heads) {
+  return p.splits > 1 ? (size_t)p.splits * b->rows * q_heads * (c->dim + 2) * 4 : 0;
+}
+
+tern_status check_heads(const tern_kv* c, const tern_kv_batch* b, int q_heads) {
+  if (q_heads < 1 || q_heads % c->heads)
+    return fail(TERN_E_INVAL, "%d query heads over %d cache heads", q_heads, c->heads);
+  if (q_heads > (1 << 20) || (long long)b->max_rows * (q_heads / c->heads) > (1 << 30))
+    return fail(TERN_E_UNSUPPORTED, "%d query heads, %d rows of a sequence: too many", q_heads, b->max_rows);
+  return TERN_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+tern_status tern_rope_frequencies(int32_t rot, double base, int32_t scaling, double factor, double low, double high,
+                                  int32_t trained, double* freq, float* amp) {
+  if (rot < 0 || rot % 2) return fail(TERN_E_INVAL, "rot=%d must be even", rot);
+  if (!(base > 1.0) || !std::isfinite(base)) return fail(TERN_E_INVAL, "base=%g must be above 1", base);
+  if (rot && !freq) return fail(TERN_E_INVAL, "freq is NULL");
+  if (!amp) return fail(TERN_E_INVAL, "amp is NULL");
+  if (scaling < TERN_ROPE_PLAIN || scaling > TERN_ROPE_WAVES) return fail(TERN_E_UNSUPPORTED, "unknown scaling %d", scaling);
+  if (scaling != TERN_ROPE_PLAIN && (!(factor >= 1.0) || !std::isfinite(factor)))
+    return fail(TERN_E_INVAL, "factor=%g must be 1 or more", factor);
+  const bool bands = scaling == TERN_ROPE_RAMP || scaling == TERN_ROPE_WAVES;
+  if (bands && (!(low > 0.0) || !(high > low) || !std::isfinite(high) || trained < 1))
+    return fail(TERN_E_INVAL, "low=%g, high=%g, trained=%d: 0 < low < high and a length are wanted", low, high, trained);
+  const double turn = 2.0 * M_PI;
+  if (scaling == TERN_ROPE_BASE && rot > 2) base *= std::pow(factor, (double)rot / (rot - 2));
+  // the pair (as a real number) that turns `turns` times in the trained length
+  auto pair_of = [&](double turns) { return 0.5 * rot * std::log(trained / (turns * turn)) / std::log(base); };
+  const double first = bands ? std::max(0.0, std::floor(pair_of(high))) : 0.0;
+  const double last = bands ? std::min(rot - 1.0, std::ceil(pair_of(low))) : 0.0;
+  for (int i = 0; i < rot / 2; ++i) {
+    const double f = std::pow(base, -2.0 * i / rot);
+    double keep = 1.0;  // of f; the rest is f / factor
+    if (scaling == TERN_ROPE_LINEAR) keep = 0.0;
+    if (scaling == TERN_ROPE_RAMP) keep = 1.0 - std::min(1.0, std::max(0.0, (i - first) / std::max(last - first, 1e-3)));
+    if (scaling == TERN_ROPE_WAVES) keep = std::min(1.0, std::max(0.0, (trained * f / turn - low) / (high - low)));
+    freq[i] = f * keep + f / (scaling == TERN_ROPE_BASE ? 1.0 : factor) * (1.0 - keep);
+    if (keep == 1.0) freq[i] = f;
+  }
+  *amp = scaling == TERN_ROPE_RAMP ? (float)(0.1 * std::log(factor) + 1.0) : 1.0f;
+  return TERN_OK;
+}
+
+tern_status tern_rope(const uint16_t* x, int64_t x_stride, int32_t m, int32_t heads, int32_t dim, const int32_t* pos,
+                      const tern_rotary* r, uint16_t* out, int64_t out_stride, void* stream) {
+  if (m < 0 || heads < 0 || dim < 0) return fail(TERN_E_INVAL, "m=%d heads=%d dim=%d", m, heads, dim);
+  if (dim % 8 || dim > 512) return fail(TERN_E_UNSUPPORTED, "head size %d is no multiple of 8 up to 512", dim);
+  if (!r) return fail(TERN_E_INVAL, "rotary descriptor is NULL");
+  if (!m || !heads || !dim) return TERN_OK;
+  KV_TRY(check_rows(x, x_stride, "x"));
+  KV_TRY(check_rows(out, out_stride, "out"));
+  KV_TRY(check_ptr(pos, "pos", 4));
+  KV_TRY(check_rotary(r, dim, "rotary"));
+  tern::RopeArgs a = {};
+  a.x = x;
+  a.out = out;
+  a.x_stride = x_stride;
+  a.out_stride = out_stride;
+  a.pos = pos;
+  a.r = rotary_of(r);
+  a.m = m;
+  a.heads = heads;
+  a.dim = dim;
+  KV_HIP(tern::launch_rope(a, (hipStream_t)stream));
+  return TERN_OK;
+}
+
+tern_status tern_kv_check(const tern_kv* c) { return check_cache(c); }
+
+tern_status tern_kv_write(const tern_kv* c, const tern_kv_batch* b, const uint16_t* k, int64_t k_stride,
+                          const uint16_t* v, int64_t v_stride, const tern_rotary* rope, const uint16_t* q,
+                          int64_t q_stride, int32_t q_heads, const tern_rotary* q_rope, uint16_t* q_out, void* stream) {
+  KV_TRY(check_shape(c));
+  KV_TRY(check_batch(b));
+  if (rope) KV_TRY(check_rotary(rope, c->dim, "rope"));
+  if (q) {
+    if (!q_rope) return fail(TERN_E_INVAL, "q_rope is NULL");
+    KV_TRY(check_rotary(q_rope, c->dim, "q_rope"));
+    if (q_heads < 0 || q_heads > (1 << 20)) return fail(TERN_E_INVAL, "%d query heads", q_heads);
+  }
+  if (nothing(b)) return TERN_OK;
+  KV_TRY(check_arrays(c, b));
+  KV_TRY(check_rows(k, k_stride, "k"));
+  KV_TRY(check_rows(v, v_stride, "v"));
+  if (q && q_heads) {
+    KV_TRY(check_rows(q, q_stride, "q"));
+    KV_TRY(check_ptr(q_out, "q_out", 16));
+  }
+  tern::WriteArgs a = {};
+  a.c = cache_of(c);
+  a.b = batch_of(b);
+  a.k = k;
+  a.v = v;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.rk = rotary_of(rope);
+  if (q && q_heads) {
+    a.q = q;
+    a.q_out = q_out;
+    a.q_stride = q_stride;
+    a.q_heads = q_heads;
+    a.rq = rotary_of(q_rope);
+  }
+  a.items = items_of(b);
+  const long long blocks = 2ll * b->count * a.items * c->heads;
+  if (!tern::kv_grid_fits(blocks, 256)) return fail(TERN_E_UNSUPPORTED, "the call needs too many workgroups");
+  a.kv_blocks = (int)blocks;
+  KV_HIP(tern::launch_kv_write(a, c->dim, (hipStream_t)stream));
+  return TERN_OK;
+}
+
+tern_status tern_kv_read(const tern_kv* c, const tern_kv_batch* b, void* k, void* v, int32_t dtype, void* stream) {
+  KV_TRY(check_shape(c));
+  KV_TRY(check_batch(b));
+  if (dtype != TERN_F16 && dtype != TERN_F32) return fail(TERN_E_UNSUPPORTED, "unknown output dtype %d", dtype);
+  if (nothing(b) || (!k && !v)) return TERN_OK;
+  KV_TRY(check_arrays(c, b));
+  if (k) KV_TRY(check_ptr(k, "k", 16));
+  if (v) KV_TRY(check_ptr(v, "v", 16));
+  tern::ReadArgs a = {};
+  a.c = cache_of(c);
+  a.b = batch_of(b);
+  a.k = k;
+  a.v = v;
+  a.f32 = dtype == TERN_F32;
+  a.items = items_of(b);
+  KV_HIP(tern::launch_kv_read(a, c->dim, (hipStream_t)stream));
+  return TERN_OK;
+}
+
+size_t tern_kv_attention_workspace_bytes(const tern_kv* c, const tern_kv_batch* b, int32_t q_heads) {
+  if (check_shape(c) != TERN_OK || check_sizes(b) != TERN_OK || check_heads(c, b, q_heads) != TERN_OK) return 0;
+  const long long parts = std::max(1, pages_of(b, 0) / kPartPages);
+  const double rows = (double)b->rows * q_heads * parts;
+  return (size_t)std::max(256.0, std::min(rows, (double)kPartRows) * (c->dim + 2) * 4);
+}
+
+int32_t tern_kv_attention_parts(const tern_kv* c, const tern_kv_batch* b, int32_t q_heads, int32_t window) {
+  if (check_shape(c) != TERN_OK || check_sizes(b) != TERN_OK || check_heads(c, b, q_heads) != TERN_OK || window < 0) return -1;
+  if (nothing(b)) return 0;
+  const AttnPlan p = plan_of(c, b, q_heads / c->heads, window);
+  return p.blocks ? p.splits : -1 - p.splits;
+}
+
+tern_status tern_kv_attention(const tern_kv* c, const tern_kv_batch* b, const uint16_t* q, int64_t q_stride,
+                              int32_t q_heads, float scale, int32_t window, int32_t causal, uint16_t* y, void* ws,
+                              size_t ws_bytes, void* stream) {
+  KV_TRY(check_shape(c));
+  KV_TRY(check_batch(b));
+  KV_TRY(check_heads(c, b, q_heads));
+  if (!(scale >= 0.0f) || !std::isfinite(scale)) return fail(TERN_E_INVAL, "scale=%g must be finite and not negative", scale);
+  if (window < 0) return fail(TERN_E_INVAL, "window=%d must not be negative", window);
+  if (window && !causal) return fail(TERN_E_UNSUPPORTED, "a window needs causal rows");
+  if (nothing(b)) return TERN_OK;
+  KV_TRY(check_arrays(c, b));
+  KV_TRY(check_rows(q, q_stride, "q"));
+  KV_TRY(check_ptr(y, "y", 16));
+  const AttnPlan p = plan_of(c, b, q_heads / c->heads, window);
+  const size_t need = attn_need(p, c, b, q_heads);
+  if (need && (!ws || ws_bytes < need))
+    return fail(TERN_E_WORKSPACE, "workspace of %zu bytes, %zu are needed", ws ? ws_bytes : (size_t)0, need);
+  if (need) KV_TRY(check_ptr(ws, "workspace", 16));
+  tern::AttnArgs a = {};
+  a.c = cache_of(c);
+  a.b = batch_of(b);
+  a.q = q;
+  a.q_stride = q_stride;
+  a.y = y;
+  a.part = (float*)ws;
+  a.scale = scale * (float)M_LOG2E;
+  a.q_heads = q_heads;
+  a.group = q_heads / c->heads;
+  a.window = window;
+  a.causal = causal != 0;
+  a.splits = p.splits;
+  a.tiles = p.tiles;
+  const hipStream_t s = (hipStream_t)stream;
+  if (p.blocks)
+    KV_HIP(tern::launch_attn_rows(a, c->dim, p.blocks, s));
+  else
+    KV_HIP(tern::launch_attn_tile(a, c->dim, s));
+  if (a.splits > 1) KV_HIP(tern::launch_attn_join(a, c->dim, s));
+  return TERN_OK;
+}
+
+}  // extern "C"

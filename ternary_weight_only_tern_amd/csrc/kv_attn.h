@@ -1,0 +1,93 @@
+// Device code shared by the attention kernels: what a workgroup looks at, and
+// the running softmax of a row (q. v. kv_attn_rows.hip).
+#pragma once
+
+#include "kv.h"
+
+namespace tern {
+
+#ifdef __HIPCC__
+// Pages [begin, end) that the rows at positions first..last see.
+struct Range {
+  int begin, end;
+};
+__device__ inline Range range_of(const AttnArgs& a, const Span& sp, int first, int last) {
+  const int end = min(a.causal ? last + 1 : sp.len, sp.len);
+  const int begin = a.window > 0 ? max(first - a.window + 1, 0) : 0;
+  Range r = {begin / kPage, min((end + kPage - 1) / kPage, a.b.max_pages)};
+  if ((a.causal && last < 0) || r.end < r.begin) r.end = r.begin;
+  return r;
+}
+
+// This workgroup's part of them, all wavefronts'.
+__device__ inline Range part_of(const Range& r, int split, int splits) {
+  const long long n = r.end - r.begin;
+  return {r.begin + (int)(n * split / splits), r.begin + (int)(n * (split + 1) / splits)};
+}
+
+// Tokens [low, high) that the row at position pos sees.
+struct Sees {
+  int low, high;
+};
+__device__ inline Sees sees_of(const AttnArgs& a, const Span& sp, int pos, bool there) {
+  Sees s = {a.window > 0 ? max(pos - a.window + 1, 0) : 0, a.causal ? min(pos + 1, sp.len) : sp.len};
+  if (!there || (a.causal && pos < 0)) s.high = 0;
+  return s;
+}
+
+// A row's running softmax, held by every lane of the row: the reference of
+// the exponents (log2), the sum of the weights, and the scale of the values in
+// whose units the sums stand.
+//
+// The reference follows the largest score only where that has grown by more
+// than kLag (weights stay below 2^5; exponents and FP16's 11 bits do not
+// care), and the units follow the pages' scales only where a page's is larger
+// or kSpan times smaller: most pages rescale nothing.  The FP16 weights are
+// kLift times as large (below FP16's 2^16), so that those down to 2^-24 of the
+// reference keep their 11 bits, and what is below has 2^-35 of it.
+constexpr float kLag = 5.0f, kSpan = 64.0f, kLift = 1024.0f;
+struct Row {
+  float top, sum, unit;
+};
+
+// The row before the weights of a page: best is its largest score there
+// (minus infinity: it sees nothing of it), scale the page's.  Returns what
+// the row's sums have to be multiplied with; *ratio: what the page's weights
+// are multiplied with before they meet its codes.
+__device__ inline float step_row(Row& r, float best, float scale, float* ratio) {
+  float factor = 1.0f;
+  if (best > r.top + kLag || (r.top == -INFINITY && best > -INFINITY)) {
+    factor = r.top == -INFINITY ? 0.0f : exp2f(r.top - best);
+    r.sum *= factor;
+    r.top = best;
+  }
+  if (best > -INFINITY && scale < INFINITY && (scale > r.unit || (scale > 0.f && scale * kSpan < r.unit))) {
+    factor *= r.unit / scale;
+    r.unit = scale;
+  }
+  // a page of zeros has no units; a scale that is NaN goes into the sums
+  *ratio = scale == 0.f ? 0.f : kLift * scale / (r.unit > 0.f ? r.unit : 1.f);
+  return factor;
+}
+
+// Four values of a row of y (0 where the row has seen nothing).
+__device__ inline void finish_row(const AttnArgs& a, size_t at, kf4_t v, float sum) {
+  const float inv = sum == 0.f ? 0.f : 1.0f / sum;
+  v *= inv;
+  *reinterpret_cast<kh4_t*>(a.y + at) = kh4_t{(_Float16)v.x, (_Float16)v.y, (_Float16)v.z, (_Float16)v.w};
+}
+
+// Four sums of row `out` ([row][q head]), to y or to a part's sums.
+template <int D>
+__device__ inline void store_row(const AttnArgs& a, int split, size_t out, int d, kf4_t v, float top, float sum) {
+  if (a.splits == 1) {
+    finish_row(a, out * D + d, v, sum);
+    return;
+  }
+  const size_t rows = (size_t)a.b.rows * a.q_heads, at = (size_t)split * rows + out;
+  *reinterpret_cast<kf4_t*>(a.part + at * D + d) = v;
+  if (d == 0) *reinterpret_cast<kw2_t*>(a.part + (size_t)a.splits * rows * D + at * 2) = kw2_t{__float_as_uint(top), __float_as_uint(sum)};
+}
+#endif
+
+}  // namespace tern

@@ -1,0 +1,337 @@
+// Writing rows of keys and values into the 8-bit cache and reading them back
+// (tern_kv_write and tern_kv_read in tern.h).
+//
+// A page's scale s has 8 significant bits and the values 11 (the keys are
+// rounded to FP16 after they are turned, as if a call of tern_rope had done
+// it), so that the quotient of a value and s, where it is no tie, lies at
+// least 2^-9 away from one: an FP32 division rounded to an integer is the
+// exact quotient's rounding.  127 s is exact, so that is the growth's
+// comparison too.
+//
+// One workgroup has a (page, head) of the keys or of the values, so that a
+// scale has one writer.  A thread owns 16-byte pieces of the page: of the
+// keys a token's 16 dimensions, of the values 16 tokens of four dimensions,
+// which it transposes by byte permutations.  It alone reads, rounds again and
+// writes those bytes; nothing is shared but the largest value.
+#include "kv.h"
+
+namespace tern {
+namespace {
+
+// Scale of 8 significant bits, the smallest with most <= 127 s.
+__device__ inline float least_scale(float most) {
+  return __uint_as_float((__float_as_uint(most / 127.0f) + 0xFFFFu) & 0xFFFF0000u);
+}
+
+// The byte of x in steps of s.
+__device__ inline uint32_t byte_of(float x, float s) {
+  const float c = s > 0.f ? rintf(x / s) : 0.f;  // 0 beside a scale that is 0 or NaN
+  return (uint32_t)((int)c + 128);
+}
+
+// Four bytes rounded again to steps that are 1 / shrink times as large.
+__device__ inline uint32_t again4(uint32_t w, float shrink) {
+  uint32_t out = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    out |= (uint32_t)((int)rintf((float)((int)((w >> (8 * i)) & 255u) - 128) * shrink) + 128) << (8 * i);
+  return out;
+}
+
+// 4 x 4 bytes: out[j] has byte j of every in.
+__device__ inline void transpose4(const uint32_t in[4], uint32_t out[4]) {
+  const uint32_t a = __builtin_amdgcn_perm(in[1], in[0], 0x05010400u), b = __builtin_amdgcn_perm(in[1], in[0], 0x07030602u);
+  const uint32_t c = __builtin_amdgcn_perm(in[3], in[2], 0x05010400u), d = __builtin_amdgcn_perm(in[3], in[2], 0x07030602u);
+  out[0] = __builtin_amdgcn_perm(c, a, 0x05040100u);
+  out[1] = __builtin_amdgcn_perm(c, a, 0x07060302u);
+  out[2] = __builtin_amdgcn_perm(d, b, 0x05040100u);
+  out[3] = __builtin_amdgcn_perm(d, b, 0x07060302u);
+}
+
+// The page's new scale, from the largest magnitude's FP16 bits that each
+// thread has seen, and what old codes shrink by.
+struct Grown {
+  float s, shrink;
+  bool keep;  // old codes stay as they are
+};
+__device__ inline Grown grow(uint32_t bits, bool fresh, float old) {
+  __shared__ uint32_t seen[4];
+  for (int o = 32; o; o >>= 1) bits = max(bits, (uint32_t)__shfl_xor((int)bits, o));
+  if (threadIdx.x % 64 == 0) seen[threadIdx.x / 64] = bits;
+  __syncthreads();
+  bits = max(max(seen[0], seen[1]), max(seen[2], seen[3]));
+  Grown g = {old, 1.0f, true};
+  if (bits >= 0x7C00u) {  // an infinity or a NaN
+    g.s = NAN;
+    return g;
+  }
+  const float most = kv_half((uint16_t)bits);
+  if (fresh || old == 0.f) {
+    g.s = least_scale(most);
+    return g;
+  }
+  for (int i = 0; i < 300 && most > 127.0f * g.s; ++i) {  // 41 times at most between FP16 values
+    g.s *= 2.0f;
+    g.shrink *= 0.5f;
+    g.keep = false;
+  }
+  return g;
+}
+
+template <int D>
+__device__ void write_keys(const WriteArgs& a, const Span& sp, int page, int id, int head, int t0, int t1) {
+  constexpr int kLanes = D / 16, kRound = 256 / kLanes, kRounds = kPage / kRound;
+  const size_t at = (size_t)id * a.c.heads + head;
+  const float old = fabsf(a.c.ks[at]);
+  const int lane = threadIdx.x % kLanes;
+  kh8_t y[kRounds][2];
+  uint32_t bits = 0;
+#pragma unroll
+  for (int i = 0; i < kRounds; ++i) {
+    const int token = i * kRound + threadIdx.x / kLanes;
+    const bool live = token >= t0 && token < t1;
+    const int row = sp.first + page * kPage + token - sp.from;
+    float v[16];
+    turned<16>(a.k + row * a.k_stride + head * D, lane * 16, D, live, kLanes, a.rk, page * kPage + token, v);
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      const uint16_t h = live ? kv_bits(v[e]) : 0;
+      y[i][e / 8][e % 8] = __builtin_bit_cast(_Float16, h);
+      bits = max(bits, (uint32_t)h & 0x7FFFu);
+    }
+  }
+  const Grown g = grow(bits, t0 == 0, old);
+  if (threadIdx.x == 0) a.c.ks[at] = g.s;
+  uint8_t* const base = a.c.k + at * (kPage * D);
+#pragma unroll
+  for (int i = 0; i < kRounds; ++i) {
+    const int token = i * kRound + threadIdx.x / kLanes;
+    const bool live = token >= t0 && token < t1;
+    if (!live && g.keep) continue;
+    kw4_t* const to = reinterpret_cast<kw4_t*>(base + ((lane / 4 * 4 + token / 4 % 4) * 64 + lane % 4 * 16 + token / 16 * 4 + token % 4) * 16);
+    kw4_t w;
+    if (live) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        uint32_t b = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) b |= byte_of((float)y[i][q / 2][q % 2 * 4 + e], g.s) << (8 * e);
+        w[q] = b;
+      }
+    } else {
+      w = *to;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) w[q] = again4(w[q], g.shrink);
+    }
+    *to = w;
+  }
+}
+
+// Of the values a thread owns 16 tokens of four dimensions, 64 contiguous bytes.
+template <int D>
+__device__ void write_values(const WriteArgs& a, const Span& sp, int page, int id, int head, int t0, int t1) {
+  const size_t at = (size_t)id * a.c.heads + head;
+  const float old = fabsf(a.c.vs[at]);
+  const int part = threadIdx.x / (D / 4), d0 = threadIdx.x % (D / 4) * 4;  // D = 256: four parts, else idle threads
+  kh4_t y[16];
+  uint32_t bits = 0;
+  const bool some = part < 4 && t0 < part * 16 + 16 && t1 > part * 16;
+#pragma unroll
+  for (int j = 0; j < 16; ++j) {
+    const int token = part * 16 + j;
+    y[j] = kh4_t{0, 0, 0, 0};
+    if (some && token >= t0 && token < t1)
+      y[j] = *reinterpret_cast<const kh4_t*>(a.v + (sp.first + page * kPage + token - sp.from) * a.v_stride + head * D + d0);
+  }
+#pragma unroll
+  for (int j = 0; j < 16; ++j)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const _Float16 x = y[j][e];  // a bit cast of the element itself would read the first
+      bits = max(bits, (uint32_t)__builtin_bit_cast(uint16_t, x) & 0x7FFFu);
+    }
+  const Grown g = grow(bits, t0 == 0, old);
+  if (threadIdx.x == 0) a.c.vs[at] = g.s;
+  if (part >= 4 || (g.keep && !some)) return;
+  kw4_t* const to = reinterpret_cast<kw4_t*>(a.c.v + at * (kPage * D) + ((d0 / 16 * 4 + part) * 16 + d0 % 16) * 16);
+  const bool all = t0 <= part * 16 && t1 >= part * 16 + 16;
+  kw4_t o[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    o[e] = all ? kw4_t{0, 0, 0, 0} : to[e];
+    if (!g.keep)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) o[e][q] = again4(o[e][q], g.shrink);
+  }
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    uint32_t in[4], out[4], mask = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int token = part * 16 + q * 4 + i;
+      in[i] = 0;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) in[i] |= byte_of((float)y[q * 4 + i][e], g.s) << (8 * e);
+      if (token >= t0 && token < t1) mask |= 255u << (8 * i);
+    }
+    transpose4(in, out);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[e][q] = (o[e][q] & ~mask) | (out[e] & mask);
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) to[e] = o[e];
+}
+
+template <int D>
+__global__ __launch_bounds__(256) void kv_write_kernel(const WriteArgs a) {
+  int bid = blockIdx.x;
+  if (bid >= a.kv_blocks) {  // a row of q: all its heads
+    bid -= a.kv_blocks;
+    const int s = bid / a.b.max_rows, j = bid % a.b.max_rows;
+    const Span sp = span_of(a.b, s);
+    if (j >= sp.n) return;
+    constexpr int lanes = D / 8, slots = 256 / lanes;
+    const int64_t row = sp.first + j;
+    const int d0 = threadIdx.x % lanes * 8;
+    for (int h0 = 0; h0 < a.q_heads; h0 += slots) {
+      const int h = h0 + threadIdx.x / lanes;
+      float y[8];
+      turned<8>(a.q + row * a.q_stride + (int64_t)h * D, d0, D, h < a.q_heads, lanes, a.rq, sp.from + j, y);
+      kh8_t o;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) o[e] = (_Float16)y[e];
+      if (h < a.q_heads) *reinterpret_cast<kh8_t*>(a.q_out + (row * a.q_heads + h) * D + d0) = o;
+    }
+    return;
+  }
+  const bool values = bid & 1;
+  bid >>= 1;
+  const int head = bid % a.c.heads;
+  bid /= a.c.heads;
+  const int s = bid / a.items;
+  const Span sp = span_of(a.b, s);
+  const int begin = max(sp.from, 0), end = sp.from + sp.n;  // positions of the rows that are there
+  const int page = begin / kPage + bid % a.items;
+  const int t0 = max(begin - page * kPage, 0), t1 = min(end - page * kPage, kPage);
+  if (t0 >= t1) return;
+  const int id = page_of(a.b, a.c, s, page);
+  if (id < 0) return;
+  if (values)
+    write_values<D>(a, sp, page, id, head, t0, t1);
+  else
+    write_keys<D>(a, sp, page, id, head, t0, t1);
+}
+
+constexpr kw4_t kNone = {0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u};  // codes 0
+
+// One workgroup has a (page, head), its keys or its values.
+template <int D, bool F32>
+__global__ __launch_bounds__(256) void kv_read_kernel(const ReadArgs a) {
+  int bid = blockIdx.x;
+  const bool values = bid & 1;
+  bid >>= 1;
+  const int head = bid % a.c.heads;
+  bid /= a.c.heads;
+  const int s = bid / a.items;
+  const Span sp = span_of(a.b, s);
+  void* const out = values ? a.v : a.k;
+  if (!out) return;
+  const int begin = sp.from, end = sp.from + sp.n;
+  // pages of the rows before the sequence's beginning count as negative ones
+  const int page = (begin >= 0 ? begin / kPage : -((-begin + kPage - 1) / kPage)) + bid % a.items;
+  const int t0 = max(begin - page * kPage, 0), t1 = min(end - page * kPage, kPage);
+  if (t0 >= t1) return;
+  const int id = page < 0 ? -1 : page_of(a.b, a.c, s, page);
+  const size_t at = (size_t)max(id, 0) * a.c.heads + head;
+  const float scale = id < 0 ? 0.f : (values ? a.c.vs : a.c.ks)[at];
+  const int64_t row0 = (int64_t)sp.first + page * kPage - sp.from;  // of token 0
+  auto place = [&](int token, int d) { return ((row0 + token) * a.c.heads + head) * D + d; };
+  if (values) {
+    const int part = threadIdx.x / (D / 4), d0 = threadIdx.x % (D / 4) * 4;
+    if (part >= 4) return;
+    const kw4_t* const from = reinterpret_cast<const kw4_t*>(a.c.v + at * (kPage * D) + ((d0 / 16 * 4 + part) * 16 + d0 % 16) * 16);
+    kw4_t w[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) w[e] = id < 0 ? kNone : from[e];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const uint32_t in[4] = {w[0][q], w[1][q], w[2][q], w[3][q]};
+      uint32_t tok[4];
+      transpose4(in, tok);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int token = part * 16 + q * 4 + i;
+        if (token < t0 || token >= t1) continue;
+        float v[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = (float)((int)((tok[i] >> (8 * e)) & 255u) - 128) * scale;
+        if (F32)
+          *reinterpret_cast<kf4_t*>((float*)out + place(token, d0)) = kf4_t{v[0], v[1], v[2], v[3]};
+        else
+          *reinterpret_cast<kh4_t*>((_Float16*)out + place(token, d0)) =
+              kh4_t{(_Float16)v[0], (_Float16)v[1], (_Float16)v[2], (_Float16)v[3]};
+      }
+    }
+    return;
+  }
+  constexpr int kLanes = D / 16, kRound = 256 / kLanes;
+  const int lane = threadIdx.x % kLanes;
+#pragma unroll
+  for (int i = 0; i < kPage / kRound; ++i) {
+    const int token = i * kRound + threadIdx.x / kLanes;
+    if (token < t0 || token >= t1) continue;
+    kw4_t w = kNone;
+    if (id >= 0)
+      w = *reinterpret_cast<const kw4_t*>(a.c.k + at * (kPage * D) +
+                                          ((lane / 4 * 4 + token / 4 % 4) * 64 + lane % 4 * 16 + token / 16 * 4 + token % 4) * 16);
+    float v[16];
+#pragma unroll
+    for (int e = 0; e < 16; ++e) v[e] = (float)((int)((w[e / 4] >> (8 * (e % 4))) & 255u) - 128) * scale;
+    if (F32) {
+      kf4_t* const to = reinterpret_cast<kf4_t*>((float*)out + place(token, lane * 16));
+#pragma unroll
+      for (int q = 0; q < 4; ++q) to[q] = kf4_t{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
+    } else {
+      kh8_t* const to = reinterpret_cast<kh8_t*>((_Float16*)out + place(token, lane * 16));
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        kh8_t h;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) h[e] = (_Float16)v[8 * q + e];
+        to[q] = h;
+      }
+    }
+  }
+}
+
+template <int D>
+hipError_t write(const WriteArgs& a, long long blocks, hipStream_t s) {
+  hipLaunchKernelGGL((kv_write_kernel<D>), dim3((unsigned)blocks), dim3(256), 0, s, a);
+  return hipGetLastError();
+}
+template <int D>
+hipError_t read(const ReadArgs& a, long long blocks, hipStream_t s) {
+  if (a.f32)
+    hipLaunchKernelGGL((kv_read_kernel<D, true>), dim3((unsigned)blocks), dim3(256), 0, s, a);
+  else
+    hipLaunchKernelGGL((kv_read_kernel<D, false>), dim3((unsigned)blocks), dim3(256), 0, s, a);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_kv_write(const WriteArgs& a, int dim, hipStream_t s) {
+  const long long blocks = a.kv_blocks + (a.q ? (long long)a.b.count * a.b.max_rows : 0);
+  if (!kv_grid_fits(blocks, 256)) return hipErrorInvalidConfiguration;
+  if (dim == 64) return write<64>(a, blocks, s);
+  return dim == 128 ? write<128>(a, blocks, s) : write<256>(a, blocks, s);
+}
+
+hipError_t launch_kv_read(const ReadArgs& a, int dim, hipStream_t s) {
+  const long long blocks = 2ll * a.b.count * a.items * a.c.heads;
+  if (!kv_grid_fits(blocks, 256)) return hipErrorInvalidConfiguration;
+  if (dim == 64) return read<64>(a, blocks, s);
+  return dim == 128 ? read<128>(a, blocks, s) : read<256>(a, blocks, s);
+}
+
+}  // namespace tern

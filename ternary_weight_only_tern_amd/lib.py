@@ -9,7 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from ctypes import POINTER, c_double, c_float, c_int32, c_size_t, c_uint32, c_void_p
+from ctypes import POINTER, c_double, c_float, c_int32, c_int64, c_size_t, c_uint32, c_void_p
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libtern.so")
@@ -31,6 +31,8 @@ TERN_F16 = 0
 TERN_F32 = 1
 TERN_SCORE_SOFTMAX = 0
 TERN_SCORE_SIGMOID = 1
+(TERN_ROPE_PLAIN, TERN_ROPE_LINEAR, TERN_ROPE_BASE, TERN_ROPE_RAMP, TERN_ROPE_WAVES) = range(5)
+TERN_KV_PAGE = 64
 
 (TERN_BUF_PLANE0, TERN_BUF_SCALE0, TERN_BUF_OFFSET, TERN_BUF_MASK, TERN_BUF_ROWPTR,
  TERN_BUF_BLOCKS1, TERN_BUF_BLOCKS2, TERN_BUF_RSCALE1, TERN_BUF_RSCALE2, TERN_NBUF) = range(10)
@@ -41,6 +43,8 @@ SYMBOLS = ["tern_row_stride", "tern_check", "tern_packed_sizes", "tern_workspace
            "tern_rotated_workspace_bytes", "tern_plan_create_rotated",
            "tern_bits", "tern_quantize", "tern_rotate", "tern_rotate_batched", "tern_q4_check", "tern_q4_pack", "tern_q4_unpack", "tern_q4_workspace_bytes", "tern_q4_gemm",
            "tern_route", "tern_q4_experts_workspace_bytes", "tern_q4_experts", "tern_q4_tile_rows", "tern_q4_experts_tile_rows",
+           "tern_rope_frequencies", "tern_rope", "tern_kv_check", "tern_kv_write", "tern_kv_read",
+           "tern_kv_attention_workspace_bytes", "tern_kv_attention", "tern_kv_attention_parts",
            "tern_read_probe", "tern_status_str", "tern_last_error"]
 
 
@@ -61,6 +65,21 @@ class tern_router(ctypes.Structure):
     _fields_ = [("experts", c_int32), ("topk", c_int32), ("score", c_int32), ("groups", c_int32),
                 ("group_best", c_int32), ("keep_groups", c_int32), ("renorm", c_int32), ("scale", c_float),
                 ("bias", c_void_p)]
+
+
+class tern_rotary(ctypes.Structure):
+    _fields_ = [("rot", c_int32), ("interleaved", c_int32), ("freq", c_void_p), ("amp", c_float), ("eps", c_float),
+                ("norm", c_void_p)]
+
+
+class tern_kv(ctypes.Structure):
+    _fields_ = [("heads", c_int32), ("dim", c_int32), ("pages", c_int32), ("k", c_void_p), ("v", c_void_p),
+                ("k_scale", c_void_p), ("v_scale", c_void_p)]
+
+
+class tern_kv_batch(ctypes.Structure):
+    _fields_ = [("count", c_int32), ("rows", c_int32), ("max_rows", c_int32), ("max_len", c_int32),
+                ("max_pages", c_int32), ("start", c_void_p), ("len", c_void_p), ("pages", c_void_p)]
 
 
 class TernError(RuntimeError):
@@ -119,6 +138,18 @@ def load() -> ctypes.CDLL:
                                       c_int32, c_void_p, c_size_t, c_void_p]),
         "tern_q4_tile_rows": (c_int32, [c_void_p, c_int32]),
         "tern_q4_experts_tile_rows": (c_int32, [c_void_p, c_void_p, c_int32, c_int32]),
+        "tern_rope_frequencies": (c_int32, [c_int32, c_double, c_int32, c_double, c_double, c_double, c_int32,
+                                            POINTER(c_double), POINTER(c_float)]),
+        "tern_rope": (c_int32, [c_void_p, c_int64, c_int32, c_int32, c_int32, c_void_p, c_void_p, c_void_p, c_int64,
+                                c_void_p]),
+        "tern_kv_check": (c_int32, [c_void_p]),
+        "tern_kv_write": (c_int32, [c_void_p, c_void_p, c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_void_p,
+                                    c_int64, c_int32, c_void_p, c_void_p, c_void_p]),
+        "tern_kv_read": (c_int32, [c_void_p, c_void_p, c_void_p, c_void_p, c_int32, c_void_p]),
+        "tern_kv_attention_workspace_bytes": (c_size_t, [c_void_p, c_void_p, c_int32]),
+        "tern_kv_attention": (c_int32, [c_void_p, c_void_p, c_void_p, c_int64, c_int32, c_float, c_int32, c_int32,
+                                        c_void_p, c_void_p, c_size_t, c_void_p]),
+        "tern_kv_attention_parts": (c_int32, [c_void_p, c_void_p, c_int32, c_int32]),
         "tern_read_probe": (c_int32, [c_void_p, c_size_t, c_void_p, c_void_p]),
         "tern_status_str": (ctypes.c_char_p, [c_int32]),
         "tern_last_error": (ctypes.c_char_p, []),
@@ -670,6 +701,246 @@ class Q4Experts:
             _refuse(f"logits have shape {tuple(logits.shape)}, not {(x.shape[0], self.down.count)}")
         ids, weights = tern_route(logits, self.topk, stream=stream, **self._route)
         return tern_q4_experts(self.gate_up, self.down, x, ids, weights, y_dtype, out, stream, ws)
+
+
+# ---------------------------------------------------------------- positions, cache, attention
+def tern_rope_frequencies(rot, base=1e6, scaling=TERN_ROPE_PLAIN, factor=1.0, low=1.0, high=32.0, trained=4096):
+    """(frequencies fp64 [rot/2] on the host, amplitude) of rotary positions;
+    see tern_rope_frequencies in tern.h for the scalings."""
+    import torch
+    freq = torch.empty(_count(max(rot, 0)) // 2, dtype=torch.float64)
+    amp = c_float()
+    check(load().tern_rope_frequencies(rot, base, scaling, factor, low, high, trained,
+                                       ctypes.cast(freq.data_ptr(), POINTER(c_double)), ctypes.byref(amp)))
+    return freq, amp.value
+
+
+class Rope:
+    """tern_rotary: how a head's values turn.  freq: fp64 device tensor
+    [rot/2]; norm: fp16 device tensor [dim] or None, the weights of an RMS norm
+    of each head before.  Keeps the tensors."""
+
+    def __init__(self, freq, interleaved=False, amp=1.0, norm=None, eps=1e-6):
+        import torch
+        if freq.device.type != "cuda" or freq.dim() != 1:
+            _refuse(f"freq of shape {tuple(freq.shape)} on {freq.device}, not [rot/2] on a GPU")
+        _tensor(freq, "freq", (torch.float64,), freq.device)
+        if norm is not None:
+            _tensor(norm, "norm", (torch.float16,), freq.device)
+            if norm.dim() != 1:
+                _refuse(f"norm has shape {tuple(norm.shape)}, not [dim]")
+        _use_torch()
+        self.freq, self.norm, self.device = freq, norm, freq.device
+        self.dim = None if norm is None else norm.numel()
+        self._desc = tern_rotary(2 * _count(freq.numel()), int(bool(interleaved)), _ptr(freq), amp, eps, _ptr(norm))
+        self._at = ctypes.addressof(self._desc)
+
+    def _of(self, device, dim):
+        """The descriptor's address, for heads of dim elements on a device."""
+        if self.device != device:
+            _refuse(f"the rotary frequencies are on {self.device}, not {device}")
+        if self.dim is not None and self.dim != dim:
+            _refuse(f"a norm of {self.dim} elements for heads of {dim}")
+        return self._at
+
+
+def _heads(t, name, device, heads, dim):
+    """Checks rows of heads, fp16 [m][heads][dim] whose heads follow each
+    other (heads None: any number); the rows' stride."""
+    if t.dtype != _torch.float16 or t.device != device:
+        _refuse(f"{name} is {t.dtype} on {t.device}, not torch.float16 on {device}")
+    shape = t.shape
+    if len(shape) != 3 or shape[2] != dim or (heads is not None and shape[1] != heads):
+        _refuse(f"{name} has shape {tuple(shape)}, not [m][{'heads' if heads is None else heads}][{dim}]")
+    m, heads = shape[0], shape[1]
+    row, head, step = t.stride()
+    if not m * heads * dim:
+        return 0
+    if (step != 1 and dim > 1) or (head != dim and heads > 1):
+        _refuse(f"{name} has strides {(row, head, step)}: a row's heads have to follow each other")
+    return row if m > 1 else heads * dim
+
+
+def tern_rope(x, pos, rope: Rope, out=None, stream=None):
+    """x fp16 [m][heads][dim] turned, row r by pos[r] (int32 [m]); in `out`
+    if given, which may be x."""
+    torch = _torch or _use_torch()
+    device = rope.device
+    if _elsewhere(device):
+        with torch.cuda.device(device):
+            return tern_rope(x, pos, rope, out, stream)
+    if x.dim() != 3:
+        _refuse(f"x has shape {tuple(x.shape)}, not [m][heads][dim]")
+    m, heads, dim = x.shape
+    x_stride = _heads(x, "x", device, heads, dim)
+    _tensor(pos, "pos", (torch.int32,), device, (m,))
+    if out is None:
+        out = _fresh((m, heads, dim), torch.float16, device, stream)
+    elif out.shape != x.shape:
+        _refuse(f"out has shape {tuple(out.shape)}, not {tuple(x.shape)}")
+    out_stride = _heads(out, "out", device, heads, dim)
+    check(load().tern_rope(x.data_ptr(), x_stride, _count(m), _count(heads), _count(dim), pos.data_ptr(),
+                           rope._of(device, dim), out.data_ptr(), out_stride, _stream_of(device, stream)))
+    return out
+
+
+class KvCache:
+    """tern_kv: a paged cache in 8 bits.  k, v: uint8 [pages][heads][64][dim]
+    (the bytes of a (page, head) in tern_kv's order), k_scale, v_scale: fp32
+    [pages][heads].  Keeps the tensors; makes no copy."""
+
+    def __init__(self, k, v, k_scale, v_scale):
+        import torch
+        if k.device.type != "cuda":
+            _refuse(f"the cache is on {k.device}, not on a GPU")
+        if k.dim() != 4 or k.size(2) != TERN_KV_PAGE:
+            _refuse(f"k has shape {tuple(k.shape)}, not [pages][heads][{TERN_KV_PAGE}][dim]")
+        device = k.device
+        _tensor(k, "k", (torch.uint8,), device)
+        _tensor(v, "v", (torch.uint8,), device, k.shape)
+        _tensor(k_scale, "k_scale", (torch.float32,), device, k.shape[:2])
+        _tensor(v_scale, "v_scale", (torch.float32,), device, k.shape[:2])
+        _use_torch()
+        self.k, self.v, self.k_scale, self.v_scale, self.device = k, v, k_scale, v_scale, device
+        self.pages, self.heads, _, self.dim = k.shape
+        self._desc = tern_kv(_count(self.heads), _count(self.dim), _count(self.pages), _ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale))
+        self._at = ctypes.addressof(self._desc)
+        check(load().tern_kv_check(self._at))
+
+    @classmethod
+    def empty(cls, pages, heads, dim, device="cuda"):
+        """A cache of zeros (every scale 0)."""
+        import torch
+        code = lambda: torch.full((pages, heads, TERN_KV_PAGE, dim), 128, dtype=torch.uint8, device=device)
+        scale = lambda: torch.zeros((pages, heads), dtype=torch.float32, device=device)
+        return cls(code(), code(), scale(), scale())
+
+
+class KvBatch:
+    """tern_kv_batch: the sequences of a call.  len: int32 [count], tokens with
+    the call's rows; pages: int32 [count][max_pages]; max_rows: rows of a
+    sequence at most; start: int32 [count + 1], or None where every sequence
+    has max_rows rows; max_len: bound of len for the choice of kernels (default
+    what the pages hold).  Keeps the tensors, whose contents may change between
+    calls."""
+
+    def __init__(self, len, pages, max_rows, start=None, max_len=None):
+        import torch
+        device = len.device
+        if device.type != "cuda" or len.dim() != 1 or pages.dim() != 2:
+            _refuse(f"len {tuple(len.shape)} and pages {tuple(pages.shape)} on {device} are no batch on a GPU")
+        count = len.numel()
+        _tensor(len, "len", (torch.int32,), device)
+        _tensor(pages, "pages", (torch.int32,), device, (count, pages.size(1)))
+        if start is not None:
+            _tensor(start, "start", (torch.int32,), device, (count + 1,))
+        _use_torch()
+        self.len, self.pages, self.start, self.device = len, pages, start, device
+        self.count, self.max_rows = _count(count), _count(max_rows)
+        self.max_len = _count(pages.size(1) * TERN_KV_PAGE if max_len is None else max_len)
+        self._descs = {}
+
+    def _of(self, device, rows):
+        """The descriptor's address for so many rows."""
+        if self.device != device:
+            _refuse(f"the batch is on {self.device}, not {device}")
+        d = self._descs.get(rows)
+        if d is None:
+            if len(self._descs) >= 64:
+                self._descs.clear()
+            d = tern_kv_batch(self.count, _count(rows), self.max_rows, self.max_len, self.pages.size(1),
+                              _ptr(self.start), _ptr(self.len), _ptr(self.pages))
+            self._descs[rows] = d
+        return ctypes.addressof(d)
+
+
+def tern_kv_write(cache: KvCache, batch: KvBatch, k, v, rope=None, q=None, q_rope=None, q_out=None, stream=None):
+    """Writes the rows k, v fp16 [m][heads][dim] into the cache, k turned by
+    `rope` first if given.  With q (fp16 [m][q_heads][dim]) its rows are turned
+    by q_rope in the same launch: returns q_out, contiguous, in `q_out` if
+    given (which may be q)."""
+    device, dim = cache.device, cache.dim
+    if _elsewhere(device):
+        with _torch.cuda.device(device):
+            return tern_kv_write(cache, batch, k, v, rope, q, q_rope, q_out, stream)
+    k_stride = _heads(k, "k", device, cache.heads, dim)
+    v_stride = _heads(v, "v", device, cache.heads, dim)
+    m = k.size(0)
+    if v.size(0) != m:
+        _refuse(f"{v.size(0)} rows of v and {m} of k")
+    q_at = q_out_at = None
+    q_stride = q_heads = 0
+    if q is not None:
+        q_stride = _heads(q, "q", device, None, dim)
+        q_heads = _count(q.size(1))
+        if q.size(0) != m:
+            _refuse(f"{q.size(0)} rows of q and {m} of k")
+        if q_rope is None:
+            _refuse("q without q_rope")
+        if q_out is None:
+            q_out = _fresh((m, q_heads, dim), _torch.float16, device, stream)
+        else:
+            _tensor(q_out, "q_out", _halves, device, (m, q_heads, dim))
+        q_at, q_out_at = q.data_ptr(), q_out.data_ptr()
+    check(load().tern_kv_write(cache._at, batch._of(device, m), k.data_ptr(), k_stride, v.data_ptr(), v_stride,
+                               None if rope is None else rope._of(device, dim), q_at, q_stride, q_heads,
+                               None if q is None else q_rope._of(device, dim), q_out_at, _stream_of(device, stream)))
+    return q_out
+
+
+def tern_kv_read(cache: KvCache, batch: KvBatch, rows=None, y_dtype=TERN_F16, k=None, v=None, stream=None):
+    """The values of the batch's rows (k, v) back, [m][heads][dim], in fp16 or
+    fp32; in `k` and `v` if given.  rows: m (default count * max_rows, or the
+    rows of k)."""
+    device = cache.device
+    if _elsewhere(device):
+        with _torch.cuda.device(device):
+            return tern_kv_read(cache, batch, rows, y_dtype, k, v, stream)
+    if rows is None:
+        rows = k.size(0) if k is not None else v.size(0) if v is not None else batch.count * batch.max_rows
+    shape = (_count(rows), cache.heads, cache.dim)
+    given = k if k is not None else v
+    kind = _y_type(y_dtype) if given is None else given.dtype
+    if kind not in (_torch.float16, _torch.float32):
+        _refuse(f"unknown output dtype {kind}")
+    k = _fresh(shape, kind, device, stream) if k is None else _tensor(k, "k", (kind,), device, shape)
+    v = _fresh(shape, kind, device, stream) if v is None else _tensor(v, "v", (kind,), device, shape)
+    check(load().tern_kv_read(cache._at, batch._of(device, rows), k.data_ptr(), v.data_ptr(),
+                              TERN_F32 if kind == _torch.float32 else TERN_F16, _stream_of(device, stream)))
+    return k, v
+
+
+def tern_kv_attention_workspace(cache: KvCache, batch: KvBatch, rows: int, q_heads: int):
+    """A workspace for tern_kv_attention with up to `rows` rows of q_heads
+    heads and no longer sequences than the batch's max_len."""
+    return _scratch(_bytes(load().tern_kv_attention_workspace_bytes(cache._at, batch._of(cache.device, rows), _count(q_heads))),
+                    cache.device, None)
+
+
+def tern_kv_attention(cache: KvCache, batch: KvBatch, q, scale=None, window=0, causal=True, out=None, stream=None,
+                      ws=None):
+    """Attention of the rows q fp16 [m][q_heads][dim] over the cache; returns
+    y fp16 [m][q_heads][dim], in `out` if given.  scale: of the scores (default
+    dim ** -0.5); window: tokens a row sees at most (0: all)."""
+    device, dim = cache.device, cache.dim
+    if _elsewhere(device):
+        with _torch.cuda.device(device):
+            return tern_kv_attention(cache, batch, q, scale, window, causal, out, stream, ws)
+    q_stride = _heads(q, "q", device, None, dim)
+    m, q_heads = q.shape[0], q.shape[1]
+    if out is None:
+        out = _fresh((m, q_heads, dim), _torch.float16, device, stream)
+    else:
+        _tensor(out, "out", _halves, device, q.shape)
+    at = batch._of(device, m)
+    if ws is None:
+        ws = _scratch(load().tern_kv_attention_workspace_bytes(cache._at, at, _count(q_heads)), device, stream)
+    else:
+        _space(ws, device)
+    check(load().tern_kv_attention(cache._at, at, q.data_ptr(), q_stride, _count(q_heads), dim ** -0.5 if scale is None else scale,
+                                   _count(window), 1 if causal else 0, out.data_ptr(), ws.data_ptr(), ws.nbytes,
+                                   _stream_of(device, stream)))
+    return out
 
 
 def tern_read_probe(buf, sink, stream=None) -> None:
