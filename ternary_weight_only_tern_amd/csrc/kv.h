@@ -84,10 +84,11 @@ struct AttnArgs {
   const uint16_t* q;
   int64_t q_stride;
   uint16_t* y;         // [rows][q_heads][dim]
-  float* part;         // [splits][rows][q_heads][dim], then [splits][rows][q_heads][2]
+  float* part;         // [parts][rows][q_heads][dim], then [parts][rows][q_heads][2]
   float scale;         // times log2(e)
   int32_t q_heads, group, window, causal;
-  int32_t splits, tiles;
+  int32_t parts, per;  // parts of the context at most, their pages at least
+  int32_t tiles;
 };
 
 // Rows (of a sequence, times the query heads of one cache head) of one
@@ -100,7 +101,8 @@ hipError_t launch_kv_read(const ReadArgs& a, int dim, hipStream_t s);
 // blocks: of 16 rows, 1, 2 or 4 (2 at most at dim 256)
 hipError_t launch_attn_rows(const AttnArgs& a, int dim, int blocks, hipStream_t s);
 hipError_t launch_attn_tile(const AttnArgs& a, int dim, hipStream_t s);
-hipError_t launch_attn_join(const AttnArgs& a, int dim, hipStream_t s);
+// block_rows: of a workgroup of the launch before
+hipError_t launch_attn_join(const AttnArgs& a, int dim, int block_rows, hipStream_t s);
 
 // A grid's threads have to be countable in 32 bits.
 inline bool kv_grid_fits(long long blocks, int threads) { return blocks * threads < (1ll << 32); }
@@ -154,6 +156,20 @@ __device__ inline kh8_t codes8(uint32_t w0, uint32_t w1) {
   codes4(w0, a, b);
   codes4(w1, c, d);
   return kh8_t{a.x, a.y, b.x, b.y, c.x, c.y, d.x, d.y};
+}
+
+// A buffer of bytes at p, the same in every lane (said so explicitly: a
+// descriptor that the compiler cannot prove uniform costs a loop around every
+// load).  A load past its end gives zeros and moves nothing, which stands in
+// for branches around loads.
+__device__ inline __amdgpu_buffer_rsrc_t kv_buffer(const void* p, int bytes) {
+  const uint64_t v = reinterpret_cast<uint64_t>(p);
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v), hi = __builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
+  return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>((uint64_t)hi << 32 | lo), (short)0,
+                                           __builtin_amdgcn_readfirstlane(bytes), 0x00020000);
+}
+__device__ inline kw4_t kv_load16(__amdgpu_buffer_rsrc_t r, int offset) {
+  return __builtin_bit_cast(kw4_t, __builtin_amdgcn_raw_buffer_load_b128(r, offset, 0, 0));
 }
 
 __device__ inline float kv_half(uint16_t v) { return (float)__builtin_bit_cast(_Float16, v); }

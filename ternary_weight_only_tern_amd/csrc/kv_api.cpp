@@ -130,10 +130,10 @@ int items_of(const tern_kv_batch* b) { return (b->max_rows + 2 * (tern::kPage - 
 // How attention runs.
 struct AttnPlan {
   int blocks;  // of 16 rows in the kernel for few rows; 0: tiles
-  int tiles, splits;
+  int block_rows, tiles, parts, per;
 };
 constexpr int kPartPages = 4;       // the least of a part
-constexpr int kRowsTarget = 1024;   // workgroups
+constexpr int kRowsTarget = 2048;   // workgroups
 constexpr int kTileTarget = 512;
 constexpr int kPartRows = 2 * kRowsTarget * 64;  // rows of all parts at most, either way (plan_of)
 
@@ -148,17 +148,17 @@ AttnPlan plan_of(const tern_kv* c, const tern_kv_batch* b, int group, int window
   const long long rows = (long long)b->max_rows * group;
   const int most = c->dim == 256 ? 32 : 64;
   if (rows <= most) p.blocks = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
-  p.tiles = p.blocks ? 1 : (int)((rows + tern::kAttnTile - 1) / tern::kAttnTile);
+  p.block_rows = p.blocks ? 16 * p.blocks : tern::kAttnTile;
+  p.tiles = (int)((rows + p.block_rows - 1) / p.block_rows);
   const long long groups = (long long)p.tiles * c->heads * b->count;
-  const int target = p.blocks ? kRowsTarget : kTileTarget;
-  p.splits = 1;
-  if (groups < target / 2)
-    p.splits = (int)std::max<long long>(1, std::min<long long>((target + groups - 1) / groups, pages_of(b, window) / kPartPages));
+  const int target = p.blocks ? kRowsTarget : kTileTarget, pages = pages_of(b, window);
+  p.per = std::max(kPartPages, (int)std::min<long long>((groups * pages + target - 1) / target, pages));
+  p.parts = std::max(1, (pages + p.per - 1) / p.per);
   return p;
 }
 
 size_t attn_need(const AttnPlan& p, const tern_kv* c, const tern_kv_batch* b, int q_heads) {
-  return p.splits > 1 ? (size_t)p.splits * b->rows * q_heads * (c->dim + 2) * 4 : 0;
+  return p.parts > 1 ? (size_t)p.parts * b->rows * q_heads * (c->dim + 2) * 4 : 0;
 }
 
 tern_status check_heads(const tern_kv* c, const tern_kv_batch* b, int q_heads) {
@@ -293,7 +293,7 @@ tern_status tern_kv_read(const tern_kv* c, const tern_kv_batch* b, void* k, void
 
 size_t tern_kv_attention_workspace_bytes(const tern_kv* c, const tern_kv_batch* b, int32_t q_heads) {
   if (check_shape(c) != TERN_OK || check_sizes(b) != TERN_OK || check_heads(c, b, q_heads) != TERN_OK) return 0;
-  const long long parts = std::max(1, pages_of(b, 0) / kPartPages);
+  const long long parts = (pages_of(b, 0) + kPartPages - 1) / kPartPages;
   const double rows = (double)b->rows * q_heads * parts;
   return (size_t)std::max(256.0, std::min(rows, (double)kPartRows) * (c->dim + 2) * 4);
 }
@@ -302,7 +302,7 @@ int32_t tern_kv_attention_parts(const tern_kv* c, const tern_kv_batch* b, int32_
   if (check_shape(c) != TERN_OK || check_sizes(b) != TERN_OK || check_heads(c, b, q_heads) != TERN_OK || window < 0) return -1;
   if (nothing(b)) return 0;
   const AttnPlan p = plan_of(c, b, q_heads / c->heads, window);
-  return p.blocks ? p.splits : -1 - p.splits;
+  return p.blocks ? p.parts : -1 - p.parts;
 }
 
 tern_status tern_kv_attention(const tern_kv* c, const tern_kv_batch* b, const uint16_t* q, int64_t q_stride,
@@ -335,14 +335,15 @@ tern_status tern_kv_attention(const tern_kv* c, const tern_kv_batch* b, const ui
   a.group = q_heads / c->heads;
   a.window = window;
   a.causal = causal != 0;
-  a.splits = p.splits;
+  a.parts = p.parts;
+  a.per = p.per;
   a.tiles = p.tiles;
   const hipStream_t s = (hipStream_t)stream;
   if (p.blocks)
     KV_HIP(tern::launch_attn_rows(a, c->dim, p.blocks, s));
   else
     KV_HIP(tern::launch_attn_tile(a, c->dim, s));
-  if (a.splits > 1) KV_HIP(tern::launch_attn_join(a, c->dim, s));
+  if (a.parts > 1) KV_HIP(tern::launch_attn_join(a, c->dim, p.block_rows, s));
   return TERN_OK;
 }
 

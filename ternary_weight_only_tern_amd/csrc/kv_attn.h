@@ -19,10 +19,26 @@ __device__ inline Range range_of(const AttnArgs& a, const Span& sp, int first, i
   return r;
 }
 
-// This workgroup's part of them, all wavefronts'.
-__device__ inline Range part_of(const Range& r, int split, int splits) {
-  const long long n = r.end - r.begin;
-  return {r.begin + (int)(n * split / splits), r.begin + (int)(n * (split + 1) / splits)};
+// Pages of a part: what the host chose, or more where the context is longer
+// than it was told; and the parts that there are.
+struct Parts {
+  int per, count;
+};
+__device__ inline Parts parts_of(const AttnArgs& a, const Range& r) {
+  const int n = r.end - r.begin;
+  Parts p;
+  p.per = max(a.per, (n + a.parts - 1) / a.parts);
+  p.count = max(1, (n + p.per - 1) / p.per);
+  return p;
+}
+__device__ inline Range part_of(const Range& r, const Parts& p, int part) {
+  const int begin = r.begin + part * p.per;
+  return {begin, min(begin + p.per, r.end)};
+}
+
+// What the rows first .. last (token * group + query head) of a sequence see.
+__device__ inline Range range_of_rows(const AttnArgs& a, const Span& sp, int first, int last) {
+  return range_of(a, sp, max(sp.from + first / a.group, 0), sp.from + last / a.group);
 }
 
 // Tokens [low, high) that the row at position pos sees.
@@ -65,8 +81,9 @@ __device__ inline float step_row(Row& r, float best, float scale, float* ratio) 
     factor *= r.unit / scale;
     r.unit = scale;
   }
-  // a page of zeros has no units; a scale that is NaN goes into the sums
-  *ratio = scale == 0.f ? 0.f : kLift * scale / (r.unit > 0.f ? r.unit : 1.f);
+  // a page of zeros has no units; a scale that is NaN goes into the sums of the
+  // rows that see a token of its page
+  *ratio = scale == 0.f || best == -INFINITY ? 0.f : kLift * scale / (r.unit > 0.f ? r.unit : 1.f);
   return factor;
 }
 
@@ -79,14 +96,14 @@ __device__ inline void finish_row(const AttnArgs& a, size_t at, kf4_t v, float s
 
 // Four sums of row `out` ([row][q head]), to y or to a part's sums.
 template <int D>
-__device__ inline void store_row(const AttnArgs& a, int split, size_t out, int d, kf4_t v, float top, float sum) {
-  if (a.splits == 1) {
+__device__ inline void store_row(const AttnArgs& a, const Parts& p, int part, size_t out, int d, kf4_t v, float top, float sum) {
+  if (p.count == 1) {
     finish_row(a, out * D + d, v, sum);
     return;
   }
-  const size_t rows = (size_t)a.b.rows * a.q_heads, at = (size_t)split * rows + out;
+  const size_t rows = (size_t)a.b.rows * a.q_heads, at = (size_t)part * rows + out;
   *reinterpret_cast<kf4_t*>(a.part + at * D + d) = v;
-  if (d == 0) *reinterpret_cast<kw2_t*>(a.part + (size_t)a.splits * rows * D + at * 2) = kw2_t{__float_as_uint(top), __float_as_uint(sum)};
+  if (d == 0) *reinterpret_cast<kw2_t*>(a.part + (size_t)a.parts * rows * D + at * 2) = kw2_t{__float_as_uint(top), __float_as_uint(sum)};
 }
 #endif
 

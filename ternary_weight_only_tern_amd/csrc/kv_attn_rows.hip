@@ -20,20 +20,22 @@ namespace {
 constexpr int kWaves = 4;
 
 template <int D, int NT>
-__global__ __launch_bounds__(64 * kWaves) void attn_rows_kernel(const AttnArgs a) {
+__global__ __launch_bounds__(64 * kWaves, NT <= 2 && D <= 128 ? 2 : 1) void attn_rows_kernel(const AttnArgs a) {
   constexpr int C = D / 64, DT = D / 16;
   constexpr int P = D + 4;  // pitch of a row in LDS: rows fall in other banks
   __shared__ float sums[kWaves * 16 * P];
   __shared__ float tops[kWaves][16 * NT], totals[kWaves][16 * NT];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int col = lane & 15, kq = lane >> 4;
-  const int split = blockIdx.x % a.splits, head = blockIdx.x / a.splits % a.c.heads;
-  const int s = blockIdx.x / a.splits / a.c.heads;
+  const int part = blockIdx.x % a.parts, head = blockIdx.x / a.parts % a.c.heads;
+  const int s = blockIdx.x / a.parts / a.c.heads;
   const Span sp = span_of(a.b, s);
   const int total = sp.n * a.group;
   if (total <= 0) return;
-  const Range all = range_of(a, sp, max(sp.from, 0), sp.from + sp.n - 1);
-  const Range mine = part_of(all, split, a.splits);
+  const Range all = range_of_rows(a, sp, 0, total - 1);
+  const Parts parts = parts_of(a, all);
+  if (part >= parts.count) return;
+  const Range mine = part_of(all, parts, part);
 
   // rows of the operand: j * group + h
   kh8_t q[NT][C][2];
@@ -70,31 +72,37 @@ __global__ __launch_bounds__(64 * kWaves) void attn_rows_kernel(const AttnArgs a
   high = __builtin_amdgcn_readfirstlane(high);
 
   kw4_t kr[C][4], vr[DT];
-  // the page's bytes; a page that is not there reads page 0 and is masked
+  // a page that is not there reads as zeros, and is masked
   auto page_at = [&](int p) { return p < mine.end ? __builtin_amdgcn_readfirstlane(page_of(a.b, a.c, s, p)) : -1; };
   auto load_keys = [&](int id) {
-    const kw4_t* const from = reinterpret_cast<const kw4_t*>(a.c.k + ((size_t)max(id, 0) * a.c.heads + head) * (kPage * D)) + lane;
+    const __amdgpu_buffer_rsrc_t from = kv_buffer(a.c.k + ((size_t)max(id, 0) * a.c.heads + head) * (kPage * D), id < 0 ? 0 : kPage * D);
 #pragma unroll
     for (int c = 0; c < C; ++c)
 #pragma unroll
-      for (int t = 0; t < 4; ++t) kr[c][t] = from[(4 * c + t) * 64];
+      for (int t = 0; t < 4; ++t) kr[c][t] = kv_load16(from, ((4 * c + t) * 64 + lane) * 16);
   };
   auto load_values = [&](int id) {
-    const kw4_t* const from = reinterpret_cast<const kw4_t*>(a.c.v + ((size_t)max(id, 0) * a.c.heads + head) * (kPage * D)) + lane;
+    const __amdgpu_buffer_rsrc_t from = kv_buffer(a.c.v + ((size_t)max(id, 0) * a.c.heads + head) * (kPage * D), id < 0 ? 0 : kPage * D);
 #pragma unroll
-    for (int d = 0; d < DT; ++d) vr[d] = from[d * 64];
+    for (int d = 0; d < DT; ++d) vr[d] = kv_load16(from, (d * 64 + lane) * 16);
   };
 
+  // Page numbers are read two pages ahead, scales one: their use never waits.
+  auto scale_at = [&](const float* scales, int id) { return scales[(size_t)max(id, 0) * a.c.heads + head]; };
   int p = mine.begin + wave;
-  int id = page_at(p);
+  int id = page_at(p), next = page_at(p + kWaves);
+  float ks_next = 0.f, vs_next = 0.f;
   if (p < mine.end) {
     load_keys(id);
     load_values(id);
+    ks_next = scale_at(a.c.ks, id);
+    vs_next = scale_at(a.c.vs, id);
   }
   for (; p < mine.end; p += kWaves) {
-    const int next = page_at(p + kWaves);
-    const size_t at = (size_t)max(id, 0) * a.c.heads + head;
-    const float ks = a.c.ks[at] * a.scale, vs = a.c.vs[at];
+    const int later = page_at(p + 2 * kWaves);
+    const float ks = ks_next * a.scale, vs = vs_next;
+    ks_next = scale_at(a.c.ks, next);
+    vs_next = scale_at(a.c.vs, next);
     kf4_t z[NT][4];
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
@@ -109,24 +117,23 @@ __global__ __launch_bounds__(64 * kWaves) void attn_rows_kernel(const AttnArgs a
           for (int n = 0; n < NT; ++n) z[n][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k, q[n][c][u], z[n][t], 0, 0, 0);
         }
     }
-    if (p + kWaves < mine.end) load_keys(next);
+    load_keys(next);
     const bool whole = id >= 0 && p * kPage >= low && p * kPage + kPage <= high;
     kh8_t w[NT][2];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       float best = -INFINITY;
 #pragma unroll
-      for (int t = 0; t < 4; ++t)
+      for (int t = 0; t < 4; ++t) z[n][t] *= ks;
+      if (!whole) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          float v = z[n][t][i] * ks;
-          if (!whole) {
-            const int token = p * kPage + 16 * kq + 4 * t + i;
-            if (id < 0 || token < sees[n].low || token >= sees[n].high) v = -INFINITY;
-          }
-          z[n][t][i] = v;
-          best = fmaxf(best, v);
+        for (int x = 0; x < 16; ++x) {
+          const int token = p * kPage + 16 * kq + x;
+          if (id < 0 || token < sees[n].low || token >= sees[n].high) z[n][x / 4][x % 4] = -INFINITY;
         }
+      }
+#pragma unroll
+      for (int x = 0; x < 16; ++x) best = fmaxf(best, z[n][x / 4][x % 4]);
       best = fmaxf(best, __shfl_xor(best, 16));
       best = fmaxf(best, __shfl_xor(best, 32));
       float ratio;
@@ -141,10 +148,9 @@ __global__ __launch_bounds__(64 * kWaves) void attn_rows_kernel(const AttnArgs a
       for (int t = 0; t < 4; ++t)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const bool dark = !whole && z[n][t][i] == -INFINITY;
           const float e = __builtin_amdgcn_exp2f(z[n][t][i] - top);
           sum += e;
-          w[n][t / 2][t % 2 * 4 + i] = (_Float16)(dark ? 0.f : e * ratio);
+          w[n][t / 2][t % 2 * 4 + i] = (_Float16)(e * ratio);
         }
       row[n].sum += sum;
     }
@@ -156,8 +162,9 @@ __global__ __launch_bounds__(64 * kWaves) void attn_rows_kernel(const AttnArgs a
 #pragma unroll
         for (int n = 0; n < NT; ++n) o[n][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v, w[n][u], o[n][d], 0, 0, 0);
       }
-    if (p + kWaves < mine.end) load_values(next);
+    load_values(next);
     id = next;
+    next = later;
   }
 
   // The wavefronts' sums: references first, then 16 rows at a time.
@@ -197,30 +204,47 @@ __global__ __launch_bounds__(64 * kWaves) void attn_rows_kernel(const AttnArgs a
       for (int x = 0; x < kWaves; ++x)
         sum += tops[x][r] == -INFINITY ? totals[x][r] : totals[x][r] * __builtin_amdgcn_exp2f(tops[x][r] - best);
       const size_t out = (size_t)(sp.first + r / a.group) * a.q_heads + head * a.group + r % a.group;
-      store_row<D>(a, split, out, d, v, best, sum);
+      store_row<D>(a, parts, part, out, d, v, best, sum);
     }
     __syncthreads();
   }
 }
 
-// y from the parts' sums, in their order.
+// y from the parts' sums, in their order: a workgroup has a row's head, its
+// groups of lanes take turns at the parts.
 template <int D>
-__global__ __launch_bounds__(256) void attn_join_kernel(const AttnArgs a) {
-  constexpr int L = D / 4;  // lanes of a head
+__global__ __launch_bounds__(256) void attn_join_kernel(const AttnArgs a, int block_rows) {
+  constexpr int L = D / 4, G = 256 / L;  // lanes of a row, groups
+  __shared__ kf4_t sums[256];
+  __shared__ float totals[G];
   const Span sp = span_of(a.b, blockIdx.x / a.b.max_rows);
-  const int j = blockIdx.x % a.b.max_rows, head = blockIdx.y * (256 / L) + threadIdx.x / L, d = threadIdx.x % L * 4;
-  if (j >= sp.n || head >= a.q_heads) return;
+  const int j = blockIdx.x % a.b.max_rows, head = blockIdx.y;
+  if (j >= sp.n) return;
+  const int block = (j * a.group + head % a.group) / block_rows * block_rows;
+  const Parts p = parts_of(a, range_of_rows(a, sp, block, min(block + block_rows, sp.n * a.group) - 1));
+  if (p.count == 1) return;  // written where it was computed
+  const int lane = threadIdx.x & 63, g = threadIdx.x / L, d = threadIdx.x % L * 4;
   const size_t rows = (size_t)a.b.rows * a.q_heads, r = (size_t)(sp.first + j) * a.q_heads + head;
-  const float* const tops = a.part + (size_t)a.splits * rows * D;
+  const kw2_t* const tops = reinterpret_cast<const kw2_t*>(a.part + (size_t)a.parts * rows * D) + r;
   float top = -INFINITY;
-  for (int i = 0; i < a.splits; ++i) top = fmaxf(top, tops[((size_t)i * rows + r) * 2]);
+  for (int i = lane; i < p.count; i += 64) top = fmaxf(top, __uint_as_float(tops[i * rows].x));
+  for (int o = 32; o; o >>= 1) top = fmaxf(top, __shfl_xor(top, o));
   kf4_t v = {0.f, 0.f, 0.f, 0.f};
   float sum = 0.f;
-  for (int i = 0; i < a.splits; ++i) {
-    const size_t at = (size_t)i * rows + r;
-    const float t = tops[at * 2], f = t == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(t - top);
-    sum += tops[at * 2 + 1] * f;
-    v += *reinterpret_cast<const kf4_t*>(a.part + at * D + d) * f;
+#pragma unroll 4
+  for (int i = g; i < p.count; i += G) {
+    const kw2_t t = tops[i * rows];
+    const float at = __uint_as_float(t.x), f = at == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(at - top);
+    sum += __uint_as_float(t.y) * f;
+    v += *reinterpret_cast<const kf4_t*>(a.part + (i * rows + r) * D + d) * f;
+  }
+  sums[threadIdx.x] = v;
+  if (threadIdx.x % L == 0) totals[g] = sum;
+  __syncthreads();
+  if (threadIdx.x >= L) return;
+  for (int i = 1; i < G; ++i) {
+    v += sums[i * L + threadIdx.x];
+    sum += totals[i];
   }
   finish_row(a, r * D + d, v, sum);
 }
@@ -237,26 +261,25 @@ hipError_t rows(const AttnArgs& a, int blocks, long long grid, hipStream_t s) {
 }
 
 template <int D>
-hipError_t join(const AttnArgs& a, hipStream_t s) {
-  constexpr int per = 256 / (D / 4);
-  const long long x = (long long)a.b.count * a.b.max_rows, y = (a.q_heads + per - 1) / per;
-  if (y > 65535 || !kv_grid_fits(x * y, 256)) return hipErrorInvalidConfiguration;
-  hipLaunchKernelGGL((attn_join_kernel<D>), dim3((unsigned)x, (unsigned)y), dim3(256), 0, s, a);
+hipError_t join(const AttnArgs& a, int block_rows, hipStream_t s) {
+  const long long x = (long long)a.b.count * a.b.max_rows;
+  if (a.q_heads > 65535 || !kv_grid_fits(x * a.q_heads, 256)) return hipErrorInvalidConfiguration;
+  hipLaunchKernelGGL((attn_join_kernel<D>), dim3((unsigned)x, (unsigned)a.q_heads), dim3(256), 0, s, a, block_rows);
   return hipGetLastError();
 }
 
 }  // namespace
 
 hipError_t launch_attn_rows(const AttnArgs& a, int dim, int blocks, hipStream_t s) {
-  const long long grid = (long long)a.b.count * a.c.heads * a.splits;
+  const long long grid = (long long)a.b.count * a.c.heads * a.parts;
   if (!kv_grid_fits(grid, 64 * kWaves)) return hipErrorInvalidConfiguration;
   if (dim == 64) return rows<64>(a, blocks, grid, s);
   return dim == 128 ? rows<128>(a, blocks, grid, s) : rows<256>(a, blocks, grid, s);
 }
 
-hipError_t launch_attn_join(const AttnArgs& a, int dim, hipStream_t s) {
-  if (dim == 64) return join<64>(a, s);
-  return dim == 128 ? join<128>(a, s) : join<256>(a, s);
+hipError_t launch_attn_join(const AttnArgs& a, int dim, int block_rows, hipStream_t s) {
+  if (dim == 64) return join<64>(a, block_rows, s);
+  return dim == 128 ? join<128>(a, block_rows, s) : join<256>(a, block_rows, s);
 }
 
 }  // namespace tern

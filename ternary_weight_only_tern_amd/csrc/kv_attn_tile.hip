@@ -20,7 +20,7 @@ namespace {
 constexpr int kTileWaves = 4;
 
 template <int D>
-__global__ __launch_bounds__(64 * kTileWaves) void attn_tile_kernel(const AttnArgs a) {
+__global__ __launch_bounds__(64 * kTileWaves, D <= 128 ? 2 : 1) void attn_tile_kernel(const AttnArgs a) {
   constexpr int THREADS = 64 * kTileWaves, ROWS = 32 * kTileWaves;
   constexpr int KS = D / 16;                        // products of 16 dimensions in a score
   constexpr int DB = D / 32;                        // blocks of 32 dimensions of the sums
@@ -33,13 +33,14 @@ __global__ __launch_bounds__(64 * kTileWaves) void attn_tile_kernel(const AttnAr
   bid /= a.c.heads;
   const int s = bid % a.b.count;
   bid /= a.b.count;
-  const int split = bid % a.splits, tile = a.tiles - 1 - bid / a.splits;
+  const int part = bid % a.parts, tile = a.tiles - 1 - bid / a.parts;
   const Span sp = span_of(a.b, s);
   const int total = sp.n * a.group;
   if (tile * ROWS >= total) return;
-  const int last_row = min(tile * ROWS + ROWS, total) - 1;
-  const Range all = range_of(a, sp, max(sp.from + tile * ROWS / a.group, 0), sp.from + last_row / a.group);
-  const Range mine = part_of(all, split, a.splits);
+  const Range all = range_of_rows(a, sp, tile * ROWS, min(tile * ROWS + ROWS, total) - 1);
+  const Parts parts = parts_of(a, all);
+  if (part >= parts.count) return;
+  const Range mine = part_of(all, parts, part);
 
   const int r = tile * ROWS + wave * 32 + c32, j = r / a.group, h = r % a.group;
   const bool there = r < total;
@@ -79,12 +80,13 @@ __global__ __launch_bounds__(64 * kTileWaves) void attn_tile_kernel(const AttnAr
   auto page_at = [&](int p) { return p < mine.end ? __builtin_amdgcn_readfirstlane(page_of(a.b, a.c, s, p)) : -1; };
   auto load = [&](int id) {
     const size_t at = ((size_t)max(id, 0) * a.c.heads + head) * (kPage * D);
+    const __amdgpu_buffer_rsrc_t fk = kv_buffer(a.c.k + at, id < 0 ? 0 : kPage * D), fv = kv_buffer(a.c.v + at, id < 0 ? 0 : kPage * D);
 #pragma unroll
     for (int i = 0; i < PIECES; ++i) {
       const int st = i * kTileWaves + wave;
-      kr[i] = *reinterpret_cast<const kw4_t*>(a.c.k + at + ((st / 4 * 4 + lane / 4 % 4) * 64 + st % 4 * 16 + lane / 16 * 4 + lane % 4) * 16);
+      kr[i] = kv_load16(fk, ((st / 4 * 4 + lane / 4 % 4) * 64 + st % 4 * 16 + lane / 16 * 4 + lane % 4) * 16);
       const int part = st % 4, d = st / 4 * 64 + lane;
-      vr[i] = *reinterpret_cast<const kw4_t*>(a.c.v + at + ((d / 16 * 4 + part) * 16 + d % 16) * 16);
+      vr[i] = kv_load16(fv, ((d / 16 * 4 + part) * 16 + d % 16) * 16);
     }
   };
   auto decode = [&](kw4_t* ks, kw4_t* vs) {
@@ -115,20 +117,22 @@ __global__ __launch_bounds__(64 * kTileWaves) void attn_tile_kernel(const AttnAr
         z[b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(kh8_t, ks[(i * 2 + b) * 64 + lane]), q[i], z[b], 0, 0, 0);
     }
     const bool whole = id >= 0 && p * kPage >= low && p * kPage + kPage <= high;
-    float best = -INFINITY;
+    float by = kscale, best = -INFINITY;  // the scores are by z
+    if (!whole) {
+#pragma unroll
+      for (int b = 0; b < 2; ++b)
+#pragma unroll
+        for (int v = 0; v < 16; ++v) {
+          const int token = p * kPage + 32 * b + 8 * (v / 4) + 4 * hq + v % 4;
+          z[b][v] = id < 0 || token < sees.low || token >= sees.high ? -INFINITY : z[b][v] * by;
+        }
+      by = 1.0f;
+    }
 #pragma unroll
     for (int b = 0; b < 2; ++b)
 #pragma unroll
-      for (int v = 0; v < 16; ++v) {
-        float x = z[b][v] * kscale;
-        if (!whole) {
-          const int token = p * kPage + 32 * b + 8 * (v / 4) + 4 * hq + v % 4;
-          if (id < 0 || token < sees.low || token >= sees.high) x = -INFINITY;
-        }
-        z[b][v] = x;
-        best = fmaxf(best, x);
-      }
-    best = fmaxf(best, __shfl_xor(best, 32));
+      for (int v = 0; v < 16; ++v) best = fmaxf(best, z[b][v]);
+    best = fmaxf(best, __shfl_xor(best, 32)) * by;
     float ratio;
     const float factor = step_row(row, best, vscale, &ratio);
     if (__any(factor != 1.0f)) {
@@ -142,10 +146,9 @@ __global__ __launch_bounds__(64 * kTileWaves) void attn_tile_kernel(const AttnAr
     for (int b = 0; b < 2; ++b)
 #pragma unroll
       for (int v = 0; v < 16; ++v) {
-        const bool dark = !whole && z[b][v] == -INFINITY;
-        const float e = __builtin_amdgcn_exp2f(z[b][v] - top);
+        const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(z[b][v], by, -top));
         sum += e;
-        w[b * 2 + v / 8][v % 8] = (_Float16)(dark ? 0.f : e * ratio);
+        w[b * 2 + v / 8][v % 8] = (_Float16)(e * ratio);
       }
     row.sum += sum;
 #pragma unroll
@@ -182,7 +185,7 @@ __global__ __launch_bounds__(64 * kTileWaves) void attn_tile_kernel(const AttnAr
 #pragma unroll
     for (int v = 0; v < 4; ++v) {
       const kf4_t x = {o[d][4 * v], o[d][4 * v + 1], o[d][4 * v + 2], o[d][4 * v + 3]};
-      store_row<D>(a, split, out, d * 32 + 8 * v + 4 * hq, x * (row.unit / kLift), row.top, sum);
+      store_row<D>(a, parts, part, out, d * 32 + 8 * v + 4 * hq, x * (row.unit / kLift), row.top, sum);
     }
 }
 
@@ -195,7 +198,7 @@ hipError_t tile(const AttnArgs& a, long long grid, hipStream_t s) {
 }  // namespace
 
 hipError_t launch_attn_tile(const AttnArgs& a, int dim, hipStream_t s) {
-  const long long grid = (long long)a.b.count * a.c.heads * a.splits * a.tiles;
+  const long long grid = (long long)a.b.count * a.c.heads * a.parts * a.tiles;
   if (!kv_grid_fits(grid, 64 * kTileWaves)) return hipErrorInvalidConfiguration;
   if (dim == 64) return tile<64>(a, grid, s);
   return dim == 128 ? tile<128>(a, grid, s) : tile<256>(a, grid, s);
