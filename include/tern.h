@@ -606,16 +606,16 @@ tern_status tern_kv_read(const tern_kv *c, const tern_kv_batch *b, void *k, void
  * it, whatever they or their scales hold.  Scores and sums are FP32; the
  * softmax's weights meet the codes of v in FP16 (11 bits each).  scale finite,
  * not negative.  ws: tern_kv_attention_workspace_bytes (0 for arguments that
- * are refused), 16-byte aligned, enough for every batch with no more rows and
- * no larger max_len too; calls that overlap in time must not share it. */
+ * are refused), 16-byte aligned, enough for every batch with no more
+ * sequences and rows and no larger max_len too; calls that overlap in time must not share it. */
 size_t tern_kv_attention_workspace_bytes(const tern_kv *c, const tern_kv_batch *b, int32_t q_heads);
 tern_status tern_kv_attention(const tern_kv *c, const tern_kv_batch *b, const uint16_t *q, int64_t q_stride,
                               int32_t q_heads, float scale, int32_t window, int32_t causal, uint16_t *y, void *ws,
                               size_t ws_bytes, void *stream);
 
 /* Which way an attention call goes, for tests and measurements (host-only):
- * the parts the context is cut into, P, on the kernel for few rows, -1 - P on
- * tiles; 0: nothing to do; -1: refused. */
+ * the pieces P that the kernel for few rows takes, -1 - P for the parts of the
+ * context on tiles; 0: nothing to do; -1: refused. */
 int32_t tern_kv_attention_parts(const tern_kv *c, const tern_kv_batch *b, int32_t q_heads, int32_t window);
 
 /* Measurement aid, not part of the product: a plain streaming read of

@@ -28,6 +28,7 @@ namespace tern {
 constexpr int kPage = TERN_KV_PAGE;
 // Positions and rows stay below these, so that their sums fit 32 bits.
 constexpr int kMaxTokens = 1 << 30, kMaxRows = 1 << 29;
+constexpr int kMaxStride = 1 << 23;  // of q in attention: 64 rows lie in one buffer
 
 // Turning and norm of a head's values (tern_rotary).
 struct Rotary {
@@ -84,11 +85,16 @@ struct AttnArgs {
   const uint16_t* q;
   int64_t q_stride;
   uint16_t* y;         // [rows][q_heads][dim]
-  float* part;         // [parts][rows][q_heads][dim], then [parts][rows][q_heads][2]
+  // Few rows: pieces of the line of all pages (a.whole: units), `per` pages each
+  // at least; their sums [pieces][2][max_rows * group][dim] and references and
+  // sums of weights [pieces][2][max_rows * group][2] in part; info: a unit's first
+  // piece and how many it has.  Tiles (tiles > 0): parts of the context at most,
+  // `per` pages each at least; part: [parts][rows][q_heads][dim], then [..][2].
+  float* part;
+  int2* info;
   float scale;         // times log2(e)
   int32_t q_heads, group, window, causal;
-  int32_t parts, per;  // parts of the context at most, their pages at least
-  int32_t tiles;
+  int32_t pieces, whole, parts, per, tiles;
 };
 
 // Rows (of a sequence, times the query heads of one cache head) of one
@@ -101,8 +107,7 @@ hipError_t launch_kv_read(const ReadArgs& a, int dim, hipStream_t s);
 // blocks: of 16 rows, 1, 2 or 4 (2 at most at dim 256)
 hipError_t launch_attn_rows(const AttnArgs& a, int dim, int blocks, hipStream_t s);
 hipError_t launch_attn_tile(const AttnArgs& a, int dim, hipStream_t s);
-// block_rows: of a workgroup of the launch before
-hipError_t launch_attn_join(const AttnArgs& a, int dim, int block_rows, hipStream_t s);
+hipError_t launch_attn_join(const AttnArgs& a, int dim, hipStream_t s);
 
 // A grid's threads have to be countable in 32 bits.
 inline bool kv_grid_fits(long long blocks, int threads) { return blocks * threads < (1ll << 32); }
@@ -117,6 +122,14 @@ typedef float kf16_t __attribute__((ext_vector_type(16)));
 typedef uint32_t kw2_t __attribute__((ext_vector_type(2)));
 typedef uint32_t kw4_t __attribute__((ext_vector_type(4)));
 
+// An element of an array that nothing writes while the kernel runs: with an
+// index that is the same in every lane a scalar load, which does not queue
+// behind the vector loads in flight, whatever the kernel stores elsewhere.
+template <class T>
+__device__ inline T kv_const(const T* p, size_t i) {
+  return ((const __attribute__((address_space(4))) T*)p)[i];
+}
+
 // A sequence's rows in the arrays of rows and its place in the cache.  Rows
 // beyond max_rows or behind the arrays' end are left out, whatever start says.
 struct Span {
@@ -129,11 +142,11 @@ __device__ inline Span span_of(const Batch& b, int s) {
   int n = b.max_rows;
   r.first = s * b.max_rows;
   if (b.start) {
-    r.first = min(max(b.start[s], 0), b.rows);
-    n = min(max(b.start[s + 1] - r.first, 0), b.rows - r.first);
+    r.first = min(max(kv_const(b.start, s), 0), b.rows);
+    n = min(max(kv_const(b.start, s + 1) - r.first, 0), b.rows - r.first);
   }
   r.n = min(n, b.max_rows);
-  r.len = min(max(b.len[s], 0), kMaxTokens);
+  r.len = min(max(kv_const(b.len, s), 0), kMaxTokens);
   r.from = r.len - n;
   return r;
 }
@@ -141,7 +154,7 @@ __device__ inline Span span_of(const Batch& b, int s) {
 // The page of a sequence's tokens 64 p ..; -1: none.
 __device__ inline int page_of(const Batch& b, const Cache& c, int s, int p) {
   if (p >= b.max_pages) return -1;
-  const int id = b.pages[(size_t)s * b.max_pages + p];
+  const int id = kv_const(b.pages, (size_t)s * b.max_pages + p);
   return id >= 0 && id < c.pages ? id : -1;
 }
 
@@ -168,8 +181,11 @@ __device__ inline __amdgpu_buffer_rsrc_t kv_buffer(const void* p, int bytes) {
   return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>((uint64_t)hi << 32 | lo), (short)0,
                                            __builtin_amdgcn_readfirstlane(bytes), 0x00020000);
 }
+constexpr int kFarAway = (int)0x80000000;  // an offset past every buffer
+constexpr int kv_stream = 2;  // bytes that are read once pass the caches by
+template <int AUX = 0>
 __device__ inline kw4_t kv_load16(__amdgpu_buffer_rsrc_t r, int offset) {
-  return __builtin_bit_cast(kw4_t, __builtin_amdgcn_raw_buffer_load_b128(r, offset, 0, 0));
+  return __builtin_bit_cast(kw4_t, __builtin_amdgcn_raw_buffer_load_b128(r, offset, 0, AUX));
 }
 
 __device__ inline float kv_half(uint16_t v) { return (float)__builtin_bit_cast(_Float16, v); }

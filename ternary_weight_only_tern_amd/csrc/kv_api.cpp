@@ -130,12 +130,14 @@ int items_of(const tern_kv_batch* b) { return (b->max_rows + 2 * (tern::kPage - 
 // How attention runs.
 struct AttnPlan {
   int blocks;  // of 16 rows in the kernel for few rows; 0: tiles
-  int block_rows, tiles, parts, per;
+  int pieces, whole, parts, per, tiles;
+  bool join;
+  size_t rows, info;  // of partial sums, and units whose pieces are noted
 };
-constexpr int kPartPages = 4;       // the least of a part
-constexpr int kRowsTarget = 2048;   // workgroups
-constexpr int kTileTarget = 512;
-constexpr int kPartRows = 2 * kRowsTarget * 64;  // rows of all parts at most, either way (plan_of)
+constexpr int kPieces = 2048;     // of the kernel for few rows: two wavefronts on each SIMD
+constexpr int kWholePages = 1;    // pages of a unit that is not cut
+constexpr int kTileTarget = 512;  // workgroups on tiles
+constexpr int kPartPages = 4;     // the least of a part on tiles
 
 int pages_of(const tern_kv_batch* b, int window) {
   long long tokens = b->max_len;
@@ -143,29 +145,51 @@ int pages_of(const tern_kv_batch* b, int window) {
   return (int)((tokens + tern::kPage - 1) / tern::kPage);
 }
 
+// Rows on which a unit goes to the kernel for few rows.
+int few_rows(int dim) { return dim == 256 ? 32 : 64; }
+
 AttnPlan plan_of(const tern_kv* c, const tern_kv_batch* b, int group, int window) {
   AttnPlan p = {};
-  const long long rows = (long long)b->max_rows * group;
-  const int most = c->dim == 256 ? 32 : 64;
-  if (rows <= most) p.blocks = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
-  p.block_rows = p.blocks ? 16 * p.blocks : tern::kAttnTile;
-  p.tiles = (int)((rows + p.block_rows - 1) / p.block_rows);
-  const long long groups = (long long)p.tiles * c->heads * b->count;
-  const int target = p.blocks ? kRowsTarget : kTileTarget, pages = pages_of(b, window);
-  p.per = std::max(kPartPages, (int)std::min<long long>((groups * pages + target - 1) / target, pages));
+  const long long rows = (long long)b->max_rows * group, units = (long long)b->count * c->heads;
+  const int pages = pages_of(b, window);
+  if (rows <= few_rows(c->dim)) {
+    p.blocks = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
+    p.whole = pages <= kWholePages;
+    p.pieces = (int)(p.whole ? std::min<long long>(units, 1ll << 30) : std::min<long long>(p.blocks * c->dim > 128 ? kPieces / 2 : kPieces, units * pages));
+    p.per = 1;
+    p.join = !p.whole;
+    p.rows = p.join ? (size_t)p.pieces * 2 * rows : 0;
+    p.info = p.join ? units : 0;
+    return p;
+  }
+  p.tiles = (int)((rows + tern::kAttnTile - 1) / tern::kAttnTile);
+  const long long groups = p.tiles * units;
+  p.per = std::max(kPartPages, (int)std::min<long long>((groups * pages + kTileTarget - 1) / kTileTarget, pages));
   p.parts = std::max(1, (pages + p.per - 1) / p.per);
+  p.join = p.parts > 1;
+  p.rows = p.join ? (size_t)p.parts * b->rows * group * c->heads : 0;
   return p;
 }
 
-size_t attn_need(const AttnPlan& p, const tern_kv* c, const tern_kv_batch* b, int q_heads) {
-  return p.parts > 1 ? (size_t)p.parts * b->rows * q_heads * (c->dim + 2) * 4 : 0;
+size_t attn_need(const AttnPlan& p, const tern_kv* c) { return p.rows * (c->dim + 2) * 4 + p.info * 8; }
+
+// The most that any batch with no more sequences and rows and no larger
+// max_len needs: few rows leave at most kPieces pairs of slots, parts of tiles
+// come to at most twice kTileTarget workgroups.
+size_t attn_need_upto(const tern_kv* c, const tern_kv_batch* b, int group) {
+  const double rows = (double)b->rows * group, pages = pages_of(b, 0);
+  const double few = 2.0 * std::min<double>(kPieces, (double)b->count * c->heads * pages) * std::min<double>(rows, few_rows(c->dim));
+  const double tiles = std::min(rows * c->heads * std::ceil(pages / kPartPages), 2.0 * kTileTarget * tern::kAttnTile);
+  return (size_t)(std::max(few, tiles) * (c->dim + 2) * 4) + (size_t)b->count * c->heads * 8;
 }
 
 tern_status check_heads(const tern_kv* c, const tern_kv_batch* b, int q_heads) {
   if (q_heads < 1 || q_heads % c->heads)
     return fail(TERN_E_INVAL, "%d query heads over %d cache heads", q_heads, c->heads);
-  if (q_heads > (1 << 20) || (long long)b->max_rows * (q_heads / c->heads) > (1 << 30))
+  if (q_heads > 65535 || (long long)b->max_rows * (q_heads / c->heads) > (1 << 30))
     return fail(TERN_E_UNSUPPORTED, "%d query heads, %d rows of a sequence: too many", q_heads, b->max_rows);
+  if ((long long)b->count * c->heads > (1 << 24) || (long long)b->count * c->heads * b->max_pages > 0x7fffffff)
+    return fail(TERN_E_UNSUPPORTED, "%d cache heads of %d sequences, %d pages: too many", c->heads, b->count, b->max_pages);
   return TERN_OK;
 }
 
@@ -293,16 +317,14 @@ tern_status tern_kv_read(const tern_kv* c, const tern_kv_batch* b, void* k, void
 
 size_t tern_kv_attention_workspace_bytes(const tern_kv* c, const tern_kv_batch* b, int32_t q_heads) {
   if (check_shape(c) != TERN_OK || check_sizes(b) != TERN_OK || check_heads(c, b, q_heads) != TERN_OK) return 0;
-  const long long parts = (pages_of(b, 0) + kPartPages - 1) / kPartPages;
-  const double rows = (double)b->rows * q_heads * parts;
-  return (size_t)std::max(256.0, std::min(rows, (double)kPartRows) * (c->dim + 2) * 4);
+  return std::max<size_t>(256, attn_need_upto(c, b, q_heads / c->heads));
 }
 
 int32_t tern_kv_attention_parts(const tern_kv* c, const tern_kv_batch* b, int32_t q_heads, int32_t window) {
   if (check_shape(c) != TERN_OK || check_sizes(b) != TERN_OK || check_heads(c, b, q_heads) != TERN_OK || window < 0) return -1;
   if (nothing(b)) return 0;
   const AttnPlan p = plan_of(c, b, q_heads / c->heads, window);
-  return p.blocks ? p.parts : -1 - p.parts;
+  return p.blocks ? p.pieces : -1 - p.parts;
 }
 
 tern_status tern_kv_attention(const tern_kv* c, const tern_kv_batch* b, const uint16_t* q, int64_t q_stride,
@@ -317,9 +339,10 @@ tern_status tern_kv_attention(const tern_kv* c, const tern_kv_batch* b, const ui
   if (nothing(b)) return TERN_OK;
   KV_TRY(check_arrays(c, b));
   KV_TRY(check_rows(q, q_stride, "q"));
+  if (q_stride > tern::kMaxStride) return fail(TERN_E_UNSUPPORTED, "q has the row stride %lld: %d at most", (long long)q_stride, tern::kMaxStride);
   KV_TRY(check_ptr(y, "y", 16));
   const AttnPlan p = plan_of(c, b, q_heads / c->heads, window);
-  const size_t need = attn_need(p, c, b, q_heads);
+  const size_t need = attn_need(p, c);
   if (need && (!ws || ws_bytes < need))
     return fail(TERN_E_WORKSPACE, "workspace of %zu bytes, %zu are needed", ws ? ws_bytes : (size_t)0, need);
   if (need) KV_TRY(check_ptr(ws, "workspace", 16));
@@ -335,6 +358,9 @@ tern_status tern_kv_attention(const tern_kv* c, const tern_kv_batch* b, const ui
   a.group = q_heads / c->heads;
   a.window = window;
   a.causal = causal != 0;
+  a.info = (int2*)(a.part + p.rows * (c->dim + 2));
+  a.pieces = p.pieces;
+  a.whole = p.whole;
   a.parts = p.parts;
   a.per = p.per;
   a.tiles = p.tiles;
@@ -343,7 +369,7 @@ tern_status tern_kv_attention(const tern_kv* c, const tern_kv_batch* b, const ui
     KV_HIP(tern::launch_attn_rows(a, c->dim, p.blocks, s));
   else
     KV_HIP(tern::launch_attn_tile(a, c->dim, s));
-  if (a.parts > 1) KV_HIP(tern::launch_attn_join(a, c->dim, p.block_rows, s));
+  if (p.join) KV_HIP(tern::launch_attn_join(a, c->dim, s));
   return TERN_OK;
 }
 

@@ -1,111 +1,236 @@
 // Attention of few rows over the 8-bit cache (tern_kv_attention in tern.h):
 //   y = sum_t exp(z_t) v_t / sum_t exp(z_t),  z_t = scale q . k_t.
 //
-// The rows of a sequence and the query heads that share a cache head, R =
-// rows * group of them, are the 16 columns of a matrix operand (NT of them).
-// A workgroup's four wavefronts walk the pages of their part of the context,
-// a page each at a time: 16-byte loads of codes in operand order (kv.h), K^T
-// products in FP32 from exact FP16 codes, one page's softmax in registers, the
-// weights rounded to FP16 (the only rounding; 2^-11 of a weight, as the
-// output's own) against the value codes.  The keys' scale multiplies the
-// scores, the values' scale the weights, in FP32.  The next page's keys are
-// requested when this page's have been multiplied, the values likewise.  Then
-// the wavefronts' sums meet in LDS, in order, and those of the parts in
-// attn_join_kernel.
+// A unit is a sequence's cache head: its rows, R = rows * group of them (the
+// query heads that share the cache head), are the 16 columns of a matrix
+// operand (NT of them), its pages a run.  All units' pages form one line, cut
+// into equal pieces by the lengths that the device finds, a piece for every
+// wavefront: a ragged batch fills the card evenly, and nothing waits for
+// another wavefront.  A wavefront walks its pages one by one: 16-byte loads of
+// codes in operand order (kv.h), K^T products in FP32 from exact FP16 codes, the
+// page's softmax in registers, the weights rounded to FP16 (the only rounding;
+// 2^-11 of a weight, as the output's own) against the value codes.  The keys'
+// scale multiplies the scores, the values' scale the weights, in FP32.  The
+// next page's keys are requested when this page's have been multiplied, the
+// values likewise, page numbers two pages ahead, and the next unit's queries
+// when this unit's last scores are done.  A unit that lies in one piece goes
+// to y; others leave their sums in the workspace, at most two a wavefront,
+// which attn_join_kernel adds in the pieces' order.
 #include "kv_attn.h"
 
 namespace tern {
 namespace {
 
-constexpr int kWaves = 4;
+// A page of the line: sequence, head and page, the page's number in the cache;
+// left: pages behind it that are this wavefront's.
+struct Step {
+  int s, head, p, id, left;
+};
+
+// A sequence's pages, for the cursor along the line.
+struct Run {
+  Span sp;
+  Range r;
+};
+__device__ inline Run run_of(const AttnArgs& a, int s) {
+  Run x;
+  x.sp = span_of(a.b, s);
+  x.r = range_of(a, x.sp, max(x.sp.from, 0), x.sp.from + x.sp.n - 1);
+  if (x.sp.n <= 0) x.r = {0, 0};
+  return x;
+}
+__device__ inline int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
+// Where this wavefront's pieces of a unit that does not lie in one piece go: two
+// slots a wavefront, the first for a unit that others have begun.
+struct Slot {
+  float* sums;  // [R][D]
+  kw2_t* tops;  // [R]
+};
+template <int D>
+__device__ inline Slot slot_of(const AttnArgs& a, long long wave, int which) {
+  const size_t rows = (size_t)a.b.max_rows * a.group, at = (size_t)(wave * 2 + which) * rows;
+  return {a.part + at * D, reinterpret_cast<kw2_t*>(a.part + (size_t)a.pieces * 2 * rows * D) + at};
+}
 
 template <int D, int NT>
-__global__ __launch_bounds__(64 * kWaves, NT <= 2 && D <= 128 ? 2 : 1) void attn_rows_kernel(const AttnArgs a) {
+__global__ __launch_bounds__(64, NT * D <= 128 ? 2 : 1) void attn_rows_kernel(const AttnArgs a) {
   constexpr int C = D / 64, DT = D / 16;
-  constexpr int P = D + 4;  // pitch of a row in LDS: rows fall in other banks
-  __shared__ float sums[kWaves * 16 * P];
-  __shared__ float tops[kWaves][16 * NT], totals[kWaves][16 * NT];
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int col = lane & 15, kq = lane >> 4;
-  const int part = blockIdx.x % a.parts, head = blockIdx.x / a.parts % a.c.heads;
-  const int s = blockIdx.x / a.parts / a.c.heads;
-  const Span sp = span_of(a.b, s);
-  const int total = sp.n * a.group;
-  if (total <= 0) return;
-  const Range all = range_of_rows(a, sp, 0, total - 1);
-  const Parts parts = parts_of(a, all);
-  if (part >= parts.count) return;
-  const Range mine = part_of(all, parts, part);
+  const int lane = threadIdx.x, col = lane & 15, kq = lane >> 4;
+  const int wave = blockIdx.x;
 
-  // rows of the operand: j * group + h
+  // The line's length, then where this wavefront's piece begins.
+  Step now = {0, 0, 0, -1, -1};
+  Run run = {};
+  uint32_t per = 1;
+  if (a.whole) {  // a unit each, whatever its length
+    now.s = wave / a.c.heads;
+    now.head = wave % a.c.heads;
+    run = run_of(a, now.s);
+    now.p = run.r.begin;
+    now.left = run.r.end - run.r.begin - 1;
+  } else {
+    auto pages = [&](int x) {
+      if (x >= a.b.count) return 0;
+      const Run r = run_of(a, x);
+      return r.r.end - r.r.begin;
+    };
+    const int n0 = pages(lane);
+    uint32_t total = 0;
+    for (int s0 = 0; s0 < a.b.count; s0 += 64) {
+      int n = s0 ? pages(s0 + lane) : n0;
+      for (int i = 1; i < 64; i <<= 1) n += __shfl_xor(n, i);
+      total += uniform(n);
+    }
+    total *= a.c.heads;
+    per = max((uint32_t)a.per, (total + a.pieces - 1) / a.pieces);
+    const uint32_t from = wave * per;
+    if (from < total) {
+      uint32_t before = 0;  // pages of the sequences before s0
+      for (int s0 = 0;; s0 += 64) {
+        const int n = s0 ? pages(s0 + lane) : n0;
+        int upto = n;
+        for (int i = 1; i < 64; i <<= 1) {
+          const int other = __shfl_up(upto, i);
+          if (lane >= i) upto += other;
+        }
+        const unsigned long long mine = __ballot(from < (before + upto) * a.c.heads);
+        if (mine || s0 + 64 >= a.b.count) {
+          const int at = mine ? __ffsll(mine) - 1 : 0;
+          now.s = s0 + at;
+          before += uniform(__shfl(upto - n, at));
+          break;
+        }
+        before += uniform(__shfl(upto, 63));
+      }
+      run = run_of(a, now.s);
+      const int n = max(run.r.end - run.r.begin, 1), off = (int)(from - before * a.c.heads);
+      now.head = off / n;
+      now.p = run.r.begin + off % n;
+      now.left = (int)(min(per, total - from) - 1);
+    }
+  }
+  // units without pages: their rows are zero
+  for (int u = wave; u < a.b.count * a.c.heads; u += a.pieces) {
+    const Run x = run_of(a, u / a.c.heads);
+    if (x.r.end > x.r.begin) continue;
+    for (int i = lane; i < x.sp.n * a.group * (D / 4); i += 64) {
+      const int r = i / (D / 4);
+      const size_t out = (size_t)(x.sp.first + r / a.group) * a.q_heads + u % a.c.heads * a.group + r % a.group;
+      finish_row(a, out * D + i % (D / 4) * 4, kf4_t{0.f, 0.f, 0.f, 0.f}, 0.f);
+    }
+    if (lane == 0 && !a.whole) a.info[u] = make_int2(0, 1);
+  }
+  if (now.left < 0) return;
+
+  // The step behind one; the run it lies in.
+  auto number = [&](const Step& x) { return uniform(page_of(a.b, a.c, x.s, x.p)); };
+  auto behind = [&](Step x, Run& in) {
+    if (x.left <= 0) return Step{-1, 0, 0, -1, -1};
+    --x.left;
+    if (++x.p >= in.r.end) {
+      if (++x.head >= a.c.heads) {  // the line goes on: a sequence with pages follows
+        x.head = 0;
+        do {
+          if (++x.s >= a.b.count) return Step{-1, 0, 0, -1, -1};
+          in = run_of(a, x.s);
+        } while (in.r.end <= in.r.begin);
+      }
+      x.p = in.r.begin;
+    }
+    x.id = number(x);
+    return x;
+  };
+
   kh8_t q[NT][C][2];
   Sees sees[NT];
-  int low = 0, high = 0x7fffffff;  // tokens that every row sees
+  int low, high;  // tokens that every row sees
   Row row[NT];
   kf4_t o[NT][DT];
+  // of a unit's row: its place in q (bytes) and y (heads), from the first's
+  int place_q[NT], place_y[NT];
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
-    const int r = n * 16 + col, j = r / a.group, h = r % a.group;
-    const bool there = r < total;
-    sees[n] = sees_of(a, sp, sp.from + j, there);
-    if (there) {
-      low = max(low, sees[n].low);
-      high = min(high, sees[n].high);
+    const int r = n * 16 + col;
+    place_q[n] = (r / a.group * (int)a.q_stride + r % a.group * D + 16 * kq) * 2;
+    place_y[n] = r / a.group * a.q_heads + r % a.group;
+  }
+  auto load_q = [&](const Step& x, const Span& sp) {
+    const __amdgpu_buffer_rsrc_t from = kv_buffer(a.q + sp.first * a.q_stride + x.head * a.group * D, 0x7fffffff);
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const int at = n * 16 + col < sp.n * a.group ? place_q[n] : kFarAway;
+#pragma unroll
+      for (int c = 0; c < C; ++c)
+#pragma unroll
+        for (int u = 0; u < 2; ++u) q[n][c][u] = __builtin_bit_cast(kh8_t, kv_load16(from, at + 128 * c + 16 * u));
     }
-    const uint16_t* const from = a.q + (int64_t)(sp.first + j) * a.q_stride + (head * a.group + h) * D;
+  };
+  auto begin_rows = [&](const Span& sp) {
+    low = 0;
+    high = 0x7fffffff;
 #pragma unroll
-    for (int c = 0; c < C; ++c)
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        q[n][c][u] = kh8_t{0, 0, 0, 0, 0, 0, 0, 0};
-        if (there) q[n][c][u] = *reinterpret_cast<const kh8_t*>(from + 64 * c + 16 * kq + 8 * u);
+    for (int n = 0; n < NT; ++n) {
+      const int r = n * 16 + col;
+      const bool there = r < sp.n * a.group;
+      sees[n] = sees_of(a, sp, sp.from + r / a.group, there);
+      if (there) {
+        low = max(low, sees[n].low);
+        high = min(high, sees[n].high);
       }
-    row[n] = {-INFINITY, 0.f, 0.f};
+      row[n] = {-INFINITY, 0.f, 0.f};
 #pragma unroll
-    for (int d = 0; d < DT; ++d) o[n][d] = kf4_t{0.f, 0.f, 0.f, 0.f};
-  }
-  for (int i = 1; i < 16; i <<= 1) {
-    low = max(low, __shfl_xor(low, i));
-    high = min(high, __shfl_xor(high, i));
-  }
-  low = __builtin_amdgcn_readfirstlane(low);
-  high = __builtin_amdgcn_readfirstlane(high);
+      for (int d = 0; d < DT; ++d) o[n][d] = kf4_t{0.f, 0.f, 0.f, 0.f};
+    }
+    for (int i = 1; i < 16; i <<= 1) {
+      low = max(low, __shfl_xor(low, i));
+      high = min(high, __shfl_xor(high, i));
+    }
+    low = uniform(low);
+    high = uniform(high);
+  };
 
-  kw4_t kr[C][4], vr[DT];
   // a page that is not there reads as zeros, and is masked
-  auto page_at = [&](int p) { return p < mine.end ? __builtin_amdgcn_readfirstlane(page_of(a.b, a.c, s, p)) : -1; };
-  auto load_keys = [&](int id) {
-    const __amdgpu_buffer_rsrc_t from = kv_buffer(a.c.k + ((size_t)max(id, 0) * a.c.heads + head) * (kPage * D), id < 0 ? 0 : kPage * D);
+  kw4_t kr[C][4], vr[DT];
+  auto page_at = [&](const uint8_t* pages, const Step& x) {
+    return kv_buffer(pages + ((size_t)max(x.id, 0) * a.c.heads + x.head) * (kPage * D), x.id < 0 ? 0 : kPage * D);
+  };
+  auto load_keys = [&](const Step& x) {
+    const __amdgpu_buffer_rsrc_t from = page_at(a.c.k, x);
 #pragma unroll
     for (int c = 0; c < C; ++c)
 #pragma unroll
-      for (int t = 0; t < 4; ++t) kr[c][t] = kv_load16(from, ((4 * c + t) * 64 + lane) * 16);
+      for (int t = 0; t < 4; ++t) kr[c][t] = kv_load16<kv_stream>(from, ((4 * c + t) * 64 + lane) * 16);
   };
-  auto load_values = [&](int id) {
-    const __amdgpu_buffer_rsrc_t from = kv_buffer(a.c.v + ((size_t)max(id, 0) * a.c.heads + head) * (kPage * D), id < 0 ? 0 : kPage * D);
+  auto load_values = [&](const Step& x) {
+    const __amdgpu_buffer_rsrc_t from = page_at(a.c.v, x);
 #pragma unroll
-    for (int d = 0; d < DT; ++d) vr[d] = kv_load16(from, (d * 64 + lane) * 16);
+    for (int d = 0; d < DT; ++d) vr[d] = kv_load16<kv_stream>(from, (d * 64 + lane) * 16);
   };
+  auto scale_at = [&](const float* scales, const Step& x) { return kv_const(scales, (size_t)max(x.id, 0) * a.c.heads + x.head); };
 
-  // Page numbers are read two pages ahead, scales one: their use never waits.
-  auto scale_at = [&](const float* scales, int id) { return scales[(size_t)max(id, 0) * a.c.heads + head]; };
-  int p = mine.begin + wave;
-  int id = page_at(p), next = page_at(p + kWaves);
-  float ks_next = 0.f, vs_next = 0.f;
-  if (p < mine.end) {
-    load_keys(id);
-    load_values(id);
-    ks_next = scale_at(a.c.ks, id);
-    vs_next = scale_at(a.c.vs, id);
-  }
-  for (; p < mine.end; p += kWaves) {
-    const int later = page_at(p + 2 * kWaves);
+  now.id = number(now);
+  Run ahead = run;  // of the step that is looked at first
+  Step next = behind(now, ahead);
+  Run run_next = ahead;
+  load_keys(now);
+  load_q(now, run.sp);
+  load_values(now);
+  float ks_next = scale_at(a.c.ks, now), vs_next = scale_at(a.c.vs, now);
+  begin_rows(run.sp);
+  bool opened = now.p == run.r.begin;  // the unit begins in this piece,
+  int room = now.left + 1;             // which had so many pages left then
+
+  for (;;) {
+    const Step later = behind(next, ahead);
     const float ks = ks_next * a.scale, vs = vs_next;
     ks_next = scale_at(a.c.ks, next);
     vs_next = scale_at(a.c.vs, next);
+    const bool last = next.left < 0 || next.head != now.head || next.s != now.s;  // of the unit, here
     kf4_t z[NT][4];
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
+      if (NT > 1) __builtin_amdgcn_sched_barrier(0);  // decoding far ahead takes registers that are not there
 #pragma unroll
       for (int n = 0; n < NT; ++n) z[n][t] = kf4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -117,8 +242,10 @@ __global__ __launch_bounds__(64 * kWaves, NT <= 2 && D <= 128 ? 2 : 1) void attn
           for (int n = 0; n < NT; ++n) z[n][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k, q[n][c][u], z[n][t], 0, 0, 0);
         }
     }
+    __builtin_amdgcn_sched_barrier(0);
     load_keys(next);
-    const bool whole = id >= 0 && p * kPage >= low && p * kPage + kPage <= high;
+    if (last && next.left >= 0) load_q(next, run_next.sp);
+    const bool whole = now.id >= 0 && now.p * kPage >= low && now.p * kPage + kPage <= high;
     kh8_t w[NT][2];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
@@ -128,8 +255,8 @@ __global__ __launch_bounds__(64 * kWaves, NT <= 2 && D <= 128 ? 2 : 1) void attn
       if (!whole) {
 #pragma unroll
         for (int x = 0; x < 16; ++x) {
-          const int token = p * kPage + 16 * kq + x;
-          if (id < 0 || token < sees[n].low || token >= sees[n].high) z[n][x / 4][x % 4] = -INFINITY;
+          const int token = now.p * kPage + 16 * kq + x;
+          if (now.id < 0 || token < sees[n].low || token >= sees[n].high) z[n][x / 4][x % 4] = -INFINITY;
         }
       }
 #pragma unroll
@@ -145,141 +272,157 @@ __global__ __launch_bounds__(64 * kWaves, NT <= 2 && D <= 128 ? 2 : 1) void attn
       const float top = row[n].top == -INFINITY ? 0.f : row[n].top;
       float sum = 0.f;
 #pragma unroll
-      for (int t = 0; t < 4; ++t)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float e = __builtin_amdgcn_exp2f(z[n][t][i] - top);
-          sum += e;
-          w[n][t / 2][t % 2 * 4 + i] = (_Float16)(e * ratio);
-        }
+      for (int x = 0; x < 16; ++x) {
+        const float e = __builtin_amdgcn_exp2f(z[n][x / 4][x % 4] - top);
+        sum += e;
+        w[n][x / 8][x % 8] = (_Float16)(e * ratio);
+      }
       row[n].sum += sum;
     }
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int d = 0; d < DT; ++d)
+    for (int d = 0; d < DT; ++d) {
+      if (NT > 1 && d % 2 == 0) __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int u = 0; u < 2; ++u) {
         const kh8_t v = codes8(vr[d][2 * u], vr[d][2 * u + 1]);
 #pragma unroll
         for (int n = 0; n < NT; ++n) o[n][d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v, w[n][u], o[n][d], 0, 0, 0);
       }
+    }
+    __builtin_amdgcn_sched_barrier(0);
     load_values(next);
-    id = next;
-    next = later;
-  }
-
-  // The wavefronts' sums: references first, then 16 rows at a time.
+    if (last) {
+      const bool all = opened && now.p + 1 == run.r.end;
+      const Slot slot = slot_of<D>(a, wave, opened ? 1 : 0);
 #pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    float sum = row[n].sum;
-    sum += __shfl_xor(sum, 16);
-    sum += __shfl_xor(sum, 32);
-    row[n].sum = sum;
-    if (kq == 0) {
-      tops[wave][n * 16 + col] = row[n].top;
-      totals[wave][n * 16 + col] = sum;
-    }
-  }
-  __syncthreads();
+      for (int n = 0; n < NT; ++n) {
+        const int r = n * 16 + col;
+        float sum = row[n].sum;
+        sum += __shfl_xor(sum, 16);
+        sum += __shfl_xor(sum, 32);
+        if (r >= run.sp.n * a.group) continue;
+        const float unit = row[n].unit / kLift;
+        const size_t out = (size_t)run.sp.first * a.q_heads + now.head * a.group + place_y[n];
 #pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    if (n * 16 >= total) break;
-    float top = tops[0][n * 16 + col];
-    for (int i = 1; i < kWaves; ++i) top = fmaxf(top, tops[i][n * 16 + col]);
-    const float own = row[n].top == -INFINITY ? 0.f : __builtin_amdgcn_exp2f(row[n].top - top) * (row[n].unit / kLift);
-#pragma unroll
-    for (int d = 0; d < DT; ++d) {
-      const kf4_t v = o[n][d] * own;
-      *reinterpret_cast<kf4_t*>(&sums[(wave * 16 + col) * P + d * 16 + 4 * kq]) = v;
-    }
-    __syncthreads();
-    for (int i = threadIdx.x; i < 16 * D / 4; i += 64 * kWaves) {
-      const int c = i / (D / 4), d = i % (D / 4) * 4, r = n * 16 + c;
-      if (r >= total) break;
-      kf4_t v = *reinterpret_cast<const kf4_t*>(&sums[c * P + d]);
-      float best = tops[0][r], sum = 0.f;
-      for (int x = 1; x < kWaves; ++x) {
-        v += *reinterpret_cast<const kf4_t*>(&sums[(x * 16 + c) * P + d]);
-        best = fmaxf(best, tops[x][r]);
+        for (int d = 0; d < DT; ++d) {
+          const kf4_t v = o[n][d] * unit;
+          if (all)
+            finish_row(a, out * D + 16 * d + 4 * kq, v, sum);
+          else
+            *reinterpret_cast<kf4_t*>(slot.sums + (size_t)r * D + 16 * d + 4 * kq) = v;
+        }
+        if (!all && kq == 0) slot.tops[r] = kw2_t{__float_as_uint(row[n].top), __float_as_uint(sum)};
       }
-      for (int x = 0; x < kWaves; ++x)
-        sum += tops[x][r] == -INFINITY ? totals[x][r] : totals[x][r] * __builtin_amdgcn_exp2f(tops[x][r] - best);
-      const size_t out = (size_t)(sp.first + r / a.group) * a.q_heads + head * a.group + r % a.group;
-      store_row<D>(a, parts, part, out, d, v, best, sum);
+      if (opened && lane == 0 && !a.whole) {
+        const int more = run.r.end - run.r.begin - room;
+        a.info[now.s * a.c.heads + now.head] = make_int2(wave, more > 0 ? 1 + (int)(((uint32_t)more + per - 1) / per) : 1);
+      }
+      if (next.left < 0) break;
+      begin_rows(run_next.sp);
+      opened = next.p == run_next.r.begin;
+      room = next.left + 1;
     }
-    __syncthreads();
+    now = next;
+    run = run_next;
+    next = later;
+    run_next = ahead;
   }
 }
 
-// y from the parts' sums, in their order: a workgroup has a row's head, its
-// groups of lanes take turns at the parts.
+// y from the sums of a unit's pieces, or of a tile's parts, in their order: a
+// workgroup has a row's head, its groups of lanes take turns at the pieces.
 template <int D>
-__global__ __launch_bounds__(256) void attn_join_kernel(const AttnArgs a, int block_rows) {
+__global__ __launch_bounds__(256) void attn_join_kernel(const AttnArgs a) {
   constexpr int L = D / 4, G = 256 / L;  // lanes of a row, groups
   __shared__ kf4_t sums[256];
-  __shared__ float totals[G];
-  const Span sp = span_of(a.b, blockIdx.x / a.b.max_rows);
-  const int j = blockIdx.x % a.b.max_rows, head = blockIdx.y;
+  __shared__ float2 totals[G];
+  const int s = blockIdx.x / a.b.max_rows, j = blockIdx.x % a.b.max_rows, head = blockIdx.y;
+  const Span sp = span_of(a.b, s);
   if (j >= sp.n) return;
-  const int block = (j * a.group + head % a.group) / block_rows * block_rows;
-  const Parts p = parts_of(a, range_of_rows(a, sp, block, min(block + block_rows, sp.n * a.group) - 1));
-  if (p.count == 1) return;  // written where it was computed
-  const int lane = threadIdx.x & 63, g = threadIdx.x / L, d = threadIdx.x % L * 4;
-  const size_t rows = (size_t)a.b.rows * a.q_heads, r = (size_t)(sp.first + j) * a.q_heads + head;
-  const kw2_t* const tops = reinterpret_cast<const kw2_t*>(a.part + (size_t)a.parts * rows * D) + r;
-  float top = -INFINITY;
-  for (int i = lane; i < p.count; i += 64) top = fmaxf(top, __uint_as_float(tops[i * rows].x));
-  for (int o = 32; o; o >>= 1) top = fmaxf(top, __shfl_xor(top, o));
+  // the pieces' rows: the first, how many, how far apart
+  const int local = j * a.group + head % a.group;
+  const size_t out = (size_t)(sp.first + j) * a.q_heads + head;
+  size_t first, step, all;
+  int count;
+  if (a.tiles) {
+    const int block = local / kAttnTile * kAttnTile;
+    count = parts_of(a, range_of_rows(a, sp, block, min(block + kAttnTile, sp.n * a.group) - 1)).count;
+    first = out;
+    step = (size_t)a.b.rows * a.q_heads;
+    all = step * a.parts;
+  } else {
+    const int2 info = a.info[s * a.c.heads + head / a.group];
+    const size_t rows = (size_t)a.b.max_rows * a.group;
+    count = info.y;
+    first = (size_t)info.x * 2 * rows + local;  // its second slot, the others' first ones
+    step = 2 * rows;
+    all = (size_t)a.pieces * 2 * rows;
+  }
+  if (count == 1) return;  // written where it was computed
+  auto at = [&](int i) { return first + i * step + (!a.tiles && i == 0 ? step / 2 : 0); };
+  const int g = threadIdx.x / L, d = threadIdx.x % L * 4;
+  const kw2_t* const tops = reinterpret_cast<const kw2_t*>(a.part + all * D);
+  // one pass: every group keeps its own reference
   kf4_t v = {0.f, 0.f, 0.f, 0.f};
-  float sum = 0.f;
+  float sum = 0.f, top = -INFINITY;
 #pragma unroll 4
-  for (int i = g; i < p.count; i += G) {
-    const kw2_t t = tops[i * rows];
-    const float at = __uint_as_float(t.x), f = at == -INFINITY ? 1.f : __builtin_amdgcn_exp2f(at - top);
-    sum += __uint_as_float(t.y) * f;
-    v += *reinterpret_cast<const kf4_t*>(a.part + (i * rows + r) * D + d) * f;
+  for (int i = g; i < count; i += G) {
+    const kw2_t t = tops[at(i)];
+    const kf4_t x = *reinterpret_cast<const kf4_t*>(a.part + at(i) * D + d);
+    const float own = __uint_as_float(t.x), most = fmaxf(top, own);
+    const float keep = top == most ? 1.f : __builtin_amdgcn_exp2f(top - most);
+    const float f = own == most ? 1.f : __builtin_amdgcn_exp2f(own - most);
+    sum = sum * keep + __uint_as_float(t.y) * f;
+    v = v * keep + x * f;
+    top = most;
   }
   sums[threadIdx.x] = v;
-  if (threadIdx.x % L == 0) totals[g] = sum;
+  if (threadIdx.x % L == 0) totals[g] = make_float2(top, sum);
   __syncthreads();
   if (threadIdx.x >= L) return;
-  for (int i = 1; i < G; ++i) {
-    v += sums[i * L + threadIdx.x];
-    sum += totals[i];
+  for (int i = 1; i < G; ++i) top = fmaxf(top, totals[i].x);
+  v = kf4_t{0.f, 0.f, 0.f, 0.f};
+  sum = 0.f;
+  for (int i = 0; i < G; ++i) {
+    const float f = totals[i].x == top ? 1.f : __builtin_amdgcn_exp2f(totals[i].x - top);
+    v += sums[i * L + threadIdx.x] * f;
+    sum += totals[i].y * f;
   }
-  finish_row(a, r * D + d, v, sum);
+  finish_row(a, out * D + d, v, sum);
 }
 
 template <int D>
-hipError_t rows(const AttnArgs& a, int blocks, long long grid, hipStream_t s) {
+hipError_t rows(const AttnArgs& a, int blocks, hipStream_t s) {
+  const long long grid = a.pieces;
+  if (!kv_grid_fits(grid, 64)) return hipErrorInvalidConfiguration;
   if (blocks == 1)
-    hipLaunchKernelGGL((attn_rows_kernel<D, 1>), dim3((unsigned)grid), dim3(64 * kWaves), 0, s, a);
+    hipLaunchKernelGGL((attn_rows_kernel<D, 1>), dim3((unsigned)grid), dim3(64), 0, s, a);
   else if (blocks == 2)
-    hipLaunchKernelGGL((attn_rows_kernel<D, 2>), dim3((unsigned)grid), dim3(64 * kWaves), 0, s, a);
+    hipLaunchKernelGGL((attn_rows_kernel<D, 2>), dim3((unsigned)grid), dim3(64), 0, s, a);
   else if constexpr (D <= 128)
-    hipLaunchKernelGGL((attn_rows_kernel<D, 4>), dim3((unsigned)grid), dim3(64 * kWaves), 0, s, a);
+    hipLaunchKernelGGL((attn_rows_kernel<D, 4>), dim3((unsigned)grid), dim3(64), 0, s, a);
   return hipGetLastError();
 }
 
 template <int D>
-hipError_t join(const AttnArgs& a, int block_rows, hipStream_t s) {
+hipError_t join(const AttnArgs& a, hipStream_t s) {
   const long long x = (long long)a.b.count * a.b.max_rows;
   if (a.q_heads > 65535 || !kv_grid_fits(x * a.q_heads, 256)) return hipErrorInvalidConfiguration;
-  hipLaunchKernelGGL((attn_join_kernel<D>), dim3((unsigned)x, (unsigned)a.q_heads), dim3(256), 0, s, a, block_rows);
+  hipLaunchKernelGGL((attn_join_kernel<D>), dim3((unsigned)x, (unsigned)a.q_heads), dim3(256), 0, s, a);
   return hipGetLastError();
 }
 
 }  // namespace
 
 hipError_t launch_attn_rows(const AttnArgs& a, int dim, int blocks, hipStream_t s) {
-  const long long grid = (long long)a.b.count * a.c.heads * a.parts;
-  if (!kv_grid_fits(grid, 64 * kWaves)) return hipErrorInvalidConfiguration;
-  if (dim == 64) return rows<64>(a, blocks, grid, s);
-  return dim == 128 ? rows<128>(a, blocks, grid, s) : rows<256>(a, blocks, grid, s);
+  if (dim == 64) return rows<64>(a, blocks, s);
+  return dim == 128 ? rows<128>(a, blocks, s) : rows<256>(a, blocks, s);
 }
 
-hipError_t launch_attn_join(const AttnArgs& a, int dim, int block_rows, hipStream_t s) {
-  if (dim == 64) return join<64>(a, block_rows, s);
-  return dim == 128 ? join<128>(a, block_rows, s) : join<256>(a, block_rows, s);
+hipError_t launch_attn_join(const AttnArgs& a, int dim, hipStream_t s) {
+  if (dim == 64) return join<64>(a, s);
+  return dim == 128 ? join<128>(a, s) : join<256>(a, s);
 }
 
 }  // namespace tern

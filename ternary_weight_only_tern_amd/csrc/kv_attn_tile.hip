@@ -106,7 +106,7 @@ __global__ __launch_bounds__(64 * kTileWaves, D <= 128 ? 2 : 1) void attn_tile_k
   auto compute = [&](int p, int id, const kw4_t* ks, const kw4_t* vs) {
     if (p * kPage >= most || p * kPage + kPage <= least) return;  // none of the wavefront's rows sees it
     const size_t at = (size_t)max(id, 0) * a.c.heads + head;
-    const float kscale = a.c.ks[at] * a.scale, vscale = a.c.vs[at];
+    const float kscale = kv_const(a.c.ks, at) * a.scale, vscale = kv_const(a.c.vs, at);
     kf16_t z[2];
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
