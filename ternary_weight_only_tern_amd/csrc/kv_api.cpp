@@ -129,7 +129,7 @@ int items_of(const tern_kv_batch* b) { return (b->max_rows + 2 * (tern::kPage - 
 
 // How attention runs.
 struct AttnPlan {
-  int blocks;  // of 16 rows in the kernel for few rows; 0: tiles
+  int blocks;  // of 16 rows in the kernel for few rows, 1 or 2; 0: tiles
   int pieces, whole, parts, per, tiles;
   bool join;
   size_t rows, info;  // of partial sums, and units whose pieces are noted
@@ -146,14 +146,14 @@ int pages_of(const tern_kv_batch* b, int window) {
 }
 
 // Rows on which a unit goes to the kernel for few rows.
-int few_rows(int dim) { return dim == 256 ? 32 : 64; }
+int few_rows(int dim) { return dim == 256 ? 16 : 32; }
 
 AttnPlan plan_of(const tern_kv* c, const tern_kv_batch* b, int group, int window) {
   AttnPlan p = {};
   const long long rows = (long long)b->max_rows * group, units = (long long)b->count * c->heads;
   const int pages = pages_of(b, window);
   if (rows <= few_rows(c->dim)) {
-    p.blocks = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
+    p.blocks = rows <= 16 ? 1 : 2;
     p.whole = pages <= kWholePages;
     p.pieces = (int)(p.whole ? std::min<long long>(units, 1ll << 30) : std::min<long long>(p.blocks * c->dim > 128 ? kPieces / 2 : kPieces, units * pages));
     p.per = 1;
@@ -164,7 +164,7 @@ AttnPlan plan_of(const tern_kv* c, const tern_kv_batch* b, int group, int window
   }
   p.tiles = (int)((rows + tern::kAttnTile - 1) / tern::kAttnTile);
   const long long groups = p.tiles * units;
-  p.per = std::max(kPartPages, (int)std::min<long long>((groups * pages + kTileTarget - 1) / kTileTarget, pages));
+  p.per = groups < kTileTarget / 2 ? std::max(kPartPages, (int)((groups * pages + kTileTarget - 1) / kTileTarget)) : std::max(1, pages);
   p.parts = std::max(1, (pages + p.per - 1) / p.per);
   p.join = p.parts > 1;
   p.rows = p.join ? (size_t)p.parts * b->rows * group * c->heads : 0;

@@ -63,27 +63,33 @@ __device__ inline Sees sees_of(const AttnArgs& a, const Span& sp, int pos, bool 
 // reference keep their 11 bits, and what is below has 2^-35 of it.
 constexpr float kLag = 5.0f, kSpan = 64.0f, kLift = 1024.0f;
 struct Row {
-  float top, sum, unit;
+  float top, sum, unit, inv;  // inv: 1 / unit
 };
+__device__ inline Row new_row() { return {-INFINITY, 0.f, 0.f, 1.f}; }
 
 // The row before the weights of a page: best is its largest score there
-// (minus infinity: it sees nothing of it), scale the page's.  Returns what
-// the row's sums have to be multiplied with; *ratio: what the page's weights
-// are multiplied with before they meet its codes.
-__device__ inline float step_row(Row& r, float best, float scale, float* ratio) {
+// (minus infinity: it sees nothing of it), scale the page's, not 0.  Returns
+// what the row's sums have to be multiplied with.  A weight in the units of the
+// sums is exp2(score - top_of(r) + lift), and `back` times that in its own.  A
+// scale that is NaN goes into the sums of the rows that see a token of its page
+// alone.
+__device__ inline float top_of(const Row& r) { return r.top == -INFINITY ? 0.f : r.top; }
+__device__ inline float step_row(Row& r, float best, float scale, float& lift, float& back) {
+  const bool sees = best > -INFINITY;
   float factor = 1.0f;
-  if (best > r.top + kLag || (r.top == -INFINITY && best > -INFINITY)) {
-    factor = r.top == -INFINITY ? 0.0f : exp2f(r.top - best);
+  if (best > r.top + kLag || (sees && r.top == -INFINITY)) {
+    factor = r.top == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f(r.top - best);
     r.sum *= factor;
     r.top = best;
   }
-  if (best > -INFINITY && scale < INFINITY && (scale > r.unit || (scale > 0.f && scale * kSpan < r.unit))) {
-    factor *= r.unit / scale;
+  if (sees && (scale > r.unit || scale * kSpan < r.unit)) {
+    r.inv = 1.0f / scale;
+    factor *= r.unit * r.inv;
     r.unit = scale;
   }
-  // a page of zeros has no units; a scale that is NaN goes into the sums of the
-  // rows that see a token of its page
-  *ratio = scale == 0.f || best == -INFINITY ? 0.f : kLift * scale / (r.unit > 0.f ? r.unit : 1.f);
+  const float ratio = !sees ? 1.0f : scale == r.unit ? kLift : kLift * scale * r.inv;
+  back = __builtin_amdgcn_rcpf(ratio);
+  lift = __builtin_amdgcn_logf(ratio);
   return factor;
 }
 

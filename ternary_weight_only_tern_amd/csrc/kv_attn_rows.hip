@@ -178,7 +178,7 @@ __global__ __launch_bounds__(64, NT * D <= 128 ? 2 : 1) void attn_rows_kernel(co
         low = max(low, sees[n].low);
         high = min(high, sees[n].high);
       }
-      row[n] = {-INFINITY, 0.f, 0.f};
+      row[n] = new_row();
 #pragma unroll
       for (int d = 0; d < DT; ++d) o[n][d] = kf4_t{0.f, 0.f, 0.f, 0.f};
     }
@@ -263,21 +263,22 @@ __global__ __launch_bounds__(64, NT * D <= 128 ? 2 : 1) void attn_rows_kernel(co
       for (int x = 0; x < 16; ++x) best = fmaxf(best, z[n][x / 4][x % 4]);
       best = fmaxf(best, __shfl_xor(best, 16));
       best = fmaxf(best, __shfl_xor(best, 32));
-      float ratio;
-      const float factor = step_row(row[n], best, vs, &ratio);
+      float lift, back;
+      const float factor = step_row(row[n], best, vs == 0.f ? 1.f : vs, lift, back);
+      const float top = top_of(row[n]);
       if (__any(factor != 1.0f)) {
 #pragma unroll
         for (int d = 0; d < DT; ++d) o[n][d] *= factor;
       }
-      const float top = row[n].top == -INFINITY ? 0.f : row[n].top;
       float sum = 0.f;
 #pragma unroll
       for (int x = 0; x < 16; ++x) {
-        const float e = __builtin_amdgcn_exp2f(z[n][x / 4][x % 4] - top);
+        const float e = __builtin_amdgcn_exp2f((z[n][x / 4][x % 4] - top) + lift);  // the reference's weight is exact
         sum += e;
-        w[n][x / 8][x % 8] = (_Float16)(e * ratio);
+        w[n][x / 8][x % 8] = (_Float16)e;
       }
-      row[n].sum += sum;
+      row[n].sum += sum * back;
+      if (vs == 0.f) w[n][0] = w[n][1] = kh8_t{0, 0, 0, 0, 0, 0, 0, 0};  // values of 0, whatever the codes
     }
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -398,10 +399,8 @@ hipError_t rows(const AttnArgs& a, int blocks, hipStream_t s) {
   if (!kv_grid_fits(grid, 64)) return hipErrorInvalidConfiguration;
   if (blocks == 1)
     hipLaunchKernelGGL((attn_rows_kernel<D, 1>), dim3((unsigned)grid), dim3(64), 0, s, a);
-  else if (blocks == 2)
-    hipLaunchKernelGGL((attn_rows_kernel<D, 2>), dim3((unsigned)grid), dim3(64), 0, s, a);
   else if constexpr (D <= 128)
-    hipLaunchKernelGGL((attn_rows_kernel<D, 4>), dim3((unsigned)grid), dim3(64), 0, s, a);
+    hipLaunchKernelGGL((attn_rows_kernel<D, 2>), dim3((unsigned)grid), dim3(64), 0, s, a);
   return hipGetLastError();
 }
 

@@ -17,7 +17,7 @@
 namespace tern {
 namespace {
 
-constexpr int kTileWaves = 4;
+constexpr int kTileWaves = 4, kCus = 256;
 
 template <int D>
 __global__ __launch_bounds__(64 * kTileWaves, D <= 128 ? 2 : 1) void attn_tile_kernel(const AttnArgs a) {
@@ -33,7 +33,12 @@ __global__ __launch_bounds__(64 * kTileWaves, D <= 128 ? 2 : 1) void attn_tile_k
   bid /= a.c.heads;
   const int s = bid % a.b.count;
   bid /= a.b.count;
-  const int part = bid % a.parts, tile = a.tiles - 1 - bid / a.parts;
+  const int part = bid % a.parts;
+  int tile = a.tiles - 1 - bid / a.parts;
+  // Where the card holds the whole grid at once, every CU's second workgroup is
+  // the lighter the heavier its first.
+  const int per = a.c.heads * a.b.count * a.parts, firsts = (kCus + per - 1) / per;
+  if (a.tiles * per <= 2 * kCus && bid / a.parts >= firsts) tile = bid / a.parts - firsts;
   const Span sp = span_of(a.b, s);
   const int total = sp.n * a.group;
   if (tile * ROWS >= total) return;
@@ -60,18 +65,15 @@ __global__ __launch_bounds__(64 * kTileWaves, D <= 128 ? 2 : 1) void attn_tile_k
   most = __builtin_amdgcn_readfirstlane(most);
 
   kh8_t q[KS];
-  const uint16_t* const from = a.q + (int64_t)(sp.first + j) * a.q_stride + (head * a.group + h) * D;
+  const uint16_t* const from = a.q + (int64_t)(sp.first + (there ? j : 0)) * a.q_stride + (head * a.group + h) * D;
 #pragma unroll
-  for (int i = 0; i < KS; ++i) {
-    q[i] = kh8_t{0, 0, 0, 0, 0, 0, 0, 0};
-    if (there) q[i] = *reinterpret_cast<const kh8_t*>(from + 16 * i + 8 * hq);
-  }
+  for (int i = 0; i < KS; ++i) q[i] = *reinterpret_cast<const kh8_t*>(from + 16 * i + 8 * hq);
   kf16_t o[DB];
 #pragma unroll
   for (int d = 0; d < DB; ++d)
 #pragma unroll
     for (int v = 0; v < 16; ++v) o[d][v] = 0.f;
-  Row row = {-INFINITY, 0.f, 0.f};
+  Row row = new_row();
 
   // A thread's pieces: of the keys 16 dimensions (16 st ..) of a token, of the
   // values 16 tokens (16 part ..) of a dimension; a wavefront's 64 are
@@ -133,24 +135,25 @@ __global__ __launch_bounds__(64 * kTileWaves, D <= 128 ? 2 : 1) void attn_tile_k
 #pragma unroll
       for (int v = 0; v < 16; ++v) best = fmaxf(best, z[b][v]);
     best = fmaxf(best, __shfl_xor(best, 32)) * by;
-    float ratio;
-    const float factor = step_row(row, best, vscale, &ratio);
+    float lift, back;
+    const float factor = step_row(row, best, vscale == 0.f ? 1.f : vscale, lift, back);
+    const float shift = lift - top_of(row);
     if (__any(factor != 1.0f)) {
 #pragma unroll
       for (int d = 0; d < DB; ++d) o[d] *= factor;
     }
-    const float top = row.top == -INFINITY ? 0.f : row.top;
     kh8_t w[4];
     float sum = 0.f;
 #pragma unroll
     for (int b = 0; b < 2; ++b)
 #pragma unroll
       for (int v = 0; v < 16; ++v) {
-        const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(z[b][v], by, -top));
+        const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(z[b][v], by, shift));
         sum += e;
-        w[b * 2 + v / 8][v % 8] = (_Float16)(e * ratio);
+        w[b * 2 + v / 8][v % 8] = (_Float16)e;
       }
-    row.sum += sum;
+    row.sum += sum * back;
+    if (vscale == 0.f) return;  // values of 0, whatever the codes
 #pragma unroll
     for (int d = 0; d < DB; ++d)
 #pragma unroll
@@ -158,6 +161,7 @@ __global__ __launch_bounds__(64 * kTileWaves, D <= 128 ? 2 : 1) void attn_tile_k
         o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(kh8_t, vs[(d * 4 + t) * 64 + lane]), w[t], o[d], 0, 0, 0);
   };
 
+  __builtin_amdgcn_s_waitcnt(0x0F70);  // the queries, once: in the loop their wait would be for the pages too
   int p = mine.begin, id = page_at(p);
   if (p < mine.end) {
     load(id);
