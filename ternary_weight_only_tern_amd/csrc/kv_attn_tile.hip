@@ -79,104 +79,179 @@ __global__ __launch_bounds__(64 * kTileWaves, D <= 128 ? 2 : 1) void attn_tile_k
   // values 16 tokens (16 part ..) of a dimension; a wavefront's 64 are
   // neighbours in LDS.
   kw4_t kr[PIECES], vr[PIECES];
-  auto page_at = [&](int p) { return p < mine.end ? __builtin_amdgcn_readfirstlane(page_of(a.b, a.c, s, p)) : -1; };
-  auto load = [&](int id) {
-    const size_t at = ((size_t)max(id, 0) * a.c.heads + head) * (kPage * D);
-    const __amdgpu_buffer_rsrc_t fk = kv_buffer(a.c.k + at, id < 0 ? 0 : kPage * D), fv = kv_buffer(a.c.v + at, id < 0 ? 0 : kPage * D);
+  // Page numbers and scales come by vector loads, a step and more ahead: they
+  // are there with the pages that the decoding waits for, and no scalar load
+  // in flight makes an LDS read wait.
+  const int32_t* const table = a.b.pages + (size_t)s * a.b.max_pages;
+  auto load_id = [&](int p) {
+    return (int)__builtin_amdgcn_raw_buffer_load_b32(kv_buffer(table + (p < mine.end ? p : 0), p < mine.end ? 4 : 0), 0, 0, 0);
+  };
+  auto id_of = [&](int raw, int p) {
+    const int id = __builtin_amdgcn_readfirstlane(raw);
+    return p < mine.end && id >= 0 && id < a.c.pages ? id : -1;
+  };
+  auto load_scale = [&](const float* scales, int id) {
+    return __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(kv_buffer(scales + (size_t)max(id, 0) * a.c.heads + head, 4), 0, 0, 0));
+  };
+  auto buffer = [&](const uint8_t* pages, int id) {
+    return kv_buffer(pages + ((size_t)max(id, 0) * a.c.heads + head) * (kPage * D), id < 0 ? 0 : kPage * D);
+  };
+  auto load_keys = [&](int id) {
+    const __amdgpu_buffer_rsrc_t f = buffer(a.c.k, id);
 #pragma unroll
     for (int i = 0; i < PIECES; ++i) {
       const int st = i * kTileWaves + wave;
-      kr[i] = kv_load16(fk, ((st / 4 * 4 + lane / 4 % 4) * 64 + st % 4 * 16 + lane / 16 * 4 + lane % 4) * 16);
-      const int part = st % 4, d = st / 4 * 64 + lane;
-      vr[i] = kv_load16(fv, ((d / 16 * 4 + part) * 16 + d % 16) * 16);
+      kr[i] = kv_load16(f, ((st / 4 * 4 + lane / 4 % 4) * 64 + st % 4 * 16 + lane / 16 * 4 + lane % 4) * 16);
     }
   };
-  auto decode = [&](kw4_t* ks, kw4_t* vs) {
+  auto load_values = [&](int id) {
+    const __amdgpu_buffer_rsrc_t f = buffer(a.c.v, id);
 #pragma unroll
     for (int i = 0; i < PIECES; ++i) {
-      const int st = i * kTileWaves + wave;
-      kw4_t* const k = ks + (st * 2 + lane / 32) * 64 + lane % 32;
-      k[0] = __builtin_bit_cast(kw4_t, codes8(kr[i][0], kr[i][1]));
-      k[32] = __builtin_bit_cast(kw4_t, codes8(kr[i][2], kr[i][3]));
-      const int part = st % 4, d = st / 4 * 64 + lane;
-      kw4_t* const v = vs + (d / 32 * 4 + part) * 64 + d % 32;
-      v[0] = __builtin_bit_cast(kw4_t, codes8(vr[i][0], vr[i][2]));
-      v[32] = __builtin_bit_cast(kw4_t, codes8(vr[i][1], vr[i][3]));
+      const int st = i * kTileWaves + wave, part = st % 4, d = st / 4 * 64 + lane;
+      vr[i] = kv_load16(f, ((d / 16 * 4 + part) * 16 + d % 16) * 16);
     }
   };
+  // An eighth or so of a page's decoding: half a piece of the keys (units below
+  // 2 PIECES) or of the values.
+  auto decode = [&](int unit, kw4_t* keys, kw4_t* values) {
+    const int i = unit / 2 % PIECES, half = unit % 2, st = i * kTileWaves + wave;
+    if (unit < 2 * PIECES) {
+      keys[(st * 2 + lane / 32) * 64 + lane % 32 + 32 * half] = __builtin_bit_cast(kw4_t, codes8(kr[i][2 * half], kr[i][2 * half + 1]));
+    } else {
+      const int part = st % 4, d = st / 4 * 64 + lane;
+      values[(d / 32 * 4 + part) * 64 + d % 32 + 32 * half] = __builtin_bit_cast(kw4_t, codes8(vr[i][half], vr[i][2 + half]));
+    }
+  };
+  // Operand i of a step from LDS: the next page's keys, then this page's
+  // values, in an order in which neighbours add to different sums.
+  constexpr int MK = 2 * KS, AHEAD = D == 64 ? 8 : 4;  // instructions of a product, operands on their way
+  auto operand = [&](int i, const kw4_t* ks, const kw4_t* vs) {
+    if (i < MK) return __builtin_bit_cast(kh8_t, ks[i * 64 + lane]);
+    const int t = (i - MK) / DB, db = (i - MK) % DB;
+    return __builtin_bit_cast(kh8_t, vs[(db * 4 + t) * 64 + lane]);
+  };
+  kf16_t z[2];
+  auto multiply = [&](const kw4_t* ks) {
+#pragma unroll
+    for (int v = 0; v < 16; ++v) z[0][v] = z[1][v] = 0.f;
+#pragma unroll
+    for (int i = 0; i < MK; ++i)
+      z[i % 2] = __builtin_amdgcn_mfma_f32_32x32x16_f16(operand(i, ks, nullptr), q[i / 2], z[i % 2], 0, 0, 0);
+  };
+  // whether any of the wavefront's rows sees page p
+  auto seen = [&](int p) { return p * kPage < most && p * kPage + kPage > least; };
 
-  auto compute = [&](int p, int id, const kw4_t* ks, const kw4_t* vs) {
-    if (p * kPage >= most || p * kPage + kPage <= least) return;  // none of the wavefront's rows sees it
-    const size_t at = (size_t)max(id, 0) * a.c.heads + head;
-    const float kscale = kv_const(a.c.ks, at) * a.scale, vscale = kv_const(a.c.vs, at);
-    kf16_t z[2];
+  // A step multiplies the next page's keys with the queries while the vector
+  // units turn this page's scores into weights, and decodes the keys after
+  // that and the next values while the matrix units sum this page's values.
+  int p = mine.begin, cur = 0;
+  int raw = load_id(p), raw1 = load_id(p + 1), raw2 = load_id(p + 2), raw3 = load_id(p + 3);
+  int id = id_of(raw, p), id1 = id_of(raw1, p + 1), id2 = id_of(raw2, p + 2);
+  load_keys(id);
+  load_values(id);
+  float ks0 = load_scale(a.c.ks, id), vs0 = load_scale(a.c.vs, id);  // this page's, the next one's
+  float ks1 = load_scale(a.c.ks, id1), vs1 = load_scale(a.c.vs, id1);
+  __builtin_amdgcn_s_waitcnt(0x0F70);  // with the queries, once: in the loop their wait would be for the pages too
+  if (mine.begin < mine.end) {
 #pragma unroll
-    for (int b = 0; b < 2; ++b) {
+    for (int u = 0; u < 4 * PIECES; ++u) decode(u, lk[0], lv[0]);
+    load_keys(id1);
 #pragma unroll
-      for (int v = 0; v < 16; ++v) z[b][v] = 0.f;
+    for (int u = 0; u < 2 * PIECES; ++u) decode(u, lk[1], nullptr);
+    load_keys(id2);
+    load_values(id1);
+    __syncthreads();
+    multiply(lk[0]);
+    __syncthreads();
+  }
+  for (; p < mine.end; ++p, cur ^= 1) {
+    const kw4_t *const ks = lk[cur ^ 1], *const vs = lv[cur];
+    if (seen(p)) {
+      kh8_t f[AHEAD];
 #pragma unroll
-      for (int i = 0; i < KS; ++i)
-        z[b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(kh8_t, ks[(i * 2 + b) * 64 + lane]), q[i], z[b], 0, 0, 0);
-    }
-    const bool whole = id >= 0 && p * kPage >= low && p * kPage + kPage <= high;
-    float by = kscale, best = -INFINITY;  // the scores are by z
-    if (!whole) {
+      for (int i = 0; i < AHEAD; ++i) f[i] = operand(i, ks, vs);
+      const float vscale = __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(__float_as_int(vs0)));
+      float by = ks0 * a.scale, best = -INFINITY;  // the scores are by z
+      const bool whole = id >= 0 && p * kPage >= low && p * kPage + kPage <= high;
+      if (!whole) {
+#pragma unroll
+        for (int b = 0; b < 2; ++b)
+#pragma unroll
+          for (int v = 0; v < 16; ++v) {
+            const int token = p * kPage + 32 * b + 8 * (v / 4) + 4 * hq + v % 4;
+            z[b][v] = id < 0 || token < sees.low || token >= sees.high ? -INFINITY : z[b][v] * by;
+          }
+        by = 1.0f;
+      }
 #pragma unroll
       for (int b = 0; b < 2; ++b)
 #pragma unroll
-        for (int v = 0; v < 16; ++v) {
-          const int token = p * kPage + 32 * b + 8 * (v / 4) + 4 * hq + v % 4;
-          z[b][v] = id < 0 || token < sees.low || token >= sees.high ? -INFINITY : z[b][v] * by;
-        }
-      by = 1.0f;
-    }
+        for (int v = 0; v < 16; ++v) best = fmaxf(best, z[b][v]);
+      best = fmaxf(best, __shfl_xor(best, 32)) * by;
+      float lift, back;
+      const float factor = step_row(row, best, vscale == 0.f ? 1.f : vscale, lift, back);
+      const float shift = lift - top_of(row);
+      if (__any(factor != 1.0f)) {
 #pragma unroll
-    for (int b = 0; b < 2; ++b)
-#pragma unroll
-      for (int v = 0; v < 16; ++v) best = fmaxf(best, z[b][v]);
-    best = fmaxf(best, __shfl_xor(best, 32)) * by;
-    float lift, back;
-    const float factor = step_row(row, best, vscale == 0.f ? 1.f : vscale, lift, back);
-    const float shift = lift - top_of(row);
-    if (__any(factor != 1.0f)) {
-#pragma unroll
-      for (int d = 0; d < DB; ++d) o[d] *= factor;
-    }
-    kh8_t w[4];
-    float sum = 0.f;
-#pragma unroll
-    for (int b = 0; b < 2; ++b)
-#pragma unroll
-      for (int v = 0; v < 16; ++v) {
-        const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(z[b][v], by, shift));
-        sum += e;
-        w[b * 2 + v / 8][v % 8] = (_Float16)e;
+        for (int d = 0; d < DB; ++d) o[d] *= factor;
       }
-    row.sum += sum * back;
-    if (vscale == 0.f) return;  // values of 0, whatever the codes
+      // Behind the last page `next` is what lies there, and not used.
+      kf16_t next[2];
 #pragma unroll
-    for (int d = 0; d < DB; ++d)
+      for (int v = 0; v < 16; ++v) next[0][v] = next[1][v] = 0.f;
+      kh8_t w[4];
+      float sum = 0.f;
+      constexpr int E = 32 / MK;  // scores for each matrix instruction
+      auto weigh = [&](int x) { z[x / 16][x % 16] = __builtin_amdgcn_exp2f(__builtin_fmaf(z[x / 16][x % 16], by, shift)); };
+      auto round2 = [&](int x) {  // the sum is of the rounded weights
+        const kh2_t two = {(_Float16)z[x / 16][x % 16], (_Float16)z[x / 16][x % 16 + 1]};
+        w[x / 8][x % 8] = two.x;
+        w[x / 8][x % 8 + 1] = two.y;
+        sum = __builtin_amdgcn_fdot2(two, kh2_t{(_Float16)1.0f, (_Float16)1.0f}, sum, false);
+      };
 #pragma unroll
-      for (int t = 0; t < 4; ++t)
-        o[d] = __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(kh8_t, vs[(d * 4 + t) * 64 + lane]), w[t], o[d], 0, 0, 0);
-  };
-
-  __builtin_amdgcn_s_waitcnt(0x0F70);  // the queries, once: in the loop their wait would be for the pages too
-  int p = mine.begin, id = page_at(p);
-  if (p < mine.end) {
-    load(id);
-    decode(lk[0], lv[0]);
-    load(page_at(p + 1));
-    __syncthreads();
-  }
-  for (int cur = 0; p < mine.end; ++p, cur ^= 1) {
-    const int next = page_at(p + 1);
-    compute(p, id, lk[cur], lv[cur]);
-    if (p + 1 < mine.end) {
-      decode(lk[cur ^ 1], lv[cur ^ 1]);
-      if (p + 2 < mine.end) load(page_at(p + 2));
+      for (int i = 0; i < MK; ++i) {
+        __builtin_amdgcn_sched_barrier(0);
+        next[i % 2] = __builtin_amdgcn_mfma_f32_32x32x16_f16(f[i % AHEAD], q[i / 2], next[i % 2], 0, 0, 0);
+        f[i % AHEAD] = operand(i + AHEAD, ks, vs);
+#pragma unroll
+        for (int x = i * E; x < i * E + E; ++x) weigh(x);
+        if (i > 0)
+#pragma unroll
+          for (int x = (i - 1) * E & ~1; x + 1 < i * E; x += 2) round2(x);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int x = (MK - 1) * E & ~1; x < 32; x += 2) round2(x);
+      row.sum += sum * back;
+      if (vscale == 0.f) w[0] = w[1] = w[2] = w[3] = kh8_t{0, 0, 0, 0, 0, 0, 0, 0};  // values of 0, whatever the codes
+#pragma unroll
+      for (int i = 0; i < MK; ++i) {
+        __builtin_amdgcn_sched_barrier(0);
+        o[i % DB] = __builtin_amdgcn_mfma_f32_32x32x16_f16(f[(MK + i) % AHEAD], w[i / DB], o[i % DB], 0, 0, 0);
+        if (i + AHEAD < MK) f[(MK + i) % AHEAD] = operand(MK + i + AHEAD, ks, vs);
+        if (i % 2) decode(i / 2, lk[cur], lv[cur ^ 1]);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      z[0] = next[0];
+      z[1] = next[1];
+    } else {
+      multiply(ks);
+#pragma unroll
+      for (int u = 0; u < 4 * PIECES; ++u) decode(u, lk[cur], lv[cur ^ 1]);
     }
-    id = next;
+    const int id3 = id_of(raw3, p + 3);
+    ks0 = ks1;
+    vs0 = vs1;
+    ks1 = load_scale(a.c.ks, id2);
+    vs1 = load_scale(a.c.vs, id2);
+    raw3 = load_id(p + 4);
+    load_keys(id3);
+    load_values(id2);
+    id = id1;
+    id1 = id2;
+    id2 = id3;
     __syncthreads();
   }
 
