@@ -165,12 +165,19 @@ __global__ __launch_bounds__(64 * kTileWaves, D <= 128 ? 2 : 1) void attn_tile_k
     multiply(lk[0]);
     __syncthreads();
   }
+  int id3 = -1;
+  float ks2 = 0.f, vs2 = 0.f;
+  auto fetch = [&]() {  // what the next step decodes
+    id3 = id_of(raw3, p + 3);
+    load_keys(id3);
+    load_values(id2);
+    ks2 = load_scale(a.c.ks, id2);
+    vs2 = load_scale(a.c.vs, id2);
+    raw3 = load_id(p + 4);
+  };
   for (; p < mine.end; ++p, cur ^= 1) {
     const kw4_t *const ks = lk[cur ^ 1], *const vs = lv[cur];
     if (seen(p)) {
-      kh8_t f[AHEAD];
-#pragma unroll
-      for (int i = 0; i < AHEAD; ++i) f[i] = operand(i, ks, vs);
       const float vscale = __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(__float_as_int(vs0)));
       float by = ks0 * a.scale, best = -INFINITY;  // the scores are by z
       const bool whole = id >= 0 && p * kPage >= low && p * kPage + kPage <= high;
@@ -184,25 +191,41 @@ __global__ __launch_bounds__(64 * kTileWaves, D <= 128 ? 2 : 1) void attn_tile_k
           }
         by = 1.0f;
       }
+      kh8_t f[AHEAD];
 #pragma unroll
-      for (int b = 0; b < 2; ++b)
+      for (int i = 0; i < AHEAD; ++i) f[i] = operand(i, ks, vs);
+      // The next page's scores; behind the last page they are of what lies there,
+      // and not used.  Beside them the largest score, then the decoding.
+      const kf16_t zero = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+      kf16_t next[2];
+      float other = 0.f;
 #pragma unroll
-        for (int v = 0; v < 16; ++v) best = fmaxf(best, z[b][v]);
-      best = fmaxf(best, __shfl_xor(best, 32)) * by;
+      for (int i = 0; i < MK; ++i) {
+        __builtin_amdgcn_sched_barrier(0);
+        next[i % 2] = __builtin_amdgcn_mfma_f32_32x32x16_f16(f[i % AHEAD], q[i / 2], i < 2 ? zero : next[i % 2], 0, 0, 0);
+        f[i % AHEAD] = operand(i + AHEAD, ks, vs);
+        if (i < MK / 2) {
+          constexpr int E = 64 / MK;
+#pragma unroll
+          for (int x = i * E; x < i * E + E; ++x) best = fmaxf(best, z[x / 16][x % 16]);
+          if (i == MK / 2 - 1) other = __shfl_xor(best, 32);
+        } else {
+          decode(i - MK / 2, lk[cur], lv[cur ^ 1]);
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      fetch();
+      best = fmaxf(best, other) * by;
       float lift, back;
       const float factor = step_row(row, best, vscale == 0.f ? 1.f : vscale, lift, back);
-      const float shift = lift - top_of(row);
+      float shift = lift - top_of(row);
       if (__any(factor != 1.0f)) {
 #pragma unroll
         for (int d = 0; d < DB; ++d) o[d] *= factor;
       }
-      // Behind the last page `next` is what lies there, and not used.
-      kf16_t next[2];
-#pragma unroll
-      for (int v = 0; v < 16; ++v) next[0][v] = next[1][v] = 0.f;
+      // This page's weights, 16 tokens ahead of the sums of its values.
       kh8_t w[4];
       float sum = 0.f;
-      constexpr int E = 32 / MK;  // scores for each matrix instruction
       auto weigh = [&](int x) { z[x / 16][x % 16] = __builtin_amdgcn_exp2f(__builtin_fmaf(z[x / 16][x % 16], by, shift)); };
       auto round2 = [&](int x) {  // the sum is of the rounded weights
         const kh2_t two = {(_Float16)z[x / 16][x % 16], (_Float16)z[x / 16][x % 16 + 1]};
@@ -210,48 +233,53 @@ __global__ __launch_bounds__(64 * kTileWaves, D <= 128 ? 2 : 1) void attn_tile_k
         w[x / 8][x % 8 + 1] = two.y;
         sum = __builtin_amdgcn_fdot2(two, kh2_t{(_Float16)1.0f, (_Float16)1.0f}, sum, false);
       };
+      if (vscale == 0.f) {  // values of 0, whatever the codes: the weights' sum alone
+        float alone = 0.f;
 #pragma unroll
-      for (int i = 0; i < MK; ++i) {
-        __builtin_amdgcn_sched_barrier(0);
-        next[i % 2] = __builtin_amdgcn_mfma_f32_32x32x16_f16(f[i % AHEAD], q[i / 2], next[i % 2], 0, 0, 0);
-        f[i % AHEAD] = operand(i + AHEAD, ks, vs);
-#pragma unroll
-        for (int x = i * E; x < i * E + E; ++x) weigh(x);
-        if (i > 0)
-#pragma unroll
-          for (int x = (i - 1) * E & ~1; x + 1 < i * E; x += 2) round2(x);
+        for (int x = 0; x < 32; ++x) alone += __builtin_amdgcn_exp2f(__builtin_fmaf(z[x / 16][x % 16], by, shift));
+        row.sum += alone * back;
+        shift = -INFINITY;
       }
-      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int x = (MK - 1) * E & ~1; x < 32; x += 2) round2(x);
-      row.sum += sum * back;
-      if (vscale == 0.f) w[0] = w[1] = w[2] = w[3] = kh8_t{0, 0, 0, 0, 0, 0, 0, 0};  // values of 0, whatever the codes
+      for (int x = 0; x < 8; ++x) weigh(x);
+#pragma unroll
+      for (int x = 0; x < 8; x += 2) round2(x);
 #pragma unroll
       for (int i = 0; i < MK; ++i) {
+        const int t = i / DB, db = i % DB;
+        constexpr int E = 8 / DB;
         __builtin_amdgcn_sched_barrier(0);
-        o[i % DB] = __builtin_amdgcn_mfma_f32_32x32x16_f16(f[(MK + i) % AHEAD], w[i / DB], o[i % DB], 0, 0, 0);
+        if (t > 0 && db == 0)
+#pragma unroll
+          for (int x = t * 8 + 8 - (E > 2 ? E : 2); x < t * 8 + 8; x += 2) round2(x);
+        o[db] = __builtin_amdgcn_mfma_f32_32x32x16_f16(f[(MK + i) % AHEAD], w[t], o[db], 0, 0, 0);
         if (i + AHEAD < MK) f[(MK + i) % AHEAD] = operand(MK + i + AHEAD, ks, vs);
-        if (i % 2) decode(i / 2, lk[cur], lv[cur ^ 1]);
+        if (t < 3) {
+#pragma unroll
+          for (int x = (t + 1) * 8 + db * E; x < (t + 1) * 8 + db * E + E; ++x) weigh(x);
+          // of the instruction before
+#pragma unroll
+          for (int x = (t + 1) * 8 + (db - 1) * E; db > 0 && x < (t + 1) * 8 + db * E; ++x)
+            if (x % 2) round2(x - 1);
+        }
       }
       __builtin_amdgcn_sched_barrier(0);
+      row.sum += sum * back;
       z[0] = next[0];
       z[1] = next[1];
     } else {
       multiply(ks);
 #pragma unroll
       for (int u = 0; u < 4 * PIECES; ++u) decode(u, lk[cur], lv[cur ^ 1]);
+      fetch();
     }
-    const int id3 = id_of(raw3, p + 3);
-    ks0 = ks1;
-    vs0 = vs1;
-    ks1 = load_scale(a.c.ks, id2);
-    vs1 = load_scale(a.c.vs, id2);
-    raw3 = load_id(p + 4);
-    load_keys(id3);
-    load_values(id2);
     id = id1;
     id1 = id2;
     id2 = id3;
+    ks0 = ks1;
+    vs0 = vs1;
+    ks1 = ks2;
+    vs1 = vs2;
     __syncthreads();
   }
 
