@@ -25,6 +25,9 @@ __global__ __launch_bounds__(64 * kTileWaves, D <= 128 ? 2 : 1) void attn_tile_k
   constexpr int KS = D / 16;                        // products of 16 dimensions in a score
   constexpr int DB = D / 32;                        // blocks of 32 dimensions of the sums
   constexpr int PIECES = kPage * D / 16 / THREADS;  // of 16 codes a thread, keys and values each
+  // Whether a step computes the next page's scores (two pages' scores are in
+  // registers then, which there are not enough of at 256 dimensions).
+  constexpr bool LEAD = D <= 128;
   __shared__ kw4_t lk[2][kPage * D / 8], lv[2][kPage * D / 8];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c32 = lane & 31, hq = lane >> 5;
@@ -132,7 +135,7 @@ __global__ __launch_bounds__(64 * kTileWaves, D <= 128 ? 2 : 1) void attn_tile_k
     return __builtin_bit_cast(kh8_t, vs[(db * 4 + t) * 64 + lane]);
   };
   kf16_t z[2];
-  auto multiply = [&](const kw4_t* ks) {
+  auto multiply = [&](const kw4_t* ks) {  // the scores of a page alone
 #pragma unroll
     for (int v = 0; v < 16; ++v) z[0][v] = z[1][v] = 0.f;
 #pragma unroll
@@ -142,9 +145,10 @@ __global__ __launch_bounds__(64 * kTileWaves, D <= 128 ? 2 : 1) void attn_tile_k
   // whether any of the wavefront's rows sees page p
   auto seen = [&](int p) { return p * kPage < most && p * kPage + kPage > least; };
 
-  // A step multiplies the next page's keys with the queries while the vector
-  // units turn this page's scores into weights, and decodes the keys after
-  // that and the next values while the matrix units sum this page's values.
+  // A step multiplies the next page's (LEAD) or this page's keys with the
+  // queries while the vector units find this page's largest score and decode
+  // the keys after those and the next values; then it sums this page's values
+  // while the vector units turn scores into weights, 16 tokens ahead.
   int p = mine.begin, cur = 0;
   int raw = load_id(p), raw1 = load_id(p + 1), raw2 = load_id(p + 2), raw3 = load_id(p + 3);
   int id = id_of(raw, p), id1 = id_of(raw1, p + 1), id2 = id_of(raw2, p + 2);
@@ -157,31 +161,37 @@ __global__ __launch_bounds__(64 * kTileWaves, D <= 128 ? 2 : 1) void attn_tile_k
 #pragma unroll
     for (int u = 0; u < 4 * PIECES; ++u) decode(u, lk[0], lv[0]);
     load_keys(id1);
+    if constexpr (LEAD) {
 #pragma unroll
-    for (int u = 0; u < 2 * PIECES; ++u) decode(u, lk[1], nullptr);
-    load_keys(id2);
+      for (int u = 0; u < 2 * PIECES; ++u) decode(u, lk[1], nullptr);
+      load_keys(id2);
+    }
     load_values(id1);
     __syncthreads();
-    multiply(lk[0]);
-    __syncthreads();
+    if constexpr (LEAD) {
+      multiply(lk[0]);
+      __syncthreads();
+    }
   }
   int id3 = -1;
   float ks2 = 0.f, vs2 = 0.f;
   auto fetch = [&]() {  // what the next step decodes
     id3 = id_of(raw3, p + 3);
-    load_keys(id3);
+    load_keys(LEAD ? id3 : id2);
     load_values(id2);
     ks2 = load_scale(a.c.ks, id2);
     vs2 = load_scale(a.c.vs, id2);
     raw3 = load_id(p + 4);
   };
   for (; p < mine.end; ++p, cur ^= 1) {
-    const kw4_t *const ks = lk[cur ^ 1], *const vs = lv[cur];
+    const kw4_t *const ks = lk[LEAD ? cur ^ 1 : cur], *const vs = lv[cur];
+    kw4_t* const keys = lk[LEAD ? cur : cur ^ 1];
     if (seen(p)) {
       const float vscale = __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(__float_as_int(vs0)));
       float by = ks0 * a.scale, best = -INFINITY;  // the scores are by z
       const bool whole = id >= 0 && p * kPage >= low && p * kPage + kPage <= high;
-      if (!whole) {
+      auto mask = [&]() {
+        if (whole) return;
 #pragma unroll
         for (int b = 0; b < 2; ++b)
 #pragma unroll
@@ -190,31 +200,40 @@ __global__ __launch_bounds__(64 * kTileWaves, D <= 128 ? 2 : 1) void attn_tile_k
             z[b][v] = id < 0 || token < sees.low || token >= sees.high ? -INFINITY : z[b][v] * by;
           }
         by = 1.0f;
-      }
+      };
+      if (LEAD) mask();
       kh8_t f[AHEAD];
 #pragma unroll
       for (int i = 0; i < AHEAD; ++i) f[i] = operand(i, ks, vs);
-      // The next page's scores; behind the last page they are of what lies there,
-      // and not used.  Beside them the largest score, then the decoding.
+      // Behind the last page the next scores are of what lies there, and not used.
       const kf16_t zero = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
       kf16_t next[2];
       float other = 0.f;
+      auto largest = [&](int x, int n) {
+#pragma unroll
+        for (int y = x; y < x + n; ++y) best = fmaxf(best, z[y / 16][y % 16]);
+      };
 #pragma unroll
       for (int i = 0; i < MK; ++i) {
         __builtin_amdgcn_sched_barrier(0);
         next[i % 2] = __builtin_amdgcn_mfma_f32_32x32x16_f16(f[i % AHEAD], q[i / 2], i < 2 ? zero : next[i % 2], 0, 0, 0);
         f[i % AHEAD] = operand(i + AHEAD, ks, vs);
         if (i < MK / 2) {
-          constexpr int E = 64 / MK;
-#pragma unroll
-          for (int x = i * E; x < i * E + E; ++x) best = fmaxf(best, z[x / 16][x % 16]);
-          if (i == MK / 2 - 1) other = __shfl_xor(best, 32);
+          if (LEAD) largest(i * (64 / MK), 64 / MK);
+          if (LEAD && i == MK / 2 - 1) other = __shfl_xor(best, 32);
         } else {
-          decode(i - MK / 2, lk[cur], lv[cur ^ 1]);
+          decode(i - MK / 2, keys, lv[cur ^ 1]);
         }
       }
       __builtin_amdgcn_sched_barrier(0);
       fetch();
+      if (!LEAD) {
+        z[0] = next[0];
+        z[1] = next[1];
+        mask();
+        largest(0, 32);
+        other = __shfl_xor(best, 32);
+      }
       best = fmaxf(best, other) * by;
       float lift, back;
       const float factor = step_row(row, best, vscale == 0.f ? 1.f : vscale, lift, back);
@@ -265,12 +284,14 @@ __global__ __launch_bounds__(64 * kTileWaves, D <= 128 ? 2 : 1) void attn_tile_k
       }
       __builtin_amdgcn_sched_barrier(0);
       row.sum += sum * back;
-      z[0] = next[0];
-      z[1] = next[1];
+      if (LEAD) {
+        z[0] = next[0];
+        z[1] = next[1];
+      }
     } else {
-      multiply(ks);
+      if (LEAD) multiply(ks);
 #pragma unroll
-      for (int u = 0; u < 4 * PIECES; ++u) decode(u, lk[cur], lv[cur ^ 1]);
+      for (int u = 0; u < 4 * PIECES; ++u) decode(u, keys, lv[cur ^ 1]);
       fetch();
     }
     id = id1;
