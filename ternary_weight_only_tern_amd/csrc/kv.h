@@ -70,6 +70,7 @@ struct WriteArgs {
   int32_t q_heads;
   int32_t items;       // pages that a sequence's rows may lie in
   int32_t kv_blocks;   // workgroups before those of q
+  int32_t q_waves;     // wavefronts for a row of q
 };
 
 struct ReadArgs {
@@ -102,12 +103,21 @@ struct AttnArgs {
 constexpr int kAttnFew = 16, kAttnTile = 128;
 
 hipError_t launch_rope(const RopeArgs& a, hipStream_t s);
-hipError_t launch_kv_write(const WriteArgs& a, int dim, hipStream_t s);
+hipError_t launch_kv_write(WriteArgs a, int dim, hipStream_t s);
 hipError_t launch_kv_read(const ReadArgs& a, int dim, hipStream_t s);
 // blocks: of 16 rows, 1 or 2 (1 at dim 256)
 hipError_t launch_attn_rows(const AttnArgs& a, int dim, int blocks, hipStream_t s);
 hipError_t launch_attn_tile(const AttnArgs& a, int dim, hipStream_t s);
 hipError_t launch_attn_join(const AttnArgs& a, int dim, hipStream_t s);
+
+// Wavefronts that share a row's heads: one where there are rows enough to fill
+// the card, as many as have heads where there are few.
+inline int kv_waves(long long rows, int heads, int lanes) {
+  const int most = (heads * lanes + 63) / 64;
+  int waves = 1;
+  while (waves < most && rows * waves < 2048) waves *= 2;
+  return waves < most ? waves : most;
+}
 
 // A grid's threads have to be countable in 32 bits.
 inline bool kv_grid_fits(long long blocks, int threads) { return blocks * threads < (1ll << 32); }
@@ -199,81 +209,113 @@ __device__ inline void angle_of(double pos, double freq, float amp, float& c, fl
   s = amp * __builtin_amdgcn_sinf(t);
 }
 
-// N (8 or 16) consecutive values of a head from dimension d0 on, normed and
-// turned, in FP32, the same bits for either N (the norm's sum is a tree over
-// eights, and every product and sum is spelled out).  All lanes of the head (`lanes` of them, a power of two,
-// neighbours) call it together; those without values have live false.  x is
-// 16-byte aligned.
-template <int N>
-__device__ inline void turned(const uint16_t* x, int d0, int dim, bool live, int lanes, const Rotary& r, int pos, float* y) {
-  union Row {
-    kw4_t w[N / 8];
-    uint16_t h[N];
-  };
-  Row v = {}, w = {};
-  if (live)
-    for (int i = 0; i < N / 8; ++i) v.w[i] = *reinterpret_cast<const kw4_t*>(x + d0 + 8 * i);
+// The eight values of a head that a lane holds: four from dimension a on and
+// four from b on, their pairs' first angle i0.  In the half layout (rot a
+// multiple of 8) these are the two sides of four pairs, so that a lane turns
+// what it holds; elsewhere they are neighbours.
+struct Place {
+  int a, b, i0;
+};
+__device__ inline bool sided(const Rotary& r) { return !r.inter && r.rot % 8 == 0; }
+__device__ inline Place place_of(const Rotary& r, int lane) {
+  if (sided(r) && lane < r.rot / 8) return {4 * lane, 4 * lane + r.rot / 2, 4 * lane};
+  return {8 * lane, 8 * lane + 4, sided(r) ? r.rot / 2 : 4 * lane};
+}
+
+// cos and sin of the lane's four pairs at position pos.
+struct Angles {
+  float c[4], s[4];
+};
+__device__ inline Angles angles_of(const Rotary& r, const Place& at, bool live, int pos) {
+  Angles g;
 #pragma unroll
-  for (int e = 0; e < N; ++e) y[e] = kv_half(v.h[e]);
+  for (int e = 0; e < 4; ++e) {
+    g.c[e] = 1.f;
+    g.s[e] = 0.f;
+    if (live && at.i0 + e < r.rot / 2) angle_of((double)pos, r.freq[at.i0 + e], r.amp, g.c[e], g.s[e]);
+  }
+  return g;
+}
+
+union Eight {
+  kw2_t w[2];
+  uint16_t h[8];
+};
+__device__ inline Eight load_eight(const uint16_t* x, const Place& at) {
+  Eight v;
+  v.w[0] = *reinterpret_cast<const kw2_t*>(x + at.a);
+  v.w[1] = *reinterpret_cast<const kw2_t*>(x + at.b);
+  return v;
+}
+
+// A lane's values v of the head x, normed (by the weights w at its place) and
+// turned, in FP32: y.  All lanes of the head (`lanes` of them, a power of two,
+// neighbours) call it together; those without values have live false.  Every
+// product and sum is spelled out, so that all kernels round alike.
+__device__ inline void turn_eight(const uint16_t* x, const Eight& v, const Eight& w, const Place& at, int dim, bool live,
+                                  int lanes, const Rotary& r, const Angles& g, int pos, float* y) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) y[e] = kv_half(v.h[e]);
   if (!r.on) return;
   float inv = 1.0f;
   if (r.norm) {
     float sum = 0.f;
 #pragma unroll
-    for (int i = 0; i < N; i += 8) {
-      float eight = 0.f;
-#pragma unroll
-      for (int e = i; e < i + 8; ++e) eight = __builtin_fmaf(y[e], y[e], eight);
-      sum += eight;
-    }
+    for (int e = 0; e < 8; ++e) sum = __builtin_fmaf(y[e], y[e], sum);
     for (int o = 1; o < lanes; o <<= 1) sum += __shfl_xor(sum, o);
     inv = 1.0f / sqrtf(sum / dim + r.eps);
-    if (live)
-      for (int i = 0; i < N / 8; ++i) w.w[i] = *reinterpret_cast<const kw4_t*>(r.norm + d0 + 8 * i);
 #pragma unroll
-    for (int e = 0; e < N; ++e) y[e] = (inv * kv_half(w.h[e])) * y[e];
+    for (int e = 0; e < 8; ++e) y[e] = (inv * kv_half(w.h[e])) * y[e];
   }
-  if (!live || d0 >= r.rot) return;
-  const double at = (double)pos;
-  float c, s;
-  if (r.inter) {
+  if (!live) return;
+  if (r.inter || sided(r)) {
 #pragma unroll
-    for (int e = 0; e < N; e += 2) {
-      if (d0 + e >= r.rot) break;
-      angle_of(at, r.freq[(d0 + e) / 2], r.amp, c, s);
-      const float a = y[e], b = y[e + 1];
-      y[e] = __builtin_fmaf(a, c, -(b * s));
-      y[e + 1] = __builtin_fmaf(b, c, a * s);
+    for (int e = 0; e < 4; ++e) {
+      if (at.i0 + e >= r.rot / 2) break;
+      float &p = r.inter ? y[2 * e] : y[e], &q = r.inter ? y[2 * e + 1] : y[4 + e];
+      const float a = p, b = q;
+      p = __builtin_fmaf(a, g.c[e], -(b * g.s[e]));
+      q = __builtin_fmaf(b, g.c[e], a * g.s[e]);
     }
     return;
   }
-  // pairs (i, i + rot / 2): the other one is another lane's
+  // half layout, rot no multiple of 8: the other side is read one by one
   const int half = r.rot / 2;
-  if (half % N == 0) {
-    const bool low = d0 < half;
-    const int other = low ? d0 + half : d0 - half, i0 = low ? d0 : d0 - half;
-    for (int i = 0; i < N / 8; ++i) v.w[i] = *reinterpret_cast<const kw4_t*>(x + other + 8 * i);
-    if (r.norm)
-      for (int i = 0; i < N / 8; ++i) w.w[i] = *reinterpret_cast<const kw4_t*>(r.norm + other + 8 * i);
 #pragma unroll
-    for (int e = 0; e < N; ++e) {
-      float o = kv_half(v.h[e]);
-      if (r.norm) o = (inv * kv_half(w.h[e])) * o;
-      angle_of(at, r.freq[i0 + e], r.amp, c, s);
-      y[e] = low ? __builtin_fmaf(y[e], c, -(o * s)) : __builtin_fmaf(y[e], c, o * s);
-    }
-    return;
-  }
-#pragma unroll
-  for (int e = 0; e < N; ++e) {
-    const int d = d0 + e;
+  for (int e = 0; e < 8; ++e) {
+    const int d = at.a + e;
     if (d >= r.rot) break;
     const bool low = d < half;
     const int other = low ? d + half : d - half;
-    float o = kv_half(x[other]);
+    float o = kv_half(x[other]), c, s;
     if (r.norm) o = (inv * kv_half(r.norm[other])) * o;
-    angle_of(at, r.freq[low ? d : d - half], r.amp, c, s);
+    angle_of((double)pos, r.freq[low ? d : d - half], r.amp, c, s);
     y[e] = low ? __builtin_fmaf(y[e], c, -(o * s)) : __builtin_fmaf(y[e], c, o * s);
+  }
+}
+
+// A wavefront turns heads first, first + step, .. of a row, several at a time.
+__device__ inline void turn_row(const uint16_t* x, uint16_t* out, int heads, int dim, int lanes, int first, int step,
+                                const Rotary& r, int pos) {
+  const int lane = threadIdx.x % lanes;
+  const bool live = lane * 8 < dim;
+  const Place at = place_of(r, lane);
+  const Angles g = angles_of(r, at, live, pos);
+  Eight w = {};
+  if (live && r.norm) w = load_eight(r.norm, at);
+  for (int h0 = first; h0 < heads; h0 += step) {
+    const int h = h0 + (threadIdx.x & 63) / lanes;
+    const bool there = live && h < heads;
+    const uint16_t* const from = x + (int64_t)h * dim;
+    Eight v = {};
+    if (there) v = load_eight(from, at);
+    float y[8];
+    turn_eight(from, v, w, at, dim, there, lanes, r, g, pos, y);
+    if (there) {
+      uint16_t* const to = out + (int64_t)h * dim;
+      *reinterpret_cast<kh4_t*>(to + at.a) = kh4_t{(_Float16)y[0], (_Float16)y[1], (_Float16)y[2], (_Float16)y[3]};
+      *reinterpret_cast<kh4_t*>(to + at.b) = kh4_t{(_Float16)y[4], (_Float16)y[5], (_Float16)y[6], (_Float16)y[7]};
+    }
   }
 }
 

@@ -9,10 +9,10 @@
 // comparison too.
 //
 // One workgroup has a (page, head) of the keys or of the values, so that a
-// scale has one writer.  A thread owns 16-byte pieces of the page: of the
-// keys a token's 16 dimensions, of the values 16 tokens of four dimensions,
-// which it transposes by byte permutations.  It alone reads, rounds again and
-// writes those bytes; nothing is shared but the largest value.
+// scale has one writer.  A thread owns pieces of the page: of the
+// keys two words of four dimensions of a token, of the values 16 tokens of four
+// dimensions, which it transposes by byte permutations.  It alone reads, rounds
+// again and writes those bytes; nothing is shared but the largest value.
 #include "kv.h"
 
 namespace tern {
@@ -78,26 +78,41 @@ __device__ inline Grown grow(uint32_t bits, bool fresh, float old) {
   return g;
 }
 
+// Of the keys a thread owns, token by token, what a lane holds of a head (kv.h),
+// two words of the page.
 template <int D>
-__device__ void write_keys(const WriteArgs& a, const Span& sp, int page, int id, int head, int t0, int t1) {
-  constexpr int kLanes = D / 16, kRound = 256 / kLanes, kRounds = kPage / kRound;
+__device__ void write_keys(const WriteArgs& a, const Span& sp, int s, int page, int head, int t0, int t1) {
+  constexpr int kLanes = D / 8, kRound = 256 / kLanes, kRounds = kPage / kRound;
+  const int lane = threadIdx.x % kLanes;
+  const Place place = place_of(a.rk, lane);
+  Eight v[kRounds], weight = {};
+  const int first = threadIdx.x / kLanes;  // tokens of a round
+#pragma unroll
+  for (int i = 0; i < kRounds; ++i) {
+    const int token = i * kRound + first;
+    v[i] = {};
+    if (token >= t0 && token < t1)
+      v[i] = load_eight(a.k + (sp.first + page * kPage + token - sp.from) * a.k_stride + head * D, place);
+  }
+  if (a.rk.norm) weight = load_eight(a.rk.norm, place);
+  const int id = page_of(a.b, a.c, s, page);
+  if (id < 0) return;
   const size_t at = (size_t)id * a.c.heads + head;
   const float old = fabsf(a.c.ks[at]);
-  const int lane = threadIdx.x % kLanes;
-  kh8_t y[kRounds][2];
   uint32_t bits = 0;
 #pragma unroll
   for (int i = 0; i < kRounds; ++i) {
-    const int token = i * kRound + threadIdx.x / kLanes;
+    const int token = i * kRound + first;
+    if (i * kRound >= t1 || i * kRound + kRound <= t0) continue;  // the same for all: no token of this round
     const bool live = token >= t0 && token < t1;
     const int row = sp.first + page * kPage + token - sp.from;
-    float v[16];
-    turned<16>(a.k + row * a.k_stride + head * D, lane * 16, D, live, kLanes, a.rk, page * kPage + token, v);
+    float y[8];
+    const Angles g = angles_of(a.rk, place, live && a.rk.on, page * kPage + token);
+    turn_eight(a.k + row * a.k_stride + head * D, v[i], weight, place, D, live, kLanes, a.rk, g, page * kPage + token, y);
 #pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      const uint16_t h = live ? kv_bits(v[e]) : 0;
-      y[i][e / 8][e % 8] = __builtin_bit_cast(_Float16, h);
-      bits = max(bits, (uint32_t)h & 0x7FFFu);
+    for (int e = 0; e < 8; ++e) {
+      v[i].h[e] = live ? kv_bits(y[e]) : 0;
+      bits = max(bits, (uint32_t)v[i].h[e] & 0x7FFFu);
     }
   }
   const Grown g = grow(bits, t0 == 0, old);
@@ -105,33 +120,29 @@ __device__ void write_keys(const WriteArgs& a, const Span& sp, int page, int id,
   uint8_t* const base = a.c.k + at * (kPage * D);
 #pragma unroll
   for (int i = 0; i < kRounds; ++i) {
-    const int token = i * kRound + threadIdx.x / kLanes;
+    const int token = i * kRound + first;
     const bool live = token >= t0 && token < t1;
     if (!live && g.keep) continue;
-    kw4_t* const to = reinterpret_cast<kw4_t*>(base + ((lane / 4 * 4 + token / 4 % 4) * 64 + lane % 4 * 16 + token / 16 * 4 + token % 4) * 16);
-    kw4_t w;
-    if (live) {
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        uint32_t b = 0;
+    for (int q = 0; q < 2; ++q) {
+      const int d = q ? place.b : place.a;
+      uint32_t* const to = reinterpret_cast<uint32_t*>(
+          base + ((d / 64 * 4 + token / 4 % 4) * 64 + d / 16 % 4 * 16 + token / 16 * 4 + token % 4) * 16 + d % 16);
+      uint32_t w = 0;
+      if (live) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) b |= byte_of((float)y[i][q / 2][q % 2 * 4 + e], g.s) << (8 * e);
-        w[q] = b;
+        for (int e = 0; e < 4; ++e) w |= byte_of(kv_half(v[i].h[4 * q + e]), g.s) << (8 * e);
+      } else {
+        w = again4(*to, g.shrink);
       }
-    } else {
-      w = *to;
-#pragma unroll
-      for (int q = 0; q < 4; ++q) w[q] = again4(w[q], g.shrink);
+      *to = w;
     }
-    *to = w;
   }
 }
 
 // Of the values a thread owns 16 tokens of four dimensions, 64 contiguous bytes.
 template <int D>
-__device__ void write_values(const WriteArgs& a, const Span& sp, int page, int id, int head, int t0, int t1) {
-  const size_t at = (size_t)id * a.c.heads + head;
-  const float old = fabsf(a.c.vs[at]);
+__device__ void write_values(const WriteArgs& a, const Span& sp, int s, int page, int head, int t0, int t1) {
   const int part = threadIdx.x / (D / 4), d0 = threadIdx.x % (D / 4) * 4;  // D = 256: four parts, else idle threads
   kh4_t y[16];
   uint32_t bits = 0;
@@ -143,6 +154,10 @@ __device__ void write_values(const WriteArgs& a, const Span& sp, int page, int i
     if (some && token >= t0 && token < t1)
       y[j] = *reinterpret_cast<const kh4_t*>(a.v + (sp.first + page * kPage + token - sp.from) * a.v_stride + head * D + d0);
   }
+  const int id = page_of(a.b, a.c, s, page);
+  if (id < 0) return;
+  const size_t at = (size_t)id * a.c.heads + head;
+  const float old = fabsf(a.c.vs[at]);
 #pragma unroll
   for (int j = 0; j < 16; ++j)
 #pragma unroll
@@ -150,15 +165,17 @@ __device__ void write_values(const WriteArgs& a, const Span& sp, int page, int i
       const _Float16 x = y[j][e];  // a bit cast of the element itself would read the first
       bits = max(bits, (uint32_t)__builtin_bit_cast(uint16_t, x) & 0x7FFFu);
     }
+  // the bytes of other tokens are read before it is known whether they grow
+  const bool all = t0 <= part * 16 && t1 >= part * 16 + 16;
+  kw4_t* const to = reinterpret_cast<kw4_t*>(a.c.v + at * (kPage * D) + ((d0 / 16 * 4 + part % 4) * 16 + d0 % 16) * 16);
+  kw4_t o[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) o[e] = all || part >= 4 || (!some && t0 == 0) ? kw4_t{0, 0, 0, 0} : to[e];
   const Grown g = grow(bits, t0 == 0, old);
   if (threadIdx.x == 0) a.c.vs[at] = g.s;
   if (part >= 4 || (g.keep && !some)) return;
-  kw4_t* const to = reinterpret_cast<kw4_t*>(a.c.v + at * (kPage * D) + ((d0 / 16 * 4 + part) * 16 + d0 % 16) * 16);
-  const bool all = t0 <= part * 16 && t1 >= part * 16 + 16;
-  kw4_t o[4];
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
-    o[e] = all ? kw4_t{0, 0, 0, 0} : to[e];
     if (!g.keep)
 #pragma unroll
       for (int q = 0; q < 4; ++q) o[e][q] = again4(o[e][q], g.shrink);
@@ -185,23 +202,17 @@ __device__ void write_values(const WriteArgs& a, const Span& sp, int page, int i
 template <int D>
 __global__ __launch_bounds__(256) void kv_write_kernel(const WriteArgs a) {
   int bid = blockIdx.x;
-  if (bid >= a.kv_blocks) {  // a row of q: all its heads
-    bid -= a.kv_blocks;
-    const int s = bid / a.b.max_rows, j = bid % a.b.max_rows;
+  if (bid >= a.kv_blocks) {  // wavefronts of rows of q
+    constexpr int lanes = D / 8, per = 64 / lanes;
+    const int64_t wave = (int64_t)(bid - a.kv_blocks) * 4 + threadIdx.x / 64;
+    const int64_t r = wave / a.q_waves;
+    const int s = (int)(r / a.b.max_rows), j = (int)(r % a.b.max_rows);
+    if (s >= a.b.count) return;
     const Span sp = span_of(a.b, s);
     if (j >= sp.n) return;
-    constexpr int lanes = D / 8, slots = 256 / lanes;
     const int64_t row = sp.first + j;
-    const int d0 = threadIdx.x % lanes * 8;
-    for (int h0 = 0; h0 < a.q_heads; h0 += slots) {
-      const int h = h0 + threadIdx.x / lanes;
-      float y[8];
-      turned<8>(a.q + row * a.q_stride + (int64_t)h * D, d0, D, h < a.q_heads, lanes, a.rq, sp.from + j, y);
-      kh8_t o;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) o[e] = (_Float16)y[e];
-      if (h < a.q_heads) *reinterpret_cast<kh8_t*>(a.q_out + (row * a.q_heads + h) * D + d0) = o;
-    }
+    turn_row(a.q + row * a.q_stride, a.q_out + row * a.q_heads * D, a.q_heads, D, lanes, (int)(wave % a.q_waves) * per,
+             a.q_waves * per, a.rq, sp.from + j);
     return;
   }
   const bool values = bid & 1;
@@ -214,12 +225,10 @@ __global__ __launch_bounds__(256) void kv_write_kernel(const WriteArgs a) {
   const int page = begin / kPage + bid % a.items;
   const int t0 = max(begin - page * kPage, 0), t1 = min(end - page * kPage, kPage);
   if (t0 >= t1) return;
-  const int id = page_of(a.b, a.c, s, page);
-  if (id < 0) return;
   if (values)
-    write_values<D>(a, sp, page, id, head, t0, t1);
+    write_values<D>(a, sp, s, page, head, t0, t1);
   else
-    write_keys<D>(a, sp, page, id, head, t0, t1);
+    write_keys<D>(a, sp, s, page, head, t0, t1);
 }
 
 constexpr kw4_t kNone = {0x80808080u, 0x80808080u, 0x80808080u, 0x80808080u};  // codes 0
@@ -320,8 +329,9 @@ hipError_t read(const ReadArgs& a, long long blocks, hipStream_t s) {
 
 }  // namespace
 
-hipError_t launch_kv_write(const WriteArgs& a, int dim, hipStream_t s) {
-  const long long blocks = a.kv_blocks + (a.q ? (long long)a.b.count * a.b.max_rows : 0);
+hipError_t launch_kv_write(WriteArgs a, int dim, hipStream_t s) {
+  a.q_waves = kv_waves((long long)a.b.count * a.b.max_rows, a.q_heads, dim / 8);
+  const long long blocks = a.kv_blocks + (a.q ? ((long long)a.b.count * a.b.max_rows * a.q_waves + 3) / 4 : 0);
   if (!kv_grid_fits(blocks, 256)) return hipErrorInvalidConfiguration;
   if (dim == 64) return write<64>(a, blocks, s);
   return dim == 128 ? write<128>(a, blocks, s) : write<256>(a, blocks, s);
