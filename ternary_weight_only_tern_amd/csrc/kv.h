@@ -198,6 +198,8 @@ __device__ inline kw4_t kv_load16(__amdgpu_buffer_rsrc_t r, int offset) {
   return __builtin_bit_cast(kw4_t, __builtin_amdgcn_raw_buffer_load_b128(r, offset, 0, AUX));
 }
 
+// Bits of the FP16 value nearest to v.
+__device__ inline uint16_t kv_bits(float v) { return __builtin_bit_cast(uint16_t, (_Float16)v); }
 __device__ inline float kv_half(uint16_t v) { return (float)__builtin_bit_cast(_Float16, v); }
 
 // cos and sin of the angle pos * freq, times amp.  The angle is taken to a
@@ -209,17 +211,24 @@ __device__ inline void angle_of(double pos, double freq, float amp, float& c, fl
   s = amp * __builtin_amdgcn_sinf(t);
 }
 
-// The eight values of a head that a lane holds: four from dimension a on and
-// four from b on, their pairs' first angle i0.  In the half layout (rot a
-// multiple of 8) these are the two sides of four pairs, so that a lane turns
-// what it holds; elsewhere they are neighbours.
+// The eight values of a head that a lane holds, four pairs (y[e], y[4 + e])
+// from pair i0 on in the half layout, four neighbours of dimension a and four
+// of b elsewhere.  Pair i is dimensions (i, i + rot / 2) where it turns, and
+// (2i, 2i + 1) behind that: one lane of a head may hold both kinds (mixed).
 struct Place {
   int a, b, i0;
+  bool mixed;
 };
-__device__ inline bool sided(const Rotary& r) { return !r.inter && r.rot % 8 == 0; }
+__device__ inline bool sided(const Rotary& r) { return !r.inter && r.rot > 0; }
 __device__ inline Place place_of(const Rotary& r, int lane) {
-  if (sided(r) && lane < r.rot / 8) return {4 * lane, 4 * lane + r.rot / 2, 4 * lane};
-  return {8 * lane, 8 * lane + 4, sided(r) ? r.rot / 2 : 4 * lane};
+  const int half = r.rot / 2, i0 = 4 * lane;
+  if (!sided(r) || i0 >= half) return {8 * lane, 8 * lane + 4, i0, false};
+  return {i0, i0 + half, i0, i0 + 4 > half};
+}
+__device__ inline int dim_of(const Rotary& r, const Place& at, int e) {
+  if (!at.mixed) return e < 4 ? at.a + e : at.b + e - 4;
+  const int i = at.i0 + e % 4;
+  return i < r.rot / 2 ? (e < 4 ? i : i + r.rot / 2) : 2 * i + e / 4;
 }
 
 // cos and sin of the lane's four pairs at position pos.
@@ -241,57 +250,58 @@ union Eight {
   kw2_t w[2];
   uint16_t h[8];
 };
-__device__ inline Eight load_eight(const uint16_t* x, const Place& at) {
+typedef kw2_t kw2u_t __attribute__((aligned(2)));  // the pairs' second side lies anywhere
+__device__ inline Eight load_eight(const uint16_t* x, const Rotary& r, const Place& at) {
   Eight v;
+  if (at.mixed) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v.h[e] = x[dim_of(r, at, e)];
+    return v;
+  }
   v.w[0] = *reinterpret_cast<const kw2_t*>(x + at.a);
-  v.w[1] = *reinterpret_cast<const kw2_t*>(x + at.b);
+  v.w[1] = *reinterpret_cast<const kw2u_t*>(x + at.b);
   return v;
 }
+__device__ inline void store_eight(uint16_t* x, const Rotary& r, const Place& at, const Eight& v) {
+  if (at.mixed) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[dim_of(r, at, e)] = v.h[e];
+    return;
+  }
+  *reinterpret_cast<kw2_t*>(x + at.a) = v.w[0];
+  *reinterpret_cast<kw2u_t*>(x + at.b) = v.w[1];
+}
 
-// A lane's values v of the head x, normed (by the weights w at its place) and
-// turned, in FP32: y.  All lanes of the head (`lanes` of them, a power of two,
-// neighbours) call it together; those without values have live false.  Every
+// A lane's values v of a head, normed (by the weights w at its place) and
+// turned, rounded to FP16.  All lanes of the head (`lanes` of them, a power of
+// two, neighbours) call it together; those without values hold zeros.  Every
 // product and sum is spelled out, so that all kernels round alike.
-__device__ inline void turn_eight(const uint16_t* x, const Eight& v, const Eight& w, const Place& at, int dim, bool live,
-                                  int lanes, const Rotary& r, const Angles& g, int pos, float* y) {
+__device__ inline Eight turn_eight(Eight v, const Eight& w, const Place& at, int dim, int lanes, const Rotary& r, const Angles& g) {
+  if (!r.on) return v;
+  float y[8];
 #pragma unroll
   for (int e = 0; e < 8; ++e) y[e] = kv_half(v.h[e]);
-  if (!r.on) return;
-  float inv = 1.0f;
   if (r.norm) {
     float sum = 0.f;
 #pragma unroll
     for (int e = 0; e < 8; ++e) sum = __builtin_fmaf(y[e], y[e], sum);
     for (int o = 1; o < lanes; o <<= 1) sum += __shfl_xor(sum, o);
-    inv = 1.0f / sqrtf(sum / dim + r.eps);
+    const float inv = 1.0f / sqrtf(sum / dim + r.eps);
 #pragma unroll
     for (int e = 0; e < 8; ++e) y[e] = (inv * kv_half(w.h[e])) * y[e];
   }
-  if (!live) return;
-  if (r.inter || sided(r)) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      if (at.i0 + e >= r.rot / 2) break;
+  for (int e = 0; e < 4; ++e) {
+    if (at.i0 + e < r.rot / 2) {
       float &p = r.inter ? y[2 * e] : y[e], &q = r.inter ? y[2 * e + 1] : y[4 + e];
       const float a = p, b = q;
       p = __builtin_fmaf(a, g.c[e], -(b * g.s[e]));
       q = __builtin_fmaf(b, g.c[e], a * g.s[e]);
     }
-    return;
   }
-  // half layout, rot no multiple of 8: the other side is read one by one
-  const int half = r.rot / 2;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const int d = at.a + e;
-    if (d >= r.rot) break;
-    const bool low = d < half;
-    const int other = low ? d + half : d - half;
-    float o = kv_half(x[other]), c, s;
-    if (r.norm) o = (inv * kv_half(r.norm[other])) * o;
-    angle_of((double)pos, r.freq[low ? d : d - half], r.amp, c, s);
-    y[e] = low ? __builtin_fmaf(y[e], c, -(o * s)) : __builtin_fmaf(y[e], c, o * s);
-  }
+  for (int e = 0; e < 8; ++e) v.h[e] = kv_bits(y[e]);
+  return v;
 }
 
 // A wavefront turns heads first, first + step, .. of a row, several at a time.
@@ -302,25 +312,17 @@ __device__ inline void turn_row(const uint16_t* x, uint16_t* out, int heads, int
   const Place at = place_of(r, lane);
   const Angles g = angles_of(r, at, live, pos);
   Eight w = {};
-  if (live && r.norm) w = load_eight(r.norm, at);
+  if (live && r.norm) w = load_eight(r.norm, r, at);
   for (int h0 = first; h0 < heads; h0 += step) {
     const int h = h0 + (threadIdx.x & 63) / lanes;
     const bool there = live && h < heads;
-    const uint16_t* const from = x + (int64_t)h * dim;
     Eight v = {};
-    if (there) v = load_eight(from, at);
-    float y[8];
-    turn_eight(from, v, w, at, dim, there, lanes, r, g, pos, y);
-    if (there) {
-      uint16_t* const to = out + (int64_t)h * dim;
-      *reinterpret_cast<kh4_t*>(to + at.a) = kh4_t{(_Float16)y[0], (_Float16)y[1], (_Float16)y[2], (_Float16)y[3]};
-      *reinterpret_cast<kh4_t*>(to + at.b) = kh4_t{(_Float16)y[4], (_Float16)y[5], (_Float16)y[6], (_Float16)y[7]};
-    }
+    if (there) v = load_eight(x + (int64_t)h * dim, r, at);
+    v = turn_eight(v, w, at, dim, lanes, r, g);
+    if (there) store_eight(out + (int64_t)h * dim, r, at, v);
   }
 }
 
-// Bits of the FP16 value nearest to v.
-__device__ inline uint16_t kv_bits(float v) { return __builtin_bit_cast(uint16_t, (_Float16)v); }
 #endif
 
 }  // namespace tern

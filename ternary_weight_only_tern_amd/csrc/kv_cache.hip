@@ -3,10 +3,8 @@
 //
 // A page's scale s has 8 significant bits and the values 11 (the keys are
 // rounded to FP16 after they are turned, as if a call of tern_rope had done
-// it), so that the quotient of a value and s, where it is no tie, lies at
-// least 2^-9 away from one: an FP32 division rounded to an integer is the
-// exact quotient's rounding.  127 s is exact, so that is the growth's
-// comparison too.
+// it): codes are the exact quotients' roundings (byte_of), and the growth's
+// comparison with 127 s is exact.
 //
 // One workgroup has a (page, head) of the keys or of the values, so that a
 // scale has one writer.  A thread owns pieces of the page: of the
@@ -23,10 +21,15 @@ __device__ inline float least_scale(float most) {
   return __uint_as_float((__float_as_uint(most / 127.0f) + 0xFFFFu) & 0xFFFF0000u);
 }
 
-// The byte of x in steps of s.
-__device__ inline uint32_t byte_of(float x, float s) {
-  const float c = s > 0.f ? rintf(x / s) : 0.f;  // 0 beside a scale that is 0 or NaN
-  return (uint32_t)((int)c + 128);
+// The byte of x in steps of s, inv = 1 / s (0 beside a scale that is 0 or NaN).
+// x inv is off by 2^-23 of the quotient.  A quotient that is no tie is 2^-16 of
+// itself away from one: |2X 2^a - (2n+1) S 2^b|, with X of 11 bits and S of 8, is
+// 2^b at least, against (2n+1) S 2^b with 2n+1 < 256, or 2^(a+1), against 2X 2^a.
+// So with 18 bits left a tie is one again and nothing else becomes one.
+__device__ inline float steps_of(float s) { return s > 0.f ? 1.0f / s : 0.f; }
+__device__ inline uint32_t byte_of(float x, float inv) {
+  const float c = rintf(__uint_as_float((__float_as_uint(x * inv) + 0x20u) & ~0x3Fu));
+  return inv > 0.f ? (uint32_t)((int)__builtin_amdgcn_fmed3f(c, -127.f, 127.f) + 128) : 128u;
 }
 
 // Four bytes rounded again to steps that are 1 / shrink times as large.
@@ -92,9 +95,9 @@ __device__ void write_keys(const WriteArgs& a, const Span& sp, int s, int page, 
     const int token = i * kRound + first;
     v[i] = {};
     if (token >= t0 && token < t1)
-      v[i] = load_eight(a.k + (sp.first + page * kPage + token - sp.from) * a.k_stride + head * D, place);
+      v[i] = load_eight(a.k + (sp.first + page * kPage + token - sp.from) * a.k_stride + head * D, a.rk, place);
   }
-  if (a.rk.norm) weight = load_eight(a.rk.norm, place);
+  if (a.rk.norm) weight = load_eight(a.rk.norm, a.rk, place);
   const int id = page_of(a.b, a.c, s, page);
   if (id < 0) return;
   const size_t at = (size_t)id * a.c.heads + head;
@@ -104,38 +107,43 @@ __device__ void write_keys(const WriteArgs& a, const Span& sp, int s, int page, 
   for (int i = 0; i < kRounds; ++i) {
     const int token = i * kRound + first;
     if (i * kRound >= t1 || i * kRound + kRound <= t0) continue;  // the same for all: no token of this round
-    const bool live = token >= t0 && token < t1;
-    const int row = sp.first + page * kPage + token - sp.from;
-    float y[8];
-    const Angles g = angles_of(a.rk, place, live && a.rk.on, page * kPage + token);
-    turn_eight(a.k + row * a.k_stride + head * D, v[i], weight, place, D, live, kLanes, a.rk, g, page * kPage + token, y);
+    const Angles g = angles_of(a.rk, place, a.rk.on && token >= t0 && token < t1, page * kPage + token);
+    v[i] = turn_eight(v[i], weight, place, D, kLanes, a.rk, g);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      v[i].h[e] = live ? kv_bits(y[e]) : 0;
-      bits = max(bits, (uint32_t)v[i].h[e] & 0x7FFFu);
-    }
+    for (int e = 0; e < 8; ++e) bits = max(bits, (uint32_t)v[i].h[e] & 0x7FFFu);
   }
   const Grown g = grow(bits, t0 == 0, old);
   if (threadIdx.x == 0) a.c.ks[at] = g.s;
   uint8_t* const base = a.c.k + at * (kPage * D);
+  const float inv = steps_of(g.s);
+  const bool words = !sided(a.rk) || a.rk.rot % 8 == 0;  // four dimensions are a word of the page
 #pragma unroll
   for (int i = 0; i < kRounds; ++i) {
     const int token = i * kRound + first;
     const bool live = token >= t0 && token < t1;
     if (!live && g.keep) continue;
+    auto byte_at = [&](int d) {
+      return base + ((d / 64 * 4 + token / 4 % 4) * 64 + d / 16 % 4 * 16 + token / 16 * 4 + token % 4) * 16 + d % 16;
+    };
+    if (words) {
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
-      const int d = q ? place.b : place.a;
-      uint32_t* const to = reinterpret_cast<uint32_t*>(
-          base + ((d / 64 * 4 + token / 4 % 4) * 64 + d / 16 % 4 * 16 + token / 16 * 4 + token % 4) * 16 + d % 16);
-      uint32_t w = 0;
-      if (live) {
+      for (int q = 0; q < 2; ++q) {
+        uint32_t* const to = reinterpret_cast<uint32_t*>(byte_at(q ? place.b : place.a));
+        uint32_t w = 0;
+        if (live) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) w |= byte_of(kv_half(v[i].h[4 * q + e]), g.s) << (8 * e);
-      } else {
-        w = again4(*to, g.shrink);
+          for (int e = 0; e < 4; ++e) w |= byte_of(kv_half(v[i].h[4 * q + e]), inv) << (8 * e);
+        } else {
+          w = again4(*to, g.shrink);
+        }
+        *to = w;
       }
-      *to = w;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        uint8_t* const to = byte_at(dim_of(a.rk, place, e));
+        *to = (uint8_t)(live ? byte_of(kv_half(v[i].h[e]), inv) : again4(*to, g.shrink));
+      }
     }
   }
 }
@@ -174,21 +182,22 @@ __device__ void write_values(const WriteArgs& a, const Span& sp, int s, int page
   const Grown g = grow(bits, t0 == 0, old);
   if (threadIdx.x == 0) a.c.vs[at] = g.s;
   if (part >= 4 || (g.keep && !some)) return;
+  if (!g.keep)
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    if (!g.keep)
+    for (int e = 0; e < 4; ++e)
 #pragma unroll
       for (int q = 0; q < 4; ++q) o[e][q] = again4(o[e][q], g.shrink);
-  }
+  const float inv = steps_of(g.s);
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
+    if (t1 <= part * 16 + q * 4 || t0 >= part * 16 + q * 4 + 4) continue;
     uint32_t in[4], out[4], mask = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int token = part * 16 + q * 4 + i;
       in[i] = 0;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) in[i] |= byte_of((float)y[q * 4 + i][e], g.s) << (8 * e);
+      for (int e = 0; e < 4; ++e) in[i] |= byte_of((float)y[q * 4 + i][e], inv) << (8 * e);
       if (token >= t0 && token < t1) mask |= 255u << (8 * i);
     }
     transpose4(in, out);
@@ -283,32 +292,28 @@ __global__ __launch_bounds__(256) void kv_read_kernel(const ReadArgs a) {
     }
     return;
   }
-  constexpr int kLanes = D / 16, kRound = 256 / kLanes;
-  const int lane = threadIdx.x % kLanes;
+  constexpr int E = F32 ? 4 : 8;  // 16 bytes of a row a lane
+  constexpr int kLanes = D / E, kRound = 256 / kLanes;
+  const int d = threadIdx.x % kLanes * E;
 #pragma unroll
   for (int i = 0; i < kPage / kRound; ++i) {
     const int token = i * kRound + threadIdx.x / kLanes;
     if (token < t0 || token >= t1) continue;
-    kw4_t w = kNone;
-    if (id >= 0)
-      w = *reinterpret_cast<const kw4_t*>(a.c.k + at * (kPage * D) +
-                                          ((lane / 4 * 4 + token / 4 % 4) * 64 + lane % 4 * 16 + token / 16 * 4 + token % 4) * 16);
-    float v[16];
+    const uint32_t* const from = reinterpret_cast<const uint32_t*>(
+        a.c.k + at * (kPage * D) + ((d / 64 * 4 + token / 4 % 4) * 64 + d / 16 % 4 * 16 + token / 16 * 4 + token % 4) * 16 + d % 16);
+    uint32_t w[E / 4];
 #pragma unroll
-    for (int e = 0; e < 16; ++e) v[e] = (float)((int)((w[e / 4] >> (8 * (e % 4))) & 255u) - 128) * scale;
-    if (F32) {
-      kf4_t* const to = reinterpret_cast<kf4_t*>((float*)out + place(token, lane * 16));
+    for (int q = 0; q < E / 4; ++q) w[q] = id < 0 ? kNone.x : from[q];
+    float v[E];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) to[q] = kf4_t{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
+    for (int e = 0; e < E; ++e) v[e] = (float)((int)((w[e / 4] >> (8 * (e % 4))) & 255u) - 128) * scale;
+    if constexpr (F32) {
+      *reinterpret_cast<kf4_t*>((float*)out + place(token, d)) = kf4_t{v[0], v[1], v[2], v[3]};
     } else {
-      kh8_t* const to = reinterpret_cast<kh8_t*>((_Float16*)out + place(token, lane * 16));
+      kh8_t h;
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        kh8_t h;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) h[e] = (_Float16)v[8 * q + e];
-        to[q] = h;
-      }
+      for (int e = 0; e < 8; ++e) h[e] = (_Float16)v[e];
+      *reinterpret_cast<kh8_t*>((_Float16*)out + place(token, d)) = h;
     }
   }
 }
