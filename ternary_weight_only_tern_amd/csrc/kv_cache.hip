@@ -284,10 +284,10 @@ __global__ __launch_bounds__(256) void kv_read_kernel(const ReadArgs a) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[e] = (float)((int)((tok[i] >> (8 * e)) & 255u) - 128) * scale;
         if (F32)
-          *reinterpret_cast<kf4_t*>((float*)out + place(token, d0)) = kf4_t{v[0], v[1], v[2], v[3]};
+          __builtin_nontemporal_store(kf4_t{v[0], v[1], v[2], v[3]}, reinterpret_cast<kf4_t*>((float*)out + place(token, d0)));
         else
-          *reinterpret_cast<kh4_t*>((_Float16*)out + place(token, d0)) =
-              kh4_t{(_Float16)v[0], (_Float16)v[1], (_Float16)v[2], (_Float16)v[3]};
+          __builtin_nontemporal_store(kh4_t{(_Float16)v[0], (_Float16)v[1], (_Float16)v[2], (_Float16)v[3]},
+                                      reinterpret_cast<kh4_t*>((_Float16*)out + place(token, d0)));
       }
     }
     return;
@@ -308,12 +308,12 @@ __global__ __launch_bounds__(256) void kv_read_kernel(const ReadArgs a) {
 #pragma unroll
     for (int e = 0; e < E; ++e) v[e] = (float)((int)((w[e / 4] >> (8 * (e % 4))) & 255u) - 128) * scale;
     if constexpr (F32) {
-      *reinterpret_cast<kf4_t*>((float*)out + place(token, d)) = kf4_t{v[0], v[1], v[2], v[3]};
+      __builtin_nontemporal_store(kf4_t{v[0], v[1], v[2], v[3]}, reinterpret_cast<kf4_t*>((float*)out + place(token, d)));
     } else {
       kh8_t h;
 #pragma unroll
       for (int e = 0; e < 8; ++e) h[e] = (_Float16)v[e];
-      *reinterpret_cast<kh8_t*>((_Float16*)out + place(token, d)) = h;
+      __builtin_nontemporal_store(h, reinterpret_cast<kh8_t*>((_Float16*)out + place(token, d)));
     }
   }
 }
