@@ -313,13 +313,16 @@ __device__ inline void turn_row(const uint16_t* x, uint16_t* out, int heads, int
   const Angles g = angles_of(r, at, live, pos);
   Eight w = {};
   if (live && r.norm) w = load_eight(r.norm, r, at);
-  for (int h0 = first; h0 < heads; h0 += step) {
-    const int h = h0 + (threadIdx.x & 63) / lanes;
-    const bool there = live && h < heads;
-    Eight v = {};
-    if (there) v = load_eight(x + (int64_t)h * dim, r, at);
-    v = turn_eight(v, w, at, dim, lanes, r, g);
-    if (there) store_eight(out + (int64_t)h * dim, r, at, v);
+  // the next heads are read while these are turned (out may be x: they are others)
+  int h = first + (threadIdx.x & 63) / lanes;
+  Eight v = {};
+  if (live && h < heads) v = load_eight(x + (int64_t)h * dim, r, at);
+  for (int h0 = first; h0 < heads; h0 += step, h += step) {
+    Eight next = {};
+    if (live && h + step < heads) next = load_eight(x + (int64_t)(h + step) * dim, r, at);
+    const Eight y = turn_eight(v, w, at, dim, lanes, r, g);
+    if (live && h < heads) store_eight(out + (int64_t)h * dim, r, at, y);
+    v = next;
   }
 }
 
