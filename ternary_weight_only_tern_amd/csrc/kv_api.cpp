@@ -135,7 +135,14 @@ struct AttnPlan {
   size_t rows, info;  // of partial sums, and units whose pieces are noted
 };
 constexpr int kPieces = 2048;     // of the kernel for few rows: two wavefronts on each SIMD
-constexpr int kWholePages = 1;    // pages of a unit that is not cut
+// A unit is cut into at most so many pieces: more make the joining longer than
+// the pieces shorter (us, pages a piece at least 1 / 2 / 3 / 4: one token of 8
+// cache heads after 1000 tokens 8.9 / 10.2 / 12.4 / 13.1, 4000 10.9 / 11.3 / 12.6 /
+// 14.7, 16000 18.8 / 16.1 / 15.1 / 16.0).
+constexpr int kUnitPieces = 96;
+// Units of so few pages are not cut: a page more costs a wavefront 1.5 us,
+// joining 4.5 us.
+constexpr int kWholePages = 3;
 constexpr int kTileTarget = 512;  // workgroups on tiles
 constexpr int kPartPages = 4;     // the least of a part on tiles
 
@@ -156,7 +163,7 @@ AttnPlan plan_of(const tern_kv* c, const tern_kv_batch* b, int group, int window
     p.blocks = rows <= 16 ? 1 : 2;
     p.whole = pages <= kWholePages;
     p.pieces = (int)(p.whole ? std::min<long long>(units, 1ll << 30) : std::min<long long>(p.blocks * c->dim > 128 ? kPieces / 2 : kPieces, units * pages));
-    p.per = 1;
+    p.per = (pages + kUnitPieces - 1) / kUnitPieces;
     p.join = !p.whole;
     p.rows = p.join ? (size_t)p.pieces * 2 * rows : 0;
     p.info = p.join ? units : 0;
