@@ -747,12 +747,21 @@ class Rope:
 def _heads(t, name, device, heads, dim):
     """Checks rows of heads, fp16 [m][heads][dim] whose heads follow each
     other (heads None: any number); the rows' stride."""
+    shape, stride = t.shape, t.stride()
+    if (len(shape) == 3 and t.dtype is _halves[0] and t.device == device and shape[2] == dim and stride[2] == 1
+            and stride[1] == dim and (heads is None or shape[1] == heads) and 0 < shape[0] < 2 ** 31 and shape[1] < 2 ** 31):
+        return stride[0] if shape[0] > 1 else shape[1] * dim
+    return _heads_slowly(t, name, device, heads, dim)
+
+
+def _heads_slowly(t, name, device, heads, dim):
+    """The same where a size is 1 or 0, and what is wrong otherwise."""
     if t.dtype != _torch.float16 or t.device != device:
         _refuse(f"{name} is {t.dtype} on {t.device}, not torch.float16 on {device}")
     shape = t.shape
     if len(shape) != 3 or shape[2] != dim or (heads is not None and shape[1] != heads):
         _refuse(f"{name} has shape {tuple(shape)}, not [m][{'heads' if heads is None else heads}][{dim}]")
-    m, heads = shape[0], shape[1]
+    m, heads = _count(shape[0]), _count(shape[1])
     row, head, step = t.stride()
     if not m * heads * dim:
         return 0
@@ -769,18 +778,18 @@ def tern_rope(x, pos, rope: Rope, out=None, stream=None):
     if _elsewhere(device):
         with torch.cuda.device(device):
             return tern_rope(x, pos, rope, out, stream)
-    if x.dim() != 3:
-        _refuse(f"x has shape {tuple(x.shape)}, not [m][heads][dim]")
-    m, heads, dim = x.shape
+    shape = x.shape
+    if len(shape) != 3:
+        _refuse(f"x has shape {tuple(shape)}, not [m][heads][dim]")
+    m, heads, dim = shape
     x_stride = _heads(x, "x", device, heads, dim)
     _tensor(pos, "pos", (torch.int32,), device, (m,))
     if out is None:
         out = _fresh((m, heads, dim), torch.float16, device, stream)
-    elif out.shape != x.shape:
-        _refuse(f"out has shape {tuple(out.shape)}, not {tuple(x.shape)}")
-    out_stride = _heads(out, "out", device, heads, dim)
-    check(load().tern_rope(x.data_ptr(), x_stride, _count(m), _count(heads), _count(dim), pos.data_ptr(),
-                           rope._of(device, dim), out.data_ptr(), out_stride, _stream_of(device, stream)))
+    elif out.shape != shape:
+        _refuse(f"out has shape {tuple(out.shape)}, not {tuple(shape)}")
+    check((_lib or load()).tern_rope(x.data_ptr(), x_stride, m, heads, _count(dim), pos.data_ptr(), rope._of(device, dim),
+                                     out.data_ptr(), _heads(out, "out", device, heads, dim), _stream_of(device, stream)))
     return out
 
 
@@ -865,16 +874,16 @@ def tern_kv_write(cache: KvCache, batch: KvBatch, k, v, rope=None, q=None, q_rop
             return tern_kv_write(cache, batch, k, v, rope, q, q_rope, q_out, stream)
     k_stride = _heads(k, "k", device, cache.heads, dim)
     v_stride = _heads(v, "v", device, cache.heads, dim)
-    m = k.size(0)
-    if v.size(0) != m:
-        _refuse(f"{v.size(0)} rows of v and {m} of k")
+    m = k.shape[0]
+    if v.shape[0] != m:
+        _refuse(f"{v.shape[0]} rows of v and {m} of k")
     q_at = q_out_at = None
     q_stride = q_heads = 0
     if q is not None:
         q_stride = _heads(q, "q", device, None, dim)
-        q_heads = _count(q.size(1))
-        if q.size(0) != m:
-            _refuse(f"{q.size(0)} rows of q and {m} of k")
+        rows, q_heads, _ = q.shape
+        if rows != m:
+            _refuse(f"{rows} rows of q and {m} of k")
         if q_rope is None:
             _refuse("q without q_rope")
         if q_out is None:
@@ -882,7 +891,7 @@ def tern_kv_write(cache: KvCache, batch: KvBatch, k, v, rope=None, q=None, q_rop
         else:
             _tensor(q_out, "q_out", _halves, device, (m, q_heads, dim))
         q_at, q_out_at = q.data_ptr(), q_out.data_ptr()
-    check(load().tern_kv_write(cache._at, batch._of(device, m), k.data_ptr(), k_stride, v.data_ptr(), v_stride,
+    check((_lib or load()).tern_kv_write(cache._at, batch._of(device, m), k.data_ptr(), k_stride, v.data_ptr(), v_stride,
                                None if rope is None else rope._of(device, dim), q_at, q_stride, q_heads,
                                None if q is None else q_rope._of(device, dim), q_out_at, _stream_of(device, stream)))
     return q_out
@@ -932,14 +941,14 @@ def tern_kv_attention(cache: KvCache, batch: KvBatch, q, scale=None, window=0, c
         out = _fresh((m, q_heads, dim), _torch.float16, device, stream)
     else:
         _tensor(out, "out", _halves, device, q.shape)
-    at = batch._of(device, m)
+    at, lib = batch._of(device, m), _lib or load()
     if ws is None:
-        ws = _scratch(load().tern_kv_attention_workspace_bytes(cache._at, at, _count(q_heads)), device, stream)
+        ws = _scratch(lib.tern_kv_attention_workspace_bytes(cache._at, at, q_heads), device, stream)
     else:
         _space(ws, device)
-    check(load().tern_kv_attention(cache._at, at, q.data_ptr(), q_stride, _count(q_heads), dim ** -0.5 if scale is None else scale,
-                                   _count(window), 1 if causal else 0, out.data_ptr(), ws.data_ptr(), ws.nbytes,
-                                   _stream_of(device, stream)))
+    check(lib.tern_kv_attention(cache._at, at, q.data_ptr(), q_stride, q_heads, dim ** -0.5 if scale is None else scale,
+                                _count(window), 1 if causal else 0, out.data_ptr(), ws.data_ptr(), ws.nbytes,
+                                _stream_of(device, stream)))
     return out
 
 
