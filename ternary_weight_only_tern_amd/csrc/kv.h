@@ -105,7 +105,7 @@ constexpr int kAttnFew = 16, kAttnTile = 128;
 hipError_t launch_rope(const RopeArgs& a, hipStream_t s);
 hipError_t launch_kv_write(WriteArgs a, int dim, hipStream_t s);
 hipError_t launch_kv_read(const ReadArgs& a, int dim, hipStream_t s);
-// blocks: of 16 rows, 1 or 2 (1 at dim 256)
+// blocks: of 16 rows, 1 or 2
 hipError_t launch_attn_rows(const AttnArgs& a, int dim, int blocks, hipStream_t s);
 hipError_t launch_attn_tile(const AttnArgs& a, int dim, hipStream_t s);
 hipError_t launch_attn_join(const AttnArgs& a, int dim, hipStream_t s);

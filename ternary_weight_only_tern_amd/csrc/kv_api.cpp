@@ -152,14 +152,16 @@ int pages_of(const tern_kv_batch* b, int window) {
   return (int)((tokens + tern::kPage - 1) / tern::kPage);
 }
 
-// Rows on which a unit goes to the kernel for few rows.
-int few_rows(int dim) { return dim == 256 ? 16 : 32; }
+// Rows up to which a unit goes to the kernel for few rows.  us, few rows / tiles:
+// 8 x 8 cache heads after 8000 tokens, 16 rows each 37 / -, 20 rows at 256
+// dimensions 80 / 104, 40 rows (four blocks, not kept) 73 / 56, 64 rows 75 / 56.
+constexpr int kFewRows = 32;
 
 AttnPlan plan_of(const tern_kv* c, const tern_kv_batch* b, int group, int window) {
   AttnPlan p = {};
   const long long rows = (long long)b->max_rows * group, units = (long long)b->count * c->heads;
   const int pages = pages_of(b, window);
-  if (rows <= few_rows(c->dim)) {
+  if (rows <= kFewRows) {
     p.blocks = rows <= 16 ? 1 : 2;
     p.whole = pages <= kWholePages;
     p.pieces = (int)(p.whole ? std::min<long long>(units, 1ll << 30) : std::min<long long>(p.blocks * c->dim > 128 ? kPieces / 2 : kPieces, units * pages));
@@ -185,7 +187,7 @@ size_t attn_need(const AttnPlan& p, const tern_kv* c) { return p.rows * (c->dim 
 // come to at most twice kTileTarget workgroups.
 size_t attn_need_upto(const tern_kv* c, const tern_kv_batch* b, int group) {
   const double rows = (double)b->rows * group, pages = pages_of(b, 0);
-  const double few = 2.0 * std::min<double>(kPieces, (double)b->count * c->heads * pages) * std::min<double>(rows, few_rows(c->dim));
+  const double few = 2.0 * std::min<double>(kPieces, (double)b->count * c->heads * pages) * std::min<double>(rows, kFewRows);
   const double tiles = std::min(rows * c->heads * std::ceil(pages / kPartPages), 2.0 * kTileTarget * tern::kAttnTile);
   return (size_t)(std::max(few, tiles) * (c->dim + 2) * 4) + (size_t)b->count * c->heads * 8;
 }

@@ -142,7 +142,13 @@ __global__ __launch_bounds__(64, NT * D <= 128 ? 2 : 1) void attn_rows_kernel(co
     return x;
   };
 
-  kh8_t q[NT][C][2];
+  // Two blocks' queries of 256 dimensions lie in LDS: there are no registers for them.
+  constexpr bool kInLds = NT * C > 4;
+  __shared__ kw4_t lq[kInLds ? NT * C * 2 * 64 : 1];
+  kh8_t q[kInLds ? 1 : NT][C][2];
+  auto query = [&](int n, int c, int u) {
+    return kInLds ? __builtin_bit_cast(kh8_t, lq[((n * C + c) * 2 + u) * 64 + lane]) : q[kInLds ? 0 : n][c][u];
+  };
   Sees sees[NT];
   int low, high;  // tokens that every row sees
   Row row[NT];
@@ -163,7 +169,13 @@ __global__ __launch_bounds__(64, NT * D <= 128 ? 2 : 1) void attn_rows_kernel(co
 #pragma unroll
       for (int c = 0; c < C; ++c)
 #pragma unroll
-        for (int u = 0; u < 2; ++u) q[n][c][u] = __builtin_bit_cast(kh8_t, kv_load16(from, at + 128 * c + 16 * u));
+        for (int u = 0; u < 2; ++u) {
+          const kw4_t v = kv_load16(from, at + 128 * c + 16 * u);
+          if (kInLds)
+            lq[((n * C + c) * 2 + u) * 64 + lane] = v;
+          else
+            q[kInLds ? 0 : n][c][u] = __builtin_bit_cast(kh8_t, v);
+        }
     }
   };
   auto begin_rows = [&](const Span& sp) {
@@ -227,6 +239,8 @@ __global__ __launch_bounds__(64, NT * D <= 128 ? 2 : 1) void attn_rows_kernel(co
     ks_next = scale_at(a.c.ks, next);
     vs_next = scale_at(a.c.vs, next);
     const bool last = next.left < 0 || next.head != now.head || next.s != now.s;  // of the unit, here
+    const bool whole = now.id >= 0 && now.p * kPage >= low && now.p * kPage + kPage <= high;
+    kh8_t w[NT][2];
     kf4_t z[NT][4];
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
@@ -239,14 +253,12 @@ __global__ __launch_bounds__(64, NT * D <= 128 ? 2 : 1) void attn_rows_kernel(co
         for (int u = 0; u < 2; ++u) {
           const kh8_t k = codes8(kr[c][t][2 * u], kr[c][t][2 * u + 1]);
 #pragma unroll
-          for (int n = 0; n < NT; ++n) z[n][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k, q[n][c][u], z[n][t], 0, 0, 0);
+          for (int n = 0; n < NT; ++n) z[n][t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(k, query(n, c, u), z[n][t], 0, 0, 0);
         }
     }
     __builtin_amdgcn_sched_barrier(0);
     load_keys(next);
     if (last && next.left >= 0) load_q(next, run_next.sp);
-    const bool whole = now.id >= 0 && now.p * kPage >= low && now.p * kPage + kPage <= high;
-    kh8_t w[NT][2];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
       float best = -INFINITY;
@@ -399,7 +411,7 @@ hipError_t rows(const AttnArgs& a, int blocks, hipStream_t s) {
   if (!kv_grid_fits(grid, 64)) return hipErrorInvalidConfiguration;
   if (blocks == 1)
     hipLaunchKernelGGL((attn_rows_kernel<D, 1>), dim3((unsigned)grid), dim3(64), 0, s, a);
-  else if constexpr (D <= 128)
+  else
     hipLaunchKernelGGL((attn_rows_kernel<D, 2>), dim3((unsigned)grid), dim3(64), 0, s, a);
   return hipGetLastError();
 }

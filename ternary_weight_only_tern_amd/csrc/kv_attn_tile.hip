@@ -152,6 +152,10 @@ __global__ __launch_bounds__(64 * kTileWaves, D <= 128 ? 2 : 1) void attn_tile_k
   int p = mine.begin, cur = 0;
   int raw = load_id(p), raw1 = load_id(p + 1), raw2 = load_id(p + 2), raw3 = load_id(p + 3);
   int id = id_of(raw, p), id1 = id_of(raw1, p + 1), id2 = id_of(raw2, p + 2);
+  load_keys(id1);  // the first pages together, the second's keys kept aside
+  kw4_t second[PIECES];
+#pragma unroll
+  for (int i = 0; i < PIECES; ++i) second[i] = kr[i];
   load_keys(id);
   load_values(id);
   float ks0 = load_scale(a.c.ks, id), vs0 = load_scale(a.c.vs, id);  // this page's, the next one's
@@ -160,7 +164,8 @@ __global__ __launch_bounds__(64 * kTileWaves, D <= 128 ? 2 : 1) void attn_tile_k
   if (mine.begin < mine.end) {
 #pragma unroll
     for (int u = 0; u < 4 * PIECES; ++u) decode(u, lk[0], lv[0]);
-    load_keys(id1);
+#pragma unroll
+    for (int i = 0; i < PIECES; ++i) kr[i] = second[i];
     if constexpr (LEAD) {
 #pragma unroll
       for (int u = 0; u < 2 * PIECES; ++u) decode(u, lk[1], nullptr);

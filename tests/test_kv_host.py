@@ -152,7 +152,7 @@ def test_which_way_a_call_goes():
     assert parts(count=1, max_rows=1, max_len=100) == 8  # whole units
     assert parts(count=4, max_rows=5, max_len=120000) == 1024  # two blocks of rows
     assert parts(count=1, max_rows=9, max_len=5000) < -2 and parts(count=1, max_rows=2048, max_len=4000) == -2
-    assert parts(count=1, max_rows=5, max_len=5000, c=cache(dim=256)) < -2
+    assert parts(count=1, max_rows=8, max_len=5000, c=cache(dim=256)) == 632 and parts(count=1, max_rows=9, max_len=5000, c=cache(dim=256)) < -2
     assert parts(count=1, max_rows=1, max_len=100000, window=100) == 8 and parts(count=0) == 0  # three pages are not cut
     assert parts(count=1, max_rows=1, max_len=100000, window=300) == 48
     assert parts(q_heads=30) == -1 and parts(window=-1) == -1
