@@ -143,6 +143,12 @@ constexpr int kUnitPieces = 96;
 // Units of so few pages are not cut: a page more costs a wavefront 1.5 us,
 // joining 4.5 us.
 constexpr int kWholePages = 3;
+// Nor are units that are many for their pages: joining then costs more than
+// the wait for the longest ones.  32 query heads over 8, ragged lengths,
+// cut -> whole: 512 units of up to 8 pages 16.9 -> 15.9 us, of 16 20.4 -> 27.1;
+// 1024 of 8 27.7 -> 19.0; 2048 of 16 71.9 -> 61.7, of 64 210 -> 231; 4096 of 32
+// 220 -> 204, of 128 710 -> 764.  Four rows each, 1024 of 8: 40.5 -> 20.3.
+constexpr int kWholeUnits = 64;  // for every page
 constexpr int kTileTarget = 512;  // workgroups on tiles
 constexpr int kPartPages = 4;     // the least of a part on tiles
 
@@ -163,7 +169,7 @@ AttnPlan plan_of(const tern_kv* c, const tern_kv_batch* b, int group, int window
   const int pages = pages_of(b, window);
   if (rows <= kFewRows) {
     p.blocks = rows <= 16 ? 1 : 2;
-    p.whole = pages <= kWholePages;
+    p.whole = pages <= kWholePages || units >= (long long)kWholeUnits * pages;
     p.pieces = (int)(p.whole ? std::min<long long>(units, 1ll << 30) : std::min<long long>(p.blocks * c->dim > 128 ? kPieces / 2 : kPieces, units * pages));
     p.per = (pages + kUnitPieces - 1) / kUnitPieces;
     p.join = !p.whole;

@@ -199,6 +199,18 @@ def test_parts_give_what_one_gives(rows):
         run(c, 2, rng, q=q, max_len=max_len, note=f"max_len {max_len}")
 
 
+@pytest.mark.parametrize("dim,rows", [(64, 1), (128, 3)])
+def test_many_short_sequences(dim, rows):
+    """More units than 64 for every page: a wavefront each; cut by a max_len
+    that leaves too few."""
+    rng = np.random.default_rng(48)
+    lens = [int(n) for n in rng.integers(0, 513, 77)] + [512, 1, 64]
+    c = Case(rng, [rows] * len(lens), [n + rows for n in lens], 8, dim)
+    q = half(rng, c.m, 32, dim)
+    for max_len in (None, 8192):
+        run(c, 32, rng, q=q, max_len=max_len, note=f"max_len {max_len}")
+
+
 def test_long_context():
     """A table of 2^15 pages over few pages of memory: positions past 10^6."""
     rng = np.random.default_rng(53)

@@ -155,6 +155,7 @@ def test_which_way_a_call_goes():
     assert parts(count=1, max_rows=8, max_len=5000, c=cache(dim=256)) == 632 and parts(count=1, max_rows=9, max_len=5000, c=cache(dim=256)) < -2
     assert parts(count=1, max_rows=1, max_len=100000, window=100) == 8 and parts(count=0) == 0  # three pages are not cut
     assert parts(count=1, max_rows=1, max_len=100000, window=300) == 48
+    assert parts(count=64, max_rows=1, max_len=512) == 512 and parts(count=64, max_rows=1, max_len=513) == 2048  # 64 units a page
     assert parts(q_heads=30) == -1 and parts(window=-1) == -1
 
 
