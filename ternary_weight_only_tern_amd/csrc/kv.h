@@ -90,7 +90,8 @@ struct AttnArgs {
   // at least; their sums [pieces][2][max_rows * group][dim] and references and
   // sums of weights [pieces][2][max_rows * group][2] in part; info: a unit's first
   // piece and how many it has.  Tiles (tiles > 0): parts of the context at most,
-  // `per` pages each at least; part: [parts][rows][q_heads][dim], then [..][2].
+  // `per` pages each at least; part: [tiles][count][heads][parts][128][dim] in an order of the
+  // kernel's own, then [tiles][count][heads][parts][128][2].
   float* part;
   int2* info;
   float scale;         // times log2(e)
@@ -108,7 +109,8 @@ hipError_t launch_kv_read(const ReadArgs& a, int dim, hipStream_t s);
 // blocks: of 16 rows, 1 or 2
 hipError_t launch_attn_rows(const AttnArgs& a, int dim, int blocks, hipStream_t s);
 hipError_t launch_attn_tile(const AttnArgs& a, int dim, hipStream_t s);
-hipError_t launch_attn_join(const AttnArgs& a, int dim, hipStream_t s);
+hipError_t launch_attn_join_rows(const AttnArgs& a, int dim, hipStream_t s);
+hipError_t launch_attn_join_tile(const AttnArgs& a, int dim, hipStream_t s);
 
 // Wavefronts that share a row's heads: one where there are rows enough to fill
 // the card, as many as have heads where there are few.

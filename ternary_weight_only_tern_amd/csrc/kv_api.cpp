@@ -120,12 +120,13 @@ tern_status check_arrays(const tern_kv* c, const tern_kv_batch* b) {
 }
 
 tern::Cache cache_of(const tern_kv* c) { return {c->k, c->v, c->k_scale, c->v_scale, c->heads, c->pages}; }
+int most_rows(const tern_kv_batch* b) { return std::min(b->max_rows, b->rows); }
 tern::Batch batch_of(const tern_kv_batch* b) {
-  return {b->start, b->len, b->pages, b->count, b->rows, b->max_rows, b->max_pages};
+  return {b->start, b->len, b->pages, b->count, b->rows, most_rows(b), b->max_pages};
 }
 
 // Pages that a sequence's rows may lie in.
-int items_of(const tern_kv_batch* b) { return (b->max_rows + 2 * (tern::kPage - 1)) / tern::kPage; }
+int items_of(const tern_kv_batch* b) { return (most_rows(b) + 2 * (tern::kPage - 1)) / tern::kPage; }
 
 // How attention runs.
 struct AttnPlan {
@@ -154,7 +155,7 @@ constexpr int kPartPages = 4;     // the least of a part on tiles
 
 int pages_of(const tern_kv_batch* b, int window) {
   long long tokens = b->max_len;
-  if (window > 0) tokens = std::min<long long>(tokens, (long long)window + b->max_rows + tern::kPage);
+  if (window > 0) tokens = std::min<long long>(tokens, (long long)window + most_rows(b) + tern::kPage);
   return (int)((tokens + tern::kPage - 1) / tern::kPage);
 }
 
@@ -165,7 +166,7 @@ constexpr int kFewRows = 32;
 
 AttnPlan plan_of(const tern_kv* c, const tern_kv_batch* b, int group, int window) {
   AttnPlan p = {};
-  const long long rows = (long long)b->max_rows * group, units = (long long)b->count * c->heads;
+  const long long rows = (long long)most_rows(b) * group, units = (long long)b->count * c->heads;
   const int pages = pages_of(b, window);
   if (rows <= kFewRows) {
     p.blocks = rows <= 16 ? 1 : 2;
@@ -182,7 +183,7 @@ AttnPlan plan_of(const tern_kv* c, const tern_kv_batch* b, int group, int window
   p.per = groups < kTileTarget / 2 ? std::max(kPartPages, (int)((groups * pages + kTileTarget - 1) / kTileTarget)) : std::max(1, pages);
   p.parts = std::max(1, (pages + p.per - 1) / p.per);
   p.join = p.parts > 1;
-  p.rows = p.join ? (size_t)p.parts * b->rows * group * c->heads : 0;
+  p.rows = p.join ? (size_t)groups * p.parts * tern::kAttnTile : 0;
   return p;
 }
 
@@ -190,11 +191,12 @@ size_t attn_need(const AttnPlan& p, const tern_kv* c) { return p.rows * (c->dim 
 
 // The most that any batch with no more sequences and rows and no larger
 // max_len needs: few rows leave at most kPieces pairs of slots, parts of tiles
-// come to at most twice kTileTarget workgroups.
+// come to at most 1.5 kTileTarget workgroups.
 size_t attn_need_upto(const tern_kv* c, const tern_kv_batch* b, int group) {
   const double rows = (double)b->rows * group, pages = pages_of(b, 0);
   const double few = 2.0 * std::min<double>(kPieces, (double)b->count * c->heads * pages) * std::min<double>(rows, kFewRows);
-  const double tiles = std::min(rows * c->heads * std::ceil(pages / kPartPages), 2.0 * kTileTarget * tern::kAttnTile);
+  const double groups = (double)b->count * c->heads * std::ceil(rows / tern::kAttnTile);
+  const double tiles = rows <= kFewRows ? 0.0 : std::min(groups * std::ceil(pages / kPartPages), 1.5 * kTileTarget) * tern::kAttnTile;
   return (size_t)(std::max(few, tiles) * (c->dim + 2) * 4) + (size_t)b->count * c->heads * 8;
 }
 
@@ -384,7 +386,7 @@ tern_status tern_kv_attention(const tern_kv* c, const tern_kv_batch* b, const ui
     KV_HIP(tern::launch_attn_rows(a, c->dim, p.blocks, s));
   else
     KV_HIP(tern::launch_attn_tile(a, c->dim, s));
-  if (p.join) KV_HIP(tern::launch_attn_join(a, c->dim, s));
+  if (p.join) KV_HIP(p.blocks ? tern::launch_attn_join_rows(a, c->dim, s) : tern::launch_attn_join_tile(a, c->dim, s));
   return TERN_OK;
 }
 

@@ -99,18 +99,6 @@ __device__ inline void finish_row(const AttnArgs& a, size_t at, kf4_t v, float s
   v *= inv;
   *reinterpret_cast<kh4_t*>(a.y + at) = kh4_t{(_Float16)v.x, (_Float16)v.y, (_Float16)v.z, (_Float16)v.w};
 }
-
-// Four sums of row `out` ([row][q head]), to y or to a part's sums.
-template <int D>
-__device__ inline void store_row(const AttnArgs& a, const Parts& p, int part, size_t out, int d, kf4_t v, float top, float sum) {
-  if (p.count == 1) {
-    finish_row(a, out * D + d, v, sum);
-    return;
-  }
-  const size_t rows = (size_t)a.b.rows * a.q_heads, at = (size_t)part * rows + out;
-  *reinterpret_cast<kf4_t*>(a.part + at * D + d) = v;
-  if (d == 0) *reinterpret_cast<kw2_t*>(a.part + (size_t)a.parts * rows * D + at * 2) = kw2_t{__float_as_uint(top), __float_as_uint(sum)};
-}
 #endif
 
 }  // namespace tern

@@ -343,8 +343,8 @@ __global__ __launch_bounds__(64, NT * D <= 128 ? 2 : 1) void attn_rows_kernel(co
   }
 }
 
-// y from the sums of a unit's pieces, or of a tile's parts, in their order: a
-// workgroup has a row's head, its groups of lanes take turns at the pieces.
+// y from the sums of a unit's pieces, in their order: a workgroup has a row's
+// head, its groups of lanes take turns at the pieces.
 template <int D>
 __global__ __launch_bounds__(256) void attn_join_kernel(const AttnArgs a) {
   constexpr int L = D / 4, G = 256 / L;  // lanes of a row, groups
@@ -353,27 +353,13 @@ __global__ __launch_bounds__(256) void attn_join_kernel(const AttnArgs a) {
   const int s = blockIdx.x / a.b.max_rows, j = blockIdx.x % a.b.max_rows, head = blockIdx.y;
   const Span sp = span_of(a.b, s);
   if (j >= sp.n) return;
-  // the pieces' rows: the first, how many, how far apart
-  const int local = j * a.group + head % a.group;
-  const size_t out = (size_t)(sp.first + j) * a.q_heads + head;
-  size_t first, step, all;
-  int count;
-  if (a.tiles) {
-    const int block = local / kAttnTile * kAttnTile;
-    count = parts_of(a, range_of_rows(a, sp, block, min(block + kAttnTile, sp.n * a.group) - 1)).count;
-    first = out;
-    step = (size_t)a.b.rows * a.q_heads;
-    all = step * a.parts;
-  } else {
-    const int2 info = a.info[s * a.c.heads + head / a.group];
-    const size_t rows = (size_t)a.b.max_rows * a.group;
-    count = info.y;
-    first = (size_t)info.x * 2 * rows + local;  // its second slot, the others' first ones
-    step = 2 * rows;
-    all = (size_t)a.pieces * 2 * rows;
-  }
+  const int2 info = a.info[s * a.c.heads + head / a.group];
+  const int count = info.y;
   if (count == 1) return;  // written where it was computed
-  auto at = [&](int i) { return first + i * step + (!a.tiles && i == 0 ? step / 2 : 0); };
+  // the pieces' rows: the second slot of the first, the others' first ones
+  const size_t rows = (size_t)a.b.max_rows * a.group, step = 2 * rows, all = (size_t)a.pieces * step;
+  const size_t first = (size_t)info.x * step + j * a.group + head % a.group, out = (size_t)(sp.first + j) * a.q_heads + head;
+  auto at = [&](int i) { return first + i * step + (i == 0 ? rows : 0); };
   const int g = threadIdx.x / L, d = threadIdx.x % L * 4;
   const kw2_t* const tops = reinterpret_cast<const kw2_t*>(a.part + all * D);
   // one pass: every group keeps its own reference
@@ -431,7 +417,7 @@ hipError_t launch_attn_rows(const AttnArgs& a, int dim, int blocks, hipStream_t 
   return dim == 128 ? rows<128>(a, blocks, s) : rows<256>(a, blocks, s);
 }
 
-hipError_t launch_attn_join(const AttnArgs& a, int dim, hipStream_t s) {
+hipError_t launch_attn_join_rows(const AttnArgs& a, int dim, hipStream_t s) {
   if (dim == 64) return join<64>(a, s);
   return dim == 128 ? join<128>(a, s) : join<256>(a, s);
 }

@@ -19,6 +19,16 @@ namespace {
 
 constexpr int kTileWaves = 4, kCus = 256;
 
+// A tile's first part among all parts' sums, and the references and sums of
+// weights behind them.
+__device__ inline size_t part_slot(const AttnArgs& a, int s, int head, int tile) {
+  return (((size_t)tile * a.b.count + s) * a.c.heads + head) * a.parts;
+}
+template <int D>
+__device__ inline kw2_t* part_totals(const AttnArgs& a) {
+  return reinterpret_cast<kw2_t*>(a.part + (size_t)a.tiles * a.b.count * a.c.heads * a.parts * kAttnTile * D);
+}
+
 template <int D>
 __global__ __launch_bounds__(64 * kTileWaves, D <= 128 ? 2 : 1) void attn_tile_kernel(const AttnArgs a) {
   constexpr int THREADS = 64 * kTileWaves, ROWS = 32 * kTileWaves;
@@ -312,19 +322,67 @@ __global__ __launch_bounds__(64 * kTileWaves, D <= 128 ? 2 : 1) void attn_tile_k
   float sum = row.sum;
   sum += __shfl_xor(sum, 32);
   if (!there) return;
-  const size_t out = (size_t)(sp.first + j) * a.q_heads + head * a.group + h;
+  if (parts.count == 1) {
+    const size_t out = ((size_t)(sp.first + j) * a.q_heads + head * a.group + h) * D;
 #pragma unroll
-  for (int d = 0; d < DB; ++d)
-#pragma unroll
-    for (int v = 0; v < 4; ++v) {
-      const kf4_t x = {o[d][4 * v], o[d][4 * v + 1], o[d][4 * v + 2], o[d][4 * v + 3]};
-      store_row<D>(a, parts, part, out, d * 32 + 8 * v + 4 * hq, x * (row.unit / kLift), row.top, sum);
+    for (int i = 0; i < D / 8; ++i) {
+      const kf4_t x = {o[i / 4][i % 4 * 4], o[i / 4][i % 4 * 4 + 1], o[i / 4][i % 4 * 4 + 2], o[i / 4][i % 4 * 4 + 3]};
+      finish_row(a, out + 8 * i + 4 * hq, x * (row.unit / kLift), sum);
     }
+    return;
+  }
+  // A part's sums as the lanes have them, 1 KB a store.
+  const size_t slot = part_slot(a, s, head, tile) + part;
+  kf4_t* const to = reinterpret_cast<kf4_t*>(a.part) + slot * (D / 8) * THREADS + threadIdx.x;
+#pragma unroll
+  for (int i = 0; i < D / 8; ++i) {
+    const kf4_t x = {o[i / 4][i % 4 * 4], o[i / 4][i % 4 * 4 + 1], o[i / 4][i % 4 * 4 + 2], o[i / 4][i % 4 * 4 + 3]};
+    to[i * THREADS] = x * (row.unit / kLift);
+  }
+  if (hq == 0) part_totals<D>(a)[slot * ROWS + wave * 32 + c32] = kw2_t{__float_as_uint(row.top), __float_as_uint(sum)};
+}
+
+// y from the sums of a tile's parts, in their order: a workgroup has 8 of the
+// dimensions, its threads what the tile's own threads left.
+template <int D>
+__global__ __launch_bounds__(64 * kTileWaves) void attn_join_tile_kernel(const AttnArgs a) {
+  constexpr int THREADS = 64 * kTileWaves, ROWS = 32 * kTileWaves;
+  const int head = blockIdx.x % a.c.heads, s = blockIdx.x / a.c.heads % a.b.count, tile = blockIdx.x / a.c.heads / a.b.count;
+  const Span sp = span_of(a.b, s);
+  const int total = sp.n * a.group;
+  if (tile * ROWS >= total) return;
+  const int count = parts_of(a, range_of_rows(a, sp, tile * ROWS, min(tile * ROWS + ROWS, total) - 1)).count;
+  const int lane = threadIdx.x & 63, in = threadIdx.x / 64 * 32 + lane % 32, r = tile * ROWS + in;
+  if (count == 1 || r >= total) return;
+  const size_t slot = part_slot(a, s, head, tile);
+  const kf4_t* const sums = reinterpret_cast<const kf4_t*>(a.part) + (slot * (D / 8) + blockIdx.y) * THREADS + threadIdx.x;
+  const kw2_t* const totals = part_totals<D>(a) + slot * ROWS + in;
+  kf4_t v = {0.f, 0.f, 0.f, 0.f};
+  float sum = 0.f, top = -INFINITY;
+#pragma unroll 4
+  for (int i = 0; i < count; ++i) {
+    const kw2_t t = totals[(size_t)i * ROWS];
+    const kf4_t x = sums[(size_t)i * (D / 8) * THREADS];
+    const float own = __uint_as_float(t.x), most = fmaxf(top, own);
+    const float keep = top == most ? 1.f : __builtin_amdgcn_exp2f(top - most);
+    const float f = own == most ? 1.f : __builtin_amdgcn_exp2f(own - most);
+    sum = sum * keep + __uint_as_float(t.y) * f;
+    v = v * keep + x * f;
+    top = most;
+  }
+  const size_t out = ((size_t)(sp.first + r / a.group) * a.q_heads + head * a.group + r % a.group) * D;
+  finish_row(a, out + 8 * blockIdx.y + lane / 32 * 4, v, sum);
 }
 
 template <int D>
 hipError_t tile(const AttnArgs& a, long long grid, hipStream_t s) {
   hipLaunchKernelGGL((attn_tile_kernel<D>), dim3((unsigned)grid), dim3(64 * kTileWaves), 0, s, a);
+  return hipGetLastError();
+}
+
+template <int D>
+hipError_t join(const AttnArgs& a, hipStream_t s) {
+  hipLaunchKernelGGL((attn_join_tile_kernel<D>), dim3((unsigned)(a.b.count * a.c.heads * a.tiles), D / 8), dim3(64 * kTileWaves), 0, s, a);
   return hipGetLastError();
 }
 
@@ -335,6 +393,11 @@ hipError_t launch_attn_tile(const AttnArgs& a, int dim, hipStream_t s) {
   if (!kv_grid_fits(grid, 64 * kTileWaves)) return hipErrorInvalidConfiguration;
   if (dim == 64) return tile<64>(a, grid, s);
   return dim == 128 ? tile<128>(a, grid, s) : tile<256>(a, grid, s);
+}
+
+hipError_t launch_attn_join_tile(const AttnArgs& a, int dim, hipStream_t s) {
+  if (dim == 64) return join<64>(a, s);
+  return dim == 128 ? join<128>(a, s) : join<256>(a, s);
 }
 
 }  // namespace tern
