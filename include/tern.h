@@ -615,7 +615,7 @@ tern_status tern_kv_attention(const tern_kv *c, const tern_kv_batch *b, const ui
 
 /* Which way an attention call goes, for tests and measurements (host-only):
  * the pieces P that the kernel for few rows takes, -1 - P for the parts of the
- * context on tiles; 0: nothing to do; -1: refused. */
+ * context on tiles (of causal rows); 0: nothing to do; -1: refused. */
 int32_t tern_kv_attention_parts(const tern_kv *c, const tern_kv_batch *b, int32_t q_heads, int32_t window);
 
 /* Measurement aid, not part of the product: a plain streaming read of

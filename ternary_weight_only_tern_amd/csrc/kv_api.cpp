@@ -150,13 +150,41 @@ constexpr int kWholePages = 3;
 // 1024 of 8 27.7 -> 19.0; 2048 of 16 71.9 -> 61.7, of 64 210 -> 231; 4096 of 32
 // 220 -> 204, of 128 710 -> 764.  Four rows each, 1024 of 8: 40.5 -> 20.3.
 constexpr int kWholeUnits = 64;  // for every page
-constexpr int kTileTarget = 512;  // workgroups on tiles
-constexpr int kPartPages = 4;     // the least of a part on tiles
+constexpr int kTileSlots = 1024;  // parts of tiles at most, where tiles are cut
 
-int pages_of(const tern_kv_batch* b, int window) {
+// Pages that `rows` neighbouring rows see at most.
+int pages_of(const tern_kv_batch* b, int window, int rows) {
   long long tokens = b->max_len;
-  if (window > 0) tokens = std::min<long long>(tokens, (long long)window + most_rows(b) + tern::kPage);
+  if (window > 0) tokens = std::min<long long>(tokens, (long long)window + rows + tern::kPage);
   return (int)((tokens + tern::kPage - 1) / tern::kPage);
+}
+
+// Parts for `groups` tiles that see `pages` pages at most, `mean` on average:
+// those that cost the least by a model of the time, in us, whose figures are
+// fitted to measurements.  A page takes a workgroup `step`, or 1.4 times that
+// where two share a CU (which they do not at 256 dimensions); tiles of
+// different lengths fill CUs unevenly.  Joining takes 2 and what the parts'
+// sums take to be written and read.  Uncut and cut, us: 64 tiles of 125 pages,
+// 4 / 8 / 12 parts 177 -> 58.9 / 50.1 / 56.7; 16 tiles of 63 pages, 8 / 16 / 32 parts
+// 98.0 -> 23.0 / 20.4 / 24.0; a prompt of 2048, 128 tiles, 3 / 4 / 6 / 8 parts 54.7 ->
+// 39.6 / 35.5 / 32.8 / 42.6; one of 512, 128 tiles, 2 / 3 parts 19.7 -> 21.0 / 23.9.
+int parts_for(long long groups, int pages, double mean, int dim) {
+  const double step = 0.4 + 0.01 * dim, share = dim > 128 ? 1.0 : 1.4;
+  const int slots = dim > 128 ? 256 : 512, alone = mean < pages - 1 ? 160 : 256;
+  int best = 1;
+  double least = 1e30;
+  for (int n = 1; n == 1 || (n <= pages && groups * n <= kTileSlots); n += 1 + n / 8) {
+    const int per = (pages + n - 1) / n;
+    const double all = groups * std::min<double>(n, mean / per);  // workgroups that have pages
+    double us = (all <= alone ? 1.0 : std::ceil(all / slots) * share) * per * step;
+    if (n == 1) us = std::max(std::min(us, groups * mean * step * share / slots), pages * step);  // long tiles first
+    if (n > 1) us += 2.0 + 1.6e-4 * groups * n * dim;
+    if (us < least) {
+      least = us;
+      best = n;
+    }
+  }
+  return best;
 }
 
 // Rows up to which a unit goes to the kernel for few rows.  us, few rows / tiles:
@@ -164,11 +192,11 @@ int pages_of(const tern_kv_batch* b, int window) {
 // dimensions 80 / 104, 40 rows (four blocks, not kept) 73 / 56, 64 rows 75 / 56.
 constexpr int kFewRows = 32;
 
-AttnPlan plan_of(const tern_kv* c, const tern_kv_batch* b, int group, int window) {
+AttnPlan plan_of(const tern_kv* c, const tern_kv_batch* b, int group, int window, bool causal) {
   AttnPlan p = {};
   const long long rows = (long long)most_rows(b) * group, units = (long long)b->count * c->heads;
-  const int pages = pages_of(b, window);
   if (rows <= kFewRows) {
+    const int pages = pages_of(b, window, most_rows(b));
     p.blocks = rows <= 16 ? 1 : 2;
     p.whole = pages <= kWholePages || units >= (long long)kWholeUnits * pages;
     p.pieces = (int)(p.whole ? std::min<long long>(units, 1ll << 30) : std::min<long long>(p.blocks * c->dim > 128 ? kPieces / 2 : kPieces, units * pages));
@@ -180,8 +208,12 @@ AttnPlan plan_of(const tern_kv* c, const tern_kv_batch* b, int group, int window
   }
   p.tiles = (int)((rows + tern::kAttnTile - 1) / tern::kAttnTile);
   const long long groups = p.tiles * units;
-  p.per = groups < kTileTarget / 2 ? std::max(kPartPages, (int)((groups * pages + kTileTarget - 1) / kTileTarget)) : std::max(1, pages);
-  p.parts = std::max(1, (pages + p.per - 1) / p.per);
+  const int tokens = std::min(most_rows(b), (tern::kAttnTile - 1) / group + 2);  // of a tile
+  const int pages = std::max(1, pages_of(b, window, tokens));
+  const double fewer = causal && !window ? 0.5 * (most_rows(b) - tokens) / tern::kPage : 0.0;
+  const int n = parts_for(groups, pages, std::max(1.0, pages - fewer), c->dim);
+  p.per = (pages + n - 1) / n;
+  p.parts = (pages + p.per - 1) / p.per;
   p.join = p.parts > 1;
   p.rows = p.join ? (size_t)groups * p.parts * tern::kAttnTile : 0;
   return p;
@@ -190,13 +222,13 @@ AttnPlan plan_of(const tern_kv* c, const tern_kv_batch* b, int group, int window
 size_t attn_need(const AttnPlan& p, const tern_kv* c) { return p.rows * (c->dim + 2) * 4 + p.info * 8; }
 
 // The most that any batch with no more sequences and rows and no larger
-// max_len needs: few rows leave at most kPieces pairs of slots, parts of tiles
-// come to at most 1.5 kTileTarget workgroups.
+// max_len needs: few rows leave at most kPieces pairs of slots, tiles kTileSlots
+// parts.
 size_t attn_need_upto(const tern_kv* c, const tern_kv_batch* b, int group) {
-  const double rows = (double)b->rows * group, pages = pages_of(b, 0);
+  const double rows = (double)b->rows * group, pages = pages_of(b, 0, 0);
   const double few = 2.0 * std::min<double>(kPieces, (double)b->count * c->heads * pages) * std::min<double>(rows, kFewRows);
   const double groups = (double)b->count * c->heads * std::ceil(rows / tern::kAttnTile);
-  const double tiles = rows <= kFewRows ? 0.0 : std::min(groups * std::ceil(pages / kPartPages), 1.5 * kTileTarget) * tern::kAttnTile;
+  const double tiles = rows <= kFewRows ? 0.0 : std::min<double>(groups * pages, kTileSlots) * tern::kAttnTile;
   return (size_t)(std::max(few, tiles) * (c->dim + 2) * 4) + (size_t)b->count * c->heads * 8;
 }
 
@@ -340,7 +372,7 @@ size_t tern_kv_attention_workspace_bytes(const tern_kv* c, const tern_kv_batch* 
 int32_t tern_kv_attention_parts(const tern_kv* c, const tern_kv_batch* b, int32_t q_heads, int32_t window) {
   if (check_shape(c) != TERN_OK || check_sizes(b) != TERN_OK || check_heads(c, b, q_heads) != TERN_OK || window < 0) return -1;
   if (nothing(b)) return 0;
-  const AttnPlan p = plan_of(c, b, q_heads / c->heads, window);
+  const AttnPlan p = plan_of(c, b, q_heads / c->heads, window, true);
   return p.blocks ? p.pieces : -1 - p.parts;
 }
 
@@ -358,7 +390,7 @@ tern_status tern_kv_attention(const tern_kv* c, const tern_kv_batch* b, const ui
   KV_TRY(check_rows(q, q_stride, "q"));
   if (q_stride > tern::kMaxStride) return fail(TERN_E_UNSUPPORTED, "q has the row stride %lld: %d at most", (long long)q_stride, tern::kMaxStride);
   KV_TRY(check_ptr(y, "y", 16));
-  const AttnPlan p = plan_of(c, b, q_heads / c->heads, window);
+  const AttnPlan p = plan_of(c, b, q_heads / c->heads, window, causal != 0);
   const size_t need = attn_need(p, c);
   if (need && (!ws || ws_bytes < need))
     return fail(TERN_E_WORKSPACE, "workspace of %zu bytes, %zu are needed", ws ? ws_bytes : (size_t)0, need);

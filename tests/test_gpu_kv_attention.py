@@ -199,6 +199,14 @@ def test_parts_give_what_one_gives(rows):
         run(c, 2, rng, q=q, max_len=max_len, note=f"max_len {max_len}")
 
 
+@pytest.mark.parametrize("rows,most", [([1, 2], 500), ([30, 50], 2000)])
+def test_more_rows_announced_than_there_are(rows, most):
+    rng = np.random.default_rng(44)
+    c = Case(rng, rows, [700, 900], 2, 64, ragged=True, tail=1)
+    c.max_rows = most
+    run(c, 4, rng)
+
+
 @pytest.mark.parametrize("dim,rows", [(64, 1), (128, 3)])
 def test_many_short_sequences(dim, rows):
     """More units than 64 for every page: a wavefront each; cut by a max_len

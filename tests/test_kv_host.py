@@ -156,6 +156,10 @@ def test_which_way_a_call_goes():
     assert parts(count=1, max_rows=1, max_len=100000, window=100) == 8 and parts(count=0) == 0  # three pages are not cut
     assert parts(count=1, max_rows=1, max_len=100000, window=300) == 48
     assert parts(count=64, max_rows=1, max_len=512) == 512 and parts(count=64, max_rows=1, max_len=513) == 2048  # 64 units a page
+    # tiles: no more parts than pay for their joining
+    assert parts(count=1, max_rows=512, max_len=512) == -2 and parts(count=1, max_rows=512, max_len=8000) == -5
+    assert parts(count=64, max_rows=512, max_len=8000) == -2 and parts(count=1, max_rows=64, max_len=4000) == -17
+    assert parts(count=1, max_rows=64, max_len=100000, window=64) == -4  # three pages
     assert parts(q_heads=30) == -1 and parts(window=-1) == -1
 
 
