@@ -48,10 +48,10 @@ __global__ __launch_bounds__(64 * kTileWaves, D <= 128 ? 2 : 1) void attn_tile_k
   bid /= a.b.count;
   const int part = bid % a.parts;
   int tile = a.tiles - 1 - bid / a.parts;
-  // Where the card holds the whole grid at once, every CU's second workgroup is
-  // the lighter the heavier its first.
+  // Where the card holds the whole grid at once, two workgroups a CU, its second
+  // is the lighter the heavier its first.
   const int per = a.c.heads * a.b.count * a.parts, firsts = (kCus + per - 1) / per;
-  if (a.tiles * per <= 2 * kCus && bid / a.parts >= firsts) tile = bid / a.parts - firsts;
+  if (D <= 128 && a.tiles * per <= 2 * kCus && bid / a.parts >= firsts) tile = bid / a.parts - firsts;
   const Span sp = span_of(a.b, s);
   const int total = sp.n * a.group;
   if (tile * ROWS >= total) return;
