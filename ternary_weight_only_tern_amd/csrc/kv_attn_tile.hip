@@ -60,7 +60,10 @@ __global__ __launch_bounds__(64 * kTileWaves, D <= 128 ? 2 : 1) void attn_tile_k
   if (part >= parts.count) return;
   const Range mine = part_of(all, parts, part);
 
-  const int r = tile * ROWS + wave * 32 + c32, j = r / a.group, h = r % a.group;
+  // Two workgroups on a CU have their first rows on different SIMDs: where a
+  // tile has 64 rows or fewer, each SIMD has one wavefront with rows.
+  const int block = (wave + blockIdx.x / kCus % 2 * 2) % kTileWaves;
+  const int r = tile * ROWS + block * 32 + c32, j = r / a.group, h = r % a.group;
   const bool there = r < total;
   const Sees sees = sees_of(a, sp, sp.from + j, there);
   // tokens that every row of the wavefront sees, and that any does
@@ -304,7 +307,7 @@ __global__ __launch_bounds__(64 * kTileWaves, D <= 128 ? 2 : 1) void attn_tile_k
         z[1] = next[1];
       }
     } else {
-      if (LEAD) multiply(ks);
+      if (LEAD && seen(p + 1)) multiply(ks);
 #pragma unroll
       for (int u = 0; u < 4 * PIECES; ++u) decode(u, keys, lv[cur ^ 1]);
       fetch();
@@ -333,13 +336,13 @@ __global__ __launch_bounds__(64 * kTileWaves, D <= 128 ? 2 : 1) void attn_tile_k
   }
   // A part's sums as the lanes have them, 1 KB a store.
   const size_t slot = part_slot(a, s, head, tile) + part;
-  kf4_t* const to = reinterpret_cast<kf4_t*>(a.part) + slot * (D / 8) * THREADS + threadIdx.x;
+  kf4_t* const to = reinterpret_cast<kf4_t*>(a.part) + slot * (D / 8) * THREADS + block * 64 + lane;
 #pragma unroll
   for (int i = 0; i < D / 8; ++i) {
     const kf4_t x = {o[i / 4][i % 4 * 4], o[i / 4][i % 4 * 4 + 1], o[i / 4][i % 4 * 4 + 2], o[i / 4][i % 4 * 4 + 3]};
     to[i * THREADS] = x * (row.unit / kLift);
   }
-  if (hq == 0) part_totals<D>(a)[slot * ROWS + wave * 32 + c32] = kw2_t{__float_as_uint(row.top), __float_as_uint(sum)};
+  if (hq == 0) part_totals<D>(a)[slot * ROWS + block * 32 + c32] = kw2_t{__float_as_uint(row.top), __float_as_uint(sum)};
 }
 
 // y from the sums of a tile's parts, in their order: a workgroup has 8 of the
