@@ -207,17 +207,29 @@ __global__ __launch_bounds__(64 * kTileWaves, D <= 128 ? 2 : 1) void attn_tile_k
     if (seen(p)) {
       const float vscale = __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(__float_as_int(vs0)));
       float by = ks0 * a.scale, best = -INFINITY;  // the scores are by z
-      const bool whole = id >= 0 && p * kPage >= low && p * kPage + kPage <= high;
+      // Minus infinity where a row does not see the token: one comparison a
+      // score, on the side where the page crosses a border.
       auto mask = [&]() {
-        if (whole) return;
+        const int first = p * kPage, side = first + 4 * hq;
+        const bool none = id < 0, below = none || first < low, above = first + kPage > high;
+        if (!below && !above) return;
+        if (!(by > 0.f)) {  // of no use beside infinities
 #pragma unroll
-        for (int b = 0; b < 2; ++b)
+          for (int x = 0; x < 32; ++x) z[x / 16][x % 16] *= by;
+          by = 1.0f;
+        }
+        if (below) {
+          const int from = none ? kPage : sees.low - side;
 #pragma unroll
-          for (int v = 0; v < 16; ++v) {
-            const int token = p * kPage + 32 * b + 8 * (v / 4) + 4 * hq + v % 4;
-            z[b][v] = id < 0 || token < sees.low || token >= sees.high ? -INFINITY : z[b][v] * by;
-          }
-        by = 1.0f;
+          for (int x = 0; x < 32; ++x)
+            if (x / 4 * 8 + x % 4 < from) z[x / 16][x % 16] = -INFINITY;
+        }
+        if (above) {
+          const int to = sees.high - side;
+#pragma unroll
+          for (int x = 0; x < 32; ++x)
+            if (x / 4 * 8 + x % 4 >= to) z[x / 16][x % 16] = -INFINITY;
+        }
       };
       if (LEAD) mask();
       kh8_t f[AHEAD];
