@@ -233,18 +233,24 @@ __device__ inline int dim_of(const Rotary& r, const Place& at, int e) {
   return i < r.rot / 2 ? (e < 4 ? i : i + r.rot / 2) : 2 * i + e / 4;
 }
 
-// cos and sin of the lane's four pairs at position pos.
+// The frequencies of the lane's four pairs (0 for those that do not turn), and
+// cos and sin of their angles at position pos.
+struct Freqs {
+  double f[4];
+};
 struct Angles {
   float c[4], s[4];
 };
-__device__ inline Angles angles_of(const Rotary& r, const Place& at, bool live, int pos) {
+__device__ inline Freqs freqs_of(const Rotary& r, const Place& at) {
+  Freqs q;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) q.f[e] = at.i0 + e < r.rot / 2 ? r.freq[at.i0 + e] : 0.0;
+  return q;
+}
+__device__ inline Angles angles_of(const Rotary& r, const Freqs& q, int pos) {
   Angles g;
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    g.c[e] = 1.f;
-    g.s[e] = 0.f;
-    if (live && at.i0 + e < r.rot / 2) angle_of((double)pos, r.freq[at.i0 + e], r.amp, g.c[e], g.s[e]);
-  }
+  for (int e = 0; e < 4; ++e) angle_of((double)pos, q.f[e], r.amp, g.c[e], g.s[e]);
   return g;
 }
 
@@ -292,14 +298,20 @@ __device__ inline Eight turn_eight(Eight v, const Eight& w, const Place& at, int
 #pragma unroll
     for (int e = 0; e < 8; ++e) y[e] = (inv * kv_half(w.h[e])) * y[e];
   }
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    if (at.i0 + e < r.rot / 2) {
-      float &p = r.inter ? y[2 * e] : y[e], &q = r.inter ? y[2 * e + 1] : y[4 + e];
-      const float a = p, b = q;
+  const int pairs = r.rot / 2 - at.i0;  // that turn
+  auto turn = [&](int e, float& p, float& q) {
+    const float a = p, b = q;
+    if (e < pairs) {
       p = __builtin_fmaf(a, g.c[e], -(b * g.s[e]));
       q = __builtin_fmaf(b, g.c[e], a * g.s[e]);
     }
+  };
+  if (r.inter) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) turn(e, y[2 * e], y[2 * e + 1]);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) turn(e, y[e], y[4 + e]);
   }
 #pragma unroll
   for (int e = 0; e < 8; ++e) v.h[e] = kv_bits(y[e]);
@@ -312,7 +324,7 @@ __device__ inline void turn_row(const uint16_t* x, uint16_t* out, int heads, int
   const int lane = threadIdx.x % lanes;
   const bool live = lane * 8 < dim;
   const Place at = place_of(r, lane);
-  const Angles g = angles_of(r, at, live, pos);
+  const Angles g = angles_of(r, freqs_of(r, at), pos);
   Eight w = {};
   if (live && r.norm) w = load_eight(r.norm, r, at);
   // the next heads are read while these are turned (out may be x: they are others)

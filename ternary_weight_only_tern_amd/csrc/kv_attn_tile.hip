@@ -6,12 +6,26 @@
 // them sees.  A page's codes are decoded once for the workgroup, into LDS as
 // FP16 operands of v_mfma_f32_32x32x16_f16 in the order in which lanes read
 // them (no bank conflicts), one page ahead, the page after that on its way
-// into registers meanwhile.  Scores come out transposed (a lane has one row's
-// scores of 32 tokens of the page, its partner 32 lanes on the others), so
-// the softmax needs one exchange, and the weights are the next product's
-// operand where they are.  Heavy tiles (the last of a causal prompt) start
-// first; the workgroups of a cache head are neighbours modulo the number of
-// heads, so that an XCD's L2 keeps few heads' pages.
+// into registers meanwhile.  Up to 128 dimensions a step multiplies the next page's
+// keys while it looks for this page's largest scores.  Scores come out
+// transposed (a lane has one row's scores of 32 tokens of the page, its partner
+// 32 lanes on the others), so the softmax needs one exchange, and the weights are
+// the next product's operand where they are.  Heavy tiles (the last of a causal
+// prompt) start first; the workgroups of a cache head are neighbours modulo the
+// number of heads, so that an XCD's L2 keeps few heads' pages.  Where tiles are
+// few, their contexts are cut into parts (parts_for in kv_api.cpp), whose sums
+// attn_join_tile_kernel adds.
+//
+// Bound by instructions: a wavefront's page of 128 dimensions is 32 matrix
+// instructions (1024 cycles) and about 1400 cycles of exponentials, maxima,
+// roundings and decoding, which overlap little: 2048 rows of 32 heads over 8
+// after 1000 tokens 89 us, 762 TFLOP/s; 8192 rows 585 us, 935 TFLOP/s (the
+// library's FP16 product of 8192^3: 1190).  Other orders of the tiles, other
+// priorities and four wavefronts a SIMD gained nothing or spilled.  Where tiles
+// are short, 3 to 5 us pass before a workgroup's first page: four dependent trips
+// to memory and code that no cache holds yet.  At 256 dimensions a CU has one
+// workgroup, and its operands from LDS take as long as its matrix instructions (4
+// prompts of 2048 rows, 8 heads, 120 us, 571 TFLOP/s).
 #include "kv_attn.h"
 
 namespace tern {

@@ -9,8 +9,16 @@
 // One workgroup has a (page, head) of the keys or of the values, so that a
 // scale has one writer.  A thread owns pieces of the page: of the
 // keys two words of four dimensions of a token, of the values 16 tokens of four
-// dimensions, which it transposes by byte permutations.  It alone reads, rounds
-// again and writes those bytes; nothing is shared but the largest value.
+// dimensions.  It alone reads, rounds
+// again and writes those bytes; nothing is shared but the largest value.  q's
+// rows are turned by further workgroups of the same launch (rope.hip's way).
+//
+// Bound by bytes and vector instructions: a prompt of 4096 tokens, 8 heads of
+// 128 with 32 of q, takes 24.4 us (4.8 TB/s read and written; the vector units
+// are busy for more than half of it: norms, FP64 angles of every head's keys,
+// codes).  Prefixes of 96000 tokens, 8 heads, are read back as FP32 in 123 us (4.6
+// TB/s), as FP16 in 80.  A token each of 48 sequences takes 5.8 us, a chain of
+// four trips to memory: lengths, page number, scale, the page's other codes.
 #include "kv.h"
 
 namespace tern {
@@ -26,19 +34,25 @@ __device__ inline float least_scale(float most) {
 // itself away from one: |2X 2^a - (2n+1) S 2^b|, with X of 11 bits and S of 8, is
 // 2^b at least, against (2n+1) S 2^b with 2n+1 < 256, or 2^(a+1), against 2X 2^a.
 // So with 18 bits left a tie is one again and nothing else becomes one.
+// The sum with 1.5 2^23 + 128 rounds to a whole number, whose low byte is it + 128;
+// nothing is past 127 steps of its page's scale.
 __device__ inline float steps_of(float s) { return s > 0.f ? 1.0f / s : 0.f; }
+constexpr float kToByte = 12583040.0f;
 __device__ inline uint32_t byte_of(float x, float inv) {
-  const float c = rintf(__uint_as_float((__float_as_uint(x * inv) + 0x20u) & ~0x3Fu));
-  return inv > 0.f ? (uint32_t)((int)__builtin_amdgcn_fmed3f(c, -127.f, 127.f) + 128) : 128u;
+  return __float_as_uint(__uint_as_float((__float_as_uint(x * inv) + 0x20u) & ~0x3Fu) + kToByte);
+}
+
+// The low bytes of four words.
+__device__ inline uint32_t pack4(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  return __builtin_amdgcn_perm(b, a, 0x0c0c0400u) | __builtin_amdgcn_perm(d, c, 0x04000c0cu);
 }
 
 // Four bytes rounded again to steps that are 1 / shrink times as large.
 __device__ inline uint32_t again4(uint32_t w, float shrink) {
-  uint32_t out = 0;
+  uint32_t b[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    out |= (uint32_t)((int)rintf((float)((int)((w >> (8 * i)) & 255u) - 128) * shrink) + 128) << (8 * i);
-  return out;
+  for (int i = 0; i < 4; ++i) b[i] = __float_as_uint(__builtin_fmaf((float)((w >> (8 * i)) & 255u) - 128.f, shrink, kToByte));
+  return pack4(b[0], b[1], b[2], b[3]);
 }
 
 // 4 x 4 bytes: out[j] has byte j of every in.
@@ -98,6 +112,7 @@ __device__ void write_keys(const WriteArgs& a, const Span& sp, int s, int page, 
       v[i] = load_eight(a.k + (sp.first + page * kPage + token - sp.from) * a.k_stride + head * D, a.rk, place);
   }
   if (a.rk.norm) weight = load_eight(a.rk.norm, a.rk, place);
+  const Freqs freqs = freqs_of(a.rk, place);
   const int id = page_of(a.b, a.c, s, page);
   if (id < 0) return;
   const size_t at = (size_t)id * a.c.heads + head;
@@ -107,7 +122,7 @@ __device__ void write_keys(const WriteArgs& a, const Span& sp, int s, int page, 
   for (int i = 0; i < kRounds; ++i) {
     const int token = i * kRound + first;
     if (i * kRound >= t1 || i * kRound + kRound <= t0) continue;  // the same for all: no token of this round
-    const Angles g = angles_of(a.rk, place, a.rk.on && token >= t0 && token < t1, page * kPage + token);
+    const Angles g = angles_of(a.rk, freqs, page * kPage + token);
     v[i] = turn_eight(v[i], weight, place, D, kLanes, a.rk, g);
 #pragma unroll
     for (int e = 0; e < 8; ++e) bits = max(bits, (uint32_t)v[i].h[e] & 0x7FFFu);
@@ -116,6 +131,9 @@ __device__ void write_keys(const WriteArgs& a, const Span& sp, int s, int page, 
   if (threadIdx.x == 0) a.c.ks[at] = g.s;
   uint8_t* const base = a.c.k + at * (kPage * D);
   const float inv = steps_of(g.s);
+  if (!(inv > 0.f))  // codes 0, whatever the values
+#pragma unroll
+    for (int i = 0; i < kRounds; ++i) v[i] = {};
   const bool words = !sided(a.rk) || a.rk.rot % 8 == 0;  // four dimensions are a word of the page
 #pragma unroll
   for (int i = 0; i < kRounds; ++i) {
@@ -129,14 +147,8 @@ __device__ void write_keys(const WriteArgs& a, const Span& sp, int s, int page, 
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
         uint32_t* const to = reinterpret_cast<uint32_t*>(byte_at(q ? place.b : place.a));
-        uint32_t w = 0;
-        if (live) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) w |= byte_of(kv_half(v[i].h[4 * q + e]), inv) << (8 * e);
-        } else {
-          w = again4(*to, g.shrink);
-        }
-        *to = w;
+        auto byte = [&](int e) { return byte_of(kv_half(v[i].h[4 * q + e]), inv); };
+        *to = live ? pack4(byte(0), byte(1), byte(2), byte(3)) : again4(*to, g.shrink);
       }
     } else {
 #pragma unroll
@@ -188,30 +200,28 @@ __device__ void write_values(const WriteArgs& a, const Span& sp, int s, int page
 #pragma unroll
       for (int q = 0; q < 4; ++q) o[e][q] = again4(o[e][q], g.shrink);
   const float inv = steps_of(g.s);
+  if (!(inv > 0.f))
+#pragma unroll
+    for (int j = 0; j < 16; ++j) y[j] = kh4_t{0, 0, 0, 0};
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
     if (t1 <= part * 16 + q * 4 || t0 >= part * 16 + q * 4 + 4) continue;
-    uint32_t in[4], out[4], mask = 0;
+    uint32_t mask = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int token = part * 16 + q * 4 + i;
-      in[i] = 0;
+    for (int i = 0; i < 4; ++i)
+      if (part * 16 + q * 4 + i >= t0 && part * 16 + q * 4 + i < t1) mask |= 255u << (8 * i);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) in[i] |= byte_of((float)y[q * 4 + i][e], inv) << (8 * e);
-      if (token >= t0 && token < t1) mask |= 255u << (8 * i);
+    for (int e = 0; e < 4; ++e) {
+      auto byte = [&](int i) { return byte_of((float)y[q * 4 + i][e], inv); };
+      o[e][q] = (o[e][q] & ~mask) | (pack4(byte(0), byte(1), byte(2), byte(3)) & mask);
     }
-    transpose4(in, out);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) o[e][q] = (o[e][q] & ~mask) | (out[e] & mask);
   }
 #pragma unroll
   for (int e = 0; e < 4; ++e) to[e] = o[e];
 }
 
-// Six wavefronts a SIMD (two registers fewer than five take): 24 prompts of 64
-// tokens, 32 heads over 8, 17.2 -> 14.7 us; seven or eight spill: 14.9, 15.3.
 template <int D>
-__global__ __launch_bounds__(256, 6) void kv_write_kernel(const WriteArgs a) {
+__global__ __launch_bounds__(256) void kv_write_kernel(const WriteArgs a) {
   int bid = blockIdx.x;
   if (bid >= a.kv_blocks) {  // wavefronts of rows of q
     constexpr int lanes = D / 8, per = 64 / lanes;
