@@ -586,7 +586,7 @@ typedef struct tern_kv_batch {
  * NaN among the rows makes the scale NaN: the page's tokens of that head read
  * as NaN until its first token is written again.  A sequence's tokens are
  * written in order from the first of a page on; a page that is written belongs to
- * one sequence.  q: NULL, or rows that are turned in the same launch,
+ * one sequence and stands in its table once.  q: NULL, or rows that are turned in the same launch,
  * q_out [rows][q_heads][dim], by q_rope at the same positions; q_out may equal
  * q. */
 tern_status tern_kv_write(const tern_kv *c, const tern_kv_batch *b, const uint16_t *k, int64_t k_stride,
@@ -607,7 +607,9 @@ tern_status tern_kv_read(const tern_kv *c, const tern_kv_batch *b, void *k, void
  * softmax's weights meet the codes of v in FP16 (11 bits each).  scale finite,
  * not negative.  ws: tern_kv_attention_workspace_bytes (0 for arguments that
  * are refused), 16-byte aligned, enough for every batch with no more
- * sequences and rows and no larger max_len too; calls that overlap in time must not share it. */
+ * sequences and rows and no larger max_len too; calls that overlap in time must
+ * not share it.  At most (TERN_E_UNSUPPORTED): 65535 query heads, a q_stride of
+ * 2^23, max_rows g of 2^30, count heads of 2^24, count heads max_pages of 2^31 - 1. */
 size_t tern_kv_attention_workspace_bytes(const tern_kv *c, const tern_kv_batch *b, int32_t q_heads);
 tern_status tern_kv_attention(const tern_kv *c, const tern_kv_batch *b, const uint16_t *q, int64_t q_stride,
                               int32_t q_heads, float scale, int32_t window, int32_t causal, uint16_t *y, void *ws,

@@ -21,7 +21,7 @@
 // roundings and decoding, which overlap little: 2048 rows of 32 heads over 8
 // after 1000 tokens 89 us, 762 TFLOP/s; 8192 rows 585 us, 935 TFLOP/s (the
 // library's FP16 product of 8192^3: 1190).  Other orders of the tiles, other
-// priorities and four wavefronts a SIMD gained nothing or spilled.  Where tiles
+// priorities and three wavefronts a SIMD (at 64 dimensions) gained nothing or spilled.  Where tiles
 // are short, 3 to 5 us pass before a workgroup's first page: four dependent trips
 // to memory and code that no cache holds yet.  At 256 dimensions a CU has one
 // workgroup, and its operands from LDS take as long as its matrix instructions (4
