@@ -534,7 +534,7 @@ tern_status tern_rope_frequencies(int32_t rot, double base, int32_t scaling, dou
 
 /* out = x [m][heads][dim] turned, row r by pos[r] (int32 [m], any value).
  * dim a multiple of 8, at most 512 (TERN_E_UNSUPPORTED).  out may equal x
- * (with the same stride). */
+ * (with the same stride); its rows do not overlap. */
 tern_status tern_rope(const uint16_t *x, int64_t x_stride, int32_t m, int32_t heads, int32_t dim, const int32_t *pos,
                       const tern_rotary *r, uint16_t *out, int64_t out_stride, void *stream);
 
@@ -588,7 +588,7 @@ typedef struct tern_kv_batch {
  * written in order from the first of a page on; a page that is written belongs to
  * one sequence and stands in its table once.  q: NULL, or rows that are turned in the same launch,
  * q_out [rows][q_heads][dim], by q_rope at the same positions; q_out may equal
- * q. */
+ * q (whose rows then follow each other). */
 tern_status tern_kv_write(const tern_kv *c, const tern_kv_batch *b, const uint16_t *k, int64_t k_stride,
                           const uint16_t *v, int64_t v_stride, const tern_rotary *rope, const uint16_t *q,
                           int64_t q_stride, int32_t q_heads, const tern_rotary *q_rope, uint16_t *q_out, void *stream);

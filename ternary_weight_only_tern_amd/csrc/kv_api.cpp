@@ -285,6 +285,10 @@ tern_status tern_rope(const uint16_t* x, int64_t x_stride, int32_t m, int32_t he
   if (!m || !heads || !dim) return TERN_OK;
   KV_TRY(check_rows(x, x_stride, "x"));
   KV_TRY(check_rows(out, out_stride, "out"));
+  if (m > 1 && out_stride < (int64_t)heads * dim)
+    return fail(TERN_E_INVAL, "rows of out overlap: %d heads of %d, %lld apart", heads, dim, (long long)out_stride);
+  if (m > 1 && out == x && out_stride != x_stride)
+    return fail(TERN_E_INVAL, "out is x with the row stride %lld, not %lld", (long long)out_stride, (long long)x_stride);
   KV_TRY(check_ptr(pos, "pos", 4));
   KV_TRY(check_rotary(r, dim, "rotary"));
   tern::RopeArgs a = {};
@@ -321,6 +325,8 @@ tern_status tern_kv_write(const tern_kv* c, const tern_kv_batch* b, const uint16
   if (q && q_heads) {
     KV_TRY(check_rows(q, q_stride, "q"));
     KV_TRY(check_ptr(q_out, "q_out", 16));
+    if (b->rows > 1 && q_out == q && q_stride != (int64_t)q_heads * c->dim)
+      return fail(TERN_E_INVAL, "q_out is q, whose rows are %lld apart", (long long)q_stride);
   }
   tern::WriteArgs a = {};
   a.c = cache_of(c);

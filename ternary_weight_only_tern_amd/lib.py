@@ -850,7 +850,8 @@ class KvBatch:
         self._descs = {}
 
     def _of(self, device, rows):
-        """The descriptor's address for so many rows."""
+        """The descriptor for so many rows (held by the caller while it is in
+        use: another thread's call may clear the ones kept here)."""
         if self.device != device:
             _refuse(f"the batch is on {self.device}, not {device}")
         d = self._descs.get(rows)
@@ -860,7 +861,7 @@ class KvBatch:
             d = tern_kv_batch(self.count, _count(rows), self.max_rows, self.max_len, self.pages.size(1),
                               _ptr(self.start), _ptr(self.len), _ptr(self.pages))
             self._descs[rows] = d
-        return ctypes.addressof(d)
+        return d
 
 
 def tern_kv_write(cache: KvCache, batch: KvBatch, k, v, rope=None, q=None, q_rope=None, q_out=None, stream=None):
@@ -891,9 +892,10 @@ def tern_kv_write(cache: KvCache, batch: KvBatch, k, v, rope=None, q=None, q_rop
         else:
             _tensor(q_out, "q_out", _halves, device, (m, q_heads, dim))
         q_at, q_out_at = q.data_ptr(), q_out.data_ptr()
-    check((_lib or load()).tern_kv_write(cache._at, batch._of(device, m), k.data_ptr(), k_stride, v.data_ptr(), v_stride,
-                               None if rope is None else rope._of(device, dim), q_at, q_stride, q_heads,
-                               None if q is None else q_rope._of(device, dim), q_out_at, _stream_of(device, stream)))
+    desc = batch._of(device, m)
+    check((_lib or load()).tern_kv_write(cache._at, ctypes.addressof(desc), k.data_ptr(), k_stride, v.data_ptr(), v_stride,
+                                         None if rope is None else rope._of(device, dim), q_at, q_stride, q_heads,
+                                         None if q is None else q_rope._of(device, dim), q_out_at, _stream_of(device, stream)))
     return q_out
 
 
@@ -914,7 +916,8 @@ def tern_kv_read(cache: KvCache, batch: KvBatch, rows=None, y_dtype=TERN_F16, k=
         _refuse(f"unknown output dtype {kind}")
     k = _fresh(shape, kind, device, stream) if k is None else _tensor(k, "k", (kind,), device, shape)
     v = _fresh(shape, kind, device, stream) if v is None else _tensor(v, "v", (kind,), device, shape)
-    check(load().tern_kv_read(cache._at, batch._of(device, rows), k.data_ptr(), v.data_ptr(),
+    desc = batch._of(device, rows)
+    check(load().tern_kv_read(cache._at, ctypes.addressof(desc), k.data_ptr(), v.data_ptr(),
                               TERN_F32 if kind == _torch.float32 else TERN_F16, _stream_of(device, stream)))
     return k, v
 
@@ -922,7 +925,8 @@ def tern_kv_read(cache: KvCache, batch: KvBatch, rows=None, y_dtype=TERN_F16, k=
 def tern_kv_attention_workspace(cache: KvCache, batch: KvBatch, rows: int, q_heads: int):
     """A workspace for tern_kv_attention with up to `rows` rows of q_heads
     heads and no longer sequences than the batch's max_len."""
-    return _scratch(_bytes(load().tern_kv_attention_workspace_bytes(cache._at, batch._of(cache.device, rows), _count(q_heads))),
+    desc = batch._of(cache.device, rows)
+    return _scratch(_bytes(load().tern_kv_attention_workspace_bytes(cache._at, ctypes.addressof(desc), _count(q_heads))),
                     cache.device, None)
 
 
@@ -941,7 +945,8 @@ def tern_kv_attention(cache: KvCache, batch: KvBatch, q, scale=None, window=0, c
         out = _fresh((m, q_heads, dim), _torch.float16, device, stream)
     else:
         _tensor(out, "out", _halves, device, q.shape)
-    at, lib = batch._of(device, m), _lib or load()
+    desc, lib = batch._of(device, m), _lib or load()
+    at = ctypes.addressof(desc)
     if ws is None:
         ws = _scratch(lib.tern_kv_attention_workspace_bytes(cache._at, at, q_heads), device, stream)
     else:

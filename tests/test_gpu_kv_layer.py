@@ -1,6 +1,7 @@
 """Positions, cache and attention as a program uses them: a decoder layer's
 attention block with packed projections, prompt and tokens; captured and
 replayed calls; streams; two calls at once; refusals of the binding."""
+import threading
 from types import SimpleNamespace
 
 import numpy as np
@@ -203,6 +204,28 @@ def test_streams():
         torch.cuda.synchronize()
         for y, t, k, v in got:
             assert torch.equal(y, want) and torch.equal(t, turned) and torch.equal(k, read[0]) and torch.equal(v, read[1])
+
+
+def test_threads_with_many_numbers_of_rows():
+    """More than the descriptors that a batch keeps, from two threads."""
+    rng = np.random.default_rng(15)
+    c = Case(rng, [3, 5], [90, 70], 2, 64, ragged=True)
+    cache, batch = c.cache(), c.on_device()
+    want = [t[:8].clone() for t in L.tern_kv_read(cache, batch, rows=8)]
+    torch.cuda.synchronize()
+    bad = []
+
+    def work(first):
+        for rows in range(first, first + 150):
+            if not all(torch.equal(a[:8], b) for a, b in zip(L.tern_kv_read(cache, batch, rows=rows), want)):
+                bad.append(rows)
+
+    threads = [threading.Thread(target=work, args=(first,)) for first in (8, 300)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad
 
 
 def test_smaller_workspace_is_refused_and_bad_arguments():

@@ -79,6 +79,7 @@ def test_write_refusals():
     assert f(q=0x4000, qr=rotary(), qo=None) == INVAL and f(q=0x4000, qr=rotary(), qh=-1) == INVAL
     assert f(q=0x4008, qr=rotary()) == ALIGN and f(q=0x4000, qr=rotary(), qo=0x3008) == ALIGN
     assert f(q=0x4000, qr=rotary(), qs=4100) == ALIGN
+    assert f(q=0x4000, qr=rotary(), qo=0x4000, qs=4104) == INVAL and b"q_out is q" in lib.tern_last_error()
     empty = batch(count=0, len=None, pages=None)
     assert f(b=empty, k=None, v=None) == L.TERN_OK and f(b=batch(max_rows=0), k=None, v=None) == L.TERN_OK
     assert f(b=batch(count=1 << 20, max_rows=500)) == UNSUPPORTED and b"too many workgroups" in lib.tern_last_error()
@@ -122,6 +123,8 @@ def test_rope_refusals():
     assert f(x=None) == INVAL and f(out=None) == INVAL and f(pos=None) == INVAL
     assert f(x=0x1002) == ALIGN and f(xs=636) == ALIGN and f(os=641) == ALIGN and f(pos=0x2002) == ALIGN
     assert f(r=rotary(rot=136)) == INVAL and f(r=rotary(rot=7)) == INVAL and f(r=rotary(rot=64, norm=0x4004)) == ALIGN
+    assert f(os=632) == INVAL and f(os=0) == INVAL  # rows of out that overlap
+    assert f(out=0x1000, os=648) == INVAL and f(out=0x1000, xs=1280) == INVAL  # in place at another stride
     for kw in (dict(m=0), dict(heads=0), dict(dim=0)):
         assert f(x=None, out=None, pos=None, **kw) == L.TERN_OK
 
