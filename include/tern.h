@@ -620,6 +620,12 @@ tern_status tern_kv_attention(const tern_kv *c, const tern_kv_batch *b, const ui
  * context on tiles (of causal rows); 0: nothing to do; -1: refused. */
 int32_t tern_kv_attention_parts(const tern_kv *c, const tern_kv_batch *b, int32_t q_heads, int32_t window);
 
+/* The rows of attention's tiles, for tests and measurements: 64 or 128 sets
+ * them for every call, 0 (the default) leaves the choice to the library, any
+ * other value only queries.  Returns the setting before.  Process-wide;
+ * workspace sizes do not depend on it.  Host-only. */
+int32_t tern_kv_tile_rows(int32_t rows);
+
 /* Measurement aid, not part of the product: a plain streaming read of
  * `bytes` bytes (a multiple of 16) of device memory at `buf` (16-byte
  * aligned), the attainable-bandwidth reference for the products above.

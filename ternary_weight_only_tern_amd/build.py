@@ -20,7 +20,8 @@ OBJDIR = os.path.join(PKG, "_build")
 
 SOURCES = ["tern_api.cpp", "pack.hip", "gemv.hip", "gemv_mfma.hip", "gemv_b3.hip", "gemm.hip", "quant.hip", "noalloc.hip",
            "rotate.hip", "q4_api.cpp", "q4_rows.hip", "q4_tile.hip", "q4_experts.hip", "route.hip",
-           "kv_api.cpp", "rope.hip", "kv_cache.hip", "kv_attn_rows.hip", "kv_attn_tile.hip"]
+           "kv_api.cpp", "rope.hip", "kv_cache.hip", "kv_attn_rows.hip", "kv_attn_mid.hip",
+           "kv_attn_tile.hip"]
 ARCH = os.environ.get("TERN_OFFLOAD_ARCH", "gfx950")
 
 

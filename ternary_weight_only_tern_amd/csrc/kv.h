@@ -101,7 +101,7 @@ struct AttnArgs {
 
 // Rows (of a sequence, times the query heads of one cache head) of one
 // workgroup: the kernel for few rows, by blocks of 16, and the tiles.
-constexpr int kAttnFew = 16, kAttnTile = 128;
+constexpr int kAttnFew = 16, kAttnMid = 64, kAttnTile = 128;
 
 hipError_t launch_rope(const RopeArgs& a, hipStream_t s);
 hipError_t launch_kv_write(WriteArgs a, int dim, hipStream_t s);
@@ -110,7 +110,9 @@ hipError_t launch_kv_read(const ReadArgs& a, int dim, hipStream_t s);
 hipError_t launch_attn_rows(const AttnArgs& a, int dim, int blocks, hipStream_t s);
 hipError_t launch_attn_tile(const AttnArgs& a, int dim, hipStream_t s);
 hipError_t launch_attn_join_rows(const AttnArgs& a, int dim, hipStream_t s);
-hipError_t launch_attn_join_tile(const AttnArgs& a, int dim, hipStream_t s);
+hipError_t launch_attn_mid(const AttnArgs& a, int dim, hipStream_t s);
+// rows: of a tile
+hipError_t launch_attn_join_tile(const AttnArgs& a, int dim, int rows, hipStream_t s);
 
 // Wavefronts that share a row's heads: one where there are rows enough to fill
 // the card, as many as have heads where there are few.

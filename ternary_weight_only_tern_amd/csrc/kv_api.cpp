@@ -4,6 +4,7 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -131,7 +132,7 @@ int items_of(const tern_kv_batch* b) { return (most_rows(b) + 2 * (tern::kPage -
 // How attention runs.
 struct AttnPlan {
   int blocks;  // of 16 rows in the kernel for few rows, 1 or 2; 0: tiles
-  int pieces, whole, parts, per, tiles;
+  int pieces, whole, parts, per, tiles, tile;
   bool join;
   size_t rows, info;  // of partial sums, and units whose pieces are noted
 };
@@ -159,26 +160,35 @@ int pages_of(const tern_kv_batch* b, int window, int rows) {
   return (int)((tokens + tern::kPage - 1) / tern::kPage);
 }
 
-// Parts for `groups` tiles that see `pages` pages at most, `mean` on average:
-// those that cost the least by a model of the time, in us, whose figures are
-// fitted to measurements.  A page takes a workgroup `step`, or 1.4 times that
-// where two share a CU (which they do not at 256 dimensions); tiles of
-// different lengths fill CUs unevenly.  Joining takes 2 and what the parts'
-// sums take to be written and read.  Uncut and cut, us: 64 tiles of 125 pages,
-// 4 / 8 / 12 parts 177 -> 58.9 / 50.1 / 56.7; 16 tiles of 63 pages, 8 / 16 / 32 parts
-// 98.0 -> 23.0 / 20.4 / 24.0; a prompt of 2048, 128 tiles, 3 / 4 / 6 / 8 parts 54.7 ->
-// 39.6 / 35.5 / 32.8 / 42.6; one of 512, 128 tiles, 2 / 3 parts 19.7 -> 21.0 / 23.9.
-int parts_for(long long groups, int pages, double mean, int dim) {
-  const double step = 0.4 + 0.01 * dim, share = dim > 128 ? 1.0 : 1.4;
-  const int slots = dim > 128 ? 256 : 512, alone = mean < pages - 1 ? 160 : 256;
+// Parts for `groups` tiles of `rows` rows that see `pages` pages at most, `mean` on
+// average, and their time, in us, by a model whose figures are fitted to
+// measurements of 48 shapes (its choices are 0.5 % slower than the best ones).  A
+// page takes a workgroup `step`, or `share` times that where a CU has `holds`
+// workgroups; tiles of different lengths fill CUs unevenly.  Joining takes 1.5 and
+// what the parts' sums take to be written and read.  Uncut and cut, us: 128-row
+// tiles, 64 of 125 pages, 4 / 8 / 12 parts 173 -> 56.5 / 48.5 / 53.0; 16 of 63 pages, 8 /
+// 16 / 32 parts 96.8 -> 22.8 / 20.6 / 24.1; a prompt of 2048, 128 tiles, 4 / 6 / 8 parts 53.6
+// -> 35.2 / 32.2 / 42.0.  Tiles of 64 and of 128 rows, us, each at its best number of
+// parts: prompts of 256, 512, 1024 and 4096 tokens 10.3 and 13.1, 15.8 and 19.5, 27.1
+// and 31.6, 89 and 65; 64 sequences of 40 rows 37.7 and 48.1; 512 rows after 7500
+// tokens 122 and 88; 8192 rows 850 and 570.
+struct Cost {
+  double step, share;
+  int holds;
+};
+constexpr Cost kMidCost[3] = {{0.8, 1.9, 4}, {1.25, 1.33, 2}, {2.1, 1.15, 1}};  // of 64, 128, 256 dimensions
+constexpr Cost kTileCost[3] = {{1.05, 1.4, 2}, {1.5, 1.37, 2}, {2.75, 1.0, 1}};
+int parts_for(long long groups, int pages, double mean, int dim, int rows, double& least) {
+  const Cost c = (rows == tern::kAttnMid ? kMidCost : kTileCost)[dim / 128];
+  const int slots = 256 * c.holds, alone = mean < pages - 1 ? 160 : 256;
   int best = 1;
-  double least = 1e30;
+  least = 1e30;
   for (int n = 1; n == 1 || (n <= pages && groups * n <= kTileSlots); n += 1 + n / 8) {
     const int per = (pages + n - 1) / n;
     const double all = groups * std::min<double>(n, mean / per);  // workgroups that have pages
-    double us = (all <= alone ? 1.0 : std::ceil(all / slots) * share) * per * step;
-    if (n == 1) us = std::max(std::min(us, groups * mean * step * share / slots), pages * step);  // long tiles first
-    if (n > 1) us += 2.0 + 1.6e-4 * groups * n * dim;
+    double us = std::max(1.0, all <= alone ? 1.0 : std::ceil(all / slots) * c.share) * per * c.step;
+    if (n == 1) us = std::max(std::min(us, groups * mean * c.step * c.share / slots), pages * c.step);  // long tiles first
+    if (n > 1) us += 1.5 + 1.3e-6 * groups * n * dim * rows;
     if (us < least) {
       least = us;
       best = n;
@@ -191,6 +201,8 @@ int parts_for(long long groups, int pages, double mean, int dim) {
 // 8 x 8 cache heads after 8000 tokens, 16 rows each 37 / -, 20 rows at 256
 // dimensions 80 / 104, 40 rows (four blocks, not kept) 73 / 56, 64 rows 75 / 56.
 constexpr int kFewRows = 32;
+
+std::atomic<int> g_tile_rows{0};  // of every tile, 0: by the rule
 
 AttnPlan plan_of(const tern_kv* c, const tern_kv_batch* b, int group, int window, bool causal) {
   AttnPlan p = {};
@@ -206,16 +218,24 @@ AttnPlan plan_of(const tern_kv* c, const tern_kv_batch* b, int group, int window
     p.info = p.join ? units : 0;
     return p;
   }
-  p.tiles = (int)((rows + tern::kAttnTile - 1) / tern::kAttnTile);
-  const long long groups = p.tiles * units;
-  const int tokens = std::min(most_rows(b), (tern::kAttnTile - 1) / group + 2);  // of a tile
-  const int pages = std::max(1, pages_of(b, window, tokens));
-  const double fewer = causal && !window ? 0.5 * (most_rows(b) - tokens) / tern::kPage : 0.0;
-  const int n = parts_for(groups, pages, std::max(1.0, pages - fewer), c->dim);
-  p.per = (pages + n - 1) / n;
-  p.parts = (pages + p.per - 1) / p.per;
+  double least = 1e30;
+  const int only = g_tile_rows;
+  for (const int tile : {tern::kAttnMid, tern::kAttnTile}) {
+    if (only && tile != only) continue;
+    const int tiles = (int)((rows + tile - 1) / tile), tokens = std::min(most_rows(b), (tile - 1) / group + 2);
+    const int pages = std::max(1, pages_of(b, window, tokens));
+    const double fewer = causal && !window ? 0.5 * (most_rows(b) - tokens) / tern::kPage : 0.0;
+    double us = 0.0;
+    const int n = parts_for(tiles * units, pages, std::max(1.0, pages - fewer), c->dim, tile, us);
+    if (us >= least) continue;
+    least = us;
+    p.tile = tile;
+    p.tiles = tiles;
+    p.per = (pages + n - 1) / n;
+    p.parts = (pages + p.per - 1) / p.per;
+  }
   p.join = p.parts > 1;
-  p.rows = p.join ? (size_t)groups * p.parts * tern::kAttnTile : 0;
+  p.rows = p.join ? (size_t)p.tiles * units * p.parts * p.tile : 0;
   return p;
 }
 
@@ -227,7 +247,7 @@ size_t attn_need(const AttnPlan& p, const tern_kv* c) { return p.rows * (c->dim 
 size_t attn_need_upto(const tern_kv* c, const tern_kv_batch* b, int group) {
   const double rows = (double)b->rows * group, pages = pages_of(b, 0, 0);
   const double few = 2.0 * std::min<double>(kPieces, (double)b->count * c->heads * pages) * std::min<double>(rows, kFewRows);
-  const double groups = (double)b->count * c->heads * std::ceil(rows / tern::kAttnTile);
+  const double groups = (double)b->count * c->heads * std::ceil(rows / tern::kAttnMid);
   const double tiles = rows <= kFewRows ? 0.0 : std::min<double>(groups * pages, kTileSlots) * tern::kAttnTile;
   return (size_t)(std::max(few, tiles) * (c->dim + 2) * 4) + (size_t)b->count * c->heads * 8;
 }
@@ -382,6 +402,11 @@ int32_t tern_kv_attention_parts(const tern_kv* c, const tern_kv_batch* b, int32_
   return p.blocks ? p.pieces : -1 - p.parts;
 }
 
+int32_t tern_kv_tile_rows(int32_t rows) {
+  if (rows == 0 || rows == tern::kAttnMid || rows == tern::kAttnTile) return g_tile_rows.exchange(rows);
+  return g_tile_rows;
+}
+
 tern_status tern_kv_attention(const tern_kv* c, const tern_kv_batch* b, const uint16_t* q, int64_t q_stride,
                               int32_t q_heads, float scale, int32_t window, int32_t causal, uint16_t* y, void* ws,
                               size_t ws_bytes, void* stream) {
@@ -423,8 +448,8 @@ tern_status tern_kv_attention(const tern_kv* c, const tern_kv_batch* b, const ui
   if (p.blocks)
     KV_HIP(tern::launch_attn_rows(a, c->dim, p.blocks, s));
   else
-    KV_HIP(tern::launch_attn_tile(a, c->dim, s));
-  if (p.join) KV_HIP(p.blocks ? tern::launch_attn_join_rows(a, c->dim, s) : tern::launch_attn_join_tile(a, c->dim, s));
+    KV_HIP(p.tile == tern::kAttnMid ? tern::launch_attn_mid(a, c->dim, s) : tern::launch_attn_tile(a, c->dim, s));
+  if (p.join) KV_HIP(p.blocks ? tern::launch_attn_join_rows(a, c->dim, s) : tern::launch_attn_join_tile(a, c->dim, p.tile, s));
   return TERN_OK;
 }
 

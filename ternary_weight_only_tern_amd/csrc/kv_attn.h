@@ -36,6 +36,38 @@ __device__ inline Range part_of(const Range& r, const Parts& p, int part) {
   return {begin, min(begin + p.per, r.end)};
 }
 
+// A workgroup's tile, in the order in which they start: heavy tiles (the last
+// of a causal prompt) first, the cache heads neighbours.  `pairs`: where the card
+// holds the whole grid at once, two workgroups a CU, its second is the lighter
+// the heavier its first.
+constexpr int kCus = 256;
+struct Work {
+  int s, head, part, tile;
+};
+__device__ inline Work work_of(const AttnArgs& a, bool pairs) {
+  Work w;
+  int bid = blockIdx.x;
+  w.head = bid % a.c.heads;
+  bid /= a.c.heads;
+  w.s = bid % a.b.count;
+  bid /= a.b.count;
+  w.part = bid % a.parts;
+  w.tile = a.tiles - 1 - bid / a.parts;
+  const int per = a.c.heads * a.b.count * a.parts, firsts = (kCus + per - 1) / per;
+  if (pairs && a.tiles * per <= 2 * kCus && bid / a.parts >= firsts) w.tile = bid / a.parts - firsts;
+  return w;
+}
+
+// A tile's first part among all parts' sums, and the references and sums of
+// weights behind those, for tiles of R rows.
+__device__ inline size_t part_slot(const AttnArgs& a, int s, int head, int tile) {
+  return (((size_t)tile * a.b.count + s) * a.c.heads + head) * a.parts;
+}
+template <int D, int R>
+__device__ inline kw2_t* part_totals(const AttnArgs& a) {
+  return reinterpret_cast<kw2_t*>(a.part + (size_t)a.tiles * a.b.count * a.c.heads * a.parts * R * D);
+}
+
 // What the rows first .. last (token * group + query head) of a sequence see.
 __device__ inline Range range_of_rows(const AttnArgs& a, const Span& sp, int first, int last) {
   return range_of(a, sp, max(sp.from + first / a.group, 0), sp.from + last / a.group);
@@ -91,6 +123,18 @@ __device__ inline float step_row(Row& r, float best, float scale, float& lift, f
   back = __builtin_amdgcn_rcpf(ratio);
   lift = __builtin_amdgcn_logf(ratio);
   return factor;
+}
+
+// The larger of a lane's value and its partner's, 32 or 16 lanes on, by swaps
+// between registers: a shuffle's way through the LDS queues behind the operands'
+// reads (128 pages of a 64-row tile 175 -> 169 us).
+__device__ inline float max_of_32(float v) {
+  const auto p = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(p[0]), __uint_as_float(p[1]));
+}
+__device__ inline float max_of_16(float v) {
+  const auto p = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(p[0]), __uint_as_float(p[1]));
 }
 
 // Four values of a row of y (0 where the row has seen nothing).

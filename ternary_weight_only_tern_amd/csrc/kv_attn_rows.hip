@@ -280,8 +280,7 @@ __global__ __launch_bounds__(64, NT * D <= 128 ? 2 : 1) void attn_rows_kernel(co
       }
 #pragma unroll
       for (int x = 0; x < 16; ++x) best = fmaxf(best, z[n][x / 4][x % 4]);
-      best = fmaxf(best, __shfl_xor(best, 16));
-      best = fmaxf(best, __shfl_xor(best, 32));
+      best = max_of_32(max_of_16(best));
       float lift, back;
       const float factor = step_row(row[n], best, vs == 0.f ? 1.f : vs, lift, back);
       const float top = top_of(row[n]);

@@ -31,17 +31,7 @@
 namespace tern {
 namespace {
 
-constexpr int kTileWaves = 4, kCus = 256;
-
-// A tile's first part among all parts' sums, and the references and sums of
-// weights behind them.
-__device__ inline size_t part_slot(const AttnArgs& a, int s, int head, int tile) {
-  return (((size_t)tile * a.b.count + s) * a.c.heads + head) * a.parts;
-}
-template <int D>
-__device__ inline kw2_t* part_totals(const AttnArgs& a) {
-  return reinterpret_cast<kw2_t*>(a.part + (size_t)a.tiles * a.b.count * a.c.heads * a.parts * kAttnTile * D);
-}
+constexpr int kTileWaves = 4;
 
 template <int D>
 __global__ __launch_bounds__(64 * kTileWaves, D <= 128 ? 2 : 1) void attn_tile_kernel(const AttnArgs a) {
@@ -55,17 +45,8 @@ __global__ __launch_bounds__(64 * kTileWaves, D <= 128 ? 2 : 1) void attn_tile_k
   __shared__ kw4_t lk[2][kPage * D / 8], lv[2][kPage * D / 8];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c32 = lane & 31, hq = lane >> 5;
-  int bid = blockIdx.x;
-  const int head = bid % a.c.heads;
-  bid /= a.c.heads;
-  const int s = bid % a.b.count;
-  bid /= a.b.count;
-  const int part = bid % a.parts;
-  int tile = a.tiles - 1 - bid / a.parts;
-  // Where the card holds the whole grid at once, two workgroups a CU, its second
-  // is the lighter the heavier its first.
-  const int per = a.c.heads * a.b.count * a.parts, firsts = (kCus + per - 1) / per;
-  if (D <= 128 && a.tiles * per <= 2 * kCus && bid / a.parts >= firsts) tile = bid / a.parts - firsts;
+  const Work work = work_of(a, D <= 128);
+  const int s = work.s, head = work.head, part = work.part, tile = work.tile;
   const Span sp = span_of(a.b, s);
   const int total = sp.n * a.group;
   if (tile * ROWS >= total) return;
@@ -252,7 +233,6 @@ __global__ __launch_bounds__(64 * kTileWaves, D <= 128 ? 2 : 1) void attn_tile_k
       // Behind the last page the next scores are of what lies there, and not used.
       const kf16_t zero = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
       kf16_t next[2];
-      float other = 0.f;
       auto largest = [&](int x, int n) {
 #pragma unroll
         for (int y = x; y < x + n; ++y) best = fmaxf(best, z[y / 16][y % 16]);
@@ -264,7 +244,6 @@ __global__ __launch_bounds__(64 * kTileWaves, D <= 128 ? 2 : 1) void attn_tile_k
         f[i % AHEAD] = operand(i + AHEAD, ks, vs);
         if (i < MK / 2) {
           if (LEAD) largest(i * (64 / MK), 64 / MK);
-          if (LEAD && i == MK / 2 - 1) other = __shfl_xor(best, 32);
         } else {
           decode(i - MK / 2, keys, lv[cur ^ 1]);
         }
@@ -276,9 +255,8 @@ __global__ __launch_bounds__(64 * kTileWaves, D <= 128 ? 2 : 1) void attn_tile_k
         z[1] = next[1];
         mask();
         largest(0, 32);
-        other = __shfl_xor(best, 32);
       }
-      best = fmaxf(best, other) * by;
+      best = max_of_32(best) * by;
       float lift, back;
       const float factor = step_row(row, best, vscale == 0.f ? 1.f : vscale, lift, back);
       float shift = lift - top_of(row);
@@ -368,30 +346,32 @@ __global__ __launch_bounds__(64 * kTileWaves, D <= 128 ? 2 : 1) void attn_tile_k
     const kf4_t x = {o[i / 4][i % 4 * 4], o[i / 4][i % 4 * 4 + 1], o[i / 4][i % 4 * 4 + 2], o[i / 4][i % 4 * 4 + 3]};
     to[i * THREADS] = x * (row.unit / kLift);
   }
-  if (hq == 0) part_totals<D>(a)[slot * ROWS + block * 32 + c32] = kw2_t{__float_as_uint(row.top), __float_as_uint(sum)};
+  if (hq == 0) part_totals<D, ROWS>(a)[slot * ROWS + block * 32 + c32] = kw2_t{__float_as_uint(row.top), __float_as_uint(sum)};
 }
 
-// y from the sums of a tile's parts, in their order: a workgroup has 8 of the
-// dimensions, its threads what the tile's own threads left.
-template <int D>
+// y from the sums of a tile's parts, in their order: a workgroup has one of the
+// fours of dimensions that a thread holds, its threads what the tile's own
+// threads left (32 rows a wavefront and 4 of 8 dimensions a lane, or 16 rows and
+// 4 of 16).
+template <int D, int ROWS>
 __global__ __launch_bounds__(64 * kTileWaves) void attn_join_tile_kernel(const AttnArgs a) {
-  constexpr int THREADS = 64 * kTileWaves, ROWS = 32 * kTileWaves;
+  constexpr int THREADS = 64 * kTileWaves, R = ROWS / kTileWaves, L = 64 / R * 4;  // rows a wavefront, dimensions of a store
   const int head = blockIdx.x % a.c.heads, s = blockIdx.x / a.c.heads % a.b.count, tile = blockIdx.x / a.c.heads / a.b.count;
   const Span sp = span_of(a.b, s);
   const int total = sp.n * a.group;
   if (tile * ROWS >= total) return;
   const int count = parts_of(a, range_of_rows(a, sp, tile * ROWS, min(tile * ROWS + ROWS, total) - 1)).count;
-  const int lane = threadIdx.x & 63, in = threadIdx.x / 64 * 32 + lane % 32, r = tile * ROWS + in;
+  const int lane = threadIdx.x & 63, in = threadIdx.x / 64 * R + lane % R, r = tile * ROWS + in;
   if (count == 1 || r >= total) return;
   const size_t slot = part_slot(a, s, head, tile);
-  const kf4_t* const sums = reinterpret_cast<const kf4_t*>(a.part) + (slot * (D / 8) + blockIdx.y) * THREADS + threadIdx.x;
-  const kw2_t* const totals = part_totals<D>(a) + slot * ROWS + in;
+  const kf4_t* const sums = reinterpret_cast<const kf4_t*>(a.part) + (slot * (D / L) + blockIdx.y) * THREADS + threadIdx.x;
+  const kw2_t* const totals = part_totals<D, ROWS>(a) + slot * ROWS + in;
   kf4_t v = {0.f, 0.f, 0.f, 0.f};
   float sum = 0.f, top = -INFINITY;
 #pragma unroll 4
   for (int i = 0; i < count; ++i) {
     const kw2_t t = totals[(size_t)i * ROWS];
-    const kf4_t x = sums[(size_t)i * (D / 8) * THREADS];
+    const kf4_t x = sums[(size_t)i * (D / L) * THREADS];
     const float own = __uint_as_float(t.x), most = fmaxf(top, own);
     const float keep = top == most ? 1.f : __builtin_amdgcn_exp2f(top - most);
     const float f = own == most ? 1.f : __builtin_amdgcn_exp2f(own - most);
@@ -400,7 +380,7 @@ __global__ __launch_bounds__(64 * kTileWaves) void attn_join_tile_kernel(const A
     top = most;
   }
   const size_t out = ((size_t)(sp.first + r / a.group) * a.q_heads + head * a.group + r % a.group) * D;
-  finish_row(a, out + 8 * blockIdx.y + lane / 32 * 4, v, sum);
+  finish_row(a, out + L * blockIdx.y + lane / R * 4, v, sum);
 }
 
 template <int D>
@@ -409,10 +389,15 @@ hipError_t tile(const AttnArgs& a, long long grid, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <int D>
+template <int D, int ROWS>
 hipError_t join(const AttnArgs& a, hipStream_t s) {
-  hipLaunchKernelGGL((attn_join_tile_kernel<D>), dim3((unsigned)(a.b.count * a.c.heads * a.tiles), D / 8), dim3(64 * kTileWaves), 0, s, a);
+  const dim3 grid((unsigned)(a.b.count * a.c.heads * a.tiles), D * ROWS / (64 * kTileWaves * 4));
+  hipLaunchKernelGGL((attn_join_tile_kernel<D, ROWS>), grid, dim3(64 * kTileWaves), 0, s, a);
   return hipGetLastError();
+}
+template <int D>
+hipError_t join(const AttnArgs& a, int rows, hipStream_t s) {
+  return rows == kAttnTile ? join<D, kAttnTile>(a, s) : join<D, kAttnMid>(a, s);
 }
 
 }  // namespace
@@ -424,9 +409,9 @@ hipError_t launch_attn_tile(const AttnArgs& a, int dim, hipStream_t s) {
   return dim == 128 ? tile<128>(a, grid, s) : tile<256>(a, grid, s);
 }
 
-hipError_t launch_attn_join_tile(const AttnArgs& a, int dim, hipStream_t s) {
-  if (dim == 64) return join<64>(a, s);
-  return dim == 128 ? join<128>(a, s) : join<256>(a, s);
+hipError_t launch_attn_join_tile(const AttnArgs& a, int dim, int rows, hipStream_t s) {
+  if (dim == 64) return join<64>(a, rows, s);
+  return dim == 128 ? join<128>(a, rows, s) : join<256>(a, rows, s);
 }
 
 }  // namespace tern

@@ -44,7 +44,7 @@ SYMBOLS = ["tern_row_stride", "tern_check", "tern_packed_sizes", "tern_workspace
            "tern_bits", "tern_quantize", "tern_rotate", "tern_rotate_batched", "tern_q4_check", "tern_q4_pack", "tern_q4_unpack", "tern_q4_workspace_bytes", "tern_q4_gemm",
            "tern_route", "tern_q4_experts_workspace_bytes", "tern_q4_experts", "tern_q4_tile_rows", "tern_q4_experts_tile_rows",
            "tern_rope_frequencies", "tern_rope", "tern_kv_check", "tern_kv_write", "tern_kv_read",
-           "tern_kv_attention_workspace_bytes", "tern_kv_attention", "tern_kv_attention_parts",
+           "tern_kv_attention_workspace_bytes", "tern_kv_attention", "tern_kv_attention_parts", "tern_kv_tile_rows",
            "tern_read_probe", "tern_status_str", "tern_last_error"]
 
 
@@ -150,6 +150,7 @@ def load() -> ctypes.CDLL:
         "tern_kv_attention": (c_int32, [c_void_p, c_void_p, c_void_p, c_int64, c_int32, c_float, c_int32, c_int32,
                                         c_void_p, c_void_p, c_size_t, c_void_p]),
         "tern_kv_attention_parts": (c_int32, [c_void_p, c_void_p, c_int32, c_int32]),
+        "tern_kv_tile_rows": (c_int32, [c_int32]),
         "tern_read_probe": (c_int32, [c_void_p, c_size_t, c_void_p, c_void_p]),
         "tern_status_str": (ctypes.c_char_p, [c_int32]),
         "tern_last_error": (ctypes.c_char_p, []),
@@ -955,6 +956,12 @@ def tern_kv_attention(cache: KvCache, batch: KvBatch, q, scale=None, window=0, c
                                 _count(window), 1 if causal else 0, out.data_ptr(), ws.data_ptr(), ws.nbytes,
                                 _stream_of(device, stream)))
     return out
+
+
+def tern_kv_tile_rows(rows: int = -1) -> int:
+    """The rows of attention's tiles: 64 or 128 sets them, 0 restores the rule,
+    -1 queries; returns the setting before."""
+    return load().tern_kv_tile_rows(rows)
 
 
 def tern_read_probe(buf, sink, stream=None) -> None:

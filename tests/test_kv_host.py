@@ -162,8 +162,23 @@ def test_which_way_a_call_goes():
     # tiles: no more parts than pay for their joining
     assert parts(count=1, max_rows=512, max_len=512) == -2 and parts(count=1, max_rows=512, max_len=8000) == -5
     assert parts(count=64, max_rows=512, max_len=8000) == -2 and parts(count=1, max_rows=64, max_len=4000) == -17
-    assert parts(count=1, max_rows=64, max_len=100000, window=64) == -4  # three pages
+    assert parts(count=1, max_rows=64, max_len=100000, window=64) == -2  # three pages
     assert parts(q_heads=30) == -1 and parts(window=-1) == -1
+
+
+def test_rows_of_tiles():
+    lib, c = L.load(), cache()
+    parts = lambda **kw: lib.tern_kv_attention_parts(at(c), at(batch(**kw)), 32, 0)
+    big = batch(count=1, max_rows=512, max_len=8000)
+    size = lib.tern_kv_attention_workspace_bytes(at(c), at(big), 32)
+    assert L.tern_kv_tile_rows() == 0 and parts(count=1, max_rows=64, max_len=4000) == -17
+    try:
+        assert L.tern_kv_tile_rows(64) == 0 and L.tern_kv_tile_rows(96) == 64
+        assert parts(count=1, max_rows=512, max_len=8000) == -2
+        assert lib.tern_kv_attention_workspace_bytes(at(c), at(big), 32) == size
+        assert L.tern_kv_tile_rows(128) == 64 and parts(count=1, max_rows=512, max_len=8000) == -5
+    finally:
+        assert L.tern_kv_tile_rows(0) in (64, 128)
 
 
 def test_frequencies():
