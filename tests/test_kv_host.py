@@ -174,7 +174,7 @@ def test_rows_of_tiles():
     assert L.tern_kv_tile_rows() == 0 and parts(count=1, max_rows=64, max_len=4000) == -17
     try:
         assert L.tern_kv_tile_rows(64) == 0 and L.tern_kv_tile_rows(96) == 64
-        assert parts(count=1, max_rows=512, max_len=8000) == -2
+        assert parts(count=1, max_rows=512, max_len=8000) == -3
         assert lib.tern_kv_attention_workspace_bytes(at(c), at(big), 32) == size
         assert L.tern_kv_tile_rows(128) == 64 and parts(count=1, max_rows=512, max_len=8000) == -5
     finally:
