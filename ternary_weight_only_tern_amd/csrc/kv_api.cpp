@@ -197,18 +197,22 @@ int parts_for(long long groups, int pages, double mean, int dim, int rows, doubl
   return best;
 }
 
-// Rows up to which a unit goes to the kernel for few rows.  us, few rows / tiles:
-// 8 x 8 cache heads after 8000 tokens, 16 rows each 37 / -, 20 rows at 256
-// dimensions 80 / 104, 40 rows (four blocks, not kept) 73 / 56, 64 rows 75 / 56.
-constexpr int kFewRows = 32;
+// Rows up to which a unit goes to the kernel for few rows; above one block of 16
+// only where there are more pages than kFewPages, which it reads faster.  us, few
+// rows / tiles: 20 rows of 32 heads of 256 dimensions after 3000 tokens (1500 pages) 36
+// / 25, of 64 after 8000 (8000 pages) 78 / 87; 20 ragged rows of 32 heads after up to 120000
+// (60000 pages) 115 / 170; 32 of 8 after 4000 (500) 16.7 / 11.6, of 32 after 8000 (4000) 27.9 /
+// 26.4, of 2048 after 500 (16000) 62 / 78; 64 rows of 64 after 8000, four blocks, not kept, 75 /
+// 48.
+constexpr int kFewRows = 32, kFewPages = 4096;
 
 std::atomic<int> g_tile_rows{0};  // of every tile, 0: by the rule
 
 AttnPlan plan_of(const tern_kv* c, const tern_kv_batch* b, int group, int window, bool causal) {
   AttnPlan p = {};
   const long long rows = (long long)most_rows(b) * group, units = (long long)b->count * c->heads;
-  if (rows <= kFewRows) {
-    const int pages = pages_of(b, window, most_rows(b));
+  const int pages = pages_of(b, window, most_rows(b));
+  if (rows <= tern::kAttnFew || (rows <= kFewRows && units * pages > kFewPages)) {
     p.blocks = rows <= 16 ? 1 : 2;
     p.whole = pages <= kWholePages || units >= (long long)kWholeUnits * pages;
     p.pieces = (int)(p.whole ? std::min<long long>(units, 1ll << 30) : std::min<long long>(p.blocks * c->dim > 128 ? kPieces / 2 : kPieces, units * pages));
@@ -248,7 +252,7 @@ size_t attn_need_upto(const tern_kv* c, const tern_kv_batch* b, int group) {
   const double rows = (double)b->rows * group, pages = pages_of(b, 0, 0);
   const double few = 2.0 * std::min<double>(kPieces, (double)b->count * c->heads * pages) * std::min<double>(rows, kFewRows);
   const double groups = (double)b->count * c->heads * std::ceil(rows / tern::kAttnMid);
-  const double tiles = rows <= kFewRows ? 0.0 : std::min<double>(groups * pages, kTileSlots) * tern::kAttnTile;
+  const double tiles = rows <= tern::kAttnFew ? 0.0 : std::min<double>(groups * pages, kTileSlots) * tern::kAttnTile;
   return (size_t)(std::max(few, tiles) * (c->dim + 2) * 4) + (size_t)b->count * c->heads * 8;
 }
 

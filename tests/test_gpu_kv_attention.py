@@ -207,6 +207,24 @@ def test_more_rows_announced_than_there_are(rows, most):
     run(c, 4, rng)
 
 
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("rows,lens,q_heads", [([17], [500], 1), ([5, 2, 4], [300, 2, 68], 4), ([8, 8], [700, 7], 4), ([1, 1], [900, 65], 32)])
+def test_two_blocks_of_rows(rows, lens, q_heads, dim):
+    """17 to 32 rows of a cache head, with pages enough (by max_len) for the
+    kernel for few rows."""
+    rng = np.random.default_rng(46)
+    c = Case(rng, rows, lens, 1, dim)
+    for max_len in (None, 10 ** 6):
+        run(c, q_heads, rng, max_len=max_len, note=f"max_len {max_len}")
+
+
+@pytest.mark.parametrize("window", [0, 40])
+def test_two_blocks_of_rows_of_many_sequences(window):
+    rng = np.random.default_rng(49)
+    lens = [int(n) for n in rng.integers(5, 193, 180)]
+    run(Case(rng, [5] * 180, lens, 8, 64), 32, rng, window=window)
+
+
 @pytest.mark.parametrize("dim,rows", [(64, 1), (128, 3)])
 def test_many_short_sequences(dim, rows):
     """More units than 64 for every page: a wavefront each; cut by a max_len

@@ -155,7 +155,8 @@ def test_which_way_a_call_goes():
     assert parts(count=1, max_rows=1, max_len=100) == 8  # whole units
     assert parts(count=4, max_rows=5, max_len=120000) == 1024  # two blocks of rows
     assert parts(count=1, max_rows=9, max_len=5000) < -2 and parts(count=1, max_rows=2048, max_len=4000) == -2
-    assert parts(count=1, max_rows=8, max_len=5000, c=cache(dim=256)) == 632 and parts(count=1, max_rows=9, max_len=5000, c=cache(dim=256)) < -2
+    assert parts(count=1, max_rows=4, max_len=5000, c=cache(dim=256)) == 632 and parts(count=1, max_rows=8, max_len=5000, c=cache(dim=256)) < -2
+    assert parts(count=8, max_rows=8, max_len=4097) == 1024 and parts(count=8, max_rows=8, max_len=4096) < -2  # 4160, 4096 pages
     assert parts(count=1, max_rows=1, max_len=100000, window=100) == 8 and parts(count=0) == 0  # three pages are not cut
     assert parts(count=1, max_rows=1, max_len=100000, window=300) == 48
     assert parts(count=64, max_rows=1, max_len=512) == 512 and parts(count=64, max_rows=1, max_len=513) == 2048  # 64 units a page
