@@ -5,18 +5,19 @@
 // Each of four wavefronts has 16 rows, the columns of v_mfma_f32_16x16x32_f16,
 // and walks the pages that any of the tile's rows sees.  A page's codes are in the
 // order of these instructions' operands already (kv.h): 16 bytes become two
-// operands, 1 KB a wavefront's store.  The next page is decoded behind this page's
-// scores, the page after that is on its way into registers meanwhile, and the first
-// of the values' operands arrive while the weights are found.
+// operands, 1 KB a wavefront's store.  A step multiplies the next page's keys with
+// the queries, decodes the keys after those and the next values, asks for the
+// codes behind them, and turns this page's scores into weights and sums.
 //
-// Bound by the chain of a wavefront's step, about 3100 cycles at 128 dimensions
+// Bound by the chain of a wavefront's step, about 3000 cycles at 128 dimensions
 // (scores 740, most of it the LDS, decoding and requests 970, softmax 850, sums
 // 330), which a second workgroup on the CU hides in part: every wavefront reads
 // all operands for 16 rows, so that long prompts are better off with 32
 // (kv_attn_tile.hip), and few rows, short prompts and small dimensions here.  A
-// prompt of 512 tokens, 32 heads over 8, 15.8 us (128-row tiles 19.5); 64
-// sequences of 1000 with 10 rows 37.7 (48.1); two prompts of 2048, 12 heads of 64,
-// 35.2 (41.1), 366 TFLOP/s.
+// prompt of 512 tokens, 32 heads over 8, 15.5 us (128-row tiles 19.5); 64
+// sequences of 1000 with 10 rows 38-42 (48.1); two prompts of 2048, 12 heads of 64,
+// 36-37 (41.1), 350 TFLOP/s; one of 2048, 16 heads of 256 over 8, 83 (98).  With this
+// page's scores multiplied in the step itself the last took 91, the others as long.
 #include "kv_attn.h"
 
 namespace tern {
@@ -27,7 +28,6 @@ constexpr int kMidWaves = 4;
 template <int D>
 __global__ __launch_bounds__(64 * kMidWaves, D <= 128 ? 2 : 1) void attn_mid_kernel(const AttnArgs a) {
   constexpr int THREADS = 64 * kMidWaves, ROWS = kAttnMid;
-  constexpr int AHEAD = D == 64 ? 8 : 16;
   constexpr int C = D / 64, DT = D / 16;  // a wavefront's pieces of 16 codes a lane, of keys and of values; blocks of the sums
   __shared__ kw4_t lk[2][kPage * D / 8], lv[2][kPage * D / 8];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -101,54 +101,52 @@ __global__ __launch_bounds__(64 * kMidWaves, D <= 128 ? 2 : 1) void attn_mid_ker
   auto seen = [&](int p) { return p * kPage < most && p * kPage + kPage > least; };
 
   int p = mine.begin, cur = 0;
-  int raw = load_id(p), raw1 = load_id(p + 1), raw2 = load_id(p + 2);
-  int id = id_of(raw, p), id1 = id_of(raw1, p + 1);
+  int raw = load_id(p), raw1 = load_id(p + 1), raw2 = load_id(p + 2), raw3 = load_id(p + 3);
+  int id = id_of(raw, p), id1 = id_of(raw1, p + 1), id2 = id_of(raw2, p + 2);
   const size_t at0 = place_in(id), at1 = place_in(id1);
-  load_page(a.c.k, at0, kr);
+  load_page(a.c.k, at0, kr);  // the first pages together
   load_page(a.c.v, at0, vr);
-  kw4_t k1[C], v1[C];  // the first pages together
+  kw4_t k1[C], v1[C];
   load_page(a.c.k, at1, k1);
   load_page(a.c.v, at1, v1);
   float ks0 = load_scale(a.c.ks, at0), vs0 = load_scale(a.c.vs, at0);  // this page's, the next one's
   float ks1 = load_scale(a.c.ks, at1), vs1 = load_scale(a.c.vs, at1);
+  kf4_t z[4];
+  auto multiply = [&](const kw4_t* ks, kf4_t* z) {  // a page's scores
+#pragma unroll
+    for (int t = 0; t < 4; ++t) z[t] = kf4_t{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int t = 0; t < 4; ++t) z[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(operand(ks, c * 4 + t, u), q[c][u], z[t], 0, 0, 0);
+  };
   if (mine.begin < mine.end) {
     decode(kr, lk[0]);
     decode(vr, lv[0]);
+    decode(k1, lk[1]);
+    load_page(a.c.k, place_in(id2), kr);
 #pragma unroll
-    for (int i = 0; i < C; ++i) {
-      kr[i] = k1[i];
-      vr[i] = v1[i];
-    }
+    for (int i = 0; i < C; ++i) vr[i] = v1[i];
+    __syncthreads();
+    multiply(lk[0], z);
     __syncthreads();
   }
   for (; p < mine.end; ++p, cur ^= 1) {
-    const kw4_t *const ks = lk[cur], *const vs = lv[cur];
+    const kw4_t* const vs = lv[cur];
     const bool any = seen(p);
-    kf4_t z[4];
-#pragma unroll
-    for (int t = 0; t < 4; ++t) z[t] = kf4_t{0.f, 0.f, 0.f, 0.f};
-    if (any) {
-#pragma unroll
-      for (int c = 0; c < C; ++c)
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-          for (int t = 0; t < 4; ++t)
-            z[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(operand(ks, c * 4 + t, u), q[c][u], z[t], 0, 0, 0);
-    }
-    // the first of the values' operands arrive while weights are found
-    kh8_t v[AHEAD];
-#pragma unroll
-    for (int i = 0; i < AHEAD; ++i) v[i] = operand(vs, i % DT, i / DT);
-    __builtin_amdgcn_sched_barrier(0);
-    decode(kr, lk[cur ^ 1]);
+    // Behind the last page the next scores are of what lies there, and not used.
+    kf4_t next[4];
+    multiply(lk[cur ^ 1], next);
+    decode(kr, lk[cur]);
     decode(vr, lv[cur ^ 1]);
-    const int id2 = id_of(raw2, p + 2);
     const size_t at2 = place_in(id2);
-    load_page(a.c.k, at2, kr);
-    load_page(a.c.v, at2, vr);
     const float ks2 = load_scale(a.c.ks, at2), vs2 = load_scale(a.c.vs, at2);
-    raw2 = load_id(p + 3);
+    const int id3 = id_of(raw3, p + 3);
+    raw3 = load_id(p + 4);
+    load_page(a.c.k, place_in(id3), kr);
+    load_page(a.c.v, at2, vr);
     if (any) {
       const float vscale = __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(__float_as_int(vs0)));
       float by = ks0 * a.scale, best = -INFINITY;  // the scores are by z
@@ -191,13 +189,13 @@ __global__ __launch_bounds__(64 * kMidWaves, D <= 128 ? 2 : 1) void attn_mid_ker
 #pragma unroll
       for (int u = 0; u < 2; ++u)
 #pragma unroll
-        for (int d = 0; d < DT; ++d) {
-          const int i = u * DT + d;
-          o[d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(i < AHEAD ? v[i] : operand(vs, d, u), w[u], o[d], 0, 0, 0);
-        }
+        for (int d = 0; d < DT; ++d) o[d] = __builtin_amdgcn_mfma_f32_16x16x32_f16(operand(vs, d, u), w[u], o[d], 0, 0, 0);
     }
+#pragma unroll
+    for (int t = 0; t < 4; ++t) z[t] = next[t];
     id = id1;
     id1 = id2;
+    id2 = id3;
     ks0 = ks1;
     vs0 = vs1;
     ks1 = ks2;
