@@ -176,7 +176,7 @@ struct Cost {
   double step, share;
   int holds;
 };
-constexpr Cost kMidCost[3] = {{0.8, 1.9, 4}, {1.25, 1.33, 2}, {2.1, 1.15, 1}};  // of 64, 128, 256 dimensions
+constexpr Cost kMidCost[3] = {{0.8, 1.9, 4}, {1.25, 1.33, 2}, {1.95, 1.15, 1}};  // of 64, 128, 256 dimensions
 constexpr Cost kTileCost[3] = {{1.05, 1.4, 2}, {1.5, 1.37, 2}, {2.75, 1.0, 1}};
 int parts_for(long long groups, int pages, double mean, int dim, int rows, double& least) {
   const Cost c = (rows == tern::kAttnMid ? kMidCost : kTileCost)[dim / 128];
