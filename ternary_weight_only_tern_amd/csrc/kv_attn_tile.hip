@@ -349,36 +349,55 @@ __global__ __launch_bounds__(64 * kTileWaves, D <= 128 ? 2 : 1) void attn_tile_k
   if (hq == 0) part_totals<D, ROWS>(a)[slot * ROWS + block * 32 + c32] = kw2_t{__float_as_uint(row.top), __float_as_uint(sum)};
 }
 
-// y from the sums of a tile's parts, in their order: a workgroup has one of the
-// fours of dimensions that a thread holds, its threads what the tile's own
-// threads left (32 rows a wavefront and 4 of 8 dimensions a lane, or 16 rows and
-// 4 of 16).
-template <int D, int ROWS>
-__global__ __launch_bounds__(64 * kTileWaves) void attn_join_tile_kernel(const AttnArgs a) {
+// y from the sums of a tile's parts, in an order of their own: a workgroup has one
+// of the fours of dimensions that a thread holds, the threads of each of its
+// SIDES what the tile's own threads left (32 rows a wavefront and 4 of 8 dimensions
+// a lane, or 16 rows and 4 of 16), of every SIDES-th part.  Four sides where parts
+// are more than 32 (us with the tiles: 130 parts of six 32.6 -> 25.0, 63 of eight 26.6 ->
+// 24.1, 16 of 32 20.8 -> 21.4).
+template <int D, int ROWS, int SIDES>
+__global__ __launch_bounds__(64 * kTileWaves * SIDES) void attn_join_tile_kernel(const AttnArgs a) {
   constexpr int THREADS = 64 * kTileWaves, R = ROWS / kTileWaves, L = 64 / R * 4;  // rows a wavefront, dimensions of a store
+  __shared__ kf4_t side_sums[SIDES > 1 ? SIDES - 1 : 1][SIDES > 1 ? THREADS : 1];
+  __shared__ float2 side_totals[SIDES > 1 ? SIDES - 1 : 1][SIDES > 1 ? THREADS : 1];
   const int head = blockIdx.x % a.c.heads, s = blockIdx.x / a.c.heads % a.b.count, tile = blockIdx.x / a.c.heads / a.b.count;
   const Span sp = span_of(a.b, s);
   const int total = sp.n * a.group;
   if (tile * ROWS >= total) return;
   const int count = parts_of(a, range_of_rows(a, sp, tile * ROWS, min(tile * ROWS + ROWS, total) - 1)).count;
-  const int lane = threadIdx.x & 63, in = threadIdx.x / 64 * R + lane % R, r = tile * ROWS + in;
-  if (count == 1 || r >= total) return;
+  if (count == 1) return;
+  const int side = threadIdx.x / THREADS, thread = threadIdx.x % THREADS;
+  const int lane = thread & 63, in = thread / 64 * R + lane % R, r = tile * ROWS + in;
   const size_t slot = part_slot(a, s, head, tile);
-  const kf4_t* const sums = reinterpret_cast<const kf4_t*>(a.part) + (slot * (D / L) + blockIdx.y) * THREADS + threadIdx.x;
+  const kf4_t* const sums = reinterpret_cast<const kf4_t*>(a.part) + (slot * (D / L) + blockIdx.y) * THREADS + thread;
   const kw2_t* const totals = part_totals<D, ROWS>(a) + slot * ROWS + in;
   kf4_t v = {0.f, 0.f, 0.f, 0.f};
   float sum = 0.f, top = -INFINITY;
-#pragma unroll 4
-  for (int i = 0; i < count; ++i) {
-    const kw2_t t = totals[(size_t)i * ROWS];
-    const kf4_t x = sums[(size_t)i * (D / L) * THREADS];
-    const float own = __uint_as_float(t.x), most = fmaxf(top, own);
+  auto add = [&](float own, float own_sum, kf4_t x) {
+    const float most = fmaxf(top, own);
     const float keep = top == most ? 1.f : __builtin_amdgcn_exp2f(top - most);
     const float f = own == most ? 1.f : __builtin_amdgcn_exp2f(own - most);
-    sum = sum * keep + __uint_as_float(t.y) * f;
+    sum = sum * keep + own_sum * f;
     v = v * keep + x * f;
     top = most;
+  };
+  if (r < total) {  // what lies behind the rows was not written
+#pragma unroll 4
+    for (int i = side; i < count; i += SIDES) {
+      const kw2_t t = totals[(size_t)i * ROWS];
+      add(__uint_as_float(t.x), __uint_as_float(t.y), sums[(size_t)i * (D / L) * THREADS]);
+    }
   }
+  if (SIDES > 1) {
+    if (side > 0) {
+      side_sums[side - 1][thread] = v;
+      side_totals[side - 1][thread] = make_float2(top, sum);
+    }
+    __syncthreads();
+    if (side > 0) return;
+    for (int i = 0; i < SIDES - 1; ++i) add(side_totals[i][thread].x, side_totals[i][thread].y, side_sums[i][thread]);
+  }
+  if (r >= total) return;
   const size_t out = ((size_t)(sp.first + r / a.group) * a.q_heads + head * a.group + r % a.group) * D;
   finish_row(a, out + L * blockIdx.y + lane / R * 4, v, sum);
 }
@@ -392,7 +411,10 @@ hipError_t tile(const AttnArgs& a, long long grid, hipStream_t s) {
 template <int D, int ROWS>
 hipError_t join(const AttnArgs& a, hipStream_t s) {
   const dim3 grid((unsigned)(a.b.count * a.c.heads * a.tiles), D * ROWS / (64 * kTileWaves * 4));
-  hipLaunchKernelGGL((attn_join_tile_kernel<D, ROWS>), grid, dim3(64 * kTileWaves), 0, s, a);
+  if (a.parts > 32)
+    hipLaunchKernelGGL((attn_join_tile_kernel<D, ROWS, 4>), grid, dim3(64 * kTileWaves * 4), 0, s, a);
+  else
+    hipLaunchKernelGGL((attn_join_tile_kernel<D, ROWS, 1>), grid, dim3(64 * kTileWaves), 0, s, a);
   return hipGetLastError();
 }
 template <int D>

@@ -73,6 +73,14 @@ def test_parts(tile):
     A.test_parts_give_what_one_gives(80)
 
 
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_more_than_32_parts(tile, dim):
+    """One cache head's long contexts, of which a tile's last rows alone see the
+    last page."""
+    rng = np.random.default_rng(dim)
+    A.run(Case(rng, [40, 70], [4700, 3000], 1, dim), 1, rng)
+
+
 @pytest.mark.parametrize("rows,lens,heads,q_heads", [([300, 200], [300, 700], 2, 8), ([400] * 4, [450] * 4, 8, 16)])
 def test_by_the_rule(rows, lens, heads, q_heads):
     rng = np.random.default_rng(len(rows))
