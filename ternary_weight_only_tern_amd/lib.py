@@ -476,7 +476,7 @@ def _use_torch():
     import torch
     raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
     _raw_stream = raw or (lambda index: torch.cuda.current_stream(index).cuda_stream)
-    _current_device = torch.cuda.current_device
+    _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
     _halves = (torch.float16,)
     _torch = torch
     return torch
@@ -748,10 +748,16 @@ class Rope:
 def _heads(t, name, device, heads, dim):
     """Checks rows of heads, fp16 [m][heads][dim] whose heads follow each
     other (heads None: any number); the rows' stride."""
-    shape, stride = t.shape, t.stride()
-    if (len(shape) == 3 and t.dtype is _halves[0] and t.device == device and shape[2] == dim and stride[2] == 1
-            and stride[1] == dim and (heads is None or shape[1] == heads) and 0 < shape[0] < 2 ** 31 and shape[1] < 2 ** 31):
-        return stride[0] if shape[0] > 1 else shape[1] * dim
+    if t.dtype is _halves[0] and t.device == device:
+        shape = t.shape
+        if len(shape) == 3:
+            m, h, d = shape
+            if d == dim and (heads is None or h == heads) and 0 < m < 2 ** 31 and 0 < h < 2 ** 31:
+                if t.is_contiguous():
+                    return h * d
+                row, head, step = t.stride()
+                if step == 1 and head == d and m > 1:
+                    return row
     return _heads_slowly(t, name, device, heads, dim)
 
 
