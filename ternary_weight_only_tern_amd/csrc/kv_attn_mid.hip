@@ -223,8 +223,7 @@ __global__ __launch_bounds__(64 * kMidWaves, D <= 128 ? 2 : 1) void attn_mid_ker
 
 template <int D>
 hipError_t mid(const AttnArgs& a, long long grid, hipStream_t s) {
-  hipLaunchKernelGGL((attn_mid_kernel<D>), dim3((unsigned)grid), dim3(64 * kMidWaves), 0, s, a);
-  return hipGetLastError();
+  return kv_launch(attn_mid_kernel<D>, dim3((unsigned)grid), 64 * kMidWaves, s, a);
 }
 
 }  // namespace

@@ -402,19 +402,15 @@ template <int D>
 hipError_t rows(const AttnArgs& a, int blocks, hipStream_t s) {
   const long long grid = a.pieces;
   if (!kv_grid_fits(grid, 64)) return hipErrorInvalidConfiguration;
-  if (blocks == 1)
-    hipLaunchKernelGGL((attn_rows_kernel<D, 1>), dim3((unsigned)grid), dim3(64), 0, s, a);
-  else
-    hipLaunchKernelGGL((attn_rows_kernel<D, 2>), dim3((unsigned)grid), dim3(64), 0, s, a);
-  return hipGetLastError();
+  if (blocks == 1) return kv_launch(attn_rows_kernel<D, 1>, dim3((unsigned)grid), 64, s, a);
+  return kv_launch(attn_rows_kernel<D, 2>, dim3((unsigned)grid), 64, s, a);
 }
 
 template <int D>
 hipError_t join(const AttnArgs& a, hipStream_t s) {
   const long long x = (long long)a.b.count * a.b.max_rows;
   if (a.q_heads > 65535 || !kv_grid_fits(x * a.q_heads, 256)) return hipErrorInvalidConfiguration;
-  hipLaunchKernelGGL((attn_join_kernel<D>), dim3((unsigned)x, (unsigned)a.q_heads), dim3(256), 0, s, a);
-  return hipGetLastError();
+  return kv_launch(attn_join_kernel<D>, dim3((unsigned)x, (unsigned)a.q_heads), 256, s, a);
 }
 
 }  // namespace

@@ -404,18 +404,14 @@ __global__ __launch_bounds__(64 * kTileWaves * SIDES) void attn_join_tile_kernel
 
 template <int D>
 hipError_t tile(const AttnArgs& a, long long grid, hipStream_t s) {
-  hipLaunchKernelGGL((attn_tile_kernel<D>), dim3((unsigned)grid), dim3(64 * kTileWaves), 0, s, a);
-  return hipGetLastError();
+  return kv_launch(attn_tile_kernel<D>, dim3((unsigned)grid), 64 * kTileWaves, s, a);
 }
 
 template <int D, int ROWS>
 hipError_t join(const AttnArgs& a, hipStream_t s) {
   const dim3 grid((unsigned)(a.b.count * a.c.heads * a.tiles), D * ROWS / (64 * kTileWaves * 4));
-  if (a.parts > 32)
-    hipLaunchKernelGGL((attn_join_tile_kernel<D, ROWS, 4>), grid, dim3(64 * kTileWaves * 4), 0, s, a);
-  else
-    hipLaunchKernelGGL((attn_join_tile_kernel<D, ROWS, 1>), grid, dim3(64 * kTileWaves), 0, s, a);
-  return hipGetLastError();
+  if (a.parts > 32) return kv_launch(attn_join_tile_kernel<D, ROWS, 4>, grid, 64 * kTileWaves * 4, s, a);
+  return kv_launch(attn_join_tile_kernel<D, ROWS, 1>, grid, 64 * kTileWaves, s, a);
 }
 template <int D>
 hipError_t join(const AttnArgs& a, int rows, hipStream_t s) {

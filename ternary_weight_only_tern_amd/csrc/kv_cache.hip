@@ -332,16 +332,12 @@ __global__ __launch_bounds__(256) void kv_read_kernel(const ReadArgs a) {
 
 template <int D>
 hipError_t write(const WriteArgs& a, long long blocks, hipStream_t s) {
-  hipLaunchKernelGGL((kv_write_kernel<D>), dim3((unsigned)blocks), dim3(256), 0, s, a);
-  return hipGetLastError();
+  return kv_launch(kv_write_kernel<D>, dim3((unsigned)blocks), 256, s, a);
 }
 template <int D>
 hipError_t read(const ReadArgs& a, long long blocks, hipStream_t s) {
-  if (a.f32)
-    hipLaunchKernelGGL((kv_read_kernel<D, true>), dim3((unsigned)blocks), dim3(256), 0, s, a);
-  else
-    hipLaunchKernelGGL((kv_read_kernel<D, false>), dim3((unsigned)blocks), dim3(256), 0, s, a);
-  return hipGetLastError();
+  if (a.f32) return kv_launch(kv_read_kernel<D, true>, dim3((unsigned)blocks), 256, s, a);
+  return kv_launch(kv_read_kernel<D, false>, dim3((unsigned)blocks), 256, s, a);
 }
 
 }  // namespace

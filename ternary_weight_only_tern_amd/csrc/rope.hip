@@ -32,8 +32,7 @@ hipError_t launch_rope(const RopeArgs& a, hipStream_t s) {
   const int waves = kv_waves(a.m, a.heads, lanes);
   const long long blocks = ((long long)a.m * waves + 3) / 4;
   if (!kv_grid_fits(blocks, 256)) return hipErrorInvalidConfiguration;
-  hipLaunchKernelGGL(rope_kernel, dim3((unsigned)blocks), dim3(256), 0, s, a, lanes, waves);
-  return hipGetLastError();
+  return kv_launch(rope_kernel, dim3((unsigned)blocks), 256, s, a, lanes, waves);
 }
 
 }  // namespace tern
