@@ -74,7 +74,7 @@ __global__ __launch_bounds__(64 * kMidWaves, D <= 128 ? 2 : 1) void attn_mid_ker
   // masked or not looked at.  Its number and scales come by vector loads, a step
   // and more ahead, as in kv_attn_tile.hip.
   kw4_t kr[C], vr[C];
-  const __amdgpu_buffer_rsrc_t table = kv_buffer(a.b.pages + (size_t)s * a.b.max_pages, a.b.max_pages * 4);
+  const __amdgpu_buffer_rsrc_t table = kv_buffer(a.b.pages + (size_t)s * a.b.max_pages, min(a.b.max_pages, kMaxTokens / kPage) * 4);
   auto load_id = [&](int p) { return (int)__builtin_amdgcn_raw_buffer_load_b32(table, p * 4, 0, 0); };
   auto id_of = [&](int raw, int p) {
     const int id = __builtin_amdgcn_readfirstlane(raw);
