@@ -88,7 +88,7 @@ struct AttnArgs {
   const uint16_t* q;
   int64_t q_stride;
   uint16_t* y;         // [rows][q_heads][dim]
-  // Few rows: pieces of the line of all pages (a.whole: units), `per` pages each
+  // Few rows: pieces of the line of all pages (whole: units), `per` pages each
   // at least; their sums [pieces][2][max_rows * group][dim] and references and
   // sums of weights [pieces][2][max_rows * group][2] in part; info: a unit's first
   // piece and how many it has.  Tiles (tiles > 0): parts of the context at most,
@@ -108,8 +108,8 @@ constexpr int kAttnFew = 16, kAttnMid = 64, kAttnTile = 128;
 hipError_t launch_rope(const RopeArgs& a, hipStream_t s);
 hipError_t launch_kv_write(WriteArgs a, int dim, hipStream_t s);
 hipError_t launch_kv_read(const ReadArgs& a, int dim, hipStream_t s);
-// blocks: of 16 rows, 1 or 2
-hipError_t launch_attn_rows(const AttnArgs& a, int dim, int blocks, hipStream_t s);
+// blocks: of 16 rows, 1 or 2; shares: wavefronts of a whole unit
+hipError_t launch_attn_rows(const AttnArgs& a, int dim, int blocks, int shares, hipStream_t s);
 hipError_t launch_attn_tile(const AttnArgs& a, int dim, hipStream_t s);
 hipError_t launch_attn_join_rows(const AttnArgs& a, int dim, hipStream_t s);
 hipError_t launch_attn_mid(const AttnArgs& a, int dim, hipStream_t s);

@@ -132,7 +132,7 @@ int items_of(const tern_kv_batch* b) { return (most_rows(b) + 2 * (tern::kPage -
 // How attention runs.
 struct AttnPlan {
   int blocks;  // of 16 rows in the kernel for few rows, 1 or 2; 0: tiles
-  int pieces, whole, parts, per, tiles, tile;
+  int pieces, whole, shares, parts, per, tiles, tile;
   bool join;
   size_t rows, info;  // of partial sums, and units whose pieces are noted
 };
@@ -151,6 +151,14 @@ constexpr int kWholePages = 3;
 // 1024 of 8 27.7 -> 19.0; 2048 of 16 71.9 -> 61.7, of 64 210 -> 231; 4096 of 32
 // 220 -> 204, of 128 710 -> 764.  Four rows each, 1024 of 8: 40.5 -> 20.3.
 constexpr int kWholeUnits = 64;  // for every page
+// One block of rows: a workgroup of two, four or eight wavefronts, as many as the
+// card holds for all units, has a whole unit where each wavefront then has at most
+// a page more than a piece of the line, and few enough that uneven lengths do not
+// count (us, line -> shared; 32 heads over 8 of 128 dimensions unless said): one sequence
+// of 500, 1000 and 1500 tokens 8.6 -> 7.2, 8.8 -> 9.2, 9.2 -> 12.4; 32 of 500 and 1500
+// 15.1 -> 9.7, 24.3 -> 19.9; 64 ragged ones of up to 500, 2000 and 8192 15.5 -> 12.4, 34.5 ->
+// 33.4, 112 -> 122; 64 of up to 500, 16 heads over 4 of 256 dimensions, 17.4 -> 12.5.
+constexpr int kSharePages = 12;
 constexpr int kTileSlots = 1024;  // parts of tiles at most, where tiles are cut
 
 // Pages that `rows` neighbouring rows see at most.
@@ -214,8 +222,15 @@ AttnPlan plan_of(const tern_kv* c, const tern_kv_batch* b, int group, int window
   const int pages = pages_of(b, window, most_rows(b));
   if (rows <= tern::kAttnFew || (rows <= kFewRows && units * pages > kFewPages)) {
     p.blocks = rows <= 16 ? 1 : 2;
-    p.whole = pages <= kWholePages || units >= (long long)kWholeUnits * pages;
-    p.pieces = (int)(p.whole ? std::min<long long>(units, 1ll << 30) : std::min<long long>(p.blocks * c->dim > 128 ? kPieces / 2 : kPieces, units * pages));
+    const int waves = p.blocks * c->dim > 128 ? kPieces / 2 : kPieces, line = (int)((units * pages + waves - 1) / waves);
+    p.shares = 1;
+    if (p.blocks == 1)
+      for (int w = 2; w <= (c->dim > 128 ? 4 : 8); w *= 2)
+        if (units * w <= waves) p.shares = w;
+    const int each = (pages + p.shares - 1) / p.shares;
+    if (each > line + 1 || each > kSharePages) p.shares = 1;
+    p.whole = p.shares > 1 || pages <= kWholePages || units >= (long long)kWholeUnits * pages;
+    p.pieces = (int)(p.whole ? units : std::min<long long>(waves, units * pages));
     p.per = (pages + kUnitPieces - 1) / kUnitPieces;
     p.join = !p.whole;
     p.rows = p.join ? (size_t)p.pieces * 2 * rows : 0;
@@ -450,7 +465,7 @@ tern_status tern_kv_attention(const tern_kv* c, const tern_kv_batch* b, const ui
   a.tiles = p.tiles;
   const hipStream_t s = (hipStream_t)stream;
   if (p.blocks)
-    KV_HIP(tern::launch_attn_rows(a, c->dim, p.blocks, s));
+    KV_HIP(tern::launch_attn_rows(a, c->dim, p.blocks, p.shares, s));
   else
     KV_HIP(p.tile == tern::kAttnMid ? tern::launch_attn_mid(a, c->dim, s) : tern::launch_attn_tile(a, c->dim, s));
   if (p.join) KV_HIP(p.blocks ? tern::launch_attn_join_rows(a, c->dim, s) : tern::launch_attn_join_tile(a, c->dim, p.tile, s));

@@ -15,7 +15,8 @@
 // values likewise, page numbers two pages ahead, and the next unit's queries
 // when this unit's last scores are done.  A unit that lies in one piece goes
 // to y; others leave their sums in the workspace, at most two a wavefront,
-// which attn_join_kernel adds in the pieces' order.
+// which attn_join_kernel adds in the pieces' order.  Where pages are few, a
+// workgroup of several wavefronts has a unit instead, and adds their sums itself.
 //
 // Bound by the cache's bytes, of which it is asked 16 a lane at a time: 64
 // sequences of up to 8192 tokens, 8 heads of 128, 99 us, 5.9 TB/s (a plain read
@@ -60,11 +61,15 @@ __device__ inline Slot slot_of(const AttnArgs& a, long long wave, int which) {
   return {a.part + at * D, reinterpret_cast<kw2_t*>(a.part + (size_t)a.pieces * 2 * rows * D) + at};
 }
 
-template <int D, int NT>
-__global__ __launch_bounds__(64, NT * D <= 128 ? 2 : 1) void attn_rows_kernel(const AttnArgs a) {
+// W > 1: a workgroup of W wavefronts has a whole unit, whose pages they share
+// and whose sums they add through LDS.
+template <int D, int NT, int W>
+__global__ __launch_bounds__(64 * W, NT * D <= 128 ? 2 : 1) void attn_rows_kernel(const AttnArgs a) {
   constexpr int C = D / 64, DT = D / 16;
-  const int lane = threadIdx.x, col = lane & 15, kq = lane >> 4;
-  const int wave = blockIdx.x;
+  const int lane = threadIdx.x & 63, col = lane & 15, kq = lane >> 4;
+  const int wave = blockIdx.x, share = W > 1 ? uniform(threadIdx.x >> 6) : 0;
+  __shared__ kf4_t unit_sums[W > 1 ? W * 16 * D / 4 : 1];
+  __shared__ kw2_t unit_tops[W > 1 ? W * 16 : 1];
 
   // The line's length, then where this wavefront's piece begins.
   Step now = {0, 0, 0, -1, -1};
@@ -74,8 +79,9 @@ __global__ __launch_bounds__(64, NT * D <= 128 ? 2 : 1) void attn_rows_kernel(co
     now.s = wave / a.c.heads;
     now.head = wave % a.c.heads;
     run = run_of(a, now.s);
-    now.p = run.r.begin;
-    now.left = run.r.end - run.r.begin - 1;
+    const int n = run.r.end - run.r.begin, each = (n + W - 1) / W;
+    now.p = run.r.begin + share * each;
+    now.left = min(each, n - share * each) - 1;
   } else {
     auto pages = [&](int x) {
       if (x >= a.b.count) return 0;
@@ -118,7 +124,7 @@ __global__ __launch_bounds__(64, NT * D <= 128 ? 2 : 1) void attn_rows_kernel(co
     }
   }
   // units without pages: their rows are zero
-  for (int u = wave; u < a.b.count * a.c.heads; u += a.pieces) {
+  for (int u = wave; share == 0 && u < a.b.count * a.c.heads; u += a.pieces) {
     const Run x = run_of(a, u / a.c.heads);
     if (x.r.end > x.r.begin) continue;
     for (int i = lane; i < x.sp.n * a.group * (D / 4); i += 64) {
@@ -128,7 +134,7 @@ __global__ __launch_bounds__(64, NT * D <= 128 ? 2 : 1) void attn_rows_kernel(co
     }
     if (lane == 0 && !a.whole) a.info[u] = make_int2(0, 1);
   }
-  if (now.left < 0) return;
+  if (W == 1 && now.left < 0) return;
 
   // The step behind one; the run it lies in.
   auto number = [&](const Step& x) { return uniform(page_of(a.b, a.c, x.s, x.p)); };
@@ -228,7 +234,8 @@ __global__ __launch_bounds__(64, NT * D <= 128 ? 2 : 1) void attn_rows_kernel(co
   };
   auto scale_at = [&](const float* scales, const Step& x) { return kv_const(scales, (size_t)max(x.id, 0) * a.c.heads + x.head); };
 
-  now.id = number(now);
+  if (now.left < 0) now.p = -1;  // of W wavefronts: more than there are pages
+  now.id = now.left < 0 ? -1 : number(now);
   Run ahead = run;  // of the step that is looked at first
   Step next = behind(now, ahead);
   Run run_next = ahead;
@@ -240,7 +247,7 @@ __global__ __launch_bounds__(64, NT * D <= 128 ? 2 : 1) void attn_rows_kernel(co
   bool opened = now.p == run.r.begin;  // the unit begins in this piece,
   int room = now.left + 1;             // which had so many pages left then
 
-  for (;;) {
+  for (; W == 1 || now.left >= 0;) {
     const Step later = behind(next, ahead);
     const float ks = ks_next * a.scale, vs = vs_next;
     ks_next = scale_at(a.c.ks, next);
@@ -326,12 +333,15 @@ __global__ __launch_bounds__(64, NT * D <= 128 ? 2 : 1) void attn_rows_kernel(co
 #pragma unroll
         for (int d = 0; d < DT; ++d) {
           const kf4_t v = o[n][d] * unit;
-          if (all)
+          if (W > 1)
+            unit_sums[(share * 16 + r) * (D / 4) + 4 * d + kq] = v;
+          else if (all)
             finish_row(a, out * D + 16 * d + 4 * kq, v, sum);
           else
             *reinterpret_cast<kf4_t*>(slot.sums + (size_t)r * D + 16 * d + 4 * kq) = v;
         }
-        if (!all && kq == 0) slot.tops[r] = kw2_t{__float_as_uint(row[n].top), __float_as_uint(sum)};
+        if (W > 1 && kq == 0) unit_tops[share * 16 + r] = kw2_t{__float_as_uint(row[n].top), __float_as_uint(sum)};
+        if (W == 1 && !all && kq == 0) slot.tops[r] = kw2_t{__float_as_uint(row[n].top), __float_as_uint(sum)};
       }
       if (opened && lane == 0 && !a.whole) {
         const int more = run.r.end - run.r.begin - room;
@@ -346,6 +356,27 @@ __global__ __launch_bounds__(64, NT * D <= 128 ? 2 : 1) void attn_rows_kernel(co
     run = run_next;
     next = later;
     run_next = ahead;
+  }
+  if constexpr (W > 1) {
+    const Run unit = run_of(a, wave / a.c.heads);
+    const int n = unit.r.end - unit.r.begin, each = (n + W - 1) / W, rows = unit.sp.n * a.group;
+    if (n <= 0) return;
+    const int shares = (n + each - 1) / each;
+    __syncthreads();
+    for (int i = threadIdx.x; i < rows * (D / 4); i += 64 * W) {
+      const int r = i / (D / 4), d = i % (D / 4);
+      float top = -INFINITY, sum = 0.f;
+      kf4_t v = {0.f, 0.f, 0.f, 0.f};
+      for (int x = 0; x < shares; ++x) top = fmaxf(top, __uint_as_float(unit_tops[x * 16 + r].x));
+      for (int x = 0; x < shares; ++x) {
+        const kw2_t t = unit_tops[x * 16 + r];
+        const float own = __uint_as_float(t.x), f = own == top ? 1.f : __builtin_amdgcn_exp2f(own - top);
+        sum += __uint_as_float(t.y) * f;
+        v += unit_sums[(x * 16 + r) * (D / 4) + d] * f;
+      }
+      const size_t out = (size_t)(unit.sp.first + r / a.group) * a.q_heads + wave % a.c.heads * a.group + r % a.group;
+      finish_row(a, out * D + 4 * d, v, sum);
+    }
   }
 }
 
@@ -399,11 +430,15 @@ __global__ __launch_bounds__(256) void attn_join_kernel(const AttnArgs a) {
 }
 
 template <int D>
-hipError_t rows(const AttnArgs& a, int blocks, hipStream_t s) {
-  const long long grid = a.pieces;
-  if (!kv_grid_fits(grid, 64)) return hipErrorInvalidConfiguration;
-  if (blocks == 1) return kv_launch(attn_rows_kernel<D, 1>, dim3((unsigned)grid), 64, s, a);
-  return kv_launch(attn_rows_kernel<D, 2>, dim3((unsigned)grid), 64, s, a);
+hipError_t rows(const AttnArgs& a, int blocks, int shares, hipStream_t s) {
+  const dim3 grid((unsigned)a.pieces);
+  if (!kv_grid_fits(a.pieces, 64 * shares)) return hipErrorInvalidConfiguration;
+  if (blocks == 2) return kv_launch(attn_rows_kernel<D, 2, 1>, grid, 64, s, a);
+  if (shares == 2) return kv_launch(attn_rows_kernel<D, 1, 2>, grid, 128, s, a);
+  if (shares == 4) return kv_launch(attn_rows_kernel<D, 1, 4>, grid, 256, s, a);
+  if constexpr (D < 256)
+    if (shares == 8) return kv_launch(attn_rows_kernel<D, 1, 8>, grid, 512, s, a);
+  return kv_launch(attn_rows_kernel<D, 1, 1>, grid, 64, s, a);
 }
 
 template <int D>
@@ -415,9 +450,9 @@ hipError_t join(const AttnArgs& a, hipStream_t s) {
 
 }  // namespace
 
-hipError_t launch_attn_rows(const AttnArgs& a, int dim, int blocks, hipStream_t s) {
-  if (dim == 64) return rows<64>(a, blocks, s);
-  return dim == 128 ? rows<128>(a, blocks, s) : rows<256>(a, blocks, s);
+hipError_t launch_attn_rows(const AttnArgs& a, int dim, int blocks, int shares, hipStream_t s) {
+  if (dim == 64) return rows<64>(a, blocks, shares, s);
+  return dim == 128 ? rows<128>(a, blocks, shares, s) : rows<256>(a, blocks, shares, s);
 }
 
 hipError_t launch_attn_join_rows(const AttnArgs& a, int dim, hipStream_t s) {

@@ -43,6 +43,25 @@ def test_few_rows(rows, lens, heads, q_heads, dim):
     run(c, q_heads, rng)
 
 
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("rows,lens,heads,q_heads", ROWS)
+def test_few_rows_in_pieces(rows, lens, heads, q_heads, dim):
+    """Cut into the line's pieces (by max_len), as long contexts are."""
+    rng = np.random.default_rng(sum(rows) + sum(lens) + q_heads + dim)
+    c = Case(rng, rows, lens, heads, dim, tail=3)
+    run(c, q_heads, rng, max_len=10 ** 6)
+
+
+@pytest.mark.parametrize("count,dim", [(3, 64), (60, 64), (130, 64), (3, 128), (60, 128), (130, 128), (3, 256), (40, 256), (70, 256)])
+def test_units_shared_by_wavefronts(count, dim):
+    """Eight, four and two wavefronts a unit; lengths of none to ten pages."""
+    rng = np.random.default_rng(count + dim)
+    lens = [0, 1, 64, 65, 640] + [int(n) for n in rng.integers(0, 641, count)]
+    c = Case(rng, [2] * len(lens), lens, 8, dim)
+    run(c, 16, rng)
+    run(c, 16, rng, window=100)
+
+
 TILES = [
     ([65], [65], 1, 1), ([70], [200], 1, 2), ([130], [130], 2, 4), ([33], [100], 1, 5), ([200, 3, 77], [333, 3, 400], 1, 3), ([129], [64], 1, 1),
     ([100, 100], [100, 0], 2, 2), ([90], [1500], 1, 4),

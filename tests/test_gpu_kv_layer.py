@@ -230,7 +230,7 @@ def test_threads_with_many_numbers_of_rows():
 
 def test_smaller_workspace_is_refused_and_bad_arguments():
     rng = np.random.default_rng(17)
-    c = Case(rng, [1], [900], 2, 64)
+    c = Case(rng, [1], [3000], 2, 64)
     cache, batch, q = c.cache(), c.on_device(), dev(half(rng, 1, 4, 64))
     with pytest.raises(L.TernError) as e:
         L.tern_kv_attention(cache, batch, q, ws=torch.empty(256, dtype=torch.uint8, device="cuda"))

@@ -96,7 +96,7 @@ def test_read_refusals():
 def test_attention_refusals():
     lib = L.load()
 
-    def f(c=cache(), b=batch(), q=0x1000, qs=4096, heads=32, scale=0.1, window=0, causal=1, y=0x2000, ws=0x3000, nb=1 << 40):
+    def f(c=cache(), b=batch(max_len=100000), q=0x1000, qs=4096, heads=32, scale=0.1, window=0, causal=1, y=0x2000, ws=0x3000, nb=1 << 40):
         return lib.tern_kv_attention(at(c), at(b), q, qs, heads, scale, window, causal, y, ws, nb, None)
 
     assert f(q=None) == INVAL and f(y=None) == INVAL and f(q=0x1004) == ALIGN and f(y=0x2008) == ALIGN and f(ws=0x3008) == ALIGN
@@ -107,7 +107,7 @@ def test_attention_refusals():
     assert f(c=cache(pages=0)) == INVAL
     assert f(b=batch(count=1 << 22)) == UNSUPPORTED and f(b=batch(count=1 << 12, max_pages=1 << 20)) == UNSUPPORTED
     assert f(b=batch(count=1, max_rows=1 << 28), heads=64) == UNSUPPORTED
-    need = lib.tern_kv_attention_workspace_bytes(at(cache()), at(batch()), 32)
+    need = lib.tern_kv_attention_workspace_bytes(at(cache()), at(batch(max_len=100000)), 32)
     assert need > 256 and f(nb=0) == WORKSPACE and f(ws=None) == WORKSPACE
     assert f(b=batch(count=0, len=None, pages=None), q=None, y=None, ws=None, nb=0) == L.TERN_OK
 
@@ -158,8 +158,10 @@ def test_which_way_a_call_goes():
     assert parts(count=1, max_rows=4, max_len=5000, c=cache(dim=256)) == 632 and parts(count=1, max_rows=8, max_len=5000, c=cache(dim=256)) < -2
     assert parts(count=8, max_rows=8, max_len=4097) == 1024 and parts(count=8, max_rows=8, max_len=4096) < -2  # 4160, 4096 pages
     assert parts(count=1, max_rows=1, max_len=100000, window=100) == 8 and parts(count=0) == 0  # three pages are not cut
-    assert parts(count=1, max_rows=1, max_len=100000, window=300) == 48
-    assert parts(count=64, max_rows=1, max_len=512) == 512 and parts(count=64, max_rows=1, max_len=513) == 2048  # 64 units a page
+    assert parts(count=1, max_rows=1, max_len=100000, window=300) == 8 and parts(count=1, max_rows=1, max_len=100000, window=1200) == 160
+    assert parts(count=64, max_rows=1, max_len=3008) == 512 and parts(count=64, max_rows=1, max_len=3200) == 2048  # 12 pages a wavefront
+    assert parts(count=256, max_rows=1, max_len=2048) == 2048 and parts(count=300, max_rows=1, max_len=2400) == 2048  # 64 units a page
+    assert parts(count=300, max_rows=1, max_len=2368) == 2400
     # tiles: no more parts than pay for their joining
     assert parts(count=1, max_rows=512, max_len=512) == -2 and parts(count=1, max_rows=512, max_len=8000) == -5
     assert parts(count=64, max_rows=512, max_len=8000) == -2 and parts(count=1, max_rows=64, max_len=4000) == -17
