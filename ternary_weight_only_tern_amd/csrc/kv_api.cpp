@@ -226,7 +226,7 @@ AttnPlan plan_of(const tern_kv* c, const tern_kv_batch* b, int group, int window
     p.shares = 1;
     if (p.blocks == 1)
       for (int w = 2; w <= (c->dim > 128 ? 4 : 8); w *= 2)
-        if (units * w <= waves) p.shares = w;
+        if (units * w <= (c->dim == 64 ? 2 * waves : waves)) p.shares = w;  // four wavefronts a SIMD at 64 dimensions
     const int each = (pages + p.shares - 1) / p.shares;
     if (each > line + 1 || each > kSharePages) p.shares = 1;
     p.whole = p.shares > 1 || pages <= kWholePages || units >= (long long)kWholeUnits * pages;
