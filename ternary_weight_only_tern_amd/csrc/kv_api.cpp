@@ -207,11 +207,11 @@ int parts_for(long long groups, int pages, double mean, int dim, int rows, doubl
 
 // Rows up to which a unit goes to the kernel for few rows; above one block of 16
 // only where there are more pages than kFewPages, which it reads faster.  us, few
-// rows / tiles: 20 rows of 32 heads of 256 dimensions after 3000 tokens (1500 pages) 36
-// / 25, of 64 after 8000 (8000 pages) 78 / 87; 20 ragged rows of 32 heads after up to 120000
-// (60000 pages) 115 / 170; 32 of 8 after 4000 (500) 16.7 / 11.6, of 32 after 8000 (4000) 27.9 /
-// 26.4, of 2048 after 500 (16000) 62 / 78; 64 rows of 64 after 8000, four blocks, not kept, 75 /
-// 48.
+// rows / tiles: 4 sequences of 8 cache heads of 256 dimensions, 20 rows each, after
+// 3000 tokens (1500 pages) 36 / 25, 8 after 8000 (8000 pages) 78 / 87; of 128 dimensions,
+// 32 rows each, 1 after 4000 (504) 16.7 / 11.6, 4 after 8000 (4000) 27.9 / 26.4, 256 after
+// 500 (16384) 62 / 78; 20 rows each, 4 ragged ones of up to 120000 (60000) 153 / 206; 64
+// rows each, 8 after 8000, four blocks, not kept, 75 / 48.
 constexpr int kFewRows = 32, kFewPages = 4096;
 
 std::atomic<int> g_tile_rows{0};  // of every tile, 0: by the rule

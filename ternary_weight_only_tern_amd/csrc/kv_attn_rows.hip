@@ -20,8 +20,8 @@
 //
 // Bound by the cache's bytes, of which it is asked 16 a lane at a time: 64
 // sequences of up to 8192 tokens, 8 heads of 128, 99 us, 5.9 TB/s (a plain read
-// of as much 6.4-7.0); four sequences of up to 120000 tokens, five rows each, 109 us,
-// 6.1 TB/s.  More wavefronts, deeper prefetch and other page orders gained
+// of as much 6.4-7.0); four sequences of up to 120000 tokens, five rows each,
+// 106-118 us, 5.6-6.2 TB/s.  More wavefronts, deeper prefetch and other page orders gained
 // nothing; loads that pass the L2 by (kv_stream) took 123 us to 113.  One token of 8 heads
 // after 4000: 6.6 us and 4.4 for joining, a chain of trips to memory.
 #include "kv_attn.h"
