@@ -518,7 +518,21 @@ def _bytes(size):
     return size or _refuse(last_error())
 
 
-class Q4Matrix:
+class _Fixed:
+    """An object whose descriptor holds its tensors' addresses and sizes: each
+    attribute is set once.  A tensor put in another's place would leave the
+    library with the address of one that may be gone."""
+
+    def __setattr__(self, name, value):
+        if name in self.__dict__:
+            raise AttributeError(f"{type(self).__name__}.{name} is not replaced: write into the tensor, or make another {type(self).__name__}")
+        self.__dict__[name] = value
+
+    def __delattr__(self, name):
+        raise AttributeError(f"{type(self).__name__}.{name} stays as long as its {type(self).__name__}")
+
+
+class Q4Matrix(_Fixed):
     """4-bit weights on the device: codes uint8 [n][k/2] in tern_q4's word
     order, scale fp16 [n][k/group], zero uint8 [n][k/group] or None (8
     everywhere); or a stack of them, [count][n][...] in every array.  Keeps
@@ -716,7 +730,7 @@ def tern_rope_frequencies(rot, base=1e6, scaling=TERN_ROPE_PLAIN, factor=1.0, lo
     return freq, amp.value
 
 
-class Rope:
+class Rope(_Fixed):
     """tern_rotary: how a head's values turn.  freq: fp64 device tensor
     [rot/2]; norm: fp16 device tensor [dim] or None, the weights of an RMS norm
     of each head before.  Keeps the tensors."""
@@ -800,7 +814,7 @@ def tern_rope(x, pos, rope: Rope, out=None, stream=None):
     return out
 
 
-class KvCache:
+class KvCache(_Fixed):
     """tern_kv: a paged cache in 8 bits.  k, v: uint8 [pages][heads][64][dim]
     (the bytes of a (page, head) in tern_kv's order), k_scale, v_scale: fp32
     [pages][heads].  Keeps the tensors; makes no copy."""
@@ -832,13 +846,13 @@ class KvCache:
         return cls(code(), code(), scale(), scale())
 
 
-class KvBatch:
+class KvBatch(_Fixed):
     """tern_kv_batch: the sequences of a call.  len: int32 [count], tokens with
     the call's rows; pages: int32 [count][max_pages]; max_rows: rows of a
     sequence at most; start: int32 [count + 1], or None where every sequence
     has max_rows rows; max_len: bound of len for the choice of kernels (default
     what the pages hold).  Keeps the tensors, whose contents may change between
-    calls."""
+    calls; its attributes may not (another batch takes other tensors)."""
 
     def __init__(self, len, pages, max_rows, start=None, max_len=None):
         import torch
