@@ -606,7 +606,8 @@ tern_status tern_kv_read(const tern_kv *c, const tern_kv_batch *b, void *k, void
  * it, whatever they or their scales hold.  Scores and sums are FP32; the
  * softmax's weights meet the codes of v in FP16 (11 bits each).  scale finite,
  * not negative.  ws: tern_kv_attention_workspace_bytes (0 for arguments that
- * are refused), 16-byte aligned, enough for every batch with no more
+ * are refused), 16-byte aligned (calls that need none take NULL, and refuse
+ * one that is not aligned too), enough for every batch with no more
  * sequences and rows and no larger max_len too; calls that overlap in time must
  * not share it.  At most (TERN_E_UNSUPPORTED): 65535 query heads, a q_stride of
  * 2^23, max_rows g of 2^30, count heads of 2^24, count heads max_pages of 2^31 - 1. */

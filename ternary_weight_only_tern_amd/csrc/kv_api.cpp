@@ -444,7 +444,7 @@ tern_status tern_kv_attention(const tern_kv* c, const tern_kv_batch* b, const ui
   const size_t need = attn_need(p, c);
   if (need && (!ws || ws_bytes < need))
     return fail(TERN_E_WORKSPACE, "workspace of %zu bytes, %zu are needed", ws ? ws_bytes : (size_t)0, need);
-  if (need) KV_TRY(check_ptr(ws, "workspace", 16));
+  if (ws) KV_TRY(check_ptr(ws, "workspace", 16));  // also one that this call does not need
   tern::AttnArgs a = {};
   a.c = cache_of(c);
   a.b = batch_of(b);
