@@ -129,6 +129,13 @@ tern::Batch batch_of(const tern_kv_batch* b) {
 // Pages that a sequence's rows may lie in.
 int items_of(const tern_kv_batch* b) { return (most_rows(b) + 2 * (tern::kPage - 1)) / tern::kPage; }
 
+// Workgroups of 256 threads, one a (page, head) of the keys or the values; -1: more
+// than a grid has.  The heads are divided by: all four sizes together pass 64 bits.
+long long page_blocks(const tern_kv* c, const tern_kv_batch* b) {
+  const long long pages = 2ll * b->count * items_of(b);
+  return pages <= ((1 << 24) - 1) / c->heads ? pages * c->heads : -1;
+}
+
 // How attention runs.
 struct AttnPlan {
   int blocks;  // of 16 rows in the kernel for few rows, 1 or 2; 0: tiles
@@ -383,8 +390,8 @@ tern_status tern_kv_write(const tern_kv* c, const tern_kv_batch* b, const uint16
     a.rq = rotary_of(q_rope);
   }
   a.items = items_of(b);
-  const long long blocks = 2ll * b->count * a.items * c->heads;
-  if (!tern::kv_grid_fits(blocks, 256)) return fail(TERN_E_UNSUPPORTED, "the call needs too many workgroups");
+  const long long blocks = page_blocks(c, b);
+  if (blocks < 0) return fail(TERN_E_UNSUPPORTED, "the call needs too many workgroups");
   a.kv_blocks = (int)blocks;
   KV_HIP(tern::launch_kv_write(a, c->dim, (hipStream_t)stream));
   return TERN_OK;
@@ -405,6 +412,7 @@ tern_status tern_kv_read(const tern_kv* c, const tern_kv_batch* b, void* k, void
   a.v = v;
   a.f32 = dtype == TERN_F32;
   a.items = items_of(b);
+  if (page_blocks(c, b) < 0) return fail(TERN_E_UNSUPPORTED, "the call needs too many workgroups");
   KV_HIP(tern::launch_kv_read(a, c->dim, (hipStream_t)stream));
   return TERN_OK;
 }
