@@ -496,11 +496,12 @@ int32_t tern_q4_experts_tile_rows(const tern_q4 *gate_up, const tern_q4 *down, i
  * and v; tern_kv_write; tern_kv_attention; tern_plan_run for o).
  *
  * The conventions above hold: device pointers and a stream, asynchronous,
- * status codes, no allocation, nothing kept between calls, bitwise
- * reproducible, capturable into HIP graphs.  Rows of q, k, v and x are FP16
- * [heads][dim], the rows `stride` elements apart (a multiple of 8, so that
- * they may be columns of one product's output), pointers 16-byte aligned.
- * Sums, scores, norms and angles' sines have 32 bits or more. */
+ * status codes, no allocation, nothing kept between calls (but what
+ * tern_kv_tile_rows sets), bitwise reproducible, capturable into HIP graphs.
+ * Rows of q, k, v and x are FP16 [heads][dim], the rows `stride` elements
+ * apart (a multiple of 8, so that they may be columns of one product's
+ * output), pointers 16-byte aligned.  Sums, scores, norms and angles' sines
+ * have 32 bits or more. */
 
 /* Rotary positions of a head's first `rot` elements (even; the others pass
  * unchanged): pair i turns by the angle pos * freq[i],
@@ -622,9 +623,10 @@ tern_status tern_kv_attention(const tern_kv *c, const tern_kv_batch *b, const ui
 int32_t tern_kv_attention_parts(const tern_kv *c, const tern_kv_batch *b, int32_t q_heads, int32_t window);
 
 /* The rows of attention's tiles, for tests and measurements: 64 or 128 sets
- * them for every call, 0 (the default) leaves the choice to the library, any
- * other value only queries.  Returns the setting before.  Process-wide;
- * workspace sizes do not depend on it.  Host-only. */
+ * them for every later call of the calling thread (and with them the order of
+ * its sums), 0 (the default) leaves the choice to the library, any other value
+ * only queries.  Returns the thread's setting before.  Other threads' calls and
+ * all workspace sizes do not depend on it.  Host-only. */
 int32_t tern_kv_tile_rows(int32_t rows);
 
 /* Measurement aid, not part of the product: a plain streaming read of

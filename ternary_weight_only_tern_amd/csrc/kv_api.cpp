@@ -4,7 +4,6 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
-#include <atomic>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -221,7 +220,7 @@ int parts_for(long long groups, int pages, double mean, int dim, int rows, doubl
 // rows each, 8 after 8000, four blocks, not kept, 75 / 48.
 constexpr int kFewRows = 32, kFewPages = 4096;
 
-std::atomic<int> g_tile_rows{0};  // of every tile, 0: by the rule
+thread_local int g_tile_rows = 0;  // of this thread's tiles, 0: by the rule
 
 AttnPlan plan_of(const tern_kv* c, const tern_kv_batch* b, int group, int window, bool causal) {
   AttnPlan p = {};
@@ -430,8 +429,9 @@ int32_t tern_kv_attention_parts(const tern_kv* c, const tern_kv_batch* b, int32_
 }
 
 int32_t tern_kv_tile_rows(int32_t rows) {
-  if (rows == 0 || rows == tern::kAttnMid || rows == tern::kAttnTile) return g_tile_rows.exchange(rows);
-  return g_tile_rows;
+  const int before = g_tile_rows;
+  if (rows == 0 || rows == tern::kAttnMid || rows == tern::kAttnTile) g_tile_rows = rows;
+  return before;
 }
 
 tern_status tern_kv_attention(const tern_kv* c, const tern_kv_batch* b, const uint16_t* q, int64_t q_stride,

@@ -979,8 +979,8 @@ def tern_kv_attention(cache: KvCache, batch: KvBatch, q, scale=None, window=0, c
 
 
 def tern_kv_tile_rows(rows: int = -1) -> int:
-    """The rows of attention's tiles: 64 or 128 sets them, 0 restores the rule,
-    -1 queries; returns the setting before."""
+    """The rows of attention's tiles in this thread's calls: 64 or 128 sets them,
+    0 restores the rule, -1 queries; returns the setting before."""
     return load().tern_kv_tile_rows(rows)
 
 
