@@ -546,8 +546,13 @@ tern_status tern_rope(const uint16_t *x, int64_t x_stride, int32_t m, int32_t he
  *   k: token 16a + 4t + i, dimension 64c + 16r + b at ((4c + t) 64 + 16r + 4a + i) 16 + b
  *   v: token 16a + j, dimension 16c + e            at ((4c + a) 16 + e) 16 + j.
  * dim 64, 128 or 256 (TERN_E_UNSUPPORTED).  k, v 16-byte aligned.  Scales are
- * 0, NaN or in 2^-60 .. 2^60 (tern_kv_write's are). */
+ * 0, NaN or in 2^-36 .. 2^36 (tern_kv_write's are, 2^-31 .. 2^10): attention's
+ * FP32 sums pass from the units of one page's scale to those of another's, 2^72
+ * at most, and 2^30 tokens, each a code of 2^7 times a weight of up to 2^15,
+ * leave them 2^75.  Outside of that a sum may become infinite that a later,
+ * larger score would have made vanish. */
 #define TERN_KV_PAGE 64
+#define TERN_KV_SCALE_BITS 36
 typedef struct tern_kv {
   int32_t heads, dim, pages;
   uint8_t *k, *v;           /* [pages][heads][64 * dim] */

@@ -33,6 +33,7 @@ TERN_SCORE_SOFTMAX = 0
 TERN_SCORE_SIGMOID = 1
 (TERN_ROPE_PLAIN, TERN_ROPE_LINEAR, TERN_ROPE_BASE, TERN_ROPE_RAMP, TERN_ROPE_WAVES) = range(5)
 TERN_KV_PAGE = 64
+TERN_KV_SCALE_BITS = 36
 
 (TERN_BUF_PLANE0, TERN_BUF_SCALE0, TERN_BUF_OFFSET, TERN_BUF_MASK, TERN_BUF_ROWPTR,
  TERN_BUF_BLOCKS1, TERN_BUF_BLOCKS2, TERN_BUF_RSCALE1, TERN_BUF_RSCALE2, TERN_NBUF) = range(10)
@@ -817,7 +818,8 @@ def tern_rope(x, pos, rope: Rope, out=None, stream=None):
 class KvCache(_Fixed):
     """tern_kv: a paged cache in 8 bits.  k, v: uint8 [pages][heads][64][dim]
     (the bytes of a (page, head) in tern_kv's order), k_scale, v_scale: fp32
-    [pages][heads].  Keeps the tensors; makes no copy."""
+    [pages][heads], 0, NaN or from 2^-36 to 2^36.  Keeps the tensors; makes no
+    copy."""
 
     def __init__(self, k, v, k_scale, v_scale):
         import torch
