@@ -610,13 +610,17 @@ tern_status tern_kv_read(const tern_kv *c, const tern_kv_batch *b, void *k, void
  * g - 1 share cache head h, g = q_heads / heads.  y FP16 [rows][q_heads][dim];
  * a row that sees nothing is 0.  Tokens that a row does not see do not reach
  * it, whatever they or their scales hold.  Scores and sums are FP32; the
- * softmax's weights meet the codes of v in FP16 (11 bits each).  scale finite,
- * not negative.  ws: tern_kv_attention_workspace_bytes (0 for arguments that
- * are refused), 16-byte aligned (calls that need none take NULL, and refuse
- * one that is not aligned too), enough for every batch with no more
- * sequences and rows and no larger max_len too; calls that overlap in time must
- * not share it.  At most (TERN_E_UNSUPPORTED): 65535 query heads, a q_stride of
- * 2^23, max_rows g of 2^30, count heads of 2^24, count heads max_pages of 2^31 - 1. */
+ * softmax's weights meet the codes of v in FP16 (11 bits each down to 2^-18 of
+ * the largest, within 2^-29 of it below).  scale finite, not negative.  One
+ * kernel serves a call, chosen by max_rows: single tokens beside a long
+ * prompt's rows are right, and faster in a call of their own.  ws:
+ * tern_kv_attention_workspace_bytes (0 for arguments that are refused), 16-byte
+ * aligned (calls that need none take NULL, and refuse one that is not aligned
+ * too), enough for every batch with no more sequences and rows and no larger
+ * max_len too; calls that overlap in time must not share it.  At most
+ * (TERN_E_UNSUPPORTED): 65535 query heads, a q_stride of 2^23, max_rows g of
+ * 2^30, count heads of 2^24, count heads max_pages of 2^31 - 1, and workgroups
+ * that a grid can count. */
 size_t tern_kv_attention_workspace_bytes(const tern_kv *c, const tern_kv_batch *b, int32_t q_heads);
 tern_status tern_kv_attention(const tern_kv *c, const tern_kv_batch *b, const uint16_t *q, int64_t q_stride,
                               int32_t q_heads, float scale, int32_t window, int32_t causal, uint16_t *y, void *ws,

@@ -176,16 +176,20 @@ int pages_of(const tern_kv_batch* b, int window, int rows) {
 
 // Parts for `groups` tiles of `rows` rows that see `pages` pages at most, `mean` on
 // average, and their time, in us, by a model whose figures are fitted to
-// measurements of 48 shapes (its choices are 0.5 % slower than the best ones).  A
-// page takes a workgroup `step`, or `share` times that where a CU has `holds`
-// workgroups; tiles of different lengths fill CUs unevenly.  Joining takes 1.5 and
-// what the parts' sums take to be written and read.  Uncut and cut, us: 128-row
-// tiles, 64 of 125 pages, 4 / 8 / 12 parts 173 -> 56.5 / 48.5 / 53.0; 16 of 63 pages, 8 /
-// 16 / 32 parts 96.8 -> 22.8 / 20.6 / 24.1; a prompt of 2048, 128 tiles, 4 / 6 / 8 parts 53.6
-// -> 35.2 / 32.2 / 42.0.  Tiles of 64 and of 128 rows, us, each at its best number of
-// parts: prompts of 256, 512, 1024 and 4096 tokens 10.3 and 13.1, 15.8 and 19.5, 27.1
-// and 31.6, 89 and 65; 64 sequences of 40 rows 37.7 and 48.1; 512 rows after 7500
-// tokens 122 and 88; 8192 rows 850 and 570.
+// measurements of 48 shapes (profiles/kv_attention_parts.txt: on average its choices
+// are 0.3 % slower than the best ones, at most 4 %; on 32 shapes that the fit
+// did not have 2.6 %, at most 22 %).  A page takes a workgroup `step`, or `share`
+// times that where a CU has `holds` workgroups.  Tiles of different lengths fill CUs
+// unevenly: more than 160 of them count as sharing CUs (with 256 in its place the
+// 48 shapes' choices are 1.6 % slower than the best, at most 22 %, the 32 others'
+// 2.2 %, at most 16 %).  Joining takes 1.5 and what the parts' sums take to be
+// written and read.  Uncut and cut, us: 128-row tiles, 64 of 125 pages, 4 / 8 / 12
+// parts 176 -> 56.1 / 47.0 / 52.7; 16 of 63 pages, 8 / 16 / 32 parts 96.0 -> 22.6 / 20.5 /
+// 23.6; a prompt of 2048, 128 tiles, 4 / 6 / 8 parts 52.7 -> 35.1 / 31.9 / 41.6.  Tiles of
+// 64 and of 128 rows, us, each at its best number of
+// parts: prompts of 256, 512, 1024 and 4096 tokens 10.1 and 13.1, 15.1 and 19.5, 25.5
+// and 30.9, 80 and 65; 64 sequences of 40 rows 35.7 and 44.0; 512 rows after 7500
+// tokens 114 and 88.8; 8192 rows 789 and 592.
 struct Cost {
   double step, share;
   int holds;
@@ -222,6 +226,10 @@ constexpr int kFewRows = 32, kFewPages = 4096;
 
 thread_local int g_tile_rows = 0;  // of this thread's tiles, 0: by the rule
 
+// One kernel serves a call, that of its longest sequence: the host does not know
+// the others' rows.  Single tokens beside a prompt's chunk then walk their pages on
+// tiles, a workgroup each (us, together and in two calls: 63 tokens after up to 8192
+// beside 2048 rows after 1000 476 and 190, 31 after up to 2000 beside 512 rows 64 and 34).
 AttnPlan plan_of(const tern_kv* c, const tern_kv_batch* b, int group, int window, bool causal) {
   AttnPlan p = {};
   const long long rows = (long long)most_rows(b) * group, units = (long long)b->count * c->heads;

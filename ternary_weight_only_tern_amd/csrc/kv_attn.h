@@ -90,9 +90,12 @@ __device__ inline Sees sees_of(const AttnArgs& a, const Span& sp, int pos, bool 
 // The reference follows the largest score only where that has grown by more
 // than kLag (weights stay below 2^5; exponents and FP16's 11 bits do not
 // care), and the units follow the pages' scales only where a page's is larger
-// or kSpan times smaller: most pages rescale nothing.  The FP16 weights are
-// kLift times as large (below FP16's 2^16), so that those down to 2^-24 of the
-// reference keep their 11 bits, and what is below has 2^-35 of it.
+// or kSpan times smaller: most pages rescale nothing.  A weight meets the codes
+// in FP16, in the sums' units: times kLift and the page's scale, over the unit
+// (below FP16's 2^16).  Where the page's scale is the unit, weights down to
+// 2^-24 of the reference keep their 11 bits and smaller ones are off by 2^-35 of
+// it at most; where it is kSpan times smaller, 2^-18 and 2^-29, of values that
+// are as much smaller.
 constexpr float kLag = 5.0f, kSpan = 64.0f, kLift = 1024.0f;
 struct Row {
   float top, sum, unit, inv;  // inv: 1 / unit

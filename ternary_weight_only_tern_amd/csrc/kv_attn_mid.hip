@@ -14,9 +14,9 @@
 // 330), which a second workgroup on the CU hides in part: every wavefront reads
 // all operands for 16 rows, so that long prompts are better off with 32
 // (kv_attn_tile.hip), and few rows, short prompts and small dimensions here.  A
-// prompt of 512 tokens, 32 heads over 8, 15.5 us (128-row tiles 19.5); 64
-// sequences of 1000 with 10 rows 38-42 (48.1); two prompts of 2048, 12 heads of 64,
-// 36-37 (41.1), 350 TFLOP/s; one of 2048, 16 heads of 256 over 8, 83 (98).  With this
+// prompt of 512 tokens, 32 heads over 8, 15-16 us (128-row tiles 19.5); 64
+// sequences of 1000 with 10 rows 36-42 (44.0); two prompts of 2048, 12 heads of 64,
+// 34-36 (42.6), 360 TFLOP/s; one of 2048, 16 heads of 256 over 8, 80 (97).  With this
 // page's scores multiplied in the step itself the last took 91, the others as long.
 #include "kv_attn.h"
 
@@ -176,7 +176,7 @@ __global__ __launch_bounds__(64 * kMidWaves, D <= 128 ? 2 : 1) void attn_mid_ker
       kh8_t w[2];
       float sum = 0.f;
 #pragma unroll
-      for (int x = 0; x < 16; x += 2) {  // the sum is of the rounded weights
+      for (int x = 0; x < 16; x += 2) {  // the sum is of the rounded weights, as in kv_attn_tile.hip
         kh2_t two;
         two.x = (_Float16)__builtin_amdgcn_exp2f(__builtin_fmaf(z[x / 4][x % 4], by, shift));
         two.y = (_Float16)__builtin_amdgcn_exp2f(__builtin_fmaf(z[x / 4][x % 4 + 1], by, shift));

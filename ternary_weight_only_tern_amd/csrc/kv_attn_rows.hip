@@ -23,7 +23,7 @@
 // of as much 6.4-7.0); four sequences of up to 120000 tokens, five rows each,
 // 106-118 us, 5.6-6.2 TB/s.  More wavefronts, deeper prefetch and other page orders gained
 // nothing; loads that pass the L2 by (kv_stream) took 123 us to 113.  One token of 8 heads
-// after 4000: 6.6 us and 4.4 for joining, a chain of trips to memory.
+// after 4000: 6.5 us and 4.0-5.0 for joining, a chain of trips to memory.
 #include "kv_attn.h"
 
 namespace tern {

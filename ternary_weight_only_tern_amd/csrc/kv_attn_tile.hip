@@ -19,8 +19,8 @@
 // Bound by instructions: a wavefront's page of 128 dimensions is 32 matrix
 // instructions (1024 cycles) and about 1400 cycles of exponentials, maxima,
 // roundings and decoding, which overlap little: 2048 rows of 32 heads over 8
-// after 1000 tokens 89 us, 762 TFLOP/s; 8192 rows 585 us, 935 TFLOP/s (the
-// library's FP16 product of 8192^3: 1190).  Other orders of the tiles, other
+// after 1000 tokens 90 us, 755 TFLOP/s; 8192 rows 595 us, 924 TFLOP/s (the
+// library's FP16 product of 8192^3: 1200-1340).  Other orders of the tiles, other
 // priorities and three wavefronts a SIMD (at 64 dimensions) gained nothing or spilled.  Where tiles
 // are short, 3 to 5 us pass before a workgroup's first page: four dependent trips
 // to memory and code that no cache holds yet.  At 256 dimensions a CU has one
@@ -268,7 +268,9 @@ __global__ __launch_bounds__(64 * kTileWaves, D <= 128 ? 2 : 1) void attn_tile_k
       kh8_t w[4];
       float sum = 0.f;
       auto weigh = [&](int x) { z[x / 16][x % 16] = __builtin_amdgcn_exp2f(__builtin_fmaf(z[x / 16][x % 16], by, shift)); };
-      auto round2 = [&](int x) {  // the sum is of the rounded weights
+      // The sum is of the rounded weights, two by one instruction: what a weight
+      // loses against the values it loses in the sum too.
+      auto round2 = [&](int x) {
         const kh2_t two = {(_Float16)z[x / 16][x % 16], (_Float16)z[x / 16][x % 16 + 1]};
         w[x / 8][x % 8] = two.x;
         w[x / 8][x % 8 + 1] = two.y;

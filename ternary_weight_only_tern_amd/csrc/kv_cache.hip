@@ -13,11 +13,11 @@
 // again and writes those bytes; nothing is shared but the largest value.  q's
 // rows are turned by further workgroups of the same launch (rope.hip's way).
 //
-// Bound by bytes and vector instructions: a prompt of 4096 tokens, 8 heads of
-// 128 with 32 of q, takes 24.4 us (4.8 TB/s read and written; the vector units
-// are busy for more than half of it: norms, FP64 angles of every head's keys,
-// codes).  Prefixes of 96000 tokens, 8 heads, are read back as FP32 in 123 us (4.6
-// TB/s), as FP16 in 80.  A token each of 48 sequences takes 5.8 us, a chain of
+// Bound by vector instructions and bytes: a prompt of 4096 tokens, 8 heads of
+// 128 with 32 of q, takes 26-28 us (92 MB read and written, 3.4 TB/s; the vector
+// units are busy for 72 % of the cycles: norms, FP64 angles of every head's keys,
+// codes).  Prefixes of 96000 tokens, 8 heads, are read back as FP32 in 124 us (4.6
+// TB/s), as FP16 in 79.  A token each of 48 sequences takes 5.8-6.1 us, a chain of
 // four trips to memory: lengths, page number, scale, the page's other codes.
 #include "kv.h"
 

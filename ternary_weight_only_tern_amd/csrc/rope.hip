@@ -9,7 +9,7 @@
 //
 // Bound by the bytes of x and out where rows are many: 5000 rows of 32 heads of
 // 128, half of each turned, 14.7 us, 5.6 TB/s read and written.  One row of 40
-// heads: 3.4 us, a trip to memory and the angles' FP64 behind an empty kernel's 1.9.
+// heads: 3.0-3.2 us, a trip to memory and the angles' FP64 behind an empty kernel's 1.9.
 #include "kv.h"
 
 namespace tern {

@@ -957,7 +957,8 @@ def tern_kv_attention(cache: KvCache, batch: KvBatch, q, scale=None, window=0, c
                       ws=None):
     """Attention of the rows q fp16 [m][q_heads][dim] over the cache; returns
     y fp16 [m][q_heads][dim], in `out` if given.  scale: of the scores (default
-    dim ** -0.5); window: tokens a row sees at most (0: all)."""
+    dim ** -0.5); window: tokens a row sees at most (0: all).  Single tokens
+    beside a prompt's rows are faster in a call of their own."""
     device, dim = cache.device, cache.dim
     if _elsewhere(device):
         with _torch.cuda.device(device):
